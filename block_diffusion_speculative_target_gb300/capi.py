@@ -94,6 +94,14 @@ _SIGS = {
     "dflash_argmax": (_I, [_P, _I, _I, _P, _P, _P, _P]),
     "dflash_argmax_noalloc": (_I, [_P, _I, _I, _P, _P, _P, _P]),
     "dflash_attention": (_I, [POINTER(ModelDesc), _P, _I, _I, _I, _I, _P, _I, _P, _P, _P]),
+    "dflash_pages_create": (_I, [POINTER(ModelDesc), _I, _I, _I, _I, _P, _P, POINTER(c_void_p)]),
+    "dflash_pages_free": (_I, [_P]),
+    "dflash_paged_workspace_alloc": (_I, [POINTER(ModelDesc), _I, _I, POINTER(c_void_p)]),
+    "dflash_paged_workspace_free": (_I, [_P]),
+    "dflash_paged_status": (_I, [_P, _P, POINTER(c_int32)]),
+    "dflash_paged_append": (_I, [_P, _I, _I, _P, ctypes.c_int64, _I, _I, _P, _P, _I, _P, _P, _P, _P]),
+    "dflash_paged_attention": (_I, [_P, _I, _P, _I, _I, _P, _I, _I, _I, _P, _I, _P, _P, _P, _P]),
+    "dflash_paged_attention_shared": (_I, [_P, _I, _P, _I, _I, _P, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P]),
     "dflash_profile_begin": (_I, [_I]),
     "dflash_launch_count": (ctypes.c_longlong, []),
     "dflash_profile_end": (_I, [POINTER(c_float), POINTER(c_int32), _I, POINTER(c_int32)]),
@@ -382,6 +390,58 @@ def dflash_argmax_noalloc(logits, rows, V, argmax, gap, status=None, stream=None
 def dflash_attention(desc: ModelDesc, q, batch, n, causal, cache, layer, out, ws, stream=None, window=0):
     _check(load().dflash_attention(ctypes.byref(desc), _ptr(q), batch, n, causal, window, cache, layer, _ptr(out), ws,
                                    _stream(stream)), "dflash_attention")
+
+
+# ---------------------------------------------------------------- KV pages
+
+
+def dflash_pages_create(desc: ModelDesc, n_layers, n_pages, page_size, max_pos, k, v):
+    h = c_void_p()
+    _check(load().dflash_pages_create(ctypes.byref(desc), n_layers, n_pages, page_size, max_pos, _ptr(k), _ptr(v),
+                                      ctypes.byref(h)), "dflash_pages_create")
+    return h.value
+
+
+def dflash_pages_free(pages):
+    _check(load().dflash_pages_free(pages), "dflash_pages_free")
+
+
+def dflash_paged_workspace_alloc(desc: ModelDesc, max_batch, max_rows):
+    h = c_void_p()
+    _check(load().dflash_paged_workspace_alloc(ctypes.byref(desc), max_batch, max_rows, ctypes.byref(h)),
+           "dflash_paged_workspace_alloc")
+    return h.value
+
+
+def dflash_paged_workspace_free(ws):
+    _check(load().dflash_paged_workspace_free(ws), "dflash_paged_workspace_free")
+
+
+def dflash_paged_status(ws, stream=None):
+    v = c_int32()
+    _check(load().dflash_paged_status(ws, _stream(stream), ctypes.byref(v)), "dflash_paged_status")
+    return v.value
+
+
+def dflash_paged_append(pages, layer, in_dtype, qkv, ld, batch, n, n_rows, table, table_stride, lengths, q_out, ws,
+                        stream=None):
+    _check(load().dflash_paged_append(pages, layer, in_dtype, _ptr(qkv), ld, batch, n, _ptr(n_rows), _ptr(table),
+                                      table_stride, _ptr(lengths), _ptr(q_out), ws, _stream(stream)),
+           "dflash_paged_append")
+
+
+def dflash_paged_attention(pages, layer, q, batch, n, n_rows, causal, window, sinks, table, table_stride, lengths, out,
+                           ws, stream=None):
+    _check(load().dflash_paged_attention(pages, layer, _ptr(q), batch, n, _ptr(n_rows), causal, window, sinks,
+                                         _ptr(table), table_stride, _ptr(lengths), _ptr(out), ws, _stream(stream)),
+           "dflash_paged_attention")
+
+
+def dflash_paged_attention_shared(pages, layer, q, batch, n, n_rows, causal, window, sinks, table, table_stride,
+                                  lengths, shared_len, out, ws, stream=None):
+    _check(load().dflash_paged_attention_shared(pages, layer, _ptr(q), batch, n, _ptr(n_rows), causal, window, sinks,
+                                                _ptr(table), table_stride, _ptr(lengths), _ptr(shared_len), _ptr(out),
+                                                ws, _stream(stream)), "dflash_paged_attention_shared")
 
 
 # ---------------------------------------------------------------- kernel timing

@@ -97,11 +97,13 @@ int record_cuda_error(cudaError_t e) {
 
 static size_t dtype_size(int dt) { return dt == DFLASH_BF16 ? 2 : 4; }
 
-static bool desc_ok(const dflash_model_desc* d) {
+namespace dfl {
+bool desc_ok(const dflash_model_desc* d) {
   return d && d->n_layers > 0 && d->hidden > 0 && d->n_q_heads > 0 && d->n_kv_heads > 0 &&
          d->n_q_heads % d->n_kv_heads == 0 && (d->head_dim == 64 || d->head_dim == 128) && d->ffn > 0 &&
          d->vocab > 1 && (d->dtype == DFLASH_F32 || d->dtype == DFLASH_BF16) && d->hidden % 4 == 0;
 }
+}  // namespace dfl
 
 static bool desc_shapes_ok(const dflash_model_desc* d) {
   if (d->dtype != DFLASH_BF16) return true;

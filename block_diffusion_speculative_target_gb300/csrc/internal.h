@@ -206,6 +206,8 @@ struct ArgmaxScratch {
 };
 cudaError_t argmax(const float* logits, int rows, int V, int32_t* argmax_out, float* gap, int skip_first_of,
                    const ArgmaxScratch& sc, int* status, cudaStream_t s);
+// The dimensions every entry point accepts (head_dim 64 or 128, whole GQA groups, ...).
+bool desc_ok(const dflash_model_desc* d);
 // Stores e as the thread's last CUDA error (reported by dflash_strerror) and
 // returns DFLASH_ERR_CUDA.
 int record_cuda_error(cudaError_t e);

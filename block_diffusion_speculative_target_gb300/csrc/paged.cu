@@ -1,0 +1,465 @@
+// KV pages: the RoPE table, the append of rotated keys and values, attention
+// over pages on the CUDA cores, and the merge of partial attention results.
+#include "paged.cuh"
+
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dfl {
+
+// ------------------------------------------------------------------ RoPE table
+// cos/sin of pos * theta^(-2 i / hd), angles in double precision.
+__global__ void rope_table_kernel(float2* tab, int max_pos, int half, double theta) {
+  const long long n = (long long)max_pos * half;
+  for (long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x; t < n; t += (long long)gridDim.x * blockDim.x) {
+    const int p = (int)(t / half), i = (int)(t - (long long)p * half);
+    double s, c;
+    sincos((double)p * pow(theta, -(double)i / half), &s, &c);
+    tab[t] = make_float2((float)c, (float)s);
+  }
+}
+
+cudaError_t rope_table(float2* tab, int max_pos, int half, double theta) {
+  rope_table_kernel<<<num_sms() * 4, 256>>>(tab, max_pos, half, theta);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ append
+// Row (b, j) of the packed q|k|v rows at position p = len[b] + j: q and k are
+// rotated in float32 (x_lo c - x_hi s, x_hi c + x_lo s), rounded once, and q
+// goes to q_out, k and v to slot p mod ps of page table[b][p / ps].  A thread
+// moves 8 entries of a head's lower half and the 8 they rotate with.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
+  if (vec && sizeof(T) == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else if (vec) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&a);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __bfloat1622float2(h[e]);
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = to_f<T>(p[e]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  if (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *(reinterpret_cast<float4*>(p) + 1) = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    uint4 v;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+    *reinterpret_cast<uint4*>(p) = v;
+  }
+}
+
+template <typename TI, typename T>
+__global__ void __launch_bounds__(256)
+    paged_append_kernel(const TI* __restrict__ qkv, long long ld, int vec, int batch, int n, int nq, int nkv, int hd,
+                        const int32_t* __restrict__ n_rows, const int32_t* __restrict__ table, int table_stride,
+                        const int32_t* __restrict__ len, const float2* __restrict__ tab, int max_pos, int n_pages,
+                        int ps, long long page0, T* __restrict__ qout, T* __restrict__ kp, T* __restrict__ vp,
+                        int* status) {
+  const int half = hd / 2, per_head = half / 8;
+  const int per_row = (nq + 2 * nkv) * per_head;
+  const long long total = (long long)batch * n * per_row;
+  pdl_launch();
+  pdl_wait();
+  for (long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x; t < total;
+       t += (long long)gridDim.x * blockDim.x) {
+    const int r = (int)(t / per_row), w = (int)(t - (long long)r * per_row);
+    const int b = r / n, j = r - b * n;
+    if (n_rows && j >= n_rows[b]) continue;
+    const int h = w / per_head, e = (w - h * per_head) * 8;
+    const long long pos = (long long)len[b] + j;
+    if (pos < 0 || pos >= max_pos || pos / ps >= table_stride) {
+      if (w == 0) set_status(status, DFLASH_STATUS_CAPACITY);
+      continue;
+    }
+    const TI* src = qkv + (long long)r * ld + h * hd + e;
+    float lo[8], hi[8];
+    load8<TI>(src, vec, lo);
+    load8<TI>(src + half, vec, hi);
+    if (h < nq + nkv) {
+      const float4* cs = reinterpret_cast<const float4*>(tab + pos * half + e);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float4 c = cs[x];  // two (cos, sin) pairs
+        const float a0 = lo[2 * x], b0 = hi[2 * x], a1 = lo[2 * x + 1], b1 = hi[2 * x + 1];
+        lo[2 * x] = a0 * c.x - b0 * c.y;
+        hi[2 * x] = b0 * c.x + a0 * c.y;
+        lo[2 * x + 1] = a1 * c.z - b1 * c.w;
+        hi[2 * x + 1] = b1 * c.z + a1 * c.w;
+      }
+    }
+    T* dst;
+    if (h < nq) {
+      dst = qout + ((long long)r * nq + h) * hd;
+    } else {
+      const int page = table[(long long)b * table_stride + pos / ps];
+      if ((unsigned)page >= (unsigned)n_pages) {
+        set_status(status, DFLASH_STATUS_BOUNDS);
+        continue;
+      }
+      const int hk = h - nq < nkv ? h - nq : h - nq - nkv;
+      dst = (h - nq < nkv ? kp : vp) + ((((page0 + page) * nkv) + hk) * ps + pos % ps) * hd;
+    }
+    store8<T>(dst + e, lo);
+    store8<T>(dst + e + half, hi);
+  }
+}
+
+cudaError_t paged_append(int in_dtype, int dtype, const void* qkv, long long ld, int batch, int n, int nq, int nkv,
+                         int hd, const int32_t* n_rows, const int32_t* table, int table_stride, const int32_t* len,
+                         const float2* tab, int max_pos, int n_pages, int ps, long long page0, void* qout, void* kp,
+                         void* vp, int* status, cudaStream_t s) {
+  const size_t es = in_dtype == DFLASH_BF16 ? 2 : 4;
+  const int vec = (reinterpret_cast<uintptr_t>(qkv) & 15) == 0 && (ld * es) % 16 == 0;
+  const long long total = (long long)batch * n * (nq + 2 * nkv) * (hd / 16);
+  const unsigned grid = (unsigned)std::min<long long>((total + 255) / 256, (long long)num_sms() * 64);
+#define DFL_APPEND(TI, T)                                                                                            \
+  DFL_RET(launch_pdl(paged_append_kernel<TI, T>, dim3(grid), dim3(256), 0, s, (const TI*)qkv, ld, vec, batch, n, nq, \
+                     nkv, hd, n_rows, table, table_stride, len, tab, max_pos, n_pages, ps, page0, (T*)qout, (T*)kp,  \
+                     (T*)vp, status))
+  if (dtype == DFLASH_F32) {
+    DFL_APPEND(float, float);
+  } else if (in_dtype == DFLASH_F32) {
+    DFL_APPEND(float, bf16);
+  } else {
+    DFL_APPEND(bf16, bf16);
+  }
+#undef DFL_APPEND
+  count_launch();
+  return cudaSuccess;
+}
+
+// ------------------------------------------------------------------ CUDA-core attention
+// One pass over an item's keys in tiles of 32 with the running maximum m, sum l
+// and output o of every row: s = q.k scale log2(e), m' = max(m, max s),
+// p = 2^(s - m'), l = l 2^(m - m') + sum p, o = o 2^(m - m') + p v.
+// MR = 16 MRM stacked rows (row = thread / 16 + 16 x); the 16 threads of a row
+// share its keys in the scores and its dimensions in the output.  A hidden
+// key's weight is stored as -0, which the masked tiles skip, so that an Inf or
+// NaN value behind a mask stays out of the row.
+constexpr int kCoreKeys = 32;
+constexpr int kCoreThreads = 256;
+
+template <int HD, int MRM>
+struct CoreLayout {
+  static constexpr int MR = 16 * MRM;
+  static constexpr int kRow = HD + 4;  // padded: the 16 lanes of a row read 16 key rows without bank conflicts
+  static constexpr int kK = MR * HD * 4;
+  static constexpr int kV = kK + kCoreKeys * kRow * 4;
+  static constexpr int kP = kV + kCoreKeys * HD * 4;
+  static constexpr int kRed = kP + MR * kCoreKeys * 4;
+  static constexpr int kSmem = kRed + (2 * kCoreThreads / 32 + 8) * 4;
+};
+
+template <typename T, int HD, int MRM>
+__global__ void __launch_bounds__(kCoreThreads)
+    paged_attn_core_kernel(const __grid_constant__ PagedGeom g, const T* __restrict__ q, const T* __restrict__ kp,
+                           const T* __restrict__ vp, T* __restrict__ out, float scale_log2) {
+  typedef CoreLayout<HD, MRM> L;
+  extern __shared__ uint8_t smem_raw[];
+  float* sq = reinterpret_cast<float*>(smem_raw);
+  float* sk = reinterpret_cast<float*>(smem_raw + L::kK);
+  float* sv = reinterpret_cast<float*>(smem_raw + L::kV);
+  float* sp = reinterpret_cast<float*>(smem_raw + L::kP);
+  const int tid = threadIdx.x, l16 = tid & 15, rq = tid >> 4;
+  constexpr int NC = HD / 64;  // output: float4 chunks of a thread
+  pdl_launch();
+  pdl_wait();
+  const PlanView v = plan_view<kCoreKeys, kCoreThreads>(g, reinterpret_cast<int*>(smem_raw + L::kRed));
+  SegmentWalk<kCoreKeys> walk(g, v);
+  Segment sg;
+  while (walk.next(sg)) {
+    const int r_max = sg.prefix ? g.rp : g.ri;
+    ItemRow row[MRM];
+    int sink[MRM], lo[MRM], hi[MRM];
+    float m[MRM], l[MRM], o[MRM][NC * 4];
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < MRM; ++x) {
+      const int r = rq + 16 * x;
+      row[x] = item_row(g, sg, r, r_max);
+      sink[x] = lo[x] = hi[x] = 0;
+      if (row[x].live) row_span(g, paged_len(g, row[x].b), paged_rows(g, row[x].b), row[x].i, sink[x], lo[x], hi[x]);
+      m[x] = -INFINITY;
+      l[x] = 0.f;
+#pragma unroll
+      for (int e = 0; e < NC * 4; ++e) o[x][e] = 0.f;
+      for (int d = l16; d < HD; d += 16)
+        sq[r * HD + d] = row[x].live ? to_f<T>(q[(((long long)row[x].b * g.n + row[x].i) * g.nq + row[x].head) * HD + d])
+                                     : 0.f;
+    }
+    const int key_lo = sg.prefix ? 0 : v.sh_tiles * kCoreKeys;  // keys below belong to the shared prefix
+    const int key_end = sg.prefix ? v.sh_tiles * kCoreKeys : key_limit(g, sg.b);
+    for (int t = sg.t0; t < sg.t0 + sg.nt; ++t) {
+      const int k0 = sg.span.tile(t) * kCoreKeys;
+      __syncthreads();
+      {  // 8 threads a key: its rows of keys and values (past the sequence's keys, or in a bad page: zeros)
+        const int key = k0 + (tid >> 3), part = tid & 7;
+        int page = -1;
+        if (key < key_end) {
+          page = g.table[(long long)sg.b * g.table_stride + (key >> g.ps_log2)];
+          if ((unsigned)page >= (unsigned)g.n_pages) {
+            page = -1;
+            set_status(g.status, DFLASH_STATUS_BOUNDS);
+          }
+        }
+        const long long at =
+            page < 0 ? 0 : (g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps + (key & (g.ps - 1))) * HD;
+#pragma unroll
+        for (int e = part * 8; e < HD; e += 64) {
+          float xk[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, xv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (page >= 0) {
+            load8<T>(kp + at + e, true, xk);
+            load8<T>(vp + at + e, true, xv);
+          }
+          store8<float>(sk + (tid >> 3) * L::kRow + e, xk);
+          store8<float>(sv + (tid >> 3) * HD + e, xv);
+        }
+      }
+      __syncthreads();
+      float s[MRM][2];
+#pragma unroll
+      for (int x = 0; x < MRM; ++x) s[x][0] = s[x][1] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < HD; d += 4) {
+        const float4 ka = *reinterpret_cast<const float4*>(sk + l16 * L::kRow + d);
+        const float4 kb = *reinterpret_cast<const float4*>(sk + (l16 + 16) * L::kRow + d);
+#pragma unroll
+        for (int x = 0; x < MRM; ++x) {
+          const float4 a = *reinterpret_cast<const float4*>(sq + (rq + 16 * x) * HD + d);
+          s[x][0] = fmaf(a.x, ka.x, fmaf(a.y, ka.y, fmaf(a.z, ka.z, fmaf(a.w, ka.w, s[x][0]))));
+          s[x][1] = fmaf(a.x, kb.x, fmaf(a.y, kb.y, fmaf(a.z, kb.z, fmaf(a.w, kb.w, s[x][1]))));
+        }
+      }
+      bool masked = false;
+#pragma unroll
+      for (int x = 0; x < MRM; ++x) {
+        float z[2], mx = -INFINITY;
+        bool vis[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int key = k0 + l16 + 16 * y;
+          vis[y] = key >= key_lo && key < key_end && (key < sink[x] || (key >= lo[x] && key < hi[x]));
+          z[y] = vis[y] ? s[x][y] * scale_log2 : -INFINITY;
+          mx = fmaxf(mx, z[y]);
+          masked |= !vis[y];
+        }
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        const float mn = fmaxf(m[x], mx);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float p = vis[y] ? exp2f(z[y] - ref) : -0.f;
+          sp[(rq + 16 * x) * kCoreKeys + l16 + 16 * y] = p;
+          sum += p;
+        }
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        const float f = m[x] == -INFINITY ? 0.f : exp2f(m[x] - ref);
+        l[x] = l[x] * f + sum;
+        m[x] = mn;
+#pragma unroll
+        for (int e = 0; e < NC * 4; ++e) o[x][e] *= f;
+      }
+      masked = __syncthreads_or(masked);
+      auto weigh = [&](int x, float p, const float4 (&a)[NC]) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          o[x][4 * c] = fmaf(p, a[c].x, o[x][4 * c]);
+          o[x][4 * c + 1] = fmaf(p, a[c].y, o[x][4 * c + 1]);
+          o[x][4 * c + 2] = fmaf(p, a[c].z, o[x][4 * c + 2]);
+          o[x][4 * c + 3] = fmaf(p, a[c].w, o[x][4 * c + 3]);
+        }
+      };
+#pragma unroll 4
+      for (int k = 0; k < kCoreKeys; ++k) {
+        float4 a[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) a[c] = *reinterpret_cast<const float4*>(sv + k * HD + c * 64 + l16 * 4);
+#pragma unroll
+        for (int x = 0; x < MRM; ++x) {
+          const float p = sp[(rq + 16 * x) * kCoreKeys + k];
+          if (!masked || __float_as_int(p) >= 0) weigh(x, p, a);  // -0: hidden
+        }
+      }
+    }
+    const bool whole = walk.whole(sg);
+#pragma unroll
+    for (int x = 0; x < MRM; ++x) {
+      if (!row[x].live) continue;
+      const int r = rq + 16 * x;
+      if (whole) {
+        T* dst = out + (((long long)row[x].b * g.n + row[x].i) * g.nq + row[x].head) * HD;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[c * 64 + l16 * 4 + e] = from_f<T>(o[x][4 * c + e] / l[x]);
+      } else {
+        float* dst = g.part_o + (sg.slot_row + r) * HD;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          *reinterpret_cast<float4*>(dst + c * 64 + l16 * 4) =
+              make_float4(o[x][4 * c], o[x][4 * c + 1], o[x][4 * c + 2], o[x][4 * c + 3]);
+        if (l16 == 0) g.part_ml[sg.slot_row + r] = make_float2(m[x], l[x]);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ merge
+// out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c over a row's partials c
+// (prefix pieces, then its sequence's own, each in tile order), m = max m_c.
+// One warp per (row, head); lane l owns HD / 32 dimensions.  A row that one
+// piece finished has nothing here.
+template <typename T, int HD, int KT>
+__global__ void __launch_bounds__(64) paged_merge_kernel(const __grid_constant__ PagedGeom g, T* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * 2 + (threadIdx.x >> 5);
+  pdl_launch();
+  pdl_wait();
+  if (item >= (long long)g.batch * g.n * g.nq) return;
+  const int r = (int)(item / g.nq), h = (int)(item - (long long)r * g.nq);
+  const int b = r / g.n, i = r - b * g.n;
+  if (i >= paged_rows(g, b)) return;
+  const int quota = g.plan[kPlanQuota], sh = g.plan[kPlanShared], pre = g.plan[kPlanPre];
+  const int hk = h / g.G, rt = i / g.ri;
+  // its sequence's own pieces
+  int at = g.plan[kPlanCum + b];
+  for (int x = 0; x < rt; ++x) at += suffix_span<KT>(g, b, x, sh).count() * g.nkv;
+  const int cnt = suffix_span<KT>(g, b, rt, sh).count();
+  at += hk * cnt;
+  const int c0 = at / quota, ns = cnt > 0 ? (at + cnt - 1) / quota - c0 + 1 : 0;
+  if (ns <= 1 && pre == 0) return;
+  const long long srow = ((long long)(b * g.nrt + rt) * g.nkv + hk + c0) * g.slot_s + (i - rt * g.ri) * g.G + h % g.G;
+  int np = 0;
+  long long prow = 0;
+  if (pre > 0) {
+    const int rp = r / g.rp, k = hk * g.nrp + rp;
+    const int p0 = k * pre / quota;
+    np = ((k + 1) * pre - 1) / quota - p0 + 1;
+    prow = g.pre_row0 + (long long)(k + p0) * g.slot_p + (r - rp * g.rp) * g.G + h % g.G;
+  }
+  const int nc = np + ns;
+  auto row_of = [&](int c) { return c < np ? prow + (long long)c * g.slot_p : srow + (long long)(c - np) * g.slot_s; };
+  float m = -INFINITY;
+  for (int c = lane; c < nc; c += 32) m = fmaxf(m, g.part_ml[row_of(c)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  constexpr int V = HD / 32;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, lsum = 0.f;
+  for (int cb = 0; cb < nc; cb += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (cb + lane < nc) ml = g.part_ml[row_of(cb + lane)];
+    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+    lsum += w * ml.y;
+    const int lim = min(32, nc - cb);
+#pragma unroll 8
+    for (int c = 0; c < lim; ++c) {
+      const float wc = __shfl_sync(0xffffffffu, w, c);
+      const float* src = g.part_o + row_of(cb + c) * HD + lane * V;
+      if (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        acc[0] += wc * x.x, acc[1] += wc * x.y, acc[2] += wc * x.z, acc[3] += wc * x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        acc[0] += wc * x.x, acc[1] += wc * x.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+  T* dst = out + ((long long)r * g.nq + h) * HD + lane * V;
+#pragma unroll
+  for (int e = 0; e < V; ++e) dst[e] = from_f<T>(acc[e] / lsum);
+}
+
+template <typename T, int HD, int KT>
+static cudaError_t merge_launch(const PagedGeom& g, void* out, cudaStream_t s) {
+  const long long items = (long long)g.batch * g.n * g.nq;
+  DFL_RET(launch_pdl(paged_merge_kernel<T, HD, KT>, dim3((unsigned)((items + 1) / 2)), dim3(64), 0, s, g, (T*)out));
+  count_launch();
+  return cudaSuccess;
+}
+
+// Fills in the split of a call: row groups of `ri` / `rp` rows and the partial slots.
+// Returns the partial rows it needs.
+static long long split_rows(PagedGeom& g, int ri, int rp, int grid, int min_quota) {
+  g.ri = ri;
+  g.rp = rp;
+  g.nrt = (g.n + ri - 1) / ri;
+  g.nrp = (int)(((long long)g.batch * g.n + rp - 1) / rp);
+  g.grid = grid;
+  g.min_quota = min_quota;
+  g.slot_s = std::min(g.n, ri) * g.G;
+  g.slot_p = (int)std::min<long long>((long long)g.batch * g.n, rp) * g.G;
+  g.pre_row0 = ((long long)g.batch * g.nrt * g.nkv + grid) * g.slot_s;
+  return g.pre_row0 + (g.shared ? ((long long)g.nrp * g.nkv + grid) * g.slot_p : 0);
+}
+
+// The line's tiles fit an int with room for the arithmetic on it, whatever the kernel:
+// the smallest row groups (16 stacked rows) and tiles.
+bool paged_line_fits(const PagedGeom& g) {
+  const int r = std::max(1, 16 / g.G);
+  const long long groups = (long long)g.batch * ((g.n + r - 1) / r) * (g.shared ? 2 : 1);
+  return (double)groups * g.nkv * ((double)g.cap / kCoreKeys + 2) < 1073741824.0;
+}
+
+template <typename T, int HD, int MRM>
+static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const void* vp, void* out,
+                               long long part_rows, cudaStream_t s) {
+  typedef CoreLayout<HD, MRM> L;
+  static int per_sm = 0;
+  if (!per_sm) {
+    DFL_RET(cudaFuncSetAttribute(paged_attn_core_kernel<T, HD, MRM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 L::kSmem));
+    int x = 0;
+    DFL_RET(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&x, paged_attn_core_kernel<T, HD, MRM>, kCoreThreads,
+                                                          L::kSmem));
+    per_sm = std::min(std::max(x, 1), kPagedMaxCtas);
+  }
+  const int r = L::MR / g.G;
+  if (split_rows(g, r, r, num_sms() * per_sm, 4) > part_rows) return cudaErrorInvalidValue;
+  const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
+  DFL_RET(launch_pdl(paged_attn_core_kernel<T, HD, MRM>, dim3(g.grid), dim3(kCoreThreads), L::kSmem, s, g, (const T*)q,
+                     (const T*)kp, (const T*)vp, (T*)out, scale_log2));
+  count_launch();
+  return merge_launch<T, HD, kCoreKeys>(g, out, s);
+}
+
+cudaError_t paged_attention(int dtype, int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp,
+                            void* out, long long part_rows, cudaStream_t s) {
+  // few stacked rows: the 16-row tile spends fewer products on padding
+  const bool small = (g.shared ? (long long)g.batch : 1) * g.n * g.G <= 16;
+#define DFL_CORE(T, HD)                                                            \
+  return small ? core_launch<T, HD, 1>(g, q, kp, vp, out, part_rows, s)            \
+               : core_launch<T, HD, 4>(g, q, kp, vp, out, part_rows, s)
+  if (dtype == DFLASH_F32) {
+    if (hd == 64) DFL_CORE(float, 64);
+    DFL_CORE(float, 128);
+  }
+  if (hd == 64) DFL_CORE(bf16, 64);
+  DFL_CORE(bf16, 128);
+#undef DFL_CORE
+}
+
+}  // namespace dfl

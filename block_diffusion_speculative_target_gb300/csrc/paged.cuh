@@ -1,0 +1,328 @@
+// Attention over pages: the call's geometry, the visible key range of a row,
+// and the split of a call's work over CTAs, shared by the tensor-core kernel,
+// the CUDA-core kernel and the merge of their partial results.
+//
+// Work.  An item is one KV head of one group of rows: a suffix item holds up
+// to `ri` consecutive rows of one sequence (its G query heads a row stacked),
+// a prefix item holds up to `rp` consecutive rows of the whole batch, whose
+// common keys [0, sh) are then read once for all of them.  An item's keys are
+// walked in tiles of KT keys at absolute multiples of KT, only those that some
+// row of it sees (first tokens that stay visible, then the window).  All tiles
+// of all items, in item order, form one line of T tiles that is cut into equal
+// runs of `quota` tiles, a run to a CTA, so every CTA has the same work
+// whatever the lengths; a CTA's run covers the end of one item, whole items,
+// and the start of another.  An item inside one run whose rows have no other
+// part is finished there; every other piece leaves a partial result (row
+// maximum, sum, unnormalised output) that a merge kernel adds up in tile
+// order.  Prefix items come first in the line, head by head; suffix items
+// follow in order of sequence, row group, head.  The cut depends on all
+// lengths of the call: a row's last bits may depend on the batch around it,
+// but the same call gives the same bits every time.
+#pragma once
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace dfl {
+
+struct PagedGeom {
+  int batch, n, nq, nkv, G;
+  int ri, rp;            // block rows of a suffix / prefix item
+  int nrt, nrp;          // row groups of a sequence / of the batch
+  int causal, window, sinks;
+  int ps, ps_log2, n_pages, table_stride;
+  int cap;               // keys a sequence's table row can name
+  int grid;              // CTAs of the attention kernel
+  int min_quota;
+  long long page_row0;   // pool row of (layer, page 0, head 0, slot 0)
+  const int32_t* len;
+  const int32_t* n_rows; // null: n
+  const int32_t* table;
+  const int32_t* shared; // null: no shared prefix
+  float* part_o;         // suffix slots, then prefix slots
+  float2* part_ml;
+  long long pre_row0;    // first partial row of the prefix slots
+  int slot_s, slot_p;    // partial rows per suffix / prefix slot
+  int32_t* plan;         // [8 + batch + 1] written for the merge kernel
+  int* status;
+};
+
+// Stacked rows (rows x query heads of a KV head) of one item at most, and the largest GQA group.
+constexpr int kPagedItemRows = 256;
+constexpr int kPagedMaxG = 64;
+// CTAs a SM of an attention kernel at most (bounds the partial slots).
+constexpr int kPagedMaxCtas = 4;
+
+// plan[]: kPlanT tiles of the line, quota, sh / KT, tiles of a prefix item; then the
+// line position of each sequence's first suffix item and the line's end.
+enum { kPlanT = 0, kPlanQuota = 1, kPlanShared = 2, kPlanPre = 3, kPlanCum = 8 };
+
+__device__ __forceinline__ int paged_rows(const PagedGeom& g, int b) {
+  return g.n_rows ? min(max(g.n_rows[b], 0), g.n) : g.n;
+}
+__device__ __forceinline__ int paged_len(const PagedGeom& g, int b) { return max(g.len[b], 0); }
+
+// The sequence's keys: those held and those of this call.
+__device__ __forceinline__ int key_limit(const PagedGeom& g, int b) {
+  return (int)min((long long)paged_len(g, b) + paged_rows(g, b), (long long)g.cap);
+}
+
+// First key of the window and end of the always-visible first keys of a row at
+// block index i of a sequence holding P keys: visible are [0, sink) and [lo, hi).
+__device__ __forceinline__ void row_span(const PagedGeom& g, int P, int rows, int i, int& sink, int& lo, int& hi) {
+  P = min(P, g.cap);  // (an overlong sequence is an error; its sums stay in range)
+  hi = min(g.causal ? P + i + 1 : P + rows, g.cap);
+  lo = 0;
+  sink = 0;
+  if (g.window > 0) {
+    lo = max(0, g.causal ? P + i - g.window + 1 : P - g.window);
+    sink = min(g.sinks, lo);
+  }
+}
+
+// The tiles of an item: [s0, s1) then [w0, w1), all multiples of KT keys.
+struct TileSpan {
+  int s0, s1, w0, w1;
+  __device__ __forceinline__ int count() const { return s1 - s0 + w1 - w0; }
+  __device__ __forceinline__ int tile(int t) const { return t < s1 - s0 ? s0 + t : w0 + t - (s1 - s0); }
+};
+
+template <int KT>
+__device__ __forceinline__ TileSpan suffix_span(const PagedGeom& g, int b, int rt, int sh_tiles) {
+  TileSpan s{0, 0, 0, 0};
+  const int rows = paged_rows(g, b), i0 = rt * g.ri;
+  if (i0 >= rows) return s;
+  const int P = paged_len(g, b), i1 = min(i0 + g.ri, rows) - 1;
+  int sink, lo, hi, sink1, lo1;
+  row_span(g, P, rows, i0, sink, lo, hi);    // the first row's window starts first
+  row_span(g, P, rows, i1, sink1, lo1, hi);  // the last row's ends last
+  s.w0 = max(lo / KT, sh_tiles);
+  s.w1 = max((hi + KT - 1) / KT, s.w0);
+  s.s0 = sh_tiles;
+  s.s1 = max(s.s0, min((sink1 + KT - 1) / KT, s.w0));
+  return s;
+}
+
+// The tiles of every prefix item: those below sh that some row of the batch may see
+// (min_len: the shortest live sequence).
+template <int KT>
+__device__ __forceinline__ TileSpan prefix_span(const PagedGeom& g, int sh_tiles, int min_len) {
+  TileSpan s{0, 0, 0, sh_tiles};
+  if (g.window > 0) {
+    const int lo = max(0, g.causal ? min_len - g.window + 1 : min_len - g.window);
+    s.w0 = min(lo / KT, sh_tiles);
+    s.s1 = min((int)((g.sinks + (long long)KT - 1) / KT), s.w0);
+  }
+  return s;
+}
+
+// A CTA's piece of one item.
+struct Segment {
+  bool prefix;
+  int b, rt, hk;      // suffix: sequence, row group, head; prefix: row group rt of the batch, keys named by b's table
+  TileSpan span;
+  int t0, nt, total;  // its tiles [t0, t0 + nt) of the item's `total`
+  long long slot_row; // first partial row of this piece
+};
+
+// The line as one CTA sees it.
+struct PlanView {
+  int T, quota, sh_tiles, min_len, pre_tiles;  // pre_tiles: tiles of one prefix item
+  int pre_b;   // the first live sequence: its table names the shared pages
+  int b, cum;  // the sequence that holds the CTA's first tile (past the prefix items), and its line position
+};
+
+// All threads of the block: the shared prefix, the line's length and where the CTA's run starts.
+// red: 2 NT / 32 + 8 ints of shared memory.  CTA 0 also writes the plan for the merge kernel.
+template <int KT, int NT>
+__device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  PlanView v;
+  const int per = (g.batch + NT - 1) / NT;
+  const int b0 = min(tid * per, g.batch), b1 = min(b0 + per, g.batch);
+  v.sh_tiles = 0;
+  v.min_len = 0;
+  v.pre_b = 0;
+  int* res = red + 2 * (NT / 32);
+  if (g.shared) {
+    int m = INT32_MAX, first = g.batch;
+    for (int b = b0; b < b1; ++b)
+      if (paged_rows(g, b) > 0) {
+        m = min(m, min(paged_len(g, b), g.cap));
+        first = min(first, b);
+      }
+    m = __reduce_min_sync(0xffffffffu, m);
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) {
+      red[warp] = m;
+      red[NT / 32 + warp] = first;
+    }
+    __syncthreads();
+    for (int w = 0; w < NT / 32; ++w) {
+      m = min(m, red[w]);
+      first = min(first, red[NT / 32 + w]);
+    }
+    v.min_len = m;
+    if (first < g.batch) {
+      v.sh_tiles = max(0, min(*g.shared, m)) / KT;
+      v.pre_b = first;
+    }
+    __syncthreads();
+  }
+  v.pre_tiles = v.sh_tiles > 0 ? prefix_span<KT>(g, v.sh_tiles, v.min_len).count() : 0;
+  const int pre_total = v.pre_tiles * g.nrp * g.nkv;
+  auto tiles_of = [&](int b) {
+    int c = 0;
+    for (int rt = 0; rt < g.nrt; ++rt) c += suffix_span<KT>(g, b, rt, v.sh_tiles).count();
+    return c * g.nkv;
+  };
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    sum += tiles_of(b);
+    if (blockIdx.x == 0 && paged_rows(g, b) > 0 && paged_len(g, b) > g.cap - paged_rows(g, b))
+      set_status(g.status, DFLASH_STATUS_CAPACITY);
+  }
+  int inc = sum;  // inclusive scan over the block
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) red[warp] = inc;
+  __syncthreads();
+  int base = pre_total, tot = pre_total;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) base += red[w];
+    tot += red[w];
+  }
+  v.T = tot;
+  v.quota = max(g.min_quota, (tot + g.grid - 1) / g.grid);
+  const int start = max((int)min((long long)blockIdx.x * v.quota, (long long)tot), pre_total);
+  int at = base + inc - sum;
+  if (tid == 0) {
+    res[0] = g.batch;
+    res[1] = tot;
+  }
+  __syncthreads();
+  for (int b = b0; b < b1; ++b) {
+    const int c = per == 1 ? sum : tiles_of(b);
+    if (blockIdx.x == 0) g.plan[kPlanCum + b] = at;
+    if (start >= at && start < at + c) {
+      res[0] = b;
+      res[1] = at;
+    }
+    at += c;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    g.plan[kPlanT] = v.T;
+    g.plan[kPlanQuota] = v.quota;
+    g.plan[kPlanShared] = v.sh_tiles;
+    g.plan[kPlanPre] = v.pre_tiles;
+    g.plan[kPlanCum + g.batch] = tot;
+  }
+  __syncthreads();
+  v.b = res[0];
+  v.cum = res[1];
+  return v;
+}
+
+// Walks a CTA's run piece by piece.  Every role of the CTA runs its own copy.
+template <int KT>
+struct SegmentWalk {
+  const PagedGeom& g;
+  const PlanView& v;
+  int pos, end;       // the run: line positions
+  int b, rt, hk;      // the next suffix item
+  int item_at;        // its line position
+  int pre_total;
+  __device__ __forceinline__ SegmentWalk(const PagedGeom& g_, const PlanView& v_) : g(g_), v(v_) {
+    pos = (int)min((long long)blockIdx.x * v.quota, (long long)v.T);
+    end = (int)min((long long)pos + v.quota, (long long)v.T);
+    pre_total = v.pre_tiles * g.nrp * g.nkv;
+    b = v.b;
+    item_at = v.cum;
+    rt = hk = 0;
+  }
+  __device__ __forceinline__ bool next(Segment& s) {
+    if (pos >= end) return false;
+    int ordinal;
+    if (pos < pre_total) {
+      const int k = pos / v.pre_tiles;
+      s.prefix = true;
+      s.hk = k / g.nrp;
+      s.rt = k - s.hk * g.nrp;
+      s.b = v.pre_b;
+      s.span = prefix_span<KT>(g, v.sh_tiles, v.min_len);
+      s.total = v.pre_tiles;
+      s.t0 = pos - k * v.pre_tiles;
+      ordinal = k;
+    } else {
+      TileSpan sp;
+      int c;
+      while (true) {  // ends: pos < T, so some item holds it
+        sp = suffix_span<KT>(g, b, rt, v.sh_tiles);
+        c = sp.count();
+        if (pos < item_at + c * g.nkv) break;
+        item_at += c * g.nkv;
+        if (++rt == g.nrt) {
+          rt = 0;
+          ++b;
+        }
+      }
+      hk = (pos - item_at) / c;
+      s.prefix = false;
+      s.b = b;
+      s.rt = rt;
+      s.hk = hk;
+      s.span = sp;
+      s.total = c;
+      s.t0 = pos - item_at - hk * c;
+      ordinal = (b * g.nrt + rt) * g.nkv + hk;
+    }
+    s.nt = min(s.total - s.t0, end - pos);
+    pos += s.nt;
+    const long long slot = (long long)ordinal + blockIdx.x;
+    s.slot_row = s.prefix ? g.pre_row0 + slot * g.slot_p : slot * g.slot_s;
+    return true;
+  }
+  // No other piece contributes to this one's rows.
+  __device__ __forceinline__ bool whole(const Segment& s) const {
+    return !s.prefix && s.nt == s.total && v.pre_tiles == 0;
+  }
+};
+
+// Block index and validity of the item row `r` (block row r / G, head r % G).
+struct ItemRow {
+  int b, i, head;
+  bool live;
+};
+__device__ __forceinline__ ItemRow item_row(const PagedGeom& g, const Segment& s, int r, int r_max) {
+  ItemRow w;
+  const int q = r / g.G;
+  w.head = s.hk * g.G + (r - q * g.G);
+  if (s.prefix) {
+    const int f = s.rt * g.rp + q;
+    w.live = q < r_max && f < g.batch * g.n;
+    const int fc = w.live ? f : 0;
+    w.b = fc / g.n;
+    w.i = fc - w.b * g.n;
+  } else {
+    w.b = s.b;
+    w.i = s.rt * g.ri + q;
+    w.live = q < r_max;
+  }
+  w.live = w.live && w.i < paged_rows(g, w.b);
+  return w;
+}
+
+cudaError_t rope_table(float2* tab, int max_pos, int half, double theta);
+cudaError_t paged_append(int in_dtype, int dtype, const void* qkv, long long ld, int batch, int n, int nq, int nkv,
+                         int hd, const int32_t* n_rows, const int32_t* table, int table_stride, const int32_t* len,
+                         const float2* tab, int max_pos, int n_pages, int ps, long long page0, void* qout, void* kp,
+                         void* vp, int* status, cudaStream_t s);
+bool paged_line_fits(const PagedGeom& g);
+// Attention of a call described by `g` (geometry, table, lengths; the split is filled in here).
+cudaError_t paged_attention(int dtype, int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp,
+                            void* out, long long part_rows, cudaStream_t s);
+
+}  // namespace dfl

@@ -358,3 +358,114 @@ class Session:
         torch.cuda.current_stream().wait_stream(s)
         return g
 
+
+
+class PagedCache:
+    """A pool of KV pages with the append and attention calls on it.
+
+    ``shape`` and ``dtype`` as for ``Model``.  The pool is two tensors ``k`` and
+    ``v`` [n_layers][n_pages][n_kv][page_size][head_dim]; pass them (a 4-d pair
+    is one layer) or leave them out to have zeroed ones made.  Tables, lengths
+    and row counts are the caller's device int32 tensors: ``table``
+    [batch][columns] names the page of each ``page_size`` positions, ``lengths``
+    [batch] the positions held before a call's rows, ``n_rows`` [batch] the rows
+    of each sequence in the call (None: all).  Calls are asynchronous on the
+    current stream and leave ``lengths`` as it is."""
+
+    def __init__(self, shape, dtype: str, n_pages, page_size, max_pos, max_rows, max_batch=None, n_layers=1, k=None,
+                 v=None, device="cuda"):
+        self.dtype, self.tdt = dtype, _DT[dtype][1]
+        self.nq, self.nkv, self.hd = shape.n_q, shape.n_kv, shape.head_dim
+        self.page_size, self.max_pos = page_size, max_pos
+        self.pages = self.ws = None
+        dims = (n_layers, n_pages, self.nkv, page_size, self.hd)
+        if (k is None) != (v is None):
+            raise ValueError("pass both pools or neither")
+        if k is None:
+            k, v = (torch.zeros(dims, dtype=self.tdt, device=device) for _ in range(2))
+        for t in (k, v):
+            if t.dtype != self.tdt or not t.is_cuda or not t.is_contiguous() or \
+                    tuple(t.shape) != (dims if t.dim() == 5 else dims[1:]) or (t.dim() == 4 and n_layers != 1):
+                raise ValueError(f"a pool is a contiguous {self.tdt} tensor {dims} on the GPU")
+        self.k, self.v, self.device = k, v, k.device
+        if v.device != self.device:
+            raise ValueError("the pools are on different devices")
+        desc = desc_of(shape, dtype, n_layers)
+        with torch.cuda.device(self.device):
+            self.pages = capi.dflash_pages_create(desc, n_layers, n_pages, page_size, max_pos, k, v)
+            self.ws = capi.dflash_paged_workspace_alloc(desc, max_batch or max_rows, max_rows)
+
+    def close(self):
+        """Frees the handle and the workspace (the pool is torch's).  Work of
+        the calls made so far has to be done."""
+        if self.pages:
+            capi.dflash_pages_free(self.pages)
+        if self.ws:
+            capi.dflash_paged_workspace_free(self.ws)
+        self.pages = self.ws = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def status(self):
+        return capi.dflash_paged_status(self.ws)
+
+    def _index(self, t, what, dims):
+        if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous() or tuple(t.shape) != dims:
+            raise ValueError(f"{what} is a contiguous int32 tensor {dims} on {self.device}")
+        return t
+
+    def _calls(self, table, lengths, n_rows):
+        batch = lengths.shape[0] if lengths.dim() else 0
+        if table.dim() != 2:
+            raise ValueError("table is [batch][columns]")
+        self._index(lengths, "lengths", (batch,))
+        self._index(table, "table", (batch, table.shape[1]))
+        if n_rows is not None:
+            self._index(n_rows, "n_rows", (batch,))
+        return batch
+
+    def _rows(self, t, what, batch, n):
+        if t.dtype != self.tdt or t.device != self.device or not t.is_contiguous() or \
+                t.numel() != batch * n * self.nq * self.hd:
+            raise ValueError(f"{what} is a contiguous {self.tdt} tensor [{batch}][{n}][{self.nq}][{self.hd}] on {self.device}")
+        return t
+
+    def append(self, layer, qkv, table, lengths, n, q_out=None, n_rows=None):
+        """Rotate and append ``n`` rows a sequence.  ``qkv`` [batch * n][...]
+        float32 or the pool's type, q|k|v heads side by side (k|v without
+        ``q_out``); its rows may be apart.  ``q_out`` receives the rotated
+        queries."""
+        batch = self._calls(table, lengths, n_rows)
+        width = ((0 if q_out is None else self.nq) + 2 * self.nkv) * self.hd
+        if qkv.dim() != 2 or tuple(qkv.shape) != (batch * n, width) or qkv.device != self.device or \
+                (qkv.stride(1) != 1 and width > 1) or qkv.dtype not in (torch.float32, self.tdt):
+            raise ValueError(f"qkv is a float32 or {self.tdt} tensor [{batch * n}][{width}] on {self.device}, its rows unbroken")
+        if q_out is not None:
+            self._rows(q_out, "q_out", batch, n)
+        ld = qkv.stride(0) if qkv.shape[0] > 1 else width
+        capi.dflash_paged_append(self.pages, layer, capi.F32 if qkv.dtype == torch.float32 else capi.BF16, qkv, ld,
+                                 batch, n, n_rows, table, table.shape[1], lengths, q_out, self.ws)
+
+    def attention(self, layer, q, table, lengths, out, causal=True, window=0, sinks=0, n_rows=None, shared_len=None):
+        """Attention of ``q`` [batch][n][n_q][head_dim] over the pages into
+        ``out``.  ``window`` > 0 hides keys behind it but the first ``sinks``;
+        ``shared_len`` (one device int32) says how many first positions all
+        sequences share, to be read once for the batch."""
+        batch = self._calls(table, lengths, n_rows)
+        if not batch or q.dim() != 4 or q.shape[0] != batch:
+            raise ValueError("q is [batch][n][n_q][head_dim]")
+        n = q.shape[1]
+        self._rows(q, "q", batch, n)
+        self._rows(out, "out", batch, n)
+        if shared_len is None:
+            capi.dflash_paged_attention(self.pages, layer, q, batch, n, n_rows, int(causal), window, sinks, table,
+                                        table.shape[1], lengths, out, self.ws)
+        else:
+            if shared_len.dtype != torch.int32 or shared_len.device != self.device or shared_len.numel() != 1:
+                raise ValueError(f"shared_len is one int32 on {self.device}")
+            capi.dflash_paged_attention_shared(self.pages, layer, q, batch, n, n_rows, int(causal), window, sinks, table,
+                                               table.shape[1], lengths, shared_len, out, self.ws)

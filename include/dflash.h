@@ -451,6 +451,97 @@ int dflash_attention(const dflash_model_desc *d, const void *q, int32_t batch, i
                      int32_t causal, int32_t window, dflash_cache *cache, int32_t layer, void *out,
                      dflash_workspace *ws, dflash_stream_t stream);
 
+/* ----------------------------------------------------------------- KV pages
+ * Keys and values of many sequences in pages of a common pool, for callers
+ * that schedule more sequences than fit as whole caches or let sequences share
+ * pages.  Not an operation of the method's pages ([DD] keeps one cache per
+ * sequence); the same rotation and scaled dot-product attention, with another
+ * place for the keys.  These calls stand beside dflash_attention: they take
+ * any batch, rows of any number up to the workspace's, float32 or bf16 with
+ * head_dim 64 or 128 and up to 64 query heads per KV head.
+ *
+ * The pool is the caller's memory: k and v, each
+ * [n_layers][n_pages][n_kv][page_size][head_dim] in the model dtype, 16-byte
+ * aligned, kept alive while the handle lives.  Copying, swapping or sharing
+ * pages is the caller's.  page_size is 16, 32, 64 or 128.
+ *
+ * Every call takes, as device int32 arrays read when the kernels run:
+ *   table [batch][table_stride]  page of each page_size positions: position p
+ *                                of sequence b is slot p % page_size of page
+ *                                table[b][p / page_size].  Only entries of
+ *                                positions that are written or visible are read;
+ *   len [batch]                  positions held before this call's rows;
+ *   n_rows [batch] (nullable)    rows of the sequence in this call, 0..n (values
+ *                                outside are clamped); NULL: n for all.  Rows at
+ *                                or past it are padding: their inputs are not
+ *                                used and their outputs are left as they were.
+ * len does not move: the caller adds the rows it keeps, after its last layer.
+ * Device conditions set bits in the workspace's status word: a position past
+ * the table or past max_pos sets DFLASH_STATUS_CAPACITY, a page outside
+ * [0, n_pages) DFLASH_STATUS_BOUNDS; that write is skipped, that sequence's
+ * attention output is unspecified, other sequences are not touched. */
+typedef struct dflash_pages dflash_pages;
+/* The handle: geometry, the rotation table (cos/sin of positions
+ * 0..max_pos-1, angles in double precision, library-owned device memory) and
+ * the pool's tensor maps.  Bound to the device current at the call; calls with
+ * another device current return DFLASH_ERR_INVALID_ARG.  d supplies head
+ * counts, head_dim, rope_theta and dtype. */
+int dflash_pages_create(const dflash_model_desc *d, int32_t n_layers, int32_t n_pages, int32_t page_size,
+                        int32_t max_pos, void *k, void *v, dflash_pages **out);
+int dflash_pages_free(dflash_pages *p);
+/* Scratch for the attention calls on handles of d's head counts and head_dim,
+ * with at most max_batch sequences and batch * n <= max_rows, and a status
+ * word.  Library-owned; one workspace serves one stream at a time, and so do
+ * graphs captured with it: graphs that may run at once need one each. */
+typedef struct dflash_paged_workspace dflash_paged_workspace;
+int dflash_paged_workspace_alloc(const dflash_model_desc *d, int32_t max_batch, int32_t max_rows,
+                                 dflash_paged_workspace **out);
+int dflash_paged_workspace_free(dflash_paged_workspace *w);
+/* Synchronises `stream`, returns the status bits in *status_out and clears them. */
+int dflash_paged_status(dflash_paged_workspace *w, dflash_stream_t stream, int32_t *status_out);
+
+/* Append with the rotation on the way: row (b, j), j < n_rows[b], of qkv
+ * [batch][n] rows of q|k|v heads, ld elements apart (ld >= (nq + 2 nkv) * hd),
+ * sits at position len[b] + j.  q and k are rotated at that position
+ * (rotate-half pairs, float32, rounded once); q goes to q_out
+ * [batch][n][nq][hd] (model dtype, 16-byte aligned), k and v into the pages.
+ * q_out NULL: the rows hold k|v only (injected context).  in_dtype is the type
+ * of qkv: the model dtype, or float32 (the weight product's result).  qkv may
+ * have any alignment of its type; rows on 16-byte boundaries are read in wide
+ * loads.  No two rows of one call may name the same slot. */
+int dflash_paged_append(dflash_pages *p, int32_t layer, int32_t in_dtype, const void *qkv, int64_t ld,
+                        int32_t batch, int32_t n, const int32_t *n_rows, const int32_t *table,
+                        int32_t table_stride, const int32_t *len, void *q_out, dflash_paged_workspace *ws,
+                        dflash_stream_t stream);
+
+/* Attention over pages.  q [batch][n][nq][hd] (rotated, model dtype, 16-byte
+ * aligned), the rows' own keys and values already appended; out likewise.
+ * Row (b, i) at position p = len[b] + i sees key j of its sequence when
+ *   causal      j <= p            and (j > p - window or j < sinks),
+ *   not causal  j < len[b] + n_rows[b]  and (j >= len[b] - window or j < sinks);
+ * window = 0 drops the second condition (sinks is then ignored).  The causal
+ * window slides with each row; the other is dflash_attention's, the drafter's
+ * cross-context window, with first tokens kept.  scale 1 / sqrt(hd), softmax
+ * in float32; a row's result depends on the keys it sees only, whatever values
+ * lie in hidden or unused slots.  The keys are split over the GPU by all
+ * lengths of the call, so the last bits of a row may depend on the batch it is
+ * in (dflash_attention, which fixes the split per cache, has no such
+ * dependence); equal calls give equal bits. */
+int dflash_paged_attention(dflash_pages *p, int32_t layer, const void *q, int32_t batch, int32_t n,
+                           const int32_t *n_rows, int32_t causal, int32_t window, int32_t sinks,
+                           const int32_t *table, int32_t table_stride, const int32_t *len, void *out,
+                           dflash_paged_workspace *ws, dflash_stream_t stream);
+/* The same for a batch whose first *shared_len positions (device int32) hold
+ * the same keys and values in every sequence with rows in this call: those are
+ * read once for the whole batch, from the pages that the first such sequence's
+ * table names, with all sequences' rows stacked against them.  Values of
+ * *shared_len outside [0, min len] are clamped to it. */
+int dflash_paged_attention_shared(dflash_pages *p, int32_t layer, const void *q, int32_t batch, int32_t n,
+                                  const int32_t *n_rows, int32_t causal, int32_t window, int32_t sinks,
+                                  const int32_t *table, int32_t table_stride, const int32_t *len,
+                                  const int32_t *shared_len, void *out, dflash_paged_workspace *ws,
+                                  dflash_stream_t stream);
+
 /* Kernel timing for measurement passes (not for graph capture): between
  * begin and end, the library brackets each weight-GEMM launch with a CUDA
  * event pair on the launching stream, up to max_records launches.  end
