@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "paged.cuh"
 
 namespace dfl {
 
@@ -235,6 +236,22 @@ int attn_group_tiles(int capacity, int nkv) {
   while (g < 64 && (double)g * 1.41421356 < x) g *= 2;
   while (g < 64 && (long long)((tiles + g - 1) / g) * nkv > sms) ++g;
   return g;
+}
+
+bool make_page_maps(const void* k, const void* v, long long rows, int hd, int page_size, CUtensorMap* mk,
+                    CUtensorMap* mv) {
+  const PFN_encodeTiled_t fn = encoder();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)hd * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)page_size};
+  cuuint32_t es[2] = {1, 1};
+  for (int i = 0; i < 2; ++i)
+    if (fn(i == 0 ? mk : mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(i == 0 ? k : v), dims, strides, box,
+           es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
 }
 
 bool make_q_map(const void* q, int rows, int nq, int G, CUtensorMap* out) {

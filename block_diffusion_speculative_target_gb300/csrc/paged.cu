@@ -187,7 +187,6 @@ __global__ void __launch_bounds__(kCoreThreads)
   SegmentWalk<kCoreKeys> walk(g, v);
   Segment sg;
   while (walk.next(sg)) {
-    const int r_max = sg.prefix ? g.rp : g.ri;
     ItemRow row[MRM];
     int sink[MRM], lo[MRM], hi[MRM];
     float m[MRM], l[MRM], o[MRM][NC * 4];
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(kCoreThreads)
 #pragma unroll
     for (int x = 0; x < MRM; ++x) {
       const int r = rq + 16 * x;
-      row[x] = item_row(g, sg, r, r_max);
+      row[x] = item_row(g, sg, r);
       sink[x] = lo[x] = hi[x] = 0;
       if (row[x].live) row_span(g, paged_len(g, row[x].b), paged_rows(g, row[x].b), row[x].i, sink[x], lo[x], hi[x]);
       m[x] = -INFINITY;
@@ -342,22 +341,22 @@ __global__ void __launch_bounds__(64) paged_merge_kernel(const __grid_constant__
   const int b = r / g.n, i = r - b * g.n;
   if (i >= paged_rows(g, b)) return;
   const int quota = g.plan[kPlanQuota], sh = g.plan[kPlanShared], pre = g.plan[kPlanPre];
-  const int hk = h / g.G, rt = i / g.ri;
+  const int hk = h / g.G, x = i * g.G + h % g.G, rt = x / g.ri;
   // its sequence's own pieces
   int at = g.plan[kPlanCum + b];
-  for (int x = 0; x < rt; ++x) at += suffix_span<KT>(g, b, x, sh).count() * g.nkv;
+  for (int y = 0; y < rt; ++y) at += suffix_span<KT>(g, b, y, sh).count() * g.nkv;
   const int cnt = suffix_span<KT>(g, b, rt, sh).count();
   at += hk * cnt;
   const int c0 = at / quota, ns = cnt > 0 ? (at + cnt - 1) / quota - c0 + 1 : 0;
   if (ns <= 1 && pre == 0) return;
-  const long long srow = ((long long)(b * g.nrt + rt) * g.nkv + hk + c0) * g.slot_s + (i - rt * g.ri) * g.G + h % g.G;
+  const long long srow = ((long long)(b * g.nrt + rt) * g.nkv + hk + c0) * g.slot_s + x - rt * g.ri;
   int np = 0;
   long long prow = 0;
   if (pre > 0) {
-    const int rp = r / g.rp, k = hk * g.nrp + rp;
+    const int xp = r * g.G + h % g.G, rp = xp / g.rp, k = hk * g.nrp + rp;
     const int p0 = k * pre / quota;
     np = ((k + 1) * pre - 1) / quota - p0 + 1;
-    prow = g.pre_row0 + (long long)(k + p0) * g.slot_p + (r - rp * g.rp) * g.G + h % g.G;
+    prow = g.pre_row0 + (long long)(k + p0) * g.slot_p + xp - rp * g.rp;
   }
   const int nc = np + ns;
   auto row_of = [&](int c) { return c < np ? prow + (long long)c * g.slot_p : srow + (long long)(c - np) * g.slot_s; };
@@ -400,18 +399,21 @@ static cudaError_t merge_launch(const PagedGeom& g, void* out, cudaStream_t s) {
   count_launch();
   return cudaSuccess;
 }
+cudaError_t paged_merge_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t s) {
+  return hd == 64 ? merge_launch<bf16, 64, kPagedTcKeys>(g, out, s) : merge_launch<bf16, 128, kPagedTcKeys>(g, out, s);
+}
 
-// Fills in the split of a call: row groups of `ri` / `rp` rows and the partial slots.
+// Fills in the split of a call: row groups of `ri` / `rp` stacked rows and the partial slots.
 // Returns the partial rows it needs.
-static long long split_rows(PagedGeom& g, int ri, int rp, int grid, int min_quota) {
+long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_quota) {
   g.ri = ri;
   g.rp = rp;
-  g.nrt = (g.n + ri - 1) / ri;
-  g.nrp = (int)(((long long)g.batch * g.n + rp - 1) / rp);
+  g.nrt = (g.n * g.G + ri - 1) / ri;
+  g.nrp = (g.batch * g.n * g.G + rp - 1) / rp;
   g.grid = grid;
   g.min_quota = min_quota;
-  g.slot_s = std::min(g.n, ri) * g.G;
-  g.slot_p = (int)std::min<long long>((long long)g.batch * g.n, rp) * g.G;
+  g.slot_s = std::min(g.n * g.G, ri);
+  g.slot_p = std::min(g.batch * g.n * g.G, rp);
   g.pre_row0 = ((long long)g.batch * g.nrt * g.nkv + grid) * g.slot_s;
   return g.pre_row0 + (g.shared ? ((long long)g.nrp * g.nkv + grid) * g.slot_p : 0);
 }
@@ -419,8 +421,7 @@ static long long split_rows(PagedGeom& g, int ri, int rp, int grid, int min_quot
 // The line's tiles fit an int with room for the arithmetic on it, whatever the kernel:
 // the smallest row groups (16 stacked rows) and tiles.
 bool paged_line_fits(const PagedGeom& g) {
-  const int r = std::max(1, 16 / g.G);
-  const long long groups = (long long)g.batch * ((g.n + r - 1) / r) * (g.shared ? 2 : 1);
+  const long long groups = (long long)g.batch * ((g.n * g.G + 15) / 16) * (g.shared ? 2 : 1);
   return (double)groups * g.nkv * ((double)g.cap / kCoreKeys + 2) < 1073741824.0;
 }
 
@@ -437,8 +438,7 @@ static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const
                                                           L::kSmem));
     per_sm = std::min(std::max(x, 1), kPagedMaxCtas);
   }
-  const int r = L::MR / g.G;
-  if (split_rows(g, r, r, num_sms() * per_sm, 4) > part_rows) return cudaErrorInvalidValue;
+  if (paged_split(g, L::MR, L::MR, num_sms() * per_sm, 4) > part_rows) return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
   DFL_RET(launch_pdl(paged_attn_core_kernel<T, HD, MRM>, dim3(g.grid), dim3(kCoreThreads), L::kSmem, s, g, (const T*)q,
                      (const T*)kp, (const T*)vp, (T*)out, scale_log2));
@@ -446,19 +446,15 @@ static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const
   return merge_launch<T, HD, kCoreKeys>(g, out, s);
 }
 
-cudaError_t paged_attention(int dtype, int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp,
-                            void* out, long long part_rows, cudaStream_t s) {
+cudaError_t paged_attention_core(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp,
+                                 void* out, long long part_rows, cudaStream_t s) {
   // few stacked rows: the 16-row tile spends fewer products on padding
-  const bool small = (g.shared ? (long long)g.batch : 1) * g.n * g.G <= 16;
-#define DFL_CORE(T, HD)                                                            \
-  return small ? core_launch<T, HD, 1>(g, q, kp, vp, out, part_rows, s)            \
-               : core_launch<T, HD, 4>(g, q, kp, vp, out, part_rows, s)
-  if (dtype == DFLASH_F32) {
-    if (hd == 64) DFL_CORE(float, 64);
-    DFL_CORE(float, 128);
-  }
-  if (hd == 64) DFL_CORE(bf16, 64);
-  DFL_CORE(bf16, 128);
+  const bool small = (g.shared ? g.batch : 1) * g.n * g.G <= 16;
+#define DFL_CORE(HD)                                                                    \
+  return small ? core_launch<float, HD, 1>(g, q, kp, vp, out, part_rows, s)            \
+               : core_launch<float, HD, 4>(g, q, kp, vp, out, part_rows, s)
+  if (hd == 64) DFL_CORE(64);
+  DFL_CORE(128);
 #undef DFL_CORE
 }
 

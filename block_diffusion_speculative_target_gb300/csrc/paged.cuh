@@ -2,9 +2,10 @@
 // and the split of a call's work over CTAs, shared by the tensor-core kernel,
 // the CUDA-core kernel and the merge of their partial results.
 //
-// Work.  An item is one KV head of one group of rows: a suffix item holds up
-// to `ri` consecutive rows of one sequence (its G query heads a row stacked),
-// a prefix item holds up to `rp` consecutive rows of the whole batch, whose
+// Work.  The G query heads that share a KV head are stacked: stacked row
+// i G + h is head h of block row i.  An item is one KV head and one group of
+// stacked rows: a suffix item holds up to `ri` consecutive ones of one
+// sequence, a prefix item up to `rp` consecutive ones of the whole batch, whose
 // common keys [0, sh) are then read once for all of them.  An item's keys are
 // walked in tiles of KT keys at absolute multiples of KT, only those that some
 // row of it sees (first tokens that stay visible, then the window).  All tiles
@@ -27,7 +28,7 @@ namespace dfl {
 
 struct PagedGeom {
   int batch, n, nq, nkv, G;
-  int ri, rp;            // block rows of a suffix / prefix item
+  int ri, rp;            // stacked rows of a suffix / prefix item
   int nrt, nrp;          // row groups of a sequence / of the batch
   int causal, window, sinks;
   int ps, ps_log2, n_pages, table_stride;
@@ -90,9 +91,9 @@ struct TileSpan {
 template <int KT>
 __device__ __forceinline__ TileSpan suffix_span(const PagedGeom& g, int b, int rt, int sh_tiles) {
   TileSpan s{0, 0, 0, 0};
-  const int rows = paged_rows(g, b), i0 = rt * g.ri;
-  if (i0 >= rows) return s;
-  const int P = paged_len(g, b), i1 = min(i0 + g.ri, rows) - 1;
+  const int rows = paged_rows(g, b), r0 = rt * g.ri;
+  if (r0 >= rows * g.G) return s;
+  const int P = paged_len(g, b), i0 = r0 / g.G, i1 = (min(r0 + g.ri, rows * g.G) - 1) / g.G;
   int sink, lo, hi, sink1, lo1;
   row_span(g, P, rows, i0, sink, lo, hi);    // the first row's window starts first
   row_span(g, P, rows, i1, sink1, lo1, hi);  // the last row's ends last
@@ -291,25 +292,24 @@ struct SegmentWalk {
   }
 };
 
-// Block index and validity of the item row `r` (block row r / G, head r % G).
+// Block row and head of the item's stacked row r, and whether it is a row of the call.
 struct ItemRow {
   int b, i, head;
   bool live;
 };
-__device__ __forceinline__ ItemRow item_row(const PagedGeom& g, const Segment& s, int r, int r_max) {
+__device__ __forceinline__ ItemRow item_row(const PagedGeom& g, const Segment& s, int r) {
   ItemRow w;
-  const int q = r / g.G;
-  w.head = s.hk * g.G + (r - q * g.G);
+  const int x = s.rt * (s.prefix ? g.rp : g.ri) + r, q = x / g.G;
+  w.head = s.hk * g.G + (x - q * g.G);
+  w.live = r < (s.prefix ? g.rp : g.ri);
   if (s.prefix) {
-    const int f = s.rt * g.rp + q;
-    w.live = q < r_max && f < g.batch * g.n;
-    const int fc = w.live ? f : 0;
-    w.b = fc / g.n;
-    w.i = fc - w.b * g.n;
+    w.live = w.live && q < g.batch * g.n;
+    const int f = w.live ? q : 0;
+    w.b = f / g.n;
+    w.i = f - w.b * g.n;
   } else {
     w.b = s.b;
-    w.i = s.rt * g.ri + q;
-    w.live = q < r_max;
+    w.i = q;
   }
   w.live = w.live && w.i < paged_rows(g, w.b);
   return w;
@@ -321,8 +321,21 @@ cudaError_t paged_append(int in_dtype, int dtype, const void* qkv, long long ld,
                          const float2* tab, int max_pos, int n_pages, int ps, long long page0, void* qout, void* kp,
                          void* vp, int* status, cudaStream_t s);
 bool paged_line_fits(const PagedGeom& g);
-// Attention of a call described by `g` (geometry, table, lengths; the split is filled in here).
-cudaError_t paged_attention(int dtype, int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp,
-                            void* out, long long part_rows, cudaStream_t s);
+// Fills in the split of a call: row groups of `ri` / `rp` stacked rows, the grid, the partial slots.
+// Returns the partial rows that it needs.
+long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_quota);
+// Keys of a tile of the tensor-core kernel.
+constexpr int kPagedTcKeys = 128;
+// Merge of the tensor-core kernel's partials.
+cudaError_t paged_merge_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t s);
+// Attention of a call described by `g` (geometry, table, lengths; the split is filled in here): float32 on
+// the CUDA cores, bf16 on the tensor cores.
+cudaError_t paged_attention_core(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
+                                 long long part_rows, cudaStream_t s);
+cudaError_t paged_attention_tc(int hd, const PagedGeom& g, const CUtensorMap& tk, const CUtensorMap& tv,
+                               long long pool_rows, const void* q, void* out, long long part_rows, cudaStream_t s);
+// 2-D maps over a bf16 pool [rows][hd]: boxes of 64 elements (128 B, swizzled) by one page's positions.
+bool make_page_maps(const void* k, const void* v, long long rows, int hd, int page_size, CUtensorMap* mk,
+                    CUtensorMap* mv);
 
 }  // namespace dfl

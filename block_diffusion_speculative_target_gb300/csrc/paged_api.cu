@@ -14,6 +14,7 @@ struct dflash_pages {
   int device;
   void *k, *v;     // the caller's pool
   float2* rope;    // [max_pos][hd / 2]
+  CUtensorMap tk, tv;  // bf16: over the whole pool
 };
 
 struct dflash_paged_workspace {
@@ -36,6 +37,9 @@ struct dflash_paged_workspace {
     if (!(cond)) return DFLASH_ERR_INVALID_ARG; \
   } while (0)
 
+static long long pool_rows(const dflash_pages* p) {
+  return (long long)p->n_layers * p->n_pages * p->nkv * p->page_size;
+}
 static bool on_device(int device) {
   int d = -1;
   return cudaGetDevice(&d) == cudaSuccess && d == device;
@@ -57,7 +61,11 @@ int dflash_pages_create(const dflash_model_desc* d, int32_t n_layers, int32_t n_
   dflash_pages* p = new (std::nothrow) dflash_pages();
   if (!p) return DFLASH_ERR_OOM;
   *p = dflash_pages{n_layers, n_pages, page_size, max_pos, d->n_q_heads, d->n_kv_heads, d->head_dim, d->dtype,
-                    0,        k,       v,         nullptr};
+                    0,        k,       v,         nullptr, {},           {}};
+  if (p->dtype == DFLASH_BF16 && !make_page_maps(k, v, pool_rows(p), p->hd, page_size, &p->tk, &p->tv)) {
+    delete p;
+    return record_cuda_error(cudaErrorInvalidValue);
+  }
   cudaError_t e = cudaGetDevice(&p->device);
   if (e == cudaSuccess) {
     const int half = d->head_dim / 2;
@@ -197,7 +205,10 @@ static int attend(dflash_pages* p, int32_t layer, const void* q, int32_t batch, 
   g.plan = ws->plan;
   g.status = ws->status;
   if (!paged_line_fits(g)) return DFLASH_ERR_TOO_LARGE;
-  CK(paged_attention(p->dtype, p->hd, g, q, p->k, p->v, out, ws->part_rows, (cudaStream_t)stream));
+  if (p->dtype == DFLASH_BF16)
+    CK(paged_attention_tc(p->hd, g, p->tk, p->tv, pool_rows(p), q, out, ws->part_rows, (cudaStream_t)stream));
+  else
+    CK(paged_attention_core(p->hd, g, q, p->k, p->v, out, ws->part_rows, (cudaStream_t)stream));
   return DFLASH_OK;
 }
 
