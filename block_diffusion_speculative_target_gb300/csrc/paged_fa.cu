@@ -3,27 +3,35 @@
 //
 // Two groups of four softmax warps work independently, each with a score
 // buffer S and an output accumulator O in TMEM and a warp that issues its
-// products, so one group's exponentials run under the other's products:
-//   S = Q K_t^T            128 stacked rows by 128 keys, fp32 in TMEM
-//   reference max M: the row's first tile sets it, a later tile raises it only
-//     when its own max exceeds M by more than 8 (log2 units); then O and the
-//     row sum L are rescaled by 2^(M_old - M_new)
-//   P = 2^(s - M)          <= 2^8, written over S as bf16
-//   O += P V_t             A operand from TMEM, fp32 in TMEM
-// An item of at most 128 stacked rows (few rows against many keys) has one
-// query tile; the groups take its key tiles in turn and their (M, L, O) are
-// joined at the end.  There P is kept as a bf16 pair hi + lo (about 2^-17
-// relative) and multiplied in two passes: such items wait for keys, not for
-// products.  An item of more rows has two query tiles, one a group, that share
-// every key tile, which halves the traffic from L2; there the products bound,
-// and P is rounded to bf16 once (2^-9 relative a weight, the size of the
-// result's own rounding).
+// products, so one group's exponentials run under the other's products.
+// For every row a reference M: the row's first visible keys set it, a tile
+// raises it only when its own max exceeds M by more than 8 (log2 units); then O
+// and the row sum L are rescaled by 2^(M_old - M_new).  The weights are
+// p = 2^(s - M) <= 2^8.  An item runs in one of two layouts:
+//
+// rows as columns (at most NR = 16 or 64 stacked rows: single tokens, blocks)
+//   S = K_t Q^T            128 keys by NR rows: a thread holds one key's scores
+//   O += V_t^T P           dims by rows, both operands from shared memory
+//   The products' M dimension is filled with keys and dimensions, so few rows
+//   cost few columns, and all 128 threads of a group share the exponentials of
+//   however few rows there are.  Whether a row's reference has to move is one
+//   vote a tile.  With NR = 16 P is kept as a bf16 pair hi + lo (about 2^-17
+//   relative), which is free here; with 64 it is rounded once.
+// rows as rows (more rows: chunks, shared prefixes)
+//   S = Q K_t^T            128 rows by 128 keys: a thread holds one row
+//   O += P V_t             P as bf16 over S in TMEM
+//   An item of at most 128 rows has one query tile, whose key tiles the groups
+//   take in turn; one of more rows has two, a group each, that share every key
+//   tile, which halves the traffic from L2.
+// P rounded to bf16 once is off by 2^-9 relative a weight, the size of the
+// result's own rounding; L sums the weights before it.  Where both groups work
+// on the same rows, their (M, L, O) are joined at the item's end.
 //
 // Warps: 0 streams the pages (TMA, one box a page and 64 dimensions) through a
 // ring of key and value tiles; 1 and 2 issue the groups' products; 3 owns TMEM
 // and brings the query rows (16-byte asynchronous copies, swizzled by hand:
 // stacked rows of any GQA group are packed without gaps); 4..7 and 8..11 are
-// the softmax groups, a thread a row.
+// the softmax groups.
 //
 // A hidden key's weight is 0, and 0 times an Inf or NaN value would reach rows
 // that do not see it.  So in a tile that some row sees only in part, the group
@@ -51,18 +59,77 @@ constexpr uint64_t kTcWaitNs = 500000000ull;
 template <int HD>
 struct TcLayout {
   static constexpr int kHalves = HD / 64;               // 64-dimension halves: 128-byte rows
-  static constexpr uint32_t kTile = kHalves * 16384;    // 128 rows
+  static constexpr uint32_t kTile = kHalves * 16384;    // 128 keys
   static constexpr int kSlots = HD == 128 ? 5 : 8;
-  static constexpr uint32_t kQ = 0;                     // two query tiles
-  static constexpr uint32_t kRing = 2 * kTile;
-  static constexpr uint32_t kXch = kRing + kSlots * kTile;  // [128] (M, L) of group 1
-  static constexpr uint32_t kBar = kXch + 1024;
+  // two query buffers: a tile of 128 rows, or 64 rows and, behind them, a group's P of 128 keys x 64 rows
+  static constexpr uint32_t kQ = kSlots * kTile;
+  static constexpr uint32_t kQBuf = 32768;
+  static constexpr uint32_t kP = 16384;                 // P within a buffer
+  static constexpr uint32_t kXch = kQ + 2 * kQBuf;      // [128] (M, L) of group 1
+  static constexpr uint32_t kRef = kXch + 1024;         // [2][64] row references of the rows-as-columns layout
+  static constexpr uint32_t kBar = kRef + 512;
   static constexpr int kBars = 2 * kSlots + 21;
   static constexpr uint32_t kMisc = kBar + kBars * 8;   // TMEM slot, abort flag, per-group words, scan scratch
   static constexpr int kSmem = kMisc + 256 + 1024;      // + alignment slack
   static_assert(kSmem <= 232448, "shared memory per block");
   static_assert(kMisc % 8 == 0, "alignment");
 };
+
+// max of three
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two float32 lanes at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+// Sum over the warp's lanes of N values a lane, N / 32 results a lane (N >= 32) or one (N = 16, in two lanes):
+// each step exchanges half of what is left with the lane `o` away.  Lane l ends with rows
+// warp_rows<N>(l) .. in order.
+template <int N>
+__device__ __forceinline__ void warp_scatter_sum(float (&x)[N], int lane) {
+  int n = N;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & o;
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e)
+        if (e < n) {
+          const float mine = up ? x[e + n] : x[e], theirs = up ? x[e] : x[e + n];
+          x[e] = mine + __shfl_xor_sync(0xffffffffu, theirs, o);
+        }
+    } else {
+      x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+    }
+  }
+}
+// (lane bits 16, 8, ... select halves: the first row of a lane's results)
+template <int N>
+__device__ __forceinline__ int scatter_row(int lane) {
+  int row = 0, n = N;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (n > 1) {
+      n >>= 1;
+      if (lane & o) row += n;
+    }
+  return row;
+}
 
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
@@ -114,7 +181,8 @@ __device__ __forceinline__ uint32_t bits_of(int a, int b) {
 }
 }  // namespace
 
-template <int HD>
+// NR: rows of the rows-as-columns layout (0: it is not used); TS, TP: suffix / prefix items use it.
+template <int HD, int NR, bool TS, bool TP>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ PagedGeom g, int pool_rows, const bf16* __restrict__ q,
@@ -144,6 +212,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   volatile uint32_t* bad_w = misc + 4;      // [2][4] keys of the tile with a value that is not finite
   int* red = reinterpret_cast<int*>(misc + 12);
   float2* xch = reinterpret_cast<float2*>(sm + L::kXch);
+  auto as_columns = [](const Segment& s) { return s.prefix ? TP : TS; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tma_prefetch_desc(&tmK);
@@ -224,7 +293,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               ok = false;
               break;
             }
-            uint8_t* dst = sm + L::kRing + s * L::kTile;
+            uint8_t* dst = sm + s * L::kTile;
             if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kTile);
             __syncwarp();
             if (mine) {
@@ -246,13 +315,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int gq = warp - 1;
       if (lane == 0) {
         const uint32_t idS = idesc_bf16_f32(128, 128), idO = idesc_bf16_f32(128, HD) | (1u << 16);  // values MN-major
+        const uint32_t idSt = idesc_bf16_f32(128, NR > 0 ? NR : 16);
+        const uint32_t idOt = idesc_bf16_f32(128, 64) | (3u << 15);  // values and weights both MN-major
         const uint32_t tS = tmem + gq * 128, tO = tmem + 256 + gq * 128;
         int job = 0;
         bool ok = true;
         // Both issuing warps see every tile land and release it: a slot is refilled only after both have
         // been past it, so a wait never looks at a phase two fills away.
         while (ok && walk.next(sg)) {
-          const bool two = item_rows(sg) > 128;
+          const bool cols = as_columns(sg), two = !cols && item_rows(sg) > 128;
           const int buf = two ? gq : qt;
           if (two || qt == 0) ok = wait_phase(&q_full[0], (uint32_t)qn0 & 1u, abort_f, g.status);
           if (ok && (two || qt == 1)) ok = wait_phase(&q_full[1], (uint32_t)qn1 & 1u, abort_f, g.status);
@@ -261,7 +332,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (seg > 0) ok = wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g.status);
             if (ok) mbar_arrive(&q_empty[buf]);
           }
-          const uint8_t* qs = sm + L::kQ + buf * L::kTile;
+          const uint8_t* qs = sm + L::kQ + buf * L::kQBuf;
           for (int t = 0; ok && t < sg.nt; ++t) {
             const int xk = 2 * (tiles + t), sk = xk % NS, sv = (xk + 1) % NS;
             const uint32_t pk = (uint32_t)(xk / NS) & 1u, pv_ = (uint32_t)((xk + 1) / NS) & 1u;
@@ -277,16 +348,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (job > 0) ok = wait_phase(&pv_done[gq], (uint32_t)(job - 1) & 1u, abort_f, g.status);
             if (!ok) break;
             tc_fence_after();
-            const uint8_t* kt = sm + L::kRing + sk * L::kTile;
+            const uint8_t* kt = sm + sk * L::kTile;
+            if (cols) {
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-              const uint64_t off = (uint64_t)(((kk & 3) * 32) >> 4);
-              tc_mma_f16(tS, smem_desc_sw128(qs + (kk >> 2) * 16384) + off,
-                         smem_desc_sw128(kt + (kk >> 2) * 16384) + off, idS, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint64_t off = (uint64_t)(((kk & 3) * 32) >> 4);
+                tc_mma_f16(tS, smem_desc_sw128(kt + (kk >> 2) * 16384) + off,
+                           smem_desc_sw128(qs + (kk >> 2) * 8192) + off, idSt, kk > 0 ? 1u : 0u);
+              }
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint64_t off = (uint64_t)(((kk & 3) * 32) >> 4);
+                tc_mma_f16(tS, smem_desc_sw128(qs + (kk >> 2) * 16384) + off,
+                           smem_desc_sw128(kt + (kk >> 2) * 16384) + off, idS, kk > 0 ? 1u : 0u);
+              }
             }
             tc_commit(&s_full[gq]);
             tc_commit(&empty[sk]);
-            if (t + step >= sg.nt) {  // the last scores of the piece: the query tile is free after them
+            if (!cols && t + step >= sg.nt) {  // the last scores of the piece: the query tile is free after them
               tc_commit(&q_empty[buf]);
               if (two) tc_commit(&q_empty[buf]);
             }
@@ -297,14 +377,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t acc0 = t == t0 ? acc_first[gq] : 1u;
-            const uint32_t vt = smem_u32(sm + L::kRing + sv * L::kTile);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_f16_tmem_a(tO, tS + kk * 8, smem_desc_mn(vt + kk * 2048, 16384), idO, kk > 0 ? 1u : acc0);
-            if (!two) {
+            const uint32_t vt = smem_u32(sm + sv * L::kTile);
+            if (cols) {
+              // (head_dim 64: the upper 64 lanes take what lies behind the tile, and nothing reads them)
+              const uint32_t ps = smem_u32(sm + L::kQ + gq * L::kQBuf + L::kP);
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
-                tc_mma_f16_tmem_a(tO, tS + 64 + kk * 8, smem_desc_mn(vt + kk * 2048, 16384), idO, 1u);
+                tc_mma_f16(tO, smem_desc_mn(vt + kk * 2048, 16384), smem_desc_mn(ps + kk * 2048, 16384), idOt,
+                           kk > 0 ? 1u : acc0);
+              if (t + step >= sg.nt) tc_commit(&q_empty[buf]);
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_f16_tmem_a(tO, tS + kk * 8, smem_desc_mn(vt + kk * 2048, 16384), idO, kk > 0 ? 1u : acc0);
             }
             tc_commit(&pv_done[gq]);
             tc_commit(&empty[sv]);
@@ -325,7 +410,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool ok = true;
       while (ok && walk.next(sg)) {
         const int rows = item_rows(sg);
-        const bool two = rows > 128;
+        const bool cols = as_columns(sg), two = !cols && rows > 128;
         for (int w = 0; ok && w < (two ? 2 : 1); ++w) {
           const int buf = two ? w : qt;
           int& used = buf ? qn1 : qn0;
@@ -337,7 +422,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int x = sg.rt * (sg.prefix ? g.rp : g.ri) + w * 128 + r;
           int row = x / g.G, h = x - row * g.G;
           if (!sg.prefix) row += sg.b * g.n;
-          uint8_t* dst = sm + L::kQ + buf * L::kTile + (c >> 3) * 16384;
+          uint8_t* dst = sm + L::kQ + buf * L::kQBuf + (c >> 3) * (cols ? 8192 : 16384);
           for (const int lim = min(128, rows - w * 128); r < lim; r += kLanes) {
             cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                        q + ((long long)row * g.nq + sg.hk * g.G + h) * HD + c * 8);
@@ -347,6 +432,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               ++row;
             }
           }
+          // (rows past the item's: scores of 0, which nothing reads)
+          if (cols)
+            for (; r < NR; r += kLanes)
+              *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
           cp_async_wait_all();
           fence_proxy_async_smem();
           __syncwarp();
@@ -363,310 +452,630 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int r = qr * 32 + lane;
     const uint32_t lanes = (uint32_t)(qr * 32) << 16;
     const uint32_t tS = tmem + lanes + gq * 128, tO = tmem + lanes + 256 + gq * 128;
-    int job = 0, xn = 0, fn = 0, fb = 0;  // tiles done; joins; phases of the scan barriers
+    int job = 0, xn = 0, fn = 0, fb = 0;  // tiles done; joins; phases of the group's barrier and of both groups'
+    bool handover = false;                // a query tile of the rows-as-rows layout may still lie where P goes
+    const float sl = scale_log2;
     bool ok = true;
-    while (ok && walk.next(sg)) {
-      const int rows = item_rows(sg);
-      const bool two = rows > 128;
-      const int step = two ? 1 : 2, t0 = two ? 0 : gq;
-      const int rr = r + (two ? gq * 128 : 0);  // the item's stacked row
-      const ItemRow me = item_row(g, sg, rr);
-      const bool warp_live = (rr - lane) < rows;  // uniform: some row of the warp belongs to the item
-      int sink = 0, lo = 0, hi = 0;
-      if (me.live) row_span(g, paged_len(g, me.b), paged_rows(g, me.b), me.i, sink, lo, hi);
-      const int key_lo = sg.prefix ? 0 : pv.sh_tiles * KT;
-      const int key_end = sg.prefix ? pv.sh_tiles * KT : key_limit(g, sg.b);
-      lo = max(lo, key_lo);
-      hi = min(hi, key_end);
-      sink = min(sink, key_end);
-      // keys that every row of the item sees: [all_lo, all_hi)
-      int all_lo = 0, all_hi = key_end;
+    // a barrier of the group (or of both); false: the CTA stops
+    auto meet = [&](uint64_t* b, int& ph) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b);
+      const bool good = !stop(wait_phase(b, (uint32_t)ph & 1u, abort_f, g.status));
+      ++ph;
+      return good;
+    };
+    // 16-byte chunk c of key `key` in a value tile
+    auto chunk = [&](uint8_t* vt, int key, int c) {
+      return reinterpret_cast<uint4*>(vt + (c >> 3) * 16384 + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+    };
+    auto row_is_bad = [&](uint8_t* vt) {
+      uint32_t bad = 0u;
+#pragma unroll
+      for (int c = 0; c < HD / 8; ++c) {
+        const uint4 w = *chunk(vt, r, c);
+        bad |= nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w);
+      }
+      return bad != 0u;
+    };
+    auto clean_row = [&](uint8_t* vt) {
+#pragma unroll 1
+      for (int c = 0; c < HD / 8; ++c) {
+        uint4 w = *chunk(vt, r, c);
+        uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0xffffu;
+          if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u;
+        }
+        *chunk(vt, r, c) = w;
+      }
+    };
+    // an item's first product comes after this when its accumulator starts here
+    auto zero_o = [&](int cols) {
+      uint32_t z[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) z[e] = 0u;
+      for (int c = 0; c < cols; c += 16) tmem_st16(tO + c, z);
+      tmem_st_wait();
+    };
+    // The keys of the item that every row of it sees: [lo, hi).
+    auto seen_by_all = [&](int x0, int rows, int key_lo, int key_end, int& lo, int& hi) {
+      lo = 0;
+      hi = key_end;
       if (!sg.prefix) {
         int a, b, c;
-        const int P = paged_len(g, sg.b), n = paged_rows(g, sg.b), x = sg.rt * g.ri;
-        row_span(g, P, n, (x + rows - 1) / g.G, a, all_lo, c);
-        row_span(g, P, n, x / g.G, a, b, all_hi);
-        all_lo = max(all_lo, key_lo);
-        all_hi = min(all_hi, key_end);
+        const int P = paged_len(g, sg.b), n = paged_rows(g, sg.b);
+        row_span(g, P, n, (x0 + rows - 1) / g.G, a, lo, c);
+        row_span(g, P, n, x0 / g.G, a, b, hi);
+        lo = max(lo, key_lo);
+        hi = min(hi, key_end);
       } else if (g.window > 0) {
-        all_hi = 0;
+        hi = 0;
       }
-      float M = -INFINITY, Ls = 0.f;
-      for (int t = t0; ok && t < sg.nt; t += step) {
-        const int k0 = sg.span.tile(sg.t0 + t) * KT;
-        const bool inner = k0 >= all_lo && k0 + KT <= all_hi;  // the same for all warps of the item
-        if (stop(wait_phase(&s_full[gq], (uint32_t)job & 1u, abort_f, g.status))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        uint32_t v[128];
-        uint32_t vw[4] = {0u, 0u, 0u, 0u};  // visible keys of the tile
-        float Mn = M, f = 1.f;
-        bool wfull = true;
-        if (!inner) {
-          const bool row_full = k0 >= key_lo && ((lo <= k0 && hi >= k0 + KT) || sink >= k0 + KT);
-          wfull = __all_sync(0xffffffffu, !me.live || row_full);
-          if (me.live) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-              vw[w] = bits_of(lo - k0 - 32 * w, hi - k0 - 32 * w) | bits_of(key_lo - k0 - 32 * w, sink - k0 - 32 * w);
+    };
+    bool more = walk.next(sg);
+    // Prefix items come before suffix items, so those in the rows-as-rows layout (if any) come first.
+    if constexpr (!TS || !TP) {
+      while (ok && more && !as_columns(sg)) {
+        // ------------------------------------------------ rows as rows: thread = stacked row
+        const int rows = item_rows(sg);
+        const bool two = rows > 128;
+        const int step = two ? 1 : 2, t0 = two ? 0 : gq;
+        const bool has = t0 < sg.nt, both = !two && sg.nt > 1, whole = walk.whole(sg);
+        const int x0 = sg.rt * (sg.prefix ? g.rp : g.ri);  // the item's first stacked row
+        const int key_lo = sg.prefix ? 0 : pv.sh_tiles * KT;
+        const int key_end = sg.prefix ? pv.sh_tiles * KT : key_limit(g, sg.b);
+        int all_lo, all_hi;
+        seen_by_all(x0, rows, key_lo, key_end, all_lo, all_hi);
+        const int rr = r + (two ? gq * 128 : 0);  // of the item
+        const ItemRow me = item_row(g, sg, rr);
+        const bool warp_live = (rr - lane) < rows;  // some row of the warp belongs to the item
+        int sink = 0, lo = 0, hi = 0;
+        if (me.live) row_span(g, paged_len(g, me.b), paged_rows(g, me.b), me.i, sink, lo, hi);
+        lo = max(lo, key_lo);
+        hi = min(hi, key_end);
+        sink = min(sink, key_end);
+        float M = -INFINITY, Ls = 0.f;
+        for (int t = t0; ok && t < sg.nt; t += step) {
+          const int k0 = sg.span.tile(sg.t0 + t) * KT;
+          const bool inner = k0 >= all_lo && k0 + KT <= all_hi;  // the same for all warps of the item
+          if (stop(wait_phase(&s_full[gq], (uint32_t)job & 1u, abort_f, g.status))) {
+            ok = false;
+            break;
           }
-        }
-        auto vis = [&](int e) { return ((vw[e >> 5] >> (e & 31)) & 1u) != 0u; };
-        if (warp_live) {
+          tc_fence_after();
+          float v[128];
+          uint32_t vw[4] = {0u, 0u, 0u, 0u};  // visible keys of the tile
+          float Mn = M, f = 1.f;
+          bool wfull = true;
+          if (!inner) {
+            const bool row_full = k0 >= key_lo && ((lo <= k0 && hi >= k0 + KT) || sink >= k0 + KT);
+            wfull = __all_sync(0xffffffffu, !me.live || row_full);
+            if (me.live) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
-          tmem_ld_wait();
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if (wfull) {
-#pragma unroll
-            for (int e = 0; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], vis(e) ? __uint_as_float(v[e]) : -INFINITY);
-          }
-          const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          bool raise = false;
-          if (m != -INFINITY) {
-            const float mt = m * scale_log2;
-            if (M == -INFINITY) {
-              Mn = mt;
-            } else if (mt > M + 8.f) {
-              Mn = mt;
-              raise = true;
+              for (int w = 0; w < 4; ++w)
+                vw[w] = bits_of(lo - k0 - 32 * w, hi - k0 - 32 * w) | bits_of(key_lo - k0 - 32 * w, sink - k0 - 32 * w);
             }
           }
-          if (__any_sync(0xffffffffu, raise)) {  // the group's earlier products are done: S came after them
-            f = raise ? ex2f(M - Mn) : 1.f;
+          if (warp_live) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+            tmem_ld_wait();
+            if (!wfull) {
+#pragma unroll
+              for (int e = 0; e < 128; ++e)
+                if (!((vw[e >> 5] >> (e & 31)) & 1u)) v[e] = -INFINITY;
+            }
+            float mx[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mx[w] = max3(v[w], v[w + 4], v[w + 8]);
+#pragma unroll
+            for (int e = 12; e < 124; e += 8)
+#pragma unroll
+              for (int w = 0; w < 4; ++w) mx[w] = max3(mx[w], v[e + w], v[e + w + 4]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mx[w] = fmaxf(mx[w], v[124 + w]);
+            const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            bool raise = false;
+            if (m != -INFINITY) {
+              const float mt = m * sl;
+              if (M == -INFINITY) {
+                Mn = mt;
+              } else if (mt > M + 8.f) {
+                Mn = mt;
+                raise = true;
+              }
+            }
+            if (__any_sync(0xffffffffu, raise)) {  // the group's earlier products are done: S came after them
+              f = raise ? ex2f(M - Mn) : 1.f;
 #pragma unroll 1
-            for (int c = 0; c < HD; c += 16) {
-              uint32_t o[16];
-              tmem_ld16u(tO + c, o);
-              tmem_ld_wait();
+              for (int c = 0; c < HD; c += 16) {
+                uint32_t o[16];
+                tmem_ld16u(tO + c, o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(tO + c, o);
-            }
-            tmem_st_wait();
-          }
-        }
-        const float negm = Mn == -INFINITY ? 0.f : -Mn;
-        uint32_t first_acc = 0u;
-        if (!inner) {
-          // values that are not finite, a key a thread
-          uint8_t* vt = sm + L::kRing + (2 * (tiles + t) + 1) % NS * L::kTile;
-          auto chunk = [&](int key, int c) {
-            return reinterpret_cast<uint4*>(vt + (c >> 3) * 16384 + key * 128 + (((c & 7) ^ (key & 7)) << 4));
-          };
-          uint64_t* fx = two ? &fix[2] : &fix[gq];
-          int& ph = two ? fb : fn;
-          ok = !stop(wait_phase(&v_ready[gq], (uint32_t)job & 1u, abort_f, g.status));
-          if (!ok) break;
-          uint32_t bad = 0u;
-#pragma unroll
-          for (int c = 0; c < HD / 8; ++c) {
-            const uint4 w = *chunk(r, c);
-            bad |= nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w);
-          }
-          const uint32_t word = __ballot_sync(0xffffffffu, bad != 0u);
-          if (lane == 0) {
-            bad_w[gq * 4 + qr] = word;
-            mbar_arrive(fx);
-          }
-          ok = !stop(wait_phase(fx, (uint32_t)ph & 1u, abort_f, g.status));
-          ++ph;
-          if (!ok) break;
-          const uint32_t bw[4] = {bad_w[gq * 4], bad_w[gq * 4 + 1], bad_w[gq * 4 + 2], bad_w[gq * 4 + 3]};
-          if (bw[0] | bw[1] | bw[2] | bw[3]) {  // uniform over the group
-            const bool first = t == t0;
-            if (first && warp_live) {
-              // O starts here instead of in the first product, which must not overtake its last reader
-              if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g.status));
-              if (!ok) break;
-              tc_fence_after();
-              uint32_t z[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) z[e] = 0u;
-              for (int c = 0; c < HD; c += 16) tmem_st16(tO + c, z);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(tO + c, o);
+              }
               tmem_st_wait();
             }
-            first_acc = 1u;
-            if (warp_live) {
+          }
+          const float negm = Mn == -INFINITY ? 0.f : -Mn;
+          uint32_t first_acc = 0u;
+          if (!inner) {
+            // values that are not finite, a key a thread
+            uint8_t* vt = sm + (2 * (tiles + t) + 1) % NS * L::kTile;
+            uint64_t* fx = two ? &fix[2] : &fix[gq];
+            int& ph = two ? fb : fn;
+            ok = !stop(wait_phase(&v_ready[gq], (uint32_t)job & 1u, abort_f, g.status));
+            if (!ok) break;
+            const bool bad = row_is_bad(vt);
+            const uint32_t word = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) bad_w[gq * 4 + qr] = word;
+            ok = meet(fx, ph);
+            if (!ok) break;
+            const uint32_t bw[4] = {bad_w[gq * 4], bad_w[gq * 4 + 1], bad_w[gq * 4 + 2], bad_w[gq * 4 + 3]};
+            if (bw[0] | bw[1] | bw[2] | bw[3]) {  // uniform over the item's groups
+              if (t == t0 && warp_live) {
+                // O starts here instead of in the first product, which must not overtake its last reader
+                if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g.status));
+                if (!ok) break;
+                tc_fence_after();
+                zero_o(HD);
+              }
+              first_acc = 1u;
+              if (warp_live) {
 #pragma unroll 1
-              for (int key = 0; key < KT; ++key) {
-                auto word_of = [&](const uint32_t (&w)[4]) {
-                  return key < 64 ? (key < 32 ? w[0] : w[1]) : (key < 96 ? w[2] : w[3]);
-                };
-                if (!((word_of(bw) >> (key & 31)) & 1u)) continue;
-                const float s = __uint_as_float(tmem_ld1(tS + key));
+                for (int key = 0; key < KT; ++key) {
+                  auto word_of = [&](const uint32_t (&w)[4]) {
+                    return key < 64 ? (key < 32 ? w[0] : w[1]) : (key < 96 ? w[2] : w[3]);
+                  };
+                  if (!((word_of(bw) >> (key & 31)) & 1u)) continue;
+                  const float s = __uint_as_float(tmem_ld1(tS + key));
+                  tmem_ld_wait();
+                  const bool see = (word_of(vw) >> (key & 31)) & 1u;
+                  const float p = ex2f(fmaf(s, sl, negm));
+#pragma unroll 1
+                  for (int c = 0; c < HD; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16u(tO + c, o);
+                    tmem_ld_wait();
+                    const uint4 w[2] = {*chunk(vt, key, c >> 3), *chunk(vt, key, (c >> 3) + 1)};
+                    const uint32_t* x = reinterpret_cast<const uint32_t*>(w);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                      const uint32_t hbits = (e & 1) ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16;
+                      if (see && (hbits & 0x7f800000u) == 0x7f800000u)
+                        o[e] = __float_as_uint(fmaf(p, __uint_as_float(hbits), __uint_as_float(o[e])));
+                    }
+                    tmem_st16(tO + c, o);
+                    tmem_st_wait();
+                  }
+                }
+              }
+              ok = meet(fx, ph);  // every row has taken what it sees
+              if (!ok) break;
+              if (bad) clean_row(vt);
+              fence_proxy_async_smem();
+            }
+          }
+          if (warp_live) {
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(negm, negm);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // 32 keys
+              uint32_t p16[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int k = c * 32 + 2 * e;
+                float2 p = fma2(make_float2(v[k], v[k + 1]), sl2, nm2);
+                p.x = ex2f(p.x);
+                p.y = ex2f(p.y);
+                sum[e & 1] = add2(sum[e & 1], p);
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
+                p16[e] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              tmem_st16(tS + c * 16, p16);
+            }
+            Ls = fmaf(Ls, f, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+            M = Mn;
+            tmem_st_wait();
+          }
+          if (t == t0 && r == 0) acc_first[gq] = first_acc;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[gq]);
+          ++job;
+        }
+        if (!ok) break;
+        if (has && stop(wait_phase(&pv_done[gq], (uint32_t)(job - 1) & 1u, abort_f, g.status))) break;
+        // ---- the piece's end: group 0 joins both groups' parts of a single query tile, else each has its own
+        float2 other = make_float2(-INFINITY, 0.f);
+        if (!two) {
+          if (gq == 1) {
+            if (xn > 0 && stop(wait_phase(x_free, (uint32_t)(xn - 1) & 1u, abort_f, g.status))) break;
+            xch[r] = make_float2(M, Ls);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_full);
+          } else {
+            if (stop(wait_phase(x_full, (uint32_t)xn & 1u, abort_f, g.status))) break;
+            other = xch[r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_free);
+          }
+          ++xn;
+        }
+        if (two || gq == 0) {
+          tc_fence_after();
+          const float Mx = fmaxf(M, other.x);
+          const float ref = Mx == -INFINITY ? 0.f : Mx;
+          const float wa = M == -INFINITY ? (both ? 0.f : 1.f) : ex2f(M - ref);
+          const float wb = other.x == -INFINITY ? 0.f : ex2f(other.x - ref);
+          const float Lt = fmaf(wb, other.y, wa * Ls);
+          const float inv = whole ? 1.f / Lt : 1.f;
+          if (warp_live) {
+            bf16* dst = out + (((long long)me.b * g.n + me.i) * g.nq + me.head) * HD;
+            float* pdst = g.part_o + (sg.slot_row + rr) * HD;
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 32) {
+              uint32_t a[32], b[32];
+              tmem_ld32(tO + c, a);
+              if (both) tmem_ld32(tO + 128 + c, b);
+              tmem_ld_wait();
+              float x[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                x[e] = __uint_as_float(a[e]);
+                if (both) x[e] = fmaf(wb, __uint_as_float(b[e]), wa * x[e]);
+              }
+              if (me.live) {
+                if (whole) {
+#pragma unroll
+                  for (int e = 0; e < 32; e += 8) {
+                    uint4 w;
+                    __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h2[i] = __floats2bfloat162_rn(x[e + 2 * i] * inv, x[e + 2 * i + 1] * inv);
+                    *reinterpret_cast<uint4*>(dst + c + e) = w;
+                  }
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4*>(pdst + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                }
+              }
+            }
+            if (me.live && !whole) g.part_ml[sg.slot_row + rr] = make_float2(both ? Mx : M, both ? Lt : Ls);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&o_free[gq]);
+            if (!two) mbar_arrive(&o_free[1]);
+          }
+        }
+        handover = true;
+        if (two || qt == 0) ++qn0;
+        if (two || qt == 1) ++qn1;
+        if (!two) qt ^= 1;
+        tiles += sg.nt;
+        ++seg;
+        more = walk.next(sg);
+      }
+    }
+    if constexpr (NR > 0) {
+      while (ok && more) {
+        // ------------------------------------------------ rows as columns: thread = key r of the tile
+        const int rows = item_rows(sg), t0 = gq;
+        const bool has = t0 < sg.nt, both = sg.nt > 1, whole = walk.whole(sg);
+        const int x0 = sg.rt * (sg.prefix ? g.rp : g.ri);
+        const int key_lo = sg.prefix ? 0 : pv.sh_tiles * KT;
+        const int key_end = sg.prefix ? pv.sh_tiles * KT : key_limit(g, sg.b);
+        int all_lo, all_hi;
+        seen_by_all(x0, rows, key_lo, key_end, all_lo, all_hi);
+        float* ref = reinterpret_cast<float*>(sm + L::kRef) + gq * 64;
+        uint8_t* pbuf = sm + L::kQ + gq * L::kQBuf + L::kP;
+        float* scr = reinterpret_cast<float*>(pbuf);  // scratch wherever no product reads P
+        constexpr bool kPair = NR == 16;
+        float Ls[NR];
+#pragma unroll
+        for (int c = 0; c < NR; ++c) Ls[c] = 0.f;
+        if (!meet(&fix[gq], fn)) break;  // the scratch's last readers are past it
+        for (int t = t0; ok && t < sg.nt; t += 2) {
+          const bool first = t == t0;
+          const int k0 = sg.span.tile(sg.t0 + t) * KT, key = k0 + r;
+          const bool inner = k0 >= all_lo && k0 + KT <= all_hi;
+          if (stop(wait_phase(&s_full[gq], (uint32_t)job & 1u, abort_f, g.status))) {
+            ok = false;
+            break;
+          }
+          if (handover) {
+            ok = (qn0 == 0 || !stop(wait_phase(&q_empty[0], (uint32_t)(qn0 - 1) & 1u, abort_f, g.status))) &&
+                 (qn1 == 0 || !stop(wait_phase(&q_empty[1], (uint32_t)(qn1 - 1) & 1u, abort_f, g.status)));
+            if (!ok) break;
+            handover = false;
+          }
+          tc_fence_after();
+          uint32_t v[NR];
+#pragma unroll
+          for (int c = 0; c < NR; c += 16) tmem_ld16u(tS + c, *reinterpret_cast<uint32_t(*)[16]>(&v[c]));
+          tmem_ld_wait();
+          uint64_t hid = 0;  // rows that do not see the key
+          if (!inner) {
+            int i = x0 / g.G, h = x0 - i * g.G, sink, lo, hi;
+            const int P = paged_len(g, sg.b), n = paged_rows(g, sg.b);
+            const bool in = key >= key_lo && key < key_end;
+            if (!sg.prefix) row_span(g, P, n, i, sink, lo, hi);
+#pragma unroll
+            for (int c = 0; c < NR; ++c) {
+              if (sg.prefix) {
+                const ItemRow w = item_row(g, sg, c);
+                row_span(g, paged_len(g, w.b), paged_rows(g, w.b), w.i, sink, lo, hi);
+              }
+              if (!(in && c < rows && (key < sink || (key >= lo && key < hi)))) {
+                v[c] = 0xff800000u;
+                hid |= 1ull << c;
+              }
+              if (!sg.prefix && ++h == g.G) {
+                h = 0;
+                ++i;
+                row_span(g, P, n, i, sink, lo, hi);
+              }
+            }
+          }
+          bool move = first;
+          if (!first) {
+            bool over = false;
+#pragma unroll
+            for (int c = 0; c < NR; c += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(ref + c);
+              over |= __uint_as_float(v[c]) * sl > m.x + 8.f || __uint_as_float(v[c + 1]) * sl > m.y + 8.f ||
+                      __uint_as_float(v[c + 2]) * sl > m.z + 8.f || __uint_as_float(v[c + 3]) * sl > m.w + 8.f;
+            }
+            over = __any_sync(0xffffffffu, over);
+            if (lane == 0) bad_w[gq * 4 + qr] = over;
+            ok = meet(&fix[gq], fn);
+            if (!ok) break;
+            move = bad_w[gq * 4] | bad_w[gq * 4 + 1] | bad_w[gq * 4 + 2] | bad_w[gq * 4 + 3];
+          }
+          if (move) {
+            // each row's largest score of the tile, by integers in the same order
+#pragma unroll
+            for (int c = 0; c < NR; ++c) {
+              const float x = __uint_as_float(v[c]);
+              const int b = x != x ? (int)0x807fffff : (int)v[c] ^ ((int)v[c] >> 31 & 0x7fffffff);
+              const int m = __reduce_max_sync(0xffffffffu, b);
+              if (lane == (c & 31)) scr[qr * NR + c] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
+            }
+            ok = meet(&fix[gq], fn);
+            if (!ok) break;
+            if (r < NR) {
+              const float mx = fmaxf(fmaxf(scr[r], scr[NR + r]), fmaxf(scr[2 * NR + r], scr[3 * NR + r]));
+              const float old = first ? -INFINITY : ref[r];
+              float mn = old, f = 1.f;
+              if (mx != -INFINITY) {
+                const float mt = mx * sl;
+                if (old == -INFINITY) {
+                  mn = mt;
+                } else if (mt > old + 8.f) {
+                  mn = mt;
+                  f = ex2f(old - mt);
+                }
+              }
+              ref[r] = mn;
+              scr[4 * NR + r] = f;
+            }
+            ok = meet(&fix[gq], fn);
+            if (!ok) break;
+            if (!first) {
+#pragma unroll
+              for (int c = 0; c < NR; ++c) Ls[c] *= scr[4 * NR + c];
+#pragma unroll 1
+              for (int c = 0; c < (kPair ? 2 * NR : NR); c += 16) {
+                uint32_t o[16];
+                tmem_ld16u(tO + c, o);
                 tmem_ld_wait();
-                const bool see = (word_of(vw) >> (key & 31)) & 1u;
-                const float p = ex2f(fmaf(s, scale_log2, negm));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scr[4 * NR + (c + e) % NR]);
+                tmem_st16(tO + c, o);
+              }
+              tmem_st_wait();
+              ok = meet(&fix[gq], fn);  // P overwrites the factors
+              if (!ok) break;
+            }
+          }
+          uint32_t first_acc = 0u;
+          if (!inner) {
+            uint8_t* vt = sm + (2 * (tiles + t) + 1) % NS * L::kTile;
+            ok = !stop(wait_phase(&v_ready[gq], (uint32_t)job & 1u, abort_f, g.status));
+            if (!ok) break;
+            const bool bad = row_is_bad(vt);
+            const uint32_t word = __ballot_sync(0xffffffffu, bad);
+            ok = meet(&fix[gq], fn);  // the votes have been read
+            if (!ok) break;
+            if (lane == 0) bad_w[gq * 4 + qr] = word;
+            ok = meet(&fix[gq], fn);
+            if (!ok) break;
+            const uint32_t bw[4] = {bad_w[gq * 4], bad_w[gq * 4 + 1], bad_w[gq * 4 + 2], bad_w[gq * 4 + 3]};
+            if (bw[0] | bw[1] | bw[2] | bw[3]) {
+              if (first) {
+                if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g.status));
+                if (!ok) break;
+                tc_fence_after();
+                zero_o(64);
+              }
+              first_acc = 1u;
 #pragma unroll 1
-                for (int c = 0; c < HD; c += 16) {
+              for (int k = 0; ok && k < KT; ++k) {
+                const uint32_t w = k < 64 ? (k < 32 ? bw[0] : bw[1]) : (k < 96 ? bw[2] : bw[3]);
+                if (!((w >> (k & 31)) & 1u)) continue;
+                if (k == r) {
+#pragma unroll
+                  for (int c = 0; c < NR; ++c) {
+                    const float m = ref[c];
+                    const float p = ex2f(fmaf(__uint_as_float(v[c]), sl, m == -INFINITY ? 0.f : -m));
+                    scr[c] = (hid >> c) & 1 ? -1.f : p;
+                  }
+                }
+                ok = meet(&fix[gq], fn);
+                if (!ok) break;
+                const int d = r < HD ? r : 0;  // this lane's dimension
+                const uint32_t raw = reinterpret_cast<const uint16_t*>(chunk(vt, k, d >> 3))[d & 7];
+                const float val = __uint_as_float(raw << 16);
+                const bool add = (raw & 0x7f80u) == 0x7f80u;
+#pragma unroll 1
+                for (int c = 0; c < NR; c += 16) {
                   uint32_t o[16];
                   tmem_ld16u(tO + c, o);
                   tmem_ld_wait();
-                  const uint4 w[2] = {*chunk(key, c >> 3), *chunk(key, (c >> 3) + 1)};
-                  const uint32_t* x = reinterpret_cast<const uint32_t*>(w);
 #pragma unroll
                   for (int e = 0; e < 16; ++e) {
-                    const uint32_t hbits = (e & 1) ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16;
-                    if (see && (hbits & 0x7f800000u) == 0x7f800000u)
-                      o[e] = __float_as_uint(fmaf(p, __uint_as_float(hbits), __uint_as_float(o[e])));
+                    const float p = scr[c + e];
+                    if (add && !(p < 0.f)) o[e] = __float_as_uint(fmaf(p, val, __uint_as_float(o[e])));
                   }
                   tmem_st16(tO + c, o);
                   tmem_st_wait();
                 }
+                ok = meet(&fix[gq], fn);
               }
+              if (!ok) break;
+              if (bad) clean_row(vt);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(fx);  // every row has taken what it sees
-            ok = !stop(wait_phase(fx, (uint32_t)ph & 1u, abort_f, g.status));
-            ++ph;
-            if (!ok) break;
-            if (bad) {
-#pragma unroll 1
-              for (int c = 0; c < HD / 8; ++c) {
-                uint4 w = *chunk(r, c);
-                uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+          }
+          // weights: this key's row of P, a bf16 a row of the item (with NR = 16 the pairs' low parts behind)
+          {
+            uint32_t hi[NR / 2], lo[kPair ? NR / 2 : 1];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0xffffu;
-                  if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u;
-                }
-                *chunk(r, c) = w;
+            for (int c = 0; c < NR; c += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(ref + c);
+              const float mm[4] = {m.x, m.y, m.z, m.w};
+              float p[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                p[e] = ex2f(fmaf(__uint_as_float(v[c + e]), sl, mm[e] == -INFINITY ? 0.f : -mm[e]));
+                Ls[c + e] += p[e];
+              }
+              if constexpr (kPair) {
+                pack_bf16_hilo(p[0], p[1], hi[c / 2], lo[c / 2]);
+                pack_bf16_hilo(p[2], p[3], hi[c / 2 + 1], lo[c / 2 + 1]);
+              } else {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(p[0], p[1]), b = __floats2bfloat162_rn(p[2], p[3]);
+                hi[c / 2] = *reinterpret_cast<const uint32_t*>(&a);
+                hi[c / 2 + 1] = *reinterpret_cast<const uint32_t*>(&b);
               }
             }
-            fence_proxy_async_smem();
+            uint8_t* prow = pbuf + r * 128;
+#pragma unroll
+            for (int c = 0; c < NR / 8; ++c) {
+              *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
+                  make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+              if constexpr (kPair)
+                *reinterpret_cast<uint4*>(prow + (((c + NR / 8) ^ (r & 7)) << 4)) =
+                    make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+            }
+          }
+          fence_proxy_async_smem();
+          if (first && r == 0) acc_first[gq] = first_acc;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[gq]);
+          ++job;
+        }
+        if (!ok) break;
+        // ---- the piece's end: row sums over the group, then group 0 joins both groups' parts
+        float M = -INFINITY, Lr = 0.f;  // of row r (threads below NR)
+        if (has) {
+          if (stop(wait_phase(&pv_done[gq], (uint32_t)(job - 1) & 1u, abort_f, g.status))) break;
+          warp_scatter_sum<NR>(Ls, lane);
+          const int at = scatter_row<NR>(lane);
+          if (NR >= 32) {
+#pragma unroll
+            for (int e = 0; e < NR / 32; ++e) scr[qr * NR + at + e] = Ls[e];
+          } else if (!(lane & 1)) {
+            scr[qr * NR + at] = Ls[0];
+          }
+          if (!meet(&fix[gq], fn)) break;
+          if (r < NR) {
+            M = ref[r];
+            Lr = (scr[r] + scr[NR + r]) + (scr[2 * NR + r] + scr[3 * NR + r]);
           }
         }
-        if (warp_live) {
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          const float sl = scale_log2;
-          // a loop each for the four kinds of tile: hidden keys or none, P as a pair or rounded once
-          auto weights = [&](auto all, auto pair) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {  // 32 keys
-              uint32_t hi16[16], lo16[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int k = c * 32 + 2 * e;
-                float a = fmaf(__uint_as_float(v[k]), sl, negm), b = fmaf(__uint_as_float(v[k + 1]), sl, negm);
-                if (!decltype(all)::value) {
-                  a = vis(k) ? a : -INFINITY;
-                  b = vis(k + 1) ? b : -INFINITY;
-                }
-                a = ex2f(a);
-                b = ex2f(b);
-                sum[(2 * e) & 3] += a;
-                sum[(2 * e + 1) & 3] += b;
-                if (decltype(pair)::value) {
-                  pack_bf16_hilo(a, b, hi16[e], lo16[e]);
-                } else {
-                  const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
-                  hi16[e] = *reinterpret_cast<const uint32_t*>(&h2);
-                }
-              }
-              tmem_st16(tS + c * 16, hi16);
-              if (decltype(pair)::value) tmem_st16(tS + 64 + c * 16, lo16);
-            }
-          };
-          if (two) {
-            if (wfull)
-              weights(std::true_type{}, std::false_type{});
-            else
-              weights(std::false_type{}, std::false_type{});
-          } else if (wfull) {
-            weights(std::true_type{}, std::true_type{});
-          } else {
-            weights(std::false_type{}, std::true_type{});
-          }
-          Ls = fmaf(Ls, f, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-          M = Mn;
-          tmem_st_wait();
-        }
-        if (t == t0 && r == 0) acc_first[gq] = first_acc;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[gq]);
-        ++job;
-      }
-      if (!ok) break;
-      const bool has = t0 < sg.nt;
-      if (has && stop(wait_phase(&pv_done[gq], (uint32_t)(job - 1) & 1u, abort_f, g.status))) break;
-      // ---- the piece's end: group 0 joins both groups' parts of a single query tile, else each has its own
-      float2 other = make_float2(-INFINITY, 0.f);
-      if (!two) {
         if (gq == 1) {
           if (xn > 0 && stop(wait_phase(x_free, (uint32_t)(xn - 1) & 1u, abort_f, g.status))) break;
-          xch[r] = make_float2(M, Ls);
+          if (r < NR) xch[r] = make_float2(M, Lr);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(x_full);
         } else {
           if (stop(wait_phase(x_full, (uint32_t)xn & 1u, abort_f, g.status))) break;
-          other = xch[r];
+          float2* coef = reinterpret_cast<float2*>(scr + 8 * NR);
+          if (r < NR) {
+            const float2 other = xch[r];
+            const float Mx = fmaxf(M, other.x), ref0 = Mx == -INFINITY ? 0.f : Mx;
+            const float wa = M == -INFINITY ? (both ? 0.f : 1.f) : ex2f(M - ref0);
+            const float wb = other.x == -INFINITY ? 0.f : ex2f(other.x - ref0);
+            const float Lt = fmaf(wb, other.y, wa * Lr);
+            const float inv = whole ? 1.f / Lt : 1.f;
+            coef[r] = make_float2(wa * inv, wb * inv);
+            if (!whole && r < rows) g.part_ml[sg.slot_row + r] = make_float2(Mx, Lt);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(x_free);
-        }
-        ++xn;
-      }
-      if (two || gq == 0) {
-        tc_fence_after();
-        const bool both = !two && sg.nt > 1;
-        const float Mx = fmaxf(M, other.x);
-        const float ref = Mx == -INFINITY ? 0.f : Mx;
-        // (a part whose maximum is NaN keeps its NaN through its sum)
-        const float wa = M == -INFINITY ? (both ? 0.f : 1.f) : ex2f(M - ref);
-        const float wb = other.x == -INFINITY ? 0.f : ex2f(other.x - ref);
-        const float Lt = fmaf(wb, other.y, wa * Ls);
-        const bool whole = walk.whole(sg);
-        const float inv = whole ? 1.f / Lt : 1.f;
-        if (warp_live) {
-          bf16* dst = out + (((long long)me.b * g.n + me.i) * g.nq + me.head) * HD;
-          float* pdst = g.part_o + (sg.slot_row + rr) * HD;
+          if (!meet(&fix[gq], fn)) break;
+          tc_fence_after();
+          if (qr * 32 < HD) {  // this lane's dimension is r
+            int f = x0 / g.G, h = x0 - f * g.G;  // block row (of the sequence or of the batch), head
+            const long long row0 = sg.prefix ? 0 : (long long)sg.b * g.n;
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            uint32_t a[32], b[32];
-            tmem_ld32(tO + c, a);
-            if (both) tmem_ld32(tO + 128 + c, b);
-            tmem_ld_wait();
-            float x[32];
+            for (int c0 = 0; c0 < NR && c0 < rows; c0 += 16) {
+              uint32_t a[16], a2[16], b[16], b2[16];
+              tmem_ld16u(tO + c0, a);
+              if (kPair) tmem_ld16u(tO + NR + c0, a2);
+              if (both) {
+                tmem_ld16u(tO + 128 + c0, b);
+                if (kPair) tmem_ld16u(tO + 128 + NR + c0, b2);
+              }
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              x[e] = __uint_as_float(a[e]);
-              if (both) x[e] = fmaf(wb, __uint_as_float(b[e]), wa * x[e]);
-            }
-            if (me.live) {
-              if (whole) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint4 w;
-                  __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&w);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) h2[i] = __floats2bfloat162_rn(x[e + 2 * i] * inv, x[e + 2 * i + 1] * inv);
-                  *reinterpret_cast<uint4*>(dst + c + e) = w;
+              for (int c = 0; c < 16; ++c) {
+                if (c0 + c >= rows) continue;
+                const float2 w = coef[c0 + c];
+                float xa = __uint_as_float(a[c]), xb = 0.f;
+                if (kPair) xa += __uint_as_float(a2[c]);
+                if (both) {
+                  xb = __uint_as_float(b[c]);
+                  if (kPair) xb += __uint_as_float(b2[c]);
                 }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  *reinterpret_cast<float4*>(pdst + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                const float x = both ? fmaf(w.y, xb, w.x * xa) : w.x * xa;
+                if (whole)
+                  out[((row0 + f) * g.nq + sg.hk * g.G + h) * HD + r] = __float2bfloat16_rn(x);
+                else
+                  g.part_o[(sg.slot_row + c0 + c) * HD + r] = x;
+                if (++h == g.G) {
+                  h = 0;
+                  ++f;
+                }
               }
             }
           }
-          if (me.live && !whole) g.part_ml[sg.slot_row + rr] = make_float2(both ? Mx : M, both ? Lt : Ls);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&o_free[0]);
+            mbar_arrive(&o_free[1]);
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&o_free[gq]);
-          if (!two) mbar_arrive(&o_free[1]);
-        }
+        ++xn;
+        if (qt == 0)
+          ++qn0;
+        else
+          ++qn1;
+        qt ^= 1;
+        tiles += sg.nt;
+        ++seg;
+        more = walk.next(sg);
       }
-      tiles += sg.nt;
-      ++seg;
     }
   }
   tc_fence_before();
@@ -677,29 +1086,45 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <int HD>
+template <int HD, int NR, bool TS, bool TP>
 static cudaError_t tc_launch(PagedGeom g, const CUtensorMap& tk, const CUtensorMap& tv, long long pool_rows,
                              const void* q, void* out, long long part_rows, cudaStream_t s) {
   typedef TcLayout<HD> L;
   static bool set = false;
   if (!set) {
-    DFL_RET(cudaFuncSetAttribute(paged_attn_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem));
+    DFL_RET(cudaFuncSetAttribute(paged_attn_tc_kernel<HD, NR, TS, TP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 L::kSmem));
     set = true;
   }
   // items of two query tiles where there are rows for them
   const int ri = g.n * g.G > 128 ? 256 : 128, rp = g.batch * g.n * g.G > 128 ? 256 : 128;
   if (paged_split(g, ri, rp, num_sms(), 2) > part_rows) return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
-  DFL_RET(launch_pdl(paged_attn_tc_kernel<HD>, dim3(g.grid), dim3(kTcThreads), L::kSmem, s, tk, tv, g, (int)pool_rows,
-                     (const bf16*)q, (bf16*)out, scale_log2));
+  DFL_RET(launch_pdl(paged_attn_tc_kernel<HD, NR, TS, TP>, dim3(g.grid), dim3(kTcThreads), L::kSmem, s, tk, tv, g,
+                     (int)pool_rows, (const bf16*)q, (bf16*)out, scale_log2));
   count_launch();
   return paged_merge_bf16(HD, g, out, s);
 }
 
+template <int HD>
+static cudaError_t tc_pick(const PagedGeom& g, const CUtensorMap& tk, const CUtensorMap& tv, long long pool_rows,
+                           const void* q, void* out, long long part_rows, cudaStream_t s) {
+  const int ns = g.n * g.G, np = g.shared ? g.batch * ns : ns;  // stacked rows of a sequence, of a shared prefix
+#define DFL_TC(NR, TS, TP) return tc_launch<HD, NR, TS, TP>(g, tk, tv, pool_rows, q, out, part_rows, s)
+  if (ns > 64) DFL_TC(0, false, false);
+  if (ns > 16) {
+    if (np > 64) DFL_TC(64, true, false);
+    DFL_TC(64, true, true);
+  }
+  if (np > 16) DFL_TC(16, true, false);
+  DFL_TC(16, true, true);
+#undef DFL_TC
+}
+
 cudaError_t paged_attention_tc(int hd, const PagedGeom& g, const CUtensorMap& tk, const CUtensorMap& tv,
                                long long pool_rows, const void* q, void* out, long long part_rows, cudaStream_t s) {
-  return hd == 64 ? tc_launch<64>(g, tk, tv, pool_rows, q, out, part_rows, s)
-                  : tc_launch<128>(g, tk, tv, pool_rows, q, out, part_rows, s);
+  return hd == 64 ? tc_pick<64>(g, tk, tv, pool_rows, q, out, part_rows, s)
+                  : tc_pick<128>(g, tk, tv, pool_rows, q, out, part_rows, s);
 }
 
 }  // namespace dfl
