@@ -55,6 +55,7 @@ namespace dfl {
 namespace {
 constexpr int kTcThreads = 384;
 constexpr uint64_t kTcWaitNs = 500000000ull;
+constexpr float kNoRef = 3e38f;  // -M of a row that has seen no key: every score lies more than 8 above it
 
 template <int HD>
 struct TcLayout {
@@ -294,12 +295,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               break;
             }
             uint8_t* dst = sm + s * L::kTile;
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kTile);
-            __syncwarp();
-            if (mine) {
+            if (elect_one()) mbar_arrive_expect_tx(&full[s], L::kTile);
+#pragma unroll 1
+            for (int p = 0; p < per; ++p) {
+              const int y = __shfl_sync(0xffffffffu, row, p);
+              uint8_t* at_p = dst + ((p << g.ps_log2) << 7);
+              if (elect_one()) {
 #pragma unroll
-              for (int dh = 0; dh < L::kHalves; ++dh)
-                tma_load_2d(dst + dh * 16384 + ((lane << g.ps_log2) << 7), kv == 0 ? &tmK : &tmV, &full[s], dh * 64, row);
+                for (int dh = 0; dh < L::kHalves; ++dh)
+                  tma_load_2d(at_p + dh * 16384, kv == 0 ? &tmK : &tmV, &full[s], dh * 64, y);
+              }
             }
             tiles = x + 1;  // (slots filled)
           }
@@ -313,42 +318,44 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp < 3) {
       // ---------------------------------------------------------- products of group gq
       const int gq = warp - 1;
-      if (lane == 0) {
-        const uint32_t idS = idesc_bf16_f32(128, 128), idO = idesc_bf16_f32(128, HD) | (1u << 16);  // values MN-major
-        const uint32_t idSt = idesc_bf16_f32(128, NR > 0 ? NR : 16);
-        const uint32_t idOt = idesc_bf16_f32(128, 64) | (3u << 15);  // values and weights both MN-major
-        const uint32_t tS = tmem + gq * 128, tO = tmem + 256 + gq * 128;
-        int job = 0;
-        bool ok = true;
-        // Both issuing warps see every tile land and release it: a slot is refilled only after both have
-        // been past it, so a wait never looks at a phase two fills away.
-        while (ok && walk.next(sg)) {
-          const bool cols = as_columns(sg), two = !cols && item_rows(sg) > 128;
-          const int buf = two ? gq : qt;
-          if (two || qt == 0) ok = wait_phase(&q_full[0], (uint32_t)qn0 & 1u, abort_f, g.status);
-          if (ok && (two || qt == 1)) ok = wait_phase(&q_full[1], (uint32_t)qn1 & 1u, abort_f, g.status);
-          const int t0 = two ? 0 : gq, step = two ? 1 : 2;
-          if (ok && t0 >= sg.nt) {  // no tile for this group
-            if (seg > 0) ok = wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g.status);
-            if (ok) mbar_arrive(&q_empty[buf]);
+      const uint32_t idS = idesc_bf16_f32(128, 128), idO = idesc_bf16_f32(128, HD) | (1u << 16);  // values MN-major
+      const uint32_t idSt = idesc_bf16_f32(128, NR > 0 ? NR : 16);
+      const uint32_t idOt = idesc_bf16_f32(128, 64) | (3u << 15);  // values and weights both MN-major
+      const uint32_t tS = tmem + gq * 128, tO = tmem + 256 + gq * 128;
+      auto wait = [&](uint64_t* b, uint32_t parity) { return !stop(wait_phase(b, parity & 1u, abort_f, g.status)); };
+      int job = 0;
+      bool ok = true;
+      // Both issuing warps see every tile land and release it: a slot is refilled only after both have
+      // been past it, so a wait never looks at a phase two fills away.
+      while (ok && walk.next(sg)) {
+        const bool cols = as_columns(sg), two = !cols && item_rows(sg) > 128;
+        const int buf = two ? gq : qt;
+        if (two || qt == 0) ok = wait(&q_full[0], qn0);
+        if (ok && (two || qt == 1)) ok = wait(&q_full[1], qn1);
+        const int t0 = two ? 0 : gq, step = two ? 1 : 2;
+        if (ok && t0 >= sg.nt) {  // no tile for this group
+          if (seg > 0) ok = wait(&o_free[gq], seg - 1);
+          if (ok && elect_one()) mbar_arrive(&q_empty[buf]);
+        }
+        const uint8_t* qs = sm + L::kQ + buf * L::kQBuf;
+        for (int t = 0; ok && t < sg.nt; ++t) {
+          const int xk = 2 * (tiles + t), sk = xk % NS, sv = (xk + 1) % NS;
+          const uint32_t pk = xk / NS, pv_ = (xk + 1) / NS;
+          ok = wait(&full[sk], pk);
+          if (!ok) break;
+          if (!two && (t & 1) != gq) {  // the other group's tile
+            if (elect_one()) mbar_arrive(&empty[sk]);
+            ok = wait(&full[sv], pv_);
+            if (ok && elect_one()) mbar_arrive(&empty[sv]);
+            continue;
           }
-          const uint8_t* qs = sm + L::kQ + buf * L::kQBuf;
-          for (int t = 0; ok && t < sg.nt; ++t) {
-            const int xk = 2 * (tiles + t), sk = xk % NS, sv = (xk + 1) % NS;
-            const uint32_t pk = (uint32_t)(xk / NS) & 1u, pv_ = (uint32_t)((xk + 1) / NS) & 1u;
-            ok = wait_phase(&full[sk], pk, abort_f, g.status);
-            if (!ok) break;
-            if (!two && (t & 1) != gq) {  // the other group's tile
-              mbar_arrive(&empty[sk]);
-              ok = wait_phase(&full[sv], pv_, abort_f, g.status);
-              if (ok) mbar_arrive(&empty[sv]);
-              continue;
-            }
-            // P of the last tile lies over S until its product is done
-            if (job > 0) ok = wait_phase(&pv_done[gq], (uint32_t)(job - 1) & 1u, abort_f, g.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint8_t* kt = sm + sk * L::kTile;
+          // P of the last tile lies over S (or in its buffer) until its product is done
+          if (job > 0) ok = wait(&pv_done[gq], job - 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint8_t* kt = sm + sk * L::kTile;
+          const bool last = t + step >= sg.nt;
+          if (elect_one()) {
             if (cols) {
 #pragma unroll
               for (int kk = 0; kk < HD / 16; ++kk) {
@@ -366,18 +373,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             tc_commit(&s_full[gq]);
             tc_commit(&empty[sk]);
-            if (!cols && t + step >= sg.nt) {  // the last scores of the piece: the query tile is free after them
+            if (!cols && last) {  // the last scores of the piece: the query tile is free after them
               tc_commit(&q_empty[buf]);
               if (two) tc_commit(&q_empty[buf]);
             }
-            ok = wait_phase(&full[sv], pv_, abort_f, g.status);
-            if (ok) mbar_arrive(&v_ready[gq]);
-            ok = ok && wait_phase(&p_full[gq], (uint32_t)job & 1u, abort_f, g.status);
-            if (ok && t == t0 && seg > 0) ok = wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t acc0 = t == t0 ? acc_first[gq] : 1u;
-            const uint32_t vt = smem_u32(sm + sv * L::kTile);
+          }
+          __syncwarp();
+          ok = wait(&full[sv], pv_);
+          if (ok && elect_one()) mbar_arrive(&v_ready[gq]);
+          ok = ok && wait(&p_full[gq], job);
+          if (ok && t == t0 && seg > 0) ok = wait(&o_free[gq], seg - 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t acc0 = t == t0 ? acc_first[gq] : 1u;
+          const uint32_t vt = smem_u32(sm + sv * L::kTile);
+          if (elect_one()) {
             if (cols) {
               // (head_dim 64: the upper 64 lanes take what lies behind the tile, and nothing reads them)
               const uint32_t ps = smem_u32(sm + L::kQ + gq * L::kQBuf + L::kP);
@@ -385,7 +395,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int kk = 0; kk < 8; ++kk)
                 tc_mma_f16(tO, smem_desc_mn(vt + kk * 2048, 16384), smem_desc_mn(ps + kk * 2048, 16384), idOt,
                            kk > 0 ? 1u : acc0);
-              if (t + step >= sg.nt) tc_commit(&q_empty[buf]);
+              if (last) tc_commit(&q_empty[buf]);
             } else {
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
@@ -393,17 +403,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             tc_commit(&pv_done[gq]);
             tc_commit(&empty[sv]);
-            ++job;
           }
-          tiles += sg.nt;
-          ++seg;
-          if (two || qt == 0) ++qn0;
-          if (two || qt == 1) ++qn1;
-          if (!two) qt ^= 1;
+          __syncwarp();
+          ++job;
         }
-        tc_commit(&drain[gq]);
-        mbar_wait(&drain[gq], 0, kTcWaitNs / 4);
+        tiles += sg.nt;
+        ++seg;
+        if (two || qt == 0) ++qn0;
+        if (two || qt == 1) ++qn1;
+        if (!two) qt ^= 1;
       }
+      if (elect_one()) tc_commit(&drain[gq]);
+      mbar_wait(&drain[gq], 0, kTcWaitNs / 4);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- query rows
@@ -797,26 +808,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             handover = false;
           }
           tc_fence_after();
-          uint32_t v[NR];
+          float v[NR];      // scores, then exponents s - M
+          uint64_t hid = 0; // rows that do not see the key
+          auto load_scores = [&]() {
 #pragma unroll
-          for (int c = 0; c < NR; c += 16) tmem_ld16u(tS + c, *reinterpret_cast<uint32_t(*)[16]>(&v[c]));
-          tmem_ld_wait();
-          uint64_t hid = 0;  // rows that do not see the key
+            for (int c = 0; c < NR; c += 16) tmem_ld16u(tS + c, *reinterpret_cast<uint32_t(*)[16]>(&v[c]));
+            tmem_ld_wait();
+            if (!inner) {
+#pragma unroll
+              for (int c = 0; c < NR; ++c)
+                if ((hid >> c) & 1) v[c] = -INFINITY;
+            }
+          };
+          auto exponents = [&]() {
+#pragma unroll
+            for (int c = 0; c < NR; c += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(ref + c);
+              const float2 x = fma2(make_float2(v[c], v[c + 1]), make_float2(sl, sl), make_float2(m.x, m.y));
+              const float2 y = fma2(make_float2(v[c + 2], v[c + 3]), make_float2(sl, sl), make_float2(m.z, m.w));
+              v[c] = x.x, v[c + 1] = x.y, v[c + 2] = y.x, v[c + 3] = y.y;
+            }
+          };
           if (!inner) {
+            const bool in = key >= key_lo && key < key_end;
             int i = x0 / g.G, h = x0 - i * g.G, sink, lo, hi;
             const int P = paged_len(g, sg.b), n = paged_rows(g, sg.b);
-            const bool in = key >= key_lo && key < key_end;
             if (!sg.prefix) row_span(g, P, n, i, sink, lo, hi);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < NR; ++c) {
               if (sg.prefix) {
                 const ItemRow w = item_row(g, sg, c);
                 row_span(g, paged_len(g, w.b), paged_rows(g, w.b), w.i, sink, lo, hi);
               }
-              if (!(in && c < rows && (key < sink || (key >= lo && key < hi)))) {
-                v[c] = 0xff800000u;
-                hid |= 1ull << c;
-              }
+              if (!(in && c < rows && (key < sink || (key >= lo && key < hi)))) hid |= 1ull << c;
               if (!sg.prefix && ++h == g.G) {
                 h = 0;
                 ++i;
@@ -824,27 +848,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
           }
+          load_scores();
           bool move = first;
           if (!first) {
-            bool over = false;
+            exponents();
+            float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < NR; c += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(ref + c);
-              over |= __uint_as_float(v[c]) * sl > m.x + 8.f || __uint_as_float(v[c + 1]) * sl > m.y + 8.f ||
-                      __uint_as_float(v[c + 2]) * sl > m.z + 8.f || __uint_as_float(v[c + 3]) * sl > m.w + 8.f;
-            }
-            over = __any_sync(0xffffffffu, over);
+            for (int c = 0; c < NR; c += 2) top = max3(top, v[c], v[c + 1]);
+            const uint32_t over = __any_sync(0xffffffffu, top > 8.f);
             if (lane == 0) bad_w[gq * 4 + qr] = over;
             ok = meet(&fix[gq], fn);
             if (!ok) break;
             move = bad_w[gq * 4] | bad_w[gq * 4 + 1] | bad_w[gq * 4 + 2] | bad_w[gq * 4 + 3];
           }
           if (move) {
+            if (!first) load_scores();
             // each row's largest score of the tile, by integers in the same order
 #pragma unroll
             for (int c = 0; c < NR; ++c) {
-              const float x = __uint_as_float(v[c]);
-              const int b = x != x ? (int)0x807fffff : (int)v[c] ^ ((int)v[c] >> 31 & 0x7fffffff);
+              const int raw = __float_as_int(v[c]);
+              const int b = v[c] != v[c] ? (int)0x807fffff : raw ^ (raw >> 31 & 0x7fffffff);
               const int m = __reduce_max_sync(0xffffffffu, b);
               if (lane == (c & 31)) scr[qr * NR + c] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
             }
@@ -852,18 +875,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok) break;
             if (r < NR) {
               const float mx = fmaxf(fmaxf(scr[r], scr[NR + r]), fmaxf(scr[2 * NR + r], scr[3 * NR + r]));
-              const float old = first ? -INFINITY : ref[r];
-              float mn = old, f = 1.f;
+              const float old = first ? kNoRef : ref[r];
+              float nm = old, f = 1.f;
               if (mx != -INFINITY) {
                 const float mt = mx * sl;
-                if (old == -INFINITY) {
-                  mn = mt;
-                } else if (mt > old + 8.f) {
-                  mn = mt;
-                  f = ex2f(old - mt);
+                if (old == kNoRef) {
+                  nm = -mt;
+                } else if (mt + old > 8.f) {
+                  nm = -mt;
+                  f = ex2f(-old - mt);
                 }
               }
-              ref[r] = mn;
+              ref[r] = nm;
               scr[4 * NR + r] = f;
             }
             ok = meet(&fix[gq], fn);
@@ -884,6 +907,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               ok = meet(&fix[gq], fn);  // P overwrites the factors
               if (!ok) break;
             }
+            exponents();
           }
           uint32_t first_acc = 0u;
           if (!inner) {
@@ -912,11 +936,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!((w >> (k & 31)) & 1u)) continue;
                 if (k == r) {
 #pragma unroll
-                  for (int c = 0; c < NR; ++c) {
-                    const float m = ref[c];
-                    const float p = ex2f(fmaf(__uint_as_float(v[c]), sl, m == -INFINITY ? 0.f : -m));
-                    scr[c] = (hid >> c) & 1 ? -1.f : p;
-                  }
+                  for (int c = 0; c < NR; ++c) scr[c] = (hid >> c) & 1 ? -1.f : ex2f(v[c]);
                 }
                 ok = meet(&fix[gq], fn);
                 if (!ok) break;
@@ -947,22 +967,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           {
             uint32_t hi[NR / 2], lo[kPair ? NR / 2 : 1];
 #pragma unroll
-            for (int c = 0; c < NR; c += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(ref + c);
-              const float mm[4] = {m.x, m.y, m.z, m.w};
-              float p[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                p[e] = ex2f(fmaf(__uint_as_float(v[c + e]), sl, mm[e] == -INFINITY ? 0.f : -mm[e]));
-                Ls[c + e] += p[e];
-              }
+            for (int c = 0; c < NR; c += 2) {
+              const float2 p = make_float2(ex2f(v[c]), ex2f(v[c + 1]));
+              const float2 l = add2(make_float2(Ls[c], Ls[c + 1]), p);
+              Ls[c] = l.x;
+              Ls[c + 1] = l.y;
               if constexpr (kPair) {
-                pack_bf16_hilo(p[0], p[1], hi[c / 2], lo[c / 2]);
-                pack_bf16_hilo(p[2], p[3], hi[c / 2 + 1], lo[c / 2 + 1]);
+                pack_bf16_hilo(p.x, p.y, hi[c / 2], lo[c / 2]);
               } else {
-                const __nv_bfloat162 a = __floats2bfloat162_rn(p[0], p[1]), b = __floats2bfloat162_rn(p[2], p[3]);
-                hi[c / 2] = *reinterpret_cast<const uint32_t*>(&a);
-                hi[c / 2 + 1] = *reinterpret_cast<const uint32_t*>(&b);
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
+                hi[c / 2] = *reinterpret_cast<const uint32_t*>(&h2);
               }
             }
             uint8_t* prow = pbuf + r * 128;
@@ -997,7 +1011,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           if (!meet(&fix[gq], fn)) break;
           if (r < NR) {
-            M = ref[r];
+            M = ref[r] == kNoRef ? -INFINITY : -ref[r];
             Lr = (scr[r] + scr[NR + r]) + (scr[2 * NR + r] + scr[3 * NR + r]);
           }
         }
@@ -1025,10 +1039,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (!meet(&fix[gq], fn)) break;
           tc_fence_after();
           if (qr * 32 < HD) {  // this lane's dimension is r
-            int f = x0 / g.G, h = x0 - f * g.G;  // block row (of the sequence or of the batch), head
-            const long long row0 = sg.prefix ? 0 : (long long)sg.b * g.n;
+            const int f = x0 / g.G;  // block row (of the sequence or of the batch)
+            int h = x0 - f * g.G;
+            bf16* dst = out + ((long long)((sg.prefix ? 0 : sg.b * g.n) + f) * g.nq + sg.hk * g.G + h) * HD + r;
+            float* pdst = g.part_o + sg.slot_row * HD + r;
+            const long long skip = (long long)(g.nq - g.G) * HD;  // to the next block row's heads
 #pragma unroll 1
-            for (int c0 = 0; c0 < NR && c0 < rows; c0 += 16) {
+            for (int c0 = 0; c0 < rows; c0 += 16) {
               uint32_t a[16], a2[16], b[16], b2[16];
               tmem_ld16u(tO + c0, a);
               if (kPair) tmem_ld16u(tO + NR + c0, a2);
@@ -1039,22 +1056,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               tmem_ld_wait();
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
-                if (c0 + c >= rows) continue;
                 const float2 w = coef[c0 + c];
-                float xa = __uint_as_float(a[c]), xb = 0.f;
-                if (kPair) xa += __uint_as_float(a2[c]);
-                if (both) {
-                  xb = __uint_as_float(b[c]);
-                  if (kPair) xb += __uint_as_float(b2[c]);
+                float x = __uint_as_float(a[c]);
+                if (kPair) x += __uint_as_float(a2[c]);
+                x *= w.x;
+                if (both) x = fmaf(w.y, kPair ? __uint_as_float(b[c]) + __uint_as_float(b2[c]) : __uint_as_float(b[c]), x);
+                if (c0 + c < rows) {
+                  if (whole)
+                    *dst = __float2bfloat16_rn(x);
+                  else
+                    *pdst = x;
                 }
-                const float x = both ? fmaf(w.y, xb, w.x * xa) : w.x * xa;
-                if (whole)
-                  out[((row0 + f) * g.nq + sg.hk * g.G + h) * HD + r] = __float2bfloat16_rn(x);
-                else
-                  g.part_o[(sg.slot_row + c0 + c) * HD + r] = x;
+                dst += HD;
+                pdst += HD;
                 if (++h == g.G) {
                   h = 0;
-                  ++f;
+                  dst += skip;
                 }
               }
             }
