@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kCoreThreads)
   pdl_wait();
   const PlanView v = plan_view<kCoreKeys, kCoreThreads>(g, reinterpret_cast<int*>(smem_raw + L::kRed));
   SegmentWalk<kCoreKeys> walk(g, v);
+  walk.start();
   Segment sg;
   while (walk.next(sg)) {
     ItemRow row[MRM];
@@ -322,80 +323,89 @@ __global__ void __launch_bounds__(kCoreThreads)
         if (l16 == 0) g.part_ml[sg.slot_row + r] = make_float2(m[x], l[x]);
       }
     }
+    if (!whole && v.pre_tiles == 0) {
+      int c0;
+      const int nc = walk.pieces(sg, c0);
+      int* done = reinterpret_cast<int*>(smem_raw + L::kRed);
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        *done = atomicAdd(g.tickets + 2 * sg.ordinal, 1) == nc - 1;
+      }
+      __syncthreads();
+      if (*done) {
+        __threadfence();
+        if (tid == 0) g.tickets[2 * sg.ordinal] = 0;
+        merge_item<T, HD>(g, sg.b, sg.rt, sg.hk, 0, min(g.ri, paged_rows(g, sg.b) * g.G - sg.rt * g.ri), nc, c0, tid >> 5,
+                          kCoreThreads / 32, out);
+      }
+    }
   }
 }
 
 // ------------------------------------------------------------------ merge
-// out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c over a row's partials c
-// (prefix pieces, then its sequence's own, each in tile order), m = max m_c.
-// One warp per (row, head); lane l owns HD / 32 dimensions.  A row that one
-// piece finished has nothing here.
+// Calls with a shared prefix: each row from its prefix pieces and its sequence's own, each in tile order.
+// One warp per (row, head).  A row that one piece finished has nothing here.
+constexpr int kMergeWarps = 8;
 template <typename T, int HD, int KT>
-__global__ void __launch_bounds__(64) paged_merge_kernel(const __grid_constant__ PagedGeom g, T* __restrict__ out) {
-  const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * 2 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    paged_merge_kernel(const __grid_constant__ PagedGeom g, T* __restrict__ out) {
+  const long long item = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
   pdl_launch();
   pdl_wait();
   if (item >= (long long)g.batch * g.n * g.nq) return;
   const int r = (int)(item / g.nq), h = (int)(item - (long long)r * g.nq);
   const int b = r / g.n, i = r - b * g.n;
-  if (i >= paged_rows(g, b)) return;
+  const int rows = paged_rows(g, b), P = paged_len(g, b);
   const int quota = g.plan[kPlanQuota], sh = g.plan[kPlanShared], pre = g.plan[kPlanPre];
-  const int hk = h / g.G, x = i * g.G + h % g.G, rt = x / g.ri;
-  // its sequence's own pieces
   int at = g.plan[kPlanCum + b];
-  for (int y = 0; y < rt; ++y) at += suffix_span<KT>(g, b, y, sh).count() * g.nkv;
-  const int cnt = suffix_span<KT>(g, b, rt, sh).count();
+  if (i >= rows) return;
+  const int hk = div_g(g, h), x = i * g.G + h - hk * g.G, rt = x / g.ri;
+  // its sequence's own pieces
+  for (int y = 0; y < rt; ++y) at += span_of<KT>(g, P, rows, y, sh).count() * g.nkv;
+  const int cnt = span_of<KT>(g, P, rows, rt, sh).count();
   at += hk * cnt;
   const int c0 = at / quota, ns = cnt > 0 ? (at + cnt - 1) / quota - c0 + 1 : 0;
   if (ns <= 1 && pre == 0) return;
   const long long srow = ((long long)(b * g.nrt + rt) * g.nkv + hk + c0) * g.slot_s + x - rt * g.ri;
-  int np = 0;
-  long long prow = 0;
-  if (pre > 0) {
-    const int xp = r * g.G + h % g.G, rp = xp / g.rp, k = hk * g.nrp + rp;
-    const int p0 = k * pre / quota;
-    np = ((k + 1) * pre - 1) / quota - p0 + 1;
-    prow = g.pre_row0 + (long long)(k + p0) * g.slot_p + xp - rp * g.rp;
-  }
-  const int nc = np + ns;
-  auto row_of = [&](int c) { return c < np ? prow + (long long)c * g.slot_p : srow + (long long)(c - np) * g.slot_s; };
-  float m = -INFINITY;
-  for (int c = lane; c < nc; c += 32) m = fmaxf(m, g.part_ml[row_of(c)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  constexpr int V = HD / 32;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f}, lsum = 0.f;
-  for (int cb = 0; cb < nc; cb += 32) {
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (cb + lane < nc) ml = g.part_ml[row_of(cb + lane)];
-    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-    lsum += w * ml.y;
-    const int lim = min(32, nc - cb);
-#pragma unroll 8
-    for (int c = 0; c < lim; ++c) {
-      const float wc = __shfl_sync(0xffffffffu, w, c);
-      const float* src = g.part_o + row_of(cb + c) * HD + lane * V;
-      if (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        acc[0] += wc * x.x, acc[1] += wc * x.y, acc[2] += wc * x.z, acc[3] += wc * x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        acc[0] += wc * x.x, acc[1] += wc * x.y;
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
-  T* dst = out + ((long long)r * g.nq + h) * HD + lane * V;
-#pragma unroll
-  for (int e = 0; e < V; ++e) dst[e] = from_f<T>(acc[e] / lsum);
+  const int xp = r * g.G + h - hk * g.G, rp = xp / g.rp, k = hk * g.nrp + rp;
+  const int p0 = k * pre / quota, np = pre > 0 ? ((k + 1) * pre - 1) / quota - p0 + 1 : 0;
+  const long long prow = g.pre_row0 + (long long)(k + p0) * g.slot_p + xp - rp * g.rp;
+  merge_row<T, HD>(g, np + ns, [&](int c) {
+    return c < np ? prow + (long long)c * g.slot_p : srow + (long long)(c - np) * g.slot_s;
+  }, out + ((long long)r * g.nq + h) * HD);
+}
+
+// Calls without one: block (c, y) joins rows 32 y .. 32 y + 31 of the item that CTA c recorded, if it did.
+template <typename T, int HD>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    paged_join_kernel(const __grid_constant__ PagedGeom g, T* __restrict__ out) {
+  pdl_launch();
+  pdl_wait();
+  const int4* rec = reinterpret_cast<const int4*>(g.records) + 2 * blockIdx.x;
+  const int4 a = rec[0];
+  const int c0 = rec[1].x;
+  if (a.x <= 0) return;
+  const int rows = min(g.ri, paged_rows(g, a.y) * g.G - a.z * g.ri), r0 = 32 * blockIdx.y;
+  if (r0 < rows)
+    merge_item<T, HD>(g, a.y, a.z, a.w, r0, min(32, rows - r0), a.x, c0, threadIdx.x >> 5, kMergeWarps, out);
+}
+
+cudaError_t paged_join_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t s) {
+  const dim3 grid(g.grid, (g.slot_s + 31) / 32);
+  if (hd == 64)
+    DFL_RET(launch_pdl(paged_join_kernel<bf16, 64>, grid, dim3(kMergeWarps * 32), 0, s, g, (bf16*)out));
+  else
+    DFL_RET(launch_pdl(paged_join_kernel<bf16, 128>, grid, dim3(kMergeWarps * 32), 0, s, g, (bf16*)out));
+  count_launch();
+  return cudaSuccess;
 }
 
 template <typename T, int HD, int KT>
 static cudaError_t merge_launch(const PagedGeom& g, void* out, cudaStream_t s) {
   const long long items = (long long)g.batch * g.n * g.nq;
-  DFL_RET(launch_pdl(paged_merge_kernel<T, HD, KT>, dim3((unsigned)((items + 1) / 2)), dim3(64), 0, s, g, (T*)out));
+  DFL_RET(launch_pdl(paged_merge_kernel<T, HD, KT>, dim3((unsigned)((items + kMergeWarps - 1) / kMergeWarps)),
+                     dim3(kMergeWarps * 32), 0, s, g, (T*)out));
   count_launch();
   return cudaSuccess;
 }
@@ -408,6 +418,7 @@ cudaError_t paged_merge_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t
 long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_quota) {
   g.ri = ri;
   g.rp = rp;
+  g.g_magic = (unsigned)(((1ull << 32) + g.G - 1) / g.G);
   g.nrt = (g.n * g.G + ri - 1) / ri;
   g.nrp = (g.batch * g.n * g.G + rp - 1) / rp;
   g.grid = grid;
@@ -443,7 +454,7 @@ static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const
   DFL_RET(launch_pdl(paged_attn_core_kernel<T, HD, MRM>, dim3(g.grid), dim3(kCoreThreads), L::kSmem, s, g, (const T*)q,
                      (const T*)kp, (const T*)vp, (T*)out, scale_log2));
   count_launch();
-  return merge_launch<T, HD, kCoreKeys>(g, out, s);
+  return g.shared ? merge_launch<T, HD, kCoreKeys>(g, out, s) : cudaSuccess;  // (else the CTAs join their pieces)
 }
 
 cudaError_t paged_attention_core(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp,

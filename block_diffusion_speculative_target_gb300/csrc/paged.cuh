@@ -14,8 +14,9 @@
 // whatever the lengths; a CTA's run covers the end of one item, whole items,
 // and the start of another.  An item inside one run whose rows have no other
 // part is finished there; every other piece leaves a partial result (row
-// maximum, sum, unnormalised output) that a merge kernel adds up in tile
-// order.  Prefix items come first in the line, head by head; suffix items
+// maximum, sum, unnormalised output).  Pieces are added up in tile order: by the
+// CTA that finishes an item's last one, or, where items have many rows or a
+// shared prefix has left pieces that belong to many items, by a second kernel.  Prefix items come first in the line, head by head; suffix items
 // follow in order of sequence, row group, head.  The cut depends on all
 // lengths of the call: a row's last bits may depend on the batch around it,
 // but the same call gives the same bits every time.
@@ -45,6 +46,9 @@ struct PagedGeom {
   long long pre_row0;    // first partial row of the prefix slots
   int slot_s, slot_p;    // partial rows per suffix / prefix slot
   int32_t* plan;         // [8 + batch + 1] written for the merge kernel
+  int32_t* tickets;      // [items][2] pieces done, zero between calls
+  int32_t* records;      // [CTAs][8] items to join after the kernel
+  unsigned g_magic;      // ceil(2^32 / G)
   int* status;
 };
 
@@ -88,12 +92,17 @@ struct TileSpan {
   __device__ __forceinline__ int tile(int t) const { return t < s1 - s0 ? s0 + t : w0 + t - (s1 - s0); }
 };
 
+// x / G for stacked row numbers (below 2^26, G <= 64: the error of the inverse stays below 1).
+__device__ __forceinline__ int div_g(const PagedGeom& g, int x) {
+  return g.G == 1 ? x : (int)__umulhi((unsigned)x, g.g_magic);
+}
+
 template <int KT>
-__device__ __forceinline__ TileSpan suffix_span(const PagedGeom& g, int b, int rt, int sh_tiles) {
+__device__ __forceinline__ TileSpan span_of(const PagedGeom& g, int P, int rows, int rt, int sh_tiles) {
   TileSpan s{0, 0, 0, 0};
-  const int rows = paged_rows(g, b), r0 = rt * g.ri;
+  const int r0 = rt * g.ri;
   if (r0 >= rows * g.G) return s;
-  const int P = paged_len(g, b), i0 = r0 / g.G, i1 = (min(r0 + g.ri, rows * g.G) - 1) / g.G;
+  const int i0 = div_g(g, r0), i1 = div_g(g, min(r0 + g.ri, rows * g.G) - 1);
   int sink, lo, hi, sink1, lo1;
   row_span(g, P, rows, i0, sink, lo, hi);    // the first row's window starts first
   row_span(g, P, rows, i1, sink1, lo1, hi);  // the last row's ends last
@@ -102,6 +111,11 @@ __device__ __forceinline__ TileSpan suffix_span(const PagedGeom& g, int b, int r
   s.s0 = sh_tiles;
   s.s1 = max(s.s0, min((sink1 + KT - 1) / KT, s.w0));
   return s;
+}
+
+template <int KT>
+__device__ __forceinline__ TileSpan suffix_span(const PagedGeom& g, int b, int rt, int sh_tiles) {
+  return span_of<KT>(g, paged_len(g, b), paged_rows(g, b), rt, sh_tiles);
 }
 
 // The tiles of every prefix item: those below sh that some row of the batch may see
@@ -123,6 +137,8 @@ struct Segment {
   int b, rt, hk;      // suffix: sequence, row group, head; prefix: row group rt of the batch, keys named by b's table
   TileSpan span;
   int t0, nt, total;  // its tiles [t0, t0 + nt) of the item's `total`
+  int line;           // the item's first line position
+  int ordinal;        // among the prefix or the suffix items
   long long slot_row; // first partial row of this piece
 };
 
@@ -133,11 +149,62 @@ struct PlanView {
   int b, cum;  // the sequence that holds the CTA's first tile (past the prefix items), and its line position
 };
 
+// plan_view of up to 32 sequences by every warp for itself, a lane a sequence.
+template <int KT>
+__device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write) {
+  const int lane = threadIdx.x & 31;
+  PlanView v;
+  const bool in = lane < g.batch;
+  const int rows = in ? paged_rows(g, lane) : 0, P = in ? paged_len(g, lane) : 0;
+  v.sh_tiles = v.min_len = v.pre_b = v.pre_tiles = 0;
+  if (g.shared) {
+    const unsigned live = __ballot_sync(0xffffffffu, rows > 0);
+    v.min_len = __reduce_min_sync(0xffffffffu, rows > 0 ? min(P, g.cap) : INT32_MAX);
+    if (live) {
+      v.pre_b = __ffs(live) - 1;
+      v.sh_tiles = max(0, min(*g.shared, v.min_len)) / KT;
+      if (v.sh_tiles > 0) v.pre_tiles = prefix_span<KT>(g, v.sh_tiles, v.min_len).count();
+    }
+  }
+  const int pre_total = v.pre_tiles * g.nrp * g.nkv;
+  int c = 0;
+  for (int rt = 0; rt < g.nrt; ++rt) c += span_of<KT>(g, P, rows, rt, v.sh_tiles).count();
+  c *= g.nkv;
+  int inc = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  const int at = pre_total + inc - c;
+  v.T = pre_total + __shfl_sync(0xffffffffu, inc, 31);
+  v.quota = max(g.min_quota, (int)((unsigned)(v.T + g.grid - 1) / (unsigned)g.grid));
+  const int start = max((int)min((long long)blockIdx.x * v.quota, (long long)v.T), pre_total);
+  const unsigned here = __ballot_sync(0xffffffffu, start >= at && start < at + c);
+  v.b = here ? __ffs(here) - 1 : g.batch;
+  v.cum = __shfl_sync(0xffffffffu, at, here ? v.b : 0);
+  if (write && blockIdx.x == 0 && threadIdx.x < 32) {
+    if (rows > 0 && P > g.cap - rows) set_status(g.status, DFLASH_STATUS_CAPACITY);
+    if (g.shared) {
+      if (in) g.plan[kPlanCum + lane] = at;
+      if (lane == 0) {
+        g.plan[kPlanT] = v.T;
+        g.plan[kPlanQuota] = v.quota;
+        g.plan[kPlanShared] = v.sh_tiles;
+        g.plan[kPlanPre] = v.pre_tiles;
+      }
+    }
+  }
+  return v;
+}
+
 // All threads of the block: the shared prefix, the line's length and where the CTA's run starts.
-// red: 2 NT / 32 + 8 ints of shared memory.  CTA 0 also writes the plan for the merge kernel.
+// red: 2 NT / 32 + 8 ints of shared memory.  With `write`, CTA 0 writes the plan for the merge kernel.
 template <int KT, int NT>
-__device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red) {
+__device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red, bool write = true) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (g.batch <= 32) return plan_small<KT>(g, write);
+  const bool first_cta = write && blockIdx.x == 0;
   PlanView v;
   const int per = (g.batch + NT - 1) / NT;
   const int b0 = min(tid * per, g.batch), b1 = min(b0 + per, g.batch);
@@ -180,7 +247,7 @@ __device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red) {
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
     sum += tiles_of(b);
-    if (blockIdx.x == 0 && paged_rows(g, b) > 0 && paged_len(g, b) > g.cap - paged_rows(g, b))
+    if (first_cta && paged_rows(g, b) > 0 && paged_len(g, b) > g.cap - paged_rows(g, b))
       set_status(g.status, DFLASH_STATUS_CAPACITY);
   }
   int inc = sum;  // inclusive scan over the block
@@ -207,14 +274,14 @@ __device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red) {
   __syncthreads();
   for (int b = b0; b < b1; ++b) {
     const int c = per == 1 ? sum : tiles_of(b);
-    if (blockIdx.x == 0) g.plan[kPlanCum + b] = at;
+    if (first_cta) g.plan[kPlanCum + b] = at;
     if (start >= at && start < at + c) {
       res[0] = b;
       res[1] = at;
     }
     at += c;
   }
-  if (blockIdx.x == 0 && tid == 0) {
+  if (first_cta && tid == 0) {
     g.plan[kPlanT] = v.T;
     g.plan[kPlanQuota] = v.quota;
     g.plan[kPlanShared] = v.sh_tiles;
@@ -236,7 +303,8 @@ struct SegmentWalk {
   int b, rt, hk;      // the next suffix item
   int item_at;        // its line position
   int pre_total;
-  __device__ __forceinline__ SegmentWalk(const PagedGeom& g_, const PlanView& v_) : g(g_), v(v_) {
+  __device__ __forceinline__ SegmentWalk(const PagedGeom& g_, const PlanView& v_) : g(g_), v(v_) {}
+  __device__ __forceinline__ void start() {
     pos = (int)min((long long)blockIdx.x * v.quota, (long long)v.T);
     end = (int)min((long long)pos + v.quota, (long long)v.T);
     pre_total = v.pre_tiles * g.nrp * g.nkv;
@@ -256,11 +324,13 @@ struct SegmentWalk {
       s.span = prefix_span<KT>(g, v.sh_tiles, v.min_len);
       s.total = v.pre_tiles;
       s.t0 = pos - k * v.pre_tiles;
+      s.line = k * v.pre_tiles;
       ordinal = k;
     } else {
       TileSpan sp;
       int c;
-      while (true) {  // ends: pos < T, so some item holds it
+      while (true) {  // (pos < T: some item holds it, unless the lengths changed since the plan)
+        if (b >= g.batch) return false;
         sp = suffix_span<KT>(g, b, rt, v.sh_tiles);
         c = sp.count();
         if (pos < item_at + c * g.nkv) break;
@@ -270,21 +340,28 @@ struct SegmentWalk {
           ++b;
         }
       }
-      hk = (pos - item_at) / c;
+      hk = (int)((unsigned)(pos - item_at) / (unsigned)c);
       s.prefix = false;
       s.b = b;
       s.rt = rt;
       s.hk = hk;
       s.span = sp;
       s.total = c;
-      s.t0 = pos - item_at - hk * c;
+      s.line = item_at + hk * c;
+      s.t0 = pos - s.line;
       ordinal = (b * g.nrt + rt) * g.nkv + hk;
     }
     s.nt = min(s.total - s.t0, end - pos);
     pos += s.nt;
+    s.ordinal = ordinal;
     const long long slot = (long long)ordinal + blockIdx.x;
     s.slot_row = s.prefix ? g.pre_row0 + slot * g.slot_p : slot * g.slot_s;
     return true;
+  }
+  // The pieces of the item: from CTA `c0` on, one a CTA.
+  __device__ __forceinline__ int pieces(const Segment& s, int& c0) const {
+    c0 = (int)((unsigned)s.line / (unsigned)v.quota);
+    return (int)((unsigned)(s.line + s.total - 1) / (unsigned)v.quota) - c0 + 1;
   }
   // No other piece contributes to this one's rows.
   __device__ __forceinline__ bool whole(const Segment& s) const {
@@ -299,7 +376,7 @@ struct ItemRow {
 };
 __device__ __forceinline__ ItemRow item_row(const PagedGeom& g, const Segment& s, int r) {
   ItemRow w;
-  const int x = s.rt * (s.prefix ? g.rp : g.ri) + r, q = x / g.G;
+  const int x = s.rt * (s.prefix ? g.rp : g.ri) + r, q = div_g(g, x);
   w.head = s.hk * g.G + (x - q * g.G);
   w.live = r < (s.prefix ? g.rp : g.ri);
   if (s.prefix) {
@@ -315,6 +392,73 @@ __device__ __forceinline__ ItemRow item_row(const PagedGeom& g, const Segment& s
   return w;
 }
 
+// One warp: a row of HD from `nc` partials, `row_of(c)` the row of the c-th, as
+//   sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c,  m = max m_c,
+// lane l owning HD / 32 dimensions.  Partials are read past L1: other SMs wrote them.
+template <typename T, int HD, typename F>
+__device__ __forceinline__ void merge_row(const PagedGeom& g, int nc, F row_of, T* __restrict__ dst) {
+  constexpr int V = HD / 32;
+  const int lane = threadIdx.x & 31;
+  float2 ml0 = make_float2(-INFINITY, 0.f);
+  if (lane < nc) ml0 = __ldcg(g.part_ml + row_of(lane));
+  float m = ml0.x;
+  for (int c = 32 + lane; c < nc; c += 32) m = fmaxf(m, __ldcg(g.part_ml + row_of(c)).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float acc[V], lsum = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  for (int cb = 0; cb < nc; cb += 32) {
+    float2 ml = ml0;
+    if (cb > 0) ml = cb + lane < nc ? __ldcg(g.part_ml + row_of(cb + lane)) : make_float2(-INFINITY, 0.f);
+    // (a part whose maximum is NaN keeps its NaN through its sum)
+    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+    lsum += w * ml.y;
+    const int lim = min(32, nc - cb);
+#pragma unroll 1
+    for (int c = 0; c < lim; c += 8) {
+      float x[8][V];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (c + u < lim) {
+          const float* src = g.part_o + row_of(cb + c + u) * HD + lane * V;
+          if (V == 4) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+            x[u][0] = y.x, x[u][1] = y.y, x[u][2 % V] = y.z, x[u][3 % V] = y.w;
+          } else {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+            x[u][0] = y.x, x[u][1] = y.y;
+          }
+        }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float wc = __shfl_sync(0xffffffffu, w, (c + u) & 31);
+        if (c + u < lim) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] += wc * x[u][e];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+#pragma unroll
+  for (int e = 0; e < V; ++e) dst[lane * V + e] = from_f<T>(acc[e] / lsum);
+}
+
+// One warp's share (rows w, w + warps, ...) of an item whose `nc` pieces begin with CTA c0's.
+// Not inlined: its registers are not to be kept free in the loops that it follows.
+template <typename T, int HD>
+__device__ __noinline__ void merge_item(const PagedGeom& g, int b, int rt, int hk, int r0, int rows, int nc, int c0,
+                                        int w, int warps, T* __restrict__ out) {
+  for (int r = r0 + w; r < r0 + rows; r += warps) {
+    const int x = rt * g.ri + r, i = div_g(g, x);
+    const long long base = ((long long)(b * g.nrt + rt) * g.nkv + hk + c0) * g.slot_s + r;
+    merge_row<T, HD>(g, nc, [&](int c) { return base + (long long)c * g.slot_s; },
+                     out + ((long long)(b * g.n + i) * g.nq + hk * g.G + x - i * g.G) * HD);
+  }
+}
+
 cudaError_t rope_table(float2* tab, int max_pos, int half, double theta);
 cudaError_t paged_append(int in_dtype, int dtype, const void* qkv, long long ld, int batch, int n, int nq, int nkv,
                          int hd, const int32_t* n_rows, const int32_t* table, int table_stride, const int32_t* len,
@@ -328,6 +472,7 @@ long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_quota);
 constexpr int kPagedTcKeys = 128;
 // Merge of the tensor-core kernel's partials.
 cudaError_t paged_merge_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t s);
+cudaError_t paged_join_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t s);
 // Attention of a call described by `g` (geometry, table, lengths; the split is filled in here): float32 on
 // the CUDA cores, bf16 on the tensor cores.
 cudaError_t paged_attention_core(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,

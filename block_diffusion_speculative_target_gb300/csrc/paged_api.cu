@@ -24,6 +24,9 @@ struct dflash_paged_workspace {
   float* part_o;     // [part_rows][hd]
   float2* part_ml;   // [part_rows]
   int32_t* plan;     // [kPlanCum + max_batch + 1]
+  int32_t* tickets;  // [items][2]
+  int32_t* records;  // [CTAs][8]
+  size_t ticket_bytes;
   int* status;
 };
 
@@ -102,8 +105,11 @@ int dflash_paged_workspace_alloc(const dflash_model_desc* d, int32_t max_batch, 
   if (max_rows > (1 << 20)) return DFLASH_ERR_TOO_LARGE;
   dflash_paged_workspace* w = new (std::nothrow) dflash_paged_workspace();
   if (!w) return DFLASH_ERR_OOM;
-  *w = dflash_paged_workspace{max_batch, max_rows, d->n_q_heads, d->n_kv_heads, d->head_dim, 0, 0, nullptr, nullptr,
-                              nullptr, nullptr};
+  w->max_batch = max_batch;
+  w->max_rows = max_rows;
+  w->nq = d->n_q_heads;
+  w->nkv = d->n_kv_heads;
+  w->hd = d->head_dim;
   cudaError_t e = cudaGetDevice(&w->device);
   if (e != cudaSuccess) {
     delete w;
@@ -111,12 +117,16 @@ int dflash_paged_workspace_alloc(const dflash_model_desc* d, int32_t max_batch, 
   }
   // whole row groups (at most twice the rows) and a slot per CTA, for a sequence's own pieces and the shared ones
   w->part_rows = 2 * (2ll * max_rows * d->n_q_heads + (long long)num_sms() * kPagedItemRows);
+  // items of 16 stacked rows at least, or of one sequence
+  w->ticket_bytes = (size_t)((long long)max_rows * d->n_q_heads / 16 + (long long)max_batch * d->n_kv_heads) * 8;
   struct Req {
     void** p;
     size_t bytes;
   } reqs[] = {{(void**)&w->part_o, (size_t)w->part_rows * d->head_dim * 4},
               {(void**)&w->part_ml, (size_t)w->part_rows * 8},
               {(void**)&w->plan, (size_t)(kPlanCum + max_batch + 1) * 4},
+              {(void**)&w->tickets, w->ticket_bytes},
+              {(void**)&w->records, (size_t)num_sms() * kPagedMaxCtas * 32},
               {(void**)&w->status, 4}};
   for (auto& r : reqs)
     if (cudaMalloc(r.p, r.bytes) != cudaSuccess) {
@@ -125,6 +135,7 @@ int dflash_paged_workspace_alloc(const dflash_model_desc* d, int32_t max_batch, 
       return DFLASH_ERR_OOM;
     }
   e = cudaMemset(w->status, 0, 4);
+  if (e == cudaSuccess) e = cudaMemset(w->tickets, 0, w->ticket_bytes);
   if (e == cudaSuccess) e = cudaStreamSynchronize(0);
   if (e != cudaSuccess) {
     dflash_paged_workspace_free(w);
@@ -139,6 +150,8 @@ int dflash_paged_workspace_free(dflash_paged_workspace* w) {
   cudaFree(w->part_o);
   cudaFree(w->part_ml);
   cudaFree(w->plan);
+  cudaFree(w->tickets);
+  cudaFree(w->records);
   cudaFree(w->status);
   delete w;
   return DFLASH_OK;
@@ -150,6 +163,8 @@ int dflash_paged_status(dflash_paged_workspace* w, dflash_stream_t stream, int32
   CK(cudaStreamSynchronize((cudaStream_t)stream));
   CK(cudaMemcpy(&v, w->status, 4, cudaMemcpyDeviceToHost));
   CK(cudaMemset(w->status, 0, 4));
+  // a call that timed out may have left pieces counted
+  if (v & DFLASH_STATUS_TIMEOUT) CK(cudaMemset(w->tickets, 0, w->ticket_bytes));
   *status_out = v;
   return DFLASH_OK;
 }
@@ -203,6 +218,8 @@ static int attend(dflash_pages* p, int32_t layer, const void* q, int32_t batch, 
   g.part_o = ws->part_o;
   g.part_ml = ws->part_ml;
   g.plan = ws->plan;
+  g.tickets = ws->tickets;
+  g.records = ws->records;
   g.status = ws->status;
   if (!paged_line_fits(g)) return DFLASH_ERR_TOO_LARGE;
   if (p->dtype == DFLASH_BF16)

@@ -9,14 +9,17 @@
 // and the row sum L are rescaled by 2^(M_old - M_new).  The weights are
 // p = 2^(s - M) <= 2^8.  An item runs in one of two layouts:
 //
-// rows as columns (at most NR = 16 or 64 stacked rows: single tokens, blocks)
-//   S = K_t Q^T            128 keys by NR rows: a thread holds one key's scores
+// rows as columns (at most 64 stacked rows: single tokens, blocks)
+//   S = K_t Q^T            128 keys by NR = 16 or 32 rows: a thread holds a key's scores
 //   O += V_t^T P           dims by rows, both operands from shared memory
 //   The products' M dimension is filled with keys and dimensions, so few rows
 //   cost few columns, and all 128 threads of a group share the exponentials of
 //   however few rows there are.  Whether a row's reference has to move is one
-//   vote a tile.  With NR = 16 P is kept as a bf16 pair hi + lo (about 2^-17
-//   relative), which is free here; with 64 it is rounded once.
+//   vote a tile.  P is kept as a bf16 pair hi + lo in neighbouring columns (about
+//   2^-17 relative), which is free here.  S has two buffers, and K runs ahead of
+//   V in the ring: the next scores are there before a tile's weights are done.
+//   Items of more than NR rows give each group half of them and every key tile;
+//   others are one block of rows whose key tiles the groups take in turn.
 // rows as rows (more rows: chunks, shared prefixes)
 //   S = Q K_t^T            128 rows by 128 keys: a thread holds one row
 //   O += P V_t             P as bf16 over S in TMEM
@@ -67,9 +70,9 @@ struct TcLayout {
   static constexpr uint32_t kQBuf = 32768;
   static constexpr uint32_t kP = 16384;                 // P within a buffer
   static constexpr uint32_t kXch = kQ + 2 * kQBuf;      // [128] (M, L) of group 1
-  static constexpr uint32_t kRef = kXch + 1024;         // [2][64] row references of the rows-as-columns layout
-  static constexpr uint32_t kBar = kRef + 512;
-  static constexpr int kBars = 2 * kSlots + 21;
+  static constexpr uint32_t kRef = kXch + 1024;         // [2][32] row references of the rows-as-columns layout
+  static constexpr uint32_t kBar = kRef + 256;
+  static constexpr int kBars = 2 * kSlots + 23;
   static constexpr uint32_t kMisc = kBar + kBars * 8;   // TMEM slot, abort flag, per-group words, scan scratch
   static constexpr int kSmem = kMisc + 256 + 1024;      // + alignment slack
   static_assert(kSmem <= 232448, "shared memory per block");
@@ -97,11 +100,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return d;
 }
-// Sum over the warp's lanes of N values a lane, N / 32 results a lane (N >= 32) or one (N = 16, in two lanes):
-// each step exchanges half of what is left with the lane `o` away.  Lane l ends with rows
-// warp_rows<N>(l) .. in order.
-template <int N>
-__device__ __forceinline__ void warp_scatter_sum(float (&x)[N], int lane) {
+// Sum (or maximum) over the warp's lanes of N values a lane: each step exchanges half of what is left with
+// the lane `o` away.  A lane ends with N / 32 results (N = 16: one, in two lanes), those from scatter_row on.
+template <int N, bool kMax>
+__device__ __forceinline__ void warp_scatter(float (&x)[N], int lane) {
   int n = N;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -111,11 +113,12 @@ __device__ __forceinline__ void warp_scatter_sum(float (&x)[N], int lane) {
 #pragma unroll
       for (int e = 0; e < N / 2; ++e)
         if (e < n) {
-          const float mine = up ? x[e + n] : x[e], theirs = up ? x[e] : x[e + n];
-          x[e] = mine + __shfl_xor_sync(0xffffffffu, theirs, o);
+          const float mine = up ? x[e + n] : x[e], theirs = __shfl_xor_sync(0xffffffffu, up ? x[e] : x[e + n], o);
+          x[e] = kMax ? fmaxf(mine, theirs) : mine + theirs;
         }
     } else {
-      x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+      const float theirs = __shfl_xor_sync(0xffffffffu, x[0], o);
+      x[0] = kMax ? fmaxf(x[0], theirs) : x[0] + theirs;
     }
   }
 }
@@ -197,21 +200,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* empty = bar + NS;        // [NS] both issuing warps are done with it
   uint64_t* q_full = bar + 2 * NS;   // [2]
   uint64_t* q_empty = q_full + 2;    // [2] two arrivals
-  uint64_t* s_full = q_full + 4;     // [2] scores of the group's tile in TMEM
-  uint64_t* p_full = q_full + 6;     // [2] its weights (four warps)
-  uint64_t* pv_done = q_full + 8;    // [2] its product with the values is done
-  uint64_t* o_free = q_full + 10;    // [2] the accumulator has been read (four warps)
-  uint64_t* fix = q_full + 12;       // [3] value scan: group 0, group 1 (four warps), both (eight)
-  uint64_t* x_full = q_full + 15;    // group 1's M and L are written (four warps)
-  uint64_t* x_free = q_full + 16;    // and read
-  uint64_t* drain = q_full + 17;     // [2] every product a warp issued is done
-  uint64_t* v_ready = q_full + 19;   // [2] the values of the group's tile have landed
+  uint64_t* s_full = q_full + 4;     // [2][2] scores of the group's tile in TMEM (rows as rows: one buffer)
+  uint64_t* p_full = q_full + 8;     // [2] its weights (four warps)
+  uint64_t* pv_done = q_full + 10;   // [2] its product with the values is done
+  uint64_t* o_free = q_full + 12;    // [2] the accumulator has been read (four warps)
+  uint64_t* fix = q_full + 14;       // [3] meetings of group 0, group 1 (four warps), both (eight)
+  uint64_t* x_full = q_full + 17;    // group 1's M and L are written (four warps)
+  uint64_t* x_free = q_full + 18;    // and read
+  uint64_t* drain = q_full + 19;     // [2] every product a warp issued is done
+  uint64_t* v_ready = q_full + 21;   // [2] the values of the group's tile have landed
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   uint32_t* tslot = misc;
   volatile int* abort_f = reinterpret_cast<volatile int*>(misc + 1);
   volatile uint32_t* acc_first = misc + 2;  // [2] the first product of an item adds to O instead of setting it
   volatile uint32_t* bad_w = misc + 4;      // [2][4] keys of the tile with a value that is not finite
-  int* red = reinterpret_cast<int*>(misc + 12);
+  int* red = reinterpret_cast<int*>(misc + 12);  // 32 ints
+  volatile uint32_t* last_w = misc + 44;    // [2] the group has finished an item's last piece
+  volatile uint32_t* vote_w = misc + 46;    // [2][2][4] some reference of the tile has to move
   float2* xch = reinterpret_cast<float2*>(sm + L::kXch);
   auto as_columns = [](const Segment& s) { return s.prefix ? TP : TS; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -225,7 +230,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 2);
-      mbar_init(&s_full[i], 1);
+      mbar_init(&s_full[2 * i], 1);
+      mbar_init(&s_full[2 * i + 1], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_free[i], 4);
@@ -248,28 +254,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tslot;
   pdl_launch();
-  pdl_wait();
-  const PlanView pv = plan_view<KT, kTcThreads>(g, red);
+  PlanView pv;
   SegmentWalk<KT> walk(g, pv);
   Segment sg;
+  bool more = false;
+  // The plan and the first step of the walk run twice, the first time on whatever the lengths hold while the
+  // previous kernel ends: nothing can start before these few hundred instructions, and fetching them takes
+  // three to four times as long as running them once they are there.
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass) pdl_wait();
+    pv = plan_view<KT, kTcThreads>(g, red, pass != 0);
+    walk.start();
+    more = walk.next(sg);
+  }
   // stacked rows of a piece's item, and whether it has two query tiles
   auto item_rows = [&](const Segment& s) {
     return s.prefix ? min(g.rp, g.batch * g.n * g.G - s.rt * g.rp) : min(g.ri, paged_rows(g, s.b) * g.G - s.rt * g.ri);
   };
+  // Order of an item's tiles in the ring: keys run `ahead` tiles ahead of values.
+  auto ahead_of = [&](bool cols, bool two) { return !cols ? 0 : two ? 1 : 2; };
+  auto k_at = [](int t, int ahead) { return t + max(0, t - ahead); };
+  auto v_at = [](int t, int ahead, int nt) { return min(nt, t + ahead + 1) + t; };
+  // whether both groups work on every key tile, each with its rows
+  auto both_on = [&](bool cols, int rows) { return rows > (cols ? NR : 128); };
   // query buffers: an item with one tile takes the buffer after the last one's, an item with two both
   int seg = 0, qt = 0, qn0 = 0, qn1 = 0;
   int tiles = 0;  // key tiles before the current piece
   auto stop = [&](bool ok) { return __any_sync(0xffffffffu, !ok); };
 
   if (warp < 4) {
-    reg_dec<64>();
+    reg_dec<72>();
     if (warp == 0) {
       // ---------------------------------------------------------- pages
       const int per = KT >> g.ps_log2;  // pages a tile
       const bool mine = lane < per;
-      int at = 0;  // tiles issued
-      bool ok = true;
-      while (ok && walk.next(sg)) {
+      bool ok = true;  // (`tiles` counts slots filled here)
+      for (; ok && more; more = walk.next(sg)) {
         const int key_end = sg.prefix ? pv.sh_tiles * KT : key_limit(g, sg.b);
         const int32_t* trow = g.table + (long long)sg.b * g.table_stride;
         // pool row of this lane's page of tile t (past the keys or a bad page: past the pool, read as zeros)
@@ -284,13 +305,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           return (int)(g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps);
         };
-        int row = page_row(sg.t0);
-        for (int t = sg.t0; t < sg.t0 + sg.nt; ++t) {
-          const int next_row = page_row(t + 1);
+        const bool cols = as_columns(sg);
+        const int ahead = ahead_of(cols, both_on(cols, item_rows(sg)));
+        // the rows of the next tiles: [0] the next value tile's, [ahead] the next key tile's
+        int rowq[3];
+#pragma unroll
+        for (int a = 0; a < 3; ++a) rowq[a] = page_row(sg.t0 + a);
+        for (int u = 0; ok && u < sg.nt + ahead; ++u) {
+          const int x = min(u, ahead), krow = x == 0 ? rowq[0] : x == 1 ? rowq[1] : rowq[2];
+          const int next_row = u >= ahead ? page_row(sg.t0 + u - ahead + 3) : 0;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const int x = 2 * at + kv, s = x % NS;
-            if (x >= NS && stop(wait_phase(&empty[s], (uint32_t)(x / NS - 1) & 1u, abort_f, g.status))) {
+            if (kv == 0 ? u >= sg.nt : u < ahead) continue;
+            const int s = tiles % NS;
+            if (tiles >= NS && stop(wait_phase(&empty[s], (uint32_t)(tiles / NS - 1) & 1u, abort_f, g.status))) {
               ok = false;
               break;
             }
@@ -298,7 +326,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (elect_one()) mbar_arrive_expect_tx(&full[s], L::kTile);
 #pragma unroll 1
             for (int p = 0; p < per; ++p) {
-              const int y = __shfl_sync(0xffffffffu, row, p);
+              const int y = __shfl_sync(0xffffffffu, kv == 0 ? krow : rowq[0], p);
               uint8_t* at_p = dst + ((p << g.ps_log2) << 7);
               if (elect_one()) {
 #pragma unroll
@@ -306,11 +334,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   tma_load_2d(at_p + dh * 16384, kv == 0 ? &tmK : &tmV, &full[s], dh * 64, y);
               }
             }
-            tiles = x + 1;  // (slots filled)
+            ++tiles;
           }
-          if (!ok) break;
-          row = next_row;
-          ++at;
+          if (u >= ahead) {
+            rowq[0] = rowq[1];
+            rowq[1] = rowq[2];
+            rowq[2] = next_row;
+          }
         }
       }
       // the last copies land before the CTA leaves, whatever became of their readers
@@ -327,91 +357,104 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool ok = true;
       // Both issuing warps see every tile land and release it: a slot is refilled only after both have
       // been past it, so a wait never looks at a phase two fills away.
-      while (ok && walk.next(sg)) {
-        const bool cols = as_columns(sg), two = !cols && item_rows(sg) > 128;
-        const int buf = two ? gq : qt;
-        if (two || qt == 0) ok = wait(&q_full[0], qn0);
-        if (ok && (two || qt == 1)) ok = wait(&q_full[1], qn1);
-        const int t0 = two ? 0 : gq, step = two ? 1 : 2;
-        if (ok && t0 >= sg.nt) {  // no tile for this group
+      for (; ok && more; more = walk.next(sg)) {
+        const bool cols = as_columns(sg), two = both_on(cols, item_rows(sg)), qtwo = two && !cols;
+        const int ahead = ahead_of(cols, two);
+        const int buf = qtwo ? gq : qt;
+        if (qtwo || qt == 0) ok = wait(&q_full[0], qn0);
+        if (ok && (qtwo || qt == 1)) ok = wait(&q_full[1], qn1);
+        if (ok && !two && gq >= sg.nt) {  // no tile for this group
           if (seg > 0) ok = wait(&o_free[gq], seg - 1);
           if (ok && elect_one()) mbar_arrive(&q_empty[buf]);
         }
-        const uint8_t* qs = sm + L::kQ + buf * L::kQBuf;
-        for (int t = 0; ok && t < sg.nt; ++t) {
-          const int xk = 2 * (tiles + t), sk = xk % NS, sv = (xk + 1) % NS;
-          const uint32_t pk = xk / NS, pv_ = (xk + 1) / NS;
-          ok = wait(&full[sk], pk);
-          if (!ok) break;
-          if (!two && (t & 1) != gq) {  // the other group's tile
-            if (elect_one()) mbar_arrive(&empty[sk]);
-            ok = wait(&full[sv], pv_);
-            if (ok && elect_one()) mbar_arrive(&empty[sv]);
-            continue;
-          }
-          // P of the last tile lies over S (or in its buffer) until its product is done
-          if (job > 0) ok = wait(&pv_done[gq], job - 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint8_t* kt = sm + sk * L::kTile;
-          const bool last = t + step >= sg.nt;
-          if (elect_one()) {
-            if (cols) {
-#pragma unroll
-              for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint64_t off = (uint64_t)(((kk & 3) * 32) >> 4);
-                tc_mma_f16(tS, smem_desc_sw128(kt + (kk >> 2) * 16384) + off,
-                           smem_desc_sw128(qs + (kk >> 2) * 8192) + off, idSt, kk > 0 ? 1u : 0u);
-              }
+        // (rows as columns: group 1 of a shared block has the 32 rows behind group 0's)
+        const uint8_t* qs = sm + L::kQ + buf * L::kQBuf + (two && cols ? gq * NR * 128 : 0);
+        int kjob = job;  // keys run ahead
+        for (int u = 0; ok && u < sg.nt + ahead; ++u) {
+          if (u < sg.nt) {
+            const int x = 2 * tiles + k_at(u, ahead), sk = x % NS;
+            ok = wait(&full[sk], x / NS);
+            if (!ok) break;
+            if (!two && (u & 1) != gq) {  // the other group's tile
+              if (elect_one()) mbar_arrive(&empty[sk]);
             } else {
+              // rows as rows: P of the last tile lies over S until its product is done
+              if ((!cols || (!TP && kjob == job)) && kjob > 0) ok = wait(&pv_done[gq], kjob - 1);
+              if (!ok) break;
+              tc_fence_after();
+              const uint8_t* kt = sm + sk * L::kTile;
+              const uint32_t d = cols ? tS + (kjob & 1) * 64 : tS;
+              if (elect_one()) {
+                if (cols) {
 #pragma unroll
-              for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint64_t off = (uint64_t)(((kk & 3) * 32) >> 4);
-                tc_mma_f16(tS, smem_desc_sw128(qs + (kk >> 2) * 16384) + off,
-                           smem_desc_sw128(kt + (kk >> 2) * 16384) + off, idS, kk > 0 ? 1u : 0u);
+                  for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint64_t off = (uint64_t)(((kk & 3) * 32) >> 4);
+                    tc_mma_f16(d, smem_desc_sw128(kt + (kk >> 2) * 16384) + off,
+                               smem_desc_sw128(qs + (kk >> 2) * 8192) + off, idSt, kk > 0 ? 1u : 0u);
+                  }
+                } else {
+#pragma unroll
+                  for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint64_t off = (uint64_t)(((kk & 3) * 32) >> 4);
+                    tc_mma_f16(d, smem_desc_sw128(qs + (kk >> 2) * 16384) + off,
+                               smem_desc_sw128(kt + (kk >> 2) * 16384) + off, idS, kk > 0 ? 1u : 0u);
+                  }
+                }
+                tc_commit(&s_full[2 * gq + (cols ? kjob & 1 : 0)]);
+                tc_commit(&empty[sk]);
+                // The last scores of the piece: the query tile is free after them.  (Where the other layout comes
+                // first, rows as columns free it after their last product: the hand-over below counts on it.)
+                if ((TP || !cols) && u + (two ? 1 : 2) >= sg.nt) {
+                  tc_commit(&q_empty[buf]);
+                  if (qtwo) tc_commit(&q_empty[buf]);
+                }
               }
-            }
-            tc_commit(&s_full[gq]);
-            tc_commit(&empty[sk]);
-            if (!cols && last) {  // the last scores of the piece: the query tile is free after them
-              tc_commit(&q_empty[buf]);
-              if (two) tc_commit(&q_empty[buf]);
+              __syncwarp();
+              ++kjob;
             }
           }
-          __syncwarp();
-          ok = wait(&full[sv], pv_);
-          if (ok && elect_one()) mbar_arrive(&v_ready[gq]);
-          ok = ok && wait(&p_full[gq], job);
-          if (ok && t == t0 && seg > 0) ok = wait(&o_free[gq], seg - 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t acc0 = t == t0 ? acc_first[gq] : 1u;
-          const uint32_t vt = smem_u32(sm + sv * L::kTile);
-          if (elect_one()) {
-            if (cols) {
-              // (head_dim 64: the upper 64 lanes take what lies behind the tile, and nothing reads them)
-              const uint32_t ps = smem_u32(sm + L::kQ + gq * L::kQBuf + L::kP);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_f16(tO, smem_desc_mn(vt + kk * 2048, 16384), smem_desc_mn(ps + kk * 2048, 16384), idOt,
-                           kk > 0 ? 1u : acc0);
-              if (last) tc_commit(&q_empty[buf]);
+          if (u >= ahead) {
+            const int t = u - ahead, x = 2 * tiles + v_at(t, ahead, sg.nt), sv = x % NS;
+            ok = wait(&full[sv], x / NS);
+            if (!ok) break;
+            if (!two && (t & 1) != gq) {
+              if (elect_one()) mbar_arrive(&empty[sv]);
             } else {
+              const bool first = t == (two ? 0 : gq);
+              if (elect_one()) mbar_arrive(&v_ready[gq]);
+              ok = wait(&p_full[gq], job);
+              if (ok && first && seg > 0) ok = wait(&o_free[gq], seg - 1);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t acc0 = first ? acc_first[gq] : 1u;
+              const uint32_t vt = smem_u32(sm + sv * L::kTile);
+              if (elect_one()) {
+                if (cols) {
+                  // (head_dim 64: the upper 64 lanes take what lies behind the tile, and nothing reads them)
+                  const uint32_t ps = smem_u32(sm + L::kQ + gq * L::kQBuf + L::kP);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_f16_tmem_a(tO, tS + kk * 8, smem_desc_mn(vt + kk * 2048, 16384), idO, kk > 0 ? 1u : acc0);
+                  for (int kk = 0; kk < 8; ++kk)
+                    tc_mma_f16(tO, smem_desc_mn(vt + kk * 2048, 16384), smem_desc_mn(ps + kk * 2048, 16384), idOt,
+                               kk > 0 ? 1u : acc0);
+                } else {
+#pragma unroll
+                  for (int kk = 0; kk < 8; ++kk)
+                    tc_mma_f16_tmem_a(tO, tS + kk * 8, smem_desc_mn(vt + kk * 2048, 16384), idO, kk > 0 ? 1u : acc0);
+                }
+                tc_commit(&pv_done[gq]);
+                tc_commit(&empty[sv]);
+                if (!TP && cols && t + (two ? 1 : 2) >= sg.nt) tc_commit(&q_empty[buf]);
+              }
+              __syncwarp();
+              ++job;
             }
-            tc_commit(&pv_done[gq]);
-            tc_commit(&empty[sv]);
           }
-          __syncwarp();
-          ++job;
         }
         tiles += sg.nt;
         ++seg;
-        if (two || qt == 0) ++qn0;
-        if (two || qt == 1) ++qn1;
-        if (!two) qt ^= 1;
+        if (qtwo || qt == 0) ++qn0;
+        if (qtwo || qt == 1) ++qn1;
+        if (!qtwo) qt ^= 1;
       }
       if (elect_one()) tc_commit(&drain[gq]);
       mbar_wait(&drain[gq], 0, kTcWaitNs / 4);
@@ -419,7 +462,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else {
       // ---------------------------------------------------------- query rows
       bool ok = true;
-      while (ok && walk.next(sg)) {
+      if (NR == 0 && !g.shared && lane == 0) {
+        // the item that this CTA's run begins inside of, when it is the second to hold a piece of it
+        int c0 = 0, nc = 0;
+        if (more && sg.t0 > 0) nc = walk.pieces(sg, c0);
+        if (c0 + 1 != blockIdx.x) nc = 0;
+        int4* rec = reinterpret_cast<int4*>(g.records) + 2 * blockIdx.x;
+        rec[0] = make_int4(nc, sg.b, sg.rt, sg.hk);
+        rec[1].x = c0;
+      }
+      for (; ok && more; more = walk.next(sg)) {
         const int rows = item_rows(sg);
         const bool cols = as_columns(sg), two = !cols && rows > 128;
         for (int w = 0; ok && w < (two ? 2 : 1); ++w) {
@@ -431,21 +483,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int c = lane % kChunks;
           int r = lane / kChunks;
           const int x = sg.rt * (sg.prefix ? g.rp : g.ri) + w * 128 + r;
-          int row = x / g.G, h = x - row * g.G;
-          if (!sg.prefix) row += sg.b * g.n;
+          const int row = div_g(g, x);
+          int h = x - row * g.G;
+          const bf16* src = q + ((long long)(row + (sg.prefix ? 0 : sg.b * g.n)) * g.nq + sg.hk * g.G + h) * HD + c * 8;
+          // the next row of this lane is kLanes stacked rows on
+          const int dq = div_g(g, kLanes), dh = kLanes - dq * g.G;
+          const long long step = ((long long)dq * g.nq + dh) * HD, wrap = (long long)(g.nq - g.G) * HD;
           uint8_t* dst = sm + L::kQ + buf * L::kQBuf + (c >> 3) * (cols ? 8192 : 16384);
+#pragma unroll 4
           for (const int lim = min(128, rows - w * 128); r < lim; r += kLanes) {
-            cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                       q + ((long long)row * g.nq + sg.hk * g.G + h) * HD + c * 8);
-            h += kLanes;
-            while (h >= g.G) {
+            cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src);
+            src += step;
+            h += dh;
+            if (h >= g.G) {
               h -= g.G;
-              ++row;
+              src += wrap;
             }
           }
           // (rows past the item's: scores of 0, which nothing reads)
           if (cols)
-            for (; r < NR; r += kLanes)
+            for (; r < (rows > NR ? 2 * NR : NR); r += kLanes)
               *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
           cp_async_wait_all();
           fence_proxy_async_smem();
@@ -463,7 +520,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int r = qr * 32 + lane;
     const uint32_t lanes = (uint32_t)(qr * 32) << 16;
     const uint32_t tS = tmem + lanes + gq * 128, tO = tmem + lanes + 256 + gq * 128;
-    int job = 0, xn = 0, fn = 0, fb = 0;  // tiles done; joins; phases of the group's barrier and of both groups'
+    int job = 0, xn = 0, fn = 0, fb = 0;  // tiles done; joins; phases of the group's meetings and of both groups'
+    uint32_t sn0 = 0, sn1 = 0;            // uses of the score buffers
     bool handover = false;                // a query tile of the rows-as-rows layout may still lie where P goes
     const float sl = scale_log2;
     bool ok = true;
@@ -509,6 +567,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int c = 0; c < cols; c += 16) tmem_st16(tO + c, z);
       tmem_st_wait();
     };
+    // After a partial result: the group that finishes its rows' last piece joins them all.
+    auto join = [&](int r0, int rows) {
+      int c0;
+      const int nc = walk.pieces(sg, c0), t = 2 * sg.ordinal + gq;
+      if (!meet(&fix[gq], fn)) return false;
+      if (r == 0) {
+        __threadfence();
+        const bool last = atomicAdd(g.tickets + t, 1) == nc - 1;
+        if (last) g.tickets[t] = 0;
+        last_w[gq] = last;
+      }
+      if (!meet(&fix[gq], fn)) return false;
+      if (last_w[gq]) {
+        __threadfence();
+        merge_item<bf16, HD>(g, sg.b, sg.rt, sg.hk, r0, rows, nc, c0, qr, 4, out);
+      }
+      return true;
+    };
     // The keys of the item that every row of it sees: [lo, hi).
     auto seen_by_all = [&](int x0, int rows, int key_lo, int key_end, int& lo, int& hi) {
       lo = 0;
@@ -516,15 +592,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!sg.prefix) {
         int a, b, c;
         const int P = paged_len(g, sg.b), n = paged_rows(g, sg.b);
-        row_span(g, P, n, (x0 + rows - 1) / g.G, a, lo, c);
-        row_span(g, P, n, x0 / g.G, a, b, hi);
+        row_span(g, P, n, div_g(g, x0 + rows - 1), a, lo, c);
+        row_span(g, P, n, div_g(g, x0), a, b, hi);
         lo = max(lo, key_lo);
         hi = min(hi, key_end);
       } else if (g.window > 0) {
         hi = 0;
       }
     };
-    bool more = walk.next(sg);
     // Prefix items come before suffix items, so those in the rows-as-rows layout (if any) come first.
     if constexpr (!TS || !TP) {
       while (ok && more && !as_columns(sg)) {
@@ -550,10 +625,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int t = t0; ok && t < sg.nt; t += step) {
           const int k0 = sg.span.tile(sg.t0 + t) * KT;
           const bool inner = k0 >= all_lo && k0 + KT <= all_hi;  // the same for all warps of the item
-          if (stop(wait_phase(&s_full[gq], (uint32_t)job & 1u, abort_f, g.status))) {
+          if (stop(wait_phase(&s_full[2 * gq], sn0 & 1u, abort_f, g.status))) {
             ok = false;
             break;
           }
+          ++sn0;
           tc_fence_after();
           float v[128];
           uint32_t vw[4] = {0u, 0u, 0u, 0u};  // visible keys of the tile
@@ -577,15 +653,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int e = 0; e < 128; ++e)
                 if (!((vw[e >> 5] >> (e & 31)) & 1u)) v[e] = -INFINITY;
             }
-            float mx[4];
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) mx[w] = max3(v[w], v[w + 4], v[w + 8]);
-#pragma unroll
-            for (int e = 12; e < 124; e += 8)
+            for (int e = 0; e < 128; e += 8)
 #pragma unroll
               for (int w = 0; w < 4; ++w) mx[w] = max3(mx[w], v[e + w], v[e + w + 4]);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) mx[w] = fmaxf(mx[w], v[124 + w]);
             const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             bool raise = false;
             if (m != -INFINITY) {
@@ -678,8 +750,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               uint32_t p16[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const int k = c * 32 + 2 * e;
-                float2 p = fma2(make_float2(v[k], v[k + 1]), sl2, nm2);
+                float2 p = fma2(make_float2(v[c * 32 + 2 * e], v[c * 32 + 2 * e + 1]), sl2, nm2);
                 p.x = ex2f(p.x);
                 p.y = ex2f(p.y);
                 sum[e & 1] = add2(sum[e & 1], p);
@@ -778,29 +849,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if constexpr (NR > 0) {
       while (ok && more) {
         // ------------------------------------------------ rows as columns: thread = key r of the tile
-        const int rows = item_rows(sg), t0 = gq;
-        const bool has = t0 < sg.nt, both = sg.nt > 1, whole = walk.whole(sg);
-        const int x0 = sg.rt * (sg.prefix ? g.rp : g.ri);
+        const int all_rows = item_rows(sg);
+        const bool two = both_on(true, all_rows);
+        const int rbase = two ? gq * NR : 0, rows = two ? min(NR, all_rows - rbase) : all_rows;  // the group's rows
+        const int t0 = two ? 0 : gq, step = two ? 1 : 2, ahead = ahead_of(true, two);
+        const bool has = t0 < sg.nt, both = !two && sg.nt > 1, whole = walk.whole(sg);
+        const int xi = sg.rt * (sg.prefix ? g.rp : g.ri), x0 = xi + rbase;  // the item's and the group's first row
         const int key_lo = sg.prefix ? 0 : pv.sh_tiles * KT;
         const int key_end = sg.prefix ? pv.sh_tiles * KT : key_limit(g, sg.b);
         int all_lo, all_hi;
-        seen_by_all(x0, rows, key_lo, key_end, all_lo, all_hi);
-        float* ref = reinterpret_cast<float*>(sm + L::kRef) + gq * 64;
+        seen_by_all(xi, all_rows, key_lo, key_end, all_lo, all_hi);
+        float* ref = reinterpret_cast<float*>(sm + L::kRef) + gq * 32;
         uint8_t* pbuf = sm + L::kQ + gq * L::kQBuf + L::kP;
         float* scr = reinterpret_cast<float*>(pbuf);  // scratch wherever no product reads P
-        constexpr bool kPair = NR == 16;
+        auto to_scratch = [&](float (&x)[NR]) {  // a warp's results of warp_scatter, by row
+          const int at = scatter_row<NR>(lane);
+          if (NR >= 32) {
+#pragma unroll
+            for (int e = 0; e < NR / 32; ++e) scr[qr * NR + at + e] = x[e];
+          } else if (!(lane & 1)) {
+            scr[qr * NR + at] = x[0];
+          }
+        };
         float Ls[NR];
 #pragma unroll
         for (int c = 0; c < NR; ++c) Ls[c] = 0.f;
         if (!meet(&fix[gq], fn)) break;  // the scratch's last readers are past it
-        for (int t = t0; ok && t < sg.nt; t += 2) {
+        for (int t = t0; ok && t < sg.nt; t += step) {
           const bool first = t == t0;
           const int k0 = sg.span.tile(sg.t0 + t) * KT, key = k0 + r;
           const bool inner = k0 >= all_lo && k0 + KT <= all_hi;
-          if (stop(wait_phase(&s_full[gq], (uint32_t)job & 1u, abort_f, g.status))) {
+          const int sb = job & 1;  // score buffer
+          uint32_t& sn = sb ? sn1 : sn0;
+          if (stop(wait_phase(&s_full[2 * gq + sb], sn & 1u, abort_f, g.status))) {
             ok = false;
             break;
           }
+          ++sn;
+          // the last product has read P and left O to be changed
+          bool pv_waited = first;
+          auto wait_pv = [&]() {
+            if (!pv_waited) ok = !stop(wait_phase(&pv_done[gq], (uint32_t)(job - 1) & 1u, abort_f, g.status));
+            if (!pv_waited) tc_fence_after();
+            pv_waited = true;
+            return ok;
+          };
           if (handover) {
             ok = (qn0 == 0 || !stop(wait_phase(&q_empty[0], (uint32_t)(qn0 - 1) & 1u, abort_f, g.status))) &&
                  (qn1 == 0 || !stop(wait_phase(&q_empty[1], (uint32_t)(qn1 - 1) & 1u, abort_f, g.status)));
@@ -809,10 +902,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           tc_fence_after();
           float v[NR];      // scores, then exponents s - M
-          uint64_t hid = 0; // rows that do not see the key
+          uint32_t hid = 0; // rows that do not see the key
           auto load_scores = [&]() {
 #pragma unroll
-            for (int c = 0; c < NR; c += 16) tmem_ld16u(tS + c, *reinterpret_cast<uint32_t(*)[16]>(&v[c]));
+            for (int c = 0; c < NR; c += 16) tmem_ld16u(tS + sb * 64 + c, *reinterpret_cast<uint32_t(*)[16]>(&v[c]));
             tmem_ld_wait();
             if (!inner) {
 #pragma unroll
@@ -831,16 +924,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           };
           if (!inner) {
             const bool in = key >= key_lo && key < key_end;
-            int i = x0 / g.G, h = x0 - i * g.G, sink, lo, hi;
+            int i = div_g(g, x0), h = x0 - i * g.G, sink, lo, hi;
             const int P = paged_len(g, sg.b), n = paged_rows(g, sg.b);
             if (!sg.prefix) row_span(g, P, n, i, sink, lo, hi);
 #pragma unroll 1
             for (int c = 0; c < NR; ++c) {
               if (sg.prefix) {
-                const ItemRow w = item_row(g, sg, c);
+                const ItemRow w = item_row(g, sg, rbase + c);
                 row_span(g, paged_len(g, w.b), paged_rows(g, w.b), w.i, sink, lo, hi);
               }
-              if (!(in && c < rows && (key < sink || (key >= lo && key < hi)))) hid |= 1ull << c;
+              if (!(in && c < rows && (key < sink || (key >= lo && key < hi)))) hid |= 1u << c;
               if (!sg.prefix && ++h == g.G) {
                 h = 0;
                 ++i;
@@ -856,21 +949,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int c = 0; c < NR; c += 2) top = max3(top, v[c], v[c + 1]);
             const uint32_t over = __any_sync(0xffffffffu, top > 8.f);
-            if (lane == 0) bad_w[gq * 4 + qr] = over;
+            // (two sets of votes: a warp may be at the next tile's while another reads this one's)
+            volatile uint32_t* votes = vote_w + (sb * 2 + gq) * 4;
+            if (lane == 0) votes[qr] = over;
             ok = meet(&fix[gq], fn);
             if (!ok) break;
-            move = bad_w[gq * 4] | bad_w[gq * 4 + 1] | bad_w[gq * 4 + 2] | bad_w[gq * 4 + 3];
+            move = votes[0] | votes[1] | votes[2] | votes[3];
           }
           if (move) {
+            // each row's largest score of the tile (a NaN sets no reference)
+            if (!wait_pv()) break;
             if (!first) load_scores();
-            // each row's largest score of the tile, by integers in the same order
-#pragma unroll
-            for (int c = 0; c < NR; ++c) {
-              const int raw = __float_as_int(v[c]);
-              const int b = v[c] != v[c] ? (int)0x807fffff : raw ^ (raw >> 31 & 0x7fffffff);
-              const int m = __reduce_max_sync(0xffffffffu, b);
-              if (lane == (c & 31)) scr[qr * NR + c] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
-            }
+            warp_scatter<NR, true>(v, lane);
+            to_scratch(v);
             ok = meet(&fix[gq], fn);
             if (!ok) break;
             if (r < NR) {
@@ -895,7 +986,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int c = 0; c < NR; ++c) Ls[c] *= scr[4 * NR + c];
 #pragma unroll 1
-              for (int c = 0; c < (kPair ? 2 * NR : NR); c += 16) {
+              for (int c = 0; c < 2 * NR; c += 16) {
                 uint32_t o[16];
                 tmem_ld16u(tO + c, o);
                 tmem_ld_wait();
@@ -907,17 +998,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               ok = meet(&fix[gq], fn);  // P overwrites the factors
               if (!ok) break;
             }
+            load_scores();
             exponents();
           }
           uint32_t first_acc = 0u;
           if (!inner) {
-            uint8_t* vt = sm + (2 * (tiles + t) + 1) % NS * L::kTile;
+            uint8_t* vt = sm + (2 * tiles + v_at(t, ahead, sg.nt)) % NS * L::kTile;
+            // (the last product's values had landed: this wait cannot take their phase for its own)
+            if (!wait_pv()) break;
             ok = !stop(wait_phase(&v_ready[gq], (uint32_t)job & 1u, abort_f, g.status));
             if (!ok) break;
             const bool bad = row_is_bad(vt);
             const uint32_t word = __ballot_sync(0xffffffffu, bad);
-            ok = meet(&fix[gq], fn);  // the votes have been read
-            if (!ok) break;
             if (lane == 0) bad_w[gq * 4 + qr] = word;
             ok = meet(&fix[gq], fn);
             if (!ok) break;
@@ -960,33 +1052,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = meet(&fix[gq], fn);
               }
               if (!ok) break;
+              // (a tile that both groups work on is cleaned once both have taken from it)
+              ok = two ? meet(&fix[2], fb) : meet(&fix[gq], fn);
+              if (!ok) break;
               if (bad) clean_row(vt);
             }
           }
-          // weights: this key's row of P, a bf16 a row of the item (with NR = 16 the pairs' low parts behind)
-          {
-            uint32_t hi[NR / 2], lo[kPair ? NR / 2 : 1];
+          // weights: this key's row of P, the high parts of the item's rows and the low ones behind
+          uint32_t hi[NR / 2], lo[NR / 2];
 #pragma unroll
-            for (int c = 0; c < NR; c += 2) {
-              const float2 p = make_float2(ex2f(v[c]), ex2f(v[c + 1]));
-              const float2 l = add2(make_float2(Ls[c], Ls[c + 1]), p);
-              Ls[c] = l.x;
-              Ls[c + 1] = l.y;
-              if constexpr (kPair) {
-                pack_bf16_hilo(p.x, p.y, hi[c / 2], lo[c / 2]);
-              } else {
-                const __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
-                hi[c / 2] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-            }
+          for (int c = 0; c < NR; c += 2) {
+            const float2 p = make_float2(ex2f(v[c]), ex2f(v[c + 1]));
+            const float2 l = add2(make_float2(Ls[c], Ls[c + 1]), p);
+            Ls[c] = l.x;
+            Ls[c + 1] = l.y;
+            pack_bf16_hilo(p.x, p.y, hi[c / 2], lo[c / 2]);
+          }
+          if (!wait_pv()) break;
+          {
             uint8_t* prow = pbuf + r * 128;
 #pragma unroll
             for (int c = 0; c < NR / 8; ++c) {
               *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
                   make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-              if constexpr (kPair)
-                *reinterpret_cast<uint4*>(prow + (((c + NR / 8) ^ (r & 7)) << 4)) =
-                    make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+              *reinterpret_cast<uint4*>(prow + ((c + NR / 8 ^ (r & 7)) << 4)) =
+                  make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
             }
           }
           fence_proxy_async_smem();
@@ -1001,66 +1091,65 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float M = -INFINITY, Lr = 0.f;  // of row r (threads below NR)
         if (has) {
           if (stop(wait_phase(&pv_done[gq], (uint32_t)(job - 1) & 1u, abort_f, g.status))) break;
-          warp_scatter_sum<NR>(Ls, lane);
-          const int at = scatter_row<NR>(lane);
-          if (NR >= 32) {
-#pragma unroll
-            for (int e = 0; e < NR / 32; ++e) scr[qr * NR + at + e] = Ls[e];
-          } else if (!(lane & 1)) {
-            scr[qr * NR + at] = Ls[0];
-          }
+          warp_scatter<NR, false>(Ls, lane);
+          to_scratch(Ls);
           if (!meet(&fix[gq], fn)) break;
           if (r < NR) {
             M = ref[r] == kNoRef ? -INFINITY : -ref[r];
             Lr = (scr[r] + scr[NR + r]) + (scr[2 * NR + r] + scr[3 * NR + r]);
           }
         }
-        if (gq == 1) {
-          if (xn > 0 && stop(wait_phase(x_free, (uint32_t)(xn - 1) & 1u, abort_f, g.status))) break;
-          if (r < NR) xch[r] = make_float2(M, Lr);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(x_full);
-        } else {
-          if (stop(wait_phase(x_full, (uint32_t)xn & 1u, abort_f, g.status))) break;
+        float2 other = make_float2(-INFINITY, 0.f);
+        if (!two) {
+          if (gq == 1) {
+            if (xn > 0 && stop(wait_phase(x_free, (uint32_t)(xn - 1) & 1u, abort_f, g.status))) break;
+            if (r < NR) xch[r] = make_float2(M, Lr);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_full);
+          } else {
+            if (stop(wait_phase(x_full, (uint32_t)xn & 1u, abort_f, g.status))) break;
+            if (r < NR) other = xch[r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_free);
+          }
+          ++xn;
+        }
+        if (two || gq == 0) {
           float2* coef = reinterpret_cast<float2*>(scr + 8 * NR);
+          const long long prow = sg.slot_row + rbase;
           if (r < NR) {
-            const float2 other = xch[r];
             const float Mx = fmaxf(M, other.x), ref0 = Mx == -INFINITY ? 0.f : Mx;
             const float wa = M == -INFINITY ? (both ? 0.f : 1.f) : ex2f(M - ref0);
             const float wb = other.x == -INFINITY ? 0.f : ex2f(other.x - ref0);
             const float Lt = fmaf(wb, other.y, wa * Lr);
             const float inv = whole ? 1.f / Lt : 1.f;
             coef[r] = make_float2(wa * inv, wb * inv);
-            if (!whole && r < rows) g.part_ml[sg.slot_row + r] = make_float2(Mx, Lt);
+            if (!whole && r < rows) g.part_ml[prow + r] = make_float2(Mx, Lt);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(x_free);
           if (!meet(&fix[gq], fn)) break;
           tc_fence_after();
           if (qr * 32 < HD) {  // this lane's dimension is r
-            const int f = x0 / g.G;  // block row (of the sequence or of the batch)
+            const int f = div_g(g, x0);  // block row (of the sequence or of the batch)
             int h = x0 - f * g.G;
             bf16* dst = out + ((long long)((sg.prefix ? 0 : sg.b * g.n) + f) * g.nq + sg.hk * g.G + h) * HD + r;
-            float* pdst = g.part_o + sg.slot_row * HD + r;
+            float* pdst = g.part_o + prow * HD + r;
             const long long skip = (long long)(g.nq - g.G) * HD;  // to the next block row's heads
 #pragma unroll 1
             for (int c0 = 0; c0 < rows; c0 += 16) {
               uint32_t a[16], a2[16], b[16], b2[16];
               tmem_ld16u(tO + c0, a);
-              if (kPair) tmem_ld16u(tO + NR + c0, a2);
+              tmem_ld16u(tO + NR + c0, a2);
               if (both) {
                 tmem_ld16u(tO + 128 + c0, b);
-                if (kPair) tmem_ld16u(tO + 128 + NR + c0, b2);
+                tmem_ld16u(tO + 128 + NR + c0, b2);
               }
               tmem_ld_wait();
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
                 const float2 w = coef[c0 + c];
-                float x = __uint_as_float(a[c]);
-                if (kPair) x += __uint_as_float(a2[c]);
-                x *= w.x;
-                if (both) x = fmaf(w.y, kPair ? __uint_as_float(b[c]) + __uint_as_float(b2[c]) : __uint_as_float(b[c]), x);
+                float x = (__uint_as_float(a[c]) + __uint_as_float(a2[c])) * w.x;
+                if (both) x = fmaf(w.y, __uint_as_float(b[c]) + __uint_as_float(b2[c]), x);
                 if (c0 + c < rows) {
                   if (whole)
                     *dst = __float2bfloat16_rn(x);
@@ -1079,11 +1168,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&o_free[0]);
-            mbar_arrive(&o_free[1]);
+            mbar_arrive(&o_free[gq]);
+            if (!two) mbar_arrive(&o_free[1]);
           }
+          if (!whole && pv.pre_tiles == 0 && !join(rbase, rows)) break;
         }
-        ++xn;
         if (qt == 0)
           ++qn0;
         else
@@ -1120,7 +1209,8 @@ static cudaError_t tc_launch(PagedGeom g, const CUtensorMap& tk, const CUtensorM
   DFL_RET(launch_pdl(paged_attn_tc_kernel<HD, NR, TS, TP>, dim3(g.grid), dim3(kTcThreads), L::kSmem, s, tk, tv, g,
                      (int)pool_rows, (const bf16*)q, (bf16*)out, scale_log2));
   count_launch();
-  return paged_merge_bf16(HD, g, out, s);
+  if (g.shared) return paged_merge_bf16(HD, g, out, s);
+  return NR == 0 ? paged_join_bf16(HD, g, out, s) : cudaSuccess;  // (rows as columns: the CTAs join their pieces)
 }
 
 template <int HD>
@@ -1130,8 +1220,8 @@ static cudaError_t tc_pick(const PagedGeom& g, const CUtensorMap& tk, const CUte
 #define DFL_TC(NR, TS, TP) return tc_launch<HD, NR, TS, TP>(g, tk, tv, pool_rows, q, out, part_rows, s)
   if (ns > 64) DFL_TC(0, false, false);
   if (ns > 16) {
-    if (np > 64) DFL_TC(64, true, false);
-    DFL_TC(64, true, true);
+    if (np > 64) DFL_TC(32, true, false);
+    DFL_TC(32, true, true);
   }
   if (np > 16) DFL_TC(16, true, false);
   DFL_TC(16, true, true);
