@@ -330,12 +330,12 @@ __global__ void __launch_bounds__(kCoreThreads)
       __syncthreads();
       if (tid == 0) {
         __threadfence();
-        *done = atomicAdd(g.tickets + 2 * sg.ordinal, 1) == nc - 1;
+        *done = atomicAdd(g.tickets + sg.ordinal, 1) == nc - 1;
       }
       __syncthreads();
       if (*done) {
         __threadfence();
-        if (tid == 0) g.tickets[2 * sg.ordinal] = 0;
+        if (tid == 0) g.tickets[sg.ordinal] = 0;
         merge_item<T, HD>(g, sg.b, sg.rt, sg.hk, 0, min(g.ri, paged_rows(g, sg.b) * g.G - sg.rt * g.ri), nc, c0, tid >> 5,
                           kCoreThreads / 32, out);
       }

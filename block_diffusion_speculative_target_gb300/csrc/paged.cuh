@@ -46,7 +46,7 @@ struct PagedGeom {
   long long pre_row0;    // first partial row of the prefix slots
   int slot_s, slot_p;    // partial rows per suffix / prefix slot
   int32_t* plan;         // [8 + batch + 1] written for the merge kernel
-  int32_t* tickets;      // [items][2] pieces done, zero between calls
+  int32_t* tickets;      // [items] pieces done, zero between calls
   int32_t* records;      // [CTAs][8] items to join after the kernel
   unsigned g_magic;      // ceil(2^32 / G)
   int* status;

@@ -24,7 +24,7 @@ struct dflash_paged_workspace {
   float* part_o;     // [part_rows][hd]
   float2* part_ml;   // [part_rows]
   int32_t* plan;     // [kPlanCum + max_batch + 1]
-  int32_t* tickets;  // [items][2]
+  int32_t* tickets;  // [items]
   int32_t* records;  // [CTAs][8]
   size_t ticket_bytes;
   int* status;
@@ -118,7 +118,7 @@ int dflash_paged_workspace_alloc(const dflash_model_desc* d, int32_t max_batch, 
   // whole row groups (at most twice the rows) and a slot per CTA, for a sequence's own pieces and the shared ones
   w->part_rows = 2 * (2ll * max_rows * d->n_q_heads + (long long)num_sms() * kPagedItemRows);
   // items of 16 stacked rows at least, or of one sequence
-  w->ticket_bytes = (size_t)((long long)max_rows * d->n_q_heads / 16 + (long long)max_batch * d->n_kv_heads) * 8;
+  w->ticket_bytes = (size_t)((long long)max_rows * d->n_q_heads / 16 + (long long)max_batch * d->n_kv_heads) * 4;
   struct Req {
     void** p;
     size_t bytes;

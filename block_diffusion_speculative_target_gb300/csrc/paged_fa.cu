@@ -15,8 +15,9 @@
 //   The products' M dimension is filled with keys and dimensions, so few rows
 //   cost few columns, and all 128 threads of a group share the exponentials of
 //   however few rows there are.  Whether a row's reference has to move is one
-//   vote a tile.  P is kept as a bf16 pair hi + lo in neighbouring columns (about
-//   2^-17 relative), which is free here.  S has two buffers, and K runs ahead of
+//   vote a tile.  With 16 rows P is kept as a bf16 pair hi + lo in neighbouring
+//   columns (about 2^-17 relative), which is free where keys are waited for; with
+//   32 it would double the work on a weight, and P is rounded once.  S has two buffers, and K runs ahead of
 //   V in the ring: the next scores are there before a tile's weights are done.
 //   Items of more than NR rows give each group half of them and every key tile;
 //   others are one block of rows whose key tiles the groups take in turn.
@@ -79,6 +80,12 @@ struct TcLayout {
   static_assert(kMisc % 8 == 0, "alignment");
 };
 
+// One 32-byte store (a whole sector; the address 32-byte aligned).
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 // max of three
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -172,9 +179,6 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
   }
 }
 
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {  // either of two bf16
-  return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
-}
 // Bits [a, b) of a word, clamped to it.
 __device__ __forceinline__ uint32_t bits_of(int a, int b) {
   a = max(a, 0);
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   volatile uint32_t* acc_first = misc + 2;  // [2] the first product of an item adds to O instead of setting it
   volatile uint32_t* bad_w = misc + 4;      // [2][4] keys of the tile with a value that is not finite
   int* red = reinterpret_cast<int*>(misc + 12);  // 32 ints
-  volatile uint32_t* last_w = misc + 44;    // [2] the group has finished an item's last piece
+  volatile uint32_t* last_w = misc + 44;    // the CTA has finished an item's last piece
   volatile uint32_t* vote_w = misc + 46;    // [2][2][4] some reference of the tile has to move
   float2* xch = reinterpret_cast<float2*>(sm + L::kXch);
   auto as_columns = [](const Segment& s) { return s.prefix ? TP : TS; };
@@ -293,27 +297,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (; ok && more; more = walk.next(sg)) {
         const int key_end = sg.prefix ? pv.sh_tiles * KT : key_limit(g, sg.b);
         const int32_t* trow = g.table + (long long)sg.b * g.table_stride;
-        // pool row of this lane's page of tile t (past the keys or a bad page: past the pool, read as zeros)
-        auto page_row = [&](int t) {
-          if (!mine || t >= sg.t0 + sg.nt) return pool_rows;
+        // This lane's page of tile t, -1 past the keys; and its pool row (a page that is none, or past the keys:
+        // past the pool, read as zeros).
+        auto page_of = [&](int t) {
           const int key = sg.span.tile(t) * KT + (lane << g.ps_log2);
-          if (key >= key_end) return pool_rows;
-          const int page = trow[key >> g.ps_log2];
-          if ((unsigned)page >= (unsigned)g.n_pages) {
+          const bool use = mine && t < sg.t0 + sg.nt && key < key_end;
+          return use ? trow[key >> g.ps_log2] : -1;
+        };
+        auto row_of = [&](int t, int page) {
+          if ((unsigned)page < (unsigned)g.n_pages)
+            return (int)(g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps);
+          if (mine && t < sg.t0 + sg.nt && sg.span.tile(t) * KT + (lane << g.ps_log2) < key_end)
             set_status(g.status, DFLASH_STATUS_BOUNDS);
-            return pool_rows;
-          }
-          return (int)(g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps);
+          return pool_rows;
         };
         const bool cols = as_columns(sg);
         const int ahead = ahead_of(cols, both_on(cols, item_rows(sg)));
         // the rows of the next tiles: [0] the next value tile's, [ahead] the next key tile's
-        int rowq[3];
+        int rowq[3] = {page_of(sg.t0), page_of(sg.t0 + 1), page_of(sg.t0 + 2)};
 #pragma unroll
-        for (int a = 0; a < 3; ++a) rowq[a] = page_row(sg.t0 + a);
+        for (int a = 0; a < 3; ++a) rowq[a] = row_of(sg.t0 + a, rowq[a]);
         for (int u = 0; ok && u < sg.nt + ahead; ++u) {
           const int x = min(u, ahead), krow = x == 0 ? rowq[0] : x == 1 ? rowq[1] : rowq[2];
-          const int next_row = u >= ahead ? page_row(sg.t0 + u - ahead + 3) : 0;
+          const int next_t = sg.t0 + u - ahead + 3, next_page = u >= ahead ? page_of(next_t) : -1;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             if (kv == 0 ? u >= sg.nt : u < ahead) continue;
@@ -339,7 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (u >= ahead) {
             rowq[0] = rowq[1];
             rowq[1] = rowq[2];
-            rowq[2] = next_row;
+            rowq[2] = row_of(next_t, next_page);
           }
         }
       }
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else {
       // ---------------------------------------------------------- query rows
       bool ok = true;
-      if (NR == 0 && !g.shared && lane == 0) {
+      if (NR != 16 && !g.shared && lane == 0) {
         // the item that this CTA's run begins inside of, when it is the second to hold a piece of it
         int c0 = 0, nc = 0;
         if (more && sg.t0 > 0) nc = walk.pieces(sg, c0);
@@ -537,14 +543,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto chunk = [&](uint8_t* vt, int key, int c) {
       return reinterpret_cast<uint4*>(vt + (c >> 3) * 16384 + key * 128 + (((c & 7) ^ (key & 7)) << 4));
     };
+    // x 0 is NaN for an x that is not finite, and so is a sum that has met it
     auto row_is_bad = [&](uint8_t* vt) {
-      uint32_t bad = 0u;
+      const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+      __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c) {
         const uint4 w = *chunk(vt, r, c);
-        bad |= nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w);
+        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = __hfma2(x[e], zero, acc[e]);
       }
-      return bad != 0u;
+      const float2 f = __bfloat1622float2(__hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3])));
+      return f.x != 0.f || f.y != 0.f;
     };
     auto clean_row = [&](uint8_t* vt) {
 #pragma unroll 1
@@ -567,21 +578,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int c = 0; c < cols; c += 16) tmem_st16(tO + c, z);
       tmem_st_wait();
     };
-    // After a partial result: the group that finishes its rows' last piece joins them all.
-    auto join = [&](int r0, int rows) {
+    // After a partial result: the CTA that finishes the item's last piece joins them all.
+    auto join = [&](int rows) {
       int c0;
-      const int nc = walk.pieces(sg, c0), t = 2 * sg.ordinal + gq;
+      const int nc = walk.pieces(sg, c0), t = sg.ordinal;
       if (!meet(&fix[gq], fn)) return false;
       if (r == 0) {
         __threadfence();
         const bool last = atomicAdd(g.tickets + t, 1) == nc - 1;
         if (last) g.tickets[t] = 0;
-        last_w[gq] = last;
+        *last_w = last;
       }
       if (!meet(&fix[gq], fn)) return false;
-      if (last_w[gq]) {
+      if (*last_w) {
         __threadfence();
-        merge_item<bf16, HD>(g, sg.b, sg.rt, sg.hk, r0, rows, nc, c0, qr, 4, out);
+        merge_item<bf16, HD>(g, sg.b, sg.rt, sg.hk, 0, rows, nc, c0, qr, 4, out);
       }
       return true;
     };
@@ -823,8 +834,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   }
                 } else {
 #pragma unroll
-                  for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4*>(pdst + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                  for (int e = 0; e < 32; e += 8) store32(pdst + c + e, *reinterpret_cast<const uint32_t(*)[8]>(&x[e]));
                 }
               }
             }
@@ -871,7 +881,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             scr[qr * NR + at] = x[0];
           }
         };
-        float Ls[NR];
+        constexpr bool kPair = NR == 16;
+        float Ls[NR], nm[NR];  // row sums of this thread's keys; -M
 #pragma unroll
         for (int c = 0; c < NR; ++c) Ls[c] = 0.f;
         if (!meet(&fix[gq], fn)) break;  // the scratch's last readers are past it
@@ -915,51 +926,79 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           };
           auto exponents = [&]() {
 #pragma unroll
-            for (int c = 0; c < NR; c += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(ref + c);
-              const float2 x = fma2(make_float2(v[c], v[c + 1]), make_float2(sl, sl), make_float2(m.x, m.y));
-              const float2 y = fma2(make_float2(v[c + 2], v[c + 3]), make_float2(sl, sl), make_float2(m.z, m.w));
-              v[c] = x.x, v[c + 1] = x.y, v[c + 2] = y.x, v[c + 3] = y.y;
+            for (int c = 0; c < NR; c += 2) {
+              const float2 x = fma2(make_float2(v[c], v[c + 1]), make_float2(sl, sl), make_float2(nm[c], nm[c + 1]));
+              v[c] = x.x, v[c + 1] = x.y;
             }
           };
           if (!inner) {
-            const bool in = key >= key_lo && key < key_end;
-            int i = div_g(g, x0), h = x0 - i * g.G, sink, lo, hi;
-            const int P = paged_len(g, sg.b), n = paged_rows(g, sg.b);
-            if (!sg.prefix) row_span(g, P, n, i, sink, lo, hi);
+            uint32_t see = 0u;
+            if (key >= key_lo && key < key_end) {
+              if (sg.prefix) {  // (a window over a prefix: the rows' sequences differ)
 #pragma unroll 1
-            for (int c = 0; c < NR; ++c) {
-              if (sg.prefix) {
-                const ItemRow w = item_row(g, sg, rbase + c);
-                row_span(g, paged_len(g, w.b), paged_rows(g, w.b), w.i, sink, lo, hi);
-              }
-              if (!(in && c < rows && (key < sink || (key >= lo && key < hi)))) hid |= 1u << c;
-              if (!sg.prefix && ++h == g.G) {
-                h = 0;
-                ++i;
-                row_span(g, P, n, i, sink, lo, hi);
+                for (int c = 0; c < rows; ++c) {
+                  const ItemRow w = item_row(g, sg, rbase + c);
+                  int sink, lo, hi;
+                  row_span(g, paged_len(g, w.b), paged_rows(g, w.b), w.i, sink, lo, hi);
+                  if (key < sink || (key >= lo && key < hi)) see |= 1u << c;
+                }
+              } else {
+                // block row i sees the key from i = key - P on, until the window has moved past it
+                const int d = key - min(paged_len(g, sg.b), g.cap);
+                const bool out_of = g.window > 0 && key >= g.sinks;
+                if (g.causal) {
+                  const long long from = (long long)max(d, 0) * g.G - x0;
+                  const long long to = out_of ? ((long long)d + g.window) * g.G - x0 : NR;
+                  see = bits_of((int)min(from, 32ll), (int)max(min(to, 32ll), 0ll));
+                } else if (!out_of || d >= -g.window) {
+                  see = 0xffffffffu;
+                }
               }
             }
+            hid = ~see;
           }
           load_scores();
+          // Whether a reference has to move is the group's vote.  Its answer is nearly always no, so the
+          // weights are computed while the votes come in.
+          volatile uint32_t* votes = vote_w + (sb * 2 + gq) * 4;  // (two sets: a warp may be a tile ahead)
+          uint32_t hi[NR / 2], lo[kPair ? NR / 2 : 1];
+          auto weights = [&]() {
+#pragma unroll
+            for (int c = 0; c < NR; c += 2) {
+              v[c] = ex2f(v[c]);
+              v[c + 1] = ex2f(v[c + 1]);
+              if constexpr (kPair) {
+                pack_bf16_hilo(v[c], v[c + 1], hi[c / 2], lo[c / 2]);
+              } else {
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[c], v[c + 1]);
+                hi[c / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+            }
+          };
           bool move = first;
           if (!first) {
             exponents();
-            float top = -INFINITY;
+            float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < NR; c += 2) top = max3(top, v[c], v[c + 1]);
-            const uint32_t over = __any_sync(0xffffffffu, top > 8.f);
-            // (two sets of votes: a warp may be at the next tile's while another reads this one's)
-            volatile uint32_t* votes = vote_w + (sb * 2 + gq) * 4;
-            if (lane == 0) votes[qr] = over;
-            ok = meet(&fix[gq], fn);
+            for (int c = 0; c < NR; c += 4) {
+              top[0] = max3(top[0], v[c], v[c + 1]);
+              top[1] = max3(top[1], v[c + 2], v[c + 3]);
+            }
+            const uint32_t over = __any_sync(0xffffffffu, fmaxf(top[0], top[1]) > 8.f);
+            if (lane == 0) {
+              votes[qr] = over;
+              mbar_arrive(&fix[gq]);
+            }
+            weights();
+            ok = !stop(wait_phase(&fix[gq], (uint32_t)fn & 1u, abort_f, g.status));
+            ++fn;
             if (!ok) break;
             move = votes[0] | votes[1] | votes[2] | votes[3];
           }
           if (move) {
             // each row's largest score of the tile (a NaN sets no reference)
             if (!wait_pv()) break;
-            if (!first) load_scores();
+            if (!first) load_scores();  // (v holds weights)
             warp_scatter<NR, true>(v, lane);
             to_scratch(v);
             ok = meet(&fix[gq], fn);
@@ -986,7 +1025,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int c = 0; c < NR; ++c) Ls[c] *= scr[4 * NR + c];
 #pragma unroll 1
-              for (int c = 0; c < 2 * NR; c += 16) {
+              for (int c = 0; c < (kPair ? 2 * NR : NR); c += 16) {
                 uint32_t o[16];
                 tmem_ld16u(tO + c, o);
                 tmem_ld_wait();
@@ -998,8 +1037,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               ok = meet(&fix[gq], fn);  // P overwrites the factors
               if (!ok) break;
             }
+#pragma unroll
+            for (int c = 0; c < NR; c += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(ref + c);
+              nm[c] = m.x, nm[c + 1] = m.y, nm[c + 2] = m.z, nm[c + 3] = m.w;
+            }
             load_scores();
             exponents();
+            weights();
           }
           uint32_t first_acc = 0u;
           if (!inner) {
@@ -1028,7 +1073,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!((w >> (k & 31)) & 1u)) continue;
                 if (k == r) {
 #pragma unroll
-                  for (int c = 0; c < NR; ++c) scr[c] = (hid >> c) & 1 ? -1.f : ex2f(v[c]);
+                  for (int c = 0; c < NR; ++c) scr[c] = (hid >> c) & 1 ? -1.f : v[c];
                 }
                 ok = meet(&fix[gq], fn);
                 if (!ok) break;
@@ -1058,15 +1103,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (bad) clean_row(vt);
             }
           }
-          // weights: this key's row of P, the high parts of the item's rows and the low ones behind
-          uint32_t hi[NR / 2], lo[NR / 2];
+          // this key's row of P: a bf16 a row of the item (pairs: the low parts behind the high ones)
 #pragma unroll
           for (int c = 0; c < NR; c += 2) {
-            const float2 p = make_float2(ex2f(v[c]), ex2f(v[c + 1]));
-            const float2 l = add2(make_float2(Ls[c], Ls[c + 1]), p);
+            const float2 l = add2(make_float2(Ls[c], Ls[c + 1]), make_float2(v[c], v[c + 1]));
             Ls[c] = l.x;
             Ls[c + 1] = l.y;
-            pack_bf16_hilo(p.x, p.y, hi[c / 2], lo[c / 2]);
           }
           if (!wait_pv()) break;
           {
@@ -1075,8 +1117,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int c = 0; c < NR / 8; ++c) {
               *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
                   make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-              *reinterpret_cast<uint4*>(prow + ((c + NR / 8 ^ (r & 7)) << 4)) =
-                  make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+              if constexpr (kPair)
+                *reinterpret_cast<uint4*>(prow + ((c + NR / 8 ^ (r & 7)) << 4)) =
+                    make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
             }
           }
           fence_proxy_async_smem();
@@ -1139,17 +1182,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int c0 = 0; c0 < rows; c0 += 16) {
               uint32_t a[16], a2[16], b[16], b2[16];
               tmem_ld16u(tO + c0, a);
-              tmem_ld16u(tO + NR + c0, a2);
+              if (kPair) tmem_ld16u(tO + NR + c0, a2);
               if (both) {
                 tmem_ld16u(tO + 128 + c0, b);
-                tmem_ld16u(tO + 128 + NR + c0, b2);
+                if (kPair) tmem_ld16u(tO + 128 + NR + c0, b2);
               }
               tmem_ld_wait();
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
                 const float2 w = coef[c0 + c];
-                float x = (__uint_as_float(a[c]) + __uint_as_float(a2[c])) * w.x;
-                if (both) x = fmaf(w.y, __uint_as_float(b[c]) + __uint_as_float(b2[c]), x);
+                float x = __uint_as_float(a[c]), xb = 0.f;
+                if (kPair) x += __uint_as_float(a2[c]);
+                if (both) xb = kPair ? __uint_as_float(b[c]) + __uint_as_float(b2[c]) : __uint_as_float(b[c]);
+                x *= w.x;
+                if (both) x = fmaf(w.y, xb, x);
                 if (c0 + c < rows) {
                   if (whole)
                     *dst = __float2bfloat16_rn(x);
@@ -1171,7 +1217,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_arrive(&o_free[gq]);
             if (!two) mbar_arrive(&o_free[1]);
           }
-          if (!whole && pv.pre_tiles == 0 && !join(rbase, rows)) break;
+          if (NR == 16 && !whole && pv.pre_tiles == 0 && !join(rows)) break;  // (few rows; else a kernel does)
         }
         if (qt == 0)
           ++qn0;
@@ -1210,7 +1256,7 @@ static cudaError_t tc_launch(PagedGeom g, const CUtensorMap& tk, const CUtensorM
                      (int)pool_rows, (const bf16*)q, (bf16*)out, scale_log2));
   count_launch();
   if (g.shared) return paged_merge_bf16(HD, g, out, s);
-  return NR == 0 ? paged_join_bf16(HD, g, out, s) : cudaSuccess;  // (rows as columns: the CTAs join their pieces)
+  return NR == 16 ? cudaSuccess : paged_join_bf16(HD, g, out, s);  // (few rows: the CTAs join their pieces)
 }
 
 template <int HD>
