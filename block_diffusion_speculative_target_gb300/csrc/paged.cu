@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kCoreThreads)
 #pragma unroll
     for (int x = 0; x < MRM; ++x) {
       const int r = rq + 16 * x;
-      row[x] = item_row(g, sg, r);
+      row[x] = item_row(g, sg.prefix, sg.b, sg.hk, sg.rt * (sg.prefix ? g.rp : g.ri), r);
       sink[x] = lo[x] = hi[x] = 0;
       if (row[x].live) row_span(g, paged_len(g, row[x].b), paged_rows(g, row[x].b), row[x].i, sink[x], lo[x], hi[x]);
       m[x] = -INFINITY;

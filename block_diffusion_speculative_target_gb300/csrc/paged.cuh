@@ -149,7 +149,7 @@ struct PlanView {
   int b, cum;  // the sequence that holds the CTA's first tile (past the prefix items), and its line position
 };
 
-// plan_view of up to 32 sequences by every warp for itself, a lane a sequence.
+// plan_view of up to 32 sequences by one warp for itself, a lane a sequence (`write`: it writes the plan).
 template <int KT>
 __device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write) {
   const int lane = threadIdx.x & 31;
@@ -183,7 +183,7 @@ __device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write) {
   const unsigned here = __ballot_sync(0xffffffffu, start >= at && start < at + c);
   v.b = here ? __ffs(here) - 1 : g.batch;
   v.cum = __shfl_sync(0xffffffffu, at, here ? v.b : 0);
-  if (write && blockIdx.x == 0 && threadIdx.x < 32) {
+  if (write && blockIdx.x == 0) {
     if (rows > 0 && P > g.cap - rows) set_status(g.status, DFLASH_STATUS_CAPACITY);
     if (g.shared) {
       if (in) g.plan[kPlanCum + lane] = at;
@@ -203,7 +203,7 @@ __device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write) {
 template <int KT, int NT>
 __device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red, bool write = true) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (g.batch <= 32) return plan_small<KT>(g, write);
+  if (g.batch <= 32) return plan_small<KT>(g, write && tid < 32);
   const bool first_cta = write && blockIdx.x == 0;
   PlanView v;
   const int per = (g.batch + NT - 1) / NT;
@@ -369,23 +369,24 @@ struct SegmentWalk {
   }
 };
 
-// Block row and head of the item's stacked row r, and whether it is a row of the call.
+// Block row and head of an item's stacked row r, numbered from x0 of its sequence (or of the batch), and
+// whether it is a row of the call.
 struct ItemRow {
   int b, i, head;
   bool live;
 };
-__device__ __forceinline__ ItemRow item_row(const PagedGeom& g, const Segment& s, int r) {
+__device__ __forceinline__ ItemRow item_row(const PagedGeom& g, bool prefix, int b, int hk, int x0, int r) {
   ItemRow w;
-  const int x = s.rt * (s.prefix ? g.rp : g.ri) + r, q = div_g(g, x);
-  w.head = s.hk * g.G + (x - q * g.G);
-  w.live = r < (s.prefix ? g.rp : g.ri);
-  if (s.prefix) {
+  const int x = x0 + r, q = div_g(g, x);
+  w.head = hk * g.G + (x - q * g.G);
+  w.live = r < (prefix ? g.rp : g.ri);
+  if (prefix) {
     w.live = w.live && q < g.batch * g.n;
     const int f = w.live ? q : 0;
     w.b = f / g.n;
     w.i = f - w.b * g.n;
   } else {
-    w.b = s.b;
+    w.b = b;
     w.i = q;
   }
   w.live = w.live && w.i < paged_rows(g, w.b);

@@ -73,11 +73,13 @@ struct TcLayout {
   static constexpr uint32_t kXch = kQ + 2 * kQBuf;      // [128] (M, L) of group 1
   static constexpr uint32_t kRef = kXch + 1024;         // [2][32] row references of the rows-as-columns layout
   static constexpr uint32_t kBar = kRef + 256;
-  static constexpr int kBars = 2 * kSlots + 23;
+  static constexpr int kBars = 2 * kSlots + 31;
   static constexpr uint32_t kMisc = kBar + kBars * 8;   // TMEM slot, abort flag, per-group words, scan scratch
-  static constexpr int kSmem = kMisc + 256 + 1024;      // + alignment slack
+  static constexpr uint32_t kPieces = kMisc + 256;      // [4] pieces
+  static constexpr int kUsed = kPieces + 4 * 96;
+  static constexpr int kSmem = kUsed + 512;             // room for a base off the 1024-byte grid
   static_assert(kSmem <= 232448, "shared memory per block");
-  static_assert(kMisc % 8 == 0, "alignment");
+  static_assert(kMisc % 16 == 8 || kMisc % 16 == 0, "alignment");
 };
 
 // One 32-byte store (a whole sector; the address 32-byte aligned).
@@ -86,6 +88,24 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
+// One piece of the CTA's run, as every role needs it; the last one of the run is followed by one without tiles.
+struct Piece {
+  int nt, prefix, two, whole;     // key tiles; both groups on each of them; no other piece has its rows
+  int b, hk, rt, ordinal;         // as in Segment
+  int rows, x0;                   // stacked rows of the item, the first one's number
+  int s0, sn, w0, t0;             // tile t of the piece is t0 + t of the item's: s0 + t below sn, then w0 + t - sn
+  int key_lo, key_end;            // keys of the item: [key_lo, key_end)
+  int all_lo, all_hi;             // those that every row of it sees
+  int P, n;                       // the sequence's keys before this call, its rows
+  int nc, c0;                     // pieces of the item, the first one's CTA
+  long long slot_row;
+  __device__ __forceinline__ int tile(int t) const {
+    t += t0;
+    return t < sn ? s0 + t : w0 + t - sn;
+  }
+};
+static_assert(sizeof(Piece) == 96, "a slot of the ring");
+
 // max of three
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -197,8 +217,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                          bf16* __restrict__ out, float scale_log2) {
   typedef TcLayout<HD> L;
   constexpr int KT = kPagedTcKeys, NS = L::kSlots;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (sm - smem_raw > L::kSmem - L::kUsed) {  // (the base is on the grid; were it not, nothing would be written)
+    set_status(g.status, DFLASH_STATUS_TIMEOUT);
+    return;
+  }
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::kBar);
   uint64_t* full = bar;              // [NS] a key or value tile has landed
   uint64_t* empty = bar + NS;        // [NS] both issuing warps are done with it
@@ -213,6 +237,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* x_free = q_full + 18;    // and read
   uint64_t* drain = q_full + 19;     // [2] every product a warp issued is done
   uint64_t* v_ready = q_full + 21;   // [2] the values of the group's tile have landed
+  uint64_t* pc_full = q_full + 23;   // [4] a piece is described
+  uint64_t* pc_empty = q_full + 27;  // [4] and no role needs its description (11 warps)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   uint32_t* tslot = misc;
   volatile int* abort_f = reinterpret_cast<volatile int*>(misc + 1);
@@ -222,7 +248,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   volatile uint32_t* last_w = misc + 44;    // the CTA has finished an item's last piece
   volatile uint32_t* vote_w = misc + 46;    // [2][2][4] some reference of the tile has to move
   float2* xch = reinterpret_cast<float2*>(sm + L::kXch);
-  auto as_columns = [](const Segment& s) { return s.prefix ? TP : TS; };
+  Piece* pieces = reinterpret_cast<Piece*>(sm + L::kPieces);
+  auto as_columns = [](int prefix) { return prefix ? TP : TS; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tma_prefetch_desc(&tmK);
@@ -243,6 +270,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&drain[i], 1);
       mbar_init(&v_ready[i], 1);
     }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&pc_full[i], 1);
+      mbar_init(&pc_empty[i], 11);
+    }
     mbar_init(&fix[2], 8);
     mbar_init(x_full, 4);
     mbar_init(x_free, 4);
@@ -259,33 +290,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = *tslot;
   pdl_launch();
   PlanView pv;
-  SegmentWalk<KT> walk(g, pv);
-  Segment sg;
-  bool more = false;
-  // The plan and the first step of the walk run twice, the first time on whatever the lengths hold while the
-  // previous kernel ends: nothing can start before these few hundred instructions, and fetching them takes
-  // three to four times as long as running them once they are there.
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass) pdl_wait();
-    pv = plan_view<KT, kTcThreads>(g, red, pass != 0);
-    walk.start();
-    more = walk.next(sg);
+  if (g.batch > 32) {  // a larger batch is planned by the whole block
+    pdl_wait();
+    pv = plan_view<KT, kTcThreads>(g, red);
   }
-  // stacked rows of a piece's item, and whether it has two query tiles
-  auto item_rows = [&](const Segment& s) {
-    return s.prefix ? min(g.rp, g.batch * g.n * g.G - s.rt * g.rp) : min(g.ri, paged_rows(g, s.b) * g.G - s.rt * g.ri);
-  };
   // Order of an item's tiles in the ring: keys run `ahead` tiles ahead of values.
   auto ahead_of = [&](bool cols, bool two) { return !cols ? 0 : two ? 1 : 2; };
   auto k_at = [](int t, int ahead) { return t + max(0, t - ahead); };
   auto v_at = [](int t, int ahead, int nt) { return min(nt, t + ahead + 1) + t; };
-  // whether both groups work on every key tile, each with its rows
-  auto both_on = [&](bool cols, int rows) { return rows > (cols ? NR : 128); };
   // query buffers: an item with one tile takes the buffer after the last one's, an item with two both
   int seg = 0, qt = 0, qn0 = 0, qn1 = 0;
   int tiles = 0;  // key tiles before the current piece
   auto stop = [&](bool ok) { return __any_sync(0xffffffffu, !ok); };
+  // The pieces of the run come from warp 3 through a ring of four.
+  auto wait_piece = [&](int s) {
+    return !stop(wait_phase(&pc_full[s & 3], (uint32_t)(s >> 2) & 1u, abort_f, g.status));
+  };
+  auto done_piece = [&](int s) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&pc_empty[s & 3]);
+  };
 
   if (warp < 4) {
     reg_dec<72>();
@@ -294,35 +318,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int per = KT >> g.ps_log2;  // pages a tile
       const bool mine = lane < per;
       bool ok = true;  // (`tiles` counts slots filled here)
-      for (; ok && more; more = walk.next(sg)) {
-        const int key_end = sg.prefix ? pv.sh_tiles * KT : key_limit(g, sg.b);
-        const int32_t* trow = g.table + (long long)sg.b * g.table_stride;
+      pdl_wait();
+      for (; (ok = wait_piece(seg)); ++seg) {
+        const Piece& pc = pieces[seg & 3];
+        const int nt = pc.nt, hk = pc.hk, key_end = pc.key_end;
+        if (nt == 0) break;
+        const int32_t* trow = g.table + (long long)pc.b * g.table_stride;
         // This lane's page of tile t, -1 past the keys; and its pool row (a page that is none, or past the keys:
         // past the pool, read as zeros).
         auto page_of = [&](int t) {
-          const int key = sg.span.tile(t) * KT + (lane << g.ps_log2);
-          const bool use = mine && t < sg.t0 + sg.nt && key < key_end;
+          const int key = pc.tile(t) * KT + (lane << g.ps_log2);
+          const bool use = mine && t < nt && key < key_end;
           return use ? trow[key >> g.ps_log2] : -1;
         };
         auto row_of = [&](int t, int page) {
           if ((unsigned)page < (unsigned)g.n_pages)
-            return (int)(g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps);
-          if (mine && t < sg.t0 + sg.nt && sg.span.tile(t) * KT + (lane << g.ps_log2) < key_end)
+            return (int)(g.page_row0 + ((long long)page * g.nkv + hk) * g.ps);
+          if (mine && t < nt && pc.tile(t) * KT + (lane << g.ps_log2) < key_end)
             set_status(g.status, DFLASH_STATUS_BOUNDS);
           return pool_rows;
         };
-        const bool cols = as_columns(sg);
-        const int ahead = ahead_of(cols, both_on(cols, item_rows(sg)));
+        const int ahead = ahead_of(as_columns(pc.prefix), pc.two);
         // the rows of the next tiles: [0] the next value tile's, [ahead] the next key tile's
-        int rowq[3] = {page_of(sg.t0), page_of(sg.t0 + 1), page_of(sg.t0 + 2)};
+        int rowq[3] = {page_of(0), page_of(1), page_of(2)};
 #pragma unroll
-        for (int a = 0; a < 3; ++a) rowq[a] = row_of(sg.t0 + a, rowq[a]);
-        for (int u = 0; ok && u < sg.nt + ahead; ++u) {
+        for (int a = 0; a < 3; ++a) rowq[a] = row_of(a, rowq[a]);
+        for (int u = 0; ok && u < nt + ahead; ++u) {
           const int x = min(u, ahead), krow = x == 0 ? rowq[0] : x == 1 ? rowq[1] : rowq[2];
-          const int next_t = sg.t0 + u - ahead + 3, next_page = u >= ahead ? page_of(next_t) : -1;
+          const int next_t = u - ahead + 3, next_page = u >= ahead ? page_of(next_t) : -1;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            if (kv == 0 ? u >= sg.nt : u < ahead) continue;
+            if (kv == 0 ? u >= nt : u < ahead) continue;
             const int s = tiles % NS;
             if (tiles >= NS && stop(wait_phase(&empty[s], (uint32_t)(tiles / NS - 1) & 1u, abort_f, g.status))) {
               ok = false;
@@ -348,6 +374,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             rowq[2] = row_of(next_t, next_page);
           }
         }
+        if (!ok) break;
+        done_piece(seg);
       }
       // the last copies land before the CTA leaves, whatever became of their readers
       for (int x = max(0, tiles - NS); x < tiles; ++x) mbar_wait(&full[x % NS], (uint32_t)(x / NS) & 1u, kTcWaitNs / 4);
@@ -361,23 +389,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       auto wait = [&](uint64_t* b, uint32_t parity) { return !stop(wait_phase(b, parity & 1u, abort_f, g.status)); };
       int job = 0;
       bool ok = true;
+      pdl_wait();
       // Both issuing warps see every tile land and release it: a slot is refilled only after both have
       // been past it, so a wait never looks at a phase two fills away.
-      for (; ok && more; more = walk.next(sg)) {
-        const bool cols = as_columns(sg), two = both_on(cols, item_rows(sg)), qtwo = two && !cols;
+      while (ok && (ok = wait_piece(seg))) {
+        const int nt = pieces[seg & 3].nt;
+        if (nt == 0) break;
+        const bool cols = as_columns(pieces[seg & 3].prefix), two = pieces[seg & 3].two, qtwo = two && !cols;
+        done_piece(seg);
         const int ahead = ahead_of(cols, two);
         const int buf = qtwo ? gq : qt;
         if (qtwo || qt == 0) ok = wait(&q_full[0], qn0);
         if (ok && (qtwo || qt == 1)) ok = wait(&q_full[1], qn1);
-        if (ok && !two && gq >= sg.nt) {  // no tile for this group
+        if (ok && !two && gq >= nt) {  // no tile for this group
           if (seg > 0) ok = wait(&o_free[gq], seg - 1);
           if (ok && elect_one()) mbar_arrive(&q_empty[buf]);
         }
         // (rows as columns: group 1 of a shared block has the 32 rows behind group 0's)
         const uint8_t* qs = sm + L::kQ + buf * L::kQBuf + (two && cols ? gq * NR * 128 : 0);
         int kjob = job;  // keys run ahead
-        for (int u = 0; ok && u < sg.nt + ahead; ++u) {
-          if (u < sg.nt) {
+        for (int u = 0; ok && u < nt + ahead; ++u) {
+          if (u < nt) {
             const int x = 2 * tiles + k_at(u, ahead), sk = x % NS;
             ok = wait(&full[sk], x / NS);
             if (!ok) break;
@@ -410,7 +442,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_commit(&empty[sk]);
                 // The last scores of the piece: the query tile is free after them.  (Where the other layout comes
                 // first, rows as columns free it after their last product: the hand-over below counts on it.)
-                if ((TP || !cols) && u + (two ? 1 : 2) >= sg.nt) {
+                if ((TP || !cols) && u + (two ? 1 : 2) >= nt) {
                   tc_commit(&q_empty[buf]);
                   if (qtwo) tc_commit(&q_empty[buf]);
                 }
@@ -420,7 +452,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           if (u >= ahead) {
-            const int t = u - ahead, x = 2 * tiles + v_at(t, ahead, sg.nt), sv = x % NS;
+            const int t = u - ahead, x = 2 * tiles + v_at(t, ahead, nt), sv = x % NS;
             ok = wait(&full[sv], x / NS);
             if (!ok) break;
             if (!two && (t & 1) != gq) {
@@ -449,14 +481,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 tc_commit(&pv_done[gq]);
                 tc_commit(&empty[sv]);
-                if (!TP && cols && t + (two ? 1 : 2) >= sg.nt) tc_commit(&q_empty[buf]);
+                if (!TP && cols && t + (two ? 1 : 2) >= nt) tc_commit(&q_empty[buf]);
               }
               __syncwarp();
               ++job;
             }
           }
         }
-        tiles += sg.nt;
+        tiles += nt;
         ++seg;
         if (qtwo || qt == 0) ++qn0;
         if (qtwo || qt == 1) ++qn1;
@@ -466,8 +498,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_wait(&drain[gq], 0, kTcWaitNs / 4);
       __syncwarp();
     } else {
-      // ---------------------------------------------------------- query rows
-      bool ok = true;
+      // ---------------------------------------------------------- pieces, query rows
+      bool ok = true, more = false;
+      SegmentWalk<KT> walk(g, pv);
+      Segment sg;
+      if (g.batch <= 32) {
+        // The plan and the first step of the walk run twice, the first time on whatever the lengths hold while
+        // the previous kernel ends: nothing can start before these few hundred instructions, and fetching them
+        // takes three to four times as long as running them once they are there.
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          if (pass) pdl_wait();
+          pv = plan_small<KT>(g, pass != 0);
+          walk.start();
+          more = walk.next(sg);
+        }
+      } else {
+        walk.start();
+        more = walk.next(sg);
+      }
       if (NR != 16 && !g.shared && lane == 0) {
         // the item that this CTA's run begins inside of, when it is the second to hold a piece of it
         int c0 = 0, nc = 0;
@@ -477,9 +526,59 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         rec[0] = make_int4(nc, sg.b, sg.rt, sg.hk);
         rec[1].x = c0;
       }
-      for (; ok && more; more = walk.next(sg)) {
-        const int rows = item_rows(sg);
-        const bool cols = as_columns(sg), two = !cols && rows > 128;
+      bool ended = false;
+      auto publish = [&](int s) {
+        if (ended) return true;
+        if (s >= 4 && stop(wait_phase(&pc_empty[s & 3], (uint32_t)((s >> 2) - 1) & 1u, abort_f, g.status))) return false;
+        Piece pc = {};
+        if (more) {
+          pc.nt = sg.nt;
+          pc.prefix = sg.prefix;
+          pc.whole = walk.whole(sg);
+          pc.b = sg.b;
+          pc.hk = sg.hk;
+          pc.rt = sg.rt;
+          pc.ordinal = sg.ordinal;
+          pc.n = paged_rows(g, sg.b);
+          pc.P = min(paged_len(g, sg.b), g.cap);
+          pc.x0 = sg.rt * (sg.prefix ? g.rp : g.ri);
+          pc.rows = sg.prefix ? min(g.rp, g.batch * g.n * g.G - pc.x0) : min(g.ri, pc.n * g.G - pc.x0);
+          pc.two = pc.rows > (as_columns(sg.prefix) ? NR : 128);
+          pc.s0 = sg.span.s0;
+          pc.sn = sg.span.s1 - sg.span.s0;
+          pc.w0 = sg.span.w0;
+          pc.t0 = sg.t0;
+          pc.key_lo = sg.prefix ? 0 : pv.sh_tiles * KT;
+          pc.key_end = sg.prefix ? pv.sh_tiles * KT : min(pc.P + pc.n, g.cap);
+          pc.all_lo = pc.key_lo;
+          pc.all_hi = pc.key_end;
+          if (!sg.prefix) {
+            int a, b, lo, hi;
+            row_span(g, pc.P, pc.n, div_g(g, pc.x0 + pc.rows - 1), a, lo, b);
+            row_span(g, pc.P, pc.n, div_g(g, pc.x0), a, b, hi);
+            pc.all_lo = max(lo, pc.key_lo);
+            pc.all_hi = min(hi, pc.key_end);
+          } else if (g.window > 0) {
+            pc.all_hi = 0;
+          }
+          if (pv.pre_tiles == 0) pc.nc = walk.pieces(sg, pc.c0);
+          pc.slot_row = sg.slot_row;
+        }
+        if (lane == 0) {
+          pieces[s & 3] = pc;
+          mbar_arrive(&pc_full[s & 3]);
+        }
+        __syncwarp();
+        ended = !more;
+        if (more) more = walk.next(sg);
+        return true;
+      };
+      ok = publish(0) && publish(1);
+      for (; ok; ++seg) {
+        const Piece& pc = pieces[seg & 3];
+        if (pc.nt == 0) break;
+        const int rows = pc.rows;
+        const bool cols = as_columns(pc.prefix), two = !cols && pc.two;
         for (int w = 0; ok && w < (two ? 2 : 1); ++w) {
           const int buf = two ? w : qt;
           int& used = buf ? qn1 : qn0;
@@ -488,10 +587,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           constexpr int kChunks = HD / 8, kLanes = 32 / kChunks;  // 16-byte chunks a row, rows an iteration
           const int c = lane % kChunks;
           int r = lane / kChunks;
-          const int x = sg.rt * (sg.prefix ? g.rp : g.ri) + w * 128 + r;
+          const int x = pc.x0 + w * 128 + r;
           const int row = div_g(g, x);
           int h = x - row * g.G;
-          const bf16* src = q + ((long long)(row + (sg.prefix ? 0 : sg.b * g.n)) * g.nq + sg.hk * g.G + h) * HD + c * 8;
+          const bf16* src = q + ((long long)(row + (pc.prefix ? 0 : pc.b * g.n)) * g.nq + pc.hk * g.G + h) * HD + c * 8;
           // the next row of this lane is kLanes stacked rows on
           const int dq = div_g(g, kLanes), dh = kLanes - dq * g.G;
           const long long step = ((long long)dq * g.nq + dh) * HD, wrap = (long long)(g.nq - g.G) * HD;
@@ -517,6 +616,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ++used;
         }
         if (!two) qt ^= 1;
+        if (ok) ok = publish(seg + 2);
       }
     }
   } else {
@@ -579,53 +679,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tmem_st_wait();
     };
     // After a partial result: the CTA that finishes the item's last piece joins them all.
-    auto join = [&](int rows) {
-      int c0;
-      const int nc = walk.pieces(sg, c0), t = sg.ordinal;
+    auto join = [&](const Piece& pc) {
       if (!meet(&fix[gq], fn)) return false;
       if (r == 0) {
         __threadfence();
-        const bool last = atomicAdd(g.tickets + t, 1) == nc - 1;
-        if (last) g.tickets[t] = 0;
+        const bool last = atomicAdd(g.tickets + pc.ordinal, 1) == pc.nc - 1;
+        if (last) g.tickets[pc.ordinal] = 0;
         *last_w = last;
       }
       if (!meet(&fix[gq], fn)) return false;
       if (*last_w) {
         __threadfence();
-        merge_item<bf16, HD>(g, sg.b, sg.rt, sg.hk, 0, rows, nc, c0, qr, 4, out);
+        merge_item<bf16, HD>(g, pc.b, pc.rt, pc.hk, 0, pc.rows, pc.nc, pc.c0, qr, 4, out);
       }
       return true;
     };
-    // The keys of the item that every row of it sees: [lo, hi).
-    auto seen_by_all = [&](int x0, int rows, int key_lo, int key_end, int& lo, int& hi) {
-      lo = 0;
-      hi = key_end;
-      if (!sg.prefix) {
-        int a, b, c;
-        const int P = paged_len(g, sg.b), n = paged_rows(g, sg.b);
-        row_span(g, P, n, div_g(g, x0 + rows - 1), a, lo, c);
-        row_span(g, P, n, div_g(g, x0), a, b, hi);
-        lo = max(lo, key_lo);
-        hi = min(hi, key_end);
-      } else if (g.window > 0) {
-        hi = 0;
-      }
-    };
+    pdl_wait();
+    ok = wait_piece(0);
     // Prefix items come before suffix items, so those in the rows-as-rows layout (if any) come first.
     if constexpr (!TS || !TP) {
-      while (ok && more && !as_columns(sg)) {
+      while (ok && pieces[seg & 3].nt > 0 && !as_columns(pieces[seg & 3].prefix)) {
         // ------------------------------------------------ rows as rows: thread = stacked row
-        const int rows = item_rows(sg);
-        const bool two = rows > 128;
+        const Piece& pc = pieces[seg & 3];
+        const int nt = pc.nt, rows = pc.rows, key_lo = pc.key_lo, key_end = pc.key_end;
+        const bool two = pc.two, whole = pc.whole;
         const int step = two ? 1 : 2, t0 = two ? 0 : gq;
-        const bool has = t0 < sg.nt, both = !two && sg.nt > 1, whole = walk.whole(sg);
-        const int x0 = sg.rt * (sg.prefix ? g.rp : g.ri);  // the item's first stacked row
-        const int key_lo = sg.prefix ? 0 : pv.sh_tiles * KT;
-        const int key_end = sg.prefix ? pv.sh_tiles * KT : key_limit(g, sg.b);
-        int all_lo, all_hi;
-        seen_by_all(x0, rows, key_lo, key_end, all_lo, all_hi);
+        const bool has = t0 < nt, both = !two && nt > 1;
         const int rr = r + (two ? gq * 128 : 0);  // of the item
-        const ItemRow me = item_row(g, sg, rr);
+        const ItemRow me = item_row(g, pc.prefix, pc.b, pc.hk, pc.x0, rr);
         const bool warp_live = (rr - lane) < rows;  // some row of the warp belongs to the item
         int sink = 0, lo = 0, hi = 0;
         if (me.live) row_span(g, paged_len(g, me.b), paged_rows(g, me.b), me.i, sink, lo, hi);
@@ -633,9 +714,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         hi = min(hi, key_end);
         sink = min(sink, key_end);
         float M = -INFINITY, Ls = 0.f;
-        for (int t = t0; ok && t < sg.nt; t += step) {
-          const int k0 = sg.span.tile(sg.t0 + t) * KT;
-          const bool inner = k0 >= all_lo && k0 + KT <= all_hi;  // the same for all warps of the item
+        for (int t = t0; ok && t < nt; t += step) {
+          const int k0 = pc.tile(t) * KT;
+          const bool inner = k0 >= pc.all_lo && k0 + KT <= pc.all_hi;  // the same for all warps of the item
           if (stop(wait_phase(&s_full[2 * gq], sn0 & 1u, abort_f, g.status))) {
             ok = false;
             break;
@@ -809,7 +890,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float inv = whole ? 1.f / Lt : 1.f;
           if (warp_live) {
             bf16* dst = out + (((long long)me.b * g.n + me.i) * g.nq + me.head) * HD;
-            float* pdst = g.part_o + (sg.slot_row + rr) * HD;
+            float* pdst = g.part_o + (pc.slot_row + rr) * HD;
 #pragma unroll 1
             for (int c = 0; c < HD; c += 32) {
               uint32_t a[32], b[32];
@@ -838,7 +919,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
               }
             }
-            if (me.live && !whole) g.part_ml[sg.slot_row + rr] = make_float2(both ? Mx : M, both ? Lt : Ls);
+            if (me.live && !whole) g.part_ml[pc.slot_row + rr] = make_float2(both ? Mx : M, both ? Lt : Ls);
           }
           tc_fence_before();
           __syncwarp();
@@ -851,24 +932,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (two || qt == 0) ++qn0;
         if (two || qt == 1) ++qn1;
         if (!two) qt ^= 1;
-        tiles += sg.nt;
+        tiles += nt;
+        done_piece(seg);
         ++seg;
-        more = walk.next(sg);
+        ok = wait_piece(seg);
       }
     }
     if constexpr (NR > 0) {
-      while (ok && more) {
+      while (ok && pieces[seg & 3].nt > 0) {
         // ------------------------------------------------ rows as columns: thread = key r of the tile
-        const int all_rows = item_rows(sg);
-        const bool two = both_on(true, all_rows);
-        const int rbase = two ? gq * NR : 0, rows = two ? min(NR, all_rows - rbase) : all_rows;  // the group's rows
+        const Piece& pc = pieces[seg & 3];
+        const int nt = pc.nt;
+        const bool two = pc.two, whole = pc.whole;
+        const int rbase = two ? gq * NR : 0, rows = two ? min(NR, pc.rows - rbase) : pc.rows;  // the group's rows
         const int t0 = two ? 0 : gq, step = two ? 1 : 2, ahead = ahead_of(true, two);
-        const bool has = t0 < sg.nt, both = !two && sg.nt > 1, whole = walk.whole(sg);
-        const int xi = sg.rt * (sg.prefix ? g.rp : g.ri), x0 = xi + rbase;  // the item's and the group's first row
-        const int key_lo = sg.prefix ? 0 : pv.sh_tiles * KT;
-        const int key_end = sg.prefix ? pv.sh_tiles * KT : key_limit(g, sg.b);
-        int all_lo, all_hi;
-        seen_by_all(xi, all_rows, key_lo, key_end, all_lo, all_hi);
+        const bool has = t0 < nt, both = !two && nt > 1;
+        const int x0 = pc.x0 + rbase;  // the group's first row
         float* ref = reinterpret_cast<float*>(sm + L::kRef) + gq * 32;
         uint8_t* pbuf = sm + L::kQ + gq * L::kQBuf + L::kP;
         float* scr = reinterpret_cast<float*>(pbuf);  // scratch wherever no product reads P
@@ -886,10 +965,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int c = 0; c < NR; ++c) Ls[c] = 0.f;
         if (!meet(&fix[gq], fn)) break;  // the scratch's last readers are past it
-        for (int t = t0; ok && t < sg.nt; t += step) {
+        for (int t = t0; ok && t < nt; t += step) {
           const bool first = t == t0;
-          const int k0 = sg.span.tile(sg.t0 + t) * KT, key = k0 + r;
-          const bool inner = k0 >= all_lo && k0 + KT <= all_hi;
+          const int k0 = pc.tile(t) * KT, key = k0 + r;
+          const bool inner = k0 >= pc.all_lo && k0 + KT <= pc.all_hi;
           const int sb = job & 1;  // score buffer
           uint32_t& sn = sb ? sn1 : sn0;
           if (stop(wait_phase(&s_full[2 * gq + sb], sn & 1u, abort_f, g.status))) {
@@ -933,18 +1012,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           };
           if (!inner) {
             uint32_t see = 0u;
-            if (key >= key_lo && key < key_end) {
-              if (sg.prefix) {  // (a window over a prefix: the rows' sequences differ)
+            if (key >= pc.key_lo && key < pc.key_end) {
+              if (pc.prefix) {  // (a window over a prefix: the rows' sequences differ)
 #pragma unroll 1
                 for (int c = 0; c < rows; ++c) {
-                  const ItemRow w = item_row(g, sg, rbase + c);
+                  const ItemRow w = item_row(g, true, 0, pc.hk, pc.x0, rbase + c);
                   int sink, lo, hi;
                   row_span(g, paged_len(g, w.b), paged_rows(g, w.b), w.i, sink, lo, hi);
                   if (key < sink || (key >= lo && key < hi)) see |= 1u << c;
                 }
               } else {
                 // block row i sees the key from i = key - P on, until the window has moved past it
-                const int d = key - min(paged_len(g, sg.b), g.cap);
+                const int d = key - pc.P;
                 const bool out_of = g.window > 0 && key >= g.sinks;
                 if (g.causal) {
                   const long long from = (long long)max(d, 0) * g.G - x0;
@@ -1048,7 +1127,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           uint32_t first_acc = 0u;
           if (!inner) {
-            uint8_t* vt = sm + (2 * tiles + v_at(t, ahead, sg.nt)) % NS * L::kTile;
+            uint8_t* vt = sm + (2 * tiles + v_at(t, ahead, nt)) % NS * L::kTile;
             // (the last product's values had landed: this wait cannot take their phase for its own)
             if (!wait_pv()) break;
             ok = !stop(wait_phase(&v_ready[gq], (uint32_t)job & 1u, abort_f, g.status));
@@ -1160,7 +1239,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (two || gq == 0) {
           float2* coef = reinterpret_cast<float2*>(scr + 8 * NR);
-          const long long prow = sg.slot_row + rbase;
+          const long long prow = pc.slot_row + rbase;
           if (r < NR) {
             const float Mx = fmaxf(M, other.x), ref0 = Mx == -INFINITY ? 0.f : Mx;
             const float wa = M == -INFINITY ? (both ? 0.f : 1.f) : ex2f(M - ref0);
@@ -1175,7 +1254,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (qr * 32 < HD) {  // this lane's dimension is r
             const int f = div_g(g, x0);  // block row (of the sequence or of the batch)
             int h = x0 - f * g.G;
-            bf16* dst = out + ((long long)((sg.prefix ? 0 : sg.b * g.n) + f) * g.nq + sg.hk * g.G + h) * HD + r;
+            bf16* dst = out + ((long long)((pc.prefix ? 0 : pc.b * g.n) + f) * g.nq + pc.hk * g.G + h) * HD + r;
             float* pdst = g.part_o + prow * HD + r;
             const long long skip = (long long)(g.nq - g.G) * HD;  // to the next block row's heads
 #pragma unroll 1
@@ -1217,16 +1296,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_arrive(&o_free[gq]);
             if (!two) mbar_arrive(&o_free[1]);
           }
-          if (NR == 16 && !whole && pv.pre_tiles == 0 && !join(rows)) break;  // (few rows; else a kernel does)
+          if (NR == 16 && !whole && pc.nc > 0 && !join(pc)) break;  // (few rows; else a kernel does)
         }
         if (qt == 0)
           ++qn0;
         else
           ++qn1;
         qt ^= 1;
-        tiles += sg.nt;
+        tiles += nt;
+        done_piece(seg);
         ++seg;
-        more = walk.next(sg);
+        ok = wait_piece(seg);
       }
     }
   }
