@@ -365,38 +365,41 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   for (int y = 0; y < rt; ++y) at += span_of<KT>(g, P, rows, y, sh).count() * g.nkv;
   const int cnt = span_of<KT>(g, P, rows, rt, sh).count();
   at += hk * cnt;
-  const int c0 = at / quota, ns = cnt > 0 ? (at + cnt - 1) / quota - c0 + 1 : 0;
+  int c0 = 0, p0 = 0;
+  const int ns = cnt > 0 ? pieces_of(at, cnt, quota, c0) : 0;
   if (ns <= 1 && pre == 0) return;
   const long long srow = ((long long)(b * g.nrt + rt) * g.nkv + hk + c0) * g.slot_s + x - rt * g.ri;
   const int xp = r * g.G + h - hk * g.G, rp = xp / g.rp, k = hk * g.nrp + rp;
-  const int p0 = k * pre / quota, np = pre > 0 ? ((k + 1) * pre - 1) / quota - p0 + 1 : 0;
+  const int np = pre > 0 ? pieces_of(k * pre, pre, quota, p0) : 0;
   const long long prow = g.pre_row0 + (long long)(k + p0) * g.slot_p + xp - rp * g.rp;
   merge_row<T, HD>(g, np + ns, [&](int c) {
     return c < np ? prow + (long long)c * g.slot_p : srow + (long long)(c - np) * g.slot_s;
   }, out + ((long long)r * g.nq + h) * HD);
 }
 
-// Calls without one: block (c, y) joins rows 32 y .. 32 y + 31 of the item that CTA c recorded, if it did.
+// Calls without one: block (c, y) joins `per` rows from per y on of the item that CTA c recorded, if it did.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kMergeWarps * 32)
-    paged_join_kernel(const __grid_constant__ PagedGeom g, T* __restrict__ out) {
+    paged_join_kernel(const __grid_constant__ PagedGeom g, int per, T* __restrict__ out) {
   pdl_launch();
   pdl_wait();
   const int4* rec = reinterpret_cast<const int4*>(g.records) + 2 * blockIdx.x;
   const int4 a = rec[0];
   const int c0 = rec[1].x;
   if (a.x <= 0) return;
-  const int rows = min(g.ri, paged_rows(g, a.y) * g.G - a.z * g.ri), r0 = 32 * blockIdx.y;
+  const int rows = min(g.ri, paged_rows(g, a.y) * g.G - a.z * g.ri), r0 = per * blockIdx.y;
   if (r0 < rows)
-    merge_item<T, HD>(g, a.y, a.z, a.w, r0, min(32, rows - r0), a.x, c0, threadIdx.x >> 5, kMergeWarps, out);
+    merge_item<T, HD>(g, a.y, a.z, a.w, r0, min(per, rows - r0), a.x, c0, threadIdx.x >> 5, kMergeWarps, out);
 }
 
 cudaError_t paged_join_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t s) {
-  const dim3 grid(g.grid, (g.slot_s + 31) / 32);
+  // at most 8 blocks an SM: more would run in waves, and most find nothing to do
+  const int per = std::max(kMergeWarps, (g.slot_s + 7) / 8);
+  const dim3 grid(g.grid, (g.slot_s + per - 1) / per);
   if (hd == 64)
-    DFL_RET(launch_pdl(paged_join_kernel<bf16, 64>, grid, dim3(kMergeWarps * 32), 0, s, g, (bf16*)out));
+    DFL_RET(launch_pdl(paged_join_kernel<bf16, 64>, grid, dim3(kMergeWarps * 32), 0, s, g, per, (bf16*)out));
   else
-    DFL_RET(launch_pdl(paged_join_kernel<bf16, 128>, grid, dim3(kMergeWarps * 32), 0, s, g, (bf16*)out));
+    DFL_RET(launch_pdl(paged_join_kernel<bf16, 128>, grid, dim3(kMergeWarps * 32), 0, s, g, per, (bf16*)out));
   count_launch();
   return cudaSuccess;
 }

@@ -9,8 +9,8 @@
 // common keys [0, sh) are then read once for all of them.  An item's keys are
 // walked in tiles of KT keys at absolute multiples of KT, only those that some
 // row of it sees (first tokens that stay visible, then the window).  All tiles
-// of all items, in item order, form one line of T tiles that is cut into equal
-// runs of `quota` tiles, a run to a CTA, so every CTA has the same work
+// of all items, in item order, form one line of T tiles that is cut into
+// runs of about `quota` tiles, a run to a CTA, so every CTA has the same work
 // whatever the lengths; a CTA's run covers the end of one item, whole items,
 // and the start of another.  An item inside one run whose rows have no other
 // part is finished there; every other piece leaves a partial result (row
@@ -141,6 +141,27 @@ struct Segment {
   int ordinal;        // among the prefix or the suffix items
   long long slot_row; // first partial row of this piece
 };
+
+// Cuts of the line.  Cut k lies at k quota, but one that would leave `snap` tiles or fewer of an item on one
+// side moves to that item's edge: a piece costs about three tiles besides its own (start, partial result,
+// joining), so short ones do not pay.  Items of several runs are cut everywhere but within a quarter of a run.
+__device__ __forceinline__ int snap_of(int total, int quota) {
+  return total <= 2 * quota ? min(3, total / 2) : min(3, quota / 4);
+}
+// Where the cut at `pos` inside the item [line, line + total) comes to lie.
+__device__ __forceinline__ int cut_at(int pos, int line, int total, int quota) {
+  const int snap = snap_of(total, quota);
+  return pos - line <= snap ? line : line + total - pos <= snap ? line + total : pos;
+}
+// The pieces of an item: from CTA `c0` on, one a CTA.
+__device__ __forceinline__ int pieces_of(int line, int total, int quota, int& c0) {
+  const int snap = snap_of(total, quota);
+  // the first and the last cut inside the item
+  const int k0 = (int)((unsigned)(line + snap) / (unsigned)quota) + 1;
+  const int k1 = (int)((unsigned)(max(line + total - snap, 1) - 1) / (unsigned)quota);
+  c0 = k0 - 1;
+  return max(k1 - k0 + 2, 1);
+}
 
 // The line as one CTA sees it.
 struct PlanView {
@@ -303,6 +324,7 @@ struct SegmentWalk {
   int b, rt, hk;      // the next suffix item
   int item_at;        // its line position
   int pre_total;
+  bool at_start;      // the first cut has not been placed yet
   __device__ __forceinline__ SegmentWalk(const PagedGeom& g_, const PlanView& v_) : g(g_), v(v_) {}
   __device__ __forceinline__ void start() {
     pos = (int)min((long long)blockIdx.x * v.quota, (long long)v.T);
@@ -311,10 +333,10 @@ struct SegmentWalk {
     b = v.b;
     item_at = v.cum;
     rt = hk = 0;
+    at_start = true;
   }
-  __device__ __forceinline__ bool next(Segment& s) {
-    if (pos >= end) return false;
-    int ordinal;
+  // The item at `pos` (which lies in it, or where it begins).
+  __device__ __forceinline__ bool item(Segment& s) {
     if (pos < pre_total) {
       const int k = pos / v.pre_tiles;
       s.prefix = true;
@@ -323,9 +345,8 @@ struct SegmentWalk {
       s.b = v.pre_b;
       s.span = prefix_span<KT>(g, v.sh_tiles, v.min_len);
       s.total = v.pre_tiles;
-      s.t0 = pos - k * v.pre_tiles;
       s.line = k * v.pre_tiles;
-      ordinal = k;
+      s.ordinal = k;
     } else {
       TileSpan sp;
       int c;
@@ -348,20 +369,31 @@ struct SegmentWalk {
       s.span = sp;
       s.total = c;
       s.line = item_at + hk * c;
-      s.t0 = pos - s.line;
-      ordinal = (b * g.nrt + rt) * g.nkv + hk;
+      s.ordinal = (b * g.nrt + rt) * g.nkv + hk;
     }
-    s.nt = min(s.total - s.t0, end - pos);
-    pos += s.nt;
-    s.ordinal = ordinal;
-    const long long slot = (long long)ordinal + blockIdx.x;
-    s.slot_row = s.prefix ? g.pre_row0 + slot * g.slot_p : slot * g.slot_s;
     return true;
   }
-  // The pieces of the item: from CTA `c0` on, one a CTA.
+  __device__ __forceinline__ bool next(Segment& s) {
+    while (pos < end) {
+      if (!item(s)) return false;
+      if (at_start) {  // the run's first cut
+        at_start = false;
+        pos = cut_at(pos, s.line, s.total, v.quota);
+        if (pos == s.line + s.total) continue;
+      }
+      const int stop = end < s.line + s.total ? cut_at(end, s.line, s.total, v.quota) : s.line + s.total;
+      if (stop <= pos) return false;  // (the last cut lies where this item begins)
+      s.t0 = pos - s.line;
+      s.nt = stop - pos;
+      pos = stop;
+      const long long slot = (long long)s.ordinal + blockIdx.x;
+      s.slot_row = s.prefix ? g.pre_row0 + slot * g.slot_p : slot * g.slot_s;
+      return true;
+    }
+    return false;
+  }
   __device__ __forceinline__ int pieces(const Segment& s, int& c0) const {
-    c0 = (int)((unsigned)s.line / (unsigned)v.quota);
-    return (int)((unsigned)(s.line + s.total - 1) / (unsigned)v.quota) - c0 + 1;
+    return pieces_of(s.line, s.total, v.quota, c0);
   }
   // No other piece contributes to this one's rows.
   __device__ __forceinline__ bool whole(const Segment& s) const {

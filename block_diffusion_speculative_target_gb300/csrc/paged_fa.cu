@@ -71,8 +71,8 @@ struct TcLayout {
   static constexpr uint32_t kQBuf = 32768;
   static constexpr uint32_t kP = 16384;                 // P within a buffer
   static constexpr uint32_t kXch = kQ + 2 * kQBuf;      // [128] (M, L) of group 1
-  static constexpr uint32_t kRef = kXch + 1024;         // [2][32] row references of the rows-as-columns layout
-  static constexpr uint32_t kBar = kRef + 256;
+  static constexpr uint32_t kRef = kXch + 1024;         // [2][64] row references of the rows-as-columns layout
+  static constexpr uint32_t kBar = kRef + 512;
   static constexpr int kBars = 2 * kSlots + 31;
   static constexpr uint32_t kMisc = kBar + kBars * 8;   // TMEM slot, abort flag, per-group words, scan scratch
   static constexpr uint32_t kPieces = kMisc + 256;      // [4] pieces
@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (more) more = walk.next(sg);
         return true;
       };
-      ok = publish(0) && publish(1);
+      int next = 1;  // pieces published: two ahead of the one whose rows are brought
+      ok = publish(0);
       for (; ok; ++seg) {
         const Piece& pc = pieces[seg & 3];
         if (pc.nt == 0) break;
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (!ok) break;
           constexpr int kChunks = HD / 8, kLanes = 32 / kChunks;  // 16-byte chunks a row, rows an iteration
           const int c = lane % kChunks;
-          int r = lane / kChunks;
+          const int r = lane / kChunks;
           const int x = pc.x0 + w * 128 + r;
           const int row = div_g(g, x);
           int h = x - row * g.G;
@@ -594,21 +595,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // the next row of this lane is kLanes stacked rows on
           const int dq = div_g(g, kLanes), dh = kLanes - dq * g.G;
           const long long step = ((long long)dq * g.nq + dh) * HD, wrap = (long long)(g.nq - g.G) * HD;
-          uint8_t* dst = sm + L::kQ + buf * L::kQBuf + (c >> 3) * (cols ? 8192 : 16384);
-#pragma unroll 4
-          for (const int lim = min(128, rows - w * 128); r < lim; r += kLanes) {
-            cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src);
-            src += step;
-            h += dh;
-            if (h >= g.G) {
-              h -= g.G;
-              src += wrap;
-            }
+          // four steps at a time: their swizzled places repeat every 8 rows
+          uint8_t* dst = sm + L::kQ + buf * L::kQBuf + (c >> 3) * (cols ? 8192 : 16384) + r * 128;
+          uint32_t at[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) at[k] = k * kLanes * 128 + (((c & 7) ^ ((r + k * kLanes) & 7)) << 4);
+          const int lim = min(128, rows - w * 128) - r;
+#pragma unroll 1
+          for (int x4 = 0; x4 < lim; x4 += 4 * kLanes) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (x4 + k * kLanes < lim) {
+                cp_async16(dst + at[k], src);
+                src += step;
+                h += dh;
+                if (h >= g.G) {
+                  h -= g.G;
+                  src += wrap;
+                }
+              }
+            dst += 4 * kLanes * 128;
           }
           // (rows past the item's: scores of 0, which nothing reads)
-          if (cols)
-            for (; r < (rows > NR ? 2 * NR : NR); r += kLanes)
-              *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          if (cols) {
+            dst = sm + L::kQ + buf * L::kQBuf + (c >> 3) * 8192;
+            for (int y = rows / kLanes * kLanes + r; y < NR; y += kLanes)
+              if (y >= rows) *reinterpret_cast<uint4*>(dst + y * 128 + (((c & 7) ^ (y & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          }
           cp_async_wait_all();
           fence_proxy_async_smem();
           __syncwarp();
@@ -616,7 +629,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ++used;
         }
         if (!two) qt ^= 1;
-        if (ok) ok = publish(seg + 2);
+        for (; ok && next <= seg + 2; ++next) ok = publish(next);
       }
     }
   } else {
@@ -948,7 +961,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int t0 = two ? 0 : gq, step = two ? 1 : 2, ahead = ahead_of(true, two);
         const bool has = t0 < nt, both = !two && nt > 1;
         const int x0 = pc.x0 + rbase;  // the group's first row
-        float* ref = reinterpret_cast<float*>(sm + L::kRef) + gq * 32;
+        float* ref = reinterpret_cast<float*>(sm + L::kRef) + gq * 64;
         uint8_t* pbuf = sm + L::kQ + gq * L::kQBuf + L::kP;
         float* scr = reinterpret_cast<float*>(pbuf);  // scratch wherever no product reads P
         auto to_scratch = [&](float (&x)[NR]) {  // a warp's results of warp_scatter, by row
@@ -961,7 +974,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         };
         constexpr bool kPair = NR == 16;
-        float Ls[NR], nm[NR];  // row sums of this thread's keys; -M
+        constexpr bool kRegRef = NR <= 32;      // (registers for the references too)
+        float Ls[NR], nm[kRegRef ? NR : 2];     // row sums of this thread's keys; -M
 #pragma unroll
         for (int c = 0; c < NR; ++c) Ls[c] = 0.f;
         if (!meet(&fix[gq], fn)) break;  // the scratch's last readers are past it
@@ -992,7 +1006,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           tc_fence_after();
           float v[NR];      // scores, then exponents s - M
-          uint32_t hid = 0; // rows that do not see the key
+          uint64_t hid = 0; // rows that do not see the key
           auto load_scores = [&]() {
 #pragma unroll
             for (int c = 0; c < NR; c += 16) tmem_ld16u(tS + sb * 64 + c, *reinterpret_cast<uint32_t(*)[16]>(&v[c]));
@@ -1005,13 +1019,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           };
           auto exponents = [&]() {
 #pragma unroll
-            for (int c = 0; c < NR; c += 2) {
-              const float2 x = fma2(make_float2(v[c], v[c + 1]), make_float2(sl, sl), make_float2(nm[c], nm[c + 1]));
-              v[c] = x.x, v[c + 1] = x.y;
+            for (int c = 0; c < NR; c += 4) {
+              float4 m;
+              if constexpr (kRegRef)
+                m = make_float4(nm[c], nm[c + 1], nm[c + 2], nm[c + 3]);
+              else
+                m = *reinterpret_cast<const float4*>(ref + c);
+              const float2 x = fma2(make_float2(v[c], v[c + 1]), make_float2(sl, sl), make_float2(m.x, m.y));
+              const float2 y = fma2(make_float2(v[c + 2], v[c + 3]), make_float2(sl, sl), make_float2(m.z, m.w));
+              v[c] = x.x, v[c + 1] = x.y, v[c + 2] = y.x, v[c + 3] = y.y;
             }
           };
           if (!inner) {
-            uint32_t see = 0u;
+            uint64_t see = 0u;
             if (key >= pc.key_lo && key < pc.key_end) {
               if (pc.prefix) {  // (a window over a prefix: the rows' sequences differ)
 #pragma unroll 1
@@ -1019,7 +1039,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   const ItemRow w = item_row(g, true, 0, pc.hk, pc.x0, rbase + c);
                   int sink, lo, hi;
                   row_span(g, paged_len(g, w.b), paged_rows(g, w.b), w.i, sink, lo, hi);
-                  if (key < sink || (key >= lo && key < hi)) see |= 1u << c;
+                  if (key < sink || (key >= lo && key < hi)) see |= 1ull << c;
                 }
               } else {
                 // block row i sees the key from i = key - P on, until the window has moved past it
@@ -1027,25 +1047,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool out_of = g.window > 0 && key >= g.sinks;
                 if (g.causal) {
                   const long long from = (long long)max(d, 0) * g.G - x0;
-                  const long long to = out_of ? ((long long)d + g.window) * g.G - x0 : NR;
-                  see = bits_of((int)min(from, 32ll), (int)max(min(to, 32ll), 0ll));
+                  const long long to = out_of ? ((long long)d + g.window) * g.G - x0 : 64;
+                  const int a = (int)min(from, 64ll), b = (int)max(min(to, 64ll), 0ll);
+                  see = bits_of(a, b) | (uint64_t)bits_of(a - 32, b - 32) << 32;
                 } else if (!out_of || d >= -g.window) {
-                  see = 0xffffffffu;
+                  see = ~0ull;
                 }
               }
             }
             hid = ~see;
           }
           load_scores();
-          // Whether a reference has to move is the group's vote.  Its answer is nearly always no, so the
-          // weights are computed while the votes come in.
+          // Whether a reference has to move is the group's vote.  Its answer is nearly always no, so with up to
+          // 32 rows the weights are computed while the votes come in (with 64 their sums would need registers
+          // that are not there).
           volatile uint32_t* votes = vote_w + (sb * 2 + gq) * 4;  // (two sets: a warp may be a tile ahead)
           uint32_t hi[NR / 2], lo[kPair ? NR / 2 : 1];
+          auto add_sum = [&](int c) {
+            const float2 l = add2(make_float2(Ls[c], Ls[c + 1]), make_float2(v[c], v[c + 1]));
+            Ls[c] = l.x;
+            Ls[c + 1] = l.y;
+          };
           auto weights = [&]() {
 #pragma unroll
             for (int c = 0; c < NR; c += 2) {
               v[c] = ex2f(v[c]);
               v[c + 1] = ex2f(v[c + 1]);
+              if constexpr (!kRegRef) add_sum(c);
               if constexpr (kPair) {
                 pack_bf16_hilo(v[c], v[c + 1], hi[c / 2], lo[c / 2]);
               } else {
@@ -1068,7 +1096,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               votes[qr] = over;
               mbar_arrive(&fix[gq]);
             }
-            weights();
+            if constexpr (kRegRef) weights();
             ok = !stop(wait_phase(&fix[gq], (uint32_t)fn & 1u, abort_f, g.status));
             ++fn;
             if (!ok) break;
@@ -1116,14 +1144,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               ok = meet(&fix[gq], fn);  // P overwrites the factors
               if (!ok) break;
             }
+            if constexpr (kRegRef) {
 #pragma unroll
-            for (int c = 0; c < NR; c += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(ref + c);
-              nm[c] = m.x, nm[c + 1] = m.y, nm[c + 2] = m.z, nm[c + 3] = m.w;
+              for (int c = 0; c < NR; c += 4) {
+                const float4 m = *reinterpret_cast<const float4*>(ref + c);
+                nm[c] = m.x, nm[c + 1] = m.y, nm[c + 2] = m.z, nm[c + 3] = m.w;
+              }
             }
             load_scores();
             exponents();
-            weights();
+            if constexpr (kRegRef) weights();
           }
           uint32_t first_acc = 0u;
           if (!inner) {
@@ -1152,7 +1182,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!((w >> (k & 31)) & 1u)) continue;
                 if (k == r) {
 #pragma unroll
-                  for (int c = 0; c < NR; ++c) scr[c] = (hid >> c) & 1 ? -1.f : v[c];
+                  for (int c = 0; c < NR; ++c) scr[c] = (hid >> c) & 1 ? -1.f : kRegRef ? v[c] : ex2f(v[c]);
                 }
                 ok = meet(&fix[gq], fn);
                 if (!ok) break;
@@ -1183,11 +1213,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           // this key's row of P: a bf16 a row of the item (pairs: the low parts behind the high ones)
+          if constexpr (kRegRef) {
 #pragma unroll
-          for (int c = 0; c < NR; c += 2) {
-            const float2 l = add2(make_float2(Ls[c], Ls[c + 1]), make_float2(v[c], v[c + 1]));
-            Ls[c] = l.x;
-            Ls[c + 1] = l.y;
+            for (int c = 0; c < NR; c += 2) add_sum(c);
+          } else {
+            weights();
           }
           if (!wait_pv()) break;
           {
@@ -1345,8 +1375,12 @@ static cudaError_t tc_pick(const PagedGeom& g, const CUtensorMap& tk, const CUte
   const int ns = g.n * g.G, np = g.shared ? g.batch * ns : ns;  // stacked rows of a sequence, of a shared prefix
 #define DFL_TC(NR, TS, TP) return tc_launch<HD, NR, TS, TP>(g, tk, tv, pool_rows, q, out, part_rows, s)
   if (ns > 64) DFL_TC(0, false, false);
+  if (ns > 32) {
+    if (np > 64) DFL_TC(64, true, false);
+    DFL_TC(64, true, true);
+  }
   if (ns > 16) {
-    if (np > 64) DFL_TC(32, true, false);
+    if (np > 32) DFL_TC(32, true, false);
     DFL_TC(32, true, true);
   }
   if (np > 16) DFL_TC(16, true, false);
