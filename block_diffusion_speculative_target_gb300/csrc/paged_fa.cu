@@ -22,7 +22,8 @@
 //   Items of more than NR rows give each group half of them and every key tile;
 //   others are one block of rows whose key tiles the groups take in turn.
 // rows as rows (more rows: chunks, shared prefixes)
-//   S = Q K_t^T            128 rows by 128 keys: a thread holds one row
+//   S = Q K_t^T            128 rows by 64 keys (half a tile), two buffers: a thread
+//                          holds one row
 //   O += P V_t             P as bf16 over S in TMEM
 //   An item of at most 128 rows has one query tile, whose key tiles the groups
 //   take in turn; one of more rows has two, a group each, that share every key
@@ -73,7 +74,7 @@ struct TcLayout {
   static constexpr uint32_t kXch = kQ + 2 * kQBuf;      // [128] (M, L) of group 1
   static constexpr uint32_t kRef = kXch + 1024;         // [2][64] row references of the rows-as-columns layout
   static constexpr uint32_t kBar = kRef + 512;
-  static constexpr int kBars = 2 * kSlots + 31;
+  static constexpr int kBars = 2 * kSlots + 35;
   static constexpr uint32_t kMisc = kBar + kBars * 8;   // TMEM slot, abort flag, per-group words, scan scratch
   static constexpr uint32_t kPieces = kMisc + 256;      // [4] pieces
   static constexpr int kUsed = kPieces + 4 * 96;
@@ -229,16 +230,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* q_full = bar + 2 * NS;   // [2]
   uint64_t* q_empty = q_full + 2;    // [2] two arrivals
   uint64_t* s_full = q_full + 4;     // [2][2] scores of the group's tile in TMEM (rows as rows: one buffer)
-  uint64_t* p_full = q_full + 8;     // [2] its weights (four warps)
-  uint64_t* pv_done = q_full + 10;   // [2] its product with the values is done
-  uint64_t* o_free = q_full + 12;    // [2] the accumulator has been read (four warps)
-  uint64_t* fix = q_full + 14;       // [3] meetings of group 0, group 1 (four warps), both (eight)
-  uint64_t* x_full = q_full + 17;    // group 1's M and L are written (four warps)
-  uint64_t* x_free = q_full + 18;    // and read
-  uint64_t* drain = q_full + 19;     // [2] every product a warp issued is done
-  uint64_t* v_ready = q_full + 21;   // [2] the values of the group's tile have landed
-  uint64_t* pc_full = q_full + 23;   // [4] a piece is described
-  uint64_t* pc_empty = q_full + 27;  // [4] and no role needs its description (11 warps)
+  uint64_t* p_full = q_full + 8;     // [2][2] the buffer's weights (four warps; one may be a job ahead of another)
+  uint64_t* pv_done = q_full + 12;   // [2][2] the product of weights and values of the buffer's job is done
+  uint64_t* o_free = q_full + 16;    // [2] the accumulator has been read (four warps)
+  uint64_t* fix = q_full + 18;       // [3] meetings of group 0, group 1 (four warps), both (eight)
+  uint64_t* x_full = q_full + 21;    // group 1's M and L are written (four warps)
+  uint64_t* x_free = q_full + 22;    // and read
+  uint64_t* drain = q_full + 23;     // [2] every product a warp issued is done
+  uint64_t* v_ready = q_full + 25;   // [2] the values of the group's tile have landed
+  uint64_t* pc_full = q_full + 27;   // [4] a piece is described
+  uint64_t* pc_empty = q_full + 31;  // [4] and no role needs its description (11 warps)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   uint32_t* tslot = misc;
   volatile int* abort_f = reinterpret_cast<volatile int*>(misc + 1);
@@ -263,8 +264,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&q_empty[i], 2);
       mbar_init(&s_full[2 * i], 1);
       mbar_init(&s_full[2 * i + 1], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&pv_done[i], 1);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&pv_done[2 * i], 1);
+      mbar_init(&pv_done[2 * i + 1], 1);
       mbar_init(&o_free[i], 4);
       mbar_init(&fix[i], 4);
       mbar_init(&drain[i], 1);
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
 
   if (warp < 4) {
-    reg_dec<72>();
+    reg_dec<88>();
     if (warp == 0) {
       // ---------------------------------------------------------- pages
       const int per = KT >> g.ps_log2;  // pages a tile
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp < 3) {
       // ---------------------------------------------------------- products of group gq
       const int gq = warp - 1;
-      const uint32_t idS = idesc_bf16_f32(128, 128), idO = idesc_bf16_f32(128, HD) | (1u << 16);  // values MN-major
+      const uint32_t idS = idesc_bf16_f32(128, 64), idO = idesc_bf16_f32(128, HD) | (1u << 16);  // values MN-major
       const uint32_t idSt = idesc_bf16_f32(128, NR > 0 ? NR : 16);
       const uint32_t idOt = idesc_bf16_f32(128, 64) | (3u << 15);  // values and weights both MN-major
       const uint32_t tS = tmem + gq * 128, tO = tmem + 256 + gq * 128;
@@ -407,84 +410,149 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         // (rows as columns: group 1 of a shared block has the 32 rows behind group 0's)
         const uint8_t* qs = sm + L::kQ + buf * L::kQBuf + (two && cols ? gq * NR * 128 : 0);
-        int kjob = job;  // keys run ahead
-        for (int u = 0; ok && u < nt + ahead; ++u) {
-          if (u < nt) {
-            const int x = 2 * tiles + k_at(u, ahead), sk = x % NS;
-            ok = wait(&full[sk], x / NS);
-            if (!ok) break;
-            if (!two && (u & 1) != gq) {  // the other group's tile
-              if (elect_one()) mbar_arrive(&empty[sk]);
-            } else {
-              // rows as rows: P of the last tile lies over S until its product is done
-              if ((!cols || (!TP && kjob == job)) && kjob > 0) ok = wait(&pv_done[gq], kjob - 1);
+        if (cols) {
+          int kjob = job;  // keys run ahead
+          for (int u = 0; ok && u < nt + ahead; ++u) {
+            if (u < nt) {
+              const int x = 2 * tiles + k_at(u, ahead), sk = x % NS;
+              ok = wait(&full[sk], x / NS);
               if (!ok) break;
-              tc_fence_after();
-              const uint8_t* kt = sm + sk * L::kTile;
-              const uint32_t d = cols ? tS + (kjob & 1) * 64 : tS;
-              if (elect_one()) {
-                if (cols) {
+              if (!two && (u & 1) != gq) {  // the other group's tile
+                if (elect_one()) mbar_arrive(&empty[sk]);
+              } else {
+                // (after the other layout: its last P lies where these scores go)
+                if (!TP && kjob == job && kjob > 0) ok = wait(&pv_done[2 * gq + (kjob - 1 & 1)], kjob - 1 >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint8_t* kt = sm + sk * L::kTile;
+                const uint32_t d = tS + (kjob & 1) * 64;
+                if (elect_one()) {
 #pragma unroll
                   for (int kk = 0; kk < HD / 16; ++kk) {
                     const uint64_t off = (uint64_t)(((kk & 3) * 32) >> 4);
                     tc_mma_f16(d, smem_desc_sw128(kt + (kk >> 2) * 16384) + off,
                                smem_desc_sw128(qs + (kk >> 2) * 8192) + off, idSt, kk > 0 ? 1u : 0u);
                   }
-                } else {
-#pragma unroll
-                  for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint64_t off = (uint64_t)(((kk & 3) * 32) >> 4);
-                    tc_mma_f16(d, smem_desc_sw128(qs + (kk >> 2) * 16384) + off,
-                               smem_desc_sw128(kt + (kk >> 2) * 16384) + off, idS, kk > 0 ? 1u : 0u);
-                  }
+                  tc_commit(&s_full[2 * gq + (kjob & 1)]);
+                  tc_commit(&empty[sk]);
+                  // The last scores of the piece: the query tile is free after them.  (Where the other layout comes
+                  // first, it is free after the last product: the hand-over below counts on it.)
+                  if (TP && u + (two ? 1 : 2) >= nt) tc_commit(&q_empty[buf]);
                 }
-                tc_commit(&s_full[2 * gq + (cols ? kjob & 1 : 0)]);
-                tc_commit(&empty[sk]);
-                // The last scores of the piece: the query tile is free after them.  (Where the other layout comes
-                // first, rows as columns free it after their last product: the hand-over below counts on it.)
-                if ((TP || !cols) && u + (two ? 1 : 2) >= nt) {
-                  tc_commit(&q_empty[buf]);
-                  if (qtwo) tc_commit(&q_empty[buf]);
-                }
+                __syncwarp();
+                ++kjob;
               }
-              __syncwarp();
-              ++kjob;
             }
-          }
-          if (u >= ahead) {
-            const int t = u - ahead, x = 2 * tiles + v_at(t, ahead, nt), sv = x % NS;
-            ok = wait(&full[sv], x / NS);
-            if (!ok) break;
-            if (!two && (t & 1) != gq) {
-              if (elect_one()) mbar_arrive(&empty[sv]);
-            } else {
-              const bool first = t == (two ? 0 : gq);
-              if (elect_one()) mbar_arrive(&v_ready[gq]);
-              ok = wait(&p_full[gq], job);
-              if (ok && first && seg > 0) ok = wait(&o_free[gq], seg - 1);
+            if (u >= ahead) {
+              const int t = u - ahead, x = 2 * tiles + v_at(t, ahead, nt), sv = x % NS;
+              ok = wait(&full[sv], x / NS);
               if (!ok) break;
-              tc_fence_after();
-              const uint32_t acc0 = first ? acc_first[gq] : 1u;
-              const uint32_t vt = smem_u32(sm + sv * L::kTile);
-              if (elect_one()) {
-                if (cols) {
+              if (!two && (t & 1) != gq) {
+                if (elect_one()) mbar_arrive(&empty[sv]);
+              } else {
+                const bool first = t == (two ? 0 : gq);
+                if (elect_one()) mbar_arrive(&v_ready[gq]);
+                ok = wait(&p_full[2 * gq + (job & 1)], job >> 1);
+                if (ok && first && seg > 0) ok = wait(&o_free[gq], seg - 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc0 = first ? acc_first[gq] : 1u;
+                const uint32_t vt = smem_u32(sm + sv * L::kTile);
+                if (elect_one()) {
                   // (head_dim 64: the upper 64 lanes take what lies behind the tile, and nothing reads them)
                   const uint32_t ps = smem_u32(sm + L::kQ + gq * L::kQBuf + L::kP);
 #pragma unroll
                   for (int kk = 0; kk < 8; ++kk)
                     tc_mma_f16(tO, smem_desc_mn(vt + kk * 2048, 16384), smem_desc_mn(ps + kk * 2048, 16384), idOt,
                                kk > 0 ? 1u : acc0);
-                } else {
-#pragma unroll
-                  for (int kk = 0; kk < 8; ++kk)
-                    tc_mma_f16_tmem_a(tO, tS + kk * 8, smem_desc_mn(vt + kk * 2048, 16384), idO, kk > 0 ? 1u : acc0);
+                  tc_commit(&pv_done[2 * gq + (job & 1)]);
+                  tc_commit(&empty[sv]);
+                  if (!TP && t + (two ? 1 : 2) >= nt) tc_commit(&q_empty[buf]);
                 }
-                tc_commit(&pv_done[gq]);
-                tc_commit(&empty[sv]);
-                if (!TP && cols && t + (two ? 1 : 2) >= nt) tc_commit(&q_empty[buf]);
+                __syncwarp();
+                ++job;
               }
-              __syncwarp();
-              ++job;
+            }
+          }
+        } else {
+          // Half a tile is a job: scores of 64 keys in one of two buffers, P over them.  The first half's product
+          // and the next tile's first scores run while the group is at the second half, and the other way round.
+          int vp = -1;  // slot of the value tile whose second half is still to be multiplied
+          auto half_pv = [&](int j, int sv, uint32_t acc0) {  // P V of job j
+            const int hf = j & 1;
+            const uint32_t vt = smem_u32(sm + sv * L::kTile) + hf * 8192;
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_f16_tmem_a(tO, tS + hf * 64 + kk * 8, smem_desc_mn(vt + kk * 2048, 16384), idO,
+                                  kk > 0 ? 1u : acc0);
+              tc_commit(&pv_done[2 * gq + hf]);
+              if (hf) tc_commit(&empty[sv]);
+            }
+            __syncwarp();
+          };
+          auto half_s = [&](int hf, const uint8_t* kt) {  // scores of a half
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint64_t off = (uint64_t)(((kk & 3) * 32) >> 4);
+                tc_mma_f16(tS + hf * 64, smem_desc_sw128(qs + (kk >> 2) * 16384) + off,
+                           smem_desc_sw128(kt + (kk >> 2) * 16384 + hf * 8192) + off, idS, kk > 0 ? 1u : 0u);
+              }
+              tc_commit(&s_full[2 * gq + hf]);
+            }
+            __syncwarp();
+          };
+          for (int u = 0; ok && u < nt; ++u) {
+            const int xk = 2 * (tiles + u), sk = xk % NS, sv = (xk + 1) % NS;
+            ok = wait(&full[sk], xk / NS);
+            if (!ok) break;
+            if (!two && (u & 1) != gq) {  // the other group's tile
+              if (elect_one()) mbar_arrive(&empty[sk]);
+              ok = wait(&full[sv], (xk + 1) / NS);
+              if (ok && elect_one()) mbar_arrive(&empty[sv]);
+              continue;
+            }
+            const uint8_t* kt = sm + sk * L::kTile;
+            const bool first = u == (two ? 0 : gq);
+            // P lies over the last scores of a buffer until its product is done
+            if (job > 1) ok = wait(&pv_done[2 * gq + (job - 2 & 1)], job - 2 >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            half_s(0, kt);
+            if (vp >= 0) {
+              ok = wait(&p_full[2 * gq + 1], job - 1 >> 1);
+              if (!ok) break;
+              tc_fence_after();
+              half_pv(job - 1, vp, 1u);
+            }
+            if (job > 0) ok = wait(&pv_done[2 * gq + (job - 1 & 1)], job - 1 >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            half_s(1, kt);
+            if (elect_one()) {
+              tc_commit(&empty[sk]);
+              if (u + (two ? 1 : 2) >= nt) {  // the last scores of the piece: the query tile is free after them
+                tc_commit(&q_empty[buf]);
+                if (two) tc_commit(&q_empty[buf]);
+              }
+            }
+            __syncwarp();
+            ok = wait(&full[sv], (xk + 1) / NS);
+            if (ok && elect_one()) mbar_arrive(&v_ready[gq]);
+            ok = ok && wait(&p_full[2 * gq], job >> 1);
+            if (ok && first && seg > 0) ok = wait(&o_free[gq], seg - 1);
+            if (!ok) break;
+            tc_fence_after();
+            half_pv(job, sv, first ? acc_first[gq] : 1u);
+            vp = sv;
+            job += 2;
+          }
+          if (ok && vp >= 0) {
+            ok = wait(&p_full[2 * gq + 1], job - 1 >> 1);
+            if (ok) {
+              tc_fence_after();
+              half_pv(job - 1, vp, 1u);
             }
           }
         }
@@ -634,12 +702,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    reg_inc<216>();
+    reg_inc<208>();
     const int gq = (warp - 4) >> 2, qr = warp & 3;  // TMEM lane quarter
     const int r = qr * 32 + lane;
     const uint32_t lanes = (uint32_t)(qr * 32) << 16;
     const uint32_t tS = tmem + lanes + gq * 128, tO = tmem + lanes + 256 + gq * 128;
-    int job = 0, xn = 0, fn = 0, fb = 0;  // tiles done; joins; phases of the group's meetings and of both groups'
+    int vjob = 0;                         // tiles done
+    int job = 0, xn = 0, fn = 0, fb = 0;  // score buffers done (half tiles of rows as rows); joins; phases of the group's meetings and of both groups'
     uint32_t sn0 = 0, sn1 = 0;            // uses of the score buffers
     bool handover = false;                // a query tile of the rows-as-rows layout may still lie where P goes
     const float sl = scale_log2;
@@ -656,13 +725,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto chunk = [&](uint8_t* vt, int key, int c) {
       return reinterpret_cast<uint4*>(vt + (c >> 3) * 16384 + key * 128 + (((c & 7) ^ (key & 7)) << 4));
     };
-    // x 0 is NaN for an x that is not finite, and so is a sum that has met it
-    auto row_is_bad = [&](uint8_t* vt) {
+    // x 0 is NaN for an x that is not finite, and so is a sum that has met it (n chunks of a key from c0 on)
+    auto row_is_bad = [&](uint8_t* vt, int key, int c0, const int n) {
       const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
       __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
 #pragma unroll
-      for (int c = 0; c < HD / 8; ++c) {
-        const uint4 w = *chunk(vt, r, c);
+      for (int c = 0; c < n; ++c) {
+        const uint4 w = *chunk(vt, key, c0 + c);
         const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] = __hfma2(x[e], zero, acc[e]);
@@ -670,17 +739,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float2 f = __bfloat1622float2(__hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3])));
       return f.x != 0.f || f.y != 0.f;
     };
-    auto clean_row = [&](uint8_t* vt) {
+    auto clean_row = [&](uint8_t* vt, int key, int c0, int n) {
 #pragma unroll 1
-      for (int c = 0; c < HD / 8; ++c) {
-        uint4 w = *chunk(vt, r, c);
+      for (int c = c0; c < c0 + n; ++c) {
+        uint4 w = *chunk(vt, key, c);
         uint32_t* x = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0xffffu;
           if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u;
         }
-        *chunk(vt, r, c) = w;
+        *chunk(vt, key, c) = w;
       }
     };
     // an item's first product comes after this when its accumulator starts here
@@ -727,40 +796,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         hi = min(hi, key_end);
         sink = min(sink, key_end);
         float M = -INFINITY, Ls = 0.f;
-        for (int t = t0; ok && t < nt; t += step) {
-          const int k0 = pc.tile(t) * KT;
-          const bool inner = k0 >= pc.all_lo && k0 + KT <= pc.all_hi;  // the same for all warps of the item
-          if (stop(wait_phase(&s_full[2 * gq], sn0 & 1u, abort_f, g.status))) {
+        int own = 0;  // tiles of this group in the piece
+        for (int x = 2 * t0; ok && x < 2 * nt; x += (x & 1) ? 2 * step - 1 : 1) {  // half tiles
+          const int t = x >> 1, hf = x & 1;
+          const bool first = x == 2 * t0;
+          const int k0 = pc.tile(t) * KT + hf * 64;
+          const bool inner = k0 >= pc.all_lo && k0 + 64 <= pc.all_hi;  // the same for all warps of the item
+          const uint32_t tH = tS + hf * 64;
+          uint32_t& sn = hf ? sn1 : sn0;
+          if (stop(wait_phase(&s_full[2 * gq + hf], sn & 1u, abort_f, g.status))) {
             ok = false;
             break;
           }
-          ++sn0;
+          ++sn;
+          // O may be changed once the last product is done (the one before it is: these scores came after it)
+          auto wait_pv = [&]() {
+            if (!first) {
+              ok = !stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g.status));
+              tc_fence_after();
+            }
+            return ok;
+          };
           tc_fence_after();
-          float v[128];
-          uint32_t vw[4] = {0u, 0u, 0u, 0u};  // visible keys of the tile
+          float v[64];
+          uint32_t vw[2] = {0u, 0u};  // visible keys of the half
           float Mn = M, f = 1.f;
           bool wfull = true;
           if (!inner) {
-            const bool row_full = k0 >= key_lo && ((lo <= k0 && hi >= k0 + KT) || sink >= k0 + KT);
+            const bool row_full = k0 >= key_lo && ((lo <= k0 && hi >= k0 + 64) || sink >= k0 + 64);
             wfull = __all_sync(0xffffffffu, !me.live || row_full);
             if (me.live) {
 #pragma unroll
-              for (int w = 0; w < 4; ++w)
+              for (int w = 0; w < 2; ++w)
                 vw[w] = bits_of(lo - k0 - 32 * w, hi - k0 - 32 * w) | bits_of(key_lo - k0 - 32 * w, sink - k0 - 32 * w);
             }
           }
           if (warp_live) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+            for (int c = 0; c < 2; ++c) tmem_ld32(tH + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
             tmem_ld_wait();
             if (!wfull) {
 #pragma unroll
-              for (int e = 0; e < 128; ++e)
+              for (int e = 0; e < 64; ++e)
                 if (!((vw[e >> 5] >> (e & 31)) & 1u)) v[e] = -INFINITY;
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 128; e += 8)
+            for (int e = 0; e < 64; e += 8)
 #pragma unroll
               for (int w = 0; w < 4; ++w) mx[w] = max3(mx[w], v[e + w], v[e + w + 4]);
             const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
@@ -774,7 +856,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 raise = true;
               }
             }
-            if (__any_sync(0xffffffffu, raise)) {  // the group's earlier products are done: S came after them
+            if (__any_sync(0xffffffffu, raise)) {
+              if (!wait_pv()) break;
               f = raise ? ex2f(M - Mn) : 1.f;
 #pragma unroll 1
               for (int c = 0; c < HD; c += 16) {
@@ -791,48 +874,47 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float negm = Mn == -INFINITY ? 0.f : -Mn;
           uint32_t first_acc = 0u;
           if (!inner) {
-            // values that are not finite, a key a thread
+            // values that are not finite, two threads a key
             uint8_t* vt = sm + (2 * (tiles + t) + 1) % NS * L::kTile;
             uint64_t* fx = two ? &fix[2] : &fix[gq];
             int& ph = two ? fb : fn;
-            ok = !stop(wait_phase(&v_ready[gq], (uint32_t)job & 1u, abort_f, g.status));
+            ok = !stop(wait_phase(&v_ready[gq], (uint32_t)(vjob + own) & 1u, abort_f, g.status));
             if (!ok) break;
-            const bool bad = row_is_bad(vt);
+            const int vkey = hf * 64 + (r & 63), c0 = (r >> 6) * (HD / 16);
+            const bool bad = row_is_bad(vt, vkey, c0, HD / 16);
             const uint32_t word = __ballot_sync(0xffffffffu, bad);
-            if (lane == 0) bad_w[gq * 4 + qr] = word;
+            volatile uint32_t* words = vote_w + (hf * 2 + gq) * 4;  // (two sets: a warp may be a half ahead)
+            if (lane == 0) words[qr] = word;
             ok = meet(fx, ph);
             if (!ok) break;
-            const uint32_t bw[4] = {bad_w[gq * 4], bad_w[gq * 4 + 1], bad_w[gq * 4 + 2], bad_w[gq * 4 + 3]};
-            if (bw[0] | bw[1] | bw[2] | bw[3]) {  // uniform over the item's groups
-              if (t == t0 && warp_live) {
-                // O starts here instead of in the first product, which must not overtake its last reader
-                if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g.status));
-                if (!ok) break;
-                tc_fence_after();
-                zero_o(HD);
-              }
-              first_acc = 1u;
+            const uint32_t bw[2] = {words[0] | words[2], words[1] | words[3]};
+            if (bw[0] | bw[1]) {  // uniform over the item's groups
               if (warp_live) {
+                if (!wait_pv()) break;
+                if (first) {
+                  // O starts here instead of in the first product, which must not overtake its last reader
+                  if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g.status));
+                  if (!ok) break;
+                  tc_fence_after();
+                  zero_o(HD);
+                }
 #pragma unroll 1
-                for (int key = 0; key < KT; ++key) {
-                  auto word_of = [&](const uint32_t (&w)[4]) {
-                    return key < 64 ? (key < 32 ? w[0] : w[1]) : (key < 96 ? w[2] : w[3]);
-                  };
-                  if (!((word_of(bw) >> (key & 31)) & 1u)) continue;
-                  const float s = __uint_as_float(tmem_ld1(tS + key));
+                for (int key = 0; key < 64; ++key) {
+                  if (!(((key < 32 ? bw[0] : bw[1]) >> (key & 31)) & 1u)) continue;
+                  const float s = __uint_as_float(tmem_ld1(tH + key));
                   tmem_ld_wait();
-                  const bool see = (word_of(vw) >> (key & 31)) & 1u;
+                  const bool see = ((key < 32 ? vw[0] : vw[1]) >> (key & 31)) & 1u;
                   const float p = ex2f(fmaf(s, sl, negm));
 #pragma unroll 1
                   for (int c = 0; c < HD; c += 16) {
                     uint32_t o[16];
                     tmem_ld16u(tO + c, o);
                     tmem_ld_wait();
-                    const uint4 w[2] = {*chunk(vt, key, c >> 3), *chunk(vt, key, (c >> 3) + 1)};
-                    const uint32_t* x = reinterpret_cast<const uint32_t*>(w);
+                    const uint4 w[2] = {*chunk(vt, hf * 64 + key, c >> 3), *chunk(vt, hf * 64 + key, (c >> 3) + 1)};
+                    const uint32_t* y = reinterpret_cast<const uint32_t*>(w);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                      const uint32_t hbits = (e & 1) ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16;
+                      const uint32_t hbits = (e & 1) ? y[e >> 1] & 0xffff0000u : y[e >> 1] << 16;
                       if (see && (hbits & 0x7f800000u) == 0x7f800000u)
                         o[e] = __float_as_uint(fmaf(p, __uint_as_float(hbits), __uint_as_float(o[e])));
                     }
@@ -841,9 +923,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   }
                 }
               }
+              first_acc = 1u;
               ok = meet(fx, ph);  // every row has taken what it sees
               if (!ok) break;
-              if (bad) clean_row(vt);
+              if (bad) clean_row(vt, vkey, c0, HD / 16);
               fence_proxy_async_smem();
             }
           }
@@ -851,7 +934,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(negm, negm);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {  // 32 keys
+            for (int c = 0; c < 2; ++c) {  // 32 keys
               uint32_t p16[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
@@ -862,20 +945,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const __nv_bfloat162 h2 = __floats2bfloat162_rn(p.x, p.y);
                 p16[e] = *reinterpret_cast<const uint32_t*>(&h2);
               }
-              tmem_st16(tS + c * 16, p16);
+              tmem_st16(tH + c * 16, p16);
             }
             Ls = fmaf(Ls, f, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
             M = Mn;
             tmem_st_wait();
           }
-          if (t == t0 && r == 0) acc_first[gq] = first_acc;
+          if (first && r == 0) acc_first[gq] = first_acc;
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[gq]);
+          if (lane == 0) mbar_arrive(&p_full[2 * gq + (job & 1)]);
           ++job;
+          own += hf;
         }
+        vjob += own;
         if (!ok) break;
-        if (has && stop(wait_phase(&pv_done[gq], (uint32_t)(job - 1) & 1u, abort_f, g.status))) break;
+        if (has && stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g.status))) break;
         // ---- the piece's end: group 0 joins both groups' parts of a single query tile, else each has its own
         float2 other = make_float2(-INFINITY, 0.f);
         if (!two) {
@@ -993,7 +1078,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // the last product has read P and left O to be changed
           bool pv_waited = first;
           auto wait_pv = [&]() {
-            if (!pv_waited) ok = !stop(wait_phase(&pv_done[gq], (uint32_t)(job - 1) & 1u, abort_f, g.status));
+            if (!pv_waited) ok = !stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g.status));
             if (!pv_waited) tc_fence_after();
             pv_waited = true;
             return ok;
@@ -1160,9 +1245,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint8_t* vt = sm + (2 * tiles + v_at(t, ahead, nt)) % NS * L::kTile;
             // (the last product's values had landed: this wait cannot take their phase for its own)
             if (!wait_pv()) break;
-            ok = !stop(wait_phase(&v_ready[gq], (uint32_t)job & 1u, abort_f, g.status));
+            ok = !stop(wait_phase(&v_ready[gq], (uint32_t)vjob & 1u, abort_f, g.status));
             if (!ok) break;
-            const bool bad = row_is_bad(vt);
+            const bool bad = row_is_bad(vt, r, 0, HD / 8);
             const uint32_t word = __ballot_sync(0xffffffffu, bad);
             if (lane == 0) bad_w[gq * 4 + qr] = word;
             ok = meet(&fix[gq], fn);
@@ -1209,7 +1294,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               // (a tile that both groups work on is cleaned once both have taken from it)
               ok = two ? meet(&fix[2], fb) : meet(&fix[gq], fn);
               if (!ok) break;
-              if (bad) clean_row(vt);
+              if (bad) clean_row(vt, r, 0, HD / 8);
             }
           }
           // this key's row of P: a bf16 a row of the item (pairs: the low parts behind the high ones)
@@ -1235,14 +1320,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (first && r == 0) acc_first[gq] = first_acc;
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[gq]);
+          if (lane == 0) mbar_arrive(&p_full[2 * gq + (job & 1)]);
           ++job;
+          ++vjob;
         }
         if (!ok) break;
         // ---- the piece's end: row sums over the group, then group 0 joins both groups' parts
         float M = -INFINITY, Lr = 0.f;  // of row r (threads below NR)
         if (has) {
-          if (stop(wait_phase(&pv_done[gq], (uint32_t)(job - 1) & 1u, abort_f, g.status))) break;
+          if (stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g.status))) break;
           warp_scatter<NR, false>(Ls, lane);
           to_scratch(Ls);
           if (!meet(&fix[gq], fn)) break;
