@@ -508,6 +508,87 @@ def test_equal_calls_give_equal_bits():
         assert torch.equal(first, attend(x, q))
 
 
+# stacked rows (n x query heads of a KV head) on both sides of every size at which the work is laid out anew
+STACKED = [(1, 15), (1, 16), (1, 17), (2, 16), (11, 3), (16, 4), (13, 5), (64, 1), (65, 1), (32, 4), (43, 3), (128, 2), (257, 1)]
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n,G", STACKED, ids=[f"{n * G}" for n, G in STACKED])
+def test_stacked_rows(n, G, hd):
+    """Few long sequences (pieces to join) and short ones, all and one of them padded, with and without the
+    window, causal or not, on their own and behind a shared prefix; the same call gives the same bits."""
+    x = Batch("bf16", 2 * G, 2, hd, 32, [6000, 640, 1000], n, rows=[n, max(n - 3, 0), 1], fill=float("nan"), seed=n * G, shared=640)
+    q = x.query()
+    for kw in (dict(), dict(window=700, sinks=5), dict(causal=False)):
+        want = reference(x, q, **kw)
+        for sh in (None, 640):
+            out = attend(x, q, shared=sh, **kw)
+            untouched(x, out)
+            check(x, out, want, f"{kw} shared {sh}")
+            assert torch.equal(out, attend(x, q, shared=sh, **kw))
+    assert x.cache.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,n", [(33, 1), (64, 3), (128, 1), (129, 2), (300, 1), (700, 1)])
+def test_many_sequences(B, n, dtype):
+    """More sequences than lanes, than a warp plans, than threads and CTAs; one is long, some have no rows."""
+    own = [(37 * b) % 200 for b in range(B)]
+    own[B // 2] = 2000
+    rows = [0 if b % 7 == 3 else 1 + b % n for b in range(B)]
+    x = Batch(dtype, 8, 2, 64, 16, [160 + o for o in own], n, rows=rows, fill=float("nan"), seed=B, shared=160)
+    q = x.query()
+    for kw in (dict(), dict(window=90, sinks=2)):
+        want = reference(x, q, **kw)
+        for sh in (None, 160):
+            out = attend(x, q, shared=sh, **kw)
+            untouched(x, out)
+            check(x, out, want, f"{kw} shared {sh}")
+            assert torch.equal(out, attend(x, q, shared=sh, **kw))
+    assert x.cache.status() == 0
+
+
+def test_calls_at_the_same_time():
+    """Two workspaces over one pool, on two streams, eager and from graphs: neither disturbs the other."""
+    xs = [Batch("bf16", 8, 2, 128, 16, lens, n, seed=n) for lens, n in (([5000, 700, 3], 1), ([900, 4000], 16))]
+    qs = [x.query() for x in xs]
+    wants = [reference(x, q) for x, q in zip(xs, qs)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    outs = [[torch.full_like(q, 77.0) for _ in range(8)] for q in qs]
+    torch.cuda.synchronize()
+    graphs = []
+    for x, q, s, o in zip(xs, qs, streams, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            for y in o[4:]:
+                x.cache.attention(0, q, x.table, x.len, y)
+    for k in range(4):
+        for x, q, s, o in zip(xs, qs, streams, outs):
+            with torch.cuda.stream(s):
+                x.cache.attention(0, q, x.table, x.len, o[k])
+    for s, g in zip(streams, graphs):
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    for x, o, want in zip(xs, outs, wants):
+        check(x, o[0], want)
+        assert all(torch.equal(o[0], y) for y in o[1:])
+        assert x.cache.status() == 0
+
+
+def test_results_at_sixteen_bytes():
+    """Queries and results that start 16 bytes past any larger boundary."""
+    x = Batch("bf16", 8, 2, 128, 16, [900, 40], 5)
+    q = x.query()
+    first = attend(x, q)
+    qb, ob = (torch.full((q.numel() + 16,), 77.0, dtype=x.dt, device="cuda") for _ in range(2))
+    q2, o2 = qb[8:-8].view(q.shape), ob[8:-8].view(q.shape)
+    q2.copy_(q)
+    x.cache.attention(0, q2, x.table, x.len, o2)
+    assert torch.equal(first, o2) and (ob[:8] == 77.0).all() and (ob[-8:] == 77.0).all()
+    check(x, first, reference(x, q))
+
+
 # ------------------------------------------------------------------ refusals
 
 
