@@ -362,15 +362,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (i >= rows) return;
   const int hk = div_g(g, h), x = i * g.G + h - hk * g.G, rt = x / g.ri;
   // its sequence's own pieces
-  for (int y = 0; y < rt; ++y) at += span_of<KT>(g, P, rows, y, sh).count() * g.nkv;
+  for (int y = 0; y < rt; ++y) at += item_len(span_of<KT>(g, P, rows, y, sh).count(), g.w_s, g.oh_s) * g.nkv;
   const int cnt = span_of<KT>(g, P, rows, rt, sh).count();
-  at += hk * cnt;
+  at += hk * item_len(cnt, g.w_s, g.oh_s);
   int c0 = 0, p0 = 0;
-  const int ns = cnt > 0 ? pieces_of(at, cnt, quota, c0) : 0;
+  const int ns = cnt > 0 ? pieces_of(Span1{at, cnt, g.w_s, g.oh_s}, quota, c0) : 0;
   if (ns <= 1 && pre == 0) return;
   const long long srow = ((long long)(b * g.nrt + rt) * g.nkv + hk + c0) * g.slot_s + x - rt * g.ri;
   const int xp = r * g.G + h - hk * g.G, rp = xp / g.rp, k = hk * g.nrp + rp;
-  const int np = pre > 0 ? pieces_of(k * pre, pre, quota, p0) : 0;
+  const int np = pre > 0 ? pieces_of(Span1{k * item_len(pre, g.w_p, g.oh_p), pre, g.w_p, g.oh_p}, quota, p0) : 0;
   const long long prow = g.pre_row0 + (long long)(k + p0) * g.slot_p + xp - rp * g.rp;
   merge_row<T, HD>(g, np + ns, [&](int c) {
     return c < np ? prow + (long long)c * g.slot_p : srow + (long long)(c - np) * g.slot_s;
@@ -418,14 +418,14 @@ cudaError_t paged_merge_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t
 
 // Fills in the split of a call: row groups of `ri` / `rp` stacked rows and the partial slots.
 // Returns the partial rows it needs.
-long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_quota) {
+long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_tiles) {
   g.ri = ri;
   g.rp = rp;
   g.g_magic = (unsigned)(((1ull << 32) + g.G - 1) / g.G);
   g.nrt = (g.n * g.G + ri - 1) / ri;
   g.nrp = (g.batch * g.n * g.G + rp - 1) / rp;
   g.grid = grid;
-  g.min_quota = min_quota;
+  g.min_quota = min_tiles * std::max(g.w_s, g.w_p);
   g.slot_s = std::min(g.n * g.G, ri);
   g.slot_p = std::min(g.batch * g.n * g.G, rp);
   g.pre_row0 = ((long long)g.batch * g.nrt * g.nkv + grid) * g.slot_s;
@@ -436,7 +436,7 @@ long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_quota) {
 // the smallest row groups (16 stacked rows) and tiles.
 bool paged_line_fits(const PagedGeom& g) {
   const long long groups = (long long)g.batch * ((g.n * g.G + 15) / 16) * (g.shared ? 2 : 1);
-  return (double)groups * g.nkv * ((double)g.cap / kCoreKeys + 2) < 1073741824.0;
+  return (double)groups * g.nkv * ((double)g.cap / kCoreKeys + 2) < 134217728.0;  // (at most 8 positions a tile)
 }
 
 template <typename T, int HD, int MRM>
@@ -452,6 +452,7 @@ static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const
                                                           L::kSmem));
     per_sm = std::min(std::max(x, 1), kPagedMaxCtas);
   }
+  g.w_s = g.w_p = 1;
   if (paged_split(g, L::MR, L::MR, num_sms() * per_sm, 4) > part_rows) return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
   DFL_RET(launch_pdl(paged_attn_core_kernel<T, HD, MRM>, dim3(g.grid), dim3(kCoreThreads), L::kSmem, s, g, (const T*)q,

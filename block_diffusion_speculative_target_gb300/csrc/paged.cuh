@@ -9,17 +9,19 @@
 // common keys [0, sh) are then read once for all of them.  An item's keys are
 // walked in tiles of KT keys at absolute multiples of KT, only those that some
 // row of it sees (first tokens that stay visible, then the window).  All tiles
-// of all items, in item order, form one line of T tiles that is cut into
-// runs of about `quota` tiles, a run to a CTA, so every CTA has the same work
-// whatever the lengths; a CTA's run covers the end of one item, whole items,
-// and the start of another.  An item inside one run whose rows have no other
-// part is finished there; every other piece leaves a partial result (row
-// maximum, sum, unnormalised output).  Pieces are added up in tile order: by the
-// CTA that finishes an item's last one, or, where items have many rows or a
-// shared prefix has left pieces that belong to many items, by a second kernel.  Prefix items come first in the line, head by head; suffix items
-// follow in order of sequence, row group, head.  The cut depends on all
-// lengths of the call: a row's last bits may depend on the batch around it,
-// but the same call gives the same bits every time.
+// of all items, in item order, form one line: a tile takes `w` positions and an
+// item `oh` more, for its start and its end, in the proportion of their times.
+// Prefix items come first, head by head; suffix items follow in order of
+// sequence, row group, head.  The line is cut into runs of `quota` positions, a
+// run to a CTA, so every CTA has the same work whatever the lengths; a run
+// covers the end of one item, whole items, and the start of another.  An item
+// inside one run whose rows have no other part is finished there; every other
+// piece leaves a partial result (row maximum, sum, unnormalised output).
+// Pieces are added up in tile order: by the CTA that finishes an item's last
+// one, or, where items have many rows or a shared prefix has left pieces that
+// belong to many items, by a second kernel.  The cut depends on all lengths of
+// the call: a row's last bits may depend on the batch around it, but the same
+// call gives the same bits every time.
 #pragma once
 #include <stdint.h>
 
@@ -36,6 +38,7 @@ struct PagedGeom {
   int cap;               // keys a sequence's table row can name
   int grid;              // CTAs of the attention kernel
   int min_quota;
+  int w_s, oh_s, w_p, oh_p;  // line positions of a tile of a suffix / prefix item, and of an item's start and end
   long long page_row0;   // pool row of (layer, page 0, head 0, slot 0)
   const int32_t* len;
   const int32_t* n_rows; // null: n
@@ -131,36 +134,45 @@ __device__ __forceinline__ TileSpan prefix_span(const PagedGeom& g, int sh_tiles
   return s;
 }
 
+// An item's place on the line.
+struct Span1 {
+  int line, total;  // first position, tiles
+  int w, oh;        // positions a tile (1 or 2), and before the first one
+  __device__ __forceinline__ int end() const { return line + oh + total * w; }
+};
 // A CTA's piece of one item.
 struct Segment {
   bool prefix;
   int b, rt, hk;      // suffix: sequence, row group, head; prefix: row group rt of the batch, keys named by b's table
   TileSpan span;
   int t0, nt, total;  // its tiles [t0, t0 + nt) of the item's `total`
-  int line;           // the item's first line position
+  Span1 at;           // its place on the line
   int ordinal;        // among the prefix or the suffix items
   long long slot_row; // first partial row of this piece
 };
 
-// Cuts of the line.  Cut k lies at k quota, but one that would leave `snap` tiles or fewer of an item on one
-// side moves to that item's edge: a piece costs about three tiles besides its own (start, partial result,
-// joining), so short ones do not pay.  Items of several runs are cut everywhere but within a quarter of a run.
-__device__ __forceinline__ int snap_of(int total, int quota) {
-  return total <= 2 * quota ? min(3, total / 2) : min(3, quota / 4);
+// Cuts of the line.  Cut k lies at k quota and divides the item that it falls into at the nearest tile; but
+// where that would leave `snap` tiles or fewer on one side, it moves to that end of the item: short pieces do
+// not pay for their start, their partial result and joining them.
+__device__ __forceinline__ int snap_of(const Span1& s, int quota) {
+  if (s.total * s.w <= 2 * quota) return min(3, s.total >> 1);
+  const int q = 4 * s.w;  // min(3, quota / q)
+  return (quota >= q) + (quota >= 2 * q) + (quota >= 3 * q);
 }
-// Where the cut at `pos` inside the item [line, line + total) comes to lie.
-__device__ __forceinline__ int cut_at(int pos, int line, int total, int quota) {
-  const int snap = snap_of(total, quota);
-  return pos - line <= snap ? line : line + total - pos <= snap ? line + total : pos;
+// The tile of the item before which a cut at `pos`, inside the item, comes to lie (0 or total: at an end).
+__device__ __forceinline__ int cut_at(int pos, const Span1& s, int quota) {
+  const int snap = snap_of(s, quota), o = pos - s.line - s.oh + s.w / 2;
+  const int t = o <= 0 ? 0 : min(o >> (s.w >> 1), s.total);
+  return t <= snap ? 0 : s.total - t <= snap ? s.total : t;
 }
 // The pieces of an item: from CTA `c0` on, one a CTA.
-__device__ __forceinline__ int pieces_of(int line, int total, int quota, int& c0) {
-  const int snap = snap_of(total, quota);
-  // the first and the last cut inside the item
-  const int k0 = (int)((unsigned)(line + snap) / (unsigned)quota) + 1;
-  const int k1 = (int)((unsigned)(max(line + total - snap, 1) - 1) / (unsigned)quota);
+__device__ __forceinline__ int pieces_of(const Span1& s, int quota, int& c0) {
+  const int snap = snap_of(s, quota), at = s.line + s.oh - s.w / 2;
+  // the first cut past `snap` tiles, and the first with `snap` or fewer behind it
+  const int k0 = (int)((unsigned)(at + (snap + 1) * s.w + quota - 1) / (unsigned)quota);
+  const int k1 = (int)((unsigned)(at + (s.total - snap) * s.w + quota - 1) / (unsigned)quota);
   c0 = k0 - 1;
-  return max(k1 - k0 + 2, 1);
+  return max(k1 - k0, 0) + 1;
 }
 
 // The line as one CTA sees it.
@@ -170,51 +182,83 @@ struct PlanView {
   int b, cum;  // the sequence that holds the CTA's first tile (past the prefix items), and its line position
 };
 
-// plan_view of up to 32 sequences by one warp for itself, a lane a sequence (`write`: it writes the plan).
+// Line positions of an item of `tiles` tiles.
+__device__ __forceinline__ int item_len(int tiles, int w, int oh) { return tiles > 0 ? oh + tiles * w : 0; }
+__device__ __forceinline__ int pre_positions(const PagedGeom& g, int pre_tiles) {
+  return item_len(pre_tiles, g.w_p, g.oh_p) * g.nrp * g.nkv;
+}
+template <int KT>
+__device__ __forceinline__ int positions_of(const PagedGeom& g, int P, int rows, int sh_tiles) {
+  int c = 0;
+  for (int rt = 0; rt < g.nrt; ++rt) c += item_len(span_of<KT>(g, P, rows, rt, sh_tiles).count(), g.w_s, g.oh_s);
+  return c * g.nkv;
+}
+
+// plan_view by one warp for itself, a lane for every few sequences (`write`: it writes the plan).
+constexpr int kPlanSmall = 128;
 template <int KT>
 __device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, per = (g.batch + 31) >> 5, b0 = lane * per, b1 = min(b0 + per, g.batch);
   PlanView v;
-  const bool in = lane < g.batch;
-  const int rows = in ? paged_rows(g, lane) : 0, P = in ? paged_len(g, lane) : 0;
   v.sh_tiles = v.min_len = v.pre_b = v.pre_tiles = 0;
+  const bool in = b0 < g.batch;
+  const int rows0 = in ? paged_rows(g, b0) : 0, P0 = in ? paged_len(g, b0) : 0;  // the lane's first sequence
   if (g.shared) {
-    const unsigned live = __ballot_sync(0xffffffffu, rows > 0);
-    v.min_len = __reduce_min_sync(0xffffffffu, rows > 0 ? min(P, g.cap) : INT32_MAX);
-    if (live) {
-      v.pre_b = __ffs(live) - 1;
+    int m = rows0 > 0 ? min(P0, g.cap) : INT32_MAX, first = rows0 > 0 ? b0 : g.batch;
+    for (int b = b0 + 1; b < b1; ++b)
+      if (paged_rows(g, b) > 0) {
+        m = min(m, min(paged_len(g, b), g.cap));
+        first = min(first, b);
+      }
+    v.min_len = __reduce_min_sync(0xffffffffu, m);
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (first < g.batch) {
+      v.pre_b = first;
       v.sh_tiles = max(0, min(*g.shared, v.min_len)) / KT;
       if (v.sh_tiles > 0) v.pre_tiles = prefix_span<KT>(g, v.sh_tiles, v.min_len).count();
     }
   }
-  const int pre_total = v.pre_tiles * g.nrp * g.nkv;
-  int c = 0;
-  for (int rt = 0; rt < g.nrt; ++rt) c += span_of<KT>(g, P, rows, rt, v.sh_tiles).count();
-  c *= g.nkv;
+  const int pre_total = pre_positions(g, v.pre_tiles);
+  const int c0 = positions_of<KT>(g, P0, rows0, v.sh_tiles);
+  int c = c0;
+  for (int b = b0 + 1; b < b1; ++b) c += positions_of<KT>(g, paged_len(g, b), paged_rows(g, b), v.sh_tiles);
   int inc = c;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
-  const int at = pre_total + inc - c;
+  int at = pre_total + inc - c;
   v.T = pre_total + __shfl_sync(0xffffffffu, inc, 31);
   v.quota = max(g.min_quota, (int)((unsigned)(v.T + g.grid - 1) / (unsigned)g.grid));
   const int start = max((int)min((long long)blockIdx.x * v.quota, (long long)v.T), pre_total);
-  const unsigned here = __ballot_sync(0xffffffffu, start >= at && start < at + c);
-  v.b = here ? __ffs(here) - 1 : g.batch;
-  v.cum = __shfl_sync(0xffffffffu, at, here ? v.b : 0);
-  if (write && blockIdx.x == 0) {
-    if (rows > 0 && P > g.cap - rows) set_status(g.status, DFLASH_STATUS_CAPACITY);
-    if (g.shared) {
-      if (in) g.plan[kPlanCum + lane] = at;
-      if (lane == 0) {
-        g.plan[kPlanT] = v.T;
-        g.plan[kPlanQuota] = v.quota;
-        g.plan[kPlanShared] = v.sh_tiles;
-        g.plan[kPlanPre] = v.pre_tiles;
+  write = write && blockIdx.x == 0;
+  int hit = start >= at && start < at + c0 ? b0 : -1, hit_at = at;
+  if (per > 1 || write) {
+    for (int b = b0; b < b1; ++b) {
+      const int n = b == b0 ? c0 : positions_of<KT>(g, paged_len(g, b), paged_rows(g, b), v.sh_tiles);
+      if (start >= at && start < at + n) {
+        hit = b;
+        hit_at = at;
       }
+      if (write) {
+        if (g.shared) g.plan[kPlanCum + b] = at;
+        if (paged_rows(g, b) > 0 && paged_len(g, b) > g.cap - paged_rows(g, b))
+          set_status(g.status, DFLASH_STATUS_CAPACITY);
+      }
+      at += n;
     }
+  }
+  const unsigned here = __ballot_sync(0xffffffffu, hit >= 0);
+  const int src = here ? __ffs(here) - 1 : 0;
+  v.b = __shfl_sync(0xffffffffu, hit, src);
+  v.cum = __shfl_sync(0xffffffffu, hit_at, src);
+  if (!here) v.b = g.batch;
+  if (write && g.shared && lane == 0) {
+    g.plan[kPlanT] = v.T;
+    g.plan[kPlanQuota] = v.quota;
+    g.plan[kPlanShared] = v.sh_tiles;
+    g.plan[kPlanPre] = v.pre_tiles;
   }
   return v;
 }
@@ -224,7 +268,7 @@ __device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write) {
 template <int KT, int NT>
 __device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red, bool write = true) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (g.batch <= 32) return plan_small<KT>(g, write && tid < 32);
+  if (g.batch <= kPlanSmall) return plan_small<KT>(g, write && tid < 32);
   const bool first_cta = write && blockIdx.x == 0;
   PlanView v;
   const int per = (g.batch + NT - 1) / NT;
@@ -259,12 +303,8 @@ __device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red, bool
     __syncthreads();
   }
   v.pre_tiles = v.sh_tiles > 0 ? prefix_span<KT>(g, v.sh_tiles, v.min_len).count() : 0;
-  const int pre_total = v.pre_tiles * g.nrp * g.nkv;
-  auto tiles_of = [&](int b) {
-    int c = 0;
-    for (int rt = 0; rt < g.nrt; ++rt) c += suffix_span<KT>(g, b, rt, v.sh_tiles).count();
-    return c * g.nkv;
-  };
+  const int pre_total = pre_positions(g, v.pre_tiles);
+  auto tiles_of = [&](int b) { return positions_of<KT>(g, paged_len(g, b), paged_rows(g, b), v.sh_tiles); };
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
     sum += tiles_of(b);
@@ -329,7 +369,7 @@ struct SegmentWalk {
   __device__ __forceinline__ void start() {
     pos = (int)min((long long)blockIdx.x * v.quota, (long long)v.T);
     end = (int)min((long long)pos + v.quota, (long long)v.T);
-    pre_total = v.pre_tiles * g.nrp * g.nkv;
+    pre_total = pre_positions(g, v.pre_tiles);
     b = v.b;
     item_at = v.cum;
     rt = hk = 0;
@@ -338,22 +378,22 @@ struct SegmentWalk {
   // The item at `pos` (which lies in it, or where it begins).
   __device__ __forceinline__ bool item(Segment& s) {
     if (pos < pre_total) {
-      const int k = pos / v.pre_tiles;
+      const int len = item_len(v.pre_tiles, g.w_p, g.oh_p), k = (int)((unsigned)pos / (unsigned)len);
       s.prefix = true;
       s.hk = k / g.nrp;
       s.rt = k - s.hk * g.nrp;
       s.b = v.pre_b;
       s.span = prefix_span<KT>(g, v.sh_tiles, v.min_len);
-      s.total = v.pre_tiles;
-      s.line = k * v.pre_tiles;
+      s.at = Span1{k * len, v.pre_tiles, g.w_p, g.oh_p};
       s.ordinal = k;
     } else {
       TileSpan sp;
-      int c;
+      int c, tiles;
       while (true) {  // (pos < T: some item holds it, unless the lengths changed since the plan)
         if (b >= g.batch) return false;
         sp = suffix_span<KT>(g, b, rt, v.sh_tiles);
-        c = sp.count();
+        tiles = sp.count();
+        c = item_len(tiles, g.w_s, g.oh_s);
         if (pos < item_at + c * g.nkv) break;
         item_at += c * g.nkv;
         if (++rt == g.nrt) {
@@ -367,8 +407,7 @@ struct SegmentWalk {
       s.rt = rt;
       s.hk = hk;
       s.span = sp;
-      s.total = c;
-      s.line = item_at + hk * c;
+      s.at = Span1{item_at + hk * c, tiles, g.w_s, g.oh_s};
       s.ordinal = (b * g.nrt + rt) * g.nkv + hk;
     }
     return true;
@@ -376,16 +415,17 @@ struct SegmentWalk {
   __device__ __forceinline__ bool next(Segment& s) {
     while (pos < end) {
       if (!item(s)) return false;
-      if (at_start) {  // the run's first cut
-        at_start = false;
-        pos = cut_at(pos, s.line, s.total, v.quota);
-        if (pos == s.line + s.total) continue;
+      s.t0 = at_start ? cut_at(pos, s.at, v.quota) : 0;  // (the run's first cut)
+      at_start = false;
+      const int to = end < s.at.end() ? cut_at(end, s.at, v.quota) : s.at.total;
+      const bool last = end <= s.at.end();
+      pos = last ? end : s.at.end();
+      s.total = s.at.total;
+      s.nt = to - s.t0;
+      if (s.nt <= 0) {
+        if (last) return false;
+        continue;
       }
-      const int stop = end < s.line + s.total ? cut_at(end, s.line, s.total, v.quota) : s.line + s.total;
-      if (stop <= pos) return false;  // (the last cut lies where this item begins)
-      s.t0 = pos - s.line;
-      s.nt = stop - pos;
-      pos = stop;
       const long long slot = (long long)s.ordinal + blockIdx.x;
       s.slot_row = s.prefix ? g.pre_row0 + slot * g.slot_p : slot * g.slot_s;
       return true;
@@ -393,7 +433,7 @@ struct SegmentWalk {
     return false;
   }
   __device__ __forceinline__ int pieces(const Segment& s, int& c0) const {
-    return pieces_of(s.line, s.total, v.quota, c0);
+    return pieces_of(s.at, v.quota, c0);
   }
   // No other piece contributes to this one's rows.
   __device__ __forceinline__ bool whole(const Segment& s) const {

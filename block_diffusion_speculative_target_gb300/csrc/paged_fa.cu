@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = *tslot;
   pdl_launch();
   PlanView pv;
-  if (g.batch > 32) {  // a larger batch is planned by the whole block
+  if (g.batch > kPlanSmall) {  // a larger batch is planned by the whole block
     pdl_wait();
     pv = plan_view<KT, kTcThreads>(g, red);
   }
@@ -567,37 +567,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       __syncwarp();
     } else {
       // ---------------------------------------------------------- pieces, query rows
-      bool ok = true, more = false;
+      bool ok = true;
       SegmentWalk<KT> walk(g, pv);
       Segment sg;
-      if (g.batch <= 32) {
-        // The plan and the first step of the walk run twice, the first time on whatever the lengths hold while
-        // the previous kernel ends: nothing can start before these few hundred instructions, and fetching them
-        // takes three to four times as long as running them once they are there.
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-          if (pass) pdl_wait();
-          pv = plan_small<KT>(g, pass != 0);
+      const bool small = g.batch <= kPlanSmall;
+      // One pass ahead (seg -1) runs the plan and the first piece on whatever the lengths hold while the previous
+      // kernel ends, and leaves nothing: no role can start before these few hundred instructions, and fetching
+      // them takes three to four times as long as running them once they are there.
+      for (seg = small ? -1 : 0; ok; ++seg) {
+        if (seg <= 0) {
+          if (seg == 0) pdl_wait();
+          if (small) pv = plan_small<KT>(g, seg == 0);
           walk.start();
-          more = walk.next(sg);
         }
-      } else {
-        walk.start();
-        more = walk.next(sg);
-      }
-      if (NR != 16 && !g.shared && lane == 0) {
-        // the item that this CTA's run begins inside of, when it is the second to hold a piece of it
-        int c0 = 0, nc = 0;
-        if (more && sg.t0 > 0) nc = walk.pieces(sg, c0);
-        if (c0 + 1 != blockIdx.x) nc = 0;
-        int4* rec = reinterpret_cast<int4*>(g.records) + 2 * blockIdx.x;
-        rec[0] = make_int4(nc, sg.b, sg.rt, sg.hk);
-        rec[1].x = c0;
-      }
-      bool ended = false;
-      auto publish = [&](int s) {
-        if (ended) return true;
-        if (s >= 4 && stop(wait_phase(&pc_empty[s & 3], (uint32_t)((s >> 2) - 1) & 1u, abort_f, g.status))) return false;
+        const bool more = walk.next(sg);
         Piece pc = {};
         if (more) {
           pc.nt = sg.nt;
@@ -629,23 +612,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           } else if (g.window > 0) {
             pc.all_hi = 0;
           }
-          if (pv.pre_tiles == 0) pc.nc = walk.pieces(sg, pc.c0);
+          if (NR == 16 && pv.pre_tiles == 0 && !pc.whole) pc.nc = walk.pieces(sg, pc.c0);  // (who joins here)
           pc.slot_row = sg.slot_row;
         }
+        if (seg < 0) {
+          asm volatile("" ::"r"(pc.nt), "r"(pc.rows), "r"(pc.all_lo), "r"(pc.all_hi), "r"(pc.key_end), "r"(pc.nc),
+                       "r"(pc.whole));  // (computed here too)
+          continue;
+        }
+        if (seg >= 4) ok = !stop(wait_phase(&pc_empty[seg & 3], (uint32_t)((seg >> 2) - 1) & 1u, abort_f, g.status));
+        if (!ok) break;
         if (lane == 0) {
-          pieces[s & 3] = pc;
-          mbar_arrive(&pc_full[s & 3]);
+          pieces[seg & 3] = pc;
+          mbar_arrive(&pc_full[seg & 3]);
         }
         __syncwarp();
-        ended = !more;
-        if (more) more = walk.next(sg);
-        return true;
-      };
-      int next = 1;  // pieces published: two ahead of the one whose rows are brought
-      ok = publish(0);
-      for (; ok; ++seg) {
-        const Piece& pc = pieces[seg & 3];
-        if (pc.nt == 0) break;
+        if (NR != 16 && seg == 0 && !g.shared) {
+          // the item that this CTA's run begins inside of, when it is the second to hold a piece of it
+          int c0 = 0, nc = 0;
+          if (more && sg.t0 > 0) nc = walk.pieces(sg, c0);
+          if (c0 + 1 != blockIdx.x) nc = 0;
+          int4* rec = reinterpret_cast<int4*>(g.records) + 2 * blockIdx.x;
+          if (lane == 0) {
+            rec[0] = make_int4(nc, sg.b, sg.rt, sg.hk);
+            rec[1].x = c0;
+          }
+        }
+        if (!more) break;
         const int rows = pc.rows;
         const bool cols = as_columns(pc.prefix), two = !cols && pc.two;
         for (int w = 0; ok && w < (two ? 2 : 1); ++w) {
@@ -697,7 +690,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ++used;
         }
         if (!two) qt ^= 1;
-        for (; ok && next <= seg + 2; ++next) ok = publish(next);
       }
     }
   } else {
@@ -1446,6 +1438,11 @@ static cudaError_t tc_launch(PagedGeom g, const CUtensorMap& tk, const CUtensorM
   }
   // items of two query tiles where there are rows for them
   const int ri = g.n * g.G > 128 ? 256 : 128, rp = g.batch * g.n * g.G > 128 ? 256 : 128;
+  // A tile takes two positions of the line, an item's start and end the time of two tiles more: with 0 instead,
+  // 8 prompts' first 128 rows take 36.0 us (28.0 so), 64 tokens behind a common 12K 119 (107), 128 rows behind
+  // 36K 130 (126); only a window's pieces (15 rows, 34 tiles an item) lose, 80.7 (82.9).
+  g.w_s = g.w_p = 2;
+  g.oh_s = g.oh_p = 4;
   if (paged_split(g, ri, rp, num_sms(), 2) > part_rows) return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
   DFL_RET(launch_pdl(paged_attn_tc_kernel<HD, NR, TS, TP>, dim3(g.grid), dim3(kTcThreads), L::kSmem, s, tk, tv, g,
