@@ -31,25 +31,42 @@ cudaError_t rope_table(float2* tab, int max_pos, int half, double theta) {
 // ------------------------------------------------------------------ append
 // Row (b, j) of the packed q|k|v rows at position p = len[b] + j: q and k are
 // rotated in float32 (x_lo c - x_hi s, x_hi c + x_lo s), rounded once, and q
-// goes to q_out, k and v to slot p mod ps of page table[b][p / ps].  A thread
-// moves 8 entries of a head's lower half and the 8 they rotate with.
+// goes to q_out, k and v to slot p mod ps of page table[b][p / ps].
+//
+// Bound by the rows' bytes, in and out.  A thread moves 8 entries of the lower
+// half and the 8 they rotate with, of HPT heads of one row: their (cos, sin)
+// pairs, twice the bytes of a bf16 head's 16 entries, are fetched once for all
+// of them, and all their loads are in flight together.  Blocks take `rpb` whole
+// rows.  HPT = 1 where the rows do not fill the GPU: more threads, shorter ones.
+// 16384 rows of 40 + 2 x 8 heads of 128 in bf16: 79.9 us, 5.88 TB/s of 6.78 that a
+// copy reaches (one head a thread, (cos, sin) fetched for each: 96.6 us).
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
-  if (vec && sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else if (vec) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&a);
+struct Raw8 {  // 8 entries as they lie in memory
+  uint4 v[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p, bool vec) {
+  Raw8<T> r;
+  if (vec) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = __bfloat1622float2(h[e]);
-      x[2 * e] = f.x;
-      x[2 * e + 1] = f.y;
-    }
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = *(reinterpret_cast<const uint4*>(p) + i);
   } else {
+    T x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = to_f<T>(p[e]);
+    for (int e = 0; e < 8; ++e) x[e] = p[e];
+    memcpy(&r, x, sizeof(r));
+  }
+  return r;
+}
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&x)[8]) { memcpy(x, &r, sizeof(r)); }
+__device__ __forceinline__ void unpack8(const Raw8<bf16>& r, float (&x)[8]) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = __bfloat1622float2(h[e]);
+    x[2 * e] = f.x;
+    x[2 * e + 1] = f.y;
   }
 }
 
@@ -67,59 +84,76 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   }
 }
 
-template <typename TI, typename T>
+template <typename TI, typename T, int HPT>
 __global__ void __launch_bounds__(256)
-    paged_append_kernel(const TI* __restrict__ qkv, long long ld, int vec, int batch, int n, int nq, int nkv, int hd,
-                        const int32_t* __restrict__ n_rows, const int32_t* __restrict__ table, int table_stride,
-                        const int32_t* __restrict__ len, const float2* __restrict__ tab, int max_pos, int n_pages,
-                        int ps, long long page0, T* __restrict__ qout, T* __restrict__ kp, T* __restrict__ vp,
-                        int* status) {
-  const int half = hd / 2, per_head = half / 8;
-  const int per_row = (nq + 2 * nkv) * per_head;
-  const long long total = (long long)batch * n * per_row;
+    paged_append_kernel(const TI* __restrict__ qkv, long long ld, int vec, int rows, int n, int nq, int nkv, int hd,
+                        int rpb, const int32_t* __restrict__ n_rows, const int32_t* __restrict__ table,
+                        int table_stride, const int32_t* __restrict__ len, const float2* __restrict__ tab, int max_pos,
+                        int n_pages, int ps_log2, long long page0, T* __restrict__ qout, T* __restrict__ kp,
+                        T* __restrict__ vp, int* status) {
+  const int half = hd / 2, lanes = half / 8, heads = nq + 2 * nkv;
+  const int groups = (heads + HPT - 1) / HPT;  // group hg takes heads hg, hg + groups, ..
+  const int per_row = groups * lanes;
+  const int r0 = blockIdx.x * rpb, items = min(rpb, rows - r0) * per_row;
   pdl_launch();
   pdl_wait();
-  for (long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x; t < total;
-       t += (long long)gridDim.x * blockDim.x) {
-    const int r = (int)(t / per_row), w = (int)(t - (long long)r * per_row);
+  for (int t = threadIdx.x; t < items; t += 256) {
+    const int rr = t / per_row, w = t - rr * per_row, r = r0 + rr;
     const int b = r / n, j = r - b * n;
     if (n_rows && j >= n_rows[b]) continue;
-    const int h = w / per_head, e = (w - h * per_head) * 8;
+    const int hg = w / lanes, e = (w - hg * lanes) * 8;
+    const TI* src = qkv + (long long)r * ld + e;
+    Raw8<TI> lo[HPT], hi[HPT];
+#pragma unroll
+    for (int x = 0; x < HPT; ++x) {
+      const int h = hg + x * groups;
+      if (h < heads) {
+        lo[x] = load8<TI>(src + h * hd, vec);
+        hi[x] = load8<TI>(src + h * hd + half, vec);
+      }
+    }
     const long long pos = (long long)len[b] + j;
-    if (pos < 0 || pos >= max_pos || pos / ps >= table_stride) {
+    if (pos < 0 || pos >= max_pos || (pos >> ps_log2) >= table_stride) {
       if (w == 0) set_status(status, DFLASH_STATUS_CAPACITY);
       continue;
     }
-    const TI* src = qkv + (long long)r * ld + h * hd + e;
-    float lo[8], hi[8];
-    load8<TI>(src, vec, lo);
-    load8<TI>(src + half, vec, hi);
-    if (h < nq + nkv) {
-      const float4* cs = reinterpret_cast<const float4*>(tab + pos * half + e);
+    const int page = table[(long long)b * table_stride + (pos >> ps_log2)];
+    const bool good = (unsigned)page < (unsigned)n_pages;
+    if (!good && w == 0) set_status(status, DFLASH_STATUS_BOUNDS);
+    const float4* cs = reinterpret_cast<const float4*>(tab + pos * half + e);
+    float4 c[4];  // two (cos, sin) pairs each
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float4 c = cs[x];  // two (cos, sin) pairs
-        const float a0 = lo[2 * x], b0 = hi[2 * x], a1 = lo[2 * x + 1], b1 = hi[2 * x + 1];
-        lo[2 * x] = a0 * c.x - b0 * c.y;
-        hi[2 * x] = b0 * c.x + a0 * c.y;
-        lo[2 * x + 1] = a1 * c.z - b1 * c.w;
-        hi[2 * x + 1] = b1 * c.z + a1 * c.w;
+    for (int x = 0; x < 4; ++x) c[x] = __ldg(cs + x);
+    // slot (pos mod ps) of the page's first head
+    const long long slot = (((page0 + page) * nkv) << ps_log2) + (pos & ((1 << ps_log2) - 1));
+#pragma unroll
+    for (int x = 0; x < HPT; ++x) {
+      const int h = hg + x * groups;
+      if (h >= heads) break;
+      float a[8], z[8];
+      unpack8(lo[x], a);
+      unpack8(hi[x], z);
+      if (h < nq + nkv) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float a0 = a[2 * y], z0 = z[2 * y], a1 = a[2 * y + 1], z1 = z[2 * y + 1];
+          a[2 * y] = a0 * c[y].x - z0 * c[y].y;
+          z[2 * y] = z0 * c[y].x + a0 * c[y].y;
+          a[2 * y + 1] = a1 * c[y].z - z1 * c[y].w;
+          z[2 * y + 1] = z1 * c[y].z + a1 * c[y].w;
+        }
       }
-    }
-    T* dst;
-    if (h < nq) {
-      dst = qout + ((long long)r * nq + h) * hd;
-    } else {
-      const int page = table[(long long)b * table_stride + pos / ps];
-      if ((unsigned)page >= (unsigned)n_pages) {
-        set_status(status, DFLASH_STATUS_BOUNDS);
-        continue;
+      T* dst;
+      if (h < nq) {
+        dst = qout + ((long long)r * nq + h) * hd;
+      } else {
+        if (!good) break;  // (heads ascend: keys and values only from here on)
+        const int hk = h - nq < nkv ? h - nq : h - nq - nkv;
+        dst = (h - nq < nkv ? kp : vp) + (slot + ((long long)hk << ps_log2)) * hd;
       }
-      const int hk = h - nq < nkv ? h - nq : h - nq - nkv;
-      dst = (h - nq < nkv ? kp : vp) + ((((page0 + page) * nkv) + hk) * ps + pos % ps) * hd;
+      store8<T>(dst + e, a);
+      store8<T>(dst + e + half, z);
     }
-    store8<T>(dst + e, lo);
-    store8<T>(dst + e + half, hi);
   }
 }
 
@@ -129,12 +163,20 @@ cudaError_t paged_append(int in_dtype, int dtype, const void* qkv, long long ld,
                          void* vp, int* status, cudaStream_t s) {
   const size_t es = in_dtype == DFLASH_BF16 ? 2 : 4;
   const int vec = (reinterpret_cast<uintptr_t>(qkv) & 15) == 0 && (ld * es) % 16 == 0;
-  const long long total = (long long)batch * n * (nq + 2 * nkv) * (hd / 16);
-  const unsigned grid = (unsigned)std::min<long long>((total + 255) / 256, (long long)num_sms() * 64);
-#define DFL_APPEND(TI, T)                                                                                            \
-  DFL_RET(launch_pdl(paged_append_kernel<TI, T>, dim3(grid), dim3(256), 0, s, (const TI*)qkv, ld, vec, batch, n, nq, \
-                     nkv, hd, n_rows, table, table_stride, len, tab, max_pos, n_pages, ps, page0, (T*)qout, (T*)kp,  \
-                     (T*)vp, status))
+  const int rows = batch * n, heads = nq + 2 * nkv, lanes = hd / 16, ps_log2 = 31 - __builtin_clz(ps);
+  const bool many = (long long)rows * heads * lanes >= (long long)num_sms() * 2048 * 4;
+  const int per_row = (heads + (many ? 3 : 0)) / (many ? 4 : 1) * lanes;
+  const int rpb = many ? std::max(1, 1024 / per_row) : 1;
+  const unsigned grid = (unsigned)((rows + (long long)rpb - 1) / rpb);
+#define DFL_APPEND_H(TI, T, H)                                                                                        \
+  DFL_RET(launch_pdl(paged_append_kernel<TI, T, H>, dim3(grid), dim3(256), 0, s, (const TI*)qkv, ld, vec, rows, n, nq, \
+                     nkv, hd, rpb, n_rows, table, table_stride, len, tab, max_pos, n_pages, ps_log2, page0, (T*)qout,  \
+                     (T*)kp, (T*)vp, status))
+#define DFL_APPEND(TI, T)      \
+  if (many)                    \
+    DFL_APPEND_H(TI, T, 4);    \
+  else                         \
+    DFL_APPEND_H(TI, T, 1)
   if (dtype == DFLASH_F32) {
     DFL_APPEND(float, float);
   } else if (in_dtype == DFLASH_F32) {
@@ -143,6 +185,7 @@ cudaError_t paged_append(int in_dtype, int dtype, const void* qkv, long long ld,
     DFL_APPEND(bf16, bf16);
   }
 #undef DFL_APPEND
+#undef DFL_APPEND_H
   count_launch();
   return cudaSuccess;
 }
@@ -208,32 +251,42 @@ __global__ void __launch_bounds__(kCoreThreads)
     }
     const int key_lo = sg.prefix ? 0 : v.sh_tiles * kCoreKeys;  // keys below belong to the shared prefix
     const int key_end = sg.prefix ? v.sh_tiles * kCoreKeys : key_limit(g, sg.b);
+    // 8 threads a key: its rows of keys and values (past the sequence's keys, or in a bad page: zeros), fetched into
+    // registers while the tile before is worked on
+    Raw8<T> rk[HD / 64], rv[HD / 64];
+    auto fetch = [&](int t) {
+      const int key = sg.span.tile(t) * kCoreKeys + (tid >> 3), part = tid & 7;
+      int page = -1;
+      if (key < key_end) {
+        page = g.table[(long long)sg.b * g.table_stride + (key >> g.ps_log2)];
+        if ((unsigned)page >= (unsigned)g.n_pages) {
+          page = -1;
+          set_status(g.status, DFLASH_STATUS_BOUNDS);
+        }
+      }
+      const long long at = (g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps + (key & (g.ps - 1))) * HD + part * 8;
+#pragma unroll
+      for (int e = 0; e < HD / 64; ++e) {
+        rk[e] = rv[e] = Raw8<T>{};
+        if (page >= 0) {
+          rk[e] = load8<T>(kp + at + e * 64, true);
+          rv[e] = load8<T>(vp + at + e * 64, true);
+        }
+      }
+    };
+    fetch(sg.t0);
     for (int t = sg.t0; t < sg.t0 + sg.nt; ++t) {
       const int k0 = sg.span.tile(t) * kCoreKeys;
       __syncthreads();
-      {  // 8 threads a key: its rows of keys and values (past the sequence's keys, or in a bad page: zeros)
-        const int key = k0 + (tid >> 3), part = tid & 7;
-        int page = -1;
-        if (key < key_end) {
-          page = g.table[(long long)sg.b * g.table_stride + (key >> g.ps_log2)];
-          if ((unsigned)page >= (unsigned)g.n_pages) {
-            page = -1;
-            set_status(g.status, DFLASH_STATUS_BOUNDS);
-          }
-        }
-        const long long at =
-            page < 0 ? 0 : (g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps + (key & (g.ps - 1))) * HD;
 #pragma unroll
-        for (int e = part * 8; e < HD; e += 64) {
-          float xk[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, xv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (page >= 0) {
-            load8<T>(kp + at + e, true, xk);
-            load8<T>(vp + at + e, true, xv);
-          }
-          store8<float>(sk + (tid >> 3) * L::kRow + e, xk);
-          store8<float>(sv + (tid >> 3) * HD + e, xv);
-        }
+      for (int e = 0; e < HD / 64; ++e) {
+        float x[8];
+        unpack8(rk[e], x);
+        store8<float>(sk + (tid >> 3) * L::kRow + (tid & 7) * 8 + e * 64, x);
+        unpack8(rv[e], x);
+        store8<float>(sv + (tid >> 3) * HD + (tid & 7) * 8 + e * 64, x);
       }
+      if (t + 1 < sg.t0 + sg.nt) fetch(t + 1);
       __syncthreads();
       float s[MRM][2];
 #pragma unroll
@@ -453,7 +506,8 @@ static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const
     per_sm = std::min(std::max(x, 1), kPagedMaxCtas);
   }
   g.w_s = g.w_p = 1;
-  if (paged_split(g, L::MR, L::MR, num_sms() * per_sm, 4) > part_rows) return cudaErrorInvalidValue;
+  // runs of two tiles at least: 4 blocks of 16 rows over up to 1K keys take 17.4 us, 22.4 in runs of four
+  if (paged_split(g, L::MR, L::MR, num_sms() * per_sm, 2) > part_rows) return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
   DFL_RET(launch_pdl(paged_attn_core_kernel<T, HD, MRM>, dim3(g.grid), dim3(kCoreThreads), L::kSmem, s, g, (const T*)q,
                      (const T*)kp, (const T*)vp, (T*)out, scale_log2));
