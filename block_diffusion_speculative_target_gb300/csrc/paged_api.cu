@@ -48,6 +48,10 @@ static bool on_device(int device) {
   return cudaGetDevice(&d) == cudaSuccess && d == device;
 }
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+static bool apart(const void* a, long long abytes, const void* b, long long bbytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x + (uintptr_t)abytes <= y || y + (uintptr_t)bbytes <= x;
+}
 
 extern "C" {
 
@@ -160,11 +164,12 @@ int dflash_paged_workspace_free(dflash_paged_workspace* w) {
 int dflash_paged_status(dflash_paged_workspace* w, dflash_stream_t stream, int32_t* status_out) {
   REQ(w && status_out);
   int32_t v = 0;
-  CK(cudaStreamSynchronize((cudaStream_t)stream));
-  CK(cudaMemcpy(&v, w->status, 4, cudaMemcpyDeviceToHost));
-  CK(cudaMemset(w->status, 0, 4));
+  const cudaStream_t s = (cudaStream_t)stream;
+  CK(cudaMemcpyAsync(&v, w->status, 4, cudaMemcpyDeviceToHost, s));
+  CK(cudaMemsetAsync(w->status, 0, 4, s));  // (in the stream's order: the next call's bits stay)
+  CK(cudaStreamSynchronize(s));
   // a call that timed out may have left pieces counted
-  if (v & DFLASH_STATUS_TIMEOUT) CK(cudaMemset(w->tickets, 0, w->ticket_bytes));
+  if (v & DFLASH_STATUS_TIMEOUT) CK(cudaMemsetAsync(w->tickets, 0, w->ticket_bytes, s));
   *status_out = v;
   return DFLASH_OK;
 }
@@ -178,6 +183,9 @@ int dflash_paged_append(dflash_pages* p, int32_t layer, int32_t in_dtype, const 
   const int nq = q_out ? p->nq : 0;
   REQ(ld >= (long long)(nq + 2 * p->nkv) * p->hd && aligned16(q_out));
   REQ((reinterpret_cast<uintptr_t>(qkv) & (in_dtype == DFLASH_F32 ? 3 : 1)) == 0);
+  const long long rows = (long long)batch * n, width = (long long)(nq + 2 * p->nkv) * p->hd;
+  REQ(!q_out || apart(qkv, ((rows - 1) * ld + width) * (in_dtype == DFLASH_F32 ? 4 : 2), q_out,
+                      rows * p->nq * p->hd * (p->dtype == DFLASH_F32 ? 4 : 2)));
   REQ(on_device(p->device) && ws->device == p->device);
   CK(paged_append(in_dtype, p->dtype, qkv, ld, batch, n, nq, p->nkv, p->hd, n_rows, table, table_stride, len, p->rope,
                   p->max_pos, p->n_pages, p->page_size, (long long)layer * p->n_pages, q_out, p->k, p->v, ws->status,
@@ -194,6 +202,8 @@ static int attend(dflash_pages* p, int32_t layer, const void* q, int32_t batch, 
   REQ(batch <= ws->max_batch && (long long)batch * n <= ws->max_rows);
   REQ(ws->nq == p->nq && ws->nkv == p->nkv && ws->hd == p->hd);
   REQ(aligned16(q) && aligned16(out));
+  const long long q_bytes = (long long)batch * n * p->nq * p->hd * (p->dtype == DFLASH_F32 ? 4 : 2);
+  REQ(apart(q, q_bytes, out, q_bytes));
   REQ(on_device(p->device) && ws->device == p->device);
   if ((long long)table_stride * p->page_size > (1ll << 30)) return DFLASH_ERR_TOO_LARGE;
   PagedGeom g = {};

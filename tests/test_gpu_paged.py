@@ -589,7 +589,42 @@ def test_results_at_sixteen_bytes():
     check(x, first, reference(x, q))
 
 
+def test_status_in_stream_order():
+    """Reading the status on another stream than the default one clears it before the next call's bits, not after."""
+    x = Batch("bf16", 4, 1, 128, 16, [300, 200], 2)
+    q = x.query()
+    out = torch.zeros_like(q)
+    bad = x.table.clone()
+    bad[0, 3] = -1
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for _ in range(50):
+            x.cache.attention(0, q, bad, x.len, out)
+            assert x.cache.status() == capi.STATUS_BOUNDS
+        assert x.cache.status() == 0
+
+
 # ------------------------------------------------------------------ refusals
+
+
+def test_overlapping_memory_is_refused():
+    x = Batch("bf16", 4, 1, 128, 16, [40, 5], 4)
+    buf = torch.zeros(2, *x.query().shape, dtype=x.dt, device="cuda")
+    flat = buf.view(-1)
+    size = buf[0].numel()
+    for at in (0, 8, size - 8):
+        with pytest.raises(capi.DFlashError) as e:
+            x.cache.attention(0, flat[:size].view(buf[0].shape), x.table, x.len, flat[at:at + size].view(buf[0].shape))
+        assert e.value.code == capi.ERR_INVALID_ARG
+    x.cache.attention(0, buf[0], x.table, x.len, buf[1])
+    rows = torch.zeros(8 * 6 * 128 + size, dtype=x.dt, device="cuda")
+    qkv, width = rows[:8 * 6 * 128].view(8, 6 * 128), 8 * 6 * 128
+    for at in (0, 8, width - 8):
+        with pytest.raises(capi.DFlashError) as e:
+            x.cache.append(0, qkv, x.table, x.len, 4, q_out=rows[at:at + size].view(buf[0].shape))
+        assert e.value.code == capi.ERR_INVALID_ARG
+    x.cache.append(0, qkv, x.table, x.len, 4, q_out=rows[width:].view(buf[0].shape))
+    assert x.cache.status() == 0
 
 
 def test_refusals():
