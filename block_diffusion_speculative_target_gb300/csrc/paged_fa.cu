@@ -10,17 +10,18 @@
 // p = 2^(s - M) <= 2^8.  An item runs in one of two layouts:
 //
 // rows as columns (at most 64 stacked rows: single tokens, blocks)
-//   S = K_t Q^T            128 keys by NR = 16 or 32 rows: a thread holds a key's scores
+//   S = K_t Q^T            128 keys by NR = 16, 32 or 64 rows: a thread holds a key's scores
 //   O += V_t^T P           dims by rows, both operands from shared memory
 //   The products' M dimension is filled with keys and dimensions, so few rows
 //   cost few columns, and all 128 threads of a group share the exponentials of
 //   however few rows there are.  Whether a row's reference has to move is one
 //   vote a tile.  With 16 rows P is kept as a bf16 pair hi + lo in neighbouring
-//   columns (about 2^-17 relative), which is free where keys are waited for; with
-//   32 it would double the work on a weight, and P is rounded once.  S has two buffers, and K runs ahead of
-//   V in the ring: the next scores are there before a tile's weights are done.
-//   Items of more than NR rows give each group half of them and every key tile;
-//   others are one block of rows whose key tiles the groups take in turn.
+//   columns (2^-16 relative), which is free where keys are waited for; with 32 it
+//   would double the work on a weight, and P is rounded once.  S has two buffers,
+//   and K runs ahead of V in the ring: the next scores are there before a tile's
+//   weights are done.  An item is one block of rows, whose key tiles the groups
+//   take in turn (a shared prefix's of more than NR rows: half of them each, and
+//   every key tile).
 // rows as rows (more rows: chunks, shared prefixes)
 //   S = Q K_t^T            128 rows by 64 keys (half a tile), two buffers: a thread
 //                          holds one row
@@ -28,7 +29,7 @@
 //   An item of at most 128 rows has one query tile, whose key tiles the groups
 //   take in turn; one of more rows has two, a group each, that share every key
 //   tile, which halves the traffic from L2.
-// P rounded to bf16 once is off by 2^-9 relative a weight, the size of the
+// P rounded to bf16 once is off by 2^-8 relative a weight, the size of the
 // result's own rounding; L sums the weights before it.  Where both groups work
 // on the same rows, their (M, L, O) are joined at the item's end.
 //
@@ -43,6 +44,17 @@
 // looks through the values first; a value that is not finite is taken out of
 // the tile and added with its weight to the accumulators of the rows that do
 // see it.
+//
+// What bounds it, measured on inputs larger than L2, us a call (bytes at a copy's
+// 6.78 TB/s, products at 1.92 PFLOP/s):
+//   32 sequences, one token, 512 to 36K keys, 40 / 8 heads   399 (381): the bytes
+//   one token over 4K keys, 32 / 8 heads                    16.4 (2.5): the start (plan, cold
+//     instructions, query rows), one piece of two or three tiles a CTA, joining the pieces
+//   8 blocks of 16 rows over 2K..6K keys, 32 / 8 heads      63.7 (22): 14 tiles a CTA at about 3.5 us, a
+//     group's chain of scores, vote, weights to shared memory and products of 32 rows each
+//   128 rows over 36K keys, 40 / 8 heads                     126 (51): 2.7 us a tile of 256 rows and 128 keys
+//     (products alone 1.3), a row's 128 exponentials by one thread
+// Rows as columns and not as rows for up to 64 rows: 128 rows' worth of exponentials would be computed for 4.
 //
 // Every wait is bounded; one that gives up sets DFLASH_STATUS_TIMEOUT, the CTA
 // stops, and drains its copies and products before it releases TMEM.
