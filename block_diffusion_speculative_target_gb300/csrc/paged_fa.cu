@@ -50,8 +50,8 @@
 //   32 sequences, one token, 512 to 36K keys, 40 / 8 heads   399 (381): the bytes
 //   one token over 4K keys, 32 / 8 heads                    16.4 (2.5): the start (plan, cold
 //     instructions, query rows), one piece of two or three tiles a CTA, joining the pieces
-//   8 blocks of 16 rows over 2K..6K keys, 32 / 8 heads      63.7 (22): 14 tiles a CTA at about 3.5 us, a
-//     group's chain of scores, vote, weights to shared memory and products of 32 rows each
+//   8 blocks of 16 rows over 2K..6K keys, 32 / 8 heads      61.3 (22): the start (20 us to the first weights,
+//     most of it instructions fetched from DRAM), 14 tiles a CTA, the piece (5), the joining kernel (8)
 //   128 rows over 36K keys, 40 / 8 heads                     126 (51): 2.7 us a tile of 256 rows and 128 keys
 //     (products alone 1.3), a row's 128 exponentials by one thread
 // Rows as columns and not as rows for up to 64 rows: 128 rows' worth of exponentials would be computed for 4.
@@ -780,11 +780,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       return true;
     };
-    pdl_wait();
-    ok = wait_piece(0);
+    // While the first piece is planned and brought, the code of a first tile in the rows-as-columns layout is run
+    // once on whatever TMEM holds: fetching its instructions costs several times what running them does.  Nothing
+    // of it stays: the waits, the arrivals and the global reads are left out, and the first tile sets what it uses.
+    // 8 blocks of 16 rows over 2K..6K keys 63.3 -> 61.3 us, 15 rows in windows of 4K 82.6 -> 81.1.
+    int dry = 0;  // (where no item of the other layout comes first)
+    if constexpr (NR > 0 && TP) {
+      dry = 1;
+      asm volatile("" : "+r"(dry));  // (one copy of the code)
+    }
+    if (!dry) {
+      pdl_wait();
+      ok = wait_piece(0);
+    }
     // Prefix items come before suffix items, so those in the rows-as-rows layout (if any) come first.
     if constexpr (!TS || !TP) {
-      while (ok && pieces[seg & 3].nt > 0 && !as_columns(pieces[seg & 3].prefix)) {
+      while (ok && !dry && pieces[seg & 3].nt > 0 && !as_columns(pieces[seg & 3].prefix)) {
         // ------------------------------------------------ rows as rows: thread = stacked row
         const Piece& pc = pieces[seg & 3];
         const int nt = pc.nt, rows = pc.rows, key_lo = pc.key_lo, key_end = pc.key_end;
@@ -1041,11 +1052,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     if constexpr (NR > 0) {
-      while (ok && pieces[seg & 3].nt > 0) {
+      while (ok && (dry || pieces[seg & 3].nt > 0)) {
         // ------------------------------------------------ rows as columns: thread = key r of the tile
         const Piece& pc = pieces[seg & 3];
-        const int nt = pc.nt;
-        const bool two = pc.two, whole = pc.whole;
+        const int nt = dry ? 2 : pc.nt;
+        const bool two = !dry && pc.two, whole = pc.whole;
         const int rbase = two ? gq * NR : 0, rows = two ? min(NR, pc.rows - rbase) : pc.rows;  // the group's rows
         const int t0 = two ? 0 : gq, step = two ? 1 : 2, ahead = ahead_of(true, two);
         const bool has = t0 < nt, both = !two && nt > 1;
@@ -1068,17 +1079,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int c = 0; c < NR; ++c) Ls[c] = 0.f;
         if (!meet(&fix[gq], fn)) break;  // the scratch's last readers are past it
-        for (int t = t0; ok && t < nt; t += step) {
+        for (int t = t0; ok && t < nt; t += step) {  // (once when dry)
           const bool first = t == t0;
           const int k0 = pc.tile(t) * KT, key = k0 + r;
-          const bool inner = k0 >= pc.all_lo && k0 + KT <= pc.all_hi;
+          const bool inner = dry || (k0 >= pc.all_lo && k0 + KT <= pc.all_hi);
           const int sb = job & 1;  // score buffer
           uint32_t& sn = sb ? sn1 : sn0;
-          if (stop(wait_phase(&s_full[2 * gq + sb], sn & 1u, abort_f, g.status))) {
+          if (!dry && stop(wait_phase(&s_full[2 * gq + sb], sn & 1u, abort_f, g.status))) {
             ok = false;
             break;
           }
-          ++sn;
+          sn += !dry;
           // the last product has read P and left O to be changed
           bool pv_waited = first;
           auto wait_pv = [&]() {
@@ -1321,14 +1332,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           fence_proxy_async_smem();
-          if (first && r == 0) acc_first[gq] = first_acc;
+          if (first && !dry && r == 0) acc_first[gq] = first_acc;
           tc_fence_before();
           __syncwarp();
+          if (dry) break;
           if (lane == 0) mbar_arrive(&p_full[2 * gq + (job & 1)]);
           ++job;
           ++vjob;
         }
         if (!ok) break;
+        if (dry) {
+          dry = 0;
+          pdl_wait();
+          ok = wait_piece(0);
+          continue;
+        }
         // ---- the piece's end: row sums over the group, then group 0 joins both groups' parts
         float M = -INFINITY, Lr = 0.f;  // of row r (threads below NR)
         if (has) {
@@ -1461,7 +1479,9 @@ static cudaError_t tc_launch(PagedGeom g, const CUtensorMap& tk, const CUtensorM
                      (int)pool_rows, (const bf16*)q, (bf16*)out, scale_log2));
   count_launch();
   if (g.shared) return paged_merge_bf16(HD, g, out, s);
-  return NR == 16 ? cudaSuccess : paged_join_bf16(HD, g, out, s);  // (few rows: the CTAs join their pieces)
+  // The CTAs join their pieces where an item has up to 16 rows; beyond, one CTA's threads would take longer than a
+  // kernel over all items (8 blocks of 16 rows over 2K..6K keys: 75 us instead of 61).
+  return NR == 16 ? cudaSuccess : paged_join_bf16(HD, g, out, s);
 }
 
 template <int HD>
