@@ -390,7 +390,7 @@ struct SegmentWalk {
       TileSpan sp;
       int c, tiles;
       while (true) {  // (pos < T: some item holds it, unless the lengths changed since the plan)
-        if (b >= g.batch) return false;
+        if (b >= g.batch || pos < item_at) return false;
         sp = suffix_span<KT>(g, b, rt, v.sh_tiles);
         tiles = sp.count();
         c = item_len(tiles, g.w_s, g.oh_s);

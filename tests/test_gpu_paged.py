@@ -206,6 +206,57 @@ def test_append(c):
     assert ((x.k.double() - wk).abs() <= tk).all()
 
 
+MANY = [
+    # dtype, in, nq, nkv, hd, ps, lens, n, rows, queries, pad, shift
+    ("bf16", "bf16", 40, 8, 128, 128, [0, 5, 300], 1000, [1000, 0, 999], True, 0, 0),
+    ("bf16", "f32", 5, 1, 128, 16, [17, 4000], 11500, None, True, 0, 0),  # 7 heads: a group of one short
+    ("bf16", "bf16", 12, 3, 64, 32, [1, 70], 9000, [9000, 8191], True, 5, 3),  # rows read entry by entry
+    ("f32", "f32", 8, 2, 64, 64, [33], 26500, None, True, 0, 0),
+    ("bf16", "bf16", 9, 3, 128, 16, [9, 3], 13100, None, False, 0, 0),
+]
+
+
+@pytest.mark.parametrize("c", MANY, ids=[f"{c[0]}-{c[1]}-{c[2]}x{c[3]}x{c[4]}-p{c[5]}-n{c[7]}" for c in MANY])
+def test_append_many_rows(c):
+    """Enough rows that a thread takes several heads; one page of the first sequence is none."""
+    dtype, src, nq, nkv, hd, ps, lens, n, rows, queries, pad, shift = c
+    x = Batch(dtype, nq, nkv, hd, ps, lens, n, rows)
+    heads, B = (nq if queries else 0) + 2 * nkv, len(lens)
+    width = heads * hd
+    buf = x.normal(B * n * (width + pad) + shift, dtype=TDT[src])
+    qkv = buf[shift:].view(B * n, width + pad)[:, :width]
+    k0, v0 = x.k.clone(), x.v.clone()
+    q_out = torch.full((B, n, nq, hd), 77.0, dtype=x.dt, device="cuda") if queries else None
+    hole = (lens[0] + n // 2) // ps  # a column of the table
+    was = int(x.table[0, hole])
+    x.table[0, hole] = x.k.shape[1]
+    x.cache.append(0, qkv, x.table, x.len, n, q_out=q_out, n_rows=x.n_rows)
+    assert x.cache.status() == capi.STATUS_BOUNDS
+    x.table[0, hole] = was
+    z = qkv.double().view(B, n, heads, hd)
+    j = torch.arange(n, device="cuda")
+    pos = x.len[:, None].long() + j
+    live = j < (torch.full((B,), n, device="cuda") if rows is None else x.n_rows)[:, None]
+    turn = rotated(z[:, :, :heads - nkv], pos, hd)
+    # as above: four roundings of |x_lo| + |x_hi|, and the result's own
+    size = z.abs().view(B, n, heads, 2, hd // 2).sum(3, keepdim=True).expand(B, n, heads, 2, hd // 2).reshape(B, n, heads, hd)
+    tol = 4 * 2.0 ** -24 * size[:, :, :heads - nkv] + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * turn.abs()
+    if queries:
+        assert ((q_out.double() - turn[:, :, :nq]).abs() <= tol[:, :, :nq])[live].all()
+        assert (q_out[~live] == 77.0).all()
+    kept = live.clone()
+    kept[0] &= pos[0] // ps != hole
+    b, r = kept.nonzero(as_tuple=True)
+    page, slot = x.table[b, pos[b, r] // ps].long(), pos[b, r] % ps
+    got_k, got_v = x.k[0].permute(0, 2, 1, 3)[page, slot], x.v[0].permute(0, 2, 1, 3)[page, slot]
+    assert ((got_k.double() - turn[b, r, -nkv:]).abs() <= tol[b, r, -nkv:]).all()
+    assert torch.equal(got_v, z[b, r, -nkv:].to(x.dt))
+    rest = torch.ones(x.k.shape[1], ps, dtype=torch.bool, device="cuda")
+    rest[page, slot] = False
+    for now, then in ((x.k, k0), (x.v, v0)):
+        assert torch.equal(now[0].permute(0, 2, 1, 3)[rest], then[0].permute(0, 2, 1, 3)[rest])
+
+
 def test_append_reports_capacity_and_bad_pages():
     """A position past the table, past the rotation table and in a page outside the pool: the row is
     skipped, the bit is set, everything else is written."""
