@@ -355,7 +355,7 @@ __device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red, bool
   return v;
 }
 
-// Walks a CTA's run piece by piece.  Every role of the CTA runs its own copy.
+// Walks a CTA's run piece by piece.
 template <int KT>
 struct SegmentWalk {
   const PagedGeom& g;
@@ -538,9 +538,10 @@ cudaError_t paged_append(int in_dtype, int dtype, const void* qkv, long long ld,
                          const float2* tab, int max_pos, int n_pages, int ps, long long page0, void* qout, void* kp,
                          void* vp, int* status, cudaStream_t s);
 bool paged_line_fits(const PagedGeom& g);
-// Fills in the split of a call: row groups of `ri` / `rp` stacked rows, the grid, the partial slots.
+// Fills in the split of a call: row groups of `ri` / `rp` stacked rows, the grid, runs of `min_tiles` tiles at
+// least, the partial slots.
 // Returns the partial rows that it needs.
-long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_quota);
+long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_tiles);
 // Keys of a tile of the tensor-core kernel.
 constexpr int kPagedTcKeys = 128;
 // Merge of the tensor-core kernel's partials.

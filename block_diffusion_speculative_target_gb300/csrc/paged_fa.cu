@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* empty = bar + NS;        // [NS] both issuing warps are done with it
   uint64_t* q_full = bar + 2 * NS;   // [2]
   uint64_t* q_empty = q_full + 2;    // [2] two arrivals
-  uint64_t* s_full = q_full + 4;     // [2][2] scores of the group's tile in TMEM (rows as rows: one buffer)
+  uint64_t* s_full = q_full + 4;     // [2][2] scores of the group's tile (rows as rows: half tile) in TMEM
   uint64_t* p_full = q_full + 8;     // [2][2] the buffer's weights (four warps; one may be a job ahead of another)
   uint64_t* pv_done = q_full + 12;   // [2][2] the product of weights and values of the buffer's job is done
   uint64_t* o_free = q_full + 16;    // [2] the accumulator has been read (four warps)
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (seg > 0) ok = wait(&o_free[gq], seg - 1);
           if (ok && elect_one()) mbar_arrive(&q_empty[buf]);
         }
-        // (rows as columns: group 1 of a shared block has the 32 rows behind group 0's)
+        // (rows as columns: group 1 of a shared block has the rows behind group 0's NR)
         const uint8_t* qs = sm + L::kQ + buf * L::kQBuf + (two && cols ? gq * NR * 128 : 0);
         if (cols) {
           int kjob = job;  // keys run ahead
