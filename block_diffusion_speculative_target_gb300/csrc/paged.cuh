@@ -65,10 +65,17 @@ constexpr int kPagedMaxCtas = 4;
 // line position of each sequence's first suffix item and the line's end.
 enum { kPlanT = 0, kPlanQuota = 1, kPlanShared = 2, kPlanPre = 3, kPlanCum = 8 };
 
-__device__ __forceinline__ int paged_rows(const PagedGeom& g, int b) {
-  return g.n_rows ? min(max(g.n_rows[b], 0), g.n) : g.n;
+// `early`: a pass that comes before the call's arrays can be read.  None of them is; every sequence counts as n
+// rows behind all the keys that its table can name.
+__device__ __forceinline__ int paged_rows(const PagedGeom& g, int b, bool early = false) {
+  return g.n_rows && !early ? min(max(g.n_rows[b], 0), g.n) : g.n;
 }
-__device__ __forceinline__ int paged_len(const PagedGeom& g, int b) { return max(g.len[b], 0); }
+__device__ __forceinline__ int paged_len(const PagedGeom& g, int b, bool early = false) {
+  return early ? max(g.cap - g.n, 0) : max(g.len[b], 0);
+}
+__device__ __forceinline__ int paged_shared(const PagedGeom& g, bool early = false) {
+  return early ? g.cap : *g.shared;
+}
 
 // The sequence's keys: those held and those of this call.
 __device__ __forceinline__ int key_limit(const PagedGeom& g, int b) {
@@ -117,8 +124,8 @@ __device__ __forceinline__ TileSpan span_of(const PagedGeom& g, int P, int rows,
 }
 
 template <int KT>
-__device__ __forceinline__ TileSpan suffix_span(const PagedGeom& g, int b, int rt, int sh_tiles) {
-  return span_of<KT>(g, paged_len(g, b), paged_rows(g, b), rt, sh_tiles);
+__device__ __forceinline__ TileSpan suffix_span(const PagedGeom& g, int b, int rt, int sh_tiles, bool early) {
+  return span_of<KT>(g, paged_len(g, b, early), paged_rows(g, b, early), rt, sh_tiles);
 }
 
 // The tiles of every prefix item: those below sh that some row of the batch may see
@@ -197,31 +204,33 @@ __device__ __forceinline__ int positions_of(const PagedGeom& g, int P, int rows,
 // plan_view by one warp for itself, a lane for every few sequences (`write`: it writes the plan).
 constexpr int kPlanSmall = 128;
 template <int KT>
-__device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write) {
+__device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write, bool early) {
   const int lane = threadIdx.x & 31, per = (g.batch + 31) >> 5, b0 = lane * per, b1 = min(b0 + per, g.batch);
   PlanView v;
   v.sh_tiles = v.min_len = v.pre_b = v.pre_tiles = 0;
   const bool in = b0 < g.batch;
-  const int rows0 = in ? paged_rows(g, b0) : 0, P0 = in ? paged_len(g, b0) : 0;  // the lane's first sequence
+  // the lane's first sequence
+  const int rows0 = in ? paged_rows(g, b0, early) : 0, P0 = in ? paged_len(g, b0, early) : 0;
   if (g.shared) {
     int m = rows0 > 0 ? min(P0, g.cap) : INT32_MAX, first = rows0 > 0 ? b0 : g.batch;
     for (int b = b0 + 1; b < b1; ++b)
-      if (paged_rows(g, b) > 0) {
-        m = min(m, min(paged_len(g, b), g.cap));
+      if (paged_rows(g, b, early) > 0) {
+        m = min(m, min(paged_len(g, b, early), g.cap));
         first = min(first, b);
       }
     v.min_len = __reduce_min_sync(0xffffffffu, m);
     first = __reduce_min_sync(0xffffffffu, first);
     if (first < g.batch) {
       v.pre_b = first;
-      v.sh_tiles = max(0, min(*g.shared, v.min_len)) / KT;
+      v.sh_tiles = max(0, min(paged_shared(g, early), v.min_len)) / KT;
       if (v.sh_tiles > 0) v.pre_tiles = prefix_span<KT>(g, v.sh_tiles, v.min_len).count();
     }
   }
   const int pre_total = pre_positions(g, v.pre_tiles);
   const int c0 = positions_of<KT>(g, P0, rows0, v.sh_tiles);
   int c = c0;
-  for (int b = b0 + 1; b < b1; ++b) c += positions_of<KT>(g, paged_len(g, b), paged_rows(g, b), v.sh_tiles);
+  for (int b = b0 + 1; b < b1; ++b)
+    c += positions_of<KT>(g, paged_len(g, b, early), paged_rows(g, b, early), v.sh_tiles);
   int inc = c;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -236,7 +245,8 @@ __device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write) {
   int hit = start >= at && start < at + c0 ? b0 : -1, hit_at = at;
   if (per > 1 || write) {
     for (int b = b0; b < b1; ++b) {
-      const int n = b == b0 ? c0 : positions_of<KT>(g, paged_len(g, b), paged_rows(g, b), v.sh_tiles);
+      const int n =
+          b == b0 ? c0 : positions_of<KT>(g, paged_len(g, b, early), paged_rows(g, b, early), v.sh_tiles);
       if (start >= at && start < at + n) {
         hit = b;
         hit_at = at;
@@ -268,7 +278,7 @@ __device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write) {
 template <int KT, int NT>
 __device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red, bool write = true) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (g.batch <= kPlanSmall) return plan_small<KT>(g, write && tid < 32);
+  if (g.batch <= kPlanSmall) return plan_small<KT>(g, write && tid < 32, false);
   const bool first_cta = write && blockIdx.x == 0;
   PlanView v;
   const int per = (g.batch + NT - 1) / NT;
@@ -297,7 +307,7 @@ __device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red, bool
     }
     v.min_len = m;
     if (first < g.batch) {
-      v.sh_tiles = max(0, min(*g.shared, m)) / KT;
+      v.sh_tiles = max(0, min(paged_shared(g), m)) / KT;
       v.pre_b = first;
     }
     __syncthreads();
@@ -365,6 +375,7 @@ struct SegmentWalk {
   int item_at;        // its line position
   int pre_total;
   bool at_start;      // the first cut has not been placed yet
+  bool early = false; // the lengths are not read
   __device__ __forceinline__ SegmentWalk(const PagedGeom& g_, const PlanView& v_) : g(g_), v(v_) {}
   __device__ __forceinline__ void start() {
     pos = (int)min((long long)blockIdx.x * v.quota, (long long)v.T);
@@ -391,7 +402,7 @@ struct SegmentWalk {
       int c, tiles;
       while (true) {  // (pos < T: some item holds it, unless the lengths changed since the plan)
         if (b >= g.batch || pos < item_at) return false;
-        sp = suffix_span<KT>(g, b, rt, v.sh_tiles);
+        sp = suffix_span<KT>(g, b, rt, v.sh_tiles, early);
         tiles = sp.count();
         c = item_len(tiles, g.w_s, g.oh_s);
         if (pos < item_at + c * g.nkv) break;

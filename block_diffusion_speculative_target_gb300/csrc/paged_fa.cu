@@ -583,13 +583,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       SegmentWalk<KT> walk(g, pv);
       Segment sg;
       const bool small = g.batch <= kPlanSmall;
-      // One pass ahead (seg -1) runs the plan and the first piece on whatever the lengths hold while the previous
-      // kernel ends, and leaves nothing: no role can start before these few hundred instructions, and fetching
-      // them takes three to four times as long as running them once they are there.
+      // One pass ahead (seg -1) runs the plan and the first piece on assumed lengths while the previous kernel
+      // ends, and leaves nothing: no role can start before these few hundred instructions, and fetching them
+      // takes three to four times as long as running them once they are there.  The lengths are the previous
+      // kernels' to write until pdl_wait: before it they are only asked into L2, not read.
+      if (small) {
+        if (lane * 32 < g.batch) {
+          l2_prefetch(g.len + lane * 32);
+          if (g.n_rows) l2_prefetch(g.n_rows + lane * 32);
+        }
+        if (g.shared && lane == 0) l2_prefetch(g.shared);
+      }
       for (seg = small ? -1 : 0; ok; ++seg) {
+        walk.early = seg < 0;
         if (seg <= 0) {
           if (seg == 0) pdl_wait();
-          if (small) pv = plan_small<KT>(g, seg == 0);
+          if (small) pv = plan_small<KT>(g, seg == 0, seg < 0);
           walk.start();
         }
         const bool more = walk.next(sg);
@@ -602,8 +611,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           pc.hk = sg.hk;
           pc.rt = sg.rt;
           pc.ordinal = sg.ordinal;
-          pc.n = paged_rows(g, sg.b);
-          pc.P = min(paged_len(g, sg.b), g.cap);
+          pc.n = paged_rows(g, sg.b, seg < 0);
+          pc.P = min(paged_len(g, sg.b, seg < 0), g.cap);
           pc.x0 = sg.rt * (sg.prefix ? g.rp : g.ri);
           pc.rows = sg.prefix ? min(g.rp, g.batch * g.n * g.G - pc.x0) : min(g.ri, pc.n * g.G - pc.x0);
           pc.two = pc.rows > (as_columns(sg.prefix) ? NR : 128);
