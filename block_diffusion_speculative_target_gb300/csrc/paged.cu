@@ -254,13 +254,17 @@ __global__ void __launch_bounds__(kCoreThreads)
     }
     const int key_lo = sg.prefix ? 0 : v.sh_tiles * kCoreKeys;  // keys below belong to the shared prefix
     const int key_end = sg.prefix ? v.sh_tiles * kCoreKeys : key_limit(g, sg.b);
-    // 8 threads a key: its rows of keys and values (past the sequence's keys, or in a bad page: zeros), fetched into
+    // some row of the item sees the keys below seen_sink and those from seen_lo on: its first row's
+    int seen_sink, seen_lo, seen_hi;
+    row_span(g, sg.prefix ? v.min_len : paged_len(g, sg.b), paged_rows(g, sg.b),
+             sg.prefix ? 0 : div_g(g, sg.rt * g.ri), seen_sink, seen_lo, seen_hi);
+    // 8 threads a key: its rows of keys and values (keys that no row sees, or in a bad page: zeros), fetched into
     // registers while the tile before is worked on
     Raw8<T> rk[HD / 64], rv[HD / 64];
     auto fetch = [&](int t) {
       const int key = sg.span.tile(t) * kCoreKeys + (tid >> 3), part = tid & 7;
       int page = -1;
-      if (key < key_end) {
+      if (key < key_end && (key < seen_sink || key >= seen_lo)) {
         page = g.table[(long long)sg.b * g.table_stride + (key >> g.ps_log2)];
         if ((unsigned)page >= (unsigned)g.n_pages) {
           page = -1;

@@ -258,6 +258,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   volatile uint32_t* acc_first = misc + 2;  // [2] the first product of an item adds to O instead of setting it
   volatile uint32_t* bad_w = misc + 4;      // [2][4] keys of the tile with a value that is not finite
   int* red = reinterpret_cast<int*>(misc + 12);  // 32 ints
+  int* gap = red;                    // [4][2] after the plan, with a window: pages of a piece whose first key lies in
+                                     // the [1] keys from [0] on are seen by no row of its item
   volatile uint32_t* last_w = misc + 44;    // the CTA has finished an item's last piece
   volatile uint32_t* vote_w = misc + 46;    // [2][2][4] some reference of the tile has to move
   float2* xch = reinterpret_cast<float2*>(sm + L::kXch);
@@ -338,29 +340,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const Piece& pc = pieces[seg & 3];
         const int nt = pc.nt, hk = pc.hk, key_end = pc.key_end;
         if (nt == 0) break;
+        const int gap0 = g.window > 0 ? gap[2 * (seg & 3)] : 0;
+        const unsigned gap_n = g.window > 0 ? gap[2 * (seg & 3) + 1] : 0u;
         const int32_t* trow = g.table + (long long)pc.b * g.table_stride;
-        // This lane's page of tile t, -1 past the keys; and its pool row (a page that is none, or past the keys:
-        // past the pool, read as zeros).
-        auto page_of = [&](int t) {
+        // Whether some row sees a key of this lane's page of tile t: its entry may be anything otherwise.
+        auto used = [&](int t) {
           const int key = pc.tile(t) * KT + (lane << g.ps_log2);
-          const bool use = mine && t < nt && key < key_end;
-          return use ? trow[key >> g.ps_log2] : -1;
+          return mine && t < nt && key < key_end && (unsigned)(key - gap0) >= gap_n;
         };
-        auto row_of = [&](int t, int page) {
+        // The page, and its pool row (a page that is none, or not used: past the pool, read as zeros).
+        auto page_of = [&](int t, bool use) { return use ? trow[pc.tile(t) * per + lane] : -1; };
+        auto row_of = [&](bool use, int page) {
           if ((unsigned)page < (unsigned)g.n_pages)
             return (int)(g.page_row0 + ((long long)page * g.nkv + hk) * g.ps);
-          if (mine && t < nt && pc.tile(t) * KT + (lane << g.ps_log2) < key_end)
-            set_status(g.status, DFLASH_STATUS_BOUNDS);
+          if (use) set_status(g.status, DFLASH_STATUS_BOUNDS);
           return pool_rows;
         };
         const int ahead = ahead_of(as_columns(pc.prefix), pc.two);
         // the rows of the next tiles: [0] the next value tile's, [ahead] the next key tile's
-        int rowq[3] = {page_of(0), page_of(1), page_of(2)};
+        int rowq[3];
+        {
+          const bool use[3] = {used(0), used(1), used(2)};
 #pragma unroll
-        for (int a = 0; a < 3; ++a) rowq[a] = row_of(a, rowq[a]);
+          for (int a = 0; a < 3; ++a) rowq[a] = page_of(a, use[a]);
+#pragma unroll
+          for (int a = 0; a < 3; ++a) rowq[a] = row_of(use[a], rowq[a]);
+        }
         for (int u = 0; ok && u < nt + ahead; ++u) {
           const int x = min(u, ahead), krow = x == 0 ? rowq[0] : x == 1 ? rowq[1] : rowq[2];
-          const int next_t = u - ahead + 3, next_page = u >= ahead ? page_of(next_t) : -1;
+          const bool next_use = u >= ahead && used(u - ahead + 3);
+          const int next_page = page_of(u - ahead + 3, next_use);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             if (kv == 0 ? u >= nt : u < ahead) continue;
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (u >= ahead) {
             rowq[0] = rowq[1];
             rowq[1] = rowq[2];
-            rowq[2] = row_of(next_t, next_page);
+            rowq[2] = row_of(next_use, next_page);
           }
         }
         if (!ok) break;
@@ -645,6 +654,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
         if (lane == 0) {
           pieces[seg & 3] = pc;
+          if (g.window > 0) {
+            // between the first row's first tokens and its window (other rows' first tokens end later only where
+            // they meet it)
+            int sink, lo, hi;
+            row_span(g, pc.prefix ? pv.min_len : pc.P, pc.n, pc.prefix ? 0 : div_g(g, pc.x0), sink, lo, hi);
+            gap[2 * (seg & 3)] = sink;
+            gap[2 * (seg & 3) + 1] = max(lo - g.ps + 1 - sink, 0);
+          }
           mbar_arrive(&pc_full[seg & 3]);
         }
         __syncwarp();

@@ -469,7 +469,9 @@ int dflash_attention(const dflash_model_desc *d, const void *q, int32_t batch, i
  *   table [batch][table_stride]  page of each page_size positions: position p
  *                                of sequence b is slot p % page_size of page
  *                                table[b][p / page_size].  Only entries of
- *                                positions that are written or visible are read;
+ *                                pages with a position that is written, or that
+ *                                some row of the call sees, are read: pages
+ *                                behind a window may have been given away;
  *   len [batch]                  positions held before this call's rows;
  *   n_rows [batch] (nullable)    rows of the sequence in this call, 0..n (values
  *                                outside are clamped); NULL: n for all.  Rows at

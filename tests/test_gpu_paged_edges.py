@@ -3,7 +3,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_paged import HEADS, Batch, i32  # noqa: E402
+from test_gpu_paged import HEADS, Batch, check, i32, reference, untouched, visible  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,60 @@ def test_lengths_moved_by_the_kernel_before(heads, B, n, dtype):
             for k in range(steps):
                 assert torch.equal(outs[k], want[k]), (rep, k)
     assert x.cache.status() == 0
+
+
+def hide(x, causal, window, sinks, shared, bad):
+    """The table with every entry whose positions no row sees replaced by `bad`."""
+    t = x.table.clone()
+    seen = []
+    for P, r in zip(x.lens, x.rows):
+        s = torch.zeros(x.cols * x.ps, dtype=torch.bool, device="cuda")
+        for i in range(r):
+            see = visible(P, r, i, causal, window, sinks, P + r)
+            s[:P + r] |= see
+        seen.append(s)
+    common = torch.stack(seen).any(0)
+    common[shared:] = False  # what some row sees of the shared positions is read from one table
+    for b, s in enumerate(seen):
+        keep = (s | common).view(x.cols, x.ps).any(1)
+        t[b, ~keep] = bad
+    return t
+
+
+HIDDEN = [
+    # heads, ps, lens, n, rows, causal, window, sinks
+    ("gqa4", 16, [1000, 333, 90], 1, None, True, 100, 4),
+    ("gqa4", 16, [1000, 333, 90], 1, None, True, 37, 0),
+    ("gqa4", 16, [1000, 333, 90], 4, [4, 0, 2], True, 100, 130),
+    ("gqa5", 32, [5000, 700], 6, None, True, 200, 40),
+    ("gqa5", 16, [777, 200], 16, None, True, 64, 17),
+    ("gqa4", 64, [3000, 450], 16, [16, 9], True, 150, 64),
+    ("gqa4", 16, [2100, 640], 16, None, False, 250, 5),
+    ("mha64", 16, [900, 301], 40, None, True, 90, 20),
+    ("gqa4", 32, [1500], 40, None, True, 33, 3),
+    ("wide", 16, [900], 100, None, False, 333, 50),
+    ("gqa4", 16, [600, 700, 800], 2, None, True, 1, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", HIDDEN, ids=[f"{c[0]}-p{c[1]}-n{c[3]}-{'c' if c[5] else 'f'}-w{c[6]}-s{c[7]}" for c in HIDDEN])
+def test_entries_of_pages_that_no_row_sees_are_not_read(c, dtype):
+    """Pages behind the window, and between the first tokens and the window, may have been given away: their
+    entries are no pages, or another sequence's."""
+    heads, ps, lens, n, rows, causal, window, sinks = c
+    for shared in (0, 300):
+        if shared > min(lens):
+            continue
+        x = Batch(dtype, *HEADS[heads], ps, lens, n, rows, fill=float("nan"), shared=shared)
+        q = x.query()
+        kw = dict(causal=causal, window=window, sinks=sinks)
+        want = reference(x, q, **kw)
+        for bad in (-1, 10 ** 6):
+            t = hide(x, causal, window, sinks, shared, bad)
+            assert (t == bad).any()
+            out = torch.full_like(q, 77.0)
+            x.cache.attention(0, q, t, x.len, out, n_rows=x.n_rows, shared_len=i32([shared]) if shared else None, **kw)
+            assert x.cache.status() == 0, (shared, bad)
+            untouched(x, out)
+            check(x, out, want, f"shared {shared} bad {bad}")
