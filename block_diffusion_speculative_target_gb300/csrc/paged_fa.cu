@@ -1434,9 +1434,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
                 const float2 w = coef[c0 + c];
-                float x = __uint_as_float(a[c]), xb = 0.f;
-                if (kPair) x += __uint_as_float(a2[c]);
-                if (both) xb = kPair ? __uint_as_float(b[c]) + __uint_as_float(b2[c]) : __uint_as_float(b[c]);
+                float x = __uint_as_float(a[c]), xb = both ? __uint_as_float(b[c]) : 0.f;
+                if (kPair) {
+                  // (the high parts' sum is infinite where an infinite value is seen; its product with a low part
+                  // of 0 or below would be NaN)
+                  if (!isinf(x)) x += __uint_as_float(a2[c]);
+                  if (both && !isinf(xb)) xb += __uint_as_float(b2[c]);
+                }
                 x *= w.x;
                 if (both) x = fmaf(w.y, xb, x);
                 if (c0 + c < rows) {

@@ -3,7 +3,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_paged import HEADS, Batch, check, i32, reference, untouched, visible  # noqa: E402
+from test_gpu_paged import HEADS, Batch, attend, bound, check, i32, reference, untouched, visible  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +131,43 @@ def test_entries_of_pages_that_no_row_sees_are_not_read(c, dtype):
             assert x.cache.status() == 0, (shared, bad)
             untouched(x, out)
             check(x, out, want, f"shared {shared} bad {bad}")
+
+
+# stacked rows 4, 16, 20, 24, 32, 64, 128, 256, 260 of 4 or 5 query heads a KV head
+LAYOUTS = [(1, 4), (4, 4), (4, 5), (6, 4), (8, 4), (16, 4), (32, 4), (64, 4), (52, 5)]
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("bf16", 64), ("f32", 128)])
+@pytest.mark.parametrize("n,G", LAYOUTS, ids=[f"{n * G}" for n, G in LAYOUTS])
+@pytest.mark.parametrize("window", [0, 300])
+def test_values_that_are_not_finite(n, G, dtype, hd, window):
+    """Infinite and NaN values in tiles that every row sees and in tiles that rows see in part: a row that sees
+    one has the definition's infinity or NaN in that dimension, and nothing else of any row is touched."""
+    for shared in (0, 384):
+        x = Batch(dtype, G, 1, hd, 32, [3000, 900, 517], n, rows=[n, max(n - 2, 1), 1], seed=n * G, shared=shared)
+        q = x.query()
+        inf, nan = float("inf"), float("nan")
+
+        def put(b, p, d, value):
+            for s in range(3) if p < shared else (b,):
+                x.v[0, int(x.table[s, p // 32]), 0, p % 32, d] = value
+
+        for b, P in enumerate(x.lens):
+            for base in (P - 150, P - 450, P + x.rows[b] - 1, P - 280, 200):  # (200: in the prefix of all)
+                put(b, base, 3, inf)
+                put(b, base, 8, -inf)
+                put(b, base, 21, nan)
+                put(b, base, 30, inf)
+            put(b, P - 170, 30, -inf)  # both infinities
+            put(b, P + x.rows[b] - 1, 40, inf)  # the last row's own position
+        kw = dict(window=window, sinks=0 if n % 2 else 210)
+        ref, mag, dots, most = reference(x, q, **kw)
+        out = attend(x, q, shared=shared or None, **kw)
+        untouched(x, out)
+        lim = bound(x, ref, mag, dots, most)
+        for b, r in enumerate(x.rows):
+            got, want = out[b, :r].double(), ref[b, :r]
+            for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+                assert torch.equal(kind(got), kind(want)), (kind.__name__, shared, b)
+            ok = want.isfinite()
+            assert ((got - want).abs() <= lim[b, :r])[ok].all(), (shared, b)
