@@ -477,25 +477,37 @@ cudaError_t paged_merge_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t
   return hd == 64 ? merge_launch<bf16, 64, kPagedTcKeys>(g, out, s) : merge_launch<bf16, 128, kPagedTcKeys>(g, out, s);
 }
 
-long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_tiles) {
-  g.ri = ri;
-  g.rp = rp;
+static int groups_of(int rows, int of) { return (rows + of - 1) / of; }
+
+long long paged_split(PagedGeom& g, const PagedRule& r, int grid, int min_tiles) {
+  g.ri = r.ri;
+  g.rp = r.rp;
+  g.w_s = g.w_p = r.w;
+  g.oh_s = g.oh_p = r.oh;
   g.g_magic = (unsigned)(((1ull << 32) + g.G - 1) / g.G);
-  g.nrt = (g.n * g.G + ri - 1) / ri;
-  g.nrp = (g.batch * g.n * g.G + rp - 1) / rp;
+  g.nrt = groups_of(g.n * g.G, r.ri);
+  g.nrp = groups_of(g.batch * g.n * g.G, r.rp);
   g.grid = grid;
-  g.min_quota = min_tiles * std::max(g.w_s, g.w_p);
-  g.slot_s = std::min(g.n * g.G, ri);
-  g.slot_p = std::min(g.batch * g.n * g.G, rp);
+  g.min_quota = min_tiles * r.w;
+  g.slot_s = std::min(g.n * g.G, r.ri);
+  g.slot_p = std::min(g.batch * g.n * g.G, r.rp);
   g.pre_row0 = ((long long)g.batch * g.nrt * g.nkv + grid) * g.slot_s;
   return g.pre_row0 + (g.shared ? ((long long)g.nrp * g.nkv + grid) * g.slot_p : 0);
 }
 
-// The line's tiles fit an int with room for the arithmetic on it, whatever the kernel:
-// the smallest row groups (16 stacked rows) and tiles.
-bool paged_line_fits(const PagedGeom& g) {
-  const long long groups = (long long)g.batch * ((g.n * g.G + 15) / 16) * (g.shared ? 2 : 1);
-  return (double)groups * g.nkv * ((double)g.cap / kCoreKeys + 2) < 134217728.0;  // (at most 8 positions a tile)
+// Below 2^30 positions every sum and product on the line (a position and a run, an item's tiles by its heads) fits
+// an int.  16384 rows of 32 / 8 heads in 8 sequences behind tables of 131072 positions: 4.2 million.
+bool paged_line_fits(const PagedGeom& g, const PagedRule& r) {
+  const double items =
+      (double)g.batch * groups_of(g.n * g.G, r.ri) + (g.shared ? groups_of(g.batch * g.n * g.G, r.rp) : 0);
+  return items * g.nkv * (((double)g.cap / r.keys + 2) * r.w + r.oh) < 1073741824.0;
+}
+
+// Few stacked rows: the 16-row tile spends fewer products on padding.
+static bool core_small(const PagedGeom& g) { return (g.shared ? g.batch : 1) * g.n * g.G <= 16; }
+PagedRule paged_rule_core(const PagedGeom& g) {
+  const int rows = core_small(g) ? 16 : 64;
+  return PagedRule{rows, rows, kCoreKeys, 1, 0};
 }
 
 template <typename T, int HD, int MRM>
@@ -511,9 +523,10 @@ static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const
                                                           L::kSmem));
     per_sm = std::min(std::max(x, 1), kPagedMaxCtas);
   }
-  g.w_s = g.w_p = 1;
+  const PagedRule rule = paged_rule_core(g);
+  if (rule.ri != L::MR) return cudaErrorInvalidValue;
   // runs of two tiles at least: 4 blocks of 16 rows over up to 1K keys take 17.4 us, 22.4 in runs of four
-  if (paged_split(g, L::MR, L::MR, num_sms() * per_sm, 2) > part_rows) return cudaErrorInvalidValue;
+  if (paged_split(g, rule, num_sms() * per_sm, 2) > part_rows) return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
   DFL_RET(launch_pdl(paged_attn_core_kernel<T, HD, MRM>, dim3(g.grid), dim3(kCoreThreads), L::kSmem, s, g, (const T*)q,
                      (const T*)kp, (const T*)vp, (T*)out, scale_log2));
@@ -523,11 +536,9 @@ static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const
 
 cudaError_t paged_attention_core(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp,
                                  void* out, long long part_rows, cudaStream_t s) {
-  // few stacked rows: the 16-row tile spends fewer products on padding
-  const bool small = (g.shared ? g.batch : 1) * g.n * g.G <= 16;
-#define DFL_CORE(HD)                                                                    \
-  return small ? core_launch<float, HD, 1>(g, q, kp, vp, out, part_rows, s)            \
-               : core_launch<float, HD, 4>(g, q, kp, vp, out, part_rows, s)
+#define DFL_CORE(HD)                                                                         \
+  return core_small(g) ? core_launch<float, HD, 1>(g, q, kp, vp, out, part_rows, s)          \
+                       : core_launch<float, HD, 4>(g, q, kp, vp, out, part_rows, s)
   if (hd == 64) DFL_CORE(64);
   DFL_CORE(128);
 #undef DFL_CORE

@@ -548,11 +548,18 @@ cudaError_t paged_append(int in_dtype, int dtype, const void* qkv, long long ld,
                          int hd, const int32_t* n_rows, const int32_t* table, int table_stride, const int32_t* len,
                          const float2* tab, int max_pos, int n_pages, int ps, long long page0, void* qout, void* kp,
                          void* vp, int* status, cudaStream_t s);
-bool paged_line_fits(const PagedGeom& g);
-// Fills in the split of a call: row groups of `ri` / `rp` stacked rows, the grid, runs of `min_tiles` tiles at
-// least, the partial slots.
+// How a kernel cuts a call: stacked rows of a suffix / prefix item, keys of a tile, line positions of a tile and of
+// an item's start and end.
+struct PagedRule {
+  int ri, rp, keys, w, oh;
+};
+PagedRule paged_rule_core(const PagedGeom& g);
+PagedRule paged_rule_tc(const PagedGeom& g);
+// Whether the line of such a call fits the plan's integers, whatever lengths its tables hold.
+bool paged_line_fits(const PagedGeom& g, const PagedRule& r);
+// Fills in the split of a call: row groups, the grid, runs of `min_tiles` tiles at least, the partial slots.
 // Returns the partial rows that it needs.
-long long paged_split(PagedGeom& g, int ri, int rp, int grid, int min_tiles);
+long long paged_split(PagedGeom& g, const PagedRule& r, int grid, int min_tiles);
 // Keys of a tile of the tensor-core kernel.
 constexpr int kPagedTcKeys = 128;
 // Merge of the tensor-core kernel's partials.

@@ -231,7 +231,7 @@ static int attend(dflash_pages* p, int32_t layer, const void* q, int32_t batch, 
   g.tickets = ws->tickets;
   g.records = ws->records;
   g.status = ws->status;
-  if (!paged_line_fits(g)) return DFLASH_ERR_TOO_LARGE;
+  if (!paged_line_fits(g, p->dtype == DFLASH_BF16 ? paged_rule_tc(g) : paged_rule_core(g))) return DFLASH_ERR_TOO_LARGE;
   if (p->dtype == DFLASH_BF16)
     CK(paged_attention_tc(p->hd, g, p->tk, p->tv, pool_rows(p), q, out, ws->part_rows, (cudaStream_t)stream));
   else

@@ -1486,6 +1486,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
+PagedRule paged_rule_tc(const PagedGeom& g) {
+  // Items of two query tiles where there are rows for them.
+  const int ri = g.n * g.G > 128 ? 256 : 128, rp = g.batch * g.n * g.G > 128 ? 256 : 128;
+  // A tile takes two positions of the line, an item's start and end the time of two tiles more: with 0 instead,
+  // 8 prompts' first 128 rows take 36.0 us (28.0 so), 64 tokens behind a common 12K 119 (107), 128 rows behind
+  // 36K 130 (126); only a window's pieces (15 rows, 34 tiles an item) lose, 80.7 (82.9).
+  return PagedRule{ri, rp, kPagedTcKeys, 2, 4};
+}
+
 template <int HD, int NR, bool TS, bool TP>
 static cudaError_t tc_launch(PagedGeom g, const CUtensorMap& tk, const CUtensorMap& tv, long long pool_rows,
                              const void* q, void* out, long long part_rows, cudaStream_t s) {
@@ -1496,14 +1505,7 @@ static cudaError_t tc_launch(PagedGeom g, const CUtensorMap& tk, const CUtensorM
                                  L::kSmem));
     set = true;
   }
-  // items of two query tiles where there are rows for them
-  const int ri = g.n * g.G > 128 ? 256 : 128, rp = g.batch * g.n * g.G > 128 ? 256 : 128;
-  // A tile takes two positions of the line, an item's start and end the time of two tiles more: with 0 instead,
-  // 8 prompts' first 128 rows take 36.0 us (28.0 so), 64 tokens behind a common 12K 119 (107), 128 rows behind
-  // 36K 130 (126); only a window's pieces (15 rows, 34 tiles an item) lose, 80.7 (82.9).
-  g.w_s = g.w_p = 2;
-  g.oh_s = g.oh_p = 4;
-  if (paged_split(g, ri, rp, num_sms(), 2) > part_rows) return cudaErrorInvalidValue;
+  if (paged_split(g, paged_rule_tc(g), num_sms(), 2) > part_rows) return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
   DFL_RET(launch_pdl(paged_attn_tc_kernel<HD, NR, TS, TP>, dim3(g.grid), dim3(kTcThreads), L::kSmem, s, tk, tv, g,
                      (int)pool_rows, (const bf16*)q, (bf16*)out, scale_log2));

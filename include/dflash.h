@@ -531,7 +531,12 @@ int dflash_paged_append(dflash_pages *p, int32_t layer, int32_t in_dtype, const 
  * lie in hidden or unused slots.  The keys are split over the GPU by all
  * lengths of the call, so the last bits of a row may depend on the batch it is
  * in (dflash_attention, which fixes the split per cache, has no such
- * dependence); equal calls give equal bits. */
+ * dependence); equal calls give equal bits.
+ * DFLASH_ERR_TOO_LARGE: a table of more than 2^30 positions, or work that could
+ * outgrow the plan's 32-bit numbers, (groups of rows) * nkv * (positions of a
+ * table row) / 64 in bf16 and / 32 in float32 at 2^30 or more.  A group holds
+ * up to 256 (float32: 64) of a sequence's n * nq / nkv rows; a shared prefix
+ * adds the groups of the whole batch's. */
 int dflash_paged_attention(dflash_pages *p, int32_t layer, const void *q, int32_t batch, int32_t n,
                            const int32_t *n_rows, int32_t causal, int32_t window, int32_t sinks,
                            const int32_t *table, int32_t table_stride, const int32_t *len, void *out,

@@ -3,6 +3,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from block_diffusion_speculative_target_gb300 import capi  # noqa: E402
 from test_gpu_paged import HEADS, Batch, attend, bound, check, i32, reference, untouched, visible  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -171,3 +172,34 @@ def test_values_that_are_not_finite(n, G, dtype, hd, window):
                 assert torch.equal(kind(got), kind(want)), (kind.__name__, shared, b)
             ok = want.isfinite()
             assert ((got - want).abs() <= lim[b, :r])[ok].all(), (shared, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows_behind_a_wide_table(dtype):
+    """16384 rows of 32 / 8 heads whose tables could name 131072 positions: what the lengths come to counts,
+    and the result is that of narrow tables, bit for bit."""
+    B, n, ps = 8, 2048, 64
+    hd = 128 if dtype == "bf16" else 64
+    x = Batch(dtype, 32, 8, hd, ps, [40 * b for b in range(B)], n, rows=[n - 100 * b for b in range(B)], shared=0)
+    q = x.query()
+    narrow = attend(x, q)
+    wide = torch.full((B, 131072 // ps), -1, dtype=torch.int32, device="cuda")
+    wide[:, :x.cols] = x.table
+    for shared in (None, 0):
+        out = torch.full_like(q, 77.0)
+        x.cache.attention(0, q, wide, x.len, out, n_rows=x.n_rows, shared_len=None if shared is None else i32([shared]))
+        assert torch.equal(out, narrow)
+    assert x.cache.status() == 0
+    for b in (0, 5, 7):
+        for i in (0, 1, 1000, x.rows[b] - 1):
+            k, v = x.keys(b, x.lens[b] + i + 1)
+            a = q[b, i].double().view(8, 4, hd)
+            p = torch.softmax(a @ k.transpose(1, 2) / hd ** 0.5, -1)
+            ref, mag = (p @ v).view(32, hd), (p @ v.abs()).view(32, hd)
+            dots = float((a.abs() @ k.abs().transpose(1, 2)).max()) / hd ** 0.5
+            assert ((narrow[b, i].double() - ref).abs() <= bound(x, ref, mag, dots, k.shape[1])).all(), (b, i)
+    # a line that could outgrow the plan is refused: 2^23 tiles (float32: 2^25) a row group and head
+    L, c = capi.load(), x.cache
+    assert L.dflash_paged_attention(c.pages, 0, q.data_ptr(), B, n, None, 1, 0, 0, wide.data_ptr(), (1 << 30) // ps,
+                                    x.len.data_ptr(), out.data_ptr(), c.ws, None) == capi.ERR_TOO_LARGE
+    assert torch.equal(out, narrow)
