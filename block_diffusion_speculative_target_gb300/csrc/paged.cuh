@@ -35,7 +35,7 @@ struct PagedGeom {
   int nrt, nrp;          // row groups of a sequence / of the batch
   int causal, window, sinks;
   int ps, ps_log2, n_pages, table_stride;
-  int cap;               // keys a sequence's table row can name
+  int cap;               // positions that a sequence's table row and the handle can name
   int grid;              // CTAs of the attention kernel
   int min_quota;
   int w_s, oh_s, w_p, oh_p;  // line positions of a tile of a suffix / prefix item, and of an item's start and end
@@ -75,6 +75,12 @@ __device__ __forceinline__ int paged_len(const PagedGeom& g, int b, bool early =
 }
 __device__ __forceinline__ int paged_shared(const PagedGeom& g, bool early = false) {
   return early ? g.cap : *g.shared;
+}
+
+// The sequence's rows lie at positions that there are.
+__device__ __forceinline__ bool positions_ok(const PagedGeom& g, int b) {
+  const int rows = paged_rows(g, b);
+  return rows == 0 || (g.len[b] >= 0 && g.len[b] <= g.cap - rows);
 }
 
 // The sequence's keys: those held and those of this call.
@@ -253,8 +259,7 @@ __device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write, b
       }
       if (write) {
         if (g.shared) g.plan[kPlanCum + b] = at;
-        if (paged_rows(g, b) > 0 && paged_len(g, b) > g.cap - paged_rows(g, b))
-          set_status(g.status, DFLASH_STATUS_CAPACITY);
+        if (!positions_ok(g, b)) set_status(g.status, DFLASH_STATUS_CAPACITY);
       }
       at += n;
     }
@@ -318,8 +323,7 @@ __device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red, bool
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
     sum += tiles_of(b);
-    if (first_cta && paged_rows(g, b) > 0 && paged_len(g, b) > g.cap - paged_rows(g, b))
-      set_status(g.status, DFLASH_STATUS_CAPACITY);
+    if (first_cta && !positions_ok(g, b)) set_status(g.status, DFLASH_STATUS_CAPACITY);
   }
   int inc = sum;  // inclusive scan over the block
 #pragma unroll

@@ -1,6 +1,7 @@
 // C ABI of the KV pages: the handle, the workspace and the calls on them.
 #include <math.h>
 
+#include <algorithm>
 #include <new>
 
 #include "common.cuh"
@@ -219,7 +220,7 @@ static int attend(dflash_pages* p, int32_t layer, const void* q, int32_t batch, 
   g.ps_log2 = p->page_size == 16 ? 4 : p->page_size == 32 ? 5 : p->page_size == 64 ? 6 : 7;
   g.n_pages = p->n_pages;
   g.table_stride = table_stride;
-  g.cap = table_stride * p->page_size;
+  g.cap = std::min(table_stride * p->page_size, p->max_pos);
   g.page_row0 = (long long)layer * p->n_pages * p->nkv * p->page_size;
   g.len = len;
   g.n_rows = n_rows;

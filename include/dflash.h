@@ -478,8 +478,8 @@ int dflash_attention(const dflash_model_desc *d, const void *q, int32_t batch, i
  *                                or past it are padding: their inputs are not
  *                                used and their outputs are left as they were.
  * len does not move: the caller adds the rows it keeps, after its last layer.
- * Device conditions set bits in the workspace's status word: a position past
- * the table or past max_pos sets DFLASH_STATUS_CAPACITY, a page outside
+ * Device conditions set bits in the workspace's status word: a row's position
+ * below 0, past the table or past max_pos sets DFLASH_STATUS_CAPACITY, a page outside
  * [0, n_pages) DFLASH_STATUS_BOUNDS; that write is skipped, that sequence's
  * attention output is unspecified, other sequences are not touched. */
 typedef struct dflash_pages dflash_pages;
@@ -534,9 +534,9 @@ int dflash_paged_append(dflash_pages *p, int32_t layer, int32_t in_dtype, const 
  * dependence); equal calls give equal bits.
  * DFLASH_ERR_TOO_LARGE: a table of more than 2^30 positions, or work that could
  * outgrow the plan's 32-bit numbers, (groups of rows) * nkv * (positions of a
- * table row) / 64 in bf16 and / 32 in float32 at 2^30 or more.  A group holds
- * up to 256 (float32: 64) of a sequence's n * nq / nkv rows; a shared prefix
- * adds the groups of the whole batch's. */
+ * table row, max_pos at most) / 64 in bf16 and / 32 in float32 at 2^30 or more.
+ * A group holds up to 256 (float32: 64) of a sequence's n * nq / nkv rows; a
+ * shared prefix adds the groups of the whole batch's. */
 int dflash_paged_attention(dflash_pages *p, int32_t layer, const void *q, int32_t batch, int32_t n,
                            const int32_t *n_rows, int32_t causal, int32_t window, int32_t sinks,
                            const int32_t *table, int32_t table_stride, const int32_t *len, void *out,

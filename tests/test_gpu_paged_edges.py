@@ -4,7 +4,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from block_diffusion_speculative_target_gb300 import capi  # noqa: E402
-from test_gpu_paged import HEADS, Batch, attend, bound, check, i32, reference, untouched, visible  # noqa: E402
+from block_diffusion_speculative_target_gb300.engine import PagedCache  # noqa: E402
+from test_gpu_paged import HEADS, Batch, attend, bound, check, i32, reference, shape_of, untouched, visible  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -183,13 +184,14 @@ def test_many_rows_behind_a_wide_table(dtype):
     x = Batch(dtype, 32, 8, hd, ps, [40 * b for b in range(B)], n, rows=[n - 100 * b for b in range(B)], shared=0)
     q = x.query()
     narrow = attend(x, q)
+    cache = PagedCache(shape_of(32, 8, hd), dtype, x.k.shape[1], ps, 131072, B * n, max_batch=B, k=x.k, v=x.v)
     wide = torch.full((B, 131072 // ps), -1, dtype=torch.int32, device="cuda")
     wide[:, :x.cols] = x.table
     for shared in (None, 0):
         out = torch.full_like(q, 77.0)
-        x.cache.attention(0, q, wide, x.len, out, n_rows=x.n_rows, shared_len=None if shared is None else i32([shared]))
+        cache.attention(0, q, wide, x.len, out, n_rows=x.n_rows, shared_len=None if shared is None else i32([shared]))
         assert torch.equal(out, narrow)
-    assert x.cache.status() == 0
+    assert cache.status() == 0
     for b in (0, 5, 7):
         for i in (0, 1, 1000, x.rows[b] - 1):
             k, v = x.keys(b, x.lens[b] + i + 1)
@@ -198,8 +200,52 @@ def test_many_rows_behind_a_wide_table(dtype):
             ref, mag = (p @ v).view(32, hd), (p @ v.abs()).view(32, hd)
             dots = float((a.abs() @ k.abs().transpose(1, 2)).max()) / hd ** 0.5
             assert ((narrow[b, i].double() - ref).abs() <= bound(x, ref, mag, dots, k.shape[1])).all(), (b, i)
-    # a line that could outgrow the plan is refused: 2^23 tiles (float32: 2^25) a row group and head
-    L, c = capi.load(), x.cache
-    assert L.dflash_paged_attention(c.pages, 0, q.data_ptr(), B, n, None, 1, 0, 0, wide.data_ptr(), (1 << 30) // ps,
-                                    x.len.data_ptr(), out.data_ptr(), c.ws, None) == capi.ERR_TOO_LARGE
-    assert torch.equal(out, narrow)
+
+
+def test_work_beyond_the_plan_is_refused():
+    """65536 float32 rows of 64 heads, 2^10 groups a head, behind a table and a handle of 2^20 positions: 2^31
+    tiles could lie on the line.  (Every array is as large as the call says.)"""
+    n, heads, hd, ps = 1 << 16, 64, 64, 128
+    cache = PagedCache(shape_of(heads, heads, hd), "f32", 1, ps, 1 << 20, n, max_batch=1)
+    q = torch.zeros(1, n, heads, hd, device="cuda")
+    out = torch.full_like(q, 77.0)
+    table, length = torch.zeros(1, (1 << 20) // ps, dtype=torch.int32, device="cuda"), i32([0])
+    with pytest.raises(capi.DFlashError) as e:
+        cache.attention(0, q, table, length, out)
+    assert e.value.code == capi.ERR_TOO_LARGE and (out == 77.0).all()
+    # what lies past max_pos does not count
+    small = PagedCache(shape_of(heads, heads, hd), "f32", 1, ps, 64, 64, max_batch=1)
+    some = q[:, :64].contiguous()
+    small.attention(0, some, table, length, out[:, :64].contiguous())
+    assert small.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [3, 140])
+def test_attention_reports_positions_that_the_handle_does_not_hold(dtype, B):
+    """A length below zero, and rows past max_pos inside the table, set the status as the append does; other
+    sequences are not touched."""
+    x = Batch(dtype, 4, 1, 128, 16, [60] * B, 4, extra_cols=2)
+    cache = PagedCache(shape_of(4, 1, 128), dtype, x.k.shape[1], 16, 64, 4 * B, max_batch=B, k=x.k, v=x.v)
+    q = x.query()
+    out = torch.full_like(q, 77.0)
+    cache.attention(0, q, x.table, x.len, out)  # rows at 60..63: the last ones
+    assert cache.status() == 0
+    want = reference(x, q)
+    check(x, out, want)
+    lim = bound(x, *want)
+    for bad in (61, -1, -2 ** 31, 2 ** 31 - 1):
+        lens = x.len.clone()
+        lens[1] = bad
+        for sh in (None, 16):
+            out = torch.full_like(q, 77.0)
+            cache.attention(0, q, x.table, lens, out, shared_len=None if sh is None else i32([0]))
+            assert cache.status() == capi.STATUS_CAPACITY, bad
+            for b in (0, 2, B - 1):
+                assert ((out[b].double() - want[0][b]).abs() <= lim[b]).all(), (bad, b)
+    # a sequence without rows in the call names no position
+    lens = x.len.clone()
+    lens[1] = 61
+    rows = i32([4, 0] + [4] * (B - 2))
+    cache.attention(0, q, x.table, lens, out, n_rows=rows)
+    assert cache.status() == 0
