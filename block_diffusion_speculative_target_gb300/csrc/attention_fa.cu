@@ -651,12 +651,11 @@ cudaError_t attention_fa(int G, const KvMaps& maps, const CUtensorMap& qmap, int
   if (maps.q8 && (G > 5 || !maps.ks || !maps.vs)) return cudaErrorInvalidValue;
 #define DFL_FA_CASE(GG, QQ, LY)                                                                                  \
   {                                                                                                              \
-    static bool set = false;                                                                                     \
-    if (!set) {                                                                                                  \
-      DFL_RET(cudaFuncSetAttribute(attn_fa_kernel<GG, QQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,          \
-                                   LY<GG>::kSmem));                                                              \
-      set = true;                                                                                                \
-    }                                                                                                            \
+    static PerDevice smem;                                                                                       \
+    DFL_RET(smem.once([] {                                                                                       \
+      return cudaFuncSetAttribute(attn_fa_kernel<GG, QQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,           \
+                                  LY<GG>::kSmem);                                                                \
+    }));                                                                                                         \
     DFL_RET(launch_pdl(attn_fa_kernel<GG, QQ>, dim3((unsigned)units), dim3(kFaThreads), LY<GG>::kSmem, s, maps.k, \
                        maps.v, qmap, batch, n, nq, nkv, causal, window, maps.row0, capacity, gtiles, sc.nchunk,   \
                        len, tree_mask, maps.ks, maps.vs, sc.o, sc.ml, scale_log2, status));                       \

@@ -865,14 +865,11 @@ static bool make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_
 }
 
 int num_sms() {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (n <= 0) n = 148;
-  }
-  return n;
+  static PerDevice sms;
+  int n = 0;
+  const cudaError_t e =
+      sms.get(&n, [](int dev, int* v) { return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev); });
+  return e == cudaSuccess && n > 0 ? n : 148;
 }
 
 bool gemm_shape_ok(int dtype, int M, int K) {
@@ -913,11 +910,10 @@ template <int BN, int STAGES>
 static cudaError_t launch_cl(const CUtensorMap& tw, const CUtensorMap& tx, const GemmEpi& epi, int rows, int M, int K,
                              int S, int* status, cudaStream_t s) {
   using C = ClCfg<BN, STAGES>;
-  static bool set = false;
-  if (!set) {
-    DFL_RET(cudaFuncSetAttribute(gemm_cl_kernel<BN, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-    set = true;
-  }
+  static PerDevice smem;
+  DFL_RET(smem.once([] {
+    return cudaFuncSetAttribute(gemm_cl_kernel<BN, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  }));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(S, M / 128, 1);
   cfg.blockDim = dim3(128, 1, 1);

@@ -7,6 +7,7 @@
 #include <utility>
 
 #include "../../include/dflash.h"
+#include "per_device.h"
 
 namespace dfl {
 

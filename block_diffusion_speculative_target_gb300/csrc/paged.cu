@@ -514,15 +514,16 @@ template <typename T, int HD, int MRM>
 static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const void* vp, void* out,
                                long long part_rows, cudaStream_t s) {
   typedef CoreLayout<HD, MRM> L;
-  static int per_sm = 0;
-  if (!per_sm) {
+  static PerDevice ctas;
+  int per_sm = 0;
+  DFL_RET(ctas.get(&per_sm, [](int, int* v) {
     DFL_RET(cudaFuncSetAttribute(paged_attn_core_kernel<T, HD, MRM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  L::kSmem));
-    int x = 0;
-    DFL_RET(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&x, paged_attn_core_kernel<T, HD, MRM>, kCoreThreads,
+    DFL_RET(cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, paged_attn_core_kernel<T, HD, MRM>, kCoreThreads,
                                                           L::kSmem));
-    per_sm = std::min(std::max(x, 1), kPagedMaxCtas);
-  }
+    *v = std::min(std::max(*v, 1), kPagedMaxCtas);
+    return cudaSuccess;
+  }));
   const PagedRule rule = paged_rule_core(g);
   if (rule.ri != L::MR) return cudaErrorInvalidValue;
   // runs of two tiles at least: 4 blocks of 16 rows over up to 1K keys take 17.4 us, 22.4 in runs of four

@@ -1499,12 +1499,11 @@ template <int HD, int NR, bool TS, bool TP>
 static cudaError_t tc_launch(PagedGeom g, const CUtensorMap& tk, const CUtensorMap& tv, long long pool_rows,
                              const void* q, void* out, long long part_rows, cudaStream_t s) {
   typedef TcLayout<HD> L;
-  static bool set = false;
-  if (!set) {
-    DFL_RET(cudaFuncSetAttribute(paged_attn_tc_kernel<HD, NR, TS, TP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 L::kSmem));
-    set = true;
-  }
+  static PerDevice smem;
+  DFL_RET(smem.once([] {
+    return cudaFuncSetAttribute(paged_attn_tc_kernel<HD, NR, TS, TP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                L::kSmem);
+  }));
   if (paged_split(g, paged_rule_tc(g), num_sms(), 2) > part_rows) return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
   DFL_RET(launch_pdl(paged_attn_tc_kernel<HD, NR, TS, TP>, dim3(g.grid), dim3(kTcThreads), L::kSmem, s, tk, tv, g,
