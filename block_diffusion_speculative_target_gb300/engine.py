@@ -359,7 +359,6 @@ class Session:
         return g
 
 
-
 class PagedCache:
     """A pool of KV pages with the append and attention calls on it.
 
@@ -369,8 +368,8 @@ class PagedCache:
     and row counts are the caller's device int32 tensors: ``table``
     [batch][columns] names the page of each ``page_size`` positions, ``lengths``
     [batch] the positions held before a call's rows, ``n_rows`` [batch] the rows
-    of each sequence in the call (None: all).  Calls are asynchronous on the
-    current stream and leave ``lengths`` as it is."""
+    of each sequence in the call (None: all).  Calls enter the pool's device,
+    are asynchronous on its current stream and leave ``lengths`` as it is."""
 
     def __init__(self, shape, dtype: str, n_pages, page_size, max_pos, max_rows, max_batch=None, n_layers=1, k=None,
                  v=None, device="cuda"):
@@ -411,7 +410,8 @@ class PagedCache:
             pass
 
     def status(self):
-        return capi.dflash_paged_status(self.ws)
+        with torch.cuda.device(self.device):
+            return capi.dflash_paged_status(self.ws)
 
     def _index(self, t, what, dims):
         if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous() or tuple(t.shape) != dims:
@@ -439,6 +439,10 @@ class PagedCache:
         float32 or the pool's type, q|k|v heads side by side (k|v without
         ``q_out``); its rows may be apart.  ``q_out`` receives the rotated
         queries."""
+        stream = torch.cuda.current_stream()
+        if stream.device_index != self.device.index:
+            with torch.cuda.device(self.device):
+                return self.append(layer, qkv, table, lengths, n, q_out, n_rows)
         batch = self._calls(table, lengths, n_rows)
         width = ((0 if q_out is None else self.nq) + 2 * self.nkv) * self.hd
         if qkv.dim() != 2 or tuple(qkv.shape) != (batch * n, width) or qkv.device != self.device or \
@@ -448,13 +452,17 @@ class PagedCache:
             self._rows(q_out, "q_out", batch, n)
         ld = qkv.stride(0) if qkv.shape[0] > 1 else width
         capi.dflash_paged_append(self.pages, layer, capi.F32 if qkv.dtype == torch.float32 else capi.BF16, qkv, ld,
-                                 batch, n, n_rows, table, table.shape[1], lengths, q_out, self.ws)
+                                 batch, n, n_rows, table, table.shape[1], lengths, q_out, self.ws, stream)
 
     def attention(self, layer, q, table, lengths, out, causal=True, window=0, sinks=0, n_rows=None, shared_len=None):
         """Attention of ``q`` [batch][n][n_q][head_dim] over the pages into
         ``out``.  ``window`` > 0 hides keys behind it but the first ``sinks``;
         ``shared_len`` (one device int32) says how many first positions all
         sequences share, to be read once for the batch."""
+        stream = torch.cuda.current_stream()
+        if stream.device_index != self.device.index:
+            with torch.cuda.device(self.device):
+                return self.attention(layer, q, table, lengths, out, causal, window, sinks, n_rows, shared_len)
         batch = self._calls(table, lengths, n_rows)
         if not batch or q.dim() != 4 or q.shape[0] != batch:
             raise ValueError("q is [batch][n][n_q][head_dim]")
@@ -463,9 +471,9 @@ class PagedCache:
         self._rows(out, "out", batch, n)
         if shared_len is None:
             capi.dflash_paged_attention(self.pages, layer, q, batch, n, n_rows, int(causal), window, sinks, table,
-                                        table.shape[1], lengths, out, self.ws)
+                                        table.shape[1], lengths, out, self.ws, stream)
         else:
             if shared_len.dtype != torch.int32 or shared_len.device != self.device or shared_len.numel() != 1:
                 raise ValueError(f"shared_len is one int32 on {self.device}")
             capi.dflash_paged_attention_shared(self.pages, layer, q, batch, n, n_rows, int(causal), window, sinks, table,
-                                               table.shape[1], lengths, shared_len, out, self.ws)
+                                               table.shape[1], lengths, shared_len, out, self.ws, stream)
