@@ -53,6 +53,11 @@ static bool apart(const void* a, long long abytes, const void* b, long long bbyt
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x + (uintptr_t)abytes <= y || y + (uintptr_t)bbytes <= x;
 }
+static int elem_size(int dtype) { return dtype == DFLASH_F32 ? 4 : 2; }
+static long long pool_bytes(const dflash_pages* p) { return pool_rows(p) * p->hd * elem_size(p->dtype); }
+static bool apart_from_pool(const dflash_pages* p, const void* a, long long bytes) {
+  return apart(a, bytes, p->k, pool_bytes(p)) && apart(a, bytes, p->v, pool_bytes(p));
+}
 
 extern "C" {
 
@@ -185,8 +190,10 @@ int dflash_paged_append(dflash_pages* p, int32_t layer, int32_t in_dtype, const 
   REQ(ld >= (long long)(nq + 2 * p->nkv) * p->hd && aligned16(q_out));
   REQ((reinterpret_cast<uintptr_t>(qkv) & (in_dtype == DFLASH_F32 ? 3 : 1)) == 0);
   const long long rows = (long long)batch * n, width = (long long)(nq + 2 * p->nkv) * p->hd;
-  REQ(!q_out || apart(qkv, ((rows - 1) * ld + width) * (in_dtype == DFLASH_F32 ? 4 : 2), q_out,
-                      rows * p->nq * p->hd * (p->dtype == DFLASH_F32 ? 4 : 2)));
+  const long long qkv_bytes = ((rows - 1) * ld + width) * elem_size(in_dtype);
+  const long long q_bytes = rows * p->nq * p->hd * elem_size(p->dtype);
+  REQ(!q_out || (apart(qkv, qkv_bytes, q_out, q_bytes) && apart_from_pool(p, q_out, q_bytes)));
+  REQ(apart_from_pool(p, qkv, qkv_bytes) && apart(p->k, pool_bytes(p), p->v, pool_bytes(p)));
   REQ(on_device(p->device) && ws->device == p->device);
   CK(paged_append(in_dtype, p->dtype, qkv, ld, batch, n, nq, p->nkv, p->hd, n_rows, table, table_stride, len, p->rope,
                   p->max_pos, p->n_pages, p->page_size, (long long)layer * p->n_pages, q_out, p->k, p->v, ws->status,
@@ -203,8 +210,8 @@ static int attend(dflash_pages* p, int32_t layer, const void* q, int32_t batch, 
   REQ(batch <= ws->max_batch && (long long)batch * n <= ws->max_rows);
   REQ(ws->nq == p->nq && ws->nkv == p->nkv && ws->hd == p->hd);
   REQ(aligned16(q) && aligned16(out));
-  const long long q_bytes = (long long)batch * n * p->nq * p->hd * (p->dtype == DFLASH_F32 ? 4 : 2);
-  REQ(apart(q, q_bytes, out, q_bytes));
+  const long long q_bytes = (long long)batch * n * p->nq * p->hd * elem_size(p->dtype);
+  REQ(apart(q, q_bytes, out, q_bytes) && apart_from_pool(p, out, q_bytes));
   REQ(on_device(p->device) && ws->device == p->device);
   if ((long long)table_stride * p->page_size > (1ll << 30)) return DFLASH_ERR_TOO_LARGE;
   PagedGeom g = {};

@@ -511,8 +511,8 @@ int dflash_paged_status(dflash_paged_workspace *w, dflash_stream_t stream, int32
  * q_out NULL: the rows hold k|v only (injected context).  in_dtype is the type
  * of qkv: the model dtype, or float32 (the weight product's result).  qkv may
  * have any alignment of its type; rows on 16-byte boundaries are read in wide
- * loads.  q_out and qkv do not overlap, and no two rows of one call may name the
- * same slot. */
+ * loads.  q_out, qkv and the two pools do not overlap (ERR_INVALID_ARG), and no
+ * two rows of one call may name the same slot. */
 int dflash_paged_append(dflash_pages *p, int32_t layer, int32_t in_dtype, const void *qkv, int64_t ld,
                         int32_t batch, int32_t n, const int32_t *n_rows, const int32_t *table,
                         int32_t table_stride, const int32_t *len, void *q_out, dflash_paged_workspace *ws,
@@ -520,7 +520,7 @@ int dflash_paged_append(dflash_pages *p, int32_t layer, int32_t in_dtype, const 
 
 /* Attention over pages.  q [batch][n][nq][hd] (rotated, model dtype, 16-byte
  * aligned), the rows' own keys and values already appended; out likewise,
- * apart from q.
+ * apart from q and from the pools (ERR_INVALID_ARG).
  * Row (b, i) at position p = len[b] + i sees key j of its sequence when
  *   causal      j <= p            and (j > p - window or j < sinks),
  *   not causal  j < len[b] + n_rows[b]  and (j >= len[b] - window or j < sinks);

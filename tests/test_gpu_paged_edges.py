@@ -249,3 +249,37 @@ def test_attention_reports_positions_that_the_handle_does_not_hold(dtype, B):
     rows = i32([4, 0] + [4] * (B - 2))
     cache.attention(0, q, x.table, lens, out, n_rows=rows)
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_results_over_the_pool_are_refused(dtype):
+    """A result inside a pool, rows to append that lie in one, and an append to pools that share memory would
+    race with the call's own reads and writes."""
+    x = Batch(dtype, 4, 1, 128, 16, [40, 5], 4)
+    q, pools = x.query(), torch.zeros(3, *x.k.shape, dtype=x.dt, device="cuda")
+    size, each = q.numel(), x.k.numel()
+    flat = pools.view(-1)
+    cache = PagedCache(shape_of(4, 1, 128), dtype, x.k.shape[1], 16, 64, 8, k=pools[0], v=pools[1])
+    qkv = x.normal(8, 6 * 128)
+
+    def refused(call):
+        with pytest.raises(capi.DFlashError) as e:
+            call()
+        assert e.value.code == capi.ERR_INVALID_ARG
+
+    for at in (0, each - 8, each + 16, 2 * each - 8):
+        inside = flat[at:at + size].view(q.shape)
+        refused(lambda: cache.attention(0, q, x.table, x.len, inside))
+        refused(lambda: cache.attention(0, q, x.table, x.len, inside, shared_len=i32([0])))
+        refused(lambda: cache.append(0, qkv, x.table, x.len, 4, q_out=inside))
+    rows = flat[each - 8 * 6 * 128 + 8:][:8 * 6 * 128].view(8, 6 * 128)
+    refused(lambda: cache.append(0, rows, x.table, x.len, 4, q_out=q))
+    same = PagedCache(shape_of(4, 1, 128), dtype, x.k.shape[1], 16, 64, 8, k=pools[0], v=pools[0])
+    refused(lambda: same.append(0, qkv, x.table, x.len, 4, q_out=q))
+    assert (pools == 0).all() and cache.status() == 0
+    # right behind the pools, and reading one that serves as keys and values, is fine
+    out = flat[2 * each:2 * each + size].view(q.shape)
+    cache.append(0, qkv, x.table, x.len, 4, q_out=q)
+    cache.attention(0, q, x.table, x.len, out)
+    same.attention(0, q, x.table, x.len, out)
+    assert cache.status() == 0 and same.status() == 0 and torch.isfinite(out).all()
