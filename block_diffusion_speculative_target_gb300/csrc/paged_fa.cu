@@ -15,9 +15,11 @@
 //   The products' M dimension is filled with keys and dimensions, so few rows
 //   cost few columns, and all 128 threads of a group share the exponentials of
 //   however few rows there are.  Whether a row's reference has to move is one
-//   vote a tile.  With 16 rows P is kept as a bf16 pair hi + lo in neighbouring
-//   columns (2^-16 relative), which is free where keys are waited for; with 32 it
-//   would double the work on a weight, and P is rounded once.  S has two buffers,
+//   vote a tile.  With 16 and 32 rows P is kept as a bf16 pair hi + lo in
+//   neighbouring columns (2^-16 relative): the product has 64 columns anyway, and
+//   splitting the weights costs nothing where keys are waited for (8 blocks of 8
+//   rows over 2K..6K keys 50.5 -> 51.9 us, 32 of them 123 -> 127).  With 64 the
+//   pair would take 128 columns, and P is rounded once.  S has two buffers,
 //   and K runs ahead of V in the ring: the next scores are there before a tile's
 //   weights are done.  An item is one block of rows, whose key tiles the groups
 //   take in turn (a shared prefix's of more than NR rows: half of them each, and
@@ -1099,7 +1101,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             scr[qr * NR + at] = x[0];
           }
         };
-        constexpr bool kPair = NR == 16;
+        constexpr bool kPair = NR <= 32;
         constexpr bool kRegRef = NR <= 32;      // (registers for the references too)
         float Ls[NR], nm[kRegRef ? NR : 2];     // row sums of this thread's keys; -M
 #pragma unroll
@@ -1188,7 +1190,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // 32 rows the weights are computed while the votes come in (with 64 their sums would need registers
           // that are not there).
           volatile uint32_t* votes = vote_w + (sb * 2 + gq) * 4;  // (two sets: a warp may be a tile ahead)
-          uint32_t hi[NR / 2], lo[kPair ? NR / 2 : 1];
+          uint32_t hi[NR / 2], lo[NR == 16 ? NR / 2 : 1];
           auto add_sum = [&](int c) {
             const float2 l = add2(make_float2(Ls[c], Ls[c + 1]), make_float2(v[c], v[c + 1]));
             Ls[c] = l.x;
@@ -1200,9 +1202,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               v[c] = ex2f(v[c]);
               v[c + 1] = ex2f(v[c + 1]);
               if constexpr (!kRegRef) add_sum(c);
-              if constexpr (kPair) {
+              if constexpr (NR == 16) {
                 pack_bf16_hilo(v[c], v[c + 1], hi[c / 2], lo[c / 2]);
-              } else {
+              } else if constexpr (!kPair) {
                 const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[c], v[c + 1]);
                 hi[c / 2] = *reinterpret_cast<const uint32_t*>(&h2);
               }
@@ -1350,9 +1352,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint8_t* prow = pbuf + r * 128;
 #pragma unroll
             for (int c = 0; c < NR / 8; ++c) {
+              if constexpr (NR == 32) {  // (both parts only here: registers)
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pack_bf16_hilo(v[8 * c + 2 * e], v[8 * c + 2 * e + 1], h[e], l[e]);
+                *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(prow + ((c + 4 ^ (r & 7)) << 4)) = make_uint4(l[0], l[1], l[2], l[3]);
+                continue;
+              }
               *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
                   make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-              if constexpr (kPair)
+              if constexpr (NR == 16)
                 *reinterpret_cast<uint4*>(prow + ((c + NR / 8 ^ (r & 7)) << 4)) =
                     make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
             }

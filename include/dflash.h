@@ -528,7 +528,12 @@ int dflash_paged_append(dflash_pages *p, int32_t layer, int32_t in_dtype, const 
  * window slides with each row; the other is dflash_attention's, the drafter's
  * cross-context window, with first tokens kept.  scale 1 / sqrt(hd), softmax
  * in float32; a row's result depends on the keys it sees only, whatever values
- * lie in hidden or unused slots.  The keys are split over the GPU by all
+ * lie in hidden or unused slots.  In bf16 a softmax weight enters the product
+ * with the values as a pair of bf16, off by 2^-16 of itself, where a sequence has
+ * at most 32 rows n * nq / nkv (with a shared length: the batch at most 16), and
+ * rounded to bf16 once, 2^-8 of itself, beyond: there a block's row and the same
+ * row as a single token may differ by 2^-8 of the attention of |values|, besides
+ * their own rounding.  The keys are split over the GPU by all
  * lengths of the call, so the last bits of a row may depend on the batch it is
  * in (dflash_attention, which fixes the split per cache, has no such
  * dependence); equal calls give equal bits.

@@ -283,3 +283,33 @@ def test_results_over_the_pool_are_refused(dtype):
     cache.attention(0, q, x.table, x.len, out)
     same.attention(0, q, x.table, x.len, out)
     assert cache.status() == 0 and same.status() == 0 and torch.isfinite(out).all()
+
+
+# one token's and up to 32 stacked rows; more
+STACKS = [(1, 4, 128), (4, 4, 128), (5, 4, 128), (8, 4, 128), (6, 5, 64), (32, 1, 64), (16, 4, 128), (13, 5, 64), (40, 4, 128)]
+
+
+@pytest.mark.parametrize("n,G,hd", STACKS, ids=[f"{n * G}x{hd}" for n, G, hd in STACKS])
+def test_a_row_in_a_block_and_as_a_token(n, G, hd):
+    """Row i of a block against the definition and against the same row as a single token of the position.
+    u = 2^-24.  Up to 32 stacked rows a weight enters the product as hi + lo of bf16: lo is the rest of the
+    first rounding (2^-8 of the weight at most) rounded once more, so the pair is off by 2^-16 of the weight
+    and the sum by 2^-16 of the attention of |values|; beyond, by 2^-8 of it.  The result is rounded once
+    (2^-8 of itself); float32 sums as in `bound`."""
+    x = Batch("bf16", 2 * G, 2, hd, 32, [3000, 700], n, seed=n + G)
+    q = x.query()
+    token = PagedCache(shape_of(2 * G, 2, hd), "bf16", x.k.shape[1], 32, x.cols * 32, 2, k=x.k, v=x.v)
+    for kw in (dict(), dict(window=500, sinks=70)):
+        ref, mag, dots, most = reference(x, q, **kw)
+        sums = mag * 2.0 ** -24 * (2 * ((hd + 2) * dots + 4) + 2 * most + 16)
+        pair = sums + 2.0 ** -16 * mag
+        pair = pair + 2.0 ** -8 * (ref.abs() + pair)
+        lim = pair if n * G <= 32 else pair + 2.0 ** -8 * (1 + 2.0 ** -8) * mag
+        out = attend(x, q, **kw)
+        assert ((out.double() - ref).abs() <= lim).all(), kw
+        for i in range(0, n, max(1, n // 4)):
+            one = torch.full_like(q[:, i:i + 1].contiguous(), 77.0)
+            token.attention(0, q[:, i:i + 1].contiguous(), x.table, x.len + i, one, **kw)
+            assert ((one[:, 0].double() - ref[:, i]).abs() <= pair[:, i]).all(), (i, kw)
+            assert ((one[:, 0].double() - out[:, i].double()).abs() <= pair[:, i] + lim[:, i]).all(), (i, kw)
+    assert x.cache.status() == 0 and token.status() == 0
