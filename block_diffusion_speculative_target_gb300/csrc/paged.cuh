@@ -48,7 +48,7 @@ struct PagedGeom {
   float2* part_ml;
   long long pre_row0;    // first partial row of the prefix slots
   int slot_s, slot_p;    // partial rows per suffix / prefix slot
-  int32_t* plan;         // [8 + batch + 1] written for the merge kernel
+  int32_t* plan;         // [kPlanCum + batch] written for the merge kernel
   int32_t* tickets;      // [items] pieces done, zero between calls
   int32_t* records;      // [CTAs][8] items to join after the kernel
   unsigned g_magic;      // ceil(2^32 / G)
@@ -61,9 +61,9 @@ constexpr int kPagedMaxG = 64;
 // CTAs a SM of an attention kernel at most (bounds the partial slots).
 constexpr int kPagedMaxCtas = 4;
 
-// plan[]: kPlanT tiles of the line, quota, sh / KT, tiles of a prefix item; then the
-// line position of each sequence's first suffix item and the line's end.
-enum { kPlanT = 0, kPlanQuota = 1, kPlanShared = 2, kPlanPre = 3, kPlanCum = 8 };
+// plan[]: quota, sh / KT, tiles of a prefix item; then the line position of each
+// sequence's first suffix item.
+enum { kPlanQuota = 0, kPlanShared = 1, kPlanPre = 2, kPlanCum = 4 };
 
 // `early`: a pass that comes before the call's arrays can be read.  None of them is; every sequence counts as n
 // rows behind all the keys that its table can name.
@@ -270,7 +270,6 @@ __device__ __forceinline__ PlanView plan_small(const PagedGeom& g, bool write, b
   v.cum = __shfl_sync(0xffffffffu, hit_at, src);
   if (!here) v.b = g.batch;
   if (write && g.shared && lane == 0) {
-    g.plan[kPlanT] = v.T;
     g.plan[kPlanQuota] = v.quota;
     g.plan[kPlanShared] = v.sh_tiles;
     g.plan[kPlanPre] = v.pre_tiles;
@@ -357,11 +356,9 @@ __device__ __forceinline__ PlanView plan_view(const PagedGeom& g, int* red, bool
     at += c;
   }
   if (first_cta && tid == 0) {
-    g.plan[kPlanT] = v.T;
     g.plan[kPlanQuota] = v.quota;
     g.plan[kPlanShared] = v.sh_tiles;
     g.plan[kPlanPre] = v.pre_tiles;
-    g.plan[kPlanCum + g.batch] = tot;
   }
   __syncthreads();
   v.b = res[0];

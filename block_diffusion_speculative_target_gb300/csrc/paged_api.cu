@@ -24,7 +24,7 @@ struct dflash_paged_workspace {
   long long part_rows;
   float* part_o;     // [part_rows][hd]
   float2* part_ml;   // [part_rows]
-  int32_t* plan;     // [kPlanCum + max_batch + 1]
+  int32_t* plan;     // [kPlanCum + max_batch]
   int32_t* tickets;  // [items]
   int32_t* records;  // [CTAs][8]
   size_t ticket_bytes;
@@ -134,7 +134,7 @@ int dflash_paged_workspace_alloc(const dflash_model_desc* d, int32_t max_batch, 
     size_t bytes;
   } reqs[] = {{(void**)&w->part_o, (size_t)w->part_rows * d->head_dim * 4},
               {(void**)&w->part_ml, (size_t)w->part_rows * 8},
-              {(void**)&w->plan, (size_t)(kPlanCum + max_batch + 1) * 4},
+              {(void**)&w->plan, (size_t)(kPlanCum + max_batch) * 4},
               {(void**)&w->tickets, w->ticket_bytes},
               {(void**)&w->records, (size_t)num_sms() * kPagedMaxCtas * 32},
               {(void**)&w->status, 4}};

@@ -17,13 +17,11 @@
 //   however few rows there are.  Whether a row's reference has to move is one
 //   vote a tile.  With 16 and 32 rows P is kept as a bf16 pair hi + lo in
 //   neighbouring columns (2^-16 relative): the product has 64 columns anyway, and
-//   splitting the weights costs nothing where keys are waited for (8 blocks of 8
-//   rows over 2K..6K keys 50.5 -> 51.9 us, 32 of them 123 -> 127).  With 64 the
-//   pair would take 128 columns, and P is rounded once.  S has two buffers,
-//   and K runs ahead of V in the ring: the next scores are there before a tile's
-//   weights are done.  An item is one block of rows, whose key tiles the groups
-//   take in turn (a shared prefix's of more than NR rows: half of them each, and
-//   every key tile).
+//   splitting the weights costs 1 to 3% (with 32 rows: 8 blocks of 8 over 2K..6K
+//   keys 50.5 -> 51.9 us, 32 of them 123 -> 127).  With 64 the pair would take 128
+//   columns, and P is rounded once.  S has two buffers, and K runs two tiles ahead
+//   of V in the ring: the next scores are there before a tile's weights are done.
+//   An item's key tiles are taken by the groups in turn.
 // rows as rows (more rows: chunks, shared prefixes)
 //   S = Q K_t^T            128 rows by 64 keys (half a tile), two buffers: a thread
 //                          holds one row
@@ -314,7 +312,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pv = plan_view<KT, kTcThreads>(g, red);
   }
   // Order of an item's tiles in the ring: keys run `ahead` tiles ahead of values.
-  auto ahead_of = [&](bool cols, bool two) { return !cols ? 0 : two ? 1 : 2; };
+  auto ahead_of = [](bool cols) { return cols ? 2 : 0; };
   auto k_at = [](int t, int ahead) { return t + max(0, t - ahead); };
   auto v_at = [](int t, int ahead, int nt) { return min(nt, t + ahead + 1) + t; };
   // query buffers: an item with one tile takes the buffer after the last one's, an item with two both
@@ -358,7 +356,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (use) set_status(g.status, DFLASH_STATUS_BOUNDS);
           return pool_rows;
         };
-        const int ahead = ahead_of(as_columns(pc.prefix), pc.two);
+        const int ahead = ahead_of(as_columns(pc.prefix));
         // the rows of the next tiles: [0] the next value tile's, [ahead] the next key tile's
         int rowq[3];
         {
@@ -421,18 +419,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       while (ok && (ok = wait_piece(seg))) {
         const int nt = pieces[seg & 3].nt;
         if (nt == 0) break;
-        const bool cols = as_columns(pieces[seg & 3].prefix), two = pieces[seg & 3].two, qtwo = two && !cols;
+        const bool cols = as_columns(pieces[seg & 3].prefix), two = pieces[seg & 3].two;
         done_piece(seg);
-        const int ahead = ahead_of(cols, two);
-        const int buf = qtwo ? gq : qt;
-        if (qtwo || qt == 0) ok = wait(&q_full[0], qn0);
-        if (ok && (qtwo || qt == 1)) ok = wait(&q_full[1], qn1);
+        const int ahead = ahead_of(cols);
+        const int buf = two ? gq : qt;
+        if (two || qt == 0) ok = wait(&q_full[0], qn0);
+        if (ok && (two || qt == 1)) ok = wait(&q_full[1], qn1);
         if (ok && !two && gq >= nt) {  // no tile for this group
           if (seg > 0) ok = wait(&o_free[gq], seg - 1);
           if (ok && elect_one()) mbar_arrive(&q_empty[buf]);
         }
-        // (rows as columns: group 1 of a shared block has the rows behind group 0's NR)
-        const uint8_t* qs = sm + L::kQ + buf * L::kQBuf + (two && cols ? gq * NR * 128 : 0);
+        const uint8_t* qs = sm + L::kQ + buf * L::kQBuf;
         if (cols) {
           int kjob = job;  // keys run ahead
           for (int u = 0; ok && u < nt + ahead; ++u) {
@@ -440,7 +437,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int x = 2 * tiles + k_at(u, ahead), sk = x % NS;
               ok = wait(&full[sk], x / NS);
               if (!ok) break;
-              if (!two && (u & 1) != gq) {  // the other group's tile
+              if ((u & 1) != gq) {  // the other group's tile
                 if (elect_one()) mbar_arrive(&empty[sk]);
               } else {
                 // (after the other layout: its last P lies where these scores go)
@@ -460,7 +457,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   tc_commit(&empty[sk]);
                   // The last scores of the piece: the query tile is free after them.  (Where the other layout comes
                   // first, it is free after the last product: the hand-over below counts on it.)
-                  if (TP && u + (two ? 1 : 2) >= nt) tc_commit(&q_empty[buf]);
+                  if (TP && u + 2 >= nt) tc_commit(&q_empty[buf]);
                 }
                 __syncwarp();
                 ++kjob;
@@ -470,10 +467,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int t = u - ahead, x = 2 * tiles + v_at(t, ahead, nt), sv = x % NS;
               ok = wait(&full[sv], x / NS);
               if (!ok) break;
-              if (!two && (t & 1) != gq) {
+              if ((t & 1) != gq) {
                 if (elect_one()) mbar_arrive(&empty[sv]);
               } else {
-                const bool first = t == (two ? 0 : gq);
+                const bool first = t == gq;
                 if (elect_one()) mbar_arrive(&v_ready[gq]);
                 ok = wait(&p_full[2 * gq + (job & 1)], job >> 1);
                 if (ok && first && seg > 0) ok = wait(&o_free[gq], seg - 1);
@@ -490,7 +487,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                kk > 0 ? 1u : acc0);
                   tc_commit(&pv_done[2 * gq + (job & 1)]);
                   tc_commit(&empty[sv]);
-                  if (!TP && t + (two ? 1 : 2) >= nt) tc_commit(&q_empty[buf]);
+                  if (!TP && t + 2 >= nt) tc_commit(&q_empty[buf]);
                 }
                 __syncwarp();
                 ++job;
@@ -581,9 +578,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tiles += nt;
         ++seg;
-        if (qtwo || qt == 0) ++qn0;
-        if (qtwo || qt == 1) ++qn1;
-        if (!qtwo) qt ^= 1;
+        if (two || qt == 0) ++qn0;
+        if (two || qt == 1) ++qn1;
+        if (!two) qt ^= 1;
       }
       if (elect_one()) tc_commit(&drain[gq]);
       mbar_wait(&drain[gq], 0, kTcWaitNs / 4);
@@ -626,7 +623,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           pc.P = min(paged_len(g, sg.b, seg < 0), g.cap);
           pc.x0 = sg.rt * (sg.prefix ? g.rp : g.ri);
           pc.rows = sg.prefix ? min(g.rp, g.batch * g.n * g.G - pc.x0) : min(g.ri, pc.n * g.G - pc.x0);
-          pc.two = pc.rows > (as_columns(sg.prefix) ? NR : 128);
+          pc.two = pc.rows > 128;  // (rows as columns: never)
           pc.s0 = sg.span.s0;
           pc.sn = sg.span.s1 - sg.span.s0;
           pc.w0 = sg.span.w0;
@@ -680,7 +677,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (!more) break;
         const int rows = pc.rows;
-        const bool cols = as_columns(pc.prefix), two = !cols && pc.two;
+        const bool cols = as_columns(pc.prefix), two = pc.two;
         for (int w = 0; ok && w < (two ? 2 : 1); ++w) {
           const int buf = two ? w : qt;
           int& used = buf ? qn1 : qn0;
@@ -1084,11 +1081,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ------------------------------------------------ rows as columns: thread = key r of the tile
         const Piece& pc = pieces[seg & 3];
         const int nt = dry ? 2 : pc.nt;
-        const bool two = !dry && pc.two, whole = pc.whole;
-        const int rbase = two ? gq * NR : 0, rows = two ? min(NR, pc.rows - rbase) : pc.rows;  // the group's rows
-        const int t0 = two ? 0 : gq, step = two ? 1 : 2, ahead = ahead_of(true, two);
-        const bool has = t0 < nt, both = !two && nt > 1;
-        const int x0 = pc.x0 + rbase;  // the group's first row
+        const bool whole = pc.whole;
+        const int rows = pc.rows, x0 = pc.x0, ahead = ahead_of(true);
+        const bool has = gq < nt, both = nt > 1;
         float* ref = reinterpret_cast<float*>(sm + L::kRef) + gq * 64;
         uint8_t* pbuf = sm + L::kQ + gq * L::kQBuf + L::kP;
         float* scr = reinterpret_cast<float*>(pbuf);  // scratch wherever no product reads P
@@ -1107,8 +1102,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int c = 0; c < NR; ++c) Ls[c] = 0.f;
         if (!meet(&fix[gq], fn)) break;  // the scratch's last readers are past it
-        for (int t = t0; ok && t < nt; t += step) {  // (once when dry)
-          const bool first = t == t0;
+        for (int t = gq; ok && t < nt; t += 2) {  // (once when dry)
+          const bool first = t == gq;
           const int k0 = pc.tile(t) * KT, key = k0 + r;
           const bool inner = dry || (k0 >= pc.all_lo && k0 + KT <= pc.all_hi);
           const int sb = job & 1;  // score buffer
@@ -1164,7 +1159,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (pc.prefix) {  // (a window over a prefix: the rows' sequences differ)
 #pragma unroll 1
                 for (int c = 0; c < rows; ++c) {
-                  const ItemRow w = item_row(g, true, 0, pc.hk, pc.x0, rbase + c);
+                  const ItemRow w = item_row(g, true, 0, pc.hk, x0, c);
                   int sink, lo, hi;
                   row_span(g, paged_len(g, w.b), paged_rows(g, w.b), w.i, sink, lo, hi);
                   if (key < sink || (key >= lo && key < hi)) see |= 1ull << c;
@@ -1334,9 +1329,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = meet(&fix[gq], fn);
               }
               if (!ok) break;
-              // (a tile that both groups work on is cleaned once both have taken from it)
-              ok = two ? meet(&fix[2], fb) : meet(&fix[gq], fn);
-              if (!ok) break;
               if (bad) clean_row(vt, r, 0, HD / 8);
             }
           }
@@ -1396,24 +1388,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         float2 other = make_float2(-INFINITY, 0.f);
-        if (!two) {
-          if (gq == 1) {
-            if (xn > 0 && stop(wait_phase(x_free, (uint32_t)(xn - 1) & 1u, abort_f, g.status))) break;
-            if (r < NR) xch[r] = make_float2(M, Lr);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(x_full);
-          } else {
-            if (stop(wait_phase(x_full, (uint32_t)xn & 1u, abort_f, g.status))) break;
-            if (r < NR) other = xch[r];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(x_free);
-          }
-          ++xn;
+        if (gq == 1) {
+          if (xn > 0 && stop(wait_phase(x_free, (uint32_t)(xn - 1) & 1u, abort_f, g.status))) break;
+          if (r < NR) xch[r] = make_float2(M, Lr);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(x_full);
+        } else {
+          if (stop(wait_phase(x_full, (uint32_t)xn & 1u, abort_f, g.status))) break;
+          if (r < NR) other = xch[r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(x_free);
         }
-        if (two || gq == 0) {
+        ++xn;
+        if (gq == 0) {
           float2* coef = reinterpret_cast<float2*>(scr + 8 * NR);
-          const long long prow = pc.slot_row + rbase;
+          const long long prow = pc.slot_row;
           if (r < NR) {
             const float Mx = fmaxf(M, other.x), ref0 = Mx == -INFINITY ? 0.f : Mx;
             const float wa = M == -INFINITY ? (both ? 0.f : 1.f) : ex2f(M - ref0);
@@ -1471,8 +1461,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&o_free[gq]);
-            if (!two) mbar_arrive(&o_free[1]);
+            mbar_arrive(&o_free[0]);
+            mbar_arrive(&o_free[1]);
           }
           if (NR == 16 && !whole && pc.nc > 0 && !join(pc)) break;  // (few rows; else a kernel does)
         }
