@@ -40,11 +40,12 @@ namespace dfl {
 
 constexpr uint64_t kGemmWaitNs = 500000000ull;  // 500 ms per wait
 
-// Limit of the main-loop waits (ring slots, accumulator); the drain after a
+// Limit of the main-loop waits (ring slots, accumulator; and those of attention over pages); the drain after a
 // time-out always waits the full kGemmWaitNs / 4 so that copies and products
 // in flight complete before shared memory and TMEM are released.  Lowered only
 // by dflash_debug_set_wait_limit (failure-path tests).
 static std::atomic<unsigned long long> g_wait_ns{kGemmWaitNs};
+unsigned long long wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
 void set_gemm_wait_ns(long long ns) { g_wait_ns.store(ns < 0 ? kGemmWaitNs : (unsigned long long)ns); }
 
 template <int BN, int STAGES>
@@ -930,7 +931,7 @@ static cudaError_t launch_cl(const CUtensorMap& tw, const CUtensorMap& tx, const
   cfg.numAttrs = 2;
   count_launch();
   return cudaLaunchKernelEx(&cfg, gemm_cl_kernel<BN, STAGES>, tw, tx, epi, rows, K, S, status,
-                            (uint64_t)g_wait_ns.load(std::memory_order_relaxed));
+                            (uint64_t)wait_limit_ns());
 }
 
 cudaError_t gemm_bf16(const void* X, int ldx, int rows, const void* W, int M, int K, const GemmEpi& epi, int* status,

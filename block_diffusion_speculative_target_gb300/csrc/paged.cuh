@@ -52,6 +52,7 @@ struct PagedGeom {
   int32_t* tickets;      // [items] pieces done, zero between calls
   int32_t* records;      // [CTAs][8] items to join after the kernel
   unsigned g_magic;      // ceil(2^32 / G)
+  unsigned wait_ns;      // limit of a wait in the tensor-core kernel
   int* status;
 };
 

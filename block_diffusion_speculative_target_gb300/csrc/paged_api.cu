@@ -174,7 +174,7 @@ int dflash_paged_status(dflash_paged_workspace* w, dflash_stream_t stream, int32
   CK(cudaMemcpyAsync(&v, w->status, 4, cudaMemcpyDeviceToHost, s));
   CK(cudaMemsetAsync(w->status, 0, 4, s));  // (in the stream's order: the next call's bits stay)
   CK(cudaStreamSynchronize(s));
-  // a call that timed out may have left pieces counted
+  // a call that timed out may have left pieces counted: until here later results may be wrong too
   if (v & DFLASH_STATUS_TIMEOUT) CK(cudaMemsetAsync(w->tickets, 0, w->ticket_bytes, s));
   *status_out = v;
   return DFLASH_OK;
@@ -239,6 +239,7 @@ static int attend(dflash_pages* p, int32_t layer, const void* q, int32_t batch, 
   g.tickets = ws->tickets;
   g.records = ws->records;
   g.status = ws->status;
+  g.wait_ns = (unsigned)std::min(wait_limit_ns(), 4000000000ull);
   if (!paged_line_fits(g, p->dtype == DFLASH_BF16 ? paged_rule_tc(g) : paged_rule_core(g))) return DFLASH_ERR_TOO_LARGE;
   if (p->dtype == DFLASH_BF16)
     CK(paged_attention_tc(p->hd, g, p->tk, p->tv, pool_rows(p), q, out, ws->part_rows, (cudaStream_t)stream));

@@ -56,8 +56,9 @@
 //     (products alone 1.3), a row's 128 exponentials by one thread
 // Rows as columns and not as rows for up to 64 rows: 128 rows' worth of exponentials would be computed for 4.
 //
-// Every wait is bounded; one that gives up sets DFLASH_STATUS_TIMEOUT, the CTA
-// stops, and drains its copies and products before it releases TMEM.
+// Every wait is bounded (PagedGeom::wait_ns); one that gives up sets
+// DFLASH_STATUS_TIMEOUT, the CTA stops, and drains its copies and products,
+// whatever the limit, before it releases TMEM.
 #include <math.h>
 
 #include <algorithm>
@@ -71,7 +72,7 @@ namespace dfl {
 
 namespace {
 constexpr int kTcThreads = 384;
-constexpr uint64_t kTcWaitNs = 500000000ull;
+constexpr uint64_t kTcDrainNs = 125000000ull;
 constexpr float kNoRef = 3e38f;  // -M of a row that has seen no key: every score lies more than 8 above it
 
 template <int HD>
@@ -193,22 +194,24 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+__device__ __forceinline__ bool give_up(volatile int* abort_f, const PagedGeom& g) {
+  *abort_f = 1;
+  set_status(g.status, DFLASH_STATUS_TIMEOUT);
+  return false;
+}
 // Waits for a phase, giving up on the CTA's abort flag or after the limit (then raising the flag).
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_f, int* status) {
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_f,
+                                           const PagedGeom& g) {
 #pragma unroll 1
   for (int i = 0; i < 64; ++i)
     if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
+  const uint32_t t0 = global_ns_lo();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*abort_f) return false;
-    if (global_ns() - t0 > kTcWaitNs) {
-      *abort_f = 1;
-      set_status(status, DFLASH_STATUS_TIMEOUT);
-      return false;
-    }
+    if (global_ns_lo() - t0 > g.wait_ns) return give_up(abort_f, g);
   }
 }
 
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   auto stop = [&](bool ok) { return __any_sync(0xffffffffu, !ok); };
   // The pieces of the run come from warp 3 through a ring of four.
   auto wait_piece = [&](int s) {
-    return !stop(wait_phase(&pc_full[s & 3], (uint32_t)(s >> 2) & 1u, abort_f, g.status));
+    return !stop(wait_phase(&pc_full[s & 3], (uint32_t)(s >> 2) & 1u, abort_f, g));
   };
   auto done_piece = [&](int s) {
     __syncwarp();
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int kv = 0; kv < 2; ++kv) {
             if (kv == 0 ? u >= nt : u < ahead) continue;
             const int s = tiles % NS;
-            if (tiles >= NS && stop(wait_phase(&empty[s], (uint32_t)(tiles / NS - 1) & 1u, abort_f, g.status))) {
+            if (tiles >= NS && stop(wait_phase(&empty[s], (uint32_t)(tiles / NS - 1) & 1u, abort_f, g))) {
               ok = false;
               break;
             }
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         done_piece(seg);
       }
       // the last copies land before the CTA leaves, whatever became of their readers
-      for (int x = max(0, tiles - NS); x < tiles; ++x) mbar_wait(&full[x % NS], (uint32_t)(x / NS) & 1u, kTcWaitNs / 4);
+      for (int x = max(0, tiles - NS); x < tiles; ++x) mbar_wait(&full[x % NS], (uint32_t)(x / NS) & 1u, kTcDrainNs);
     } else if (warp < 3) {
       // ---------------------------------------------------------- products of group gq
       const int gq = warp - 1;
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t idSt = idesc_bf16_f32(128, NR > 0 ? NR : 16);
       const uint32_t idOt = idesc_bf16_f32(128, 64) | (3u << 15);  // values and weights both MN-major
       const uint32_t tS = tmem + gq * 128, tO = tmem + 256 + gq * 128;
-      auto wait = [&](uint64_t* b, uint32_t parity) { return !stop(wait_phase(b, parity & 1u, abort_f, g.status)); };
+      auto wait = [&](uint64_t* b, uint32_t parity) { return !stop(wait_phase(b, parity & 1u, abort_f, g)); };
       int job = 0;
       bool ok = true;
       pdl_wait();
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!two) qt ^= 1;
       }
       if (elect_one()) tc_commit(&drain[gq]);
-      mbar_wait(&drain[gq], 0, kTcWaitNs / 4);
+      mbar_wait(&drain[gq], 0, kTcDrainNs);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- pieces, query rows
@@ -649,7 +652,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                        "r"(pc.whole));  // (computed here too)
           continue;
         }
-        if (seg >= 4) ok = !stop(wait_phase(&pc_empty[seg & 3], (uint32_t)((seg >> 2) - 1) & 1u, abort_f, g.status));
+        if (seg >= 4) ok = !stop(wait_phase(&pc_empty[seg & 3], (uint32_t)((seg >> 2) - 1) & 1u, abort_f, g));
         if (!ok) break;
         if (lane == 0) {
           pieces[seg & 3] = pc;
@@ -676,12 +679,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         if (!more) break;
+        if (g.wait_ns == 0) {  // (a limit of 0 has expired before the first poll)
+          give_up(abort_f, g);
+          break;
+        }
         const int rows = pc.rows;
         const bool cols = as_columns(pc.prefix), two = pc.two;
         for (int w = 0; ok && w < (two ? 2 : 1); ++w) {
           const int buf = two ? w : qt;
           int& used = buf ? qn1 : qn0;
-          if (used > 0) ok = !stop(wait_phase(&q_empty[buf], (uint32_t)(used - 1) & 1u, abort_f, g.status));
+          if (used > 0) ok = !stop(wait_phase(&q_empty[buf], (uint32_t)(used - 1) & 1u, abort_f, g));
           if (!ok) break;
           constexpr int kChunks = HD / 8, kLanes = 32 / kChunks;  // 16-byte chunks a row, rows an iteration
           const int c = lane % kChunks;
@@ -746,7 +753,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto meet = [&](uint64_t* b, int& ph) {
       __syncwarp();
       if (lane == 0) mbar_arrive(b);
-      const bool good = !stop(wait_phase(b, (uint32_t)ph & 1u, abort_f, g.status));
+      const bool good = !stop(wait_phase(b, (uint32_t)ph & 1u, abort_f, g));
       ++ph;
       return good;
     };
@@ -844,7 +851,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool inner = k0 >= pc.all_lo && k0 + 64 <= pc.all_hi;  // the same for all warps of the item
           const uint32_t tH = tS + hf * 64;
           uint32_t& sn = hf ? sn1 : sn0;
-          if (stop(wait_phase(&s_full[2 * gq + hf], sn & 1u, abort_f, g.status))) {
+          if (stop(wait_phase(&s_full[2 * gq + hf], sn & 1u, abort_f, g))) {
             ok = false;
             break;
           }
@@ -852,7 +859,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // O may be changed once the last product is done (the one before it is: these scores came after it)
           auto wait_pv = [&]() {
             if (!first) {
-              ok = !stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g.status));
+              ok = !stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g));
               tc_fence_after();
             }
             return ok;
@@ -918,7 +925,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint8_t* vt = sm + (2 * (tiles + t) + 1) % NS * L::kTile;
             uint64_t* fx = two ? &fix[2] : &fix[gq];
             int& ph = two ? fb : fn;
-            ok = !stop(wait_phase(&v_ready[gq], (uint32_t)(vjob + own) & 1u, abort_f, g.status));
+            ok = !stop(wait_phase(&v_ready[gq], (uint32_t)(vjob + own) & 1u, abort_f, g));
             if (!ok) break;
             const int vkey = hf * 64 + (r & 63), c0 = (r >> 6) * (HD / 16);
             const bool bad = row_is_bad(vt, vkey, c0, HD / 16);
@@ -933,7 +940,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!wait_pv()) break;
                 if (first) {
                   // O starts here instead of in the first product, which must not overtake its last reader
-                  if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g.status));
+                  if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g));
                   if (!ok) break;
                   tc_fence_after();
                   zero_o(HD);
@@ -1000,18 +1007,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         vjob += own;
         if (!ok) break;
-        if (has && stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g.status))) break;
+        if (has && stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g))) break;
         // ---- the piece's end: group 0 joins both groups' parts of a single query tile, else each has its own
         float2 other = make_float2(-INFINITY, 0.f);
         if (!two) {
           if (gq == 1) {
-            if (xn > 0 && stop(wait_phase(x_free, (uint32_t)(xn - 1) & 1u, abort_f, g.status))) break;
+            if (xn > 0 && stop(wait_phase(x_free, (uint32_t)(xn - 1) & 1u, abort_f, g))) break;
             xch[r] = make_float2(M, Ls);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(x_full);
           } else {
-            if (stop(wait_phase(x_full, (uint32_t)xn & 1u, abort_f, g.status))) break;
+            if (stop(wait_phase(x_full, (uint32_t)xn & 1u, abort_f, g))) break;
             other = xch[r];
             __syncwarp();
             if (lane == 0) mbar_arrive(x_free);
@@ -1108,7 +1115,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool inner = dry || (k0 >= pc.all_lo && k0 + KT <= pc.all_hi);
           const int sb = job & 1;  // score buffer
           uint32_t& sn = sb ? sn1 : sn0;
-          if (!dry && stop(wait_phase(&s_full[2 * gq + sb], sn & 1u, abort_f, g.status))) {
+          if (!dry && stop(wait_phase(&s_full[2 * gq + sb], sn & 1u, abort_f, g))) {
             ok = false;
             break;
           }
@@ -1116,14 +1123,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // the last product has read P and left O to be changed
           bool pv_waited = first;
           auto wait_pv = [&]() {
-            if (!pv_waited) ok = !stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g.status));
+            if (!pv_waited) ok = !stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g));
             if (!pv_waited) tc_fence_after();
             pv_waited = true;
             return ok;
           };
           if (handover) {
-            ok = (qn0 == 0 || !stop(wait_phase(&q_empty[0], (uint32_t)(qn0 - 1) & 1u, abort_f, g.status))) &&
-                 (qn1 == 0 || !stop(wait_phase(&q_empty[1], (uint32_t)(qn1 - 1) & 1u, abort_f, g.status)));
+            ok = (qn0 == 0 || !stop(wait_phase(&q_empty[0], (uint32_t)(qn0 - 1) & 1u, abort_f, g))) &&
+                 (qn1 == 0 || !stop(wait_phase(&q_empty[1], (uint32_t)(qn1 - 1) & 1u, abort_f, g)));
             if (!ok) break;
             handover = false;
           }
@@ -1220,7 +1227,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               mbar_arrive(&fix[gq]);
             }
             if constexpr (kRegRef) weights();
-            ok = !stop(wait_phase(&fix[gq], (uint32_t)fn & 1u, abort_f, g.status));
+            ok = !stop(wait_phase(&fix[gq], (uint32_t)fn & 1u, abort_f, g));
             ++fn;
             if (!ok) break;
             move = votes[0] | votes[1] | votes[2] | votes[3];
@@ -1283,7 +1290,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint8_t* vt = sm + (2 * tiles + v_at(t, ahead, nt)) % NS * L::kTile;
             // (the last product's values had landed: this wait cannot take their phase for its own)
             if (!wait_pv()) break;
-            ok = !stop(wait_phase(&v_ready[gq], (uint32_t)vjob & 1u, abort_f, g.status));
+            ok = !stop(wait_phase(&v_ready[gq], (uint32_t)vjob & 1u, abort_f, g));
             if (!ok) break;
             const bool bad = row_is_bad(vt, r, 0, HD / 8);
             const uint32_t word = __ballot_sync(0xffffffffu, bad);
@@ -1293,7 +1300,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint32_t bw[4] = {bad_w[gq * 4], bad_w[gq * 4 + 1], bad_w[gq * 4 + 2], bad_w[gq * 4 + 3]};
             if (bw[0] | bw[1] | bw[2] | bw[3]) {
               if (first) {
-                if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g.status));
+                if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g));
                 if (!ok) break;
                 tc_fence_after();
                 zero_o(64);
@@ -1378,7 +1385,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---- the piece's end: row sums over the group, then group 0 joins both groups' parts
         float M = -INFINITY, Lr = 0.f;  // of row r (threads below NR)
         if (has) {
-          if (stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g.status))) break;
+          if (stop(wait_phase(&pv_done[2 * gq + (job - 1 & 1)], (uint32_t)(job - 1 >> 1) & 1u, abort_f, g))) break;
           warp_scatter<NR, false>(Ls, lane);
           to_scratch(Ls);
           if (!meet(&fix[gq], fn)) break;
@@ -1389,13 +1396,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         float2 other = make_float2(-INFINITY, 0.f);
         if (gq == 1) {
-          if (xn > 0 && stop(wait_phase(x_free, (uint32_t)(xn - 1) & 1u, abort_f, g.status))) break;
+          if (xn > 0 && stop(wait_phase(x_free, (uint32_t)(xn - 1) & 1u, abort_f, g))) break;
           if (r < NR) xch[r] = make_float2(M, Lr);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(x_full);
         } else {
-          if (stop(wait_phase(x_full, (uint32_t)xn & 1u, abort_f, g.status))) break;
+          if (stop(wait_phase(x_full, (uint32_t)xn & 1u, abort_f, g))) break;
           if (r < NR) other = xch[r];
           __syncwarp();
           if (lane == 0) mbar_arrive(x_free);

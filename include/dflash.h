@@ -205,12 +205,13 @@ int dflash_status(dflash_workspace *w, dflash_stream_t stream, int32_t *status_o
  * workspace or another `which`.  No synchronisation: read it on the stream. */
 float *dflash_workspace_logits(dflash_workspace *w, int32_t which);
 /* Failure-path testing: sets the limit, in nanoseconds, of the waits in the
- * main loop of the weight-product kernel (ring slots and accumulator) for
- * launches enqueued afterwards; a negative value restores the default of
- * 500 ms.  A limit of 0 expires at once, so the kernel gives up, sets
- * DFLASH_STATUS_TIMEOUT, still waits (with the default limit) for its copies
- * and products in flight, writes no result and returns.  Process-wide; not an
- * operation of the method. */
+ * main loop of the weight-product kernel (ring slots and accumulator) and of
+ * the bf16 attention over pages, for launches enqueued afterwards; a negative
+ * value restores the default of 500 ms.  A limit of 0 expires at once, so the
+ * kernel gives up, sets DFLASH_STATUS_TIMEOUT, still waits (with the default
+ * limit) for its copies and products in flight and returns; the weight product
+ * writes no result, attention over pages an unspecified one.  Process-wide; not
+ * an operation of the method. */
 int dflash_debug_set_wait_limit(int64_t ns);
 const char *dflash_strerror(int code);
 
@@ -500,7 +501,9 @@ int dflash_paged_workspace_alloc(const dflash_model_desc *d, int32_t max_batch, 
                                  dflash_paged_workspace **out);
 int dflash_paged_workspace_free(dflash_paged_workspace *w);
 /* Synchronises `stream` (the one that the workspace's calls were made on),
- * returns the status bits in *status_out and clears them. */
+ * returns the status bits in *status_out and clears them.  After
+ * DFLASH_STATUS_TIMEOUT (a wait ran out) the results of the calls since the last
+ * status are unspecified. */
 int dflash_paged_status(dflash_paged_workspace *w, dflash_stream_t stream, int32_t *status_out);
 
 /* Append with the rotation on the way: row (b, j), j < n_rows[b], of qkv

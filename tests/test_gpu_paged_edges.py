@@ -313,3 +313,51 @@ def test_a_row_in_a_block_and_as_a_token(n, G, hd):
             assert ((one[:, 0].double() - ref[:, i]).abs() <= pair[:, i]).all(), (i, kw)
             assert ((one[:, 0].double() - out[:, i].double()).abs() <= pair[:, i] + lim[:, i]).all(), (i, kw)
     assert x.cache.status() == 0 and token.status() == 0
+
+
+TIMEOUTS = [  # heads, lens, n, shared, kwargs: every layout, pieces joined by CTAs, by a kernel and with a prefix's
+    ("gqa4", [4000, 3000, 10], 1, None, {}),
+    ("gqa4", [4000, 3000, 10], 7, None, dict(window=900, sinks=9)),
+    ("gqa4", [4000, 3000, 10], 16, None, {}),
+    ("gqa5", [4000, 300], 40, None, {}),
+    ("wide", [2000, 2000, 2100], 100, 1920, {}),
+    ("gqa4", [2000, 2000, 2100], 1, 1920, {}),
+]
+
+
+@pytest.mark.parametrize("c", TIMEOUTS, ids=[f"{c[0]}-n{c[2]}-{c[3]}" for c in TIMEOUTS])
+def test_a_wait_that_runs_out(c):
+    """With a limit of 0 every wait for work has run out before it begins; with a few microseconds some do, while
+    copies and products are in flight.  The status says so, nothing but the result is written, and the next call
+    after the status is right."""
+    heads, lens, n, shared, kw = c
+    x = Batch("bf16", *HEADS[heads], 32, lens, n, shared=shared or 0)
+    q = x.query()
+    sh = None if shared is None else i32([shared])
+    buf = torch.full((q.numel() + 1024,), 77.0, dtype=x.dt, device="cuda")
+    out = buf[512:-512].view(q.shape)
+
+    def call():
+        x.cache.attention(0, q, x.table, x.len, out, shared_len=sh, **kw)
+
+    call()
+    assert x.cache.status() == 0
+    want = out.clone()
+    check(x, want, reference(x, q, **kw))
+    k0, v0 = x.k.clone(), x.v.clone()
+    try:
+        for ns in (0, 0, 20000, 5000, 2000, 1000, 300):
+            capi.dflash_debug_set_wait_limit(ns)
+            out.fill_(77.0)
+            call()
+            status = x.cache.status()
+            assert status in (0, capi.STATUS_TIMEOUT) and (ns or status)
+            if not status:
+                assert torch.equal(out, want)
+            capi.dflash_debug_set_wait_limit(-1)
+            call()
+            assert x.cache.status() == 0 and torch.equal(out, want)
+    finally:
+        capi.dflash_debug_set_wait_limit(-1)
+    assert torch.equal(x.k, k0) and torch.equal(x.v, v0)
+    assert (buf[:512] == 77.0).all() and (buf[-512:] == 77.0).all()
