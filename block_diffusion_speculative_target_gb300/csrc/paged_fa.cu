@@ -29,9 +29,11 @@
 //   An item of at most 128 rows has one query tile, whose key tiles the groups
 //   take in turn; one of more rows has two, a group each, that share every key
 //   tile, which halves the traffic from L2.
-// P rounded to bf16 once is off by 2^-8 relative a weight, the size of the
-// result's own rounding; L sums the weights before it.  Where both groups work
-// on the same rows, their (M, L, O) are joined at the item's end.
+// P rounded to bf16 once (more than 32 rows) is off by 2^-8 relative a weight,
+// the size of the result's own rounding: relative errors against 64 bits are
+// 0.0023 there and 0.0017, the result's rounding alone, where P is a pair.  L
+// sums the weights before it.  Where both groups work on the same rows, their
+// (M, L, O) are joined at the item's end.
 //
 // Warps: 0 streams the pages (TMA, one box a page and 64 dimensions) through a
 // ring of key and value tiles; 1 and 2 issue the groups' products; 3 owns TMEM
@@ -47,11 +49,11 @@
 //
 // What bounds it, measured on inputs larger than L2, us a call (bytes at a copy's
 // 6.78 TB/s, products at 1.92 PFLOP/s):
-//   32 sequences, one token, 512 to 36K keys, 40 / 8 heads   399 (381): the bytes
-//   one token over 4K keys, 32 / 8 heads                    16.4 (2.5): the start (plan, cold
-//     instructions, query rows), one piece of two or three tiles a CTA, joining the pieces
-//   8 blocks of 16 rows over 2K..6K keys, 32 / 8 heads      61.3 (22): the start (20 us to the first weights,
-//     most of it instructions fetched from DRAM), 14 tiles a CTA, the piece (5), the joining kernel (8)
+//   32 sequences, one token, 512 to 36K keys, 40 / 8 heads   396 (381): the bytes
+//   one token over 4K keys, 32 / 8 heads                    16.9 (2.5): the start (5.5 us to the first weights),
+//     one piece of two or three tiles a CTA, writing and joining the pieces (5)
+//   8 blocks of 16 rows over 2K..6K keys, 32 / 8 heads      61.4 (22): the start (10 us to the first weights),
+//     14 tiles a CTA at 2.5 us a tile and group, the piece (5.6), the joining kernel (10.5 by itself)
 //   128 rows over 36K keys, 40 / 8 heads                     126 (51): 2.7 us a tile of 256 rows and 128 keys
 //     (products alone 1.3), a row's 128 exponentials by one thread
 // Rows as columns and not as rows for up to 64 rows: 128 rows' worth of exponentials would be computed for 4.
@@ -815,7 +817,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // While the first piece is planned and brought, the code of a first tile in the rows-as-columns layout is run
     // once on whatever TMEM holds: fetching its instructions costs several times what running them does.  Nothing
     // of it stays: the waits, the arrivals and the global reads are left out, and the first tile sets what it uses.
-    // 8 blocks of 16 rows over 2K..6K keys 63.3 -> 61.3 us, 15 rows in windows of 4K 82.6 -> 81.1.
+    // 8 blocks of 16 rows over 2K..6K keys 65.7 -> 61.4 us, 15 rows in windows of 4K 85.1 -> 82.6, single tokens
+    // the same.
     int dry = 0;  // (where no item of the other layout comes first)
     if constexpr (NR > 0 && TP) {
       dry = 1;

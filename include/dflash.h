@@ -495,7 +495,11 @@ int dflash_pages_free(dflash_pages *p);
 /* Scratch for the attention calls on handles of d's head counts and head_dim,
  * with at most max_batch sequences and batch * n <= max_rows, and a status
  * word.  Library-owned; one workspace serves one stream at a time, and so do
- * graphs captured with it: graphs that may run at once need one each. */
+ * graphs captured with it: graphs that may run at once need one each.  The
+ * partial results of the attention take 4 * max_rows * nq rows of hd + 2 floats,
+ * 1.4 GB for 16384 rows of 40 heads of 128 (half of it for shared lengths), and
+ * up to 40 MB more for the pieces; the append uses the status word alone, so any
+ * workspace of the device serves it. */
 typedef struct dflash_paged_workspace dflash_paged_workspace;
 int dflash_paged_workspace_alloc(const dflash_model_desc *d, int32_t max_batch, int32_t max_rows,
                                  dflash_paged_workspace **out);
@@ -514,7 +518,7 @@ int dflash_paged_status(dflash_paged_workspace *w, dflash_stream_t stream, int32
  * q_out NULL: the rows hold k|v only (injected context).  in_dtype is the type
  * of qkv: the model dtype, or float32 (the weight product's result).  qkv may
  * have any alignment of its type; rows on 16-byte boundaries are read in wide
- * loads.  q_out, qkv and the two pools do not overlap (ERR_INVALID_ARG), and no
+ * loads.  q_out, qkv and the two pools do not overlap (DFLASH_ERR_INVALID_ARG), and no
  * two rows of one call may name the same slot. */
 int dflash_paged_append(dflash_pages *p, int32_t layer, int32_t in_dtype, const void *qkv, int64_t ld,
                         int32_t batch, int32_t n, const int32_t *n_rows, const int32_t *table,
@@ -523,7 +527,7 @@ int dflash_paged_append(dflash_pages *p, int32_t layer, int32_t in_dtype, const 
 
 /* Attention over pages.  q [batch][n][nq][hd] (rotated, model dtype, 16-byte
  * aligned), the rows' own keys and values already appended; out likewise,
- * apart from q and from the pools (ERR_INVALID_ARG).
+ * apart from q and from the pools (DFLASH_ERR_INVALID_ARG).
  * Row (b, i) at position p = len[b] + i sees key j of its sequence when
  *   causal      j <= p            and (j > p - window or j < sinks),
  *   not causal  j < len[b] + n_rows[b]  and (j >= len[b] - window or j < sinks);
