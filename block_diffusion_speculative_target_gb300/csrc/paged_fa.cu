@@ -245,11 +245,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* full = bar;              // [NS] a key or value tile has landed
   uint64_t* empty = bar + NS;        // [NS] both issuing warps are done with it
   uint64_t* q_full = bar + 2 * NS;   // [2]
-  uint64_t* q_empty = q_full + 2;    // [2] two arrivals
+  uint64_t* q_empty = q_full + 2;    // [2] read by its last product, and seen by both issuing warps
   uint64_t* s_full = q_full + 4;     // [2][2] scores of the group's tile (rows as rows: half tile) in TMEM
   uint64_t* p_full = q_full + 8;     // [2][2] the buffer's weights (four warps; one may be a job ahead of another)
   uint64_t* pv_done = q_full + 12;   // [2][2] the product of weights and values of the buffer's job is done
-  uint64_t* o_free = q_full + 16;    // [2] the accumulator has been read (four warps)
+  uint64_t* o_free = q_full + 16;    // [2] the accumulator has been read (four warps), for pieces with a tile of the
+                                     // group's
   uint64_t* fix = q_full + 18;       // [3] meetings of group 0, group 1 (four warps), both (eight)
   uint64_t* x_full = q_full + 21;    // group 1's M and L are written (four warps)
   uint64_t* x_free = q_full + 22;    // and read
@@ -267,6 +268,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                      // the [1] keys from [0] on are seen by no row of its item
   volatile uint32_t* last_w = misc + 44;    // the CTA has finished an item's last piece
   volatile uint32_t* vote_w = misc + 46;    // [2][2][4] some reference of the tile has to move
+  volatile uint32_t* o_uses = misc + 62;    // [2] pieces with a tile of the group before this one (with v_ready)
   float2* xch = reinterpret_cast<float2*>(sm + L::kXch);
   Piece* pieces = reinterpret_cast<Piece*>(sm + L::kPieces);
   auto as_columns = [](int prefix) { return prefix ? TP : TS; };
@@ -416,9 +418,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t idOt = idesc_bf16_f32(128, 64) | (3u << 15);  // values and weights both MN-major
       const uint32_t tS = tmem + gq * 128, tO = tmem + 256 + gq * 128;
       auto wait = [&](uint64_t* b, uint32_t parity) { return !stop(wait_phase(b, parity & 1u, abort_f, g)); };
-      int job = 0;
+      int job = 0, on = 0;  // on: pieces with a tile of this group
       bool ok = true;
       pdl_wait();
+      // No wait may be lapped: a barrier's next phase needs every warp that waits for this one.  So both warps let go
+      // of a query tile, also of one that only the other reads; and o_free has no phase for a piece without a tile
+      // of the group, which ends without this warp.
       // Both issuing warps see every tile land and release it: a slot is refilled only after both have
       // been past it, so a wait never looks at a phase two fills away.
       while (ok && (ok = wait_piece(seg))) {
@@ -430,10 +435,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int buf = two ? gq : qt;
         if (two || qt == 0) ok = wait(&q_full[0], qn0);
         if (ok && (two || qt == 1)) ok = wait(&q_full[1], qn1);
-        if (ok && !two && gq >= nt) {  // no tile for this group
-          if (seg > 0) ok = wait(&o_free[gq], seg - 1);
-          if (ok && elect_one()) mbar_arrive(&q_empty[buf]);
-        }
+        const bool has = two || gq < nt;  // some tile for this group
+        if (ok && (two || !has) && elect_one()) mbar_arrive(&q_empty[two ? gq ^ 1 : buf]);
         const uint8_t* qs = sm + L::kQ + buf * L::kQBuf;
         if (cols) {
           int kjob = job;  // keys run ahead
@@ -476,9 +479,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (elect_one()) mbar_arrive(&empty[sv]);
               } else {
                 const bool first = t == gq;
-                if (elect_one()) mbar_arrive(&v_ready[gq]);
+                if (elect_one()) {
+                  o_uses[gq] = on;
+                  mbar_arrive(&v_ready[gq]);
+                }
                 ok = wait(&p_full[2 * gq + (job & 1)], job >> 1);
-                if (ok && first && seg > 0) ok = wait(&o_free[gq], seg - 1);
+                if (ok && first && on > 0) ok = wait(&o_free[gq], on - 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc0 = first ? acc_first[gq] : 1u;
@@ -559,14 +565,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               tc_commit(&empty[sk]);
               if (u + (two ? 1 : 2) >= nt) {  // the last scores of the piece: the query tile is free after them
                 tc_commit(&q_empty[buf]);
-                if (two) tc_commit(&q_empty[buf]);
               }
             }
             __syncwarp();
             ok = wait(&full[sv], (xk + 1) / NS);
-            if (ok && elect_one()) mbar_arrive(&v_ready[gq]);
+            if (ok && elect_one()) {
+              o_uses[gq] = on;
+              mbar_arrive(&v_ready[gq]);
+            }
             ok = ok && wait(&p_full[2 * gq], job >> 1);
-            if (ok && first && seg > 0) ok = wait(&o_free[gq], seg - 1);
+            if (ok && first && on > 0) ok = wait(&o_free[gq], on - 1);
             if (!ok) break;
             tc_fence_after();
             half_pv(job, sv, first ? acc_first[gq] : 1u);
@@ -582,6 +590,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         tiles += nt;
+        on += has;
         ++seg;
         if (two || qt == 0) ++qn0;
         if (two || qt == 1) ++qn1;
@@ -943,7 +952,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!wait_pv()) break;
                 if (first) {
                   // O starts here instead of in the first product, which must not overtake its last reader
-                  if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g));
+                  const uint32_t on = o_uses[gq];
+                  if (on > 0) ok = !stop(wait_phase(&o_free[gq], (on - 1) & 1u, abort_f, g));
                   if (!ok) break;
                   tc_fence_after();
                   zero_o(HD);
@@ -1073,7 +1083,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&o_free[gq]);
-            if (!two) mbar_arrive(&o_free[1]);
+            if (both) mbar_arrive(&o_free[1]);
           }
         }
         handover = true;
@@ -1303,7 +1313,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint32_t bw[4] = {bad_w[gq * 4], bad_w[gq * 4 + 1], bad_w[gq * 4 + 2], bad_w[gq * 4 + 3]};
             if (bw[0] | bw[1] | bw[2] | bw[3]) {
               if (first) {
-                if (seg > 0) ok = !stop(wait_phase(&o_free[gq], (uint32_t)(seg - 1) & 1u, abort_f, g));
+                const uint32_t on = o_uses[gq];
+                if (on > 0) ok = !stop(wait_phase(&o_free[gq], (on - 1) & 1u, abort_f, g));
                 if (!ok) break;
                 tc_fence_after();
                 zero_o(64);
@@ -1472,7 +1483,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&o_free[0]);
-            mbar_arrive(&o_free[1]);
+            if (both) mbar_arrive(&o_free[1]);
           }
           if (NR == 16 && !whole && pc.nc > 0 && !join(pc)) break;  // (few rows; else a kernel does)
         }

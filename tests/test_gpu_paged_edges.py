@@ -361,3 +361,32 @@ def test_a_wait_that_runs_out(c):
         capi.dflash_debug_set_wait_limit(-1)
     assert torch.equal(x.k, k0) and torch.equal(x.v, v0)
     assert (buf[:512] == 77.0).all() and (buf[-512:] == 77.0).all()
+
+
+SHORT = [  # heads, hd, G, B, shared, window, sinks: runs of items of one tile, with one and two query tiles
+    (8, 64, 2, 130, 130, 100, 128),
+    (8, 128, 2, 130, 128, 0, 0),
+    (2, 128, 4, 300, 0, 0, 0),
+    (8, 64, 13, 21, 256, 90, 5),
+    (4, 128, 33, 12, 130, 0, 0),
+]
+
+
+@pytest.mark.parametrize("c", SHORT, ids=[f"{c[0]}x{c[2]}x{c[1]}-b{c[3]}" for c in SHORT])
+def test_short_items_one_after_another(c):
+    """Many items of one key tile in a CTA's run: its warps may be whole items apart."""
+    nkv, hd, G, B, shared, window, sinks = c
+    own = [(29 * b) % 100 for b in range(B)]
+    x = Batch("bf16", nkv * G, nkv, hd, 64, [shared + o for o in own], 1, shared=shared, fill=float("nan"))
+    q, kw = x.query(), dict(window=window, sinks=sinks)
+    want = reference(x, q, **kw)
+    for sh in (shared, None) if shared else (None,):
+        first = attend(x, q, shared=sh, **kw)
+        assert x.cache.status() == 0
+        check(x, first, want, f"shared {sh}")
+        outs = [torch.full_like(q, 77.0) for _ in range(40)]
+        one = None if sh is None else i32([sh])
+        for out in outs:
+            x.cache.attention(0, q, x.table, x.len, out, shared_len=one, **kw)
+        assert x.cache.status() == 0
+        assert all(torch.equal(out, first) for out in outs)
