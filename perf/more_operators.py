@@ -261,8 +261,9 @@ def _append(s, c):
     s["q"].copy_(torch.where(live, rot[:, :, :c.nq].to(s["q"].dtype), s["q"]))
     page, slot = s["table"].long().gather(1, pos // c.page), pos % c.page
     at = (page[..., None], torch.arange(c.nkv, device="cuda"), slot[..., None])
+    steps = torch.full((), 127.0, device="cuda")  # (a division by a Python number is a product with its inverse)
     for name, new in (("k", rot[:, :, c.nq:]), ("v", x[:, :, c.nq + c.nkv:])):
-        scale = new.abs().amax(-1, keepdim=True) / 127.0
+        scale = new.abs().amax(-1, keepdim=True) / steps
         code = (torch.round(new / scale).clamp(-127, 127) + 128.0).to(torch.uint8)
         # a padding row's slot is its sequence's own too, and keeps what it held
         s[name].index_put_(at, torch.where(live, code, s[name][at]))
