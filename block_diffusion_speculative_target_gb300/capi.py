@@ -54,6 +54,11 @@ class DraftC(ctypes.Structure):
                 ("layers", POINTER(LayerW)), ("w_kv_all", c_void_p), ("mask_id", c_int32), ("cross_ctx", c_int32)]
 
 
+class W4C(ctypes.Structure):
+    _fields_ = [("M", c_int32), ("K", c_int32), ("group", c_int32), ("scale_dtype", c_int32), ("zeros", c_int32),
+                ("packed", c_void_p)]
+
+
 _P = c_void_p
 _I = c_int32
 _SIGS = {
@@ -95,13 +100,22 @@ _SIGS = {
     "dflash_argmax_noalloc": (_I, [_P, _I, _I, _P, _P, _P, _P]),
     "dflash_attention": (_I, [POINTER(ModelDesc), _P, _I, _I, _I, _I, _P, _I, _P, _P, _P]),
     "dflash_pages_create": (_I, [POINTER(ModelDesc), _I, _I, _I, _I, _P, _P, POINTER(c_void_p)]),
+    "dflash_pages_create_q8": (_I, [POINTER(ModelDesc), _I, _I, _I, _I, _P, _P, _P, _P, POINTER(c_void_p)]),
     "dflash_pages_free": (_I, [_P]),
     "dflash_paged_workspace_alloc": (_I, [POINTER(ModelDesc), _I, _I, POINTER(c_void_p)]),
     "dflash_paged_workspace_free": (_I, [_P]),
     "dflash_paged_status": (_I, [_P, _P, POINTER(c_int32)]),
     "dflash_paged_append": (_I, [_P, _I, _I, _P, ctypes.c_int64, _I, _I, _P, _P, _I, _P, _P, _P, _P]),
+    "dflash_paged_read": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P]),
     "dflash_paged_attention": (_I, [_P, _I, _P, _I, _I, _P, _I, _I, _I, _P, _I, _P, _P, _P, _P]),
     "dflash_paged_attention_shared": (_I, [_P, _I, _P, _I, _I, _P, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P]),
+    "dflash_w4_bytes": (ctypes.c_int64, [POINTER(W4C)]),
+    "dflash_w4_pack": (_I, [POINTER(W4C), _P, _P, _P, _P]),
+    "dflash_w4_quantize": (_I, [POINTER(W4C), _I, _P, ctypes.c_int64, _P]),
+    "dflash_w4_unpack": (_I, [POINTER(W4C), _I, _P, _P]),
+    "dflash_w4_workspace_alloc": (_I, [_I, POINTER(c_void_p)]),
+    "dflash_w4_workspace_free": (_I, [_P]),
+    "dflash_linear_w4": (_I, [_I, _P, ctypes.c_int64, POINTER(W4C), _P, _I, _P, _I, _P, _P]),
     "dflash_profile_begin": (_I, [_I]),
     "dflash_launch_count": (ctypes.c_longlong, []),
     "dflash_profile_end": (_I, [POINTER(c_float), POINTER(c_int32), _I, POINTER(c_int32)]),
@@ -402,6 +416,13 @@ def dflash_pages_create(desc: ModelDesc, n_layers, n_pages, page_size, max_pos, 
     return h.value
 
 
+def dflash_pages_create_q8(desc: ModelDesc, n_layers, n_pages, page_size, max_pos, k, v, k_scales, v_scales):
+    h = c_void_p()
+    _check(load().dflash_pages_create_q8(ctypes.byref(desc), n_layers, n_pages, page_size, max_pos, _ptr(k), _ptr(v),
+                                         _ptr(k_scales), _ptr(v_scales), ctypes.byref(h)), "dflash_pages_create_q8")
+    return h.value
+
+
 def dflash_pages_free(pages):
     _check(load().dflash_pages_free(pages), "dflash_pages_free")
 
@@ -430,6 +451,12 @@ def dflash_paged_append(pages, layer, in_dtype, qkv, ld, batch, n, n_rows, table
            "dflash_paged_append")
 
 
+def dflash_paged_read(pages, layer, out_dtype, batch, n, n_rows, table, table_stride, start, k_out, v_out, ws,
+                      stream=None):
+    _check(load().dflash_paged_read(pages, layer, out_dtype, batch, n, _ptr(n_rows), _ptr(table), table_stride,
+                                    _ptr(start), _ptr(k_out), _ptr(v_out), ws, _stream(stream)), "dflash_paged_read")
+
+
 def dflash_paged_attention(pages, layer, q, batch, n, n_rows, causal, window, sinks, table, table_stride, lengths, out,
                            ws, stream=None):
     _check(load().dflash_paged_attention(pages, layer, _ptr(q), batch, n, _ptr(n_rows), causal, window, sinks,
@@ -442,6 +469,44 @@ def dflash_paged_attention_shared(pages, layer, q, batch, n, n_rows, causal, win
     _check(load().dflash_paged_attention_shared(pages, layer, _ptr(q), batch, n, _ptr(n_rows), causal, window, sinks,
                                                 _ptr(table), table_stride, _ptr(lengths), _ptr(shared_len), _ptr(out),
                                                 ws, _stream(stream)), "dflash_paged_attention_shared")
+
+
+# ---------------------------------------------------------------- weights in 4 bits
+
+
+def dflash_w4_bytes(w: W4C):
+    n = load().dflash_w4_bytes(ctypes.byref(w))
+    if n < 0:
+        _check(int(n), "dflash_w4_bytes")
+    return n
+
+
+def dflash_w4_pack(w: W4C, codes, scales, zeros, stream=None):
+    _check(load().dflash_w4_pack(ctypes.byref(w), _ptr(codes), _ptr(scales), _ptr(zeros), _stream(stream)),
+           "dflash_w4_pack")
+
+
+def dflash_w4_quantize(w: W4C, dtype, src, ld, stream=None):
+    _check(load().dflash_w4_quantize(ctypes.byref(w), dtype, _ptr(src), ld, _stream(stream)), "dflash_w4_quantize")
+
+
+def dflash_w4_unpack(w: W4C, dtype, dst, stream=None):
+    _check(load().dflash_w4_unpack(ctypes.byref(w), dtype, _ptr(dst), _stream(stream)), "dflash_w4_unpack")
+
+
+def dflash_w4_workspace_alloc(max_rows):
+    h = c_void_p()
+    _check(load().dflash_w4_workspace_alloc(max_rows, ctypes.byref(h)), "dflash_w4_workspace_alloc")
+    return h.value
+
+
+def dflash_w4_workspace_free(ws):
+    _check(load().dflash_w4_workspace_free(ws), "dflash_w4_workspace_free")
+
+
+def dflash_linear_w4(dtype, x, ldx, w: W4C, add, swiglu, y, rows, ws, stream=None):
+    _check(load().dflash_linear_w4(dtype, _ptr(x), ldx, ctypes.byref(w), _ptr(add), swiglu, _ptr(y), rows, ws,
+                                   _stream(stream)), "dflash_linear_w4")
 
 
 # ---------------------------------------------------------------- kernel timing

@@ -215,10 +215,31 @@ struct CoreLayout {
   static constexpr int kSmem = kRed + (2 * kCoreThreads / 32 + 8) * 4;
 };
 
-template <typename T, int HD, int MRM>
+// 8 entries of a pool row as they lie there, in 8-bit pages with the row's scale.
+template <typename TK>
+struct Held8 {
+  Raw8<TK> r;
+  __device__ __forceinline__ void load(const TK* p, const float*, long long at) { r = load8<TK>(p + at, true); }
+  __device__ __forceinline__ void values(float (&x)[8]) const { unpack8(r, x); }
+};
+template <>
+struct Held8<uint8_t> {
+  uint2 u;
+  float s;
+  __device__ __forceinline__ void load(const uint8_t* p, const float* scales, long long at) {
+    u = *reinterpret_cast<const uint2*>(p + at);
+    s = *scales;
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (float)((int)((e < 4 ? u.x : u.y) >> (8 * (e & 3)) & 255u) - 128) * s;
+  }
+};
+
+template <typename T, typename TK, int HD, int MRM>
 __global__ void __launch_bounds__(kCoreThreads)
-    paged_attn_core_kernel(const __grid_constant__ PagedGeom g, const T* __restrict__ q, const T* __restrict__ kp,
-                           const T* __restrict__ vp, T* __restrict__ out, float scale_log2) {
+    paged_attn_core_kernel(const __grid_constant__ PagedGeom g, const T* __restrict__ q, const TK* __restrict__ kp,
+                           const TK* __restrict__ vp, T* __restrict__ out, float scale_log2) {
   typedef CoreLayout<HD, MRM> L;
   extern __shared__ uint8_t smem_raw[];
   float* sq = reinterpret_cast<float*>(smem_raw);
@@ -260,7 +281,7 @@ __global__ void __launch_bounds__(kCoreThreads)
              sg.prefix ? 0 : div_g(g, sg.rt * g.ri), seen_sink, seen_lo, seen_hi);
     // 8 threads a key: its rows of keys and values (keys that no row sees, or in a bad page: zeros), fetched into
     // registers while the tile before is worked on
-    Raw8<T> rk[HD / 64], rv[HD / 64];
+    Held8<TK> rk[HD / 64], rv[HD / 64];
     auto fetch = [&](int t) {
       const int key = sg.span.tile(t) * kCoreKeys + (tid >> 3), part = tid & 7;
       int page = -1;
@@ -271,13 +292,14 @@ __global__ void __launch_bounds__(kCoreThreads)
           set_status(g.status, DFLASH_STATUS_BOUNDS);
         }
       }
-      const long long at = (g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps + (key & (g.ps - 1))) * HD + part * 8;
+      const long long row = g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps + (key & (g.ps - 1));
+      const long long at = row * HD + part * 8;
 #pragma unroll
       for (int e = 0; e < HD / 64; ++e) {
-        rk[e] = rv[e] = Raw8<T>{};
+        rk[e] = rv[e] = Held8<TK>{};
         if (page >= 0) {
-          rk[e] = load8<T>(kp + at + e * 64, true);
-          rv[e] = load8<T>(vp + at + e * 64, true);
+          rk[e].load(kp, g.ks + row, at + e * 64);
+          rv[e].load(vp, g.vs + row, at + e * 64);
         }
       }
     };
@@ -288,9 +310,9 @@ __global__ void __launch_bounds__(kCoreThreads)
 #pragma unroll
       for (int e = 0; e < HD / 64; ++e) {
         float x[8];
-        unpack8(rk[e], x);
+        rk[e].values(x);
         store8<float>(sk + (tid >> 3) * L::kRow + (tid & 7) * 8 + e * 64, x);
-        unpack8(rv[e], x);
+        rv[e].values(x);
         store8<float>(sv + (tid >> 3) * HD + (tid & 7) * 8 + e * 64, x);
       }
       if (t + 1 < sg.t0 + sg.nt) fetch(t + 1);
@@ -510,16 +532,16 @@ PagedRule paged_rule_core(const PagedGeom& g) {
   return PagedRule{rows, rows, kCoreKeys, 1, 0};
 }
 
-template <typename T, int HD, int MRM>
+template <typename T, typename TK, int HD, int MRM>
 static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const void* vp, void* out,
                                long long part_rows, cudaStream_t s) {
   typedef CoreLayout<HD, MRM> L;
   static PerDevice ctas;
   int per_sm = 0;
   DFL_RET(ctas.get(&per_sm, [](int, int* v) {
-    DFL_RET(cudaFuncSetAttribute(paged_attn_core_kernel<T, HD, MRM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    DFL_RET(cudaFuncSetAttribute(paged_attn_core_kernel<T, TK, HD, MRM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  L::kSmem));
-    DFL_RET(cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, paged_attn_core_kernel<T, HD, MRM>, kCoreThreads,
+    DFL_RET(cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, paged_attn_core_kernel<T, TK, HD, MRM>, kCoreThreads,
                                                           L::kSmem));
     *v = std::min(std::max(*v, 1), kPagedMaxCtas);
     return cudaSuccess;
@@ -529,20 +551,31 @@ static cudaError_t core_launch(PagedGeom g, const void* q, const void* kp, const
   // runs of two tiles at least: 4 blocks of 16 rows over up to 1K keys take 17.4 us, 22.4 in runs of four
   if (paged_split(g, rule, num_sms() * per_sm, 2) > part_rows) return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
-  DFL_RET(launch_pdl(paged_attn_core_kernel<T, HD, MRM>, dim3(g.grid), dim3(kCoreThreads), L::kSmem, s, g, (const T*)q,
-                     (const T*)kp, (const T*)vp, (T*)out, scale_log2));
+  DFL_RET(launch_pdl(paged_attn_core_kernel<T, TK, HD, MRM>, dim3(g.grid), dim3(kCoreThreads), L::kSmem, s, g, (const T*)q,
+                     (const TK*)kp, (const TK*)vp, (T*)out, scale_log2));
   count_launch();
   return g.shared ? merge_launch<T, HD, kCoreKeys>(g, out, s) : cudaSuccess;  // (else the CTAs join their pieces)
 }
 
+template <typename T, typename TK, int HD>
+static cudaError_t core_pick(const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
+                             long long part_rows, cudaStream_t s) {
+  return core_small(g) ? core_launch<T, TK, HD, 1>(g, q, kp, vp, out, part_rows, s)
+                       : core_launch<T, TK, HD, 4>(g, q, kp, vp, out, part_rows, s);
+}
+
 cudaError_t paged_attention_core(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp,
                                  void* out, long long part_rows, cudaStream_t s) {
-#define DFL_CORE(HD)                                                                         \
-  return core_small(g) ? core_launch<float, HD, 1>(g, q, kp, vp, out, part_rows, s)          \
-                       : core_launch<float, HD, 4>(g, q, kp, vp, out, part_rows, s)
-  if (hd == 64) DFL_CORE(64);
-  DFL_CORE(128);
-#undef DFL_CORE
+  if (g.ks)
+    return hd == 64 ? core_pick<float, uint8_t, 64>(g, q, kp, vp, out, part_rows, s)
+                    : core_pick<float, uint8_t, 128>(g, q, kp, vp, out, part_rows, s);
+  return hd == 64 ? core_pick<float, float, 64>(g, q, kp, vp, out, part_rows, s)
+                  : core_pick<float, float, 128>(g, q, kp, vp, out, part_rows, s);
+}
+cudaError_t paged_attention_q8(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
+                               long long part_rows, cudaStream_t s) {
+  return hd == 64 ? core_pick<bf16, uint8_t, 64>(g, q, kp, vp, out, part_rows, s)
+                  : core_pick<bf16, uint8_t, 128>(g, q, kp, vp, out, part_rows, s);
 }
 
 }  // namespace dfl

@@ -48,6 +48,8 @@ struct PagedGeom {
   float2* part_ml;
   long long pre_row0;    // first partial row of the prefix slots
   int slot_s, slot_p;    // partial rows per suffix / prefix slot
+  const float* ks;       // 8-bit pages: a scale for each pool row; else null
+  const float* vs;
   int32_t* plan;         // [kPlanCum + batch] written for the merge kernel
   int32_t* tickets;      // [items] pieces done, zero between calls
   int32_t* records;      // [CTAs][8] items to join after the kernel
@@ -571,6 +573,19 @@ cudaError_t paged_join_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t 
 // the CUDA cores, bf16 on the tensor cores.
 cudaError_t paged_attention_core(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
                                  long long part_rows, cudaStream_t s);
+// bf16 queries over 8-bit pages.
+cudaError_t paged_attention_q8(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
+                               long long part_rows, cudaStream_t s);
+// Append into 8-bit pages: codes and a scale a row.
+cudaError_t paged_append_q8(int in_dtype, int dtype, const void* qkv, long long ld, int batch, int n, int nq, int nkv,
+                            int hd, const int32_t* n_rows, const int32_t* table, int table_stride, const int32_t* len,
+                            const float2* tab, int max_pos, int n_pages, int ps, long long page0, void* qout,
+                            uint8_t* kp, uint8_t* vp, float* ks, float* vs, int* status, cudaStream_t s);
+// Rows out of pages: dtype of the pool (8-bit: ks, vs given), type of the result.
+cudaError_t paged_read(int dtype, int out_dtype, const void* kp, const void* vp, const float* ks, const float* vs,
+                       int batch, int n, int nkv, int hd, const int32_t* n_rows, const int32_t* table,
+                       int table_stride, const int32_t* start, int max_pos, int n_pages, int ps, long long page0,
+                       void* k_out, void* v_out, int* status, cudaStream_t s);
 cudaError_t paged_attention_tc(int hd, const PagedGeom& g, const CUtensorMap& tk, const CUtensorMap& tv,
                                long long pool_rows, const void* q, void* out, long long part_rows, cudaStream_t s);
 // 2-D maps over a bf16 pool [rows][hd]: boxes of 64 elements (128 B, swizzled) by one page's positions.

@@ -14,6 +14,7 @@ struct dflash_pages {
   int32_t n_layers, n_pages, page_size, max_pos, nq, nkv, hd, dtype;
   int device;
   void *k, *v;     // the caller's pool
+  float *ks, *vs;  // 8-bit pages: the scales of its rows; else null
   float2* rope;    // [max_pos][hd / 2]
   CUtensorMap tk, tv;  // bf16: over the whole pool
 };
@@ -54,15 +55,24 @@ static bool apart(const void* a, long long abytes, const void* b, long long bbyt
   return x + (uintptr_t)abytes <= y || y + (uintptr_t)bbytes <= x;
 }
 static int elem_size(int dtype) { return dtype == DFLASH_F32 ? 4 : 2; }
-static long long pool_bytes(const dflash_pages* p) { return pool_rows(p) * p->hd * elem_size(p->dtype); }
+static long long pool_bytes(const dflash_pages* p) {
+  return pool_rows(p) * p->hd * (p->ks ? 1 : elem_size(p->dtype));
+}
 static bool apart_from_pool(const dflash_pages* p, const void* a, long long bytes) {
+  if (p->ks && !(apart(a, bytes, p->ks, pool_rows(p) * 4) && apart(a, bytes, p->vs, pool_rows(p) * 4))) return false;
   return apart(a, bytes, p->k, pool_bytes(p)) && apart(a, bytes, p->v, pool_bytes(p));
 }
+// The pool's own parts.
+static bool pool_apart(const dflash_pages* p) {
+  if (!apart(p->k, pool_bytes(p), p->v, pool_bytes(p))) return false;
+  if (!p->ks) return true;
+  const long long b = pool_bytes(p), s = pool_rows(p) * 4;
+  return apart(p->ks, s, p->vs, s) && apart(p->k, b, p->ks, s) && apart(p->k, b, p->vs, s) && apart(p->v, b, p->ks, s) &&
+         apart(p->v, b, p->vs, s);
+}
 
-extern "C" {
-
-int dflash_pages_create(const dflash_model_desc* d, int32_t n_layers, int32_t n_pages, int32_t page_size,
-                        int32_t max_pos, void* k, void* v, dflash_pages** out) {
+static int create(const dflash_model_desc* d, int32_t n_layers, int32_t n_pages, int32_t page_size, int32_t max_pos,
+                  void* k, void* v, float* ks, float* vs, dflash_pages** out) {
   REQ(out);
   *out = nullptr;
   REQ(desc_ok(d) && d->rope_theta > 0.f && isfinite(d->rope_theta));
@@ -74,8 +84,12 @@ int dflash_pages_create(const dflash_model_desc* d, int32_t n_layers, int32_t n_
   dflash_pages* p = new (std::nothrow) dflash_pages();
   if (!p) return DFLASH_ERR_OOM;
   *p = dflash_pages{n_layers, n_pages, page_size, max_pos, d->n_q_heads, d->n_kv_heads, d->head_dim, d->dtype,
-                    0,        k,       v,         nullptr, {},           {}};
-  if (p->dtype == DFLASH_BF16 && !make_page_maps(k, v, pool_rows(p), p->hd, page_size, &p->tk, &p->tv)) {
+                    0,        k,       v,         ks,      vs,           nullptr,       {},          {}};
+  if (ks && !pool_apart(p)) {
+    delete p;
+    return DFLASH_ERR_INVALID_ARG;
+  }
+  if (p->dtype == DFLASH_BF16 && !ks && !make_page_maps(k, v, pool_rows(p), p->hd, page_size, &p->tk, &p->tv)) {
     delete p;
     return record_cuda_error(cudaErrorInvalidValue);
   }
@@ -97,6 +111,21 @@ int dflash_pages_create(const dflash_model_desc* d, int32_t n_layers, int32_t n_
   }
   *out = p;
   return DFLASH_OK;
+}
+
+extern "C" {
+
+int dflash_pages_create(const dflash_model_desc* d, int32_t n_layers, int32_t n_pages, int32_t page_size,
+                        int32_t max_pos, void* k, void* v, dflash_pages** out) {
+  return create(d, n_layers, n_pages, page_size, max_pos, k, v, nullptr, nullptr, out);
+}
+
+int dflash_pages_create_q8(const dflash_model_desc* d, int32_t n_layers, int32_t n_pages, int32_t page_size,
+                           int32_t max_pos, void* k, void* v, float* k_scales, float* v_scales, dflash_pages** out) {
+  REQ(out);
+  *out = nullptr;
+  REQ(k_scales && v_scales && aligned16(k_scales) && aligned16(v_scales));
+  return create(d, n_layers, n_pages, page_size, max_pos, k, v, k_scales, v_scales, out);
 }
 
 int dflash_pages_free(dflash_pages* p) {
@@ -193,11 +222,35 @@ int dflash_paged_append(dflash_pages* p, int32_t layer, int32_t in_dtype, const 
   const long long qkv_bytes = ((rows - 1) * ld + width) * elem_size(in_dtype);
   const long long q_bytes = rows * p->nq * p->hd * elem_size(p->dtype);
   REQ(!q_out || (apart(qkv, qkv_bytes, q_out, q_bytes) && apart_from_pool(p, q_out, q_bytes)));
-  REQ(apart_from_pool(p, qkv, qkv_bytes) && apart(p->k, pool_bytes(p), p->v, pool_bytes(p)));
+  REQ(apart_from_pool(p, qkv, qkv_bytes) && pool_apart(p));
   REQ(on_device(p->device) && ws->device == p->device);
+  if (p->ks) {
+    CK(paged_append_q8(in_dtype, p->dtype, qkv, ld, batch, n, nq, p->nkv, p->hd, n_rows, table, table_stride, len,
+                       p->rope, p->max_pos, p->n_pages, p->page_size, (long long)layer * p->n_pages, q_out,
+                       (uint8_t*)p->k, (uint8_t*)p->v, p->ks, p->vs, ws->status, (cudaStream_t)stream));
+    return DFLASH_OK;
+  }
   CK(paged_append(in_dtype, p->dtype, qkv, ld, batch, n, nq, p->nkv, p->hd, n_rows, table, table_stride, len, p->rope,
                   p->max_pos, p->n_pages, p->page_size, (long long)layer * p->n_pages, q_out, p->k, p->v, ws->status,
                   (cudaStream_t)stream));
+  return DFLASH_OK;
+}
+
+int dflash_paged_read(dflash_pages* p, int32_t layer, int32_t out_dtype, int32_t batch, int32_t n,
+                      const int32_t* n_rows, const int32_t* table, int32_t table_stride, const int32_t* start,
+                      void* k_out, void* v_out, dflash_paged_workspace* ws, dflash_stream_t stream) {
+  REQ(p && ws && table && start && (k_out || v_out) && layer >= 0 && layer < p->n_layers);
+  REQ(batch > 0 && n > 0 && table_stride > 0 && (long long)batch * n < (1ll << 31));
+  REQ(out_dtype == DFLASH_F32 || out_dtype == p->dtype);
+  REQ(aligned16(k_out) && aligned16(v_out));
+  const long long bytes = (long long)batch * n * p->nkv * p->hd * elem_size(out_dtype);
+  REQ(!k_out || apart_from_pool(p, k_out, bytes));
+  REQ(!v_out || apart_from_pool(p, v_out, bytes));
+  REQ(!k_out || !v_out || apart(k_out, bytes, v_out, bytes));
+  REQ(on_device(p->device) && ws->device == p->device);
+  CK(paged_read(p->dtype, out_dtype, p->k, p->v, p->ks, p->vs, batch, n, p->nkv, p->hd, n_rows, table, table_stride,
+                start, p->max_pos, p->n_pages, p->page_size, (long long)layer * p->n_pages, k_out, v_out, ws->status,
+                (cudaStream_t)stream));
   return DFLASH_OK;
 }
 
@@ -233,6 +286,8 @@ static int attend(dflash_pages* p, int32_t layer, const void* q, int32_t batch, 
   g.n_rows = n_rows;
   g.table = table;
   g.shared = shared_len;
+  g.ks = p->ks;
+  g.vs = p->vs;
   g.part_o = ws->part_o;
   g.part_ml = ws->part_ml;
   g.plan = ws->plan;
@@ -240,8 +295,11 @@ static int attend(dflash_pages* p, int32_t layer, const void* q, int32_t batch, 
   g.records = ws->records;
   g.status = ws->status;
   g.wait_ns = (unsigned)std::min(wait_limit_ns(), 4000000000ull);
-  if (!paged_line_fits(g, p->dtype == DFLASH_BF16 ? paged_rule_tc(g) : paged_rule_core(g))) return DFLASH_ERR_TOO_LARGE;
-  if (p->dtype == DFLASH_BF16)
+  const bool tc = p->dtype == DFLASH_BF16 && !p->ks;
+  if (!paged_line_fits(g, tc ? paged_rule_tc(g) : paged_rule_core(g))) return DFLASH_ERR_TOO_LARGE;
+  if (p->ks && p->dtype == DFLASH_BF16)
+    CK(paged_attention_q8(p->hd, g, q, p->k, p->v, out, ws->part_rows, (cudaStream_t)stream));
+  else if (tc)
     CK(paged_attention_tc(p->hd, g, p->tk, p->tv, pool_rows(p), q, out, ws->part_rows, (cudaStream_t)stream));
   else
     CK(paged_attention_core(p->hd, g, q, p->k, p->v, out, ws->part_rows, (cudaStream_t)stream));

@@ -364,7 +364,11 @@ class PagedCache:
 
     ``shape`` and ``dtype`` as for ``Model``.  The pool is two tensors ``k`` and
     ``v`` [n_layers][n_pages][n_kv][page_size][head_dim]; pass them (a 4-d pair
-    is one layer) or leave them out to have zeroed ones made.  Tables, lengths
+    is one layer) or leave them out to have zeroed ones made.  With ``kv_format``
+    "q8" they hold uint8 codes, and ``k_scale`` and ``v_scale``
+    [n_layers][n_pages][n_kv][page_size] the rows' float32 scales: ``append``
+    quantises, ``attention`` and ``read`` take entries as (code - 128) * scale,
+    queries and results stay in ``dtype``.  Tables, lengths
     and row counts are the caller's device int32 tensors: ``table``
     [batch][columns] names the page of each ``page_size`` positions, ``lengths``
     [batch] the positions held before a call's rows, ``n_rows`` [batch] the rows
@@ -372,26 +376,43 @@ class PagedCache:
     are asynchronous on its current stream and leave ``lengths`` as it is."""
 
     def __init__(self, shape, dtype: str, n_pages, page_size, max_pos, max_rows, max_batch=None, n_layers=1, k=None,
-                 v=None, device="cuda"):
-        self.dtype, self.tdt = dtype, _DT[dtype][1]
+                 v=None, device="cuda", kv_format="model", k_scale=None, v_scale=None):
+        if kv_format not in ("model", "q8"):
+            raise ValueError(kv_format)
+        q8 = kv_format == "q8"
+        self.dtype, self.tdt, self.kv_format = dtype, _DT[dtype][1], kv_format
+        kdt = torch.uint8 if q8 else self.tdt
         self.nq, self.nkv, self.hd = shape.n_q, shape.n_kv, shape.head_dim
         self.page_size, self.max_pos = page_size, max_pos
         self.pages = self.ws = None
         dims = (n_layers, n_pages, self.nkv, page_size, self.hd)
-        if (k is None) != (v is None):
-            raise ValueError("pass both pools or neither")
-        if k is None:
-            k, v = (torch.zeros(dims, dtype=self.tdt, device=device) for _ in range(2))
-        for t in (k, v):
-            if t.dtype != self.tdt or not t.is_cuda or not t.is_contiguous() or \
-                    tuple(t.shape) != (dims if t.dim() == 5 else dims[1:]) or (t.dim() == 4 and n_layers != 1):
-                raise ValueError(f"a pool is a contiguous {self.tdt} tensor {dims} on the GPU")
-        self.k, self.v, self.device = k, v, k.device
-        if v.device != self.device:
+        pools = {"k": k, "v": v}
+        if q8:
+            pools.update(k_scale=k_scale, v_scale=v_scale)
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError('scales belong to kv_format "q8"')
+        if len({t is None for t in pools.values()}) != 1:
+            raise ValueError("pass both pools (with their scales) or none")
+        for name in pools:
+            t, pdt, pdims = pools[name], torch.float32 if "scale" in name else kdt, dims[:4] if "scale" in name else dims
+            if t is None:
+                # (code 128 is 0)
+                t = pools[name] = torch.full(pdims, 128 if pdt == torch.uint8 else 0, dtype=pdt, device=device)
+            if t.dtype != pdt or not t.is_cuda or not t.is_contiguous() or \
+                    tuple(t.shape) != (pdims if t.dim() == len(pdims) else pdims[1:]) or \
+                    (t.dim() != len(pdims) and n_layers != 1):
+                raise ValueError(f"a pool is a contiguous {pdt} tensor {pdims} on the GPU")
+        self.k, self.v, self.device = pools["k"], pools["v"], pools["k"].device
+        self.k_scale, self.v_scale = pools.get("k_scale"), pools.get("v_scale")
+        if any(t.device != self.device for t in pools.values()):
             raise ValueError("the pools are on different devices")
         desc = desc_of(shape, dtype, n_layers)
         with torch.cuda.device(self.device):
-            self.pages = capi.dflash_pages_create(desc, n_layers, n_pages, page_size, max_pos, k, v)
+            if q8:
+                self.pages = capi.dflash_pages_create_q8(desc, n_layers, n_pages, page_size, max_pos, self.k, self.v,
+                                                         self.k_scale, self.v_scale)
+            else:
+                self.pages = capi.dflash_pages_create(desc, n_layers, n_pages, page_size, max_pos, self.k, self.v)
             self.ws = capi.dflash_paged_workspace_alloc(desc, max_batch or max_rows, max_rows)
 
     def close(self):
@@ -436,7 +457,7 @@ class PagedCache:
 
     def append(self, layer, qkv, table, lengths, n, q_out=None, n_rows=None):
         """Rotate and append ``n`` rows a sequence.  ``qkv`` [batch * n][...]
-        float32 or the pool's type, q|k|v heads side by side (k|v without
+        float32 or the model's type, q|k|v heads side by side (k|v without
         ``q_out``); its rows may be apart.  ``q_out`` receives the rotated
         queries."""
         stream = torch.cuda.current_stream()
@@ -453,6 +474,28 @@ class PagedCache:
         ld = qkv.stride(0) if qkv.shape[0] > 1 else width
         capi.dflash_paged_append(self.pages, layer, capi.F32 if qkv.dtype == torch.float32 else capi.BF16, qkv, ld,
                                  batch, n, n_rows, table, table.shape[1], lengths, q_out, self.ws, stream)
+
+    def read(self, layer, table, start, k_out=None, v_out=None, n_rows=None):
+        """Rows back out of the pages: positions ``start`` + 0, 1, .. of each
+        sequence into ``k_out`` and ``v_out`` [batch][n_kv][n][head_dim], of the
+        model's type or float32, both alike; either may be left out.  The first
+        ``n_rows`` rows of a sequence are written."""
+        stream = torch.cuda.current_stream()
+        if stream.device_index != self.device.index:
+            with torch.cuda.device(self.device):
+                return self.read(layer, table, start, k_out, v_out, n_rows)
+        batch = self._calls(table, start, n_rows)
+        outs = [t for t in (k_out, v_out) if t is not None]
+        if not outs or outs[0].dim() != 4:
+            raise ValueError("give k_out or v_out, [batch][n_kv][n][head_dim]")
+        n, odt = outs[0].shape[2], outs[0].dtype
+        for t in outs:
+            if t.dtype != odt or odt not in (torch.float32, self.tdt) or t.device != self.device or \
+                    not t.is_contiguous() or tuple(t.shape) != (batch, self.nkv, n, self.hd):
+                raise ValueError(f"k_out and v_out are contiguous tensors [{batch}][{self.nkv}][{n}][{self.hd}] of one "
+                                 f"type, float32 or {self.tdt}, on {self.device}")
+        capi.dflash_paged_read(self.pages, layer, capi.F32 if odt == torch.float32 else capi.BF16, batch, n, n_rows,
+                               table, table.shape[1], start, k_out, v_out, self.ws, stream)
 
     def attention(self, layer, q, table, lengths, out, causal=True, window=0, sinks=0, n_rows=None, shared_len=None):
         """Attention of ``q`` [batch][n][n_q][head_dim] over the pages into
@@ -477,3 +520,109 @@ class PagedCache:
                 raise ValueError(f"shared_len is one int32 on {self.device}")
             capi.dflash_paged_attention_shared(self.pages, layer, q, batch, n, n_rows, int(causal), window, sinks, table,
                                                table.shape[1], lengths, shared_len, out, self.ws, stream)
+
+
+class W4Workspace:
+    """Scratch of products with 4-bit weights for up to ``max_rows`` (<= 128)
+    rows, for any matrices: one for each stream, and for each of the graphs that
+    may run at the same time."""
+
+    def __init__(self, max_rows=128, device="cuda"):
+        self.handle, self.max_rows = None, max_rows
+        with torch.cuda.device(device):
+            self.device = torch.device("cuda", torch.cuda.current_device())
+            self.handle = capi.dflash_w4_workspace_alloc(max_rows)
+
+    def close(self):
+        """Frees the scratch.  Work of the calls made so far has to be done."""
+        if self.handle:
+            capi.dflash_w4_workspace_free(self.handle)
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class W4Linear:
+    """A weight matrix [M][K] in 4 bits: codes 0..15 with a scale, and where
+    ``zeros`` is set a zero point, for each ``group`` (32, 64, 128) columns of a
+    row; w = scale * (code - zero), the zero point 8 without.  The codes lie in
+    ``packed``, a uint8 tensor in the products' order (pass one to share it)."""
+
+    def __init__(self, M, K, group=128, scale_dtype=torch.bfloat16, zeros=False, device="cuda", packed=None):
+        if scale_dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("scales are float32 or bfloat16")
+        self.M, self.K, self.group, self.scale_dtype, self.zeros = M, K, group, scale_dtype, bool(zeros)
+        self._c = capi.W4C(M, K, group, capi.F32 if scale_dtype == torch.float32 else capi.BF16, int(self.zeros), None)
+        n = capi.dflash_w4_bytes(self._c)
+        if packed is None:
+            packed = torch.empty(n, dtype=torch.uint8, device=device)
+        if packed.dtype != torch.uint8 or not packed.is_cuda or not packed.is_contiguous() or packed.numel() != n:
+            raise ValueError(f"packed is a contiguous uint8 tensor of {n} bytes on the GPU")
+        self.packed, self.device = packed, packed.device
+        self._c.packed = packed.data_ptr()
+
+    @classmethod
+    def from_weight(cls, w, group=128, scale_dtype=torch.bfloat16, zeros=False):
+        """The nearest codes of a finite matrix w [M][K], float32 or bfloat16 (its rows may be apart)."""
+        if w.dim() != 2 or w.dtype not in (torch.float32, torch.bfloat16) or not w.is_cuda or \
+                (w.stride(1) != 1 and w.shape[1] > 1):
+            raise ValueError("w is a float32 or bfloat16 matrix on the GPU, its rows unbroken")
+        self = cls(w.shape[0], w.shape[1], group, scale_dtype, zeros, w.device)
+        with torch.cuda.device(self.device):
+            capi.dflash_w4_quantize(self._c, capi.F32 if w.dtype == torch.float32 else capi.BF16, w,
+                                    w.stride(0) if w.shape[0] > 1 else w.shape[1])
+        return self
+
+    @classmethod
+    def from_codes(cls, codes, scales, zeros=None):
+        """From codes [M][K / 2] (uint8, the even column's in the low half), scales [M][K / group] (float32 or
+        bfloat16) and, if given, zeros [M][K / group] (uint8)."""
+        if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0] or scales.shape[1] < 1 or \
+                2 * codes.shape[1] % scales.shape[1] != 0:
+            raise ValueError("codes are [M][K / 2], scales [M][K / group]")
+        if codes.dtype != torch.uint8 or not codes.is_cuda or not codes.is_contiguous() or not scales.is_contiguous() or \
+                scales.device != codes.device:
+            raise ValueError("codes (uint8) and scales are contiguous tensors on one GPU")
+        if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape or not zeros.is_contiguous() or
+                                  zeros.device != codes.device):
+            raise ValueError("zeros is a contiguous uint8 tensor of the scales' shape and device")
+        K = 2 * codes.shape[1]
+        self = cls(codes.shape[0], K, K // scales.shape[1], scales.dtype, zeros is not None, codes.device)
+        with torch.cuda.device(self.device):
+            capi.dflash_w4_pack(self._c, codes, scales, zeros)
+        return self
+
+    def weight(self, dtype=torch.float32):
+        """The matrix's values [M][K] (float32 or bfloat16)."""
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("float32 or bfloat16")
+        out = torch.empty(self.M, self.K, dtype=dtype, device=self.device)
+        with torch.cuda.device(self.device):
+            capi.dflash_w4_unpack(self._c, capi.F32 if dtype == torch.float32 else capi.BF16, out)
+        return out
+
+    def product(self, x, out, ws, add=None, swiglu=False):
+        """``out`` [rows][M] float32 = x w^T (+ ``add``, which may be ``out``), or with ``swiglu`` ``out``
+        [rows][M / 2] of x's type, silu(even rows) * odd rows.  ``x`` [rows][K] float32 or bfloat16, its rows may be
+        apart.  Asynchronous on the current stream of the weights' device."""
+        stream = torch.cuda.current_stream()
+        if stream.device_index != self.device.index:
+            with torch.cuda.device(self.device):
+                return self.product(x, out, ws, add, swiglu)
+        xdt = x.dtype
+        if x.dim() != 2 or x.shape[1] != self.K or xdt not in (torch.bfloat16, torch.float32) or \
+                x.device != self.device or (x.stride(1) != 1 and self.K > 1):
+            raise ValueError(f"x is a float32 or bfloat16 tensor [rows][{self.K}] on {self.device}, its rows unbroken")
+        rows = x.shape[0]
+        odt, cols = (xdt, self.M // 2) if swiglu else (torch.float32, self.M)
+        if out.dtype != odt or out.device != self.device or not out.is_contiguous() or tuple(out.shape) != (rows, cols):
+            raise ValueError(f"out is a contiguous {odt} tensor [{rows}][{cols}] on {self.device}")
+        if add is not None and (add.dtype != torch.float32 or add.device != self.device or not add.is_contiguous() or
+                                tuple(add.shape) != (rows, self.M)):
+            raise ValueError(f"add is a contiguous float32 tensor [{rows}][{self.M}] on {self.device}")
+        capi.dflash_linear_w4(capi.BF16 if xdt == torch.bfloat16 else capi.F32, x,
+                              x.stride(0) if rows > 1 else self.K, self._c, add, int(swiglu), out, rows, ws.handle, stream)

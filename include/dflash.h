@@ -491,6 +491,18 @@ typedef struct dflash_pages dflash_pages;
  * counts, head_dim, rope_theta and dtype. */
 int dflash_pages_create(const dflash_model_desc *d, int32_t n_layers, int32_t n_pages, int32_t page_size,
                         int32_t max_pos, void *k, void *v, dflash_pages **out);
+/* The same over a pool of 8-bit keys and values, half of bf16's bytes: k and v
+ * [n_layers][n_pages][n_kv][page_size][head_dim] uint8 codes, k_scales and
+ * v_scales [n_layers][n_pages][n_kv][page_size] float32, all 16-byte aligned and
+ * apart from one another.  A row of head_dim entries is kept as dflash_cache_alloc_ex's
+ * DFLASH_KV_Q8 keeps one, the entry (u - 128) s with s = max|x| / 127 and
+ * u = 128 + round-half-even(x / s), x the row's float32 entries after the rotation
+ * (a row of zeros: s = 0; one that holds a value that is not finite: s = NaN, so
+ * it reads back as NaN).  Every call below takes such a handle, of float32 models
+ * and of head_dim 64 too: dflash_paged_append quantises, the attention calls and
+ * dflash_paged_read take an entry as its exact value (u - 128) s. */
+int dflash_pages_create_q8(const dflash_model_desc *d, int32_t n_layers, int32_t n_pages, int32_t page_size,
+                           int32_t max_pos, void *k, void *v, float *k_scales, float *v_scales, dflash_pages **out);
 int dflash_pages_free(dflash_pages *p);
 /* Scratch for the attention calls on handles of d's head counts and head_dim,
  * with at most max_batch sequences and batch * n <= max_rows, and a status
@@ -524,6 +536,17 @@ int dflash_paged_append(dflash_pages *p, int32_t layer, int32_t in_dtype, const 
                         int32_t batch, int32_t n, const int32_t *n_rows, const int32_t *table,
                         int32_t table_stride, const int32_t *len, void *q_out, dflash_paged_workspace *ws,
                         dflash_stream_t stream);
+
+/* Rows back out of the pages, as dflash_cache_write takes them: position
+ * start[b] + j, j < n_rows[b], of sequence b goes to k_out and v_out
+ * [batch][n_kv][n][head_dim] (row j of each head), of the model dtype or float32,
+ * 16-byte aligned; either may be NULL.  8-bit entries are rounded once to the
+ * type.  Rows at or past n_rows[b], and those whose position or page sets a status
+ * bit, are left as they were.  To move a sequence to a cache or to other pages, or
+ * to look at what was kept. */
+int dflash_paged_read(dflash_pages *p, int32_t layer, int32_t out_dtype, int32_t batch, int32_t n,
+                      const int32_t *n_rows, const int32_t *table, int32_t table_stride, const int32_t *start,
+                      void *k_out, void *v_out, dflash_paged_workspace *ws, dflash_stream_t stream);
 
 /* Attention over pages.  q [batch][n][nq][hd] (rotated, model dtype, 16-byte
  * aligned), the rows' own keys and values already appended; out likewise,
@@ -563,6 +586,68 @@ int dflash_paged_attention_shared(dflash_pages *p, int32_t layer, const void *q,
                                   const int32_t *table, int32_t table_stride, const int32_t *len,
                                   const int32_t *shared_len, void *out, dflash_paged_workspace *ws,
                                   dflash_stream_t stream);
+
+/* --------------------------------------------------------- weights in 4 bits
+ * Products with weight matrices of 4-bit codes and a scale for each group of
+ * columns: what the quantised targets of the pages' engines keep ("DFlash
+ * 深度解析" §7; Q4 files of [RD] and the datacamp tutorial, named there, not
+ * shown), read as the plain affine form
+ *   w[m][k] = s[m][k / group] (code[m][k] - zero[m][k / group]),
+ * codes and zero points 0..15, zero point 8 for a matrix without zeros.  A decode
+ * step reads its weights once; in 4 bits they are a quarter of the bytes.  These
+ * calls stand beside dflash_linear.
+ *
+ * A matrix lives in one buffer of the caller's, dflash_w4_bytes long and 16-byte
+ * aligned, in the order in which the products read it (blocks of 128 rows by 128
+ * columns, each its codes, then its scales, then its zero points; rows and
+ * columns past M and K are padding).  dflash_w4_pack fills it from plain arrays,
+ * dflash_w4_quantize from a matrix, dflash_w4_unpack reads it back.  group is 32,
+ * 64 or 128 and divides K (else DFLASH_ERR_UNSUPPORTED_SHAPE); M is any; M K at
+ * most 2^34 (else DFLASH_ERR_TOO_LARGE).  Buffers that one of these calls writes
+ * overlap none that it reads (DFLASH_ERR_INVALID_ARG). */
+typedef struct dflash_w4 {
+  int32_t M, K, group;
+  int32_t scale_dtype; /* DFLASH_F32 | DFLASH_BF16 */
+  int32_t zeros;       /* 0: no zero points */
+  void *packed;
+} dflash_w4;
+/* Bytes of the buffer (w->packed is not looked at), or a negative DFLASH_ERR_*. */
+int64_t dflash_w4_bytes(const dflash_w4 *w);
+/* From codes [M][K / 2] (uint8: the even column's code in the low half), scales
+ * [M][K / group] of the scale type and zeros [M][K / group] (uint8, values above
+ * 15 count as 15; given exactly when w->zeros). */
+int dflash_w4_pack(const dflash_w4 *w, const void *codes, const void *scales, const void *zeros,
+                   dflash_stream_t stream);
+/* The nearest codes of a finite matrix src [M][K] of type dtype, rows ld elements
+ * apart.  Without zeros s = max|w| / 7 over a group and code = rhe(w / s) + 8;
+ * with them, over the range [min, max] stretched to hold 0, s = (max - min) / 15,
+ * zero = rhe(-min / s) and code = rhe(w / s) + zero; s is rounded to the scale
+ * type first and codes are clamped to 0..15 (rhe: round half to even; a group of
+ * zeros has s = 0). */
+int dflash_w4_quantize(const dflash_w4 *w, int32_t dtype, const void *src, int64_t ld, dflash_stream_t stream);
+/* dst [M][K] of type dtype: the values, rounded once. */
+int dflash_w4_unpack(const dflash_w4 *w, int32_t dtype, void *dst, dflash_stream_t stream);
+
+/* Scratch of the products: partial sums for up to max_rows (<= 128) rows and a
+ * status word, whatever the matrix.  Library-owned; bound to the device current
+ * at the call; one workspace serves one stream at a time, and so do graphs
+ * captured with it: graphs that may run at once need one each. */
+typedef struct dflash_w4_workspace dflash_w4_workspace;
+int dflash_w4_workspace_alloc(int32_t max_rows, dflash_w4_workspace **out);
+int dflash_w4_workspace_free(dflash_w4_workspace *ws);
+
+/* y[n][m] = sum_k x[n][k] w[m][k] (+ add[n][m]).  x [rows][K] of type dtype (the
+ * model's), rows ldx elements apart, of any alignment of its type; rows up to the
+ * workspace's.  swiglu = 0: y float32 [rows][M]; add, nullable, float32 [rows][M],
+ * is y itself (a residual stream) or apart from it.  swiglu = 1, M even: y
+ * [rows][M / 2] of type dtype, y[n][f] = silu(row 2f) * (row 2f + 1), the gate/up
+ * order of dflash_layer_w; add comes before the activation.
+ * Codes less zero points are small integers, exact in bf16; products are summed
+ * in float32 and the scale is applied to a group's sum, so the only roundings are
+ * float32's.  A row's result depends on its own x and the matrix only, and equal
+ * calls give equal bits. */
+int dflash_linear_w4(int32_t dtype, const void *x, int64_t ldx, const dflash_w4 *w, const float *add,
+                     int32_t swiglu, void *y, int32_t rows, dflash_w4_workspace *ws, dflash_stream_t stream);
 
 /* Kernel timing for measurement passes (not for graph capture): between
  * begin and end, the library brackets each weight-GEMM launch with a CUDA
