@@ -45,12 +45,13 @@ unsigned warp_tiles(const W4View& w) {
 }
 }  // namespace
 
+// (Packing and quantising do not let the next kernel start before their end: products read weights ahead of their
+// own wait.)
 // Codes [M][K / 2] (even column in the low half of a byte), scales and zeros [M][K / group].
 template <typename S>
 __global__ void __launch_bounds__(kPackWarps * 32)
     w4_pack_kernel(const __grid_constant__ W4View w, const uint8_t* __restrict__ codes, const S* __restrict__ scales,
                    const uint8_t* __restrict__ zeros) {
-  pdl_launch();
   pdl_wait();
   const WarpTile t = warp_tile(w);
   if (!t.live) return;
@@ -106,7 +107,6 @@ cudaError_t w4_pack(const W4View& w, const uint8_t* codes, const void* scales, c
 template <typename T>
 __global__ void __launch_bounds__(kPackWarps * 32)
     w4_quantize_kernel(const __grid_constant__ W4View w, const T* __restrict__ src, long long ld) {
-  pdl_launch();
   pdl_wait();
   const WarpTile t = warp_tile(w);
   if (!t.live) return;
@@ -221,12 +221,12 @@ cudaError_t w4_unpack(const W4View& w, int dtype, void* dst, cudaStream_t s) {
 // A block takes 64 weight rows and 16 rows of x and walks the columns 128 at a
 // time: the codes become float32 values in shared memory (code - zero times
 // scale: 2^-24 relative), a thread sums two weight rows (2 f, 2 f + 1: the pair
-// of the activation) by two rows of x, in the order of the columns.
+// of the activation) by two rows of x, in the order of the columns, 128 at a time
+// so that rounding errors grow with the number of blocks and not of columns.
 constexpr int kCoreN = 16, kCoreM = 64;
 
-template <typename T>
 __global__ void __launch_bounds__(256)
-    w4_core_kernel(const __grid_constant__ W4View w, const T* __restrict__ x, long long ldx, int rows,
+    w4_core_kernel(const __grid_constant__ W4View w, const float* __restrict__ x, long long ldx, int rows,
                    const __grid_constant__ W4Epi epi) {
   __shared__ float ws[kCoreM][kW4Tile + 1];
   __shared__ float xs[kCoreN][kW4Tile + 1];
@@ -259,18 +259,21 @@ __global__ void __launch_bounds__(256)
     }
     for (int i = tid; i < kCoreN * kW4Tile; i += 256) {
       const int r = i / kW4Tile, c = i % kW4Tile, kk = k * kW4Tile + c;
-      xs[r][c] = n0 + r < rows && kk < w.K ? to_f<T>(x[(n0 + r) * ldx + kk]) : 0.f;
+      xs[r][c] = n0 + r < rows && kk < w.K ? x[(n0 + r) * ldx + kk] : 0.f;
     }
     __syncthreads();
+    float part[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll 8
     for (int c = 0; c < kW4Tile; ++c) {
       const float w0 = ws[2 * mp][c], w1 = ws[2 * mp + 1][c];
       const float x0 = xs[2 * np][c], x1 = xs[2 * np + 1][c];
-      acc[0][0] = fmaf(x0, w0, acc[0][0]);
-      acc[0][1] = fmaf(x0, w1, acc[0][1]);
-      acc[1][0] = fmaf(x1, w0, acc[1][0]);
-      acc[1][1] = fmaf(x1, w1, acc[1][1]);
+      part[0][0] = fmaf(x0, w0, part[0][0]);
+      part[0][1] = fmaf(x0, w1, part[0][1]);
+      part[1][0] = fmaf(x1, w0, part[1][0]);
+      part[1][1] = fmaf(x1, w1, part[1][1]);
     }
+#pragma unroll
+    for (int a = 0; a < 4; ++a) acc[a >> 1][a & 1] += part[a >> 1][a & 1];
   }
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
@@ -283,12 +286,7 @@ __global__ void __launch_bounds__(256)
       if (m + 1 < w.M) y1 += epi.add[n * w.M + m + 1];
     }
     if (epi.swiglu) {
-      const float v = y0 / (1.f + expf(-y0)) * y1;
-      const long long at = n * (w.M / 2) + m / 2;
-      if (epi.out_bf16)
-        reinterpret_cast<bf16*>(epi.out)[at] = from_f<bf16>(v);
-      else
-        reinterpret_cast<float*>(epi.out)[at] = v;
+      reinterpret_cast<float*>(epi.out)[n * (w.M / 2) + m / 2] = y0 / (1.f + expf(-y0)) * y1;
     } else {
       float* out = reinterpret_cast<float*>(epi.out) + n * w.M + m;
       out[0] = y0;
@@ -297,13 +295,9 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-cudaError_t w4_linear_core(int dtype, const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi,
-                           cudaStream_t s) {
-  const dim3 grid((w.M + kCoreM - 1) / kCoreM, (rows + kCoreN - 1) / kCoreN), block(256);
-  if (dtype == DFLASH_F32)
-    DFL_RET(launch_pdl(w4_core_kernel<float>, grid, block, 0, s, w, (const float*)x, ldx, rows, epi));
-  else
-    DFL_RET(launch_pdl(w4_core_kernel<bf16>, grid, block, 0, s, w, (const bf16*)x, ldx, rows, epi));
+cudaError_t w4_linear_core(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi, cudaStream_t s) {
+  const dim3 grid((w.M + kCoreM - 1) / kCoreM, (rows + kCoreN - 1) / kCoreN);
+  DFL_RET(launch_pdl(w4_core_kernel, grid, dim3(256), 0, s, w, (const float*)x, ldx, rows, epi));
   count_launch();
   return cudaSuccess;
 }

@@ -56,15 +56,22 @@ __host__ __device__ __forceinline__ int w4_col(int h, int lane, int w, int p) {
 struct W4Epi {
   const float* add;  // null: none
   int swiglu;
-  int out_bf16;      // swiglu: the type of its result
-  void* out;
+  void* out;         // float32; with the activation of x's type
 };
 
 cudaError_t w4_pack(const W4View& w, const uint8_t* codes, const void* scales, const uint8_t* zeros, cudaStream_t s);
 cudaError_t w4_quantize(const W4View& w, int dtype, const void* src, long long ld, cudaStream_t s);
 cudaError_t w4_unpack(const W4View& w, int dtype, void* dst, cudaStream_t s);
-// The product on the CUDA cores.
-cudaError_t w4_linear_core(int dtype, const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi,
+// float32 x on the CUDA cores.
+cudaError_t w4_linear_core(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi,
                            cudaStream_t s);
+
+// bf16 x on the tensor cores.  part: w4_max_runs() * 2 pieces of 128 by (rows rounded up to 8, 16, 32 or whole 64s)
+// floats; tickets: w4_max_runs() * 2, zero between calls.
+cudaError_t w4_linear_mma(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi, float* part,
+                          int* tickets, cudaStream_t s);
+// Blocks of a run, and how many runs there are at most.
+int w4_run_blocks(const W4View& w);
+int w4_max_runs();
 
 }  // namespace dfl

@@ -11,6 +11,8 @@ using namespace dfl;
 struct dflash_w4_workspace {
   int32_t max_rows;
   int device;
+  float* part;
+  int* tickets;
 };
 
 #define CK(expr)                                         \
@@ -115,11 +117,28 @@ int dflash_w4_workspace_alloc(int32_t max_rows, dflash_w4_workspace** out) {
     delete ws;
     return record_cuda_error(e);
   }
+  const int rows = max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : (max_rows + 63) / 64 * 64;
+  const size_t runs = (size_t)w4_max_runs(), ticket_bytes = runs * 2 * sizeof(int);
+  if (cudaMalloc(&ws->part, runs * 2 * kW4Tile * rows * sizeof(float)) != cudaSuccess ||
+      cudaMalloc(&ws->tickets, ticket_bytes) != cudaSuccess) {
+    cudaGetLastError();
+    dflash_w4_workspace_free(ws);
+    return DFLASH_ERR_OOM;
+  }
+  cudaError_t z = cudaMemset(ws->tickets, 0, ticket_bytes);
+  if (z == cudaSuccess) z = cudaStreamSynchronize(0);
+  if (z != cudaSuccess) {
+    dflash_w4_workspace_free(ws);
+    return record_cuda_error(z);
+  }
   *out = ws;
   return DFLASH_OK;
 }
 
 int dflash_w4_workspace_free(dflash_w4_workspace* ws) {
+  if (!ws) return DFLASH_OK;
+  cudaFree(ws->part);
+  cudaFree(ws->tickets);
   delete ws;
   return DFLASH_OK;
 }
@@ -140,8 +159,11 @@ int dflash_linear_w4(int32_t dtype, const void* x, int64_t ldx, const dflash_w4*
   REQ(!add || (!swiglu && add == y) || apart(y, ybytes, add, (long long)rows * v.M * 4));
   int device = -1;
   REQ(cudaGetDevice(&device) == cudaSuccess && device == ws->device);
-  W4Epi epi = {add, swiglu != 0, dtype == DFLASH_BF16, y};
-  CK(w4_linear_core(dtype, v, x, ldx, rows, epi, (cudaStream_t)stream));
+  const W4Epi epi = {add, swiglu != 0, y};
+  if (dtype == DFLASH_BF16)
+    CK(w4_linear_mma(v, x, ldx, rows, epi, ws->part, ws->tickets, (cudaStream_t)stream));
+  else
+    CK(w4_linear_core(v, x, ldx, rows, epi, (cudaStream_t)stream));
   return DFLASH_OK;
 }
 

@@ -628,8 +628,8 @@ int dflash_w4_quantize(const dflash_w4 *w, int32_t dtype, const void *src, int64
 /* dst [M][K] of type dtype: the values, rounded once. */
 int dflash_w4_unpack(const dflash_w4 *w, int32_t dtype, void *dst, dflash_stream_t stream);
 
-/* Scratch of the products: partial sums for up to max_rows (<= 128) rows and a
- * status word, whatever the matrix.  Library-owned; bound to the device current
+/* Scratch of the products: partial sums for up to max_rows (<= 128) rows, whatever
+ * the matrix (0.6 MB a row).  Library-owned; bound to the device current
  * at the call; one workspace serves one stream at a time, and so do graphs
  * captured with it: graphs that may run at once need one each. */
 typedef struct dflash_w4_workspace dflash_w4_workspace;
