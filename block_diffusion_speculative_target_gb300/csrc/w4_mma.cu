@@ -8,11 +8,15 @@
 // rows of x their columns (n8), so a token costs one column of eight and not one
 // row of sixteen.
 //
-// A code pair becomes two bf16 in one register without a conversion: the bits
-// 0x4300 | code are the bf16 128 + code, and 128 + zero taken off it leaves
-// code - zero exactly: for 8 codes 3 shifts, 4 masks and 4 packed subtractions.
-// The codes lie in memory in the order of the products' fragments, so a lane
-// reads 32 of its own codes with one 16-byte load and nothing is shuffled.
+// A code pair becomes two bf16 in one register without a conversion.  Eight bits
+// v at the low end of a bf16 are the number v 2^-133, below the normal numbers and
+// just into them; so the low or the high half of a byte, masked out and multiplied
+// by 2^127 or 2^123, less zero / 64, is (code - zero) / 64 exactly: one mask and
+// one packed multiply-add a pair, one shift for every other byte.  (The integer
+// pipe has half the lanes of the others: with a shift for every pair it was the
+// bound.)  The results take the factor of 64 back.  The codes lie in memory in the
+// order of the products' fragments, so a lane reads 32 of its own codes with one
+// 16-byte load and nothing is shuffled.
 //
 // Split: the blocks of 128 by 128 of the whole matrix form a line (row blocks
 // one after another), cut into equal runs, one to a CTA, whatever M and K are.
@@ -66,16 +70,26 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Pair p of a word of codes, less the zero point: off = bf16 pair of 128 + zero.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+      "%10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Pair p (0, 1: of the low bytes) of a word of codes as (code - zero) / 64; off holds -zero / 64 twice.
 template <int P>
 __device__ __forceinline__ uint32_t pair_of(uint32_t word, uint32_t off) {
-  const uint32_t v = ((word >> (4 * P)) & 0x000F000Fu) | 0x43004300u;
   uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(off));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+      : "=r"(d)
+      : "r"(word & (P ? 0x00F000F0u : 0x000F000Fu)), "r"(P ? 0x7D007D00u : 0x7F007F00u), "r"(off));
   return d;
 }
+constexpr float kW4Unit = 64.f;
 __device__ __forceinline__ uint32_t offset_of(int zero) {
-  return 0x43004300u + (uint32_t)zero * 0x00010001u;  // (128 + zero needs 8 bits)
+  const __nv_bfloat162 v = __float2bfloat162_rn((float)zero * (-1.f / kW4Unit));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 }  // namespace
 
@@ -102,28 +116,31 @@ __global__ void __launch_bounds__(kThreads, MmaLayout<NT>::kCtas)
   const int b0 = blockIdx.x * run.per, b1 = min(b0 + run.per, run.blocks);
   const uint32_t base = smem_u32(smem);
 
-  auto load_codes = [&](int i) {  // block i of the line
-    const uint32_t dst = base + (uint32_t)((i - b0) % S) * stage_bytes;
-    const uint8_t* src = w.packed + (long long)i * w.block_bytes;
-    for (int c = tid * 16; c < w.block_bytes; c += kThreads * 16) cp16(dst + c, src + c);
+  // Codes, scales and zeros of the block at `src` into the stage at `at`.
+  auto load_codes = [&](const uint8_t* src, uint32_t at) {
+    const uint32_t dst = base + at + 16 * tid;
+    src += 16 * tid;
+#pragma unroll
+    for (int c = 0; c < kW4Codes; c += kThreads * 16) cp16(dst + c, src + c);
+    for (int c = kW4Codes; c + 16 * tid < w.block_bytes; c += kThreads * 16) cp16(dst + c, src + c);
   };
-  // the columns of x that block i meets: row r's chunk c (8 columns) at r * 256 + 16 (c ^ (r & 7))
-  auto load_x = [&](int i, bool async) {
-    const int slot = (i - b0) % S, k0 = i % w.kt * kW4Tile;
-    const uint32_t dst = base + (uint32_t)slot * stage_bytes + w.block_bytes;
-    uint8_t* sx = smem + (size_t)slot * stage_bytes + w.block_bytes;
+  // The columns k0 .. of x: row r's chunk c (8 columns) at r * 256 + 16 (c ^ (r & 7)); this thread brings chunk
+  // tid % 16 of the rows tid / 16 + 8 u.
+  const int xr = tid >> 4, xc = tid & 15;
+  const uint32_t x_at = (uint32_t)(w.block_bytes + xr * 256 + 16 * (xc ^ xr));
+  const bf16* x_row = x + (long long)(n0 + xr) * ldx + 8 * xc;
+  auto load_x = [&](int k0, uint32_t at, bool async) {
+    const bool in_k = k0 + 8 * xc < w.K;
+    at += x_at;
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-      const int r = u * 8 + (tid >> 4), c = tid & 15, k = k0 + 8 * c;
-      const uint32_t at = (uint32_t)(r * 256 + 16 * (c ^ (r & 7)));
-      const bool in = n0 + r < rows && k < w.K;
-      const bf16* src = x + (in ? (long long)(n0 + r) * ldx + k : 0);
+      const bool in = in_k && n0 + xr + 8 * u < rows;
+      const bf16* src = in ? x_row + (long long)(8 * u) * ldx + k0 : x;
+      uint4* dst = reinterpret_cast<uint4*>(smem + at + u * 2048);
       if (vec && async) {
-        cp16z(dst + at, src, in ? 16 : 0);
+        cp16z(base + at + u * 2048, src, in ? 16 : 0);
       } else if (vec) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (in) v = *reinterpret_cast<const uint4*>(src);
-        *reinterpret_cast<uint4*>(sx + at) = v;
+        *dst = in ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
       } else {
         uint32_t v[4] = {0u, 0u, 0u, 0u};
         if (in) {
@@ -131,23 +148,29 @@ __global__ void __launch_bounds__(kThreads, MmaLayout<NT>::kCtas)
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
         }
-        *reinterpret_cast<uint4*>(sx + at) = make_uint4(v[0], v[1], v[2], v[3]);
+        *dst = make_uint4(v[0], v[1], v[2], v[3]);
       }
     }
   };
 
   // The weights do not depend on the kernels before this one (packing lets no successor start early): the first
   // stages are asked for before the wait.
+  const uint8_t* next_block = w.packed + (long long)b0 * w.block_bytes;
+  int mt = b0 / w.kt, kb = b0 - mt * w.kt;  // the block at hand
+  int next_kb = kb;                         // the next one to be asked for
 #pragma unroll
   for (int u = 0; u < S - 1; ++u) {
-    if (b0 + u < b1) load_codes(b0 + u);
+    if (b0 + u < b1) load_codes(next_block, u * stage_bytes);
+    next_block += w.block_bytes;
     cp_commit();
   }
   pdl_launch();
   pdl_wait();
 #pragma unroll
-  for (int u = 0; u < S - 1; ++u)
-    if (b0 + u < b1) load_x(b0 + u, false);
+  for (int u = 0; u < S - 1; ++u) {
+    if (b0 + u < b1) load_x(next_kb * kW4Tile, u * stage_bytes, false);
+    if (++next_kb == w.kt) next_kb = 0;
+  }
 
   float acc[2][NT][4];
 #pragma unroll
@@ -161,16 +184,23 @@ __global__ void __launch_bounds__(kThreads, MmaLayout<NT>::kCtas)
 #pragma unroll
   for (int y = 0; y < 2; ++y) off[y][0] = off[y][1] = offset_of(kW4Zero);
 
+  uint32_t at = 0, next_at = (S - 1) * stage_bytes;  // the stage at hand and the one to fill
   for (int i = b0; i < b1; ++i) {
     cp_wait<S - 2>();
     __syncthreads();
     if (i + S - 1 < b1) {
-      load_codes(i + S - 1);
-      load_x(i + S - 1, true);
+      load_codes(next_block, next_at);
+      load_x(next_kb * kW4Tile, next_at, true);
+      next_block += w.block_bytes;
+      if (++next_kb == w.kt) next_kb = 0;
     }
     cp_commit();
-    const uint8_t* blk = smem + (size_t)((i - b0) % S) * stage_bytes;
-    const uint32_t xs = base + (uint32_t)((i - b0) % S) * stage_bytes + w.block_bytes;
+    const uint8_t* blk = smem + at;
+    // chunk 4 q + lane / 8 of row 8 j + lane % 8
+    const uint32_t xs = base + at + w.block_bytes + (lane & 7) * 256 + 16 * ((lane >> 3) ^ (lane & 3));
+    next_at = at;
+    at += stage_bytes;
+    if (at == S * stage_bytes) at = 0;
     float c[2][NT][4];
     uint4 word[2];
 #pragma unroll
@@ -180,21 +210,12 @@ __global__ void __launch_bounds__(kThreads, MmaLayout<NT>::kCtas)
         for (int y = 0; y < 2; ++y)
           word[y] = *reinterpret_cast<const uint4*>(blk + w4_word_at(2 * warp + y, q >> 1, lane));
       }
-      const bool first = q % groups32 == 0;
-      if (first) {
+      if (w.zeros && (q & (groups32 - 1)) == 0) {
+        const uint8_t* z = blk + zero_at + q / groups32 * kW4Tile + 32 * warp + g;
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[y][j][e] = 0.f;
-        if (w.zeros) {
-          const uint8_t* z = blk + zero_at + q / groups32 * kW4Tile + 32 * warp + g;
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) off[y][r] = offset_of(z[16 * y + 8 * r]);
-        }
+          for (int r = 0; r < 2; ++r) off[y][r] = offset_of(z[16 * y + 8 * r]);
       }
       uint32_t a[2][2][4];  // [m tile][step]
 #pragma unroll
@@ -204,27 +225,31 @@ __global__ void __launch_bounds__(kThreads, MmaLayout<NT>::kCtas)
         a[y][0][1] = pair_of<0>(hi, off[y][1]);
         a[y][0][2] = pair_of<1>(lo, off[y][0]);
         a[y][0][3] = pair_of<1>(hi, off[y][1]);
-        a[y][1][0] = pair_of<2>(lo, off[y][0]);
-        a[y][1][1] = pair_of<2>(hi, off[y][1]);
-        a[y][1][2] = pair_of<3>(lo, off[y][0]);
-        a[y][1][3] = pair_of<3>(hi, off[y][1]);
+        a[y][1][0] = pair_of<0>(lo >> 8, off[y][0]);
+        a[y][1][1] = pair_of<0>(hi >> 8, off[y][1]);
+        a[y][1][2] = pair_of<1>(lo >> 8, off[y][0]);
+        a[y][1][3] = pair_of<1>(hi >> 8, off[y][1]);
       }
-      // chunks 4 q .. 4 q + 3 of 8 rows of x: (b0, b1) of the first step, then of the second
+      // four chunks of 8 rows of x: (b0, b1) of the first step, then of the second.  (4 q ^ bit 2 of the row: the
+      // rest of the swizzle is in xs)
+      const bool fresh = (q & (groups32 - 1)) == 0;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         uint32_t b[4];
-        const int r = 8 * j + (lane & 7), ch = 4 * q + (lane >> 3);
-        ldsm4(b, xs + (uint32_t)(r * 256 + 16 * (ch ^ (r & 7))));
+        ldsm4(b, xs + j * 2048 + 16 * ((4 * q) ^ (lane & 4)));
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          mma16816(c[y][j], a[y][0], b[0], b[1]);
+          if (q == 0 || fresh)
+            mma16816_first(c[y][j], a[y][0], b[0], b[1]);
+          else
+            mma16816(c[y][j], a[y][0], b[0], b[1]);
           mma16816(c[y][j], a[y][1], b[2], b[3]);
         }
       }
-      if ((q + 1) % groups32 == 0) {
-        const int at = q / groups32 * kW4Tile + 32 * warp + g;
-        const float* sf = reinterpret_cast<const float*>(blk + kW4Codes) + at;
-        const bf16* sb = reinterpret_cast<const bf16*>(blk + kW4Codes) + at;
+      if (((q + 1) & (groups32 - 1)) == 0) {
+        const int sat = q / groups32 * kW4Tile + 32 * warp + g;
+        const float* sf = reinterpret_cast<const float*>(blk + kW4Codes) + sat;
+        const bf16* sb = reinterpret_cast<const bf16*>(blk + kW4Codes) + sat;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const float s0 = w.scale_f32 ? sf[16 * y] : to_f<bf16>(sb[16 * y]);
@@ -239,53 +264,65 @@ __global__ void __launch_bounds__(kThreads, MmaLayout<NT>::kCtas)
         }
       }
     }
-    const int mt = i / w.kt;
-    const bool tile_end = i - mt * w.kt == w.kt - 1;
-    if (!tile_end && i + 1 < b1) continue;
+    const int tile = mt;
+    const bool tile_end = ++kb == w.kt;
+    if (tile_end) {
+      kb = 0;
+      ++mt;
+    } else if (i + 1 < b1) {
+      continue;
+    }
     // The row block ends here, or the run does.
-    const int t0 = mt * w.kt, first_run = t0 / run.per, last_run = (t0 + w.kt - 1) / run.per, pieces = last_run - first_run + 1;
+    const int t0 = tile * w.kt, first_run = t0 / run.per, last_run = (t0 + w.kt - 1) / run.per;
     bool done = true;
-    if (pieces > 1) {
+    if (last_run > first_run) {
       // run r's piece of the row block: its first slot if the run begins in the block, else its second
       auto slot = [&](int r) {
-        return run.part +
-               (((long long)blockIdx.y * run.runs + r) * 2 + (r * run.per < t0)) * (kW4Tile * L::kRows);
+        return reinterpret_cast<float4*>(run.part + (((long long)blockIdx.y * run.runs + r) * 2 + (r * run.per < t0)) *
+                                                        (kW4Tile * L::kRows)) + tid;
       };
-      float4* own = reinterpret_cast<float4*>(slot(blockIdx.x));
+      float4* own = slot(blockIdx.x);
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          own[(y * NT + j) * kThreads + tid] = make_float4(acc[y][j][0], acc[y][j][1], acc[y][j][2], acc[y][j][3]);
+      for (int v = 0; v < 2 * NT; ++v) {
+        const float* p = acc[v / NT][v % NT];
+        __stcg(own + v * kThreads, make_float4(p[0], p[1], p[2], p[3]));
+      }
       __threadfence();
       __syncthreads();
-      int* ticket = run.tickets + blockIdx.y * run.runs + first_run;
       if (tid == 0) {
-        const int was = atomicAdd(ticket, 1);
-        last_s = was == pieces - 1;
-        if (was == pieces - 1) *ticket = 0;
+        int* ticket = run.tickets + blockIdx.y * run.runs + first_run;
+        last_s = atomicAdd(ticket, 1) == last_run - first_run;
+        if (last_s) *ticket = 0;
       }
       __syncthreads();
       done = last_s;
       if (done) {
         __threadfence();
+        // the pieces' sums in order, the loads of several in flight
+        constexpr int kAhead = NT <= 2 ? 4 : NT == 4 ? 2 : 1;
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int v = 0; v < 2 * NT; ++v)
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
+          for (int e = 0; e < 4; ++e) acc[v / NT][v % NT][e] = 0.f;
+        for (int r = first_run; r <= last_run; r += kAhead) {
+          float4 p[kAhead][2 * NT];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[y][j][e] = 0.f;
-        for (int r = first_run; r <= last_run; ++r) {
-          const float4* p = reinterpret_cast<const float4*>(slot(r));
+          for (int u = 0; u < kAhead; ++u) {
+            const float4* src = slot(min(r + u, last_run));
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
+            for (int v = 0; v < 2 * NT; ++v) p[u][v] = __ldcg(src + v * kThreads);
+          }
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const float4 v = __ldcg(p + (y * NT + j) * kThreads + tid);
-              acc[y][j][0] += v.x;
-              acc[y][j][1] += v.y;
-              acc[y][j][2] += v.z;
-              acc[y][j][3] += v.w;
+          for (int u = 0; u < kAhead; ++u)
+            if (r + u <= last_run) {
+#pragma unroll
+              for (int v = 0; v < 2 * NT; ++v) {
+                float* d = acc[v / NT][v % NT];
+                d[0] += p[u][v].x;
+                d[1] += p[u][v].y;
+                d[2] += p[u][v].z;
+                d[3] += p[u][v].w;
+              }
             }
         }
       }
@@ -297,10 +334,10 @@ __global__ void __launch_bounds__(kThreads, MmaLayout<NT>::kCtas)
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int m = mt * kW4Tile + 32 * warp + 16 * y + g + 8 * (e >> 1);
+            const int m = tile * kW4Tile + 32 * warp + 16 * y + g + 8 * (e >> 1);
             const int n = n0 + 8 * j + 2 * t + (e & 1);
             const bool live = m < w.M && n < rows;
-            float v = acc[y][j][e];
+            float v = acc[y][j][e] * kW4Unit;
             if (epi.add && live) v += epi.add[(long long)n * w.M + m];
             if (epi.swiglu) {  // the lane of row m + 1 is 4 further
               const float up = __shfl_down_sync(0xffffffffu, v, 4);
@@ -314,11 +351,9 @@ __global__ void __launch_bounds__(kThreads, MmaLayout<NT>::kCtas)
           }
     }
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
+    for (int v = 0; v < 2 * NT; ++v)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[y][j][e] = 0.f;
+      for (int e = 0; e < 4; ++e) acc[v / NT][v % NT][e] = 0.f;
   }
 }
 
