@@ -115,6 +115,7 @@ _SIGS = {
     "dflash_w4_unpack": (_I, [POINTER(W4C), _I, _P, _P]),
     "dflash_w4_workspace_alloc": (_I, [_I, POINTER(c_void_p)]),
     "dflash_w4_workspace_free": (_I, [_P]),
+    "dflash_w4_status": (_I, [_P, _P, POINTER(c_int32)]),
     "dflash_linear_w4": (_I, [_I, _P, ctypes.c_int64, POINTER(W4C), _P, _I, _P, _I, _P, _P]),
     "dflash_profile_begin": (_I, [_I]),
     "dflash_launch_count": (ctypes.c_longlong, []),
@@ -502,6 +503,12 @@ def dflash_w4_workspace_alloc(max_rows):
 
 def dflash_w4_workspace_free(ws):
     _check(load().dflash_w4_workspace_free(ws), "dflash_w4_workspace_free")
+
+
+def dflash_w4_status(ws, stream=None):
+    v = c_int32()
+    _check(load().dflash_w4_status(ws, _stream(stream), ctypes.byref(v)), "dflash_w4_status")
+    return v.value
 
 
 def dflash_linear_w4(dtype, x, ldx, w: W4C, add, swiglu, y, rows, ws, stream=None):

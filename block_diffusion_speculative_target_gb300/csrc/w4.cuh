@@ -66,10 +66,16 @@ cudaError_t w4_unpack(const W4View& w, int dtype, void* dst, cudaStream_t s);
 cudaError_t w4_linear_core(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi,
                            cudaStream_t s);
 
-// bf16 x on the tensor cores.  part: w4_max_runs() * 2 pieces of 128 by (rows rounded up to 8, 16, 32 or whole 64s)
-// floats; tickets: w4_max_runs() * 2, zero between calls.
-cudaError_t w4_linear_mma(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi, float* part,
-                          int* tickets, cudaStream_t s);
+// Scratch of the tensor-core products: w4_max_runs() * 2 pieces of 128 by (rows, rounded up to a power of two, 8 at
+// least) floats; w4_max_runs() * 2 tickets, zero between calls; the status word.
+struct W4Scratch {
+  float* part;
+  int* tickets;
+  int* status;
+};
+// bf16 x on the tensor cores.
+cudaError_t w4_linear_tc(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi, const W4Scratch& sc,
+                         cudaStream_t s);
 // Blocks of a run, and how many runs there are at most.
 int w4_run_blocks(const W4View& w);
 int w4_max_runs();

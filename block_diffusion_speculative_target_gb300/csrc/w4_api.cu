@@ -11,8 +11,8 @@ using namespace dfl;
 struct dflash_w4_workspace {
   int32_t max_rows;
   int device;
-  float* part;
-  int* tickets;
+  size_t ticket_bytes;
+  W4Scratch sc;
 };
 
 #define CK(expr)                                         \
@@ -117,15 +117,24 @@ int dflash_w4_workspace_alloc(int32_t max_rows, dflash_w4_workspace** out) {
     delete ws;
     return record_cuda_error(e);
   }
-  const int rows = max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : (max_rows + 63) / 64 * 64;
-  const size_t runs = (size_t)w4_max_runs(), ticket_bytes = runs * 2 * sizeof(int);
-  if (cudaMalloc(&ws->part, runs * 2 * kW4Tile * rows * sizeof(float)) != cudaSuccess ||
-      cudaMalloc(&ws->tickets, ticket_bytes) != cudaSuccess) {
-    cudaGetLastError();
-    dflash_w4_workspace_free(ws);
-    return DFLASH_ERR_OOM;
-  }
-  cudaError_t z = cudaMemset(ws->tickets, 0, ticket_bytes);
+  int rows = 8;
+  while (rows < max_rows) rows *= 2;
+  const size_t runs = (size_t)w4_max_runs();
+  ws->ticket_bytes = runs * 2 * sizeof(int);
+  struct Req {
+    void** p;
+    size_t bytes;
+  } reqs[] = {{(void**)&ws->sc.part, runs * 2 * kW4Tile * rows * sizeof(float)},
+              {(void**)&ws->sc.tickets, ws->ticket_bytes},
+              {(void**)&ws->sc.status, sizeof(int)}};
+  for (auto& r : reqs)
+    if (cudaMalloc(r.p, r.bytes) != cudaSuccess) {
+      cudaGetLastError();
+      dflash_w4_workspace_free(ws);
+      return DFLASH_ERR_OOM;
+    }
+  cudaError_t z = cudaMemset(ws->sc.tickets, 0, ws->ticket_bytes);
+  if (z == cudaSuccess) z = cudaMemset(ws->sc.status, 0, sizeof(int));
   if (z == cudaSuccess) z = cudaStreamSynchronize(0);
   if (z != cudaSuccess) {
     dflash_w4_workspace_free(ws);
@@ -137,9 +146,23 @@ int dflash_w4_workspace_alloc(int32_t max_rows, dflash_w4_workspace** out) {
 
 int dflash_w4_workspace_free(dflash_w4_workspace* ws) {
   if (!ws) return DFLASH_OK;
-  cudaFree(ws->part);
-  cudaFree(ws->tickets);
+  cudaFree(ws->sc.part);
+  cudaFree(ws->sc.tickets);
+  cudaFree(ws->sc.status);
   delete ws;
+  return DFLASH_OK;
+}
+
+int dflash_w4_status(dflash_w4_workspace* ws, dflash_stream_t stream, int32_t* status_out) {
+  REQ(ws && status_out);
+  int32_t v = 0;
+  const cudaStream_t s = (cudaStream_t)stream;
+  CK(cudaMemcpyAsync(&v, ws->sc.status, 4, cudaMemcpyDeviceToHost, s));
+  CK(cudaMemsetAsync(ws->sc.status, 0, 4, s));
+  CK(cudaStreamSynchronize(s));
+  // a call that timed out may have left pieces counted
+  if (v & DFLASH_STATUS_TIMEOUT) CK(cudaMemsetAsync(ws->sc.tickets, 0, ws->ticket_bytes, s));
+  *status_out = v;
   return DFLASH_OK;
 }
 
@@ -161,7 +184,7 @@ int dflash_linear_w4(int32_t dtype, const void* x, int64_t ldx, const dflash_w4*
   REQ(cudaGetDevice(&device) == cudaSuccess && device == ws->device);
   const W4Epi epi = {add, swiglu != 0, y};
   if (dtype == DFLASH_BF16)
-    CK(w4_linear_mma(v, x, ldx, rows, epi, ws->part, ws->tickets, (cudaStream_t)stream));
+    CK(w4_linear_tc(v, x, ldx, rows, epi, ws->sc, (cudaStream_t)stream));
   else
     CK(w4_linear_core(v, x, ldx, rows, epi, (cudaStream_t)stream));
   return DFLASH_OK;

@@ -533,6 +533,10 @@ class W4Workspace:
             self.device = torch.device("cuda", torch.cuda.current_device())
             self.handle = capi.dflash_w4_workspace_alloc(max_rows)
 
+    def status(self):
+        with torch.cuda.device(self.device):
+            return capi.dflash_w4_status(self.handle)
+
     def close(self):
         """Frees the scratch.  Work of the calls made so far has to be done."""
         if self.handle:

@@ -205,8 +205,8 @@ int dflash_status(dflash_workspace *w, dflash_stream_t stream, int32_t *status_o
  * workspace or another `which`.  No synchronisation: read it on the stream. */
 float *dflash_workspace_logits(dflash_workspace *w, int32_t which);
 /* Failure-path testing: sets the limit, in nanoseconds, of the waits in the
- * main loop of the weight-product kernel (ring slots and accumulator) and of
- * the bf16 attention over pages, for launches enqueued afterwards; a negative
+ * main loop of the weight-product kernel (ring slots and accumulator), of the
+ * bf16 products with 4-bit weights and of the bf16 attention over pages, for launches enqueued afterwards; a negative
  * value restores the default of 500 ms.  A limit of 0 expires at once, so the
  * kernel gives up, sets DFLASH_STATUS_TIMEOUT, still waits (with the default
  * limit) for its copies and products in flight and returns; the weight product
@@ -629,12 +629,16 @@ int dflash_w4_quantize(const dflash_w4 *w, int32_t dtype, const void *src, int64
 int dflash_w4_unpack(const dflash_w4 *w, int32_t dtype, void *dst, dflash_stream_t stream);
 
 /* Scratch of the products: partial sums for up to max_rows (<= 128) rows, whatever
- * the matrix (0.6 MB a row).  Library-owned; bound to the device current
+ * the matrix (0.6 MB a row), and a status word.  Library-owned; bound to the device current
  * at the call; one workspace serves one stream at a time, and so do graphs
  * captured with it: graphs that may run at once need one each. */
 typedef struct dflash_w4_workspace dflash_w4_workspace;
 int dflash_w4_workspace_alloc(int32_t max_rows, dflash_w4_workspace **out);
 int dflash_w4_workspace_free(dflash_w4_workspace *ws);
+/* Synchronises `stream` (the one that the workspace's calls were made on), returns
+ * the status bits in *status_out and clears them.  After DFLASH_STATUS_TIMEOUT (a
+ * wait ran out) the results of the calls since the last status are unspecified. */
+int dflash_w4_status(dflash_w4_workspace *ws, dflash_stream_t stream, int32_t *status_out);
 
 /* y[n][m] = sum_k x[n][k] w[m][k] (+ add[n][m]).  x [rows][K] of type dtype (the
  * model's), rows ldx elements apart, of any alignment of its type; rows up to the
