@@ -217,6 +217,16 @@ cudaError_t w4_unpack(const W4View& w, int dtype, void* dst, cudaStream_t s) {
   return cudaSuccess;
 }
 
+// ------------------------------------------------------------------ split
+constexpr int kRunsPerSm = 4;
+constexpr int kMinRun = 4;  // blocks of a run at least
+int w4_max_runs() { return num_sms() * kRunsPerSm; }
+W4Run w4_run(const W4View& w, const W4Scratch& sc, int per_sm) {
+  const int blocks = (w.M + kW4Tile - 1) / kW4Tile * w.kt, most = num_sms() * std::min(per_sm, kRunsPerSm);
+  const int per = std::max(kMinRun, (blocks + most - 1) / most);
+  return W4Run{blocks, per, (blocks + per - 1) / per, sc.part, sc.tickets, sc.status, wait_limit_ns()};
+}
+
 // ------------------------------------------------------------------ product on the CUDA cores
 // A block takes 64 weight rows and 16 rows of x and walks the columns 128 at a
 // time: the codes become float32 values in shared memory (code - zero times

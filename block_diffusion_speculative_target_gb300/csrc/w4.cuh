@@ -67,17 +67,27 @@ cudaError_t w4_linear_core(const W4View& w, const void* x, long long ldx, int ro
                            cudaStream_t s);
 
 // Scratch of the tensor-core products: w4_max_runs() * 2 pieces of 128 by (rows, rounded up to a power of two, 8 at
-// least) floats; w4_max_runs() * 2 tickets, zero between calls; the status word.
+// least) floats; w4_max_runs() * 4 tickets, zero between calls; the status word.
 struct W4Scratch {
   float* part;
   int* tickets;
   int* status;
 };
-// bf16 x on the tensor cores.
+// How a product is split, and its scratch.
+struct W4Run {
+  int blocks, per, runs;  // blocks of the matrix, blocks a run, runs
+  float* part;            // [runs][2][float4 of sums a thread][128 threads][4]
+  int* tickets;           // [runs][4 warps] of the row block that begins in the run and ends in a later one
+  int* status;
+  unsigned long long wait_ns;
+};
+// `per_sm`: runs an SM at most, up to 4.
+W4Run w4_run(const W4View& w, const W4Scratch& sc, int per_sm);
+int w4_max_runs();
+// bf16 x on the tensor cores, up to 32 rows: fed from registers; more: from TMEM and shared memory.
+cudaError_t w4_linear_mma(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi,
+                          const W4Scratch& sc, cudaStream_t s);
 cudaError_t w4_linear_tc(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi, const W4Scratch& sc,
                          cudaStream_t s);
-// Blocks of a run, and how many runs there are at most.
-int w4_run_blocks(const W4View& w);
-int w4_max_runs();
 
 }  // namespace dfl

@@ -120,7 +120,7 @@ int dflash_w4_workspace_alloc(int32_t max_rows, dflash_w4_workspace** out) {
   int rows = 8;
   while (rows < max_rows) rows *= 2;
   const size_t runs = (size_t)w4_max_runs();
-  ws->ticket_bytes = runs * 2 * sizeof(int);
+  ws->ticket_bytes = runs * 4 * sizeof(int);
   struct Req {
     void** p;
     size_t bytes;
@@ -183,7 +183,9 @@ int dflash_linear_w4(int32_t dtype, const void* x, int64_t ldx, const dflash_w4*
   int device = -1;
   REQ(cudaGetDevice(&device) == cudaSuccess && device == ws->device);
   const W4Epi epi = {add, swiglu != 0, y};
-  if (dtype == DFLASH_BF16)
+  if (dtype == DFLASH_BF16 && rows <= 32)
+    CK(w4_linear_mma(v, x, ldx, rows, epi, ws->sc, (cudaStream_t)stream));
+  else if (dtype == DFLASH_BF16)
     CK(w4_linear_tc(v, x, ldx, rows, epi, ws->sc, (cudaStream_t)stream));
   else
     CK(w4_linear_core(v, x, ldx, rows, epi, (cudaStream_t)stream));

@@ -1,0 +1,127 @@
+// What the tensor-core products with 4-bit weights share: copies, codes to bf16,
+// and the end of a row block (joining its pieces, writing its results).
+#pragma once
+#include "common.cuh"
+#include "w4.cuh"
+
+namespace dfl {
+
+constexpr uint64_t kW4DrainNs = 125000000ull;  // for copies and products in flight after a wait that ran out
+
+// `bytes` of 16 (0: none is read), the rest zeros
+__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// 8 values of x at any alignment, or zeros.
+__device__ __forceinline__ uint4 gather8(const bf16* src, bool in) {
+  uint32_t v[4] = {0u, 0u, 0u, 0u};
+  if (in) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+// A phase is complete, waited for up to the limit (0: it has expired).  Asked once by itself first: 50 cycles
+// where the phase is over, and 100 to 290 through the loop.
+__device__ __forceinline__ bool landed(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (limit_ns != 0 && mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, limit_ns);
+}
+
+// Pair P (0, 1: of the low bytes) of a word of codes as (code - zero) / 64; off holds -zero / 64 twice.
+template <int P>
+__device__ __forceinline__ uint32_t pair_of(uint32_t word, uint32_t off) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+      : "=r"(d)
+      : "r"(word & (P ? 0x00F000F0u : 0x000F000Fu)), "r"(P ? 0x7D007D00u : 0x7F007F00u), "r"(off));
+  return d;
+}
+constexpr float kW4Unit = 64.f;
+__device__ __forceinline__ uint32_t offset_of(int zero) {
+  const __nv_bfloat162 v = __float2bfloat162_rn((float)zero * (-1.f / kW4Unit));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// One warp's share of the row block `tile`, whose last column that this run holds has been added: V float4 of sums a
+// thread.  Where other runs hold some of its columns, the sums are left for whoever comes last; true if that is this
+// warp (then `acc` is the whole sum, the pieces added in order of the columns), or if there are no others.
+template <int V>
+__device__ __forceinline__ bool w4_join(const W4View& w, const W4Run& run, int tile, int tid, float (&acc)[V][4]) {
+  const int t0 = tile * w.kt, first = t0 / run.per, last = (t0 + w.kt - 1) / run.per;
+  if (first == last) return true;
+  // run r's piece of the row block: its first slot if the run begins in the block, else its second
+  auto piece = [&](int r) {
+    return reinterpret_cast<float4*>(run.part) + ((long long)r * 2 + (r * run.per < t0)) * (V * kW4Tile) + tid;
+  };
+  float4* own = piece(blockIdx.x);
+#pragma unroll
+  for (int v = 0; v < V; ++v) __stcg(own + v * kW4Tile, make_float4(acc[v][0], acc[v][1], acc[v][2], acc[v][3]));
+  __threadfence();
+  __syncwarp();
+  int ends = 0;
+  if ((tid & 31) == 0) {
+    int* ticket = run.tickets + first * 4 + (tid >> 5);
+    ends = atomicAdd(ticket, 1) == last - first;
+    if (ends) *ticket = 0;
+  }
+  if (!__shfl_sync(0xffffffffu, ends, 0)) return false;
+  __threadfence();
+  constexpr int kV = V < 4 ? V : 4, kAhead = 4;  // loads in flight: kAhead pieces
+#pragma unroll
+  for (int v0 = 0; v0 < V; v0 += kV) {
+    float sum[kV][4];
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[v][e] = 0.f;
+    for (int r = first; r <= last; r += kAhead) {
+      float4 p[kAhead][kV];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float4* src = piece(min(r + u, last)) + v0 * kW4Tile;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) p[u][v] = __ldcg(src + v * kW4Tile);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (r + u <= last) {
+#pragma unroll
+          for (int v = 0; v < kV; ++v) {
+            sum[v][0] += p[u][v].x;
+            sum[v][1] += p[u][v].y;
+            sum[v][2] += p[u][v].z;
+            sum[v][3] += p[u][v].w;
+          }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[v0 + v][e] = sum[v][e];
+  }
+  return true;
+}
+
+// Result (n, m) from its sum; with the activation row m + 1's is PAIR lanes further.
+template <int PAIR>
+__device__ __forceinline__ void w4_write(const W4View& w, const W4Epi& epi, int m, int n, int rows, float sum) {
+  const bool live = m < w.M && n < rows;
+  float v = sum * kW4Unit;
+  if (epi.add && live) v += epi.add[(long long)n * w.M + m];
+  if (epi.swiglu) {
+    const float up = __shfl_down_sync(0xffffffffu, v, PAIR);
+    if (live && !(m & 1))
+      reinterpret_cast<bf16*>(epi.out)[(long long)n * (w.M / 2) + m / 2] = from_f<bf16>(v / (1.f + expf(-v)) * up);
+  } else if (live) {
+    reinterpret_cast<float*>(epi.out)[(long long)n * w.M + m] = v;
+  }
+}
+
+}  // namespace dfl
