@@ -46,7 +46,8 @@ template <int NT>
 struct MmaLayout {
   static constexpr int kRows = 8 * NT;
   static constexpr int kX = kRows * 256;  // 128 columns of bf16, 16-byte chunks swizzled by row
-  static constexpr int kStages = NT == 1 ? 5 : NT == 2 ? 4 : 3;
+  static constexpr int kStages = NT == 1 ? 4 : 3;
+  static constexpr int kSums = 4 * kRows * kW4SumRow * 4;  // the warps' sums at a row block's end
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -247,14 +248,15 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     // The row block ends here, or the run does.  A warp deals with its 32 rows by itself.
     if (w4_join<V>(w, run, tile, tid, acc)) {
+      float* sums = reinterpret_cast<float*>(smem + S * stage_bytes) + warp * (L::kRows * kW4SumRow);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int m = tile * kW4Tile + 32 * warp + 16 * (v / NT) + g + 8 * (e >> 1);
-          const int n = 8 * (v % NT) + 2 * t + (e & 1);
-          w4_write<4>(w, epi, m, n, rows, acc[v][e]);
-        }
+        for (int e = 0; e < 4; ++e)
+          sums[(8 * (v % NT) + 2 * t + (e & 1)) * kW4SumRow + 16 * (v / NT) + g + 8 * (e >> 1)] = acc[v][e];
+      __syncwarp();
+      w4_results(w, epi, tile * kW4Tile + 32 * warp, sums, 0, rows);
+      __syncwarp();
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -270,15 +272,15 @@ cudaError_t mma_launch(const W4View& w, const bf16* x, long long ldx, int rows, 
   typedef MmaLayout<NT> L;
   static PerDevice attr;
   // (the widest block: float32 scales and zero points)
-  constexpr int kMost = L::kStages * (kW4Codes + (4 >> GS) * kW4Tile * 5 + L::kX);
+  constexpr int kMost = L::kStages * (kW4Codes + (4 >> GS) * kW4Tile * 5 + L::kX) + L::kSums;
   static_assert(kMost <= 232448 - 1024, "shared memory per block");
   DFL_RET(attr.once([] {
     return cudaFuncSetAttribute(w4_mma_kernel<NT, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   }));
   const int vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx % 8 == 0;
   const W4Run run = w4_run(w, sc, 4);
-  DFL_RET(launch_pdl(w4_mma_kernel<NT, GS>, dim3(run.runs), dim3(kThreads), L::kStages * (w.block_bytes + L::kX), s, w,
-                     run, x, ldx, vec, rows, epi));
+  DFL_RET(launch_pdl(w4_mma_kernel<NT, GS>, dim3(run.runs), dim3(kThreads), L::kStages * (w.block_bytes + L::kX) + L::kSums,
+                     s, w, run, x, ldx, vec, rows, epi));
   count_launch();
   return cudaSuccess;
 }

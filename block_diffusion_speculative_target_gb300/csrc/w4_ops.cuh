@@ -109,18 +109,34 @@ __device__ __forceinline__ bool w4_join(const W4View& w, const W4Run& run, int t
   return true;
 }
 
-// Result (n, m) from its sum; with the activation row m + 1's is PAIR lanes further.
-template <int PAIR>
-__device__ __forceinline__ void w4_write(const W4View& w, const W4Epi& epi, int m, int n, int rows, float sum) {
-  const bool live = m < w.M && n < rows;
-  float v = sum * kW4Unit;
-  if (epi.add && live) v += epi.add[(long long)n * w.M + m];
-  if (epi.swiglu) {
-    const float up = __shfl_down_sync(0xffffffffu, v, PAIR);
-    if (live && !(m & 1))
-      reinterpret_cast<bf16*>(epi.out)[(long long)n * (w.M / 2) + m / 2] = from_f<bf16>(v / (1.f + expf(-v)) * up);
-  } else if (live) {
-    reinterpret_cast<float*>(epi.out)[(long long)n * w.M + m] = v;
+// A warp's results: the whole sums of row `lane` of its 32 rows (of the matrix's from m0 on) and row n of x at
+// sums[n * kW4SumRow + lane] in shared memory, n < count, for the rows n0 + n of x.  Rolled: the code is run once a row
+// block, and fetching it unrolled takes as long as running it.
+constexpr int kW4SumRow = 36;  // (a fragment's 8 rows by 4 column pairs fall into 32 banks)
+__device__ __forceinline__ void w4_results(const W4View& w, const W4Epi& epi, int m0, const float* sums, int n0,
+                                           int count) {
+  const int lane = threadIdx.x & 31, m = m0 + lane;
+  const bool live = m < w.M;
+  constexpr int U = 4;
+#pragma unroll 1
+  for (int c = 0; c < count; c += U) {
+    float v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      v[u] = epi.add && live && c + u < count ? epi.add[(long long)(n0 + c + u) * w.M + m] : 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v[u] = fmaf(sums[(c + u) * kW4SumRow + lane], kW4Unit, v[u]);
+      const long long n = n0 + c + u;
+      if (epi.swiglu) {  // (row m + 1 is the next lane's)
+        const float up = __shfl_down_sync(0xffffffffu, v[u], 1);
+        if (live && !(m & 1) && c + u < count)
+          reinterpret_cast<bf16*>(epi.out)[n * (w.M / 2) + m / 2] =
+              from_f<bf16>(__fdividef(v[u], 1.f + __expf(-v[u])) * up);
+      } else if (live && c + u < count) {
+        reinterpret_cast<float*>(epi.out)[n * w.M + m] = v[u];
+      }
+    }
   }
 }
 

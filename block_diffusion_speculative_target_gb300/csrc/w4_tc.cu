@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bars[L::kBars];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_s;
+  __shared__ float sums_s[4][16 * kW4SumRow];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* code_full = bars;              // [CS] a block has landed
   uint64_t* code_empty = bars + CS;        // [CS] its four expanding and its four adding warps are done with it
@@ -347,8 +348,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!tile_end && i + 1 < b1) continue;
       // The row block ends here, or the run does.  A warp deals with its 32 rows by itself.
       if (w4_join<V>(w, run, tile, r, acc)) {
+        // (16 columns at a time through shared memory)
+        float* sums = sums_s[warp - 4];
 #pragma unroll
-        for (int n = 0; n < N; ++n) w4_write<1>(w, epi, tile * kW4Tile + r, n, rows, acc[n / 4][n % 4]);
+        for (int c = 0; c < N; c += 16) {
+          if (c >= rows) break;
+#pragma unroll
+          for (int n = 0; n < 16; ++n) sums[n * kW4SumRow + lane] = acc[(c + n) / 4][n % 4];
+          __syncwarp();
+          w4_results(w, epi, tile * kW4Tile + r - lane, sums, c, min(16, rows - c));
+          __syncwarp();
+        }
       }
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -431,7 +441,7 @@ cudaError_t tc_launch(const W4View& w, const bf16* x, long long ldx, int rows, c
   static PerDevice attr;
   // (the widest block: groups of 32, float32 scales and zero points)
   constexpr int kMost = 1024 + L::kCodeSlots * (kW4Codes + 4 * kW4Tile * 5) + L::kXSlots * L::kX;
-  static_assert(kMost <= 232448 - 2048, "shared memory per block");
+  static_assert(kMost <= 232448 - 12288, "shared memory per block");
   static_assert(L::kCodeSlots % 2 == 0, "two groups take every other block");
   DFL_RET(attr.once([] {
     return cudaFuncSetAttribute(w4_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
