@@ -498,6 +498,9 @@ static cudaError_t merge_launch(const PagedGeom& g, void* out, cudaStream_t s) {
 cudaError_t paged_merge_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t s) {
   return hd == 64 ? merge_launch<bf16, 64, kPagedTcKeys>(g, out, s) : merge_launch<bf16, 128, kPagedTcKeys>(g, out, s);
 }
+cudaError_t paged_merge_q8(int hd, const PagedGeom& g, void* out, cudaStream_t s) {
+  return hd == 64 ? merge_launch<bf16, 64, kPagedQ8Keys>(g, out, s) : merge_launch<bf16, 128, kPagedQ8Keys>(g, out, s);
+}
 
 static int groups_of(int rows, int of) { return (rows + of - 1) / of; }
 
@@ -572,10 +575,4 @@ cudaError_t paged_attention_core(int hd, const PagedGeom& g, const void* q, cons
   return hd == 64 ? core_pick<float, float, 64>(g, q, kp, vp, out, part_rows, s)
                   : core_pick<float, float, 128>(g, q, kp, vp, out, part_rows, s);
 }
-cudaError_t paged_attention_q8(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
-                               long long part_rows, cudaStream_t s) {
-  return hd == 64 ? core_pick<bf16, uint8_t, 64>(g, q, kp, vp, out, part_rows, s)
-                  : core_pick<bf16, uint8_t, 128>(g, q, kp, vp, out, part_rows, s);
-}
-
 }  // namespace dfl

@@ -559,6 +559,7 @@ struct PagedRule {
 };
 PagedRule paged_rule_core(const PagedGeom& g);
 PagedRule paged_rule_tc(const PagedGeom& g);
+PagedRule paged_rule_q8(const PagedGeom& g);
 // Whether the line of such a call fits the plan's integers, whatever lengths its tables hold.
 bool paged_line_fits(const PagedGeom& g, const PagedRule& r);
 // Fills in the split of a call: row groups, the grid, runs of `min_tiles` tiles at least, the partial slots.
@@ -566,8 +567,11 @@ bool paged_line_fits(const PagedGeom& g, const PagedRule& r);
 long long paged_split(PagedGeom& g, const PagedRule& r, int grid, int min_tiles);
 // Keys of a tile of the tensor-core kernel.
 constexpr int kPagedTcKeys = 128;
-// Merge of the tensor-core kernel's partials.
+// Keys of a tile of the kernel over 8-bit pages.
+constexpr int kPagedQ8Keys = 64;
+// Merge of the tensor-core kernels' partials.
 cudaError_t paged_merge_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t s);
+cudaError_t paged_merge_q8(int hd, const PagedGeom& g, void* out, cudaStream_t s);
 cudaError_t paged_join_bf16(int hd, const PagedGeom& g, void* out, cudaStream_t s);
 // Attention of a call described by `g` (geometry, table, lengths; the split is filled in here): float32 on
 // the CUDA cores, bf16 on the tensor cores.

@@ -295,9 +295,10 @@ static int attend(dflash_pages* p, int32_t layer, const void* q, int32_t batch, 
   g.records = ws->records;
   g.status = ws->status;
   g.wait_ns = (unsigned)std::min(wait_limit_ns(), 4000000000ull);
-  const bool tc = p->dtype == DFLASH_BF16 && !p->ks;
-  if (!paged_line_fits(g, tc ? paged_rule_tc(g) : paged_rule_core(g))) return DFLASH_ERR_TOO_LARGE;
-  if (p->ks && p->dtype == DFLASH_BF16)
+  const bool tc = p->dtype == DFLASH_BF16 && !p->ks, q8 = p->dtype == DFLASH_BF16 && p->ks;
+  if (!paged_line_fits(g, tc ? paged_rule_tc(g) : q8 ? paged_rule_q8(g) : paged_rule_core(g)))
+    return DFLASH_ERR_TOO_LARGE;
+  if (q8)
     CK(paged_attention_q8(p->hd, g, q, p->k, p->v, out, ws->part_rows, (cudaStream_t)stream));
   else if (tc)
     CK(paged_attention_tc(p->hd, g, p->tk, p->tv, pool_rows(p), q, out, ws->part_rows, (cudaStream_t)stream));

@@ -1,0 +1,607 @@
+// Attention over 8-bit pages (bf16 queries) on tensor cores fed from registers.
+//
+//   z_j = scale ks_j sum_d q_d (u_jd - 128),  o = sum_j 2^(z_j - m) vs_j (v_jd - 128) / sum_j 2^(z_j - m)   (log2 units)
+//
+// Codes less 128 are exact in half precision: the bytes 0x64 and u are the half
+// 1024 + u, and 1152 taken off it leaves u - 128, so two codes take one byte
+// permutation and one packed subtraction.  The queries are half too, each row
+// scaled by a power of two to a largest entry of 2^7..2^8 (exact but for entries
+// 2^25 below it).  The scales stay in float32: ks multiplies the scores, vs the
+// weights.  A weight enters the product with the values as half(2^(z - m) vs f),
+// f a factor of the row that keeps the largest one near 2^8 and all below 2^15:
+// off by 2^-11 of itself, whatever size the scales have.  m and f move only when a
+// weight outgrows that range (or a score m by 64), which a vote finds; the sum of
+// weights is taken in float32 before vs and f.
+//
+// A step is 16 keys, always inside one page.  The products run over dimensions
+// and keys in the order that suits the loads: a lane takes 16 consecutive bytes of
+// a key row, swizzled against bank conflicts, and the queries, scores and outputs
+// follow that order; nothing is shuffled between the two products.
+//
+// Four warps a CTA in RW groups of rows by 4 / RW groups of keys; a warp holds 16 MT
+// rows.  Groups of keys take the steps of a run in turn, each with its own ring of
+// stages (16-byte asynchronous copies) and its own running sums, so single tokens
+// run without a barrier; the groups' sums are joined at a piece's end.  The split
+// of a call over CTAs is that of paged.cuh, in tiles of 64 keys.
+//
+// Few rows are bound by the keys' bytes: 16 instructions a key and 16 rows, 9 of them
+// the codes' way to halves.  More rows share those in pairs of row tiles (MT = 2).
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "paged.cuh"
+
+namespace dfl {
+
+namespace {
+constexpr int kQ8Threads = 128;
+constexpr int kQ8Keys = kPagedQ8Keys;
+constexpr int kStep = 16;     // keys of a step
+
+template <int HD, int MT, int RW>
+struct Q8Layout {
+  static constexpr int KW = 4 / RW;                       // groups of keys
+  static constexpr int kRows = 16 * MT * RW;
+  static constexpr int kStages = RW == 1 ? 4 : RW == 2 ? 6 : 8;
+  static constexpr int kStage = 2 * kStep * HD + 2 * kStep * 4;  // codes of keys and values, their scales
+  static constexpr int kRing = KW * kStages * kStage;
+  static constexpr int kQRow = HD * 2 + 16;               // padded: 8 rows of 16 bytes fall into 32 banks
+  static constexpr int kPer = (HD / 2 + 4) * 32;          // floats of a warp's sums of a row tile
+  static constexpr int kJoin = (KW - 1) * RW * MT * kPer * 4;  // those of the groups, over the ring
+  static constexpr int kRingEnd = kRing > kJoin ? kRing : kJoin;
+  static constexpr int kQ = kRingEnd;
+  static constexpr int kRf = kQ + kRows * kQRow;
+  static constexpr int kRed = kRf + kRows * 4;
+  static constexpr int kSmem = kRed + (2 * kQ8Threads / 32 + 8) * 4;
+  static constexpr int kCtas = MT == 1 ? 3 : 2;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two codes (bytes 0 and 1, or 2 and 3 of w) less 128 as halves.
+template <int HI>
+__device__ __forceinline__ uint32_t two_codes(uint32_t w) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(__byte_perm(w, 0x64646464u, HI ? 0x4342 : 0x4140)), "r"(0x64806480u));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+// The key (of 8) that is column n of a score tile.
+template <int HD>
+__host__ __device__ __forceinline__ constexpr int key_of(int n) {
+  return HD == 128 ? (n & 1) << 2 | n >> 1 : n;
+}
+// Byte offset of 16-byte chunk c of key row r: rows of 128 (64) bytes, chunks swizzled.
+template <int HD>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+  return HD == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+}  // namespace
+
+template <int HD, int MT, int RW>
+__global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
+    paged_attn_q8_kernel(const __grid_constant__ PagedGeom g, const bf16* __restrict__ q,
+                         const uint8_t* __restrict__ kp, const uint8_t* __restrict__ vp, bf16* __restrict__ out,
+                         float scale_log2) {
+  typedef Q8Layout<HD, MT, RW> L;
+  constexpr int KW = L::KW, S = L::kStages, NT = HD / 8, KS = HD / 16;  // output tiles, steps of 16 dimensions
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
+  const int rw = warp % RW, kg = warp / RW;
+  float* rfs = reinterpret_cast<float*>(smem + L::kRf);
+  uint8_t* ring = smem + kg * S * L::kStage;
+  const uint32_t ring_u = smem_u32(ring);
+  auto group_sync = [&] {
+    if (RW == 1)
+      __syncwarp();
+    else if (RW == 4)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * RW) : "memory");
+  };
+  pdl_launch();
+  pdl_wait();
+  const PlanView pv = plan_view<kQ8Keys, kQ8Threads>(g, reinterpret_cast<int*>(smem + L::kRed));
+  SegmentWalk<kQ8Keys> walk(g, pv);
+  walk.start();
+  Segment sg;
+  while (walk.next(sg)) {
+    // ------------------------------------------------------------ queries: half, each row by a power of two
+    __syncthreads();
+    constexpr int kLanes = HD / 16;  // a lane takes 16 entries of a row
+    for (int r = tid / kLanes; r < L::kRows; r += kQ8Threads / kLanes) {
+      const ItemRow row = item_row(g, sg.prefix, sg.b, sg.hk, sg.rt * (sg.prefix ? g.rp : g.ri), r);
+      const int c = tid % kLanes;
+      float x[16];
+      uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      if (row.live) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(q + (((long long)row.b * g.n + row.i) * g.nq + row.head) * HD + 16 * c);
+        raw[0] = src[0];
+        raw[1] = src[1];
+      }
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
+      float most = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 f = __bfloat1622float2(h[e]);
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+        most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      // 2^up brings the largest entry to 2^7..2^8 (a row of zeros, or one that holds Inf: as it is)
+      const int ex = (int)(__float_as_uint(most) >> 23);  // biased; 0: subnormal or zero
+      const int up = ex > 0 && ex < 255 ? 134 - ex : ex == 0 && most > 0.f ? 133 : 0;
+      // (up to 2^133: in two factors)
+      const float u1 = exp2f((float)(up / 2)), u2 = exp2f((float)(up - up / 2));
+      uint8_t* dst = smem + L::kQ + r * L::kQRow + ((c >> 2) * 64 + (c & 3) * 2) * 2;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        *reinterpret_cast<uint32_t*>(dst + s * 32) = half2_of(x[4 * s] * u1 * u2, x[4 * s + 1] * u1 * u2);
+        *reinterpret_cast<uint32_t*>(dst + s * 32 + 16) = half2_of(x[4 * s + 2] * u1 * u2, x[4 * s + 3] * u1 * u2);
+      }
+      if (c == 0) rfs[r] = (float)-up;
+    }
+    __syncthreads();
+    // ------------------------------------------------------------ this warp's rows
+    const uint32_t q_at = smem_u32(smem + L::kQ) +
+                          (uint32_t)((rw * 16 * MT + (lane & 7) + 8 * ((lane >> 3) & 1)) * L::kQRow + 16 * (lane >> 4));
+    uint32_t qf[MT == 1 ? KS : 1][4];
+    if (MT == 1) {
+#pragma unroll
+      for (int s = 0; s < (MT == 1 ? KS : 1); ++s) ldsm4(qf[s], q_at + s * 32);
+    }
+    const int key_lo = sg.prefix ? 0 : pv.sh_tiles * kQ8Keys;
+    const int key_end = sg.prefix ? pv.sh_tiles * kQ8Keys : key_limit(g, sg.b);
+    int sink[MT][2], lo[MT][2], hi[MT][2], all_lo = key_lo, all_hi = key_end;
+    float rf[MT][2], m[MT][2], l[MT][2], lf[MT][2], f[MT][2];
+    float o[MT][NT][4];
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = (rw * MT + a) * 16 + gr + 8 * y;
+        const ItemRow row = item_row(g, sg.prefix, sg.b, sg.hk, sg.rt * (sg.prefix ? g.rp : g.ri), r);
+        sink[a][y] = lo[a][y] = 0;
+        hi[a][y] = INT32_MAX;
+        if (row.live) {
+          row_span(g, paged_len(g, row.b), paged_rows(g, row.b), row.i, sink[a][y], lo[a][y], hi[a][y]);
+          all_lo = max(all_lo, lo[a][y]);
+          all_hi = min(all_hi, hi[a][y]);
+        }
+        // 2^-up as a factor of the scores: kept below float32's range, the rest goes with the keys' scales
+        rf[a][y] = rfs[r];
+        m[a][y] = -INFINITY;
+        l[a][y] = lf[a][y] = 0.f;
+        f[a][y] = 1.f;
+      }
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) rf[a][y] = exp2f(rf[a][y]);
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[a][i][e] = 0.f;
+    // some row of the item sees the keys below seen_sink and those from seen_lo on: its first row's
+    int seen_sink, seen_lo, seen_hi;
+    row_span(g, sg.prefix ? pv.min_len : paged_len(g, sg.b), paged_rows(g, sg.b),
+             sg.prefix ? 0 : div_g(g, sg.rt * g.ri), seen_sink, seen_lo, seen_hi);
+    // ------------------------------------------------------------ the ring
+    const int steps = sg.nt * (kQ8Keys / kStep) / KW;  // of this group: kg, kg + KW, ..
+    auto first_key = [&](int j) {
+      const int s = j * KW + kg;
+      return sg.span.tile(sg.t0 + s / (kQ8Keys / kStep)) * kQ8Keys + s % (kQ8Keys / kStep) * kStep;
+    };
+    const int32_t* trow = g.table + (long long)sg.b * g.table_stride;
+    int pages = -1;        // lane x: the page of step x of the 32 at hand (-1: none, or no row sees a key of it)
+    uint32_t there = 0u;   // bit j % 32: step j has been asked for
+    auto ask = [&](int j) {
+      if (j < steps) {
+        if ((j & 31) == 0) {
+          const int k0 = j + lane < steps ? first_key(j + lane) : INT32_MAX;
+          pages = -1;
+          if (k0 < key_end && (k0 < seen_sink || k0 + kStep > seen_lo)) {
+            pages = trow[k0 >> g.ps_log2];
+            if ((unsigned)pages >= (unsigned)g.n_pages) {
+              pages = -1;
+              set_status(g.status, DFLASH_STATUS_BOUNDS);
+            }
+          }
+        }
+        const int page = __shfl_sync(0xffffffffu, pages, j & 31);
+        there = (there & ~(1u << (j & 31))) | (uint32_t)(page >= 0) << (j & 31);
+        if (page >= 0) {
+          const long long row = g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps + (first_key(j) & (g.ps - 1));
+          const uint32_t at = ring_u + (uint32_t)(j % S) * L::kStage;
+          constexpr int kChunks = HD / 16;
+          const int l0 = rw * 32 + lane;
+#pragma unroll
+          for (int x = 0; x < (kStep * kChunks + 32 * RW - 1) / (32 * RW); ++x) {
+            const int i = l0 + x * 32 * RW, r = i / kChunks, c = i % kChunks;
+            if (kStep * kChunks % (32 * RW) != 0 && i >= kStep * kChunks) break;
+            cp16(at + chunk_at<HD>(r, c), kp + row * HD + i * 16);
+            cp16(at + kStep * HD + chunk_at<HD>(r, c), vp + row * HD + i * 16);
+          }
+          if (l0 < 8) cp16(at + 2 * kStep * HD + l0 * 16, (l0 < 4 ? g.ks : g.vs) + row + 4 * (l0 & 3));
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll 1
+    for (int j = 0; j < S - 1; ++j) ask(j);
+#pragma unroll 1
+    for (int j = 0; j < steps; ++j) {
+      cp_wait<S - 2>();
+      group_sync();
+      ask(j + S - 1);
+      if (!(there >> (j & 31) & 1u)) continue;
+      const uint8_t* kb = ring + (j % S) * L::kStage;
+      const uint8_t* vb = kb + kStep * HD;
+      const float* sc = reinterpret_cast<const float*>(vb + kStep * HD);
+      const int k0 = first_key(j);
+      // ---------------------------------------------------------- scores
+      float c[MT][2][4];
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[a][n][e] = 0.f;
+      uint4 kc[2][HD / 64];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int h = 0; h < HD / 64; ++h)
+          kc[n][h] = *reinterpret_cast<const uint4*>(kb + chunk_at<HD>(8 * n + key_of<HD>(gr), t + 4 * h));
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint32_t b[2][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint4 v = kc[n][s >> 2];
+          const uint32_t word = (s & 3) == 0 ? v.x : (s & 3) == 1 ? v.y : (s & 3) == 2 ? v.z : v.w;
+          b[n][0] = two_codes<0>(word);
+          b[n][1] = two_codes<1>(word);
+        }
+#pragma unroll
+        for (int a = 0; a < MT; ++a) {
+          if (MT == 1) {
+            mma_f16(c[a][0], qf[MT == 1 ? s : 0], b[0][0], b[0][1]);
+            mma_f16(c[a][1], qf[MT == 1 ? s : 0], b[1][0], b[1][1]);
+          } else {
+            uint32_t x[4];
+            ldsm4(x, q_at + a * 16 * L::kQRow + s * 32);
+            mma_f16(c[a][0], x, b[0][0], b[0][1]);
+            mma_f16(c[a][1], x, b[1][0], b[1][1]);
+          }
+        }
+      }
+      // ---------------------------------------------------------- weights
+      // this lane's keys: columns 2 t, 2 t + 1 of both score tiles
+      const int kx[4] = {key_of<HD>(2 * t), key_of<HD>(2 * t + 1), 8 + key_of<HD>(2 * t), 8 + key_of<HD>(2 * t + 1)};
+      float ks[4], vs[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        ks[x] = sc[kx[x]] * scale_log2;
+        vs[x] = sc[kStep + kx[x]];
+      }
+      const bool part = k0 < all_lo || k0 + kStep > all_hi;
+      uint32_t p[MT][4];
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float z[4], w[4], vv[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            z[x] = c[a][x >> 1][2 * y + (x & 1)] * ks[x];
+            vv[x] = vs[x];
+          }
+          if (part) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = k0 + kx[x];
+              const bool see = key >= key_lo && key < key_end &&
+                               (key < sink[a][y] || (key >= lo[a][y] && key < hi[a][y]));
+              z[x] = see ? z[x] : -INFINITY;
+              vv[x] = see ? vv[x] : 0.f;
+            }
+          }
+          float e[4], sum = 0.f, emax = -INFINITY, wmax = 0.f;
+          auto weigh = [&] {
+            const float off = m[a][y] == -INFINITY ? 0.f : -m[a][y] * rf[a][y];
+            sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              e[x] = fmaf(z[x], rf[a][y], off);
+              const float pr = ex2f(e[x]);
+              sum += pr;
+              w[x] = pr * (f[a][y] * vv[x]);
+            }
+          };
+          weigh();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            emax = fmaxf(emax, e[x]);
+            wmax = fmaxf(wmax, w[x]);
+          }
+          // (without a reference every score that is seen makes one)
+          if (__any_sync(0xffffffffu, emax > (m[a][y] == -INFINITY ? -INFINITY : 64.f) || wmax > 32768.f)) {
+            float zm = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+            zm = quad_max(zm);
+            const float mn = fmaxf(m[a][y], zm);
+            if (__any_sync(0xffffffffu, mn > -INFINITY)) {
+              const bool has = mn > -INFINITY;
+              const float ref = has ? mn : 0.f, r = rf[a][y];
+              float tm = 0.f;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) tm = fmaxf(tm, ex2f((z[x] - ref) * r) * vv[x]);
+              tm = quad_max(tm);
+              const bool first = m[a][y] == -INFINITY;
+              const float dm = first ? 0.f : (mn - m[a][y]) * r;  // (in log2 units)
+              const float want = tm > 0.f ? 8.f - log2f(tm) : 0.f;
+              // weights that this step brings within 2^8; those before it keep their place unless they have to move
+              float keep = first ? want : lf[a][y] + dm;
+              const float to = fminf(fmaxf(!first && tm > 0.f && exp2f(fminf(keep, 126.f)) * tm > 32768.f ? want : keep,
+                                           -120.f), 120.f);
+              const float os = first ? 0.f : exp2f(to - keep);
+              l[a][y] *= first ? 0.f : ex2f(-dm);
+              if (has) {
+                m[a][y] = mn;
+                lf[a][y] = to;
+                f[a][y] = exp2f(to);
+              }
+#pragma unroll
+              for (int i = 0; i < NT; ++i) {
+                o[a][i][2 * y] *= first ? 1.f : os;
+                o[a][i][2 * y + 1] *= first ? 1.f : os;
+              }
+              weigh();
+            }
+          }
+          l[a][y] += sum;
+          p[a][y] = half2_of(w[0], w[1]);
+          p[a][2 + y] = half2_of(w[2], w[3]);
+        }
+      // ---------------------------------------------------------- values
+      if constexpr (HD == 128) {
+        uint4 vc[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          vc[x] = *reinterpret_cast<const uint4*>(vb + chunk_at<HD>(kx[x], (gr & 1) << 2 | gr >> 1));
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {  // 4 dimensions
+          uint32_t word[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) word[x] = d == 0 ? vc[x].x : d == 1 ? vc[x].y : d == 2 ? vc[x].z : vc[x].w;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t ab = __byte_perm(word[0], word[1], h ? 0x7362 : 0x5140);
+            const uint32_t cd = __byte_perm(word[2], word[3], h ? 0x7362 : 0x5140);
+            const uint32_t b0 = two_codes<0>(ab), b1 = two_codes<0>(cd), b2 = two_codes<1>(ab), b3 = two_codes<1>(cd);
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+              mma_f16(o[a][4 * d + 2 * h], p[a], b0, b1);
+              mma_f16(o[a][4 * d + 2 * h + 1], p[a], b2, b3);
+            }
+          }
+        }
+      } else {
+        uint2 vc[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          vc[x] = *reinterpret_cast<const uint2*>(vb + chunk_at<HD>(kx[x], gr >> 1) + (gr & 1) * 8);
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          uint32_t word[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) word[x] = d ? vc[x].y : vc[x].x;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t ab = __byte_perm(word[0], word[1], h ? 0x7362 : 0x5140);
+            const uint32_t cd = __byte_perm(word[2], word[3], h ? 0x7362 : 0x5140);
+            const uint32_t b0 = two_codes<0>(ab), b1 = two_codes<0>(cd), b2 = two_codes<1>(ab), b3 = two_codes<1>(cd);
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+              mma_f16(o[a][4 * d + 2 * h], p[a], b0, b1);
+              mma_f16(o[a][4 * d + 2 * h + 1], p[a], b2, b3);
+            }
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+    // ------------------------------------------------------------ the rows' sums: (m, l, o) with o as m has it
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        l[a][y] = quad_sum(l[a][y]);
+        m[a][y] = m[a][y] == -INFINITY ? -INFINITY : m[a][y] * rf[a][y];
+        const float back = exp2f(-lf[a][y]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          o[a][i][2 * y] *= back;
+          o[a][i][2 * y + 1] *= back;
+        }
+      }
+    if constexpr (KW > 1) {
+      __syncthreads();  // (the rings are free)
+      float* join = reinterpret_cast<float*>(smem);
+      constexpr int kPer = L::kPer;
+      if (kg > 0) {
+#pragma unroll
+        for (int a = 0; a < MT; ++a) {
+          float* dst = join + (((kg - 1) * RW + rw) * MT + a) * kPer + lane;
+#pragma unroll
+          for (int i = 0; i < NT * 4; ++i) dst[i * 32] = o[a][i >> 2][i & 3];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            dst[(NT * 4 + y) * 32] = m[a][y];
+            dst[(NT * 4 + 2 + y) * 32] = l[a][y];
+          }
+        }
+      }
+      __syncthreads();
+      if (kg == 0) {
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll 1
+          for (int k = 0; k < KW - 1; ++k) {
+            const float* src = join + ((k * RW + rw) * MT + a) * kPer + lane;
+            float x0[2], x1[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float m1 = src[(NT * 4 + y) * 32], l1 = src[(NT * 4 + 2 + y) * 32];
+              const float mn = fmaxf(m[a][y], m1);
+              x0[y] = m[a][y] == -INFINITY ? 0.f : ex2f(m[a][y] - mn);
+              x1[y] = m1 == -INFINITY ? 0.f : ex2f(m1 - mn);
+              l[a][y] = l[a][y] * x0[y] + l1 * x1[y];
+              m[a][y] = mn;
+            }
+#pragma unroll
+            for (int i = 0; i < NT * 4; ++i) {
+              const int y = (i & 3) >> 1;
+              o[a][i >> 2][i & 3] = o[a][i >> 2][i & 3] * x0[y] + src[i * 32] * x1[y];
+            }
+          }
+      }
+    }
+    const bool whole = walk.whole(sg);
+    if (kg == 0) {
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int r = (rw * MT + a) * 16 + gr + 8 * y;
+          const ItemRow row = item_row(g, sg.prefix, sg.b, sg.hk, sg.rt * (sg.prefix ? g.rp : g.ri), r);
+          if (!row.live) continue;
+          // dimension 16 t + i of output tile i in column 2 t, and column 2 t + 1: 64 further (HD = 64: 8 further)
+          constexpr int kFar = HD == 128 ? 64 : 8;
+          if (whole) {
+            const float inv = 1.f / l[a][y];
+            bf16* dst = out + (((long long)row.b * g.n + row.i) * g.nq + row.head) * HD + 16 * t;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int i = 0; i < NT; i += 8) {
+                uint4 v;
+                __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  h[x] = __floats2bfloat162_rn(o[a][i + 2 * x][2 * y + e] * inv, o[a][i + 2 * x + 1][2 * y + e] * inv);
+                *reinterpret_cast<uint4*>(dst + e * kFar + i) = v;
+              }
+          } else {
+            float* dst = g.part_o + (sg.slot_row + r) * HD + 16 * t;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int i = 0; i < NT; i += 4)
+                *reinterpret_cast<float4*>(dst + e * kFar + i) = make_float4(
+                    o[a][i][2 * y + e], o[a][i + 1][2 * y + e], o[a][i + 2][2 * y + e], o[a][i + 3][2 * y + e]);
+            if (t == 0) g.part_ml[sg.slot_row + r] = make_float2(m[a][y], l[a][y]);
+          }
+        }
+    }
+    if (!whole && pv.pre_tiles == 0) {
+      int c0;
+      const int nc = walk.pieces(sg, c0);
+      int* done = reinterpret_cast<int*>(smem + L::kRed);
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        *done = atomicAdd(g.tickets + sg.ordinal, 1) == nc - 1;
+      }
+      __syncthreads();
+      if (*done) {
+        __threadfence();
+        if (tid == 0) g.tickets[sg.ordinal] = 0;
+        merge_item<bf16, HD>(g, sg.b, sg.rt, sg.hk, 0, min(g.ri, paged_rows(g, sg.b) * g.G - sg.rt * g.ri), nc, c0, warp,
+                             kQ8Threads / 32, out);
+      }
+    }
+  }
+}
+
+// Stacked rows of an item: the smallest layout that holds them.
+static int q8_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+PagedRule paged_rule_q8(const PagedGeom& g) {
+  const int rows = q8_rows((g.shared ? g.batch : 1) * g.n * g.G);
+  return PagedRule{rows, rows, kQ8Keys, 1, 2};
+}
+
+template <int HD, int MT, int RW>
+static cudaError_t q8_launch(PagedGeom g, const void* q, const void* kp, const void* vp, void* out, long long part_rows,
+                             cudaStream_t s) {
+  typedef Q8Layout<HD, MT, RW> L;
+  static_assert(L::kSmem * L::kCtas <= 232448, "shared memory per multiprocessor");
+  static PerDevice smem;
+  DFL_RET(smem.once([] {
+    return cudaFuncSetAttribute(paged_attn_q8_kernel<HD, MT, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  }));
+  if (paged_split(g, paged_rule_q8(g), num_sms() * L::kCtas, 2) > part_rows || g.ri != L::kRows)
+    return cudaErrorInvalidValue;
+  const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
+  DFL_RET(launch_pdl(paged_attn_q8_kernel<HD, MT, RW>, dim3(g.grid), dim3(kQ8Threads), L::kSmem, s, g, (const bf16*)q,
+                     (const uint8_t*)kp, (const uint8_t*)vp, (bf16*)out, scale_log2));
+  count_launch();
+  return g.shared ? paged_merge_q8(HD, g, out, s) : cudaSuccess;  // (else the CTAs join their pieces)
+}
+
+template <int HD>
+static cudaError_t q8_pick(const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
+                           long long part_rows, cudaStream_t s) {
+  switch (q8_rows((g.shared ? g.batch : 1) * g.n * g.G)) {
+    case 16: return q8_launch<HD, 1, 1>(g, q, kp, vp, out, part_rows, s);
+    case 32: return q8_launch<HD, 2, 1>(g, q, kp, vp, out, part_rows, s);
+    case 64: return q8_launch<HD, 2, 2>(g, q, kp, vp, out, part_rows, s);
+    default: return q8_launch<HD, 2, 4>(g, q, kp, vp, out, part_rows, s);
+  }
+}
+
+cudaError_t paged_attention_q8(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
+                               long long part_rows, cudaStream_t s) {
+  return hd == 64 ? q8_pick<64>(g, q, kp, vp, out, part_rows, s) : q8_pick<128>(g, q, kp, vp, out, part_rows, s);
+}
+
+}  // namespace dfl
