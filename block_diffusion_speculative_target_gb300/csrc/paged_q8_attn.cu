@@ -29,6 +29,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -54,7 +55,8 @@ struct Q8Layout {
   static constexpr int kRingEnd = kRing > kJoin ? kRing : kJoin;
   static constexpr int kQ = kRingEnd;
   static constexpr int kRf = kQ + kRows * kQRow;
-  static constexpr int kRed = kRf + kRows * 4;
+  static constexpr int kSpan = kRf + kRows * 4;           // [rows] sink, lo, hi
+  static constexpr int kRed = kSpan + kRows * 16;
   static constexpr int kSmem = kRed + (2 * kQ8Threads / 32 + 8) * 4;
   static constexpr int kCtas = MT == 1 ? 3 : 2;
 };
@@ -78,6 +80,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c = a b
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, "
+      "%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Two codes (bytes 0 and 1, or 2 and 3 of w) less 128 as halves.
 template <int HI>
@@ -174,47 +184,37 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
         *reinterpret_cast<uint32_t*>(dst + s * 32) = half2_of(x[4 * s] * u1 * u2, x[4 * s + 1] * u1 * u2);
         *reinterpret_cast<uint32_t*>(dst + s * 32 + 16) = half2_of(x[4 * s + 2] * u1 * u2, x[4 * s + 3] * u1 * u2);
       }
-      if (c == 0) rfs[r] = (float)-up;
+      if (c == 0) {
+        int4 v = make_int4(0, 0, INT32_MAX, 0);
+        if (row.live) row_span(g, paged_len(g, row.b), paged_rows(g, row.b), row.i, v.x, v.y, v.z);
+        reinterpret_cast<int4*>(smem + L::kSpan)[r] = v;
+        rfs[r] = exp2f((float)-up);
+      }
     }
     __syncthreads();
     // ------------------------------------------------------------ this warp's rows
     const uint32_t q_at = smem_u32(smem + L::kQ) +
                           (uint32_t)((rw * 16 * MT + (lane & 7) + 8 * ((lane >> 3) & 1)) * L::kQRow + 16 * (lane >> 4));
-    uint32_t qf[MT == 1 ? KS : 1][4];
-    if (MT == 1) {
-#pragma unroll
-      for (int s = 0; s < (MT == 1 ? KS : 1); ++s) ldsm4(qf[s], q_at + s * 32);
-    }
     const int key_lo = sg.prefix ? 0 : pv.sh_tiles * kQ8Keys;
     const int key_end = sg.prefix ? pv.sh_tiles * kQ8Keys : key_limit(g, sg.b);
-    int sink[MT][2], lo[MT][2], hi[MT][2], all_lo = key_lo, all_hi = key_end;
-    float rf[MT][2], m[MT][2], l[MT][2], lf[MT][2], f[MT][2];
+    const int4* spans = reinterpret_cast<const int4*>(smem + L::kSpan) + rw * 16 * MT + gr;
+    int all_lo = key_lo, all_hi = key_end;  // keys that every row of the warp sees
+    float rf[MT][2], m[MT][2], l[MT][2], f[MT][2];
     float o[MT][NT][4];
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int r = (rw * MT + a) * 16 + gr + 8 * y;
-        const ItemRow row = item_row(g, sg.prefix, sg.b, sg.hk, sg.rt * (sg.prefix ? g.rp : g.ri), r);
-        sink[a][y] = lo[a][y] = 0;
-        hi[a][y] = INT32_MAX;
-        if (row.live) {
-          row_span(g, paged_len(g, row.b), paged_rows(g, row.b), row.i, sink[a][y], lo[a][y], hi[a][y]);
-          all_lo = max(all_lo, lo[a][y]);
-          all_hi = min(all_hi, hi[a][y]);
-        }
-        // 2^-up as a factor of the scores: kept below float32's range, the rest goes with the keys' scales
-        rf[a][y] = rfs[r];
+        const int4 v = spans[a * 16 + 8 * y];
+        all_lo = max(all_lo, v.y);
+        all_hi = min(all_hi, v.z);
+        rf[a][y] = rfs[(rw * MT + a) * 16 + gr + 8 * y];
         m[a][y] = -INFINITY;
-        l[a][y] = lf[a][y] = 0.f;
+        l[a][y] = 0.f;
         f[a][y] = 1.f;
       }
     all_lo = __reduce_max_sync(0xffffffffu, all_lo);
     all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-#pragma unroll
-    for (int a = 0; a < MT; ++a)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) rf[a][y] = exp2f(rf[a][y]);
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
@@ -234,6 +234,9 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
     const int32_t* trow = g.table + (long long)sg.b * g.table_stride;
     int pages = -1;        // lane x: the page of step x of the 32 at hand (-1: none, or no row sees a key of it)
     uint32_t there = 0u;   // bit j % 32: step j has been asked for
+    const int l0 = rw * 32 + lane;
+    const uint32_t put0 = chunk_at<HD>(l0 / (HD / 16), l0 % (HD / 16));
+    uint32_t ask_slot = 0, slot = 0;
     auto ask = [&](int j) {
       if (j < steps) {
         if ((j & 31) == 0) {
@@ -250,20 +253,23 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
         const int page = __shfl_sync(0xffffffffu, pages, j & 31);
         there = (there & ~(1u << (j & 31))) | (uint32_t)(page >= 0) << (j & 31);
         if (page >= 0) {
-          const long long row = g.page_row0 + ((long long)page * g.nkv + sg.hk) * g.ps + (first_key(j) & (g.ps - 1));
-          const uint32_t at = ring_u + (uint32_t)(j % S) * L::kStage;
-          constexpr int kChunks = HD / 16;
-          const int l0 = rw * 32 + lane;
+          // (pool rows are below 2^31)
+          const int row = (int)g.page_row0 + (page * g.nkv + sg.hk) * g.ps + (first_key(j) & (g.ps - 1));
+          const uint32_t at = ring_u + ask_slot * L::kStage;
+          const long long src = (long long)row * HD + l0 * 16;
+          constexpr int kLoads = kStep * HD / 16 / (32 * RW);  // (0: half of the threads have one)
 #pragma unroll
-          for (int x = 0; x < (kStep * kChunks + 32 * RW - 1) / (32 * RW); ++x) {
-            const int i = l0 + x * 32 * RW, r = i / kChunks, c = i % kChunks;
-            if (kStep * kChunks % (32 * RW) != 0 && i >= kStep * kChunks) break;
-            cp16(at + chunk_at<HD>(r, c), kp + row * HD + i * 16);
-            cp16(at + kStep * HD + chunk_at<HD>(r, c), vp + row * HD + i * 16);
+          for (int x = 0; x < (kLoads > 0 ? kLoads : 1); ++x) {
+            if (kLoads == 0 && l0 >= kStep * HD / 16) break;
+            // row l0 / (HD / 16) + x 512 RW / HD: the swizzle changes with x only where 4 rows a load are 128 bytes each
+            const uint32_t to = at + (HD == 128 && RW == 1 && (x & 1) ? put0 ^ 64u : put0) + x * 512 * RW;
+            cp16(to, kp + src + x * 512 * RW);
+            cp16(to + kStep * HD, vp + src + x * 512 * RW);
           }
           if (l0 < 8) cp16(at + 2 * kStep * HD + l0 * 16, (l0 < 4 ? g.ks : g.vs) + row + 4 * (l0 & 3));
         }
       }
+      if (++ask_slot == S) ask_slot = 0;
       cp_commit();
     };
 #pragma unroll 1
@@ -273,19 +279,14 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
       cp_wait<S - 2>();
       group_sync();
       ask(j + S - 1);
+      const uint8_t* kb = ring + slot * L::kStage;
+      if (++slot == S) slot = 0;
       if (!(there >> (j & 31) & 1u)) continue;
-      const uint8_t* kb = ring + (j % S) * L::kStage;
       const uint8_t* vb = kb + kStep * HD;
       const float* sc = reinterpret_cast<const float*>(vb + kStep * HD);
       const int k0 = first_key(j);
       // ---------------------------------------------------------- scores
       float c[MT][2][4];
-#pragma unroll
-      for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) c[a][n][e] = 0.f;
       uint4 kc[2][HD / 64];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
@@ -304,15 +305,14 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
         }
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
-          if (MT == 1) {
-            mma_f16(c[a][0], qf[MT == 1 ? s : 0], b[0][0], b[0][1]);
-            mma_f16(c[a][1], qf[MT == 1 ? s : 0], b[1][0], b[1][1]);
-          } else {
-            uint32_t x[4];
-            ldsm4(x, q_at + a * 16 * L::kQRow + s * 32);
-            mma_f16(c[a][0], x, b[0][0], b[0][1]);
-            mma_f16(c[a][1], x, b[1][0], b[1][1]);
-          }
+          uint32_t x[4];
+          ldsm4(x, q_at + a * 16 * L::kQRow + s * 32);
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            if (s == 0)
+              mma_f16_first(c[a][n], x, b[n][0], b[n][1]);
+            else
+              mma_f16(c[a][n], x, b[n][0], b[n][1]);
         }
       }
       // ---------------------------------------------------------- weights
@@ -326,82 +326,102 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
       }
       const bool part = k0 < all_lo || k0 + kStep > all_hi;
       uint32_t p[MT][4];
+      auto weights = [&](auto masked) {
+        constexpr bool kMasked = decltype(masked)::value;
+        uint32_t hidden = 0u;  // bit 8 a + 4 y + x
 #pragma unroll
-      for (int a = 0; a < MT; ++a)
+        for (int a = 0; a < MT; ++a)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float z[4], w[4], vv[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            z[x] = c[a][x >> 1][2 * y + (x & 1)] * ks[x];
-            vv[x] = vs[x];
-          }
-          if (part) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
+          for (int i = 0; i < 8; ++i) {
+            const int y = i >> 2, x = i & 3;
+            const int4 see = kMasked ? spans[a * 16 + 8 * y] : make_int4(0, 0, 0, 0);
+            float& z = c[a][x >> 1][2 * y + (x & 1)];
+            z *= ks[x];
+            if (kMasked) {
               const int key = k0 + kx[x];
-              const bool see = key >= key_lo && key < key_end &&
-                               (key < sink[a][y] || (key >= lo[a][y] && key < hi[a][y]));
-              z[x] = see ? z[x] : -INFINITY;
-              vv[x] = see ? vv[x] : 0.f;
+              if (!(key >= key_lo && key < key_end && (key < see.x || (key >= see.y && key < see.z)))) {
+                z = -INFINITY;
+                hidden |= 1u << (8 * a + i);
+              }
             }
           }
-          float e[4], sum = 0.f, emax = -INFINITY, wmax = 0.f;
-          auto weigh = [&] {
-            const float off = m[a][y] == -INFINITY ? 0.f : -m[a][y] * rf[a][y];
-            sum = 0.f;
+        float sum[MT][2];
+        // Weights as the rows' references and factors have them; true if some row's have to move.  (Without a
+        // reference every score that is seen makes one.)
+        auto weigh = [&] {
+          bool move = false;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              e[x] = fmaf(z[x], rf[a][y], off);
-              const float pr = ex2f(e[x]);
-              sum += pr;
-              w[x] = pr * (f[a][y] * vv[x]);
+          for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const bool none = m[a][y] == -INFINITY;
+              const float off = none ? 0.f : -m[a][y] * rf[a][y];
+              float w[4], e[4];
+              sum[a][y] = 0.f;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                e[x] = fmaf(c[a][x >> 1][2 * y + (x & 1)], rf[a][y], off);
+                const float pr = ex2f(e[x]);
+                sum[a][y] += pr;
+                const bool hide = kMasked && (hidden >> (8 * a + 4 * y + x) & 1u);
+                w[x] = pr * (hide ? 0.f : f[a][y] * vs[x]);
+              }
+              move |= fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > (none ? -INFINITY : 64.f);
+              move |= fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])) > 32768.f;
+              p[a][y] = half2_of(w[0], w[1]);
+              p[a][2 + y] = half2_of(w[2], w[3]);
             }
-          };
-          weigh();
+          return move;
+        };
+        if (__any_sync(0xffffffffu, weigh())) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            emax = fmaxf(emax, e[x]);
-            wmax = fmaxf(wmax, w[x]);
-          }
-          // (without a reference every score that is seen makes one)
-          if (__any_sync(0xffffffffu, emax > (m[a][y] == -INFINITY ? -INFINITY : 64.f) || wmax > 32768.f)) {
-            float zm = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-            zm = quad_max(zm);
-            const float mn = fmaxf(m[a][y], zm);
-            if (__any_sync(0xffffffffu, mn > -INFINITY)) {
-              const bool has = mn > -INFINITY;
-              const float ref = has ? mn : 0.f, r = rf[a][y];
+          for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float z[4], zm = -INFINITY;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                z[x] = c[a][x >> 1][2 * y + (x & 1)];
+                zm = fmaxf(zm, z[x]);
+              }
+              const float mn = fmaxf(m[a][y], quad_max(zm)), r = rf[a][y];
+              const bool has = mn > -INFINITY, first = m[a][y] == -INFINITY;
               float tm = 0.f;
 #pragma unroll
-              for (int x = 0; x < 4; ++x) tm = fmaxf(tm, ex2f((z[x] - ref) * r) * vv[x]);
+              for (int x = 0; x < 4; ++x)
+                tm = fmaxf(tm, kMasked && (hidden >> (8 * a + 4 * y + x) & 1u)
+                                   ? 0.f
+                                   : ex2f((z[x] - (has ? mn : 0.f)) * r) * vs[x]);
               tm = quad_max(tm);
-              const bool first = m[a][y] == -INFINITY;
-              const float dm = first ? 0.f : (mn - m[a][y]) * r;  // (in log2 units)
+              const float dm = first || !has ? 0.f : (mn - m[a][y]) * r;  // (in log2 units)
               const float want = tm > 0.f ? 8.f - log2f(tm) : 0.f;
-              // weights that this step brings within 2^8; those before it keep their place unless they have to move
-              float keep = first ? want : lf[a][y] + dm;
-              const float to = fminf(fmaxf(!first && tm > 0.f && exp2f(fminf(keep, 126.f)) * tm > 32768.f ? want : keep,
-                                           -120.f), 120.f);
-              const float os = first ? 0.f : exp2f(to - keep);
-              l[a][y] *= first ? 0.f : ex2f(-dm);
+              // this step's weights are brought within 2^8; those before it keep their factor unless it has to fall
+              const float keep = first ? want : log2f(f[a][y]) + dm;
+              const bool fall = !first && tm > 0.f && exp2f(fminf(keep, 126.f)) * tm > 32768.f;
+              const float to = fminf(fmaxf(fall ? want : keep, -120.f), 120.f);
+              const float os = first ? 1.f : exp2f(to - keep);
               if (has) {
+                l[a][y] *= ex2f(-dm);
                 m[a][y] = mn;
-                lf[a][y] = to;
                 f[a][y] = exp2f(to);
-              }
 #pragma unroll
-              for (int i = 0; i < NT; ++i) {
-                o[a][i][2 * y] *= first ? 1.f : os;
-                o[a][i][2 * y + 1] *= first ? 1.f : os;
+                for (int i = 0; i < NT; ++i) {
+                  o[a][i][2 * y] *= os;
+                  o[a][i][2 * y + 1] *= os;
+                }
               }
-              weigh();
             }
-          }
-          l[a][y] += sum;
-          p[a][y] = half2_of(w[0], w[1]);
-          p[a][2 + y] = half2_of(w[2], w[3]);
+          weigh();
         }
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) l[a][y] += sum[a][y];
+      };
+      if (part)
+        weights(std::true_type());
+      else
+        weights(std::false_type());
       // ---------------------------------------------------------- values
       if constexpr (HD == 128) {
         uint4 vc[4];
@@ -457,7 +477,7 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
       for (int y = 0; y < 2; ++y) {
         l[a][y] = quad_sum(l[a][y]);
         m[a][y] = m[a][y] == -INFINITY ? -INFINITY : m[a][y] * rf[a][y];
-        const float back = exp2f(-lf[a][y]);
+        const float back = 1.f / f[a][y];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           o[a][i][2 * y] *= back;
