@@ -560,6 +560,7 @@ struct PagedRule {
 PagedRule paged_rule_core(const PagedGeom& g);
 PagedRule paged_rule_tc(const PagedGeom& g);
 PagedRule paged_rule_q8(const PagedGeom& g);
+PagedRule paged_rule_q8_tc();
 // Whether the line of such a call fits the plan's integers, whatever lengths its tables hold.
 bool paged_line_fits(const PagedGeom& g, const PagedRule& r);
 // Fills in the split of a call: row groups, the grid, runs of `min_tiles` tiles at least, the partial slots.
@@ -580,6 +581,9 @@ cudaError_t paged_attention_core(int hd, const PagedGeom& g, const void* q, cons
 // bf16 queries over 8-bit pages.
 cudaError_t paged_attention_q8(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
                                long long part_rows, cudaStream_t s);
+// The same, many rows.
+cudaError_t paged_attention_q8_tc(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
+                                  long long part_rows, cudaStream_t s);
 // Append into 8-bit pages: codes and a scale a row.
 cudaError_t paged_append_q8(int in_dtype, int dtype, const void* qkv, long long ld, int batch, int n, int nq, int nkv,
                             int hd, const int32_t* n_rows, const int32_t* table, int table_stride, const int32_t* len,

@@ -583,11 +583,13 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
   }
 }
 
-// Stacked rows of an item: the smallest layout that holds them.
-static int q8_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Stacked rows that one sequence's queries, or the batch's behind a shared prefix, make.
+static int q8_stack(const PagedGeom& g) { return (g.shared ? g.batch : 1) * g.n * g.G; }
+constexpr int kFewRows = 32;
 PagedRule paged_rule_q8(const PagedGeom& g) {
-  const int rows = q8_rows((g.shared ? g.batch : 1) * g.n * g.G);
-  return PagedRule{rows, rows, kQ8Keys, 1, 2};
+  const int rows = q8_stack(g);
+  if (rows > kFewRows) return paged_rule_q8_tc();
+  return PagedRule{rows <= 16 ? 16 : 32, rows <= 16 ? 16 : 32, kQ8Keys, 1, 2};
 }
 
 template <int HD, int MT, int RW>
@@ -611,16 +613,14 @@ static cudaError_t q8_launch(PagedGeom g, const void* q, const void* kp, const v
 template <int HD>
 static cudaError_t q8_pick(const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
                            long long part_rows, cudaStream_t s) {
-  switch (q8_rows((g.shared ? g.batch : 1) * g.n * g.G)) {
-    case 16: return q8_launch<HD, 1, 1>(g, q, kp, vp, out, part_rows, s);
-    case 32: return q8_launch<HD, 2, 1>(g, q, kp, vp, out, part_rows, s);
-    case 64: return q8_launch<HD, 2, 2>(g, q, kp, vp, out, part_rows, s);
-    default: return q8_launch<HD, 2, 4>(g, q, kp, vp, out, part_rows, s);
-  }
+  const int rows = q8_stack(g);
+  return rows <= 16 ? q8_launch<HD, 1, 1>(g, q, kp, vp, out, part_rows, s)
+                    : q8_launch<HD, 2, 1>(g, q, kp, vp, out, part_rows, s);
 }
 
 cudaError_t paged_attention_q8(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
                                long long part_rows, cudaStream_t s) {
+  if (q8_stack(g) > kFewRows) return paged_attention_q8_tc(hd, g, q, kp, vp, out, part_rows, s);
   return hd == 64 ? q8_pick<64>(g, q, kp, vp, out, part_rows, s) : q8_pick<128>(g, q, kp, vp, out, part_rows, s);
 }
 
