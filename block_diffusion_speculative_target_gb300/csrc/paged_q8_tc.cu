@@ -9,7 +9,7 @@
 // as half(2^(z - m) vs f), f a factor of the row that keeps the largest below 2^15.
 //
 // An item is up to 128 stacked rows, one to a thread.  A tile of 64 keys goes
-//   pages -> registers (a key row by two threads, one tile ahead; its page two ahead)
+//   pages -> registers (one tile ahead; the pages' numbers two ahead)
 //         -> halves in shared memory, two buffers, K and V rows alike, swizzled
 //   S = Q K^T   128 rows by 64 keys in TMEM: a thread reads its row
 //   O += P V    P as halves in TMEM, O in TMEM
@@ -50,13 +50,6 @@ struct Q8TcLayout {
   static constexpr int kSmem = kUsed + 1024;
 };
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
-  return d;
-}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
   asm("mul.rn.f32x2 %0, %1, %2;"
@@ -113,7 +106,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                             const uint8_t* __restrict__ kp, const uint8_t* __restrict__ vp, bf16* __restrict__ out,
                             float scale_log2) {
   typedef Q8TcLayout<HD> L;
-  constexpr int KU = HD / 32;  // 16-byte pieces of half a key row
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_done, pv_done;
   __shared__ uint32_t tmem_slot;
@@ -210,49 +202,59 @@ __global__ void __launch_bounds__(kThreads, 2)
     int seen_sink, seen_lo, seen_hi;
     row_span(g, sg.prefix ? pv.min_len : paged_len(g, sg.b), paged_rows(g, sg.b),
              sg.prefix ? 0 : div_g(g, sg.rt * g.ri), seen_sink, seen_lo, seen_hi);
-    // ------------------------------------------------------------ keys and values: half a key row a thread
-    const int kr = tid & 63, part = tid >> 6;
+    // ------------------------------------------------------------ keys and values
+    // A thread takes 16 bytes of every kStep-th key row: whole rows by neighbours.  Every 16 keys lie in one page.
+    constexpr int kLanes = HD / 16, kStep = kThreads / kLanes, KU = kKeys / kStep;
+    const int kr = tid / kLanes, kc16 = tid % kLanes;
     const int32_t* trow = g.table + (long long)sg.b * g.table_stride;
-    auto page_of = [&](int i) {  // of this thread's key of tile i (-1: none, or no row sees it)
+    // The page of the 16 keys 16 (lane % 4) .. of tile i (-1: no row sees one of them): asked for a tile before it is
+    // looked at.
+    auto key_of = [&](int i) { return sg.span.tile(sg.t0 + i) * kKeys + 16 * (lane & 3); };
+    auto page_of = [&](int i) {
       if (i >= sg.nt) return -1;
-      const int key = sg.span.tile(sg.t0 + i) * kKeys + kr;
-      if (key >= key_end || (key >= seen_sink && key < seen_lo)) return -1;
-      return trow[key >> g.ps_log2];
+      const int key = key_of(i);
+      return key >= key_end || (key >= seen_sink && key + 16 <= seen_lo) ? -1 : trow[key >> g.ps_log2];
     };
     uint4 kc[KU], vc[KU];
     float sc = 0.f;
     auto fetch = [&](int i, int page) {
-#pragma unroll
-      for (int u = 0; u < KU; ++u) kc[u] = vc[u] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-      sc = 0.f;
-      if (page == -1) return;
-      if ((unsigned)page >= (unsigned)g.n_pages) {
+      if (i >= sg.nt) return;
+      int first = -1;  // the pool row of the 16 keys (below 2^31)
+      if ((unsigned)page < (unsigned)g.n_pages)
+        first = (int)g.page_row0 + (page * g.nkv + sg.hk) * g.ps + (key_of(i) & (g.ps - 1));
+      else if (page != -1)
         set_status(g.status, DFLASH_STATUS_BOUNDS);
-        return;
-      }
-      const int key = sg.span.tile(sg.t0 + i) * kKeys + kr;
-      const int row = (int)g.page_row0 + (page * g.nkv + sg.hk) * g.ps + (key & (g.ps - 1));
-      const long long at = (long long)row * HD + part * (HD / 2);
-#pragma unroll
-      for (int u = 0; u < KU; ++u) kc[u] = __ldg(reinterpret_cast<const uint4*>(kp + at) + u);
-#pragma unroll
-      for (int u = 0; u < KU; ++u) vc[u] = __ldg(reinterpret_cast<const uint4*>(vp + at) + u);
-      sc = part ? g.vs[row] : g.ks[row] * scale_log2;
-    };
-    auto expand = [&](int buf) {
-      uint8_t* base = sm + (HD == 128 ? part * (kKeys * 128) : 0) + buf * L::kTile + kr * 128;
 #pragma unroll
       for (int u = 0; u < KU; ++u) {
-        uint4 h[2];
-        const int c = (HD == 128 ? 0 : 4 * part) + 2 * u;
-        halves_of(kc[u], h);
-        *reinterpret_cast<uint4*>(base + L::kK + ((c ^ (kr & 7)) << 4)) = h[0];
-        *reinterpret_cast<uint4*>(base + L::kK + (((c + 1) ^ (kr & 7)) << 4)) = h[1];
-        halves_of(vc[u], h);
-        *reinterpret_cast<uint4*>(base + L::kV + ((c ^ (kr & 7)) << 4)) = h[0];
-        *reinterpret_cast<uint4*>(base + L::kV + (((c + 1) ^ (kr & 7)) << 4)) = h[1];
+        const int key = kr + kStep * u, row0 = __shfl_sync(0xffffffffu, first, key >> 4);
+        kc[u] = vc[u] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        if (row0 >= 0) {
+          const long long at = (long long)(row0 + (key & 15)) * HD + 16 * kc16;
+          kc[u] = __ldg(reinterpret_cast<const uint4*>(kp + at));
+          vc[u] = __ldg(reinterpret_cast<const uint4*>(vp + at));
+        }
       }
-      scales[(2 * buf + part) * kKeys + kr] = sc;
+      const int key = tid & 63, row0 = __shfl_sync(0xffffffffu, first, key >> 4);
+      sc = row0 < 0 ? 0.f : (tid < 64 ? g.ks : g.vs)[row0 + (key & 15)];
+    };
+    auto expand = [&](int buf) {
+      // 16 codes are two chunks of 16 bytes; lanes of the upper half of a row write theirs the other way round, so
+      // that the 8 lanes of a row fill all banks
+      const int c = 2 * (kc16 & 3), far = kc16 >> 2;
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        const int key = kr + kStep * u;
+        uint8_t* base = sm + far * (kKeys * 128) + buf * L::kTile + key * 128;
+        const int p0 = ((c + far) ^ (key & 7)) << 4, p1 = ((c + 1 - far) ^ (key & 7)) << 4;
+        uint4 h[2];
+        halves_of(kc[u], h);
+        *reinterpret_cast<uint4*>(base + L::kK + p0) = far ? h[1] : h[0];
+        *reinterpret_cast<uint4*>(base + L::kK + p1) = far ? h[0] : h[1];
+        halves_of(vc[u], h);
+        *reinterpret_cast<uint4*>(base + L::kV + p0) = far ? h[1] : h[0];
+        *reinterpret_cast<uint4*>(base + L::kV + p1) = far ? h[0] : h[1];
+      }
+      scales[2 * buf * kKeys + tid] = tid < 64 ? sc * scale_log2 : sc;
     };
     auto scores = [&](int buf) {  // one thread
       const uint64_t dq = smem_desc_sw128(sm + L::kQ), dk = smem_desc_sw128(sm + L::kK + buf * L::kTile);
@@ -301,39 +303,40 @@ __global__ void __launch_bounds__(kThreads, 2)
         // the largest scale of the tile's values (of hidden slots too: it only says when to look closer)
         const float va = fabsf(vs[lane]), vb = fabsf(vs[lane + 32]);
         const float vmax = __uint_as_float(__reduce_max_sync(
-            0xffffffffu, max(va == va ? __float_as_uint(va) : 0u, vb == vb ? __float_as_uint(vb) : 0u)));
-        // what this row sees
-        uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-        const bool whole_tile = k0 >= all_lo && k0 + kKeys <= all_hi;  // (the same for the warp)
-        if (!whole_tile) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int b = k0 + 32 * h;
-            see[h] = (bits_of(lo - b, hi - b) | bits_of(-b, sink - b)) & bits_of(key_lo - b, key_end - b);
-          }
-        }
+            0xffffffffu, max(va < INFINITY ? __float_as_uint(va) : 0u, vb < INFINITY ? __float_as_uint(vb) : 0u)));
+        const bool whole_tile = k0 >= all_lo && k0 + kKeys <= all_hi;  // every row sees every key
+        // a hidden value's scale that is not finite would reach this row through its weight of 0
+        const bool bad = !whole_tile && __any_sync(0xffffffffu, !(va < INFINITY && vb < INFINITY));
         tmem_ld_wait();
         float2* z = reinterpret_cast<float2*>(s);
         const float2 rf2 = make_float2(rf, rf);
         const float4* ks4 = reinterpret_cast<const float4*>(ks);
         const float4* vs4 = reinterpret_cast<const float4*>(vs);
         // scores in log2 units
-        float zmax = -INFINITY;
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const float4 k4 = ks4[x];
           z[2 * x] = mul2(z[2 * x], mul2(make_float2(k4.x, k4.y), rf2));
           z[2 * x + 1] = mul2(z[2 * x + 1], mul2(make_float2(k4.z, k4.w), rf2));
-          if (!whole_tile) {
-            const uint32_t b = see[x >> 3] >> (4 * (x & 7));
-            z[2 * x].x = b & 1u ? z[2 * x].x : -INFINITY;
-            z[2 * x].y = b & 2u ? z[2 * x].y : -INFINITY;
-            z[2 * x + 1].x = b & 4u ? z[2 * x + 1].x : -INFINITY;
-            z[2 * x + 1].y = b & 8u ? z[2 * x + 1].y : -INFINITY;
-          }
-          zmax = max3(zmax, z[2 * x].x, z[2 * x].y);
-          zmax = max3(zmax, z[2 * x + 1].x, z[2 * x + 1].y);
         }
+        uint32_t see[2] = {0xffffffffu, 0xffffffffu};  // the tile's keys that this row sees
+        if (!whole_tile) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int b = k0 + 32 * h;
+            see[h] = (bits_of(lo - b, hi - b) | bits_of(-b, sink - b)) & bits_of(key_lo - b, key_end - b);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float2& y = z[16 * h + x];
+              y.x = see[h] >> (2 * x) & 1u ? y.x : -INFINITY;
+              y.y = see[h] >> (2 * x + 1) & 1u ? y.y : -INFINITY;
+            }
+          }
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < 32; ++x) top[x & 3] = max3(top[x & 3], z[x].x, z[x].y);
+        const float zmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         const bool none = m == -INFINITY;
         const bool move = none ? zmax > -INFINITY : zmax - m > 64.f || ex2f(zmax - m) * (f * vmax) > 32768.f;
         if (__any_sync(0xffffffffu, move)) {
@@ -342,13 +345,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float ref = has ? mn : 0.f;
           float tm = 0.f;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
+          for (int x = 0; x < 16; ++x) {  // (a hidden key: 0, or a NaN that the maximum passes over)
             const float4 v4 = vs4[x];
-            const uint32_t b = whole_tile ? 15u : see[x >> 3] >> (4 * (x & 7));
-            tm = fmaxf(tm, b & 1u ? ex2f(z[2 * x].x - ref) * fabsf(v4.x) : 0.f);
-            tm = fmaxf(tm, b & 2u ? ex2f(z[2 * x].y - ref) * fabsf(v4.y) : 0.f);
-            tm = fmaxf(tm, b & 4u ? ex2f(z[2 * x + 1].x - ref) * fabsf(v4.z) : 0.f);
-            tm = fmaxf(tm, b & 8u ? ex2f(z[2 * x + 1].y - ref) * fabsf(v4.w) : 0.f);
+            tm = max3(tm, ex2f(z[2 * x].x - ref) * fabsf(v4.x), ex2f(z[2 * x].y - ref) * fabsf(v4.y));
+            tm = max3(tm, ex2f(z[2 * x + 1].x - ref) * fabsf(v4.z), ex2f(z[2 * x + 1].y - ref) * fabsf(v4.w));
           }
           const float dm = none || !has ? 0.f : mn - m;
           const float want = tm > 0.f ? 8.f - log2f(tm) : 0.f;
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         const float off = m == -INFINITY ? 0.f : -m;
-        const float2 one = make_float2(1.f, 1.f), off2 = make_float2(off, off), f2 = make_float2(f, f);
+        const float2 off2 = make_float2(off, off), f2 = make_float2(f, f);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -386,15 +386,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int y = 0; y < 8; ++y) {
             const int x = 8 * h + y;
             const float4 v4 = vs4[x];
-            float2 va2 = mul2(make_float2(v4.x, v4.y), f2), vb2 = mul2(make_float2(v4.z, v4.w), f2);
-            if (!whole_tile) {
-              const uint32_t b = see[h] >> (4 * y);
-              va2.x = b & 1u ? va2.x : 0.f;
-              va2.y = b & 2u ? va2.y : 0.f;
-              vb2.x = b & 4u ? vb2.x : 0.f;
-              vb2.y = b & 8u ? vb2.y : 0.f;
-            }
-            float2 a = fma2(z[2 * x], one, off2), b = fma2(z[2 * x + 1], one, off2);
+            const float2 va2 = mul2(make_float2(v4.x, v4.y), f2), vb2 = mul2(make_float2(v4.z, v4.w), f2);
+            float2 a = add2(z[2 * x], off2), b = add2(z[2 * x + 1], off2);
             a = make_float2(ex2f(a.x), ex2f(a.y));
             b = make_float2(ex2f(b.x), ex2f(b.y));
             sum = add2(sum, add2(a, b));
@@ -402,6 +395,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             b = mul2(b, vb2);
             p[2 * y] = half2_of(a.x, a.y);
             p[2 * y + 1] = half2_of(b.x, b.y);
+          }
+          if (bad) {
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              p[y] &= (see[h] >> (2 * y) & 1u ? 0xffffu : 0u) | (see[h] >> (2 * y + 1) & 1u ? 0xffff0000u : 0u);
           }
           tmem_st16(tP + 16 * h + lanes, p);
         }
@@ -422,7 +420,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int k = 0; k < kKeys / 16; ++k)
             tc_mma_f16_tmem_a(tO, tP + 8 * k, smem_desc_mn(vt + k * 2048, kKeys * 128), idO, (i | k) != 0);
           tc_commit(&pv_done);
-          if (i + 1 < sg.nt) scores((i + 1) & 1);
+        }
+        __syncwarp();
+      } else if (warp == 1 && i + 1 < sg.nt) {  // (by another warp: a product takes 30 to 60 cycles to ask for)
+        if (elect_one()) {
+          tc_fence_after();
+          scores((i + 1) & 1);
         }
         __syncwarp();
       }
