@@ -217,25 +217,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     uint4 kc[KU], vc[KU];
     float sc = 0.f;
+    // (Keys that no row sees, and those of a bad page: some row of the pool; what they hold is masked, or the sequence's
+    // result unspecified.)
     auto fetch = [&](int i, int page) {
       if (i >= sg.nt) return;
-      int first = -1;  // the pool row of the 16 keys (below 2^31)
+      int first = 0;  // the pool row of the 16 keys (below 2^31)
       if ((unsigned)page < (unsigned)g.n_pages)
         first = (int)g.page_row0 + (page * g.nkv + sg.hk) * g.ps + (key_of(i) & (g.ps - 1));
       else if (page != -1)
         set_status(g.status, DFLASH_STATUS_BOUNDS);
 #pragma unroll
       for (int u = 0; u < KU; ++u) {
-        const int key = kr + kStep * u, row0 = __shfl_sync(0xffffffffu, first, key >> 4);
-        kc[u] = vc[u] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-        if (row0 >= 0) {
-          const long long at = (long long)(row0 + (key & 15)) * HD + 16 * kc16;
-          kc[u] = __ldg(reinterpret_cast<const uint4*>(kp + at));
-          vc[u] = __ldg(reinterpret_cast<const uint4*>(vp + at));
-        }
+        const int key = kr + kStep * u;
+        const long long at = (long long)(__shfl_sync(0xffffffffu, first, key >> 4) + (key & 15)) * HD + 16 * kc16;
+        kc[u] = __ldg(reinterpret_cast<const uint4*>(kp + at));
+        vc[u] = __ldg(reinterpret_cast<const uint4*>(vp + at));
       }
-      const int key = tid & 63, row0 = __shfl_sync(0xffffffffu, first, key >> 4);
-      sc = row0 < 0 ? 0.f : (tid < 64 ? g.ks : g.vs)[row0 + (key & 15)];
+      const int key = tid & 63;
+      sc = __ldg((tid < 64 ? g.ks : g.vs) + __shfl_sync(0xffffffffu, first, key >> 4) + (key & 15));
     };
     auto expand = [&](int buf) {
       // 16 codes are two chunks of 16 bytes; lanes of the upper half of a row write theirs the other way round, so
