@@ -84,9 +84,11 @@ struct W4Run {
 // `per_sm`: runs an SM at most, up to 4.
 W4Run w4_run(const W4View& w, const W4Scratch& sc, int per_sm);
 int w4_max_runs();
-// bf16 x on the tensor cores, up to 32 rows: fed from registers; more: from TMEM and shared memory.
+// bf16 x on the tensor cores, up to 16 rows: fed from registers; more: from TMEM and shared memory.
 cudaError_t w4_linear_mma(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi,
                           const W4Scratch& sc, cudaStream_t s);
+// (A 2-D map over bf16 rows [rows][cols], ld elements apart: boxes of 64 columns, 128 bytes swizzled, by box_rows.)
+bool make_rows_map(const void* x, int rows, int cols, long long ld, int box_rows, CUtensorMap* out);
 cudaError_t w4_linear_tc(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi, const W4Scratch& sc,
                          cudaStream_t s);
 

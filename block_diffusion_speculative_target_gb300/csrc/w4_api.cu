@@ -183,7 +183,7 @@ int dflash_linear_w4(int32_t dtype, const void* x, int64_t ldx, const dflash_w4*
   int device = -1;
   REQ(cudaGetDevice(&device) == cudaSuccess && device == ws->device);
   const W4Epi epi = {add, swiglu != 0, y};
-  if (dtype == DFLASH_BF16 && rows <= 32)
+  if (dtype == DFLASH_BF16 && rows <= 16)
     CK(w4_linear_mma(v, x, ldx, rows, epi, ws->sc, (cudaStream_t)stream));
   else if (dtype == DFLASH_BF16)
     CK(w4_linear_tc(v, x, ldx, rows, epi, ws->sc, (cudaStream_t)stream));

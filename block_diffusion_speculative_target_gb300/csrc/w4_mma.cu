@@ -247,17 +247,17 @@ __global__ void __launch_bounds__(kThreads, 4)
       continue;
     }
     // The row block ends here, or the run does.  A warp deals with its 32 rows by itself.
-    if (w4_join<V>(w, run, tile, tid, acc)) {
+    w4_join<V, V>(w, run, tile, tid, acc, [&](int, const float (&sum)[V][4]) {
       float* sums = reinterpret_cast<float*>(smem + S * stage_bytes) + warp * (L::kRows * kW4SumRow);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          sums[(8 * (v % NT) + 2 * t + (e & 1)) * kW4SumRow + 16 * (v / NT) + g + 8 * (e >> 1)] = acc[v][e];
+          sums[(8 * (v % NT) + 2 * t + (e & 1)) * kW4SumRow + 16 * (v / NT) + g + 8 * (e >> 1)] = sum[v][e];
       __syncwarp();
       w4_results(w, epi, tile * kW4Tile + 32 * warp, sums, 0, rows);
       __syncwarp();
-    }
+    });
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -296,9 +296,7 @@ cudaError_t mma_group(const W4View& w, const bf16* x, long long ldx, int rows, c
 cudaError_t w4_linear_mma(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi,
                           const W4Scratch& sc, cudaStream_t s) {
   const bf16* b = (const bf16*)x;
-  if (rows <= 8) return mma_group<1>(w, b, ldx, rows, epi, sc, s);
-  if (rows <= 16) return mma_group<2>(w, b, ldx, rows, epi, sc, s);
-  return mma_group<4>(w, b, ldx, rows, epi, sc, s);
+  return rows <= 8 ? mma_group<1>(w, b, ldx, rows, epi, sc, s) : mma_group<2>(w, b, ldx, rows, epi, sc, s);
 }
 
 }  // namespace dfl

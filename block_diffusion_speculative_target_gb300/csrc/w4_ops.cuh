@@ -50,12 +50,24 @@ __device__ __forceinline__ uint32_t offset_of(int zero) {
 }
 
 // One warp's share of the row block `tile`, whose last column that this run holds has been added: V float4 of sums a
-// thread.  Where other runs hold some of its columns, the sums are left for whoever comes last; true if that is this
-// warp (then `acc` is the whole sum, the pieces added in order of the columns), or if there are no others.
-template <int V>
-__device__ __forceinline__ bool w4_join(const W4View& w, const W4Run& run, int tile, int tid, float (&acc)[V][4]) {
+// thread.  Where other runs hold some of its columns, the sums are left for whoever comes last, who adds the pieces in
+// order of the columns.  That warp, or the only one, has `emit(v0, sums)` called with kV float4 of whole sums at a time.
+template <int V, int kV, typename F>
+__device__ __forceinline__ void w4_join(const W4View& w, const W4Run& run, int tile, int tid, const float (&acc)[V][4],
+                                        F emit) {
   const int t0 = tile * w.kt, first = t0 / run.per, last = (t0 + w.kt - 1) / run.per;
-  if (first == last) return true;
+  if (first == last) {
+#pragma unroll
+    for (int v0 = 0; v0 < V; v0 += kV) {
+      float sum[kV][4];
+#pragma unroll
+      for (int v = 0; v < kV; ++v)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[v][e] = acc[v0 + v][e];
+      emit(v0, sum);
+    }
+    return;
+  }
   // run r's piece of the row block: its first slot if the run begins in the block, else its second
   auto piece = [&](int r) {
     return reinterpret_cast<float4*>(run.part) + ((long long)r * 2 + (r * run.per < t0)) * (V * kW4Tile) + tid;
@@ -71,16 +83,17 @@ __device__ __forceinline__ bool w4_join(const W4View& w, const W4Run& run, int t
     ends = atomicAdd(ticket, 1) == last - first;
     if (ends) *ticket = 0;
   }
-  if (!__shfl_sync(0xffffffffu, ends, 0)) return false;
+  if (!__shfl_sync(0xffffffffu, ends, 0)) return;
   __threadfence();
-  constexpr int kV = V < 4 ? V : 4, kAhead = 4;  // loads in flight: kAhead pieces
-#pragma unroll
+  constexpr int kAhead = V <= 4 ? 4 : 6;  // pieces in flight
+#pragma unroll 1
   for (int v0 = 0; v0 < V; v0 += kV) {
     float sum[kV][4];
 #pragma unroll
     for (int v = 0; v < kV; ++v)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[v][e] = 0.f;
+#pragma unroll 1
     for (int r = first; r <= last; r += kAhead) {
       float4 p[kAhead][kV];
 #pragma unroll
@@ -101,12 +114,8 @@ __device__ __forceinline__ bool w4_join(const W4View& w, const W4Run& run, int t
           }
         }
     }
-#pragma unroll
-    for (int v = 0; v < kV; ++v)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[v0 + v][e] = sum[v][e];
+    emit(v0, sum);
   }
-  return true;
 }
 
 // A warp's results: the whole sums of row `lane` of its 32 rows (of the matrix's from m0 on) and row n of x at

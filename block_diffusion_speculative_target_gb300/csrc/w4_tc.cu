@@ -54,12 +54,20 @@ constexpr int kMaxD = 16;
 template <int N>
 struct TcLayout {
   static constexpr int kX = N * 256;  // two halves of 64 columns: rows of 128 bytes, 16-byte chunks swizzled by row
-  static constexpr int kXSlots = N == 64 ? 6 : 3;
-  static constexpr int kXAhead = N == 64 ? 3 : 1;  // blocks asked for past the one that is announced
+  static constexpr int kXSlots = N <= 64 ? 6 : 3;
+  static constexpr int kXAhead = N <= 64 ? 3 : 1;  // blocks asked for past the one that is announced
   static constexpr int kCodeSlots = 10;
   static constexpr int kBars = 2 * kCodeSlots + 2 * kXSlots + 2 * kABufs + 2 * kMaxD + 1;
 };
 
+// Two float32 lanes at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
 // 16 lanes of 64 columns: registers 4 s + {0, 1, 2, 3} of lane 4 g + t are, of columns 8 s .. 8 s + 7, (row g, column
 // t), (row g + 8, t), (g, 4 + t), (g + 8, 4 + t).
 __device__ __forceinline__ void tmem_st_16x128b_x16(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -85,8 +93,8 @@ struct W4Sums {
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
     w4_tc_kernel(const __grid_constant__ W4View w, const __grid_constant__ W4Run run,
-                 const __grid_constant__ W4Sums sums, const bf16* __restrict__ x, long long ldx, int vec, int rows,
-                 const __grid_constant__ W4Epi epi) {
+                 const __grid_constant__ W4Sums sums, const __grid_constant__ CUtensorMap tmx,
+                 const bf16* __restrict__ x, long long ldx, int vec, int rows, const __grid_constant__ W4Epi epi) {
   typedef TcLayout<N> L;
   constexpr int V = N / 4;  // float4 of sums a thread
   constexpr int CS = L::kCodeSlots, XS = L::kXSlots;
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&code_empty[i], 8);
     }
     for (int i = 0; i < XS; ++i) {
-      mbar_init(&x_full[i], kXWarps);
+      mbar_init(&x_full[i], vec ? 1 : kXWarps);
       mbar_init(&x_empty[i], 1);
     }
     for (int i = 0; i < kABufs; ++i) {
@@ -241,8 +249,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) tc_commit(drain);
       __syncwarp();
       mbar_wait(drain, 0, kW4DrainNs);
+    } else if (vec) {
+      // ---------------------------------------------------------- x in wide rows: two boxes of 64 columns a block
+      // (columns past K and rows past the last one arrive as zeros)
+      if (warp == 2) {
+        int kb = b0 % w.kt, slot = 0, i = b0;
+        uint32_t phase = 0;
+        if (elect_one()) tma_prefetch_desc(&tmx);
+        __syncwarp();
+        pdl_wait();
+        for (; i < b1; ++i) {
+          if (i - b0 >= XS && !wait(&x_empty[slot], phase ^ 1u)) break;
+          if (elect_one()) {
+            uint8_t* to = smem + slot * L::kX;
+            mbar_arrive_expect_tx(&x_full[slot], L::kX);
+            tma_load_2d(to, &tmx, &x_full[slot], kb * kW4Tile, 0);
+            tma_load_2d(to + L::kX / 2, &tmx, &x_full[slot], kb * kW4Tile + 64, 0);
+          }
+          __syncwarp();
+          if (++slot == XS) {
+            slot = 0;
+            phase ^= 1u;
+          }
+          if (++kb == w.kt) kb = 0;
+        }
+        if (abort_s) {
+          const int asked = i - b0;
+          for (int u = max(0, asked - XS); u < asked; ++u) mbar_wait(&x_full[u % XS], (uint32_t)(u / XS) & 1u, kW4DrainNs);
+        }
+      }
     } else {
-      // ---------------------------------------------------------- x
+      // ---------------------------------------------------------- x anywhere
       // Lane l of warp 2 + v brings chunk l % 16 (8 columns) of the rows 2 v + l / 16 + 4 u.  Rows past the last one
       // are not filled: their columns of the products are not read.
       const int xc = lane & 15, xr = 2 * (warp - 2) + (lane >> 4);
@@ -270,11 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (xr + 4 * u >= live) break;
           const uint32_t dst = at + u * 512 + 16 * ((xc & 7) ^ ((xr + 4 * u) & 7));
           const bf16* p = in_k ? src + (long long)(4 * u) * ldx : x;
-          if (vec) {
-            cp16z(smem_u32(smem) + dst, p, in_k ? 16 : 0);
-          } else {
-            *reinterpret_cast<uint4*>(smem + dst) = gather8(p, in_k);
-          }
+          *reinterpret_cast<uint4*>(smem + dst) = gather8(p, in_k);
         }
         cp_commit();
         if (i - b0 >= kAhead) {
@@ -296,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int r = tid - 128;  // this thread's row of the block
     const uint32_t lanes = (uint32_t)(32 * (warp - 4)) << 16;
-    float acc[V][4];
+    alignas(8) float acc[V][4];
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -321,7 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(src + c, d);
             tmem_ld_wait();
 #pragma unroll
-            for (int n = 0; n < 32; ++n) acc[(c + n) / 4][n % 4] = fmaf(s, __uint_as_float(d[n]), acc[(c + n) / 4][n % 4]);
+            for (int n = 0; n < 32; n += 2) {
+              float2& y = *reinterpret_cast<float2*>(&acc[(c + n) / 4][n % 4]);
+              y = fma2(make_float2(s, s), make_float2(__uint_as_float(d[n]), __uint_as_float(d[n + 1])), y);
+            }
           }
         }
         tc_fence_before();
@@ -347,19 +383,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!tile_end && i + 1 < b1) continue;
       // The row block ends here, or the run does.  A warp deals with its 32 rows by itself.
-      if (w4_join<V>(w, run, tile, r, acc)) {
-        // (16 columns at a time through shared memory)
-        float* sums = sums_s[warp - 4];
+      w4_join<V, 4>(w, run, tile, r, acc, [&](int v0, const float (&sum)[4][4]) {
+        if (4 * v0 >= rows) return;
+        float* sums = sums_s[warp - 4];  // 16 columns at a time
 #pragma unroll
-        for (int c = 0; c < N; c += 16) {
-          if (c >= rows) break;
-#pragma unroll
-          for (int n = 0; n < 16; ++n) sums[n * kW4SumRow + lane] = acc[(c + n) / 4][n % 4];
-          __syncwarp();
-          w4_results(w, epi, tile * kW4Tile + r - lane, sums, c, min(16, rows - c));
-          __syncwarp();
-        }
-      }
+        for (int n = 0; n < 16; ++n) sums[n * kW4SumRow + lane] = sum[n / 4][n % 4];
+        __syncwarp();
+        w4_results(w, epi, tile * kW4Tile + r - lane, sums, 4 * v0, min(16, rows - 4 * v0));
+        __syncwarp();
+      });
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -447,6 +479,8 @@ cudaError_t tc_launch(const W4View& w, const bf16* x, long long ldx, int rows, c
     return cudaFuncSetAttribute(w4_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   }));
   const int vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx % 8 == 0;
+  CUtensorMap tmx = {};
+  if (vec && !make_rows_map(x, rows, w.K, ldx, N, &tmx)) return cudaErrorInvalidValue;
   const W4Run run = w4_run(w, sc, 1);
   W4Sums sums;
   sums.group_shift = w.group == 32 ? 0 : w.group == 64 ? 1 : 2;
@@ -454,7 +488,8 @@ cudaError_t tc_launch(const W4View& w, const bf16* x, long long ldx, int rows, c
   while (N * w.groups() >> sums.part_shift > kDColumns / 2) ++sums.part_shift;
   sums.buffers = std::min(kDColumns / (N * w.groups() >> sums.part_shift), kMaxD);
   DFL_RET(launch_pdl(w4_tc_kernel<N>, dim3(run.runs), dim3(kThreads),
-                     1024 + L::kCodeSlots * w.block_bytes + L::kXSlots * L::kX, s, w, run, sums, x, ldx, vec, rows, epi));
+                     1024 + L::kCodeSlots * w.block_bytes + L::kXSlots * L::kX, s, w, run, sums, tmx, x, ldx, vec,
+                     rows, epi));
   count_launch();
   return cudaSuccess;
 }
@@ -462,8 +497,9 @@ cudaError_t tc_launch(const W4View& w, const bf16* x, long long ldx, int rows, c
 
 cudaError_t w4_linear_tc(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi, const W4Scratch& sc,
                          cudaStream_t s) {
-  return rows <= 64 ? tc_launch<64>(w, (const bf16*)x, ldx, rows, epi, sc, s)
-                    : tc_launch<128>(w, (const bf16*)x, ldx, rows, epi, sc, s);
+  return rows <= 32   ? tc_launch<32>(w, (const bf16*)x, ldx, rows, epi, sc, s)
+         : rows <= 64 ? tc_launch<64>(w, (const bf16*)x, ldx, rows, epi, sc, s)
+                      : tc_launch<128>(w, (const bf16*)x, ldx, rows, epi, sc, s);
 }
 
 }  // namespace dfl
