@@ -29,6 +29,12 @@ def desc_of(shape, dtype: str, n_layers=None) -> capi.ModelDesc:
                           shape.head_dim, shape.ffn, shape.vocab, shape.rope_theta, shape.eps, _DT[dtype][0])
 
 
+def _raw_stream(index):
+    """The current stream of a device as the handle that the C ABI takes (torch.cuda.current_stream() makes a Stream
+    object for it, 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 class Model:
     """Target + drafter weights on the GPU.  ``shape`` has the fields n_layers,
     hidden, n_q, n_kv, head_dim, ffn, vocab, rope_theta, eps; the drafter has
@@ -480,8 +486,7 @@ class PagedCache:
         sequence into ``k_out`` and ``v_out`` [batch][n_kv][n][head_dim], of the
         model's type or float32, both alike; either may be left out.  The first
         ``n_rows`` rows of a sequence are written."""
-        stream = torch.cuda.current_stream()
-        if stream.device_index != self.device.index:
+        if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
                 return self.read(layer, table, start, k_out, v_out, n_rows)
         batch = self._calls(table, start, n_rows)
@@ -495,7 +500,7 @@ class PagedCache:
                 raise ValueError(f"k_out and v_out are contiguous tensors [{batch}][{self.nkv}][{n}][{self.hd}] of one "
                                  f"type, float32 or {self.tdt}, on {self.device}")
         capi.dflash_paged_read(self.pages, layer, capi.F32 if odt == torch.float32 else capi.BF16, batch, n, n_rows,
-                               table, table.shape[1], start, k_out, v_out, self.ws, stream)
+                               table, table.shape[1], start, k_out, v_out, self.ws, _raw_stream(self.device.index))
 
     def attention(self, layer, q, table, lengths, out, causal=True, window=0, sinks=0, n_rows=None, shared_len=None):
         """Attention of ``q`` [batch][n][n_q][head_dim] over the pages into
@@ -566,7 +571,7 @@ class W4Linear:
             packed = torch.empty(n, dtype=torch.uint8, device=device)
         if packed.dtype != torch.uint8 or not packed.is_cuda or not packed.is_contiguous() or packed.numel() != n:
             raise ValueError(f"packed is a contiguous uint8 tensor of {n} bytes on the GPU")
-        self.packed, self.device = packed, packed.device
+        self.packed, self.device, self._index = packed, packed.device, packed.device.index
         self._c.packed = packed.data_ptr()
 
     @classmethod
@@ -613,20 +618,19 @@ class W4Linear:
         """``out`` [rows][M] float32 = x w^T (+ ``add``, which may be ``out``), or with ``swiglu`` ``out``
         [rows][M / 2] of x's type, silu(even rows) * odd rows.  ``x`` [rows][K] float32 or bfloat16, its rows may be
         apart.  Asynchronous on the current stream of the weights' device."""
-        stream = torch.cuda.current_stream()
-        if stream.device_index != self.device.index:
+        if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self.product(x, out, ws, add, swiglu)
-        xdt = x.dtype
-        if x.dim() != 2 or x.shape[1] != self.K or xdt not in (torch.bfloat16, torch.float32) or \
-                x.device != self.device or (x.stride(1) != 1 and self.K > 1):
-            raise ValueError(f"x is a float32 or bfloat16 tensor [rows][{self.K}] on {self.device}, its rows unbroken")
-        rows = x.shape[0]
+        dev, xdt, dims = self.device, x.dtype, x.shape
+        if len(dims) != 2 or dims[1] != self.K or (xdt is not torch.bfloat16 and xdt is not torch.float32) or \
+                x.device != dev or (x.stride(1) != 1 and self.K > 1):
+            raise ValueError(f"x is a float32 or bfloat16 tensor [rows][{self.K}] on {dev}, its rows unbroken")
+        rows = dims[0]
         odt, cols = (xdt, self.M // 2) if swiglu else (torch.float32, self.M)
-        if out.dtype != odt or out.device != self.device or not out.is_contiguous() or tuple(out.shape) != (rows, cols):
-            raise ValueError(f"out is a contiguous {odt} tensor [{rows}][{cols}] on {self.device}")
-        if add is not None and (add.dtype != torch.float32 or add.device != self.device or not add.is_contiguous() or
-                                tuple(add.shape) != (rows, self.M)):
-            raise ValueError(f"add is a contiguous float32 tensor [{rows}][{self.M}] on {self.device}")
-        capi.dflash_linear_w4(capi.BF16 if xdt == torch.bfloat16 else capi.F32, x,
-                              x.stride(0) if rows > 1 else self.K, self._c, add, int(swiglu), out, rows, ws.handle, stream)
+        if out.dtype is not odt or out.shape != (rows, cols) or out.device != dev or not out.is_contiguous():
+            raise ValueError(f"out is a contiguous {odt} tensor [{rows}][{cols}] on {dev}")
+        if add is not None and (add.dtype is not torch.float32 or add.shape != (rows, self.M) or add.device != dev or
+                                not add.is_contiguous()):
+            raise ValueError(f"add is a contiguous float32 tensor [{rows}][{self.M}] on {dev}")
+        capi.dflash_linear_w4(capi.BF16 if xdt is torch.bfloat16 else capi.F32, x, x.stride(0) if rows > 1 else self.K,
+                              self._c, add, int(swiglu), out, rows, ws.handle, _raw_stream(self._index))
