@@ -8,19 +8,20 @@
 // multiplies the scores in float32, and a weight enters the product with the values
 // as half(2^(z - m) vs f), f a factor of the row that keeps the largest below 2^15.
 //
-// An item is up to 128 stacked rows, one to a thread.  A tile of 64 keys goes
+// An item is up to 128 stacked rows.  A tile of 64 keys goes
 //   pages -> registers (one tile ahead; the pages' numbers two ahead)
 //         -> halves in shared memory, two buffers, K and V rows alike, swizzled
-//   S = Q K^T   128 rows by 64 keys in TMEM: a thread reads its row
+//   S = Q K^T   128 rows by 64 keys in TMEM
 //   O += P V    P as halves in TMEM, O in TMEM
-// so a key's codes are expanded once for all rows, while the products of the tile
-// before run.  One barrier a tile; two CTAs share an SM, and one's products run
-// under the other's exponentials.  The split of a call over CTAs is that of
+// so a key's codes are expanded once for all rows.  Warps 0..3 take the exponentials,
+// a row a thread; warps 4..7 fetch and expand the next tile meanwhile, and two of them
+// issue the products.  Two CTAs share an SM.  The split of a call over CTAs is that of
 // paged.cuh; pieces of items are joined by a second kernel.
 //
 // Every wait is bounded (PagedGeom::wait_ns); one that gives up sets
-// DFLASH_STATUS_TIMEOUT, and the CTA drains its products, whatever the limit, and
-// ends.
+// DFLASH_STATUS_TIMEOUT, the CTA stops, drains its products, whatever the limit, and
+// ends.  No wait can be lapped by a whole phase: what completes a barrier's next phase
+// needs every warp that waits for this one (named at the barriers).
 #include <math.h>
 
 #include <algorithm>
@@ -32,7 +33,8 @@
 namespace dfl {
 
 namespace {
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int kGroup = 128;  // threads of the exponentials, and of the expansion
 constexpr int kKeys = kPagedQ8Keys;
 constexpr int kRows = 128;
 constexpr uint64_t kDrainNs = 125000000ull;
@@ -45,9 +47,23 @@ struct Q8TcLayout {
   static constexpr int kK = kHalves * kRows * 128;     // [2]
   static constexpr int kV = kK + 2 * kTile;            // [2]
   static constexpr int kScales = kV + 2 * kTile;       // [2][ks, vs][64]
-  static constexpr int kRed = kScales + 2 * 2 * kKeys * 4;
+  static constexpr int kSpan = kScales + 2 * 2 * kKeys * 4;  // [rows] sink, lo, hi, 2^-up of the queries' factor
+  static constexpr int kRed = kSpan + kRows * 16;
   static constexpr int kUsed = kRed + (2 * kThreads / 32 + 8) * 4;
   static constexpr int kSmem = kUsed + 1024;
+};
+
+// What both halves of the CTA need to know of a piece.
+struct Q8Piece {
+  int nt, prefix, b, rt, hk, whole;
+  int s0, sn, w0, t0;                 // tile t is t0 + t of the item's: s0 + t below sn, then w0 + t - sn
+  int key_lo, key_end;
+  int seen_sink, seen_lo;             // some row sees the keys below the one, and those from the other on
+  long long slot_row;
+  __device__ __forceinline__ int tile(int t) const {
+    t += t0;
+    return t < sn ? s0 + t : w0 + t - sn;
+  }
 };
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -93,11 +109,6 @@ __device__ __forceinline__ uint32_t bits_of(int a, int b) {
   if (a >= b) return 0u;
   return (b >= 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
 }
-// A phase is over, waited for up to the limit (0: it has expired).
-__device__ __forceinline__ bool over(uint64_t* bar, uint32_t parity, unsigned limit_ns) {
-  if (limit_ns != 0 && mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, limit_ns);
-}
 }  // namespace
 
 template <int HD>
@@ -107,14 +118,27 @@ __global__ void __launch_bounds__(kThreads, 2)
                             float scale_log2) {
   typedef Q8TcLayout<HD> L;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_done, pv_done;
+  // kv_full: a tile's keys and values are expanded (4 warps).  s_done: its scores are there.  s_free: and have been
+  // read (4 warps; so all have waited for s_done).  p_full: its weights are there (4 warps, which have waited for the
+  // last pv_done).  pv_done: their product with the values is done; it is asked for after p_full and the next tile's
+  // kv_full, whose warps have waited for the one before it.
+  __shared__ __align__(8) uint64_t kv_full, s_done, s_free, p_full, pv_done, drain[2];
   __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_s;
+  __shared__ Q8Piece pc;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* scales = reinterpret_cast<float*>(sm + L::kScales);
+  int4* spans = reinterpret_cast<int4*>(sm + L::kSpan);
   if (tid == 0) {
+    mbar_init(&kv_full, 4);
     mbar_init(&s_done, 1);
+    mbar_init(&s_free, 4);
+    mbar_init(&p_full, 4);
     mbar_init(&pv_done, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
+    abort_s = 0;
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -126,176 +150,276 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot, tO = tmem, tS = tmem + 128, tP = tmem + 192;
-  const uint32_t lanes = (uint32_t)(32 * warp) << 16;
   pdl_launch();
   pdl_wait();
   const PlanView pv = plan_view<kKeys, kThreads>(g, reinterpret_cast<int*>(sm + L::kRed));
-  SegmentWalk<kKeys> walk(g, pv);
-  walk.start();
-  Segment sg;
-  int seg = 0;
-  uint32_t s_n = 0, pv_n = 0;  // score products and value products asked for
-  bool ok = true;
-  constexpr uint32_t idS = idesc_f16_f32(128, kKeys), idO = idesc_f16_f32(128, HD) | (1u << 16);  // values MN-major
-  while (true) {
-    const bool more = walk.next(sg);
-    if (seg == 0 && !g.shared) {
-      // the item that this CTA's run begins inside of, when it is the second to hold a piece of it
-      int c0 = 0, nc = 0;
-      if (more && sg.t0 > 0) nc = walk.pieces(sg, c0);
-      if (c0 + 1 != (int)blockIdx.x) nc = 0;
-      int4* rec = reinterpret_cast<int4*>(g.records) + 2 * blockIdx.x;
-      if (tid == 0) {
-        rec[0] = make_int4(nc, sg.b, sg.rt, sg.hk);
-        rec[1].x = c0;
+  // Waits for phase `n` of a barrier, giving up on the CTA's abort flag or after the limit (then raising the flag).
+  // A warp's lanes wait together and agree.
+  auto wait = [&](uint64_t* bar, int n) {
+    const uint32_t parity = (uint32_t)n & 1u;
+    if (g.wait_ns != 0 && __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    bool ok = false;
+    if (g.wait_ns != 0) {
+      const uint32_t t0 = global_ns_lo();
+      while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+        if (ok || abort_s || global_ns_lo() - t0 > g.wait_ns) break;
       }
     }
-    if (!more) break;
-    ++seg;
-    const int x0 = sg.rt * (sg.prefix ? g.rp : g.ri);
-    const ItemRow mine = item_row(g, sg.prefix, sg.b, sg.hk, x0, tid);
-    // ------------------------------------------------------------ queries: half, each row by a power of two
-    float rf = 1.f;
-    int sink = 0, lo = 0, hi = INT32_MAX;
-    {
-      const uint4* src = reinterpret_cast<const uint4*>(
-          q + (((long long)mine.b * g.n + mine.i) * g.nq + mine.head) * HD);
-      float most = 0.f;
-      if (mine.live) {
-        row_span(g, paged_len(g, mine.b), paged_rows(g, mine.b), mine.i, sink, lo, hi);
-#pragma unroll 4
-        for (int c = 0; c < HD / 8; ++c) {
-          const uint4 u = src[c];
-          const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __bfloat1622float2(h[e]);
-            most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        }
+    if (__any_sync(0xffffffffu, !ok)) {
+      if (lane == 0) {
+        if (!abort_s) set_status(g.status, DFLASH_STATUS_TIMEOUT);
+        abort_s = 1;
       }
-      // 2^up brings the largest entry to 2^7..2^8 (a row of zeros, or one that holds Inf: as it is)
-      const int ex = (int)(__float_as_uint(most) >> 23);
-      const int up = ex > 0 && ex < 255 ? 134 - ex : ex == 0 && most > 0.f ? 133 : 0;
-      const float u1 = exp2f((float)(up / 2)), u2 = exp2f((float)(up - up / 2));
-      rf = exp2f((float)-up);
-#pragma unroll 4
-      for (int c = 0; c < HD / 8; ++c) {
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (mine.live) u = src[c];
-        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-        uint32_t w[4];
+      return false;
+    }
+    return true;
+  };
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  // All threads of the CTA, from either group's code.
+  auto cta_sync = [&] {
+    __syncwarp();
+    asm volatile("barrier.cta.sync 0, %0;" ::"n"(kThreads) : "memory");
+  };
+  // The piece's queries: half, each row by a power of two.
+  auto load_queries = [&] {
+    const int x0 = pc.rt * (pc.prefix ? g.rp : g.ri);
+      constexpr int kLanes = HD / 16;  // a lane takes 16 entries of a row
+      const int c = tid % kLanes;
+#pragma unroll 2
+      for (int r = tid / kLanes; r < kRows; r += kThreads / kLanes) {
+        const ItemRow row = item_row(g, pc.prefix, pc.b, pc.hk, x0, r);
+        uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        int4 span = make_int4(0, 0, INT32_MAX, 0);
+        if (row.live) {
+          const uint4* src =
+              reinterpret_cast<const uint4*>(q + (((long long)row.b * g.n + row.i) * g.nq + row.head) * HD + 16 * c);
+          raw[0] = src[0];
+          raw[1] = src[1];
+          if (c == 0) row_span(g, paged_len(g, row.b), paged_rows(g, row.b), row.i, span.x, span.y, span.z);
+        }
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
+        float most = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 8; ++e) {
+          const float2 f = __bfloat1622float2(h[e]);
+          most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        // 2^up brings the largest entry to 2^7..2^8 (a row of zeros, or one that holds Inf: as it is)
+        const int ex = (int)(__float_as_uint(most) >> 23);
+        const int up = ex > 0 && ex < 255 ? 134 - ex : ex == 0 && most > 0.f ? 133 : 0;
+        const float u1 = exp2f((float)(up / 2)), u2 = exp2f((float)(up - up / 2));
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
           const float2 f = __bfloat1622float2(h[e]);
           w[e] = half2_of(f.x * u1 * u2, f.y * u1 * u2);
         }
-        *reinterpret_cast<uint4*>(sm + L::kQ + (c >> 3) * (kRows * 128) + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+        uint8_t* dst = sm + L::kQ + (c >> 2) * (kRows * 128) + r * 128;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<uint4*>(dst + (((2 * (c & 3) + e) ^ (r & 7)) << 4)) =
+              make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        if (c == 0) {
+          span.w = __float_as_int(exp2f((float)-up));
+          spans[r] = span;
+        }
       }
+      fence_proxy_async_smem();
+  };
+  int done = 0;  // tiles of the pieces before
+  if (warp >= 4) {
+    // ------------------------------------------------------------ keys and values, and the products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    while (true) {
+      cta_sync();
+      const int nt = pc.nt;
+      if (nt == 0) break;
+      load_queries();
+      cta_sync();
+      // A thread takes 16 bytes of every kStep-th key row: whole rows by neighbours.  Every 16 keys lie in one page.
+      constexpr int kLanes = HD / 16, kStep = kGroup / kLanes, KU = kKeys / kStep;
+      const int et = tid - kGroup, kr = et / kLanes, kc16 = et % kLanes;
+      const int hk = pc.hk, key_end = pc.key_end, seen_sink = pc.seen_sink, seen_lo = pc.seen_lo;
+      const int32_t* trow = g.table + (long long)pc.b * g.table_stride;
+      // The page of the 16 keys 16 (lane % 4) .. of tile i (-1: no row sees one of them): asked for a tile before it is
+      // looked at.
+      auto key_of = [&](int i) { return pc.tile(i) * kKeys + 16 * (lane & 3); };
+      auto page_of = [&](int i) {
+        if (i >= nt) return -1;
+        const int key = key_of(i);
+        return key >= key_end || (key >= seen_sink && key + 16 <= seen_lo) ? -1 : trow[key >> g.ps_log2];
+      };
+      uint4 kc[KU], vc[KU];
+      float sc = 0.f;
+      // (Keys that no row sees, and those of a bad page: some row of the pool; what they hold is masked, or the
+      // sequence's result unspecified.)
+      auto fetch = [&](int i, int page) {
+        if (i >= nt) return;
+        int first = 0;  // the pool row of the 16 keys (below 2^31)
+        if ((unsigned)page < (unsigned)g.n_pages)
+          first = (int)g.page_row0 + (page * g.nkv + hk) * g.ps + (key_of(i) & (g.ps - 1));
+        else if (page != -1)
+          set_status(g.status, DFLASH_STATUS_BOUNDS);
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+          const int key = kr + kStep * u;
+          const long long at = (long long)(__shfl_sync(0xffffffffu, first, key >> 4) + (key & 15)) * HD + 16 * kc16;
+          kc[u] = __ldg(reinterpret_cast<const uint4*>(kp + at));
+          vc[u] = __ldg(reinterpret_cast<const uint4*>(vp + at));
+        }
+        const int key = et & 63;
+        sc = __ldg((et < kKeys ? g.ks : g.vs) + __shfl_sync(0xffffffffu, first, key >> 4) + (key & 15));
+      };
+      auto expand = [&](int buf) {
+        // 16 codes are two chunks of 16 bytes; lanes of the upper half of a row write theirs the other way round, so
+        // that the 8 lanes of a row fill all banks
+        const int c = 2 * (kc16 & 3), far = kc16 >> 2;
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+          const int key = kr + kStep * u;
+          uint8_t* base = sm + far * (kKeys * 128) + buf * L::kTile + key * 128;
+          const int p0 = ((c + far) ^ (key & 7)) << 4, p1 = ((c + 1 - far) ^ (key & 7)) << 4;
+          uint4 h[2];
+          halves_of(kc[u], h);
+          *reinterpret_cast<uint4*>(base + L::kK + p0) = far ? h[1] : h[0];
+          *reinterpret_cast<uint4*>(base + L::kK + p1) = far ? h[0] : h[1];
+          halves_of(vc[u], h);
+          *reinterpret_cast<uint4*>(base + L::kV + p0) = far ? h[1] : h[0];
+          *reinterpret_cast<uint4*>(base + L::kV + p1) = far ? h[0] : h[1];
+        }
+        scales[2 * buf * kKeys + et] = et < kKeys ? sc * scale_log2 : sc;
+      };
+      constexpr uint32_t idS = idesc_f16_f32(128, kKeys), idO = idesc_f16_f32(128, HD) | (1u << 16);  // values MN-major
+      int next_page = page_of(0);
+      fetch(0, next_page);
+      next_page = page_of(1);
+      for (int i = 0; i <= nt; ++i) {
+        const int T = done + i;  // tile i's number
+        if (i < nt) {
+          // the buffer's last values have been read (and so have its keys: their scores came before; the piece before
+          // has ended)
+          if (i >= 2 && !wait(&pv_done, T - 2)) break;
+          expand(T & 1);
+          fence_proxy_async_smem();
+          arrive(&kv_full);
+          fetch(i + 1, next_page);
+          next_page = page_of(i + 2);
+        }
+        if (warp == 4 && i < nt) {
+          if (!wait(&kv_full, T) || (i > 0 && !wait(&s_free, T - 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t dq = smem_desc_sw128(sm + L::kQ), dk = smem_desc_sw128(sm + L::kK + (T & 1) * L::kTile);
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)
+              tc_mma_f16(tS, dq + (uint64_t)((k >> 2) * (kRows * 128 / 16) + 2 * (k & 3)),
+                         dk + (uint64_t)((k >> 2) * (kKeys * 128 / 16) + 2 * (k & 3)), idS, k > 0);
+            tc_commit(&s_done);
+          }
+          __syncwarp();
+        }
+        if (warp == 5 && i > 0) {  // (of the tile before)
+          if ((i < nt && !wait(&kv_full, T)) || !wait(&p_full, T - 1)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t vt = smem_u32(sm + L::kV + ((T - 1) & 1) * L::kTile);
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              tc_mma_f16_tmem_a(tO, tP + 8 * k, smem_desc_mn(vt + k * 2048, kKeys * 128), idO,
+                                i > 1 || k > 0);
+            tc_commit(&pv_done);
+          }
+          __syncwarp();
+        }
+      }
+      cta_sync();
+      if (abort_s) break;
+      done += nt;
     }
-    const int key_lo = sg.prefix ? 0 : pv.sh_tiles * kKeys;
-    const int key_end = sg.prefix ? pv.sh_tiles * kKeys : key_limit(g, sg.b);
-    const int all_lo = __reduce_max_sync(0xffffffffu, max(key_lo, lo));
-    const int all_hi = __reduce_min_sync(0xffffffffu, min(key_end, hi));
-    const bool idle = __all_sync(0xffffffffu, !mine.live);  // none of the warp's rows is one
-    int seen_sink, seen_lo, seen_hi;
-    row_span(g, sg.prefix ? pv.min_len : paged_len(g, sg.b), paged_rows(g, sg.b),
-             sg.prefix ? 0 : div_g(g, sg.rt * g.ri), seen_sink, seen_lo, seen_hi);
-    // ------------------------------------------------------------ keys and values
-    // A thread takes 16 bytes of every kStep-th key row: whole rows by neighbours.  Every 16 keys lie in one page.
-    constexpr int kLanes = HD / 16, kStep = kThreads / kLanes, KU = kKeys / kStep;
-    const int kr = tid / kLanes, kc16 = tid % kLanes;
-    const int32_t* trow = g.table + (long long)sg.b * g.table_stride;
-    // The page of the 16 keys 16 (lane % 4) .. of tile i (-1: no row sees one of them): asked for a tile before it is
-    // looked at.
-    auto key_of = [&](int i) { return sg.span.tile(sg.t0 + i) * kKeys + 16 * (lane & 3); };
-    auto page_of = [&](int i) {
-      if (i >= sg.nt) return -1;
-      const int key = key_of(i);
-      return key >= key_end || (key >= seen_sink && key + 16 <= seen_lo) ? -1 : trow[key >> g.ps_log2];
-    };
-    uint4 kc[KU], vc[KU];
-    float sc = 0.f;
-    // (Keys that no row sees, and those of a bad page: some row of the pool; what they hold is masked, or the sequence's
-    // result unspecified.)
-    auto fetch = [&](int i, int page) {
-      if (i >= sg.nt) return;
-      int first = 0;  // the pool row of the 16 keys (below 2^31)
-      if ((unsigned)page < (unsigned)g.n_pages)
-        first = (int)g.page_row0 + (page * g.nkv + sg.hk) * g.ps + (key_of(i) & (g.ps - 1));
-      else if (page != -1)
-        set_status(g.status, DFLASH_STATUS_BOUNDS);
-#pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        const int key = kr + kStep * u;
-        const long long at = (long long)(__shfl_sync(0xffffffffu, first, key >> 4) + (key & 15)) * HD + 16 * kc16;
-        kc[u] = __ldg(reinterpret_cast<const uint4*>(kp + at));
-        vc[u] = __ldg(reinterpret_cast<const uint4*>(vp + at));
-      }
-      const int key = tid & 63;
-      sc = __ldg((tid < 64 ? g.ks : g.vs) + __shfl_sync(0xffffffffu, first, key >> 4) + (key & 15));
-    };
-    auto expand = [&](int buf) {
-      // 16 codes are two chunks of 16 bytes; lanes of the upper half of a row write theirs the other way round, so
-      // that the 8 lanes of a row fill all banks
-      const int c = 2 * (kc16 & 3), far = kc16 >> 2;
-#pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        const int key = kr + kStep * u;
-        uint8_t* base = sm + far * (kKeys * 128) + buf * L::kTile + key * 128;
-        const int p0 = ((c + far) ^ (key & 7)) << 4, p1 = ((c + 1 - far) ^ (key & 7)) << 4;
-        uint4 h[2];
-        halves_of(kc[u], h);
-        *reinterpret_cast<uint4*>(base + L::kK + p0) = far ? h[1] : h[0];
-        *reinterpret_cast<uint4*>(base + L::kK + p1) = far ? h[0] : h[1];
-        halves_of(vc[u], h);
-        *reinterpret_cast<uint4*>(base + L::kV + p0) = far ? h[1] : h[0];
-        *reinterpret_cast<uint4*>(base + L::kV + p1) = far ? h[0] : h[1];
-      }
-      scales[2 * buf * kKeys + tid] = tid < 64 ? sc * scale_log2 : sc;
-    };
-    auto scores = [&](int buf) {  // one thread
-      const uint64_t dq = smem_desc_sw128(sm + L::kQ), dk = smem_desc_sw128(sm + L::kK + buf * L::kTile);
-#pragma unroll
-      for (int k = 0; k < HD / 16; ++k)
-        tc_mma_f16(tS, dq + (uint64_t)((k >> 2) * (kRows * 128 / 16) + 2 * (k & 3)),
-                   dk + (uint64_t)((k >> 2) * (kKeys * 128 / 16) + 2 * (k & 3)), idS, k > 0);
-      tc_commit(&s_done);
-    };
-    int next_page = page_of(0);
-    fetch(0, next_page);
-    next_page = page_of(1);
-    expand(0);
-    fetch(1, next_page);
-    next_page = page_of(2);
-    fence_proxy_async_smem();
-    tc_fence_before();
-    if (__syncthreads_or(!ok)) break;
-    if (warp == 0) {
-      if (elect_one()) {
-        tc_fence_after();
-        scores(0);
-      }
+    if (abort_s && warp < 6) {
+      // products in flight end before their operands go away
+      if (elect_one()) tc_commit(&drain[warp - 4]);
       __syncwarp();
+      mbar_wait(&drain[warp - 4], 0, kDrainNs);
     }
-    ++s_n;
-    float m = -INFINITY, l = 0.f, f = 1.f;
-    for (int i = 0; i < sg.nt; ++i) {
-      // the value products of tile i - 1: their weights, their values and the other keys' buffer are free
-      if (i > 0) ok = ok && over(&pv_done, (pv_n - 1) & 1u, g.wait_ns);
-      if (i + 1 < sg.nt) {
-        expand((i + 1) & 1);
-        fetch(i + 2, next_page);
-        next_page = page_of(i + 3);
+  } else {
+    // ------------------------------------------------------------ exponentials
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    SegmentWalk<kKeys> walk(g, pv);
+    walk.start();
+    bool first = true;
+    while (true) {
+    if (warp == 0) {
+      Segment sg;
+      const bool more = walk.next(sg);
+      if (first && !g.shared) {
+        // the item that this CTA's run begins inside of, when it is the second to hold a piece of it
+        int c0 = 0, nc = 0;
+        if (more && sg.t0 > 0) nc = walk.pieces(sg, c0);
+        if (c0 + 1 != (int)blockIdx.x) nc = 0;
+        int4* rec = reinterpret_cast<int4*>(g.records) + 2 * blockIdx.x;
+        if (lane == 0) {
+          rec[0] = make_int4(nc, sg.b, sg.rt, sg.hk);
+          rec[1].x = c0;
+        }
       }
-      ok = ok && over(&s_done, (s_n - 1) & 1u, g.wait_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-      if (ok && !idle) {
-        const float* ks = scales + 2 * (i & 1) * kKeys;
+      if (lane == 0) {
+        pc.nt = more ? sg.nt : 0;
+        if (more) {
+          pc.prefix = sg.prefix;
+          pc.b = sg.b;
+          pc.rt = sg.rt;
+          pc.hk = sg.hk;
+          pc.whole = walk.whole(sg);
+          pc.s0 = sg.span.s0;
+          pc.sn = sg.span.s1 - sg.span.s0;
+          pc.w0 = sg.span.w0;
+          pc.t0 = sg.t0;
+          pc.key_lo = sg.prefix ? 0 : pv.sh_tiles * kKeys;
+          pc.key_end = sg.prefix ? pv.sh_tiles * kKeys : key_limit(g, sg.b);
+          int hi;
+          row_span(g, sg.prefix ? pv.min_len : paged_len(g, sg.b), paged_rows(g, sg.b),
+                   sg.prefix ? 0 : div_g(g, sg.rt * g.ri), pc.seen_sink, pc.seen_lo, hi);
+          pc.slot_row = sg.slot_row;
+        }
+      }
+    }
+      first = false;
+      cta_sync();
+      const int nt = pc.nt;
+      if (nt == 0) break;
+      load_queries();
+      cta_sync();
+      const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+      const int4 span = spans[tid];
+      const int sink = span.x, lo = span.y, hi = span.z, key_lo = pc.key_lo, key_end = pc.key_end;
+      const float rf = __int_as_float(span.w);
+      const int all_lo = __reduce_max_sync(0xffffffffu, max(key_lo, lo));
+      const int all_hi = __reduce_min_sync(0xffffffffu, min(key_end, hi));
+      const ItemRow mine = item_row(g, pc.prefix, pc.b, pc.hk, pc.rt * (pc.prefix ? g.rp : g.ri), tid);
+      const bool idle = __all_sync(0xffffffffu, !mine.live);  // none of the warp's rows is one
+      float m = -INFINITY, l = 0.f, f = 1.f;
+      bool ok = true;
+      for (int i = 0; i < nt; ++i) {
+        const int T = done + i;
+        if (!(ok = wait(&s_done, T))) break;
+        tc_fence_after();
+        if (idle) {  // (in step with the others: an arrival must not count for the phase before)
+          arrive(&s_free);
+          if (i > 0 && !(ok = wait(&pv_done, T - 1))) break;
+          arrive(&p_full);
+          continue;
+        }
+        const float* ks = scales + 2 * (T & 1) * kKeys;
         const float* vs = ks + kKeys;
-        const int k0 = sg.span.tile(sg.t0 + i) * kKeys;
+        const int k0 = pc.tile(i) * kKeys;
         uint32_t s[2][32];
         tmem_ld32(tS + lanes, s[0]);
         tmem_ld32(tS + 32 + lanes, s[1]);
@@ -307,6 +431,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         // a hidden value's scale that is not finite would reach this row through its weight of 0
         const bool bad = !whole_tile && __any_sync(0xffffffffu, !(va < INFINITY && vb < INFINITY));
         tmem_ld_wait();
+        tc_fence_before();
+        arrive(&s_free);
         float2* z = reinterpret_cast<float2*>(s);
         const float2 rf2 = make_float2(rf, rf);
         const float4* ks4 = reinterpret_cast<const float4*>(ks);
@@ -338,6 +464,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float zmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         const bool none = m == -INFINITY;
         const bool move = none ? zmax > -INFINITY : zmax - m > 64.f || ex2f(zmax - m) * (f * vmax) > 32768.f;
+        // the last weights have been multiplied: theirs are free, and the outputs' sums may be moved
+        if (i > 0 && !(ok = wait(&pv_done, T - 1))) break;
+        tc_fence_after();
         if (__any_sync(0xffffffffu, move)) {
           const float mn = fmaxf(m, zmax);
           const bool has = mn > -INFINITY;
@@ -404,84 +533,51 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         l += sum.x + sum.y;
         tmem_st_wait();
+        tc_fence_before();
+        arrive(&p_full);
       }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      if (__syncthreads_or(!ok)) {
-        ok = false;
-        break;
-      }
-      if (warp == 0) {
-        if (elect_one()) {
-          tc_fence_after();
-          const uint32_t vt = smem_u32(sm + L::kV + (i & 1) * L::kTile);
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            tc_mma_f16_tmem_a(tO, tP + 8 * k, smem_desc_mn(vt + k * 2048, kKeys * 128), idO, (i | k) != 0);
-          tc_commit(&pv_done);
-        }
-        __syncwarp();
-      } else if (warp == 1 && i + 1 < sg.nt) {  // (by another warp: a product takes 30 to 60 cycles to ask for)
-        if (elect_one()) {
-          tc_fence_after();
-          scores((i + 1) & 1);
-        }
-        __syncwarp();
-      }
-      ++pv_n;
-      if (i + 1 < sg.nt) ++s_n;
-    }
-    if (!ok) break;
-    // ------------------------------------------------------------ the rows' results
-    ok = over(&pv_done, (pv_n - 1) & 1u, g.wait_ns);
-    if (__syncthreads_or(!ok)) {
-      ok = false;
-      break;
-    }
-    tc_fence_after();
-    const bool whole = walk.whole(sg);
-    if (!idle) {
-      const float inv = whole ? 1.f / (f * l) : 1.f / f;
-      bf16* dst = out + (((long long)mine.b * g.n + mine.i) * g.nq + mine.head) * HD;
-      float* pdst = g.part_o + (sg.slot_row + tid) * HD;
+      // ---------------------------------------------------------- the rows' results
+      if (ok) ok = wait(&pv_done, done + nt - 1);
+      tc_fence_after();
+      if (ok && !idle) {
+        const bool whole = pc.whole;
+        const float inv = whole ? 1.f / (f * l) : 1.f / f;
+        bf16* dst = out + (((long long)mine.b * g.n + mine.i) * g.nq + mine.head) * HD;
+        float* pdst = g.part_o + (pc.slot_row + tid) * HD;
 #pragma unroll 1
-      for (int c = 0; c < HD; c += 16) {
-        uint32_t o[16];
-        tmem_ld16u(tO + lanes + c, o);
-        tmem_ld_wait();
-        float x[16];
+        for (int c = 0; c < HD; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + lanes + c, o);
+          tmem_ld_wait();
+          if (mine.live) {
+            if (whole) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[e]) * inv;
-        if (mine.live) {
-          if (whole) {
+              for (int e = 0; e < 32; e += 8) {
+                uint4 v;
+                __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
 #pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              uint4 v;
-              __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+                for (int y = 0; y < 4; ++y)
+                  h[y] = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * y]) * inv, __uint_as_float(o[e + 2 * y + 1]) * inv);
+                *reinterpret_cast<uint4*>(dst + c + e) = v;
+              }
+            } else {
 #pragma unroll
-              for (int y = 0; y < 4; ++y) h[y] = __floats2bfloat162_rn(x[e + 2 * y], x[e + 2 * y + 1]);
-              *reinterpret_cast<uint4*>(dst + c + e) = v;
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(pdst + c + e) =
+                    make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(pdst + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
           }
         }
+        if (mine.live && !whole) g.part_ml[pc.slot_row + tid] = make_float2(m, l);
       }
-      if (mine.live && !whole) g.part_ml[sg.slot_row + tid] = make_float2(m, l);
-    }
-    tc_fence_before();
-    __syncthreads();
-  }
-  if (!ok) {
-    // (some thread's wait ran out: all of them are here) products in flight end before their operands go away
-    if (tid == 0) {
-      set_status(g.status, DFLASH_STATUS_TIMEOUT);
-      if (s_n > 0) mbar_wait(&s_done, (s_n - 1) & 1u, kDrainNs);
-      if (pv_n > 0) mbar_wait(&pv_done, (pv_n - 1) & 1u, kDrainNs);
+      tc_fence_before();
+      cta_sync();
+      if (abort_s) break;
+      done += nt;
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
