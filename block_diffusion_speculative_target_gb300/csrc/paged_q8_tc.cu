@@ -9,8 +9,9 @@
 // as half(2^(z - m) vs f), f a factor of the row that keeps the largest below 2^15.
 //
 // An item is up to 128 stacked rows.  A tile of 64 keys goes
-//   pages -> registers (one tile ahead; the pages' numbers two ahead)
-//         -> halves in shared memory, two buffers, K and V rows alike, swizzled
+//   pages -> codes in shared memory by bulk copies of 16 keys (one tile ahead; the
+//            pages' numbers two ahead)
+//         -> halves in shared memory, K once and V in two buffers, swizzled
 //   S = Q K^T   128 rows by 64 keys in TMEM
 //   O += P V    P as halves in TMEM, O in TMEM
 // so a key's codes are expanded once for all rows.  Warps 0..3 take the exponentials,
@@ -44,9 +45,11 @@ struct Q8TcLayout {
   static constexpr int kHalves = HD / 64;              // 64 dimensions: rows of 128 bytes
   static constexpr int kTile = kHalves * kKeys * 128;  // 64 keys or values
   static constexpr int kQ = 0;
-  static constexpr int kK = kHalves * kRows * 128;     // [2]
-  static constexpr int kV = kK + 2 * kTile;            // [2]
-  static constexpr int kScales = kV + 2 * kTile;       // [2][ks, vs][64]
+  static constexpr int kK = kHalves * kRows * 128;
+  static constexpr int kV = kK + kTile;                // [2]
+  static constexpr int kCodes = kV + 2 * kTile;        // [K, V][64][HD] as in the pages
+  static constexpr int kCodeScales = kCodes + 2 * kKeys * HD;   // [ks, vs][64]
+  static constexpr int kScales = kCodeScales + 2 * kKeys * 4;   // [2][ks, vs][64]
   static constexpr int kSpan = kScales + 2 * 2 * kKeys * 4;  // [rows] sink, lo, hi, 2^-up of the queries' factor
   static constexpr int kRed = kSpan + kRows * 16;
   static constexpr int kUsed = kRed + (2 * kThreads / 32 + 8) * 4;
@@ -122,7 +125,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   // read (4 warps; so all have waited for s_done).  p_full: its weights are there (4 warps, which have waited for the
   // last pv_done).  pv_done: their product with the values is done; it is asked for after p_full and the next tile's
   // kv_full, whose warps have waited for the one before it.
-  __shared__ __align__(8) uint64_t kv_full, s_done, s_free, p_full, pv_done, drain[2];
+  // codes_full: a tile's codes are there.  codes_free: and have been read (4 warps; so all have waited for codes_full).
+  __shared__ __align__(8) uint64_t kv_full, s_done, s_free, p_full, pv_done, codes_full, codes_free, drain[2];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_s;
   __shared__ Q8Piece pc;
@@ -136,6 +140,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(&s_free, 4);
     mbar_init(&p_full, 4);
     mbar_init(&pv_done, 1);
+    mbar_init(&codes_full, 1);
+    mbar_init(&codes_free, 4);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     abort_s = 0;
@@ -237,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp >= 4) {
     // ------------------------------------------------------------ keys and values, and the products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    int asked = 0;  // tiles that warp 6 has asked for
     while (true) {
       cta_sync();
       const int nt = pc.nt;
@@ -256,67 +263,82 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int key = key_of(i);
         return key >= key_end || (key >= seen_sink && key + 16 <= seen_lo) ? -1 : trow[key >> g.ps_log2];
       };
-      uint4 kc[KU], vc[KU];
-      float sc = 0.f;
+      // Tile i's codes: a lane of warp 6 brings 16 keys, their values and the scales of both.
       // (Keys that no row sees, and those of a bad page: some row of the pool; what they hold is masked, or the
       // sequence's result unspecified.)
       auto fetch = [&](int i, int page) {
-        if (i >= nt) return;
-        int first = 0;  // the pool row of the 16 keys (below 2^31)
-        if ((unsigned)page < (unsigned)g.n_pages)
-          first = (int)g.page_row0 + (page * g.nkv + hk) * g.ps + (key_of(i) & (g.ps - 1));
-        else if (page != -1)
-          set_status(g.status, DFLASH_STATUS_BOUNDS);
-#pragma unroll
-        for (int u = 0; u < KU; ++u) {
-          const int key = kr + kStep * u;
-          const long long at = (long long)(__shfl_sync(0xffffffffu, first, key >> 4) + (key & 15)) * HD + 16 * kc16;
-          kc[u] = __ldg(reinterpret_cast<const uint4*>(kp + at));
-          vc[u] = __ldg(reinterpret_cast<const uint4*>(vp + at));
+        asked = done + i + 1;
+        if (lane == 0) mbar_arrive_expect_tx(&codes_full, 2 * kKeys * (HD + 4));
+        __syncwarp();
+        if (lane < 4) {
+          long long first = 0;  // the pool row of the 16 keys
+          if ((unsigned)page < (unsigned)g.n_pages)
+            first = g.page_row0 + ((long long)page * g.nkv + hk) * g.ps + (key_of(i) & (g.ps - 1));
+          else if (page != -1)
+            set_status(g.status, DFLASH_STATUS_BOUNDS);
+          uint8_t* codes = sm + L::kCodes + lane * 16 * HD;
+          uint8_t* cs = sm + L::kCodeScales + lane * 64;
+          bulk_load(codes, kp + first * HD, 16 * HD, &codes_full);
+          bulk_load(codes + kKeys * HD, vp + first * HD, 16 * HD, &codes_full);
+          bulk_load(cs, g.ks + first, 64, &codes_full);
+          bulk_load(cs + kKeys * 4, g.vs + first, 64, &codes_full);
         }
-        const int key = et & 63;
-        sc = __ldg((et < kKeys ? g.ks : g.vs) + __shfl_sync(0xffffffffu, first, key >> 4) + (key & 15));
+        __syncwarp();
       };
-      auto expand = [&](int buf) {
-        // 16 codes are two chunks of 16 bytes; lanes of the upper half of a row write theirs the other way round, so
-        // that the 8 lanes of a row fill all banks
-        const int c = 2 * (kc16 & 3), far = kc16 >> 2;
+      // 16 codes are two chunks of 16 bytes; lanes of the upper half of a row write theirs the other way round, so
+      // that the 8 lanes of a row fill all banks
+      const int c = 2 * (kc16 & 3), far = kc16 >> 2;
+      auto expand = [&](const uint4 (&codes)[KU], uint8_t* dst) {
 #pragma unroll
         for (int u = 0; u < KU; ++u) {
           const int key = kr + kStep * u;
-          uint8_t* base = sm + far * (kKeys * 128) + buf * L::kTile + key * 128;
-          const int p0 = ((c + far) ^ (key & 7)) << 4, p1 = ((c + 1 - far) ^ (key & 7)) << 4;
+          uint8_t* base = dst + far * (kKeys * 128) + key * 128;
+          const uint4 w = codes[u];
           uint4 h[2];
-          halves_of(kc[u], h);
-          *reinterpret_cast<uint4*>(base + L::kK + p0) = far ? h[1] : h[0];
-          *reinterpret_cast<uint4*>(base + L::kK + p1) = far ? h[0] : h[1];
-          halves_of(vc[u], h);
-          *reinterpret_cast<uint4*>(base + L::kV + p0) = far ? h[1] : h[0];
-          *reinterpret_cast<uint4*>(base + L::kV + p1) = far ? h[0] : h[1];
+          halves_of(far ? make_uint4(w.z, w.w, w.x, w.y) : w, h);
+          *reinterpret_cast<uint4*>(base + (((c + far) ^ (key & 7)) << 4)) = h[0];
+          *reinterpret_cast<uint4*>(base + (((c + 1 - far) ^ (key & 7)) << 4)) = h[1];
         }
-        scales[2 * buf * kKeys + et] = et < kKeys ? sc * scale_log2 : sc;
       };
       constexpr uint32_t idS = idesc_f16_f32(128, kKeys), idO = idesc_f16_f32(128, HD) | (1u << 16);  // values MN-major
-      int next_page = page_of(0);
-      fetch(0, next_page);
-      next_page = page_of(1);
+      int next_page = -1;
+      if (warp == 6) {
+        fetch(0, page_of(0));
+        next_page = page_of(1);
+      }
       for (int i = 0; i <= nt; ++i) {
         const int T = done + i;  // tile i's number
         if (i < nt) {
-          // the buffer's last values have been read (and so have its keys: their scores came before; the piece before
-          // has ended)
+          if (!wait(&codes_full, T)) break;
+          const uint4* raw = reinterpret_cast<const uint4*>(sm + L::kCodes) + et;
+          uint4 kc[KU], vc[KU];
+#pragma unroll
+          for (int u = 0; u < KU; ++u) {
+            kc[u] = raw[kGroup * u];
+            vc[u] = raw[kGroup * u + kKeys * HD / 16];
+          }
+          const float sc = reinterpret_cast<const float*>(sm + L::kCodeScales)[et];
+          arrive(&codes_free);
+          if (warp == 6 && i + 1 < nt) {
+            if (!wait(&codes_free, T)) break;
+            fetch(i + 1, next_page);
+            next_page = page_of(i + 2);
+          }
+          // the last scores have been computed; the buffer's last values and scales have been read (the piece before has
+          // ended)
+          if (i >= 1 && !wait(&s_done, T - 1)) break;
+          expand(kc, sm + L::kK);
           if (i >= 2 && !wait(&pv_done, T - 2)) break;
-          expand(T & 1);
+          expand(vc, sm + L::kV + (T & 1) * L::kTile);
+          scales[2 * (T & 1) * kKeys + et] = et < kKeys ? sc * scale_log2 : sc;
           fence_proxy_async_smem();
           arrive(&kv_full);
-          fetch(i + 1, next_page);
-          next_page = page_of(i + 2);
         }
         if (warp == 4 && i < nt) {
           if (!wait(&kv_full, T) || (i > 0 && !wait(&s_free, T - 1))) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t dq = smem_desc_sw128(sm + L::kQ), dk = smem_desc_sw128(sm + L::kK + (T & 1) * L::kTile);
+            const uint64_t dq = smem_desc_sw128(sm + L::kQ), dk = smem_desc_sw128(sm + L::kK);
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k)
               tc_mma_f16(tS, dq + (uint64_t)((k >> 2) * (kRows * 128 / 16) + 2 * (k & 3)),
@@ -349,6 +371,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       mbar_wait(&drain[warp - 4], 0, kDrainNs);
     }
+    // so do copies
+    if (abort_s && warp == 6 && asked > 0) mbar_wait(&codes_full, (uint32_t)(asked - 1) & 1u, kDrainNs);
   } else {
     // ------------------------------------------------------------ exponentials
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
