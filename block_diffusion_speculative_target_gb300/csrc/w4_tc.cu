@@ -26,9 +26,9 @@
 // and in a block.
 //
 // Warps: 0 streams the blocks (codes with their scales and zero points, one bulk
-// copy each) through a ring; 1 issues the products; 2 and 3 bring the columns of x
-// that a block meets (asynchronous copies, swizzled by hand, so that rows of x may
-// lie anywhere); 4..7 read the sums back, scale, add, join and write; 8..11 and
+// copy each) through a ring; 1 issues the products; 2 brings the columns of x that a
+// block meets by TMA, or, where rows of x do not lie on 16-byte boundaries, 2 and 3 do
+// by hand; 4..7 read the sums back, scale, add, join and write; 8..11 and
 // 12..15 expand every other block's codes into one of four TMEM buffers.
 //
 // Every wait is bounded (dflash_debug_set_wait_limit); one that runs out sets
@@ -55,7 +55,6 @@ template <int N>
 struct TcLayout {
   static constexpr int kX = N * 256;  // two halves of 64 columns: rows of 128 bytes, 16-byte chunks swizzled by row
   static constexpr int kXSlots = N <= 64 ? 6 : 3;
-  static constexpr int kXAhead = N <= 64 ? 3 : 1;  // blocks asked for past the one that is announced
   static constexpr int kCodeSlots = 10;
   static constexpr int kBars = 2 * kCodeSlots + 2 * kXSlots + 2 * kABufs + 2 * kMaxD + 1;
 };
@@ -196,10 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1u;
         }
       }
-      if (abort_s) {  // every copy asked for has landed before the CTA ends
-        const int asked = i - b0;
-        for (int u = max(0, asked - CS); u < asked; ++u) mbar_wait(&code_full[u % CS], (uint32_t)(u / CS) & 1u, kW4DrainNs);
-      }
+      // every copy asked for lands before the CTA ends, whichever warp gives up, and when
+      const int asked = i - b0;
+      for (int u = max(0, asked - CS); u < asked; ++u) mbar_wait(&code_full[u % CS], (uint32_t)(u / CS) & 1u, kW4DrainNs);
     } else if (warp == 1) {
       // ---------------------------------------------------------- products
       constexpr uint32_t idesc = idesc_bf16_f32(128, N);
@@ -273,56 +271,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (++kb == w.kt) kb = 0;
         }
-        if (abort_s) {
-          const int asked = i - b0;
-          for (int u = max(0, asked - XS); u < asked; ++u) mbar_wait(&x_full[u % XS], (uint32_t)(u / XS) & 1u, kW4DrainNs);
-        }
+        const int asked = i - b0;
+        for (int u = max(0, asked - XS); u < asked; ++u) mbar_wait(&x_full[u % XS], (uint32_t)(u / XS) & 1u, kW4DrainNs);
       }
     } else {
       // ---------------------------------------------------------- x anywhere
       // Lane l of warp 2 + v brings chunk l % 16 (8 columns) of the rows 2 v + l / 16 + 4 u.  Rows past the last one
       // are not filled: their columns of the products are not read.
       const int xc = lane & 15, xr = 2 * (warp - 2) + (lane >> 4);
-      const int live = rows;
-      int kb = b0 % w.kt, slot = 0, ready = 0;  // `ready`: the slot to be announced next
+      int kb = b0 % w.kt, slot = 0;
       uint32_t phase = 0;
       pdl_wait();
       const bf16* src0 = x + (long long)xr * ldx + 8 * xc;
       const uint32_t at0 = (uint32_t)((xc >> 3) * (N * 128) + xr * 128);
-      constexpr int kAhead = L::kXAhead;
-      auto announce = [&] {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&x_full[ready]);
-        if (++ready == XS) ready = 0;
-      };
-      bool ok = true;
       for (int i = b0; i < b1; ++i) {
-        if (i - b0 >= XS && !(ok = wait(&x_empty[slot], phase ^ 1u))) break;
+        if (i - b0 >= XS && !wait(&x_empty[slot], phase ^ 1u)) break;
         const bool in_k = kb * kW4Tile + 8 * xc < w.K;
         const bf16* src = src0 + kb * kW4Tile;
         const uint32_t at = slot * L::kX + at0;
 #pragma unroll 4
         for (int u = 0; u < N / 4; ++u) {
-          if (xr + 4 * u >= live) break;
+          if (xr + 4 * u >= rows) break;
           const uint32_t dst = at + u * 512 + 16 * ((xc & 7) ^ ((xr + 4 * u) & 7));
           const bf16* p = in_k ? src + (long long)(4 * u) * ldx : x;
           *reinterpret_cast<uint4*>(smem + dst) = gather8(p, in_k);
         }
-        cp_commit();
-        if (i - b0 >= kAhead) {
-          cp_wait<kAhead>();
-          announce();
-        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_full[slot]);
         if (++slot == XS) {
           slot = 0;
           phase ^= 1u;
         }
         if (++kb == w.kt) kb = 0;
       }
-      cp_wait<0>();
-      if (ok)
-        for (int u = max(0, b1 - b0 - kAhead); u < b1 - b0; ++u) announce();
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ sums

@@ -159,12 +159,56 @@ def test_rows_apart_and_off_alignment(rows, pad, shift, dtype):
 
 @pytest.mark.parametrize("rows, few", [(16, 1), (16, 8), (128, 1), (128, 17), (100, 16)])
 def test_a_row_by_itself_and_among_others(rows, few):
-    """A row's result depends on its own x and the matrix: any row, alone or in a block, has the same bits."""
+    """A row's result depends on its own x and the matrix: any row, alone or in a block, has the same bits (here on both
+    sides of 16 rows, as no row block of this matrix lies in runs of more than one block)."""
     c = Codes(700, 2176, 128, "f32", True, seed=8)
     x = torch.empty(rows, 2176, dtype=torch.bfloat16, device="cuda").normal_(generator=gen(9))
     whole = product(c, x)
     for at in (0, rows - few, (rows - few) // 2):
         assert torch.equal(product(c, x[at:at + few]), whole[at:at + few])
+
+
+@pytest.mark.parametrize("M, K, group", [(5000, 2560, 128), (300, 12288, 64)])
+@pytest.mark.parametrize("rows, few", [(16, 1), (16, 9), (128, 17), (65, 33)])
+def test_a_row_of_a_large_matrix_among_others(M, K, group, rows, few):
+    """Up to 16 rows, and from 17 on, the number of rows changes nothing in a row's bits, on matrices that many runs
+    share as well."""
+    c = Codes(M, K, group, "bf16", True, seed=15)
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda").normal_(generator=gen(16))
+    whole = product(c, x)
+    assert torch.equal(product(c, x[rows - few:]), whole[rows - few:])
+
+
+@pytest.mark.parametrize("rows, pad", [(1, 0), (16, 0), (16, 1), (40, 0), (40, 1), (128, 0)])
+def test_waits_that_run_out(rows, pad):
+    """With a limit of 0 every wait has run out before it begins; with a few microseconds some do, while copies and
+    products are in flight (rows of x on 16-byte boundaries come by other copies than rows off them).  The status says
+    so, nothing but the result is written, and the next call after the status is right."""
+    c = Codes(1500, 4096, 128, "bf16", True, seed=17)
+    x = torch.empty(rows, 4096 + pad, dtype=torch.bfloat16, device="cuda").normal_(generator=gen(18))[:, :4096]
+    ws = W4Workspace(rows)
+    buf = torch.full((rows * c.M + 1024,), 77.0, device="cuda")
+    out = buf[512:-512].view(rows, c.M)
+    c.w4.product(x, out, ws)
+    assert ws.status() == 0
+    want = out.clone()
+    ref, tol = bound(x, c.w, None, False, "bf16")
+    assert ((want.double() - ref).abs() <= tol).all()
+    try:
+        for ns in (0, 0, 20000, 5000, 2000, 500):
+            capi.dflash_debug_set_wait_limit(ns)
+            out.fill_(77.0)
+            c.w4.product(x, out, ws)
+            status = ws.status()
+            assert status in (0, capi.STATUS_TIMEOUT) and (ns or status)
+            if not status:
+                assert torch.equal(out, want)
+            capi.dflash_debug_set_wait_limit(-1)
+            c.w4.product(x, out, ws)
+            assert ws.status() == 0 and torch.equal(out, want)
+    finally:
+        capi.dflash_debug_set_wait_limit(-1)
+    assert (buf[:512] == 77.0).all() and (buf[-512:] == 77.0).all()
 
 
 def test_values_that_are_not_finite_stay_in_their_row():
