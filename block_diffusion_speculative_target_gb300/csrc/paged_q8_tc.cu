@@ -255,17 +255,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int et = tid - kGroup, kr = et / kLanes, kc16 = et % kLanes;
       const int hk = pc.hk, key_end = pc.key_end, seen_sink = pc.seen_sink, seen_lo = pc.seen_lo;
       const int32_t* trow = g.table + (long long)pc.b * g.table_stride;
-      // The page of the 16 keys 16 (lane % 4) .. of tile i (-1: no row sees one of them): asked for a tile before it is
-      // looked at.
+      // The page of the 16 keys 16 (lane % 4) .. of tile i (the pool's first where no row sees one of them): asked for a
+      // tile before it is looked at.
       auto key_of = [&](int i) { return pc.tile(i) * kKeys + 16 * (lane & 3); };
       auto page_of = [&](int i) {
-        if (i >= nt) return -1;
+        if (i >= nt) return 0;
         const int key = key_of(i);
-        return key >= key_end || (key >= seen_sink && key + 16 <= seen_lo) ? -1 : trow[key >> g.ps_log2];
+        return key >= key_end || (key >= seen_sink && key + 16 <= seen_lo) ? 0 : trow[key >> g.ps_log2];
       };
       // Tile i's codes: a lane of warp 6 brings 16 keys, their values and the scales of both.
-      // (Keys that no row sees, and those of a bad page: some row of the pool; what they hold is masked, or the
-      // sequence's result unspecified.)
+      // (Of a bad page: the pool's first rows; the sequence's result is unspecified.)
       auto fetch = [&](int i, int page) {
         asked = done + i + 1;
         if (lane == 0) mbar_arrive_expect_tx(&codes_full, 2 * kKeys * (HD + 4));
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           long long first = 0;  // the pool row of the 16 keys
           if ((unsigned)page < (unsigned)g.n_pages)
             first = g.page_row0 + ((long long)page * g.nkv + hk) * g.ps + (key_of(i) & (g.ps - 1));
-          else if (page != -1)
+          else
             set_status(g.status, DFLASH_STATUS_BOUNDS);
           uint8_t* codes = sm + L::kCodes + lane * 16 * HD;
           uint8_t* cs = sm + L::kCodeScales + lane * 64;
@@ -301,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       };
       constexpr uint32_t idS = idesc_f16_f32(128, kKeys), idO = idesc_f16_f32(128, HD) | (1u << 16);  // values MN-major
-      int next_page = -1;
+      int next_page = 0;
       if (warp == 6) {
         fetch(0, page_of(0));
         next_page = page_of(1);

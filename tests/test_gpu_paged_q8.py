@@ -363,6 +363,119 @@ def test_rows_that_read_as_nan_reach_only_those_that_see_them(n, dtype):
             t.copy_(keep[k])
 
 
+FAR = [  # heads, lens, n, kwargs: more sequences than a CTA has threads, lengths of every kind, items of every height
+    ("gqa4", [(7 * b) % 90 for b in range(300)], 1, {}), ("gqa4", [(13 * b) % 70 for b in range(150)], 16, {}),
+    ("mha64", [(5 * b) % 40 for b in range(260)], 3, dict(window=20, sinks=2)), ("mqa", [64 * b for b in range(9)], 3, {}),
+]
+
+
+@pytest.mark.parametrize("c", FAR, ids=[f"{c[0]}-{len(c[1])}-n{c[2]}" for c in FAR])
+def test_attention_of_many_sequences(c):
+    heads, lens, n, kw = c
+    x = Batch8("bf16", *HEADS[heads], 16, lens, n, fill=float("nan"))
+    q = x.query()
+    out = attend(x, q, **kw)
+    assert x.cache.status() == 0
+    check(x, out, reference(x, q, **kw), "many sequences")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 8, 33])
+def test_attention_reports_bad_pages(n, dtype):
+    """A page outside the pool: the status says so, and the other sequences' rows are what they were."""
+    x = Batch8(dtype, 4, 1, 128, 32, [500, 300, 200], n)
+    q = x.query()
+    want = attend(x, q)
+    for bad in (-1, x.pool["k"].shape[1], 2 ** 31 - 1, -2 ** 31):
+        good = int(x.table[1, 3])
+        x.table[1, 3] = bad
+        got = attend(x, q)
+        assert x.cache.status() == capi.STATUS_BOUNDS
+        x.table[1, 3] = good
+        assert torch.equal(got[[0, 2]], want[[0, 2]])
+        assert torch.equal(attend(x, q), want) and x.cache.status() == 0
+
+
+@pytest.mark.parametrize("n, shared", [(1, None), (16, None), (100, None), (40, 1920)])
+def test_attention_whose_waits_run_out(n, shared):
+    """With a limit of 0 every wait for copies and products has run out before it begins (calls of few rows have none).
+    The status says so, nothing but the result is written, and the next call after the status is right."""
+    x = Batch8("bf16", 8, 2, 128, 32, [2000, 2000, 2100], n, shared=shared or 0)
+    q = x.query()
+    buf = torch.full((q.numel() + 1024,), 77.0, dtype=x.dt, device="cuda")
+    out = buf[512:-512].view(q.shape)
+
+    def call():
+        x.cache.attention(0, q, x.table, x.len, out, shared_len=None if shared is None else i32([shared]))
+
+    call()
+    assert x.cache.status() == 0
+    want = out.clone()
+    check(x, want, reference(x, q), "before")
+    pool = {k: t.clone() for k, t in x.pool.items()}
+    try:
+        for ns in (0, 0, 20000, 2000, 300):
+            capi.dflash_debug_set_wait_limit(ns)
+            out.fill_(77.0)
+            call()
+            status = x.cache.status()
+            assert status in (0, capi.STATUS_TIMEOUT) and (ns or n == 1 or status)
+            if not status:
+                assert torch.equal(out, want)
+            capi.dflash_debug_set_wait_limit(-1)
+            call()
+            assert x.cache.status() == 0 and torch.equal(out, want)
+    finally:
+        capi.dflash_debug_set_wait_limit(-1)
+    assert all(torch.equal(t, pool[k]) for k, t in x.pool.items())
+    assert (buf[:512] == 77.0).all() and (buf[-512:] == 77.0).all()
+
+
+@pytest.mark.parametrize("n", [1, 9, 64])
+def test_value_scales_below_zero(n):
+    """A pool that another program filled may hold them; the entries are (u - 128) s all the same."""
+    x = Batch8("bf16", 4, 1, 128, 16, [300, 60], n)
+    x.pool["v_scale"].neg_().mul_(1e6)
+    x.pool["v_scale"][..., ::3] *= -1e-3
+    q = x.query()
+    check(x, attend(x, q), reference(x, q), "negative scales")
+
+
+@pytest.mark.parametrize("n", [1, 8, 40])
+def test_on_another_stream_and_replayed(n):
+    """Append, attention and reading back on a stream of their own and in a graph: the results of the plain calls."""
+    x = Batch8("bf16", 8, 2, 128, 64, [200, 63, 900], n)
+    q, out = x.query(), torch.zeros(3, n, 8, 128, dtype=x.dt, device="cuda")
+    qkv = x.normal(3, n, 12 * 128)
+    rows = torch.zeros(3, 2, n, 128, dtype=x.dt, device="cuda")
+    qr = torch.zeros_like(q)
+
+    def calls():
+        x.cache.append(0, qkv.view(3 * n, -1), x.table, x.len, n, q_out=qr)
+        x.cache.attention(0, qr, x.table, x.len, out)
+        x.cache.read(0, x.table, x.len, rows)
+
+    calls()
+    want = [t.clone() for t in (out, rows, qr)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for t in (out, rows, qr):
+            t.zero_()
+        calls()
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip((out, rows, qr), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for t in (out, rows, qr):
+        t.zero_()
+    graph.replay()
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip((out, rows, qr), want))
+    assert x.cache.status() == 0
+
+
 def test_refusals():
     x = Batch8("bf16", 4, 1, 128, 16, [30, 5], 4)
     c, q = x.cache, x.query()
