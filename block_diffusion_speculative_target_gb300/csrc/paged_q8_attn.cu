@@ -18,14 +18,15 @@
 // a key row, swizzled against bank conflicts, and the queries, scores and outputs
 // follow that order; nothing is shuffled between the two products.
 //
-// Four warps a CTA in RW groups of rows by 4 / RW groups of keys; a warp holds 16 MT
-// rows.  Groups of keys take the steps of a run in turn, each with its own ring of
-// stages (16-byte asynchronous copies) and its own running sums, so single tokens
-// run without a barrier; the groups' sums are joined at a piece's end.  The split
-// of a call over CTAs is that of paged.cuh, in tiles of 64 keys.
+// An item is 16 MT stacked rows, held by each of a CTA's four warps.  The warps take
+// the steps of a run in turn, each with its own ring of stages (16-byte asynchronous
+// copies) and its own running sums, so they run without a barrier; their sums are
+// joined at a piece's end.  The split of a call over CTAs is that of paged.cuh, in
+// tiles of 64 keys.
 //
 // Few rows are bound by the keys' bytes: 16 instructions a key and 16 rows, 9 of them
-// the codes' way to halves.  More rows share those in pairs of row tiles (MT = 2).
+// the codes' way to halves.  Up to 32 rows share those in pairs of row tiles (MT = 2);
+// more than 32 go to the kernel that expands a key once for 128 rows.
 #include <math.h>
 
 #include <algorithm>
@@ -42,16 +43,16 @@ constexpr int kQ8Threads = 128;
 constexpr int kQ8Keys = kPagedQ8Keys;
 constexpr int kStep = 16;     // keys of a step
 
-template <int HD, int MT, int RW>
+template <int HD, int MT>
 struct Q8Layout {
-  static constexpr int KW = 4 / RW;                       // groups of keys
-  static constexpr int kRows = 16 * MT * RW;
-  static constexpr int kStages = RW == 1 ? 4 : RW == 2 ? 6 : 8;
+  static constexpr int kWarps = kQ8Threads / 32;
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kStages = 4;
   static constexpr int kStage = 2 * kStep * HD + 2 * kStep * 4;  // codes of keys and values, their scales
-  static constexpr int kRing = KW * kStages * kStage;
+  static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kQRow = HD * 2 + 16;               // padded: 8 rows of 16 bytes fall into 32 banks
   static constexpr int kPer = (HD / 2 + 4) * 32;          // floats of a warp's sums of a row tile
-  static constexpr int kJoin = (KW - 1) * RW * MT * kPer * 4;  // those of the groups, over the ring
+  static constexpr int kJoin = (kWarps - 1) * MT * kPer * 4;  // those of the warps but the first, over the ring
   static constexpr int kRingEnd = kRing > kJoin ? kRing : kJoin;
   static constexpr int kQ = kRingEnd;
   static constexpr int kRf = kQ + kRows * kQRow;
@@ -120,27 +121,18 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 }
 }  // namespace
 
-template <int HD, int MT, int RW>
-__global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
+template <int HD, int MT>
+__global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
     paged_attn_q8_kernel(const __grid_constant__ PagedGeom g, const bf16* __restrict__ q,
                          const uint8_t* __restrict__ kp, const uint8_t* __restrict__ vp, bf16* __restrict__ out,
                          float scale_log2) {
-  typedef Q8Layout<HD, MT, RW> L;
-  constexpr int KW = L::KW, S = L::kStages, NT = HD / 8, KS = HD / 16;  // output tiles, steps of 16 dimensions
+  typedef Q8Layout<HD, MT> L;
+  constexpr int KW = L::kWarps, S = L::kStages, NT = HD / 8, KS = HD / 16;  // output tiles, steps of 16 dimensions
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
-  const int rw = warp % RW, kg = warp / RW;
   float* rfs = reinterpret_cast<float*>(smem + L::kRf);
-  uint8_t* ring = smem + kg * S * L::kStage;
+  uint8_t* ring = smem + warp * S * L::kStage;
   const uint32_t ring_u = smem_u32(ring);
-  auto group_sync = [&] {
-    if (RW == 1)
-      __syncwarp();
-    else if (RW == 4)
-      __syncthreads();
-    else
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * RW) : "memory");
-  };
   pdl_launch();
   pdl_wait();
   const PlanView pv = plan_view<kQ8Keys, kQ8Threads>(g, reinterpret_cast<int*>(smem + L::kRed));
@@ -192,13 +184,13 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
       }
     }
     __syncthreads();
-    // ------------------------------------------------------------ this warp's rows
+    // ------------------------------------------------------------ the rows
     const uint32_t q_at = smem_u32(smem + L::kQ) +
-                          (uint32_t)((rw * 16 * MT + (lane & 7) + 8 * ((lane >> 3) & 1)) * L::kQRow + 16 * (lane >> 4));
+                          (uint32_t)(((lane & 7) + 8 * ((lane >> 3) & 1)) * L::kQRow + 16 * (lane >> 4));
     const int key_lo = sg.prefix ? 0 : pv.sh_tiles * kQ8Keys;
     const int key_end = sg.prefix ? pv.sh_tiles * kQ8Keys : key_limit(g, sg.b);
-    const int4* spans = reinterpret_cast<const int4*>(smem + L::kSpan) + rw * 16 * MT + gr;
-    int all_lo = key_lo, all_hi = key_end;  // keys that every row of the warp sees
+    const int4* spans = reinterpret_cast<const int4*>(smem + L::kSpan) + gr;
+    int all_lo = key_lo, all_hi = key_end;  // keys that every row sees
     float rf[MT][2], m[MT][2], l[MT][2], f[MT][2];
     float o[MT][NT][4];
 #pragma unroll
@@ -208,7 +200,7 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
         const int4 v = spans[a * 16 + 8 * y];
         all_lo = max(all_lo, v.y);
         all_hi = min(all_hi, v.z);
-        rf[a][y] = rfs[(rw * MT + a) * 16 + gr + 8 * y];
+        rf[a][y] = rfs[a * 16 + gr + 8 * y];
         m[a][y] = -INFINITY;
         l[a][y] = 0.f;
         f[a][y] = 1.f;
@@ -226,16 +218,15 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
     row_span(g, sg.prefix ? pv.min_len : paged_len(g, sg.b), paged_rows(g, sg.b),
              sg.prefix ? 0 : div_g(g, sg.rt * g.ri), seen_sink, seen_lo, seen_hi);
     // ------------------------------------------------------------ the ring
-    const int steps = sg.nt * (kQ8Keys / kStep) / KW;  // of this group: kg, kg + KW, ..
+    const int steps = sg.nt * (kQ8Keys / kStep) / KW;  // of this warp: warp, warp + KW, ..
     auto first_key = [&](int j) {
-      const int s = j * KW + kg;
+      const int s = j * KW + warp;
       return sg.span.tile(sg.t0 + s / (kQ8Keys / kStep)) * kQ8Keys + s % (kQ8Keys / kStep) * kStep;
     };
     const int32_t* trow = g.table + (long long)sg.b * g.table_stride;
     int pages = -1;        // lane x: the page of step x of the 32 at hand (-1: none, or no row sees a key of it)
     uint32_t there = 0u;   // bit j % 32: step j has been asked for
-    const int l0 = rw * 32 + lane;
-    const uint32_t put0 = chunk_at<HD>(l0 / (HD / 16), l0 % (HD / 16));
+    const uint32_t put0 = chunk_at<HD>(lane / (HD / 16), lane % (HD / 16));
     uint32_t ask_slot = 0, slot = 0;
     auto ask = [&](int j) {
       if (j < steps) {
@@ -256,17 +247,15 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
           // (pool rows are below 2^31)
           const int row = (int)g.page_row0 + (page * g.nkv + sg.hk) * g.ps + (first_key(j) & (g.ps - 1));
           const uint32_t at = ring_u + ask_slot * L::kStage;
-          const long long src = (long long)row * HD + l0 * 16;
-          constexpr int kLoads = kStep * HD / 16 / (32 * RW);  // (0: half of the threads have one)
+          const long long src = (long long)row * HD + lane * 16;
 #pragma unroll
-          for (int x = 0; x < (kLoads > 0 ? kLoads : 1); ++x) {
-            if (kLoads == 0 && l0 >= kStep * HD / 16) break;
-            // row l0 / (HD / 16) + x 512 RW / HD: the swizzle changes with x only where 4 rows a load are 128 bytes each
-            const uint32_t to = at + (HD == 128 && RW == 1 && (x & 1) ? put0 ^ 64u : put0) + x * 512 * RW;
-            cp16(to, kp + src + x * 512 * RW);
-            cp16(to + kStep * HD, vp + src + x * 512 * RW);
+          for (int x = 0; x < kStep * HD / 512; ++x) {
+            // row lane / (HD / 16) + x 512 / HD: the swizzle changes with x only where 4 rows a load are 128 bytes each
+            const uint32_t to = at + (HD == 128 && (x & 1) ? put0 ^ 64u : put0) + x * 512;
+            cp16(to, kp + src + x * 512);
+            cp16(to + kStep * HD, vp + src + x * 512);
           }
-          if (l0 < 8) cp16(at + 2 * kStep * HD + l0 * 16, (l0 < 4 ? g.ks : g.vs) + row + 4 * (l0 & 3));
+          if (lane < 8) cp16(at + 2 * kStep * HD + lane * 16, (lane < 4 ? g.ks : g.vs) + row + 4 * (lane & 3));
         }
       }
       if (++ask_slot == S) ask_slot = 0;
@@ -277,7 +266,7 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
 #pragma unroll 1
     for (int j = 0; j < steps; ++j) {
       cp_wait<S - 2>();
-      group_sync();
+      __syncwarp();
       ask(j + S - 1);
       const uint8_t* kb = ring + slot * L::kStage;
       if (++slot == S) slot = 0;
@@ -367,7 +356,7 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
                 w[x] = pr * (hide ? 0.f : f[a][y] * vs[x]);
               }
               move |= fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > (none ? -INFINITY : 64.f);
-              move |= fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])) > 32768.f;
+              move |= fmaxf(fmaxf(fabsf(w[0]), fabsf(w[1])), fmaxf(fabsf(w[2]), fabsf(w[3]))) > 32768.f;
               p[a][y] = half2_of(w[0], w[1]);
               p[a][2 + y] = half2_of(w[2], w[3]);
             }
@@ -391,7 +380,7 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
               for (int x = 0; x < 4; ++x)
                 tm = fmaxf(tm, kMasked && (hidden >> (8 * a + 4 * y + x) & 1u)
                                    ? 0.f
-                                   : ex2f((z[x] - (has ? mn : 0.f)) * r) * vs[x]);
+                                   : ex2f((z[x] - (has ? mn : 0.f)) * r) * fabsf(vs[x]));
               tm = quad_max(tm);
               const float dm = first || !has ? 0.f : (mn - m[a][y]) * r;  // (in log2 units)
               const float want = tm > 0.f ? 8.f - log2f(tm) : 0.f;
@@ -484,55 +473,53 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT, RW>::kCtas))
           o[a][i][2 * y + 1] *= back;
         }
       }
-    if constexpr (KW > 1) {
-      __syncthreads();  // (the rings are free)
-      float* join = reinterpret_cast<float*>(smem);
-      constexpr int kPer = L::kPer;
-      if (kg > 0) {
+    __syncthreads();  // (the rings are free)
+    float* join = reinterpret_cast<float*>(smem);
+    constexpr int kPer = L::kPer;
+    if (warp > 0) {
 #pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          float* dst = join + (((kg - 1) * RW + rw) * MT + a) * kPer + lane;
+      for (int a = 0; a < MT; ++a) {
+        float* dst = join + ((warp - 1) * MT + a) * kPer + lane;
 #pragma unroll
-          for (int i = 0; i < NT * 4; ++i) dst[i * 32] = o[a][i >> 2][i & 3];
+        for (int i = 0; i < NT * 4; ++i) dst[i * 32] = o[a][i >> 2][i & 3];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            dst[(NT * 4 + y) * 32] = m[a][y];
-            dst[(NT * 4 + 2 + y) * 32] = l[a][y];
-          }
+        for (int y = 0; y < 2; ++y) {
+          dst[(NT * 4 + y) * 32] = m[a][y];
+          dst[(NT * 4 + 2 + y) * 32] = l[a][y];
         }
       }
-      __syncthreads();
-      if (kg == 0) {
+    }
+    __syncthreads();
+    if (warp == 0) {
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+      for (int a = 0; a < MT; ++a)
 #pragma unroll 1
-          for (int k = 0; k < KW - 1; ++k) {
-            const float* src = join + ((k * RW + rw) * MT + a) * kPer + lane;
-            float x0[2], x1[2];
+        for (int k = 0; k < KW - 1; ++k) {
+          const float* src = join + (k * MT + a) * kPer + lane;
+          float x0[2], x1[2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float m1 = src[(NT * 4 + y) * 32], l1 = src[(NT * 4 + 2 + y) * 32];
-              const float mn = fmaxf(m[a][y], m1);
-              x0[y] = m[a][y] == -INFINITY ? 0.f : ex2f(m[a][y] - mn);
-              x1[y] = m1 == -INFINITY ? 0.f : ex2f(m1 - mn);
-              l[a][y] = l[a][y] * x0[y] + l1 * x1[y];
-              m[a][y] = mn;
-            }
-#pragma unroll
-            for (int i = 0; i < NT * 4; ++i) {
-              const int y = (i & 3) >> 1;
-              o[a][i >> 2][i & 3] = o[a][i >> 2][i & 3] * x0[y] + src[i * 32] * x1[y];
-            }
+          for (int y = 0; y < 2; ++y) {
+            const float m1 = src[(NT * 4 + y) * 32], l1 = src[(NT * 4 + 2 + y) * 32];
+            const float mn = fmaxf(m[a][y], m1);
+            x0[y] = m[a][y] == -INFINITY ? 0.f : ex2f(m[a][y] - mn);
+            x1[y] = m1 == -INFINITY ? 0.f : ex2f(m1 - mn);
+            l[a][y] = l[a][y] * x0[y] + l1 * x1[y];
+            m[a][y] = mn;
           }
-      }
+#pragma unroll
+          for (int i = 0; i < NT * 4; ++i) {
+            const int y = (i & 3) >> 1;
+            o[a][i >> 2][i & 3] = o[a][i >> 2][i & 3] * x0[y] + src[i * 32] * x1[y];
+          }
+        }
     }
     const bool whole = walk.whole(sg);
-    if (kg == 0) {
+    if (warp == 0) {
 #pragma unroll
       for (int a = 0; a < MT; ++a)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const int r = (rw * MT + a) * 16 + gr + 8 * y;
+          const int r = a * 16 + gr + 8 * y;
           const ItemRow row = item_row(g, sg.prefix, sg.b, sg.hk, sg.rt * (sg.prefix ? g.rp : g.ri), r);
           if (!row.live) continue;
           // dimension 16 t + i of output tile i in column 2 t, and column 2 t + 1: 64 further (HD = 64: 8 further)
@@ -592,19 +579,19 @@ PagedRule paged_rule_q8(const PagedGeom& g) {
   return PagedRule{rows <= 16 ? 16 : 32, rows <= 16 ? 16 : 32, kQ8Keys, 1, 2};
 }
 
-template <int HD, int MT, int RW>
+template <int HD, int MT>
 static cudaError_t q8_launch(PagedGeom g, const void* q, const void* kp, const void* vp, void* out, long long part_rows,
                              cudaStream_t s) {
-  typedef Q8Layout<HD, MT, RW> L;
+  typedef Q8Layout<HD, MT> L;
   static_assert(L::kSmem * L::kCtas <= 232448, "shared memory per multiprocessor");
   static PerDevice smem;
   DFL_RET(smem.once([] {
-    return cudaFuncSetAttribute(paged_attn_q8_kernel<HD, MT, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    return cudaFuncSetAttribute(paged_attn_q8_kernel<HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   }));
   if (paged_split(g, paged_rule_q8(g), num_sms() * L::kCtas, 2) > part_rows || g.ri != L::kRows)
     return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
-  DFL_RET(launch_pdl(paged_attn_q8_kernel<HD, MT, RW>, dim3(g.grid), dim3(kQ8Threads), L::kSmem, s, g, (const bf16*)q,
+  DFL_RET(launch_pdl(paged_attn_q8_kernel<HD, MT>, dim3(g.grid), dim3(kQ8Threads), L::kSmem, s, g, (const bf16*)q,
                      (const uint8_t*)kp, (const uint8_t*)vp, (bf16*)out, scale_log2));
   count_launch();
   return g.shared ? paged_merge_q8(HD, g, out, s) : cudaSuccess;  // (else the CTAs join their pieces)
@@ -614,8 +601,8 @@ template <int HD>
 static cudaError_t q8_pick(const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
                            long long part_rows, cudaStream_t s) {
   const int rows = q8_stack(g);
-  return rows <= 16 ? q8_launch<HD, 1, 1>(g, q, kp, vp, out, part_rows, s)
-                    : q8_launch<HD, 2, 1>(g, q, kp, vp, out, part_rows, s);
+  return rows <= 16 ? q8_launch<HD, 1>(g, q, kp, vp, out, part_rows, s)
+                    : q8_launch<HD, 2>(g, q, kp, vp, out, part_rows, s);
 }
 
 cudaError_t paged_attention_q8(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
