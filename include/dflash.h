@@ -206,12 +206,14 @@ int dflash_status(dflash_workspace *w, dflash_stream_t stream, int32_t *status_o
 float *dflash_workspace_logits(dflash_workspace *w, int32_t which);
 /* Failure-path testing: sets the limit, in nanoseconds, of the waits in the
  * main loop of the weight-product kernel (ring slots and accumulator), of the
- * bf16 products with 4-bit weights and of the bf16 attention over pages, for launches enqueued afterwards; a negative
- * value restores the default of 500 ms.  A limit of 0 expires at once, so the
- * kernel gives up, sets DFLASH_STATUS_TIMEOUT, still waits (with the default
- * limit) for its copies and products in flight and returns; the weight product
- * writes no result, attention over pages an unspecified one.  Process-wide; not
- * an operation of the method. */
+ * bf16 products with 4-bit weights and of the bf16 attention over pages (of
+ * 8-bit ones: with more than 32 rows n * nq / nkv a sequence, or a batch with a
+ * shared length), for launches enqueued afterwards; a negative value restores
+ * the default of 500 ms.  A limit of 0 expires at once, so the kernel gives up,
+ * sets DFLASH_STATUS_TIMEOUT, still waits (whatever the limit) for its copies
+ * and products in flight and returns; the weight product writes no result, a
+ * 4-bit one at most some of it, attention over pages an unspecified one.
+ * Process-wide; not an operation of the method. */
 int dflash_debug_set_wait_limit(int64_t ns);
 const char *dflash_strerror(int code);
 
@@ -563,14 +565,16 @@ int dflash_paged_read(dflash_pages *p, int32_t layer, int32_t out_dtype, int32_t
  * at most 32 rows n * nq / nkv (with a shared length: the batch at most 16), and
  * rounded to bf16 once, 2^-8 of itself, beyond: there a block's row and the same
  * row as a single token may differ by 2^-8 of the attention of |values|, besides
- * their own rounding.  The keys are split over the GPU by all
+ * their own rounding.  Over 8-bit pages, whatever the rows, it enters as a half,
+ * with the values' scales, off by 2^-11 of itself; queries enter as halves, each
+ * row by a power of two, exact but for entries 2^25 below the row's largest.  The keys are split over the GPU by all
  * lengths of the call, so the last bits of a row may depend on the batch it is
  * in (dflash_attention, which fixes the split per cache, has no such
  * dependence); equal calls give equal bits.
  * DFLASH_ERR_TOO_LARGE: a table of more than 2^30 positions, or work that could
  * outgrow the plan's 32-bit numbers, (groups of rows) * nkv * (positions of a
  * table row, max_pos at most) / 64 in bf16 and / 32 in float32 at 2^30 or more.
- * A group holds up to 256 (float32: 64) of a sequence's n * nq / nkv rows; a
+ * A group holds up to 256 (float32: 64; 8-bit pages of bf16 models: 128) of a sequence's n * nq / nkv rows; a
  * shared prefix adds the groups of the whole batch's. */
 int dflash_paged_attention(dflash_pages *p, int32_t layer, const void *q, int32_t batch, int32_t n,
                            const int32_t *n_rows, int32_t causal, int32_t window, int32_t sinks,
@@ -649,7 +653,9 @@ int dflash_w4_status(dflash_w4_workspace *ws, dflash_stream_t stream, int32_t *s
  * Codes less zero points are small integers, exact in bf16; products are summed
  * in float32 and the scale is applied to a group's sum, so the only roundings are
  * float32's.  A row's result depends on its own x and the matrix only, and equal
- * calls give equal bits. */
+ * calls give equal bits; in bf16 neither do the other rows' number and values change
+ * its bits up to 16 rows, nor from 17 on (between the two, and in float32, sums are
+ * taken in other orders). */
 int dflash_linear_w4(int32_t dtype, const void *x, int64_t ldx, const dflash_w4 *w, const float *add,
                      int32_t swiglu, void *y, int32_t rows, dflash_w4_workspace *ws, dflash_stream_t stream);
 
