@@ -367,6 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The row block ends here, or the run does.  A warp deals with its 32 rows by itself.
       w4_join<V, 4>(w, run, tile, r, acc, [&](int v0, const float (&sum)[4][4]) {
         if (4 * v0 >= rows) return;
+        // what is added to the later rows comes closer meanwhile
+        if (epi.add && v0 == 0 && tile * kW4Tile + r - lane < w.M)
+          for (int n = 16 + lane; n < rows; n += 32) l2_prefetch(epi.add + (long long)n * w.M + tile * kW4Tile + r - lane);
         float* sums = sums_s[warp - 4];  // 16 columns at a time
 #pragma unroll
         for (int n = 0; n < 16; ++n) sums[n * kW4SumRow + lane] = sum[n / 4][n % 4];
