@@ -204,6 +204,40 @@ def test_append_of_rows_that_are_not_finite(hd):
     assert torch.equal(got[1][0][~bad], got[0][0][~bad])
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_rounds_ties_to_even(hd, dtype):
+    """Quotients at a tie and a step of float32 to its sides, at scales of powers of two and others, down to those below
+    the normal numbers: the codes of the stated rule, value for value (values are not rotated, scales are seen)."""
+    tops = [127.0, 127.0 * 2.0 ** -100, 127.0 * 2.0 ** 100, 127.0 * 2.0 ** -135, 2.0 ** -140, 3.7, 1e-20, 1e20, 0.0]
+    n = 3 * len(tops)
+    x = Batch8(dtype, 1, 1, hd, 32, [0], n)
+    half = torch.arange(hd, device="cuda") * 2 - (hd - 1)  # odd numbers
+    half = half.clamp(-253, 253).double() / 2  # ties: j + 1 / 2
+    rows = []
+    for top in tops:
+        s = float(torch.tensor(top, dtype=torch.float32).double().div(127).float())
+        v = (half * s).float()
+        up, down = torch.full_like(v, math.inf), torch.full_like(v, -math.inf)
+        for y in (v, torch.nextafter(v, up), torch.nextafter(v, down)):
+            y = y.clamp(-top, top)
+            y[0] = top
+            rows.append(y)
+    v = torch.stack(rows)
+    qkv = torch.zeros(n, 3 * hd, device="cuda")
+    qkv[:, 2 * hd:] = v
+    x.cache.append(0, qkv, x.table, x.len, n, q_out=torch.zeros(1, n, 1, hd, dtype=x.dt, device="cuda"))
+    assert x.cache.status() == 0
+    p = torch.arange(n, device="cuda")
+    page = x.table[0].long()[p // 32]
+    got, gs = x.pool["v"][0][page, 0, p % 32], x.pool["v_scale"][0][page, 0, p % 32]
+    s = (v.abs().amax(1).double() / 127).float()
+    assert torch.equal(gs, s)
+    # (the quotient in 64 bits, rounded, is float32's own; a row of zeros holds 128)
+    q = (v.double() / torch.where(s > 0, s, torch.ones_like(s)).double()[:, None]).float()
+    assert torch.equal(got.double(), torch.round(q).clamp(-127, 127).double() + 128)
+
+
 def test_append_reports_capacity_and_bad_pages():
     x = Batch8("bf16", 4, 1, 128, 16, [30, 5], 4)
     qkv = x.normal(8, 6 * 128)
