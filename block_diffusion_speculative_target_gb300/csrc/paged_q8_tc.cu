@@ -12,8 +12,8 @@
 //   pages -> codes in shared memory by bulk copies of 16 keys (one tile ahead; the
 //            pages' numbers two ahead)
 //         -> halves in shared memory, K once and V in two buffers, swizzled
-//   S = Q K^T   128 rows by 64 keys in TMEM
-//   O += P V    P as halves in TMEM, O in TMEM
+//   S = Q K^T   128 rows by 64 keys in TMEM, two buffers
+//   O += P V    P as halves over the scores they come from, O in TMEM
 // so a key's codes are expanded once for all rows.  Warps 0..3 take the exponentials,
 // a row a thread; warps 4..7 fetch and expand the next tile meanwhile, and two of them
 // issue the products.  Two CTAs share an SM.  The split of a call over CTAs is that of
@@ -121,12 +121,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                             float scale_log2) {
   typedef Q8TcLayout<HD> L;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  // kv_full: a tile's keys and values are expanded (4 warps).  s_done: its scores are there.  s_free: and have been
-  // read (4 warps; so all have waited for s_done).  p_full: its weights are there (4 warps, which have waited for the
-  // last pv_done).  pv_done: their product with the values is done; it is asked for after p_full and the next tile's
-  // kv_full, whose warps have waited for the one before it.
+  // kv_full: a tile's keys and values are expanded (4 warps, which have waited for the last scores and for the pv_done
+  // of two tiles before).  s_done: its scores are there, in buffer T % 2; the next ones of a buffer are asked for after
+  // the kv_full of two tiles on, so after all have waited for these.  p_full: its weights are there (4 warps, which
+  // have waited for the last pv_done).  pv_done: their product with the values is done; it is asked for after p_full
+  // and the next tile's kv_full, whose warps have waited for the one before it.
   // codes_full: a tile's codes are there.  codes_free: and have been read (4 warps; so all have waited for codes_full).
-  __shared__ __align__(8) uint64_t kv_full, s_done, s_free, p_full, pv_done, codes_full, codes_free, drain[2];
+  __shared__ __align__(8) uint64_t kv_full, s_done[2], p_full, pv_done, codes_full, codes_free, drain[2];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_s;
   __shared__ Q8Piece pc;
@@ -136,8 +137,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   int4* spans = reinterpret_cast<int4*>(sm + L::kSpan);
   if (tid == 0) {
     mbar_init(&kv_full, 4);
-    mbar_init(&s_done, 1);
-    mbar_init(&s_free, 4);
+    mbar_init(&s_done[0], 1);
+    mbar_init(&s_done[1], 1);
     mbar_init(&p_full, 4);
     mbar_init(&pv_done, 1);
     mbar_init(&codes_full, 1);
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot, tO = tmem, tS = tmem + 128, tP = tmem + 192;
+  const uint32_t tmem = tmem_slot, tO = tmem, tS = tmem + 128;  // scores of tile T (and its weights): 64 T % 2 further
   pdl_launch();
   pdl_wait();
   const PlanView pv = plan_view<kKeys, kThreads>(g, reinterpret_cast<int*>(sm + L::kRed));
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           // the last scores have been computed; the buffer's last values and scales have been read (the piece before has
           // ended)
-          if (i >= 1 && !wait(&s_done, T - 1)) break;
+          if (i >= 1 && !wait(&s_done[(T - 1) & 1], (T - 1) >> 1)) break;
           expand(kc, sm + L::kK);
           if (i >= 2 && !wait(&pv_done, T - 2)) break;
           expand(vc, sm + L::kV + (T & 1) * L::kTile);
@@ -334,15 +335,15 @@ __global__ void __launch_bounds__(kThreads, 2)
           arrive(&kv_full);
         }
         if (warp == 4 && i < nt) {
-          if (!wait(&kv_full, T) || (i > 0 && !wait(&s_free, T - 1))) break;
+          if (!wait(&kv_full, T)) break;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t dq = smem_desc_sw128(sm + L::kQ), dk = smem_desc_sw128(sm + L::kK);
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k)
-              tc_mma_f16(tS, dq + (uint64_t)((k >> 2) * (kRows * 128 / 16) + 2 * (k & 3)),
+              tc_mma_f16(tS + 64 * (T & 1), dq + (uint64_t)((k >> 2) * (kRows * 128 / 16) + 2 * (k & 3)),
                          dk + (uint64_t)((k >> 2) * (kKeys * 128 / 16) + 2 * (k & 3)), idS, k > 0);
-            tc_commit(&s_done);
+            tc_commit(&s_done[T & 1]);
           }
           __syncwarp();
         }
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t vt = smem_u32(sm + L::kV + ((T - 1) & 1) * L::kTile);
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
-              tc_mma_f16_tmem_a(tO, tP + 8 * k, smem_desc_mn(vt + k * 2048, kKeys * 128), idO,
+              tc_mma_f16_tmem_a(tO, tS + 64 * ((T - 1) & 1) + 8 * k, smem_desc_mn(vt + k * 2048, kKeys * 128), idO,
                                 i > 1 || k > 0);
             tc_commit(&pv_done);
           }
@@ -432,10 +433,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool ok = true;
       for (int i = 0; i < nt; ++i) {
         const int T = done + i;
-        if (!(ok = wait(&s_done, T))) break;
+        if (!(ok = wait(&s_done[T & 1], T >> 1))) break;
         tc_fence_after();
         if (idle) {  // (in step with the others: an arrival must not count for the phase before)
-          arrive(&s_free);
           if (i > 0 && !(ok = wait(&pv_done, T - 1))) break;
           arrive(&p_full);
           continue;
@@ -444,8 +444,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float* vs = ks + kKeys;
         const int k0 = pc.tile(i) * kKeys;
         uint32_t s[2][32];
-        tmem_ld32(tS + lanes, s[0]);
-        tmem_ld32(tS + 32 + lanes, s[1]);
+        const uint32_t ts = tS + 64 * (T & 1) + lanes;
+        tmem_ld32(ts, s[0]);
+        tmem_ld32(ts + 32, s[1]);
         // the largest scale of the tile's values (of hidden slots too: it only says when to look closer)
         const float va = fabsf(vs[lane]), vb = fabsf(vs[lane + 32]);
         const float vmax = __uint_as_float(__reduce_max_sync(
@@ -454,8 +455,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         // a hidden value's scale that is not finite would reach this row through its weight of 0
         const bool bad = !whole_tile && __any_sync(0xffffffffu, !(va < INFINITY && vb < INFINITY));
         tmem_ld_wait();
-        tc_fence_before();
-        arrive(&s_free);
         float2* z = reinterpret_cast<float2*>(s);
         const float2 rf2 = make_float2(rf, rf);
         const float4* ks4 = reinterpret_cast<const float4*>(ks);
@@ -487,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float zmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         const bool none = m == -INFINITY;
         const bool move = none ? zmax > -INFINITY : zmax - m > 64.f || ex2f(zmax - m) * (f * vmax) > 32768.f;
-        // the last weights have been multiplied: theirs are free, and the outputs' sums may be moved
+        // the last weights have been multiplied: the outputs' sums may be moved
         if (i > 0 && !(ok = wait(&pv_done, T - 1))) break;
         tc_fence_after();
         if (__any_sync(0xffffffffu, move)) {
@@ -552,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int y = 0; y < 16; ++y)
               p[y] &= (see[h] >> (2 * y) & 1u ? 0xffffu : 0u) | (see[h] >> (2 * y + 1) & 1u ? 0xffff0000u : 0u);
           }
-          tmem_st16(tP + 16 * h + lanes, p);
+          tmem_st16(ts + 16 * h, p);
         }
         l += sum.x + sum.y;
         tmem_st_wait();
