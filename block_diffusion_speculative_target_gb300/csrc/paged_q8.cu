@@ -60,7 +60,7 @@ __device__ __forceinline__ void put(T* p, const float (&x)[N]) {
 // that is not finite: 128 everywhere).  r = 1 / s rounded.  A quotient is at most 127 (1 + 2^-22), so x r is within
 // 127 2^-22 < 4e-5 of it and of the rounded quotient: where x r lies further than 1e-4 from a tie, its integer is
 // theirs.  The others, and rows whose scale is below the normal numbers, are divided.  (With 16 divisions a thread
-// they, not memory, were the bound: 16384 rows took 134 us where they take 115.)
+// they, not memory, were the bound: 16384 rows took 134 us where they then took 115.)
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, float r) {
   if (!(s > 0.f)) return make_uint2(0x80808080u, 0x80808080u);
   // added to an integer below 2^22 in size: the sum's low byte is the integer + 128
@@ -90,8 +90,14 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, float r) {
 // x_lo c - x_hi s with each operation rounded.  The hd / 16 threads of a head
 // exchange their maxima; a thread moves 8 entries of the lower half and the 8
 // they rotate with.
+//
+// Bound by its bytes in and out: 16384 bf16 rows of 40 + 8 + 8 heads of 128 and the
+// rows read back take 109 us for 74 us of bytes, 95 of them here (4.6 TB/s in all).
+// A thread has four heads' loads in flight where there are many rows; with bf16 rows
+// three blocks a multiprocessor (80 registers, a few spilled) are faster than two
+// (115 us), and two heads a thread no faster.  float32 rows need the registers.
 template <typename TI, typename T, int HPT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 3 : 2)
     paged_append_q8_kernel(const TI* __restrict__ qkv, long long ld, int vec, int rows, int n, int nq, int nkv, int hd,
                            int rpb, const int32_t* __restrict__ n_rows, const int32_t* __restrict__ table,
                            int table_stride, const int32_t* __restrict__ len, const float2* __restrict__ tab,
