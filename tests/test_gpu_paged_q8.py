@@ -510,6 +510,50 @@ def test_on_another_stream_and_replayed(n):
     assert x.cache.status() == 0
 
 
+@pytest.mark.parametrize("n", [1, 8, 40])
+def test_queries_that_are_not_finite_stay_in_their_row(n):
+    """A query row that holds an infinity or a NaN gives NaN in its head, and every other row what it gave before."""
+    x = Batch8("bf16", 8, 2, 128, 32, [300, 90, 700], n)
+    q = x.query()
+    want = attend(x, q)
+    bad = q.clone()
+    bad[0, 0, 3, 5], bad[1, n - 1, 6, 0], bad[2, n // 2, 1, 127] = math.inf, math.nan, -math.inf
+    got = attend(x, bad)
+    assert x.cache.status() == 0
+    for b, i, h in ((0, 0, 3), (1, n - 1, 6), (2, n // 2, 1)):
+        assert torch.isnan(got[b, i, h]).all()
+        got[b, i, h] = want[b, i, h]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pools_past_32_bits(dtype):
+    """Codes of more than 2^32 bytes: every call reaches the last pages."""
+    x = Batch8(dtype, 8, 8, 128, 128, [300, 50, 1000], 40, spare=36000)
+    assert x.pool["k"].numel() > 2 ** 32
+    x.table[0, :3] = torch.arange(3, device="cuda", dtype=torch.int32) + x.pool["k"].shape[1] - 3
+    for n in (1, 4, 40):
+        q = x.query()[:, :n].contiguous()
+        y = SimpleNamespace(**vars(x))
+        y.n, y.rows, y.keys = n, [n] * 3, x.keys
+        out = torch.zeros_like(q)
+        x.cache.attention(0, q, x.table, x.len, out)
+        check(y, out, reference(y, q), f"{n} rows")
+    back = torch.zeros(3, 8, 300, 128, device="cuda")
+    start = torch.zeros_like(x.len)
+    x.cache.read(0, x.table, start, back, n_rows=i32([300, 50, 300]))
+    assert torch.equal(back[0], x.keys(0, 300)[0].float())
+    qkv = x.normal(3, 24 * 128)
+    x.cache.append(0, qkv, x.table, x.len, 1, q_out=torch.zeros(3, 1, 8, 128, dtype=x.dt, device="cuda"))
+    page = int(x.table[0, 300 // 128])
+    v = qkv[0, 16 * 128:].view(8, 128).float()
+    s = (v.abs().amax(1).double() / 127).float()
+    assert torch.equal(x.pool["v_scale"][0, page, :, 300 % 128], s)
+    want = torch.round((v.double() / s.double()[:, None]).float()).double() + 128
+    assert torch.equal(x.pool["v"][0, page, :, 300 % 128].double(), want)
+    assert x.cache.status() == 0
+
+
 def test_refusals():
     x = Batch8("bf16", 4, 1, 128, 16, [30, 5], 4)
     c, q = x.cache, x.query()
