@@ -336,15 +336,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float s = w.scale_f32 ? reinterpret_cast<const float*>(scales)[at]
                                       : to_f<bf16>(reinterpret_cast<const bf16*>(scales)[at]);
           const uint32_t src = tD + db * part_columns + gp * N + lanes;
+          constexpr int kRead = N < 64 ? 32 : 64;  // columns read at once
 #pragma unroll
-          for (int c = 0; c < N; c += 32) {
-            uint32_t d[32];
-            tmem_ld32(src + c, d);
+          for (int c = 0; c < N; c += kRead) {
+            uint32_t d[kRead / 32][32];
+#pragma unroll
+            for (int h = 0; h < kRead / 32; ++h) tmem_ld32(src + c + 32 * h, d[h]);
             tmem_ld_wait();
 #pragma unroll
-            for (int n = 0; n < 32; n += 2) {
+            for (int n = 0; n < kRead; n += 2) {
               float2& y = *reinterpret_cast<float2*>(&acc[(c + n) / 4][n % 4]);
-              y = fma2(make_float2(s, s), make_float2(__uint_as_float(d[n]), __uint_as_float(d[n + 1])), y);
+              y = fma2(make_float2(s, s),
+                       make_float2(__uint_as_float(d[n / 32][n % 32]), __uint_as_float(d[n / 32][n % 32 + 1])), y);
             }
           }
         }
