@@ -27,8 +27,8 @@
 // K and the GPU only, and no sum on the other rows of x: a row has the same bits
 // alone and in a block.
 //
-// Measured: 15 rows of 151936 x 5120 101 us (4.05 TB/s, the floor 60), 16 rows of
-// 24576 x 4096 with the activation 22.6 us (2.4 TB/s), one row of 4096 x 4096 7.4 us.
+// Measured: 15 rows of 151936 x 5120 100 us (4.1 TB/s, the floor 60), 16 rows of
+// 24576 x 4096 with the activation 22.3 us (2.4 TB/s), one row of 4096 x 4096 7.7 us.
 // Large matrices are bound by issue (59% of the slots) and by the latency that 16 warps a
 // multiprocessor leave open; small ones by a chain of trips to memory: first block, x,
 // partial sums, ticket, join.

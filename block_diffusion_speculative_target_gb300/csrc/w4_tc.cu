@@ -33,7 +33,7 @@
 //
 // Measured: 128 rows of 4096 x 12288, groups of 64, zero points, a residual added,
 // 48 us (266 TFLOP/s; 33 MB at 0.7 TB/s); without zero points in groups of 128 and
-// without the residual 35. Bound by latency, tensor pipe 15% and issue slots 27%
+// without the residual 33. Bound by latency, tensor pipe 15% and issue slots 27%
 // taken: a CTA's 21 blocks go one after another from codes to TMEM to products
 // to sums, and the CTA that ends a row block joins up to 6 pieces of 128 x 128 alone.
 //
