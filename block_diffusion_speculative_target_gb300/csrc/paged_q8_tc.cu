@@ -16,7 +16,7 @@
 //   O += P V    P as halves over the scores they come from, O in TMEM
 // so a key's codes are expanded once for all rows.  Warps 0..3 take the exponentials,
 // a row a thread; warps 4..7 fetch and expand the next tile meanwhile, and two of them
-// issue the products.  Measured: 128 rows behind 36K keys, 40 / 8 heads, 218 us (443
+// issue the products.  Measured: 128 rows behind 36K keys, 40 / 8 heads, 215 us (450
 // TFLOP/s, 23% of the products' floor); 8 blocks of 16 rows over 2K..6K keys, 32 / 8
 // heads, 58 us; 15-row blocks in a window of 4096 54 us.  Bound by latency: 38% of the
 // issue slots and 20% of the tensor pipe are taken, a tile takes a CTA about 2.6 us, and a
@@ -617,7 +617,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-PagedRule paged_rule_q8_tc() { return PagedRule{kRows, kRows, kKeys, 1, 2}; }
+// (An item's start and end weigh as three tiles in the split: as two, the chunk takes 218 us instead of 215; as six 213, but
+// 8 blocks of 16 rows 60 instead of 58.)
+PagedRule paged_rule_q8_tc() { return PagedRule{kRows, kRows, kKeys, 1, 3}; }
 
 template <int HD>
 static cudaError_t q8_tc_launch(PagedGeom g, const void* q, const void* kp, const void* vp, void* out,
