@@ -359,7 +359,9 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
                 const float pr = ex2f(e[x]);
                 sum[a][y] += pr;
                 const bool hide = kMasked && (hidden >> (8 * a + 4 * y + x) & 1u);
-                w[x] = pr * (hide ? 0.f : f[a][y] * vs[x]);
+                // (the scale first: a factor for small values, times the scale of a large one that has next to no
+                // weight, may be past float32)
+                w[x] = pr * (hide ? 0.f : vs[x]) * f[a][y];
               }
               move |= fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > (none ? -INFINITY : 64.f);
               move |= fmaxf(fmaxf(fabsf(w[0]), fabsf(w[1])), fmaxf(fabsf(w[2]), fabsf(w[3]))) > 32768.f;

@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int x = 0; x < 32; ++x) top[x & 3] = max3(top[x & 3], z[x].x, z[x].y);
         const float zmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         const bool none = m == -INFINITY;
-        const bool move = none ? zmax > -INFINITY : zmax - m > 64.f || ex2f(zmax - m) * (f * vmax) > 32768.f;
+        const bool move = none ? zmax > -INFINITY : zmax - m > 64.f || ex2f(zmax - m) * vmax * f > 32768.f;
         // the last weights have been multiplied: the outputs' sums may be moved
         if (i > 0 && !(ok = wait(&pv_done, T - 1))) break;
         tc_fence_after();
@@ -545,13 +545,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int y = 0; y < 8; ++y) {
             const int x = 8 * h + y;
             const float4 v4 = vs4[x];
-            const float2 va2 = mul2(make_float2(v4.x, v4.y), f2), vb2 = mul2(make_float2(v4.z, v4.w), f2);
             float2 a = add2(z[2 * x], off2), b = add2(z[2 * x + 1], off2);
             a = make_float2(ex2f(a.x), ex2f(a.y));
             b = make_float2(ex2f(b.x), ex2f(b.y));
             sum = add2(sum, add2(a, b));
-            a = mul2(a, va2);
-            b = mul2(b, vb2);
+            // (the scale first: a hidden key's weight of 0 stays 0 whatever finite scale its slot holds, where the scale
+            // times the factor may be past float32)
+            a = mul2(mul2(a, make_float2(v4.x, v4.y)), f2);
+            b = mul2(mul2(b, make_float2(v4.z, v4.w)), f2);
             p[2 * y] = half2_of(a.x, a.y);
             p[2 * y + 1] = half2_of(b.x, b.y);
           }

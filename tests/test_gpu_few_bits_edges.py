@@ -1,0 +1,118 @@
+"""8-bit pages and 4-bit weights where their ranges end: value rows of zero before others, slots that hold anything,
+scales far from one another, matrices whose range float32 cannot hold; against 64-bit arithmetic."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_paged import CASES, HEADS, TDT, visible  # noqa: E402
+from test_gpu_paged_q8 import SHARED, Batch8, attend, check, reference, untouched  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+# What a weight, with its value's scale, is off by when it enters the product with the values in bf16 models.
+WEIGHT = 2.0 ** -11
+
+
+def near(x, q, got, causal=True, window=0, sinks=0, weight=WEIGHT):
+    """Each live row against 64 bits.  A rounding of float32 is u = 2^-24.  A score is a sum of hd products, which may
+    be cut instead of rounded (2 u each), times two scales: a weight is off by (2 hd + 4) u times the sum of the
+    |q k|, and by 4 u of the exponential, relative, in the numerator and in the sum that divides it; the two sums
+    over the keys by 2 u a key.  bf16: the weights with the values' scales are off by `weight` of themselves, or, below
+    half's normal numbers, by 2^-25 under a factor that brings the row's largest to 2^7 at least: 2^-32 of the largest
+    weight times value, a key; and the result is rounded once, 2^-8 of itself."""
+    G, u = x.nq // x.nkv, 2.0 ** -24
+    assert torch.isfinite(got).all(), "a value is not finite"
+    for b, (P, r) in enumerate(zip(x.lens, x.rows)):
+        r = min(max(r, 0), x.n)
+        if not r:
+            continue
+        k, v = x.keys(b, P + r)
+        for i in range(r):
+            see = visible(P, r, i, causal, window, sinks, P + r)
+            kk, vv = k[:, see], v[:, see]
+            a = q[b, i].double().view(x.nkv, G, x.hd)
+            p = torch.softmax(a @ kk.transpose(1, 2) / math.sqrt(x.hd), -1)
+            want, mag = p @ vv, p @ vv.abs()
+            dots = (a.abs() @ kk.abs().transpose(1, 2)).amax(-1, keepdim=True) / math.sqrt(x.hd)
+            keys = kk.shape[1]
+            tol = mag * u * (2 * ((2 * x.hd + 4) * dots + 4) + 4 * keys + 16)
+            if x.dtype == "bf16":
+                top = (p * vv.abs().amax(-1)[:, None]).amax(-1, keepdim=True)
+                tol = tol + weight * mag + 2.0 ** -32 * keys * top
+                tol = tol + 2.0 ** -8 * (want.abs() + tol) + 2.0 ** -134  # (bf16's least step is 2^-133)
+            off = (got[b, i].double().view(x.nkv, G, x.hd) - want).abs() - tol
+            assert float(off.max()) <= 0, f"row {i} of sequence {b}: {float(off.max()):.3e} more than its bound"
+
+
+def lift(x, q, keys, by):
+    """Raises the scores of some positions of every sequence by `by` units of log2, whatever the other entries are: the
+    first entry of keys is 0 but there, and that of every query the same."""
+    x.pool["k"][..., 0] = 128
+    at = float(torch.tensor(by / (0.01 * 127 * 1.4426950408889634 / math.sqrt(x.hd))).to(x.dt))
+    for b, P in enumerate(x.lens):
+        p = torch.tensor([y for y in keys if y < P], dtype=torch.int64, device="cuda")
+        page = x.table[b].long()[p // x.ps]
+        x.pool["k"][0, page, :, p % x.ps, 0] = 255 if by > 0 else 1
+        x.pool["k_scale"][0, page, :, p % x.ps] = 0.01
+    q[..., 0] = abs(at)
+    return q
+
+
+def set_value_scale(x, keys, to):
+    for b, P in enumerate(x.lens):
+        p = torch.tensor([y for y in keys if y < P + x.n], dtype=torch.int64, device="cuda")
+        x.pool["v_scale"][0, x.table[b].long()[p // x.ps], :, p % x.ps] = to
+
+
+# ------------------------------------------------------------------ slots that hold anything, scales far apart
+
+
+@pytest.mark.parametrize("fill", [3e38, -1e36])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("c", CASES, ids=[f"{c[0]}-p{c[1]}-n{c[3]}-{max(c[2])}-{'c' if c[5] else 'f'}-w{c[6]}-s{c[7]}"
+                                          for c in CASES])
+def test_slots_that_hold_no_position(c, dtype, fill):
+    """Their scales are whatever the memory held: as large as float32 goes."""
+    heads, ps, lens, n, rows, causal, window, sinks = c
+    x = Batch8(dtype, *HEADS[heads], ps, lens, n, rows, fill=fill, extra_cols=3)
+    q = x.query()
+    kw = dict(causal=causal, window=window, sinks=sinks)
+    out = attend(x, q, **kw)
+    assert x.cache.status() == 0
+    untouched(x, out)
+    check(x, out, reference(x, q, **kw), "attention")
+
+
+@pytest.mark.parametrize("fill", [3e38, -1e36])
+@pytest.mark.parametrize("c", SHARED, ids=[f"{c[0]}-p{c[1]}-{c[2]}-n{c[4]}-w{c[7]}" for c in SHARED])
+def test_slots_that_hold_no_position_behind_a_shared_prefix(c, fill):
+    heads, ps, shared, behind, n, rows, causal, window, sinks = c
+    x = Batch8("bf16", *HEADS[heads], ps, [shared + y for y in behind], n, rows, fill=fill, shared=shared)
+    q = x.query()
+    kw = dict(causal=causal, window=window, sinks=sinks)
+    out = attend(x, q, shared=shared, **kw)
+    assert x.cache.status() == 0
+    untouched(x, out)
+    check(x, out, reference(x, q, **kw), "shared")
+
+
+@pytest.mark.parametrize("n", [1, 4, 8, 40])
+@pytest.mark.parametrize("at", [5, 40, 299])
+def test_a_large_value_with_next_to_no_weight(n, at):
+    """Values of 1e-28 and one of 1e12 whose score lies 200 log2 units below the others'."""
+    x = Batch8("bf16", 8, 2, 128, 32, [300, 90], n)
+    x.pool["v_scale"] *= 1e-30 / 0.03
+    set_value_scale(x, [at], 1e10)
+    q = lift(x, x.query(), [at], -200)
+    near(x, q, attend(x, q))
+
+
+@pytest.mark.parametrize("n", [1, 8, 40])
+def test_large_values_under_sharp_scores(n):
+    """Value rows with entries up to 2^100, scores that rise and fall by tens of log2 units from key to key."""
+    x = Batch8("bf16", 8, 2, 128, 32, [400, 90], n)
+    x.pool["v_scale"] *= 2.0 ** 93 / 0.03
+    q = x.query(scale=20.0)
+    near(x, q, attend(x, q))
