@@ -8,8 +8,9 @@
 // scaled by a power of two to a largest entry of 2^7..2^8 (exact but for entries
 // 2^25 below it).  The scales stay in float32: ks multiplies the scores, vs the
 // weights.  A weight enters the product with the values as half(2^(z - m) vs f),
-// f a factor of the row that keeps the largest one near 2^8 and all below 2^15:
-// off by 2^-11 of itself, whatever size the scales have.  m and f move only when a
+// f a factor of the row that keeps its largest weight between 2^7 and 2^15: off by
+// 2^-11 of itself or by 2^-25, whatever size the scales have down to 2^-112.  Values
+// of zero leave f at its most, so that the first other one sets it.  m and f move only when a
 // weight outgrows that range (or a score m by 64), which a vote finds; the sum of
 // weights is taken in float32 before vs and f.
 //
@@ -48,6 +49,7 @@ namespace {
 constexpr int kQ8Threads = 128;
 constexpr int kQ8Keys = kPagedQ8Keys;
 constexpr int kStep = 16;     // keys of a step
+constexpr float kFactorLog2 = 120.f;  // a row's factor lies within 2^-120 and 2^120
 
 template <int HD, int MT>
 struct Q8Layout {
@@ -391,16 +393,17 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
                                    : ex2f((z[x] - (has ? mn : 0.f)) * r) * fabsf(vs[x]));
               tm = quad_max(tm);
               const float dm = first || !has ? 0.f : (mn - m[a][y]) * r;  // (in log2 units)
-              const float want = tm > 0.f ? 8.f - log2f(tm) : 0.f;
-              // this step's weights are brought within 2^8; those before it keep their factor unless it has to fall
-              const float keep = first ? want : log2f(f[a][y]) + dm;
+              // this step's weights are brought within 2^8 (values of zero leave the factor at its most, so that the
+              // next ones set it); those before it keep their factor unless it has to fall
+              const float want = tm > 0.f ? 8.f - log2f(tm) : kFactorLog2, was = log2f(f[a][y]);
+              const float keep = first ? want : was + dm;
               const bool fall = !first && tm > 0.f && exp2f(fminf(keep, 126.f)) * tm > 32768.f;
-              const float to = fminf(fmaxf(fall ? want : keep, -120.f), 120.f);
+              const float to = fminf(fmaxf(fall ? want : keep, -kFactorLog2), kFactorLog2);
               const float os = first ? 1.f : exp2f(to - keep);
               if (has) {
                 l[a][y] *= ex2f(-dm);
                 m[a][y] = mn;
-                f[a][y] = exp2f(to);
+                if (to != was) f[a][y] = exp2f(to);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                   o[a][i][2 * y] *= os;

@@ -47,6 +47,7 @@ constexpr int kThreads = 256;
 constexpr int kGroup = 128;  // threads of the exponentials, and of the expansion
 constexpr int kKeys = kPagedQ8Keys;
 constexpr int kRows = 128;
+constexpr float kFactorLog2 = 120.f;  // a row's factor lies within 2^-120 and 2^120
 constexpr uint64_t kDrainNs = 125000000ull;
 
 template <int HD>
@@ -510,16 +511,17 @@ __global__ void __launch_bounds__(kThreads, 2)
             tm = max3(tm, ex2f(z[2 * x + 1].x - ref) * fabsf(v4.z), ex2f(z[2 * x + 1].y - ref) * fabsf(v4.w));
           }
           const float dm = none || !has ? 0.f : mn - m;
-          const float want = tm > 0.f ? 8.f - log2f(tm) : 0.f;
-          // this tile's weights are brought within 2^8; those before it keep their factor unless it has to fall
-          const float keep = none ? want : log2f(f) + dm;
+          // this tile's weights are brought within 2^8 (values of zero leave the factor at its most, so that the next
+          // ones set it); those before it keep their factor unless it has to fall
+          const float want = tm > 0.f ? 8.f - log2f(tm) : kFactorLog2, was = log2f(f);
+          const float keep = none ? want : was + dm;
           const bool fall = !none && tm > 0.f && exp2f(fminf(keep, 126.f)) * tm > 32768.f;
-          const float to = fminf(fmaxf(fall ? want : keep, -120.f), 120.f);
+          const float to = fminf(fmaxf(fall ? want : keep, -kFactorLog2), kFactorLog2);
           const float os = none ? 1.f : exp2f(to - keep);
           if (has) {
             l *= ex2f(-dm);
             m = mn;
-            f = exp2f(to);
+            if (to != was) f = exp2f(to);
           }
           if (i > 0 && __any_sync(0xffffffffu, has && os != 1.f)) {
             const float by = has ? os : 1.f;

@@ -116,3 +116,34 @@ def test_large_values_under_sharp_scores(n):
     x.pool["v_scale"] *= 2.0 ** 93 / 0.03
     q = x.query(scale=20.0)
     near(x, q, attend(x, q))
+
+
+# ------------------------------------------------------------------ value rows of zero
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 4, 8, 40])
+@pytest.mark.parametrize("zeros, value, up, kw", [
+    (16, 1e-3, 12, {}), (64, 1e-5, 12, {}), (130, 1e-6, 0, {}), (130, 0.02, 20, {}), (1, 0.02, 20, {}), (700, 1e-9, 3, {}),
+    (1, 0.02, 20, dict(window=900, sinks=1)), (1, 1e-6, 0, dict(window=300, sinks=1)),
+    (64, 1e-5, 6, dict(causal=False, window=500, sinks=64)), (2000, 0.02, 0, {})])
+def test_values_of_zero_before_others(n, zeros, value, up, kw, dtype):
+    """The first rows of a sequence hold values of zero (their scale is 0), the first key draws the most attention: the
+    later weights keep their bits, whatever the scales of their values are."""
+    x = Batch8(dtype, 8, 2, 128, 32, [2000, 300], n)
+    x.pool["v_scale"] *= value / 0.03
+    set_value_scale(x, range(zeros), 0.0)
+    q = lift(x, x.query(), [0], up)
+    near(x, q, attend(x, q, **kw), **kw)
+
+
+@pytest.mark.parametrize("n", [1, 8, 40])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_values_of_zero_behind_a_shared_prefix(n, hd):
+    """Pieces begin anywhere: zeros at the start of the prefix, and of the sequences' own keys."""
+    x = Batch8("bf16", 4, 2, hd, 16, [1000, 1300, 1001], n, shared=999)
+    x.pool["v_scale"] *= 1e-6 / 0.03
+    set_value_scale(x, range(200), 0.0)
+    set_value_scale(x, range(960, 1050), 0.0)
+    q = x.query()
+    near(x, q, attend(x, q, shared=999))
