@@ -575,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_after();
       if (ok && !idle) {
         const bool whole = pc.whole;
-        const float inv = whole ? 1.f / (f * l) : 1.f / f;
+        // (two quotients: a factor for tiny values times the sum may be past float32)
+        const float back = 1.f / f, inv = 1.f / l;
         bf16* dst = out + (((long long)mine.b * g.n + mine.i) * g.nq + mine.head) * HD;
         float* pdst = g.part_o + (pc.slot_row + tid) * HD;
 #pragma unroll 1
@@ -591,15 +592,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
-                  h[y] = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * y]) * inv, __uint_as_float(o[e + 2 * y + 1]) * inv);
+                  h[y] = __floats2bfloat162_rn(__uint_as_float(o[e + 2 * y]) * back * inv,
+                                               __uint_as_float(o[e + 2 * y + 1]) * back * inv);
                 *reinterpret_cast<uint4*>(dst + c + e) = v;
               }
             } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<float4*>(pdst + c + e) =
-                    make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                                __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                    make_float4(__uint_as_float(o[e]) * back, __uint_as_float(o[e + 1]) * back,
+                                __uint_as_float(o[e + 2]) * back, __uint_as_float(o[e + 3]) * back);
             }
           }
         }

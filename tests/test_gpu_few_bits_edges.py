@@ -147,3 +147,15 @@ def test_values_of_zero_behind_a_shared_prefix(n, hd):
     set_value_scale(x, range(960, 1050), 0.0)
     q = x.query()
     near(x, q, attend(x, q, shared=999))
+
+
+@pytest.mark.parametrize("n", [1, 8, 40])
+def test_scores_that_rise_after_tiny_values(n):
+    """Values of 1e-28 first, then, 24 log2 units above their scores, values of zero: the sum of weights times the factor
+    that brought the first ones into range is past float32."""
+    x = Batch8("bf16", 8, 2, 128, 32, [80], n, fill=0.0)
+    x.pool["v_scale"] *= 1e-30 / 0.03
+    keys = range(64, 80 + n)
+    set_value_scale(x, keys, 0.0)
+    q = lift(x, x.query(), keys, 24)
+    near(x, q, attend(x, q))
