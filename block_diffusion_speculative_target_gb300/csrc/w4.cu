@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(kPackWarps * 32)
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       }
       float s = w.zeros ? __fdiv_rn(hi - lo, 15.f) : __fdiv_rn(fmaxf(hi, -lo), 7.f);
+      // (a range past float32: its fifteenth is not)
+      if (w.zeros && hi - lo == INFINITY) s = (float)(((double)hi - (double)lo) / 15.0);
       if (!w.scale_f32) s = to_f<bf16>(from_f<bf16>(s));
       const int z = w.zeros && s > 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : kW4Zero;
       if (keeps(lane, gi)) {

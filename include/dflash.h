@@ -627,7 +627,7 @@ int dflash_w4_pack(const dflash_w4 *w, const void *codes, const void *scales, co
  * with them, over the range [min, max] stretched to hold 0, s = (max - min) / 15,
  * zero = rhe(-min / s) and code = rhe(w / s) + zero; s is rounded to the scale
  * type first and codes are clamped to 0..15 (rhe: round half to even; a group of
- * zeros has s = 0). */
+ * zeros has s = 0).  Entries up to 3e38 in size have finite nearest values. */
 int dflash_w4_quantize(const dflash_w4 *w, int32_t dtype, const void *src, int64_t ld, dflash_stream_t stream);
 /* dst [M][K] of type dtype: the values, rounded once. */
 int dflash_w4_unpack(const dflash_w4 *w, int32_t dtype, void *dst, dflash_stream_t stream);

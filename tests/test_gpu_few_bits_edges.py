@@ -6,6 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from block_diffusion_speculative_target_gb300.engine import W4Linear  # noqa: E402
 from test_gpu_paged import CASES, HEADS, TDT, visible  # noqa: E402
 from test_gpu_paged_q8 import SHARED, Batch8, attend, check, reference, untouched  # noqa: E402
 
@@ -159,3 +160,28 @@ def test_scores_that_rise_after_tiny_values(n):
     set_value_scale(x, keys, 0.0)
     q = lift(x, x.query(), keys, 24)
     near(x, q, attend(x, q))
+
+
+# ------------------------------------------------------------------ 4-bit weights
+
+
+@pytest.mark.parametrize("scales", ["bf16", "f32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_quantize_ranges_past_float32(dtype, scales, zeros):
+    """Entries of 2e38 of both signs: their range is past float32, a fifteenth of it is not.  The stated rule, value for
+    value, with the range taken in 64 bits."""
+    M, K, group = 130, 256, 64
+    g = torch.Generator(device="cuda").manual_seed(31)
+    src = ((torch.rand(M, K, dtype=torch.float64, device="cuda", generator=g) - 0.5) * 4e38).to(TDT[dtype])
+    src[0, 0], src[0, 1] = 2e38, -2e38
+    src[1] = src[1].abs()
+    got = W4Linear.from_weight(src, group, TDT[scales], zeros).weight()
+    x = src.double().view(M, K // group, group)
+    hi, lo = x.amax(-1).clamp(min=0), x.amin(-1).clamp(max=0)
+    s = ((hi - lo) / 15 if zeros else torch.maximum(hi, -lo) / 7).float().to(TDT[scales]).float()
+    # (a quotient in 64 bits, rounded, is float32's own)
+    z = torch.round((-lo / s.double()).float()).clamp(0, 15) if zeros else torch.full_like(s, 8.0)
+    code = (torch.round((x / s.double()[..., None]).float()) + z[..., None]).clamp(0, 15)
+    assert torch.isfinite(got).all()
+    assert torch.equal(got, ((code - z[..., None]) * s[..., None]).view(M, K))
