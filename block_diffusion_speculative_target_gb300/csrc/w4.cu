@@ -220,11 +220,22 @@ cudaError_t w4_unpack(const W4View& w, int dtype, void* dst, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------ split
-constexpr int kRunsPerSm = 4;
+constexpr int kMmaRuns = 4, kTcRuns = 1;  // runs an SM at most, up to kW4MmaRows rows and beyond
 constexpr int kMinRun = 4;  // blocks of a run at least
-int w4_max_runs() { return num_sms() * kRunsPerSm; }
-W4Run w4_run(const W4View& w, const W4Scratch& sc, int per_sm) {
-  const int blocks = (w.M + kW4Tile - 1) / kW4Tile * w.kt, most = num_sms() * std::min(per_sm, kRunsPerSm);
+static int runs_of(int rows) { return num_sms() * (rows <= kW4MmaRows ? kMmaRuns : kTcRuns); }
+static int padded(int rows) {
+  int n = 8;
+  while (n < rows) n *= 2;
+  return n;
+}
+int w4_max_runs() { return num_sms() * std::max(kMmaRuns, kTcRuns); }
+size_t w4_part_floats(int max_rows) {
+  const int few = std::min(max_rows, kW4MmaRows);
+  const size_t rows = std::max((long long)runs_of(few) * padded(few), (long long)runs_of(max_rows) * padded(max_rows));
+  return rows * 2 * kW4Tile;
+}
+W4Run w4_run(const W4View& w, const W4Scratch& sc, int rows) {
+  const int blocks = (w.M + kW4Tile - 1) / kW4Tile * w.kt, most = runs_of(rows);
   const int per = std::max(kMinRun, (blocks + most - 1) / most);
   return W4Run{blocks, per, (blocks + per - 1) / per, sc.part, sc.tickets, sc.status, wait_limit_ns()};
 }

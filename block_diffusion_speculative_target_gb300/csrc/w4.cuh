@@ -66,8 +66,8 @@ cudaError_t w4_unpack(const W4View& w, int dtype, void* dst, cudaStream_t s);
 cudaError_t w4_linear_core(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi,
                            cudaStream_t s);
 
-// Scratch of the tensor-core products: w4_max_runs() * 2 pieces of 128 by (rows, rounded up to a power of two, 8 at
-// least) floats; w4_max_runs() * 4 tickets, zero between calls; the status word.
+// Scratch of the tensor-core products: two pieces a run, of 128 by (rows, rounded up to a power of two, 8 at least)
+// floats; w4_max_runs() * 4 tickets, zero between calls; the status word.
 struct W4Scratch {
   float* part;
   int* tickets;
@@ -81,9 +81,12 @@ struct W4Run {
   int* status;
   unsigned long long wait_ns;
 };
-// `per_sm`: runs an SM at most, up to 4.
-W4Run w4_run(const W4View& w, const W4Scratch& sc, int per_sm);
+// Up to this many rows go to the kernel fed from registers, whose CTAs share an SM; more take one for themselves.
+constexpr int kW4MmaRows = 16;
+W4Run w4_run(const W4View& w, const W4Scratch& sc, int rows);
 int w4_max_runs();
+// Floats of partial sums that calls of up to max_rows rows need.
+size_t w4_part_floats(int max_rows);
 // bf16 x on the tensor cores, up to 16 rows: fed from registers; more: from TMEM and shared memory.
 cudaError_t w4_linear_mma(const W4View& w, const void* x, long long ldx, int rows, const W4Epi& epi,
                           const W4Scratch& sc, cudaStream_t s);

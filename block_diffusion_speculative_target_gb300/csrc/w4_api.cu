@@ -117,14 +117,12 @@ int dflash_w4_workspace_alloc(int32_t max_rows, dflash_w4_workspace** out) {
     delete ws;
     return record_cuda_error(e);
   }
-  int rows = 8;
-  while (rows < max_rows) rows *= 2;
   const size_t runs = (size_t)w4_max_runs();
   ws->ticket_bytes = runs * 4 * sizeof(int);
   struct Req {
     void** p;
     size_t bytes;
-  } reqs[] = {{(void**)&ws->sc.part, runs * 2 * kW4Tile * rows * sizeof(float)},
+  } reqs[] = {{(void**)&ws->sc.part, w4_part_floats(max_rows) * sizeof(float)},
               {(void**)&ws->sc.tickets, ws->ticket_bytes},
               {(void**)&ws->sc.status, sizeof(int)}};
   for (auto& r : reqs)
@@ -185,7 +183,7 @@ int dflash_linear_w4(int32_t dtype, const void* x, int64_t ldx, const dflash_w4*
   const W4Epi epi = {add, swiglu != 0, y};
   // 16 rows of 6144 x 4096: 11 us fed from registers, 15 through TMEM; 15 rows of 151936 x 5120: 100 and 198.  32 rows of
   // 4096 x 12288: 30 and 21.
-  if (dtype == DFLASH_BF16 && rows <= 16)
+  if (dtype == DFLASH_BF16 && rows <= kW4MmaRows)
     CK(w4_linear_mma(v, x, ldx, rows, epi, ws->sc, (cudaStream_t)stream));
   else if (dtype == DFLASH_BF16)
     CK(w4_linear_tc(v, x, ldx, rows, epi, ws->sc, (cudaStream_t)stream));

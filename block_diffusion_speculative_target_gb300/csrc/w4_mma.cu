@@ -286,7 +286,7 @@ cudaError_t mma_launch(const W4View& w, const bf16* x, long long ldx, int rows, 
     return cudaFuncSetAttribute(w4_mma_kernel<NT, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   }));
   const int vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx % 8 == 0;
-  const W4Run run = w4_run(w, sc, 4);
+  const W4Run run = w4_run(w, sc, rows);
   DFL_RET(launch_pdl(w4_mma_kernel<NT, GS>, dim3(run.runs), dim3(kThreads), L::kStages * (w.block_bytes + L::kX) + L::kSums,
                      s, w, run, x, ldx, vec, rows, epi));
   count_launch();

@@ -475,7 +475,7 @@ cudaError_t tc_launch(const W4View& w, const bf16* x, long long ldx, int rows, c
   const int vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx % 8 == 0;
   CUtensorMap tmx = {};
   if (vec && !make_rows_map(x, rows, w.K, ldx, N, &tmx)) return cudaErrorInvalidValue;
-  const W4Run run = w4_run(w, sc, 1);
+  const W4Run run = w4_run(w, sc, rows);
   W4Sums sums;
   sums.group_shift = w.group == 32 ? 0 : w.group == 64 ? 1 : 2;
   sums.part_shift = 0;

@@ -633,9 +633,10 @@ int dflash_w4_quantize(const dflash_w4 *w, int32_t dtype, const void *src, int64
 int dflash_w4_unpack(const dflash_w4 *w, int32_t dtype, void *dst, dflash_stream_t stream);
 
 /* Scratch of the products: partial sums for up to max_rows (<= 128) rows, whatever
- * the matrix (0.6 MB a row), and a status word.  Library-owned; bound to the device current
- * at the call; one workspace serves one stream at a time, and so do graphs
- * captured with it: graphs that may run at once need one each. */
+ * the matrix (0.6 MB a row up to 16 rows, 10 MB up to 64, 20 MB beyond), and a
+ * status word.  Library-owned; bound to the device current at the call; one
+ * workspace serves one stream at a time, and so do graphs captured with it:
+ * graphs that may run at once need one each. */
 typedef struct dflash_w4_workspace dflash_w4_workspace;
 int dflash_w4_workspace_alloc(int32_t max_rows, dflash_w4_workspace **out);
 int dflash_w4_workspace_free(dflash_w4_workspace *ws);

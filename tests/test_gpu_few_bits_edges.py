@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from block_diffusion_speculative_target_gb300.engine import W4Linear  # noqa: E402
+from block_diffusion_speculative_target_gb300.engine import W4Linear, W4Workspace  # noqa: E402
 from test_gpu_paged import CASES, HEADS, TDT, visible  # noqa: E402
 from test_gpu_paged_q8 import SHARED, Batch8, attend, check, reference, untouched  # noqa: E402
 
@@ -185,3 +185,27 @@ def test_quantize_ranges_past_float32(dtype, scales, zeros):
     code = (torch.round((x / s.double()[..., None]).float()) + z[..., None]).clamp(0, 15)
     assert torch.isfinite(got).all()
     assert torch.equal(got, ((code - z[..., None]) * s[..., None]).view(M, K))
+
+
+@pytest.mark.parametrize("rows", [8, 16, 17, 32, 64, 128])
+def test_workspace_holds_no_more_than_calls_use(rows):
+    """Partial sums: at most two pieces of 128 x rows floats a run; up to 16 rows a product takes four runs a
+    multiprocessor, more rows one.  Products at that many rows, and at 16, fit it side by side with its neighbours."""
+    torch.cuda.synchronize()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    free = torch.cuda.mem_get_info()[0]
+    many = [W4Workspace(rows) for _ in range(4)]
+    used = (free - torch.cuda.mem_get_info()[0]) / 4
+    padded = next(r for r in (8, 16, 32, 64, 128) if r >= rows)
+    assert used <= sms * 2 * 128 * max(4 * min(padded, 16), padded) * 4 + (6 << 20)  # (and what an allocation rounds up to)
+    g = torch.Generator(device="cuda").manual_seed(32)
+    w = W4Linear.from_weight(torch.empty(20000, 1024, device="cuda").normal_(generator=g))
+    dense = w.weight().double()
+    for r in sorted({rows, min(rows, 16), min(rows, 9)}):
+        x = torch.empty(r, 1024, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+        out = [torch.zeros(r, 20000, device="cuda") for _ in many]
+        for o, ws in zip(out, many):
+            w.product(x, o, ws)
+        want, mag = x.double() @ dense.T, x.double().abs() @ dense.abs().T
+        for o, ws in zip(out, many):
+            assert ((o.double() - want).abs() <= (1024 + 4) * 2.0 ** -23 * mag).all() and ws.status() == 0
