@@ -7,33 +7,36 @@
 // permutation and one packed subtraction.  The queries are half too, each row
 // scaled by a power of two to a largest entry of 2^7..2^8 (exact but for entries
 // 2^25 below it).  The scales stay in float32: ks multiplies the scores, vs the
-// weights.  A weight enters the product with the values as half(2^(z - m) vs f),
-// f a factor of the row that keeps its largest weight between 2^7 and 2^15: off by
-// 2^-11 of itself or by 2^-25, whatever size the scales have down to 2^-112.  Values
-// of zero leave f at its most, so that the first other one sets it.  m and f move only when a
-// weight outgrows that range (or a score m by 64), which a vote finds; the sum of
-// weights is taken in float32 before vs and f.
+// weights.  A weight enters the product with the values as a pair of halves, w =
+// 2^(z - m) vs f rounded and what that leaves: off by 2^-22 of itself, or by 2^-25, so
+// that the outputs' own rounding is what tells (one half alone is off by 2^-11, and the
+// outputs differed by 0.0009 from those of float32 weights, 0.0001 now).  f is a factor
+// of the row that keeps its largest weight between 2^7 and 2^15, whatever size the scales
+// have down to 2^-112; values of zero leave it at its most, so that the first other one
+// sets it.  m and f move only when a weight outgrows that range (or a score m by 64),
+// which a vote finds; the sum of weights is taken in float32 before vs and f.
 //
 // A step is 16 keys, always inside one page.  The products run over dimensions
 // and keys in the order that suits the loads: a lane takes 16 consecutive bytes of
 // a key row, swizzled against bank conflicts, and the queries, scores and outputs
 // follow that order; nothing is shuffled between the two products.
 //
-// An item is 16 MT stacked rows, held by each of a CTA's four warps.  The warps take
-// the steps of a run in turn, each with its own ring of stages (16-byte asynchronous
-// copies) and its own running sums, so they run without a barrier; their sums are
-// joined at a piece's end.  The split of a call over CTAs is that of paged.cuh, in
-// tiles of 64 keys.
+// An item is up to 32 stacked rows, held by each of a CTA's four warps.  Up to 8 leave
+// half of a row tile free: the second halves of the weights take it, and no product
+// is added for them.  The warps take the steps of a run in turn, each with its own ring
+// of stages (16-byte asynchronous copies) and its own running sums, so they run without
+// a barrier; their sums are joined at a piece's end.  The split of a call over CTAs is
+// that of paged.cuh, in tiles of 64 keys.
 //
-// Few rows are bound by the keys' bytes: 16 instructions a key and 16 rows, 9 of them
-// the codes' way to halves.  Up to 32 rows share those in pairs of row tiles (MT = 2);
-// more than 32 go to the kernel that expands a key once for 128 rows (8 blocks of 16
-// rows of 4 heads over 2K..6K keys: 58 us there, 83 here, with warps in groups by rows).
+// Few rows are bound by the keys' bytes and by issue, most of it the codes' way to
+// halves.  Up to 32 rows share that in pairs of row tiles; more go to the kernel that
+// expands a key once for 128 rows.
 //
-// Measured: 32 tokens over 0.5K..36K keys, 40 / 8 heads, 213 us for 1.12 GB: 5.3 TB/s,
-// 77% of the copy rate.  48% of the issue slots are taken by 12 warps a multiprocessor
-// (168 registers): what is left is the latency of a step's chain, codes to halves to
-// scores to weights to products.
+// Measured: 32 tokens over 0.5K..36K keys, 40 / 8 heads, 190 us for 1.12 GB: 5.9 TB/s,
+// 86% of the copy rate, 54% of the issue slots taken by 12 warps a multiprocessor (168
+// registers).  (With both halves of the row tile computed and one half a weight: 213.)
+// 8 blocks of 4 rows over 2K..6K keys, 32 / 8 heads, two products a tile of values:
+// 38 us; of 8 rows 54.
 #include <math.h>
 
 #include <algorithm>
@@ -51,23 +54,26 @@ constexpr int kQ8Keys = kPagedQ8Keys;
 constexpr int kStep = 16;     // keys of a step
 constexpr float kFactorLog2 = 120.f;  // a row's factor lies within 2^-120 and 2^120
 
-template <int HD, int MT>
+// ROWS: stacked rows of an item, 8, 16 or 32.
+template <int HD, int ROWS>
 struct Q8Layout {
   static constexpr int kWarps = kQ8Threads / 32;
-  static constexpr int kRows = 16 * MT;
+  static constexpr int kRows = ROWS;
+  static constexpr int kTiles = ROWS == 32 ? 2 : 1;  // of 16 rows
+  static constexpr int kHalves = ROWS == 8 ? 1 : 2;  // of a tile that hold rows
   static constexpr int kStages = 4;
   static constexpr int kStage = 2 * kStep * HD + 2 * kStep * 4;  // codes of keys and values, their scales
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kQRow = HD * 2 + 16;               // padded: 8 rows of 16 bytes fall into 32 banks
-  static constexpr int kPer = (HD / 2 + 4) * 32;          // floats of a warp's sums of a row tile
-  static constexpr int kJoin = (kWarps - 1) * MT * kPer * 4;  // those of the warps but the first, over the ring
+  static constexpr int kPer = (HD / 4 + 2) * kHalves * 32;  // floats of a warp's sums of a row tile
+  static constexpr int kJoin = (kWarps - 1) * kTiles * kPer * 4;  // those of the warps but the first, over the ring
   static constexpr int kRingEnd = kRing > kJoin ? kRing : kJoin;
   static constexpr int kQ = kRingEnd;
   static constexpr int kRf = kQ + kRows * kQRow;
   static constexpr int kSpan = kRf + kRows * 4;           // [rows] sink, lo, hi
   static constexpr int kRed = kSpan + kRows * 16;
   static constexpr int kSmem = kRed + (2 * kQ8Threads / 32 + 8) * 4;
-  static constexpr int kCtas = MT == 1 ? 3 : 2;
+  static constexpr int kCtas = ROWS <= 16 ? 3 : 2;
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -83,6 +89,11 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// The upper 8 rows of the tile are zero.
+__device__ __forceinline__ void ldsm2(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[2]) : "r"(addr) : "memory");
+  r[1] = r[3] = 0u;
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -109,6 +120,13 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// What rounding a pair of weights to the halves `hi` leaves.  (kInf: nothing where a half is infinite.)
+template <bool kInf>
+__device__ __forceinline__ uint32_t rest_of(float a, float b, uint32_t hi) {
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  if (kInf) return half2_of(isinf(h.x) ? 0.f : a - h.x, isinf(h.y) ? 0.f : b - h.y);
+  return half2_of(a - h.x, b - h.y);
+}
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -129,13 +147,14 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 }
 }  // namespace
 
-template <int HD, int MT>
-__global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, ROWS>::kCtas))
     paged_attn_q8_kernel(const __grid_constant__ PagedGeom g, const bf16* __restrict__ q,
                          const uint8_t* __restrict__ kp, const uint8_t* __restrict__ vp, bf16* __restrict__ out,
                          float scale_log2) {
-  typedef Q8Layout<HD, MT> L;
+  typedef Q8Layout<HD, ROWS> L;
   constexpr int KW = L::kWarps, S = L::kStages, NT = HD / 8, KS = HD / 16;  // output tiles, steps of 16 dimensions
+  constexpr int MT = L::kTiles, YS = L::kHalves;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
   float* rfs = reinterpret_cast<float*>(smem + L::kRf);
@@ -194,17 +213,18 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
     __syncthreads();
     // ------------------------------------------------------------ the rows
     const uint32_t q_at = smem_u32(smem + L::kQ) +
-                          (uint32_t)(((lane & 7) + 8 * ((lane >> 3) & 1)) * L::kQRow + 16 * (lane >> 4));
+                          (YS == 1 ? (uint32_t)((lane & 7) * L::kQRow + 16 * ((lane >> 3) & 1))
+                                   : (uint32_t)(((lane & 7) + 8 * ((lane >> 3) & 1)) * L::kQRow + 16 * (lane >> 4)));
     const int key_lo = sg.prefix ? 0 : pv.sh_tiles * kQ8Keys;
     const int key_end = sg.prefix ? pv.sh_tiles * kQ8Keys : key_limit(g, sg.b);
     const int4* spans = reinterpret_cast<const int4*>(smem + L::kSpan) + gr;
     int all_lo = key_lo, all_hi = key_end;  // keys that every row sees
-    float rf[MT][2], m[MT][2], l[MT][2], f[MT][2];
-    float o[MT][NT][4];
+    float rf[MT][YS], m[MT][YS], l[MT][YS], f[MT][YS];
+    float o[MT][NT][4];  // (YS == 1: the last two are the sums of the weights' second halves)
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < YS; ++y) {
         const int4 v = spans[a * 16 + 8 * y];
         all_lo = max(all_lo, v.y);
         all_hi = min(all_hi, v.z);
@@ -303,7 +323,10 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
           uint32_t x[4];
-          ldsm4(x, q_at + a * 16 * L::kQRow + s * 32);
+          if (YS == 1)
+            ldsm2(x, q_at + s * 32);
+          else
+            ldsm4(x, q_at + a * 16 * L::kQRow + s * 32);
 #pragma unroll
           for (int n = 0; n < 2; ++n)
             if (s == 0)
@@ -322,14 +345,14 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
         vs[x] = sc[kStep + kx[x]];
       }
       const bool part = k0 < all_lo || k0 + kStep > all_hi;
-      uint32_t p[MT][4];
+      uint32_t p[MT][4], pl[MT][4];  // weights: their first halves and (YS == 2) their second ones
       auto weights = [&](auto masked) {
         constexpr bool kMasked = decltype(masked)::value;
         uint32_t hidden = 0u;  // bit 8 a + 4 y + x
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4 * YS; ++i) {
             const int y = i >> 2, x = i & 3;
             const int4 see = kMasked ? spans[a * 16 + 8 * y] : make_int4(0, 0, 0, 0);
             float& z = c[a][x >> 1][2 * y + (x & 1)];
@@ -342,15 +365,16 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
               }
             }
           }
-        float sum[MT][2];
+        float sum[MT][YS];
         // Weights as the rows' references and factors have them; true if some row's have to move.  (Without a
         // reference every score that is seen makes one.)
-        auto weigh = [&] {
+        auto weigh = [&](auto again) {
+          constexpr bool kInf = decltype(again)::value;
           bool move = false;
 #pragma unroll
           for (int a = 0; a < MT; ++a)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < YS; ++y) {
               const bool none = m[a][y] == -INFINITY;
               const float off = none ? 0.f : -m[a][y] * rf[a][y];
               float w[4], e[4];
@@ -369,14 +393,17 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
               move |= fmaxf(fmaxf(fabsf(w[0]), fabsf(w[1])), fmaxf(fabsf(w[2]), fabsf(w[3]))) > 32768.f;
               p[a][y] = half2_of(w[0], w[1]);
               p[a][2 + y] = half2_of(w[2], w[3]);
+              uint32_t(&lo)[4] = YS == 1 ? p[a] : pl[a];
+              lo[YS == 1 ? 1 : y] = rest_of<kInf>(w[0], w[1], p[a][y]);
+              lo[YS == 1 ? 3 : 2 + y] = rest_of<kInf>(w[2], w[3], p[a][2 + y]);
             }
           return move;
         };
-        if (__any_sync(0xffffffffu, weigh())) {
+        if (__any_sync(0xffffffffu, weigh(std::false_type()))) {  // (an infinite weight too)
 #pragma unroll
           for (int a = 0; a < MT; ++a)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < YS; ++y) {
               float z[4], zm = -INFINITY;
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
@@ -405,18 +432,17 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
                 m[a][y] = mn;
                 if (to != was) f[a][y] = exp2f(to);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                  o[a][i][2 * y] *= os;
-                  o[a][i][2 * y + 1] *= os;
-                }
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                  for (int e = 0; e < 4 / YS; ++e) o[a][i][2 * y + e] *= os;
               }
             }
-          weigh();
+          weigh(std::true_type());
         }
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) l[a][y] += sum[a][y];
+          for (int y = 0; y < YS; ++y) l[a][y] += sum[a][y];
       };
       if (part)
         weights(std::true_type());
@@ -442,6 +468,10 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
             for (int a = 0; a < MT; ++a) {
               mma_f16(o[a][4 * d + 2 * h], p[a], b0, b1);
               mma_f16(o[a][4 * d + 2 * h + 1], p[a], b2, b3);
+              if (YS == 2) {
+                mma_f16(o[a][4 * d + 2 * h], pl[a], b0, b1);
+                mma_f16(o[a][4 * d + 2 * h + 1], pl[a], b2, b3);
+              }
             }
           }
         }
@@ -464,6 +494,10 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
             for (int a = 0; a < MT; ++a) {
               mma_f16(o[a][4 * d + 2 * h], p[a], b0, b1);
               mma_f16(o[a][4 * d + 2 * h + 1], p[a], b2, b3);
+              if (YS == 2) {
+                mma_f16(o[a][4 * d + 2 * h], pl[a], b0, b1);
+                mma_f16(o[a][4 * d + 2 * h + 1], pl[a], b2, b3);
+              }
             }
           }
         }
@@ -474,15 +508,14 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < YS; ++y) {
         l[a][y] = quad_sum(l[a][y]);
         m[a][y] = m[a][y] == -INFINITY ? -INFINITY : m[a][y] * rf[a][y];
         const float back = 1.f / f[a][y];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          o[a][i][2 * y] *= back;
-          o[a][i][2 * y + 1] *= back;
-        }
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) o[a][i][2 * y + e] = (YS == 1 ? o[a][i][e] + o[a][i][2 + e] : o[a][i][2 * y + e]) * back;
       }
     __syncthreads();  // (the rings are free)
     float* join = reinterpret_cast<float*>(smem);
@@ -492,11 +525,11 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
       for (int a = 0; a < MT; ++a) {
         float* dst = join + ((warp - 1) * MT + a) * kPer + lane;
 #pragma unroll
-        for (int i = 0; i < NT * 4; ++i) dst[i * 32] = o[a][i >> 2][i & 3];
+        for (int i = 0; i < NT * 2 * YS; ++i) dst[i * 32] = o[a][i / (2 * YS)][i % (2 * YS)];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          dst[(NT * 4 + y) * 32] = m[a][y];
-          dst[(NT * 4 + 2 + y) * 32] = l[a][y];
+        for (int y = 0; y < YS; ++y) {
+          dst[(NT * 2 * YS + y) * 32] = m[a][y];
+          dst[(NT * 2 * YS + YS + y) * 32] = l[a][y];
         }
       }
     }
@@ -507,10 +540,10 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
 #pragma unroll 1
         for (int k = 0; k < KW - 1; ++k) {
           const float* src = join + (k * MT + a) * kPer + lane;
-          float x0[2], x1[2];
+          float x0[YS], x1[YS];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float m1 = src[(NT * 4 + y) * 32], l1 = src[(NT * 4 + 2 + y) * 32];
+          for (int y = 0; y < YS; ++y) {
+            const float m1 = src[(NT * 2 * YS + y) * 32], l1 = src[(NT * 2 * YS + YS + y) * 32];
             const float mn = fmaxf(m[a][y], m1);
             x0[y] = m[a][y] == -INFINITY ? 0.f : ex2f(m[a][y] - mn);
             x1[y] = m1 == -INFINITY ? 0.f : ex2f(m1 - mn);
@@ -518,9 +551,10 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
             m[a][y] = mn;
           }
 #pragma unroll
-          for (int i = 0; i < NT * 4; ++i) {
-            const int y = (i & 3) >> 1;
-            o[a][i >> 2][i & 3] = o[a][i >> 2][i & 3] * x0[y] + src[i * 32] * x1[y];
+          for (int i = 0; i < NT * 2 * YS; ++i) {
+            const int e = i % (2 * YS), y = e >> 1;
+            float& sum = o[a][i / (2 * YS)][e];
+            sum = sum * x0[y] + src[i * 32] * x1[y];
           }
         }
     }
@@ -529,7 +563,7 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
 #pragma unroll
       for (int a = 0; a < MT; ++a)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
+        for (int y = 0; y < YS; ++y) {
           const int r = a * 16 + gr + 8 * y;
           const ItemRow row = item_row(g, sg.prefix, sg.b, sg.hk, sg.rt * (sg.prefix ? g.rp : g.ri), r);
           if (!row.live) continue;
@@ -584,27 +618,29 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, MT>::kCtas))
 // Stacked rows that one sequence's queries, or the batch's behind a shared prefix, make.
 static int q8_stack(const PagedGeom& g) { return (g.shared ? g.batch : 1) * g.n * g.G; }
 // Up to 32 rows a key's codes are expanded for one or two row tiles; beyond, once for 128 rows.  At 32 rows (8 sequences,
-// 2K..6K keys) 50 us here and 51 there, at 30 over 0.5K..36K keys 128 and 162; at 64 83 (in groups of warps) and 58.
+// 2K..6K keys) 54 us here and 58 there, at 30 over 0.5K..36K keys 147 and 179, at 16 38 and 56; at 64 83 (in groups of
+// warps, with one half a weight) and 63.
 constexpr int kFewRows = 32;
 PagedRule paged_rule_q8(const PagedGeom& g) {
   const int rows = q8_stack(g);
   if (rows > kFewRows) return paged_rule_q8_tc();
-  return PagedRule{rows <= 16 ? 16 : 32, rows <= 16 ? 16 : 32, kQ8Keys, 1, 2};
+  const int of = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  return PagedRule{of, of, kQ8Keys, 1, 2};
 }
 
-template <int HD, int MT>
+template <int HD, int ROWS>
 static cudaError_t q8_launch(PagedGeom g, const void* q, const void* kp, const void* vp, void* out, long long part_rows,
                              cudaStream_t s) {
-  typedef Q8Layout<HD, MT> L;
+  typedef Q8Layout<HD, ROWS> L;
   static_assert(L::kSmem * L::kCtas <= 232448, "shared memory per multiprocessor");
   static PerDevice smem;
   DFL_RET(smem.once([] {
-    return cudaFuncSetAttribute(paged_attn_q8_kernel<HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    return cudaFuncSetAttribute(paged_attn_q8_kernel<HD, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   }));
   if (paged_split(g, paged_rule_q8(g), num_sms() * L::kCtas, 2) > part_rows || g.ri != L::kRows)
     return cudaErrorInvalidValue;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)HD);
-  DFL_RET(launch_pdl(paged_attn_q8_kernel<HD, MT>, dim3(g.grid), dim3(kQ8Threads), L::kSmem, s, g, (const bf16*)q,
+  DFL_RET(launch_pdl(paged_attn_q8_kernel<HD, ROWS>, dim3(g.grid), dim3(kQ8Threads), L::kSmem, s, g, (const bf16*)q,
                      (const uint8_t*)kp, (const uint8_t*)vp, (bf16*)out, scale_log2));
   count_launch();
   return g.shared ? paged_merge_q8(HD, g, out, s) : cudaSuccess;  // (else the CTAs join their pieces)
@@ -614,8 +650,9 @@ template <int HD>
 static cudaError_t q8_pick(const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,
                            long long part_rows, cudaStream_t s) {
   const int rows = q8_stack(g);
-  return rows <= 16 ? q8_launch<HD, 1>(g, q, kp, vp, out, part_rows, s)
-                    : q8_launch<HD, 2>(g, q, kp, vp, out, part_rows, s);
+  return rows <= 8    ? q8_launch<HD, 8>(g, q, kp, vp, out, part_rows, s)
+         : rows <= 16 ? q8_launch<HD, 16>(g, q, kp, vp, out, part_rows, s)
+                      : q8_launch<HD, 32>(g, q, kp, vp, out, part_rows, s);
 }
 
 cudaError_t paged_attention_q8(int hd, const PagedGeom& g, const void* q, const void* kp, const void* vp, void* out,

@@ -6,25 +6,26 @@
 // The arithmetic is that of the kernel for few rows: codes less 128 are exact in
 // half precision, queries are half, each row scaled by a power of two, ks
 // multiplies the scores in float32, and a weight enters the product with the values
-// as half(2^(z - m) vs f), f a factor of the row that keeps the largest below 2^15.
+// as a pair of halves, 2^(z - m) vs f rounded and what that leaves (off by 2^-22 of
+// itself, or by 2^-25), f a factor of the row that keeps its largest weight between
+// 2^7 and 2^15.
 //
 // An item is up to 128 stacked rows.  A tile of 64 keys goes
 //   pages -> codes in shared memory by bulk copies of 16 keys (one tile ahead; the
 //            pages' numbers two ahead)
 //         -> halves in shared memory, K once and V in two buffers, swizzled
 //   S = Q K^T   128 rows by 64 keys in TMEM, two buffers
-//   O += P V    P as halves over the scores they come from, O in TMEM
+//   O += P V    P as two halves over the scores they come from, O in TMEM
 // so a key's codes are expanded once for all rows.  Warps 0..3 take the exponentials,
 // a row a thread; warps 4..7 fetch and expand the next tile meanwhile, and two of them
-// issue the products.  Measured: 128 rows behind 36K keys, 40 / 8 heads, 215 us (450
-// TFLOP/s, 23% of the products' floor); 8 blocks of 16 rows over 2K..6K keys, 32 / 8
-// heads, 58 us; 15-row blocks in a window of 4096 54 us.  Bound by latency: 38% of the
-// issue slots and 20% of the tensor pipe are taken, a tile takes a CTA about 2.6 us, and a
+// issue the products.  Measured: 128 rows behind 36K keys, 40 / 8 heads, 244 us (400
+// TFLOP/s, 20% of the products' floor); 8 blocks of 16 rows over 2K..6K keys, 32 / 8
+// heads, 63 us; 15-row blocks in a window of 4096 58 us.  Bound by latency: 39% of the
+// issue slots and 26% of the tensor pipe are taken, a tile takes a CTA about 2.9 us, and a
 // CTA's exponentials (a chain of TMEM load, scales, maximum, weights, TMEM store) cannot
-// begin before its scores nor end a tile before the next one's.  Exponentials alone,
-// in a copy of an earlier form without loads and products, took 183 us.  One group of 128 threads for
-// everything took 238, codes through registers instead of bulk copies 239, one buffer
-// of scores 228.
+// begin before its scores nor end a tile before the next one's.  The weights' second
+// halves cost 12% of the chunk (217 us without them).  Before them, one group of 128 threads for everything took 238 us,
+// codes through registers instead of bulk copies 239, one buffer of scores 228.
 // Two CTAs share an SM.  The split of a call over CTAs is that of
 // paged.cuh; pieces of items are joined by a second kernel.
 //
@@ -101,6 +102,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What rounding a pair of weights to the halves `hi` leaves.
+__device__ __forceinline__ uint32_t rest_of(float2 w, uint32_t hi) {
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  const float2 d = add2(w, make_float2(-h.x, -h.y));
+  return half2_of(d.x, d.y);
 }
 // 16 codes less 128 as halves: two 16-byte chunks.
 __device__ __forceinline__ void halves_of(const uint4& u, uint4 (&h)[2]) {
@@ -363,9 +370,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (elect_one()) {
             const uint32_t vt = smem_u32(sm + L::kV + ((T - 1) & 1) * L::kTile);
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              tc_mma_f16_tmem_a(tO, tS + 64 * ((T - 1) & 1) + 8 * k, smem_desc_mn(vt + k * 2048, kKeys * 128), idO,
-                                i > 1 || k > 0);
+            for (int k = 0; k < 2 * (kKeys / 16); ++k)  // the weights' first halves, then their second ones
+              tc_mma_f16_tmem_a(tO, tS + 64 * ((T - 1) & 1) + 8 * k,
+                                smem_desc_mn(vt + k % (kKeys / 16) * 2048, kKeys * 128), idO, i > 1 || k > 0);
             tc_commit(&pv_done);
           }
           __syncwarp();
@@ -463,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             0xffffffffu, max(va < INFINITY ? __float_as_uint(va) : 0u, vb < INFINITY ? __float_as_uint(vb) : 0u)));
         const bool whole_tile = k0 >= all_lo && k0 + kKeys <= all_hi;  // every row sees every key
         // a hidden value's scale that is not finite would reach this row through its weight of 0
-        const bool bad = !whole_tile && __any_sync(0xffffffffu, !(va < INFINITY && vb < INFINITY));
+        const bool bad = __any_sync(0xffffffffu, !(va < INFINITY && vb < INFINITY));
         tmem_ld_wait();
         float2* z = reinterpret_cast<float2*>(s);
         const float2 rf2 = make_float2(rf, rf);
@@ -542,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t p[16];
+          uint32_t p[16], rest[16];
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
             const int x = 8 * h + y;
@@ -557,13 +564,22 @@ __global__ void __launch_bounds__(kThreads, 2)
             b = mul2(mul2(b, make_float2(v4.z, v4.w)), f2);
             p[2 * y] = half2_of(a.x, a.y);
             p[2 * y + 1] = half2_of(b.x, b.y);
+            rest[2 * y] = rest_of(a, p[2 * y]);
+            rest[2 * y + 1] = rest_of(b, p[2 * y + 1]);
           }
           if (bad) {
 #pragma unroll
-            for (int y = 0; y < 16; ++y)
-              p[y] &= (see[h] >> (2 * y) & 1u ? 0xffffu : 0u) | (see[h] >> (2 * y + 1) & 1u ? 0xffff0000u : 0u);
+            for (int y = 0; y < 16; ++y) {
+              const uint32_t on = (see[h] >> (2 * y) & 1u ? 0xffffu : 0u) | (see[h] >> (2 * y + 1) & 1u ? 0xffff0000u : 0u);
+              // (an infinite weight leaves nothing)
+              const uint32_t fine = ((p[y] & 0x7c00u) != 0x7c00u ? 0xffffu : 0u) |
+                                    ((p[y] & 0x7c000000u) != 0x7c000000u ? 0xffff0000u : 0u);
+              p[y] &= on;
+              rest[y] &= on & fine;
+            }
           }
           tmem_st16(ts + 16 * h, p);
+          tmem_st16(ts + 32 + 16 * h, rest);
         }
         l += sum.x + sum.y;
         tmem_st_wait();

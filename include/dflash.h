@@ -565,9 +565,10 @@ int dflash_paged_read(dflash_pages *p, int32_t layer, int32_t out_dtype, int32_t
  * at most 32 rows n * nq / nkv (with a shared length: the batch at most 16), and
  * rounded to bf16 once, 2^-8 of itself, beyond: there a block's row and the same
  * row as a single token may differ by 2^-8 of the attention of |values|, besides
- * their own rounding.  Over 8-bit pages, whatever the rows, it enters as a half,
- * with the values' scales, off by 2^-11 of itself; queries enter as halves, each
- * row by a power of two, exact but for entries 2^25 below the row's largest.  The keys are split over the GPU by all
+ * their own rounding.  Over 8-bit pages, whatever the rows, it enters, with its
+ * value's scale, as a pair of halves, off by 2^-22 of itself or 2^-32 of the row's
+ * largest; queries enter as halves, each row by a power of two, exact but for
+ * entries 2^25 below the row's largest.  The keys are split over the GPU by all
  * lengths of the call, so the last bits of a row may depend on the batch it is
  * in (dflash_attention, which fixes the split per cache, has no such
  * dependence); equal calls give equal bits.

@@ -13,7 +13,7 @@ from test_gpu_paged_q8 import SHARED, Batch8, attend, check, reference, untouche
 pytestmark = pytest.mark.gpu
 
 # What a weight, with its value's scale, is off by when it enters the product with the values in bf16 models.
-WEIGHT = 2.0 ** -11
+WEIGHT = 2.0 ** -22
 
 
 def near(x, q, got, causal=True, window=0, sinks=0, weight=WEIGHT):
@@ -209,3 +209,39 @@ def test_workspace_holds_no_more_than_calls_use(rows):
         want, mag = x.double() @ dense.T, x.double().abs() @ dense.abs().T
         for o, ws in zip(out, many):
             assert ((o.double() - want).abs() <= (1024 + 4) * 2.0 ** -23 * mag).all() and ws.status() == 0
+
+
+# ------------------------------------------------------------------ the bits of a weight
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 4, 8, 40])
+@pytest.mark.parametrize("shared", [None, 64])
+def test_weights_keep_their_bits(n, hd, shared):
+    """Queries of zero, so that all keys weigh the same, and values that cancel but for 2^-12: the even positions hold
+    +127 c in every entry, the odd ones -127 c (1 + 2^-12).  A weight of one half would round the difference away."""
+    x = Batch8("bf16", 8, 2, hd, 16, [59, 64] if shared is None else [64, 70], n, shared=shared or 0)
+    for b, P in enumerate(x.lens):
+        p = torch.arange(P + n, device="cuda")
+        page = x.table[b].long()[p // 16]
+        odd = (p % 2).bool()
+        x.pool["v"][0, page, :, p % 16] = torch.where(odd, 1, 255).to(torch.uint8)[:, None, None]
+        x.pool["v_scale"][0, page, :, p % 16] = torch.where(odd, 0.01 * (1 + 2.0 ** -12), 0.01)[:, None]
+    q = torch.zeros(2, n, 8, hd, dtype=x.dt, device="cuda")
+    near(x, q, attend(x, q, shared=shared))
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 8, 40])
+def test_an_infinite_value(n):
+    """A pool that another program filled may hold a value scale of Inf: the rows that see it are infinite, others are
+    what they were."""
+    x = Batch8("bf16", 8, 2, 128, 32, [100, 90], n)
+    q = x.query()
+    want = attend(x, q)
+    at = 100 + n // 2
+    page, slot = int(x.table[0, at // 32]), at % 32
+    x.pool["v"][0, page, :, slot] = torch.where(torch.arange(128, device="cuda") % 2 == 0, 200, 3).to(torch.uint8)
+    x.pool["v_scale"][0, page, :, slot] = math.inf
+    got = attend(x, q)
+    assert (got[0, n // 2:, :, 0::2] == math.inf).all() and (got[0, n // 2:, :, 1::2] == -math.inf).all()
+    assert torch.equal(got[0, :n // 2], want[0, :n // 2]) and torch.equal(got[1], want[1])
