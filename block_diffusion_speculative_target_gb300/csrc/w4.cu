@@ -45,8 +45,13 @@ unsigned warp_tiles(const W4View& w) {
 }
 }  // namespace
 
-// (Packing and quantising do not let the next kernel start before their end: products read weights ahead of their
-// own wait.)
+// Products read weights ahead of their own wait for the kernels before them, by bulk copies.  So packing and quantising
+// do not let the next kernel start before their end, and each thread makes its stores visible to such copies before
+// its own: a kernel that starts behind the trigger which the end raises has, before its wait, no other promise of that.
+__device__ __forceinline__ void publish() {
+  __threadfence();
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
 // Codes [M][K / 2] (even column in the low half of a byte), scales and zeros [M][K / group].
 template <typename S>
 __global__ void __launch_bounds__(kPackWarps * 32)
@@ -89,6 +94,7 @@ __global__ void __launch_bounds__(kPackWarps * 32)
       put_zero(w, block, gi, r, in && zeros ? min((int)zeros[m * groups + g], 15) : kW4Zero);
     }
   }
+  publish();
 }
 
 cudaError_t w4_pack(const W4View& w, const uint8_t* codes, const void* scales, const uint8_t* zeros, cudaStream_t s) {
@@ -165,6 +171,7 @@ __global__ void __launch_bounds__(kPackWarps * 32)
       }
     }
   }
+  publish();
 }
 
 cudaError_t w4_quantize(const W4View& w, int dtype, const void* src, long long ld, cudaStream_t s) {

@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   if (tid == 0) {
     for (int u = 0; u < S; ++u) mbar_init(&code_full[u], 1);
     fence_barrier_init();
-    // The weights do not depend on the kernels before this one (packing lets no successor start early): the first
-    // blocks are asked for before the wait.
+    // The weights do not depend on the kernels before this one (packing lets no successor start early, and has
+    // published its stores by its end): the first blocks are asked for before the wait.
 #pragma unroll
     for (int u = 0; u < S - 1; ++u)
       if (b0 + u < b1) load_codes(next_block + (long long)u * w.block_bytes, u);

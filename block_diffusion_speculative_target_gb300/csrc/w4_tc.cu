@@ -182,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // ---------------------------------------------------------- blocks
-      // The weights do not depend on the kernels before this one (packing lets no successor start early): they are
-      // asked for without waiting for them.
+      // The weights do not depend on the kernels before this one (packing lets no successor start early, and has
+      // published its stores by its end): they are asked for without waiting for them.
       const uint8_t* src = w.packed + (long long)b0 * w.block_bytes;
       int slot = 0;
       uint32_t phase = 0;

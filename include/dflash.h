@@ -609,7 +609,12 @@ int dflash_paged_attention_shared(dflash_pages *p, int32_t layer, const void *q,
  * dflash_w4_quantize from a matrix, dflash_w4_unpack reads it back.  group is 32,
  * 64 or 128 and divides K (else DFLASH_ERR_UNSUPPORTED_SHAPE); M is any; M K at
  * most 2^34 (else DFLASH_ERR_TOO_LARGE).  Buffers that one of these calls writes
- * overlap none that it reads (DFLASH_ERR_INVALID_ARG). */
+ * overlap none that it reads (DFLASH_ERR_INVALID_ARG).  Products read a matrix
+ * before they wait for the kernels ahead of them in their stream (they are launched
+ * as programmatic dependents): a kernel of the caller's own that fills `packed`
+ * itself must not let its dependents start early, and has to make its stores
+ * visible to asynchronous copies before its end (__threadfence, fence.proxy.async);
+ * copies need nothing. */
 typedef struct dflash_w4 {
   int32_t M, K, group;
   int32_t scale_dtype; /* DFLASH_F32 | DFLASH_BF16 */

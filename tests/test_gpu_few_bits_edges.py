@@ -6,6 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from block_diffusion_speculative_target_gb300 import capi  # noqa: E402
 from block_diffusion_speculative_target_gb300.engine import W4Linear, W4Workspace  # noqa: E402
 from test_gpu_paged import CASES, HEADS, TDT, visible  # noqa: E402
 from test_gpu_paged_q8 import SHARED, Batch8, attend, check, reference, untouched  # noqa: E402
@@ -245,3 +246,46 @@ def test_an_infinite_value(n):
     got = attend(x, q)
     assert (got[0, n // 2:, :, 0::2] == math.inf).all() and (got[0, n // 2:, :, 1::2] == -math.inf).all()
     assert torch.equal(got[0, :n // 2], want[0, :n // 2]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("rows", [1, 16, 40])
+def test_products_directly_behind_packing(rows):
+    """A buffer filled again and again, each time with other codes, and a product at once behind each: also captured."""
+    g = torch.Generator(device="cuda").manual_seed(33)
+    M, K = 3000, 1024
+    codes = [torch.randint(0, 256, (M, K // 2), dtype=torch.uint8, device="cuda", generator=g) for _ in range(2)]
+    dense = [torch.empty(M, K, device="cuda").normal_(generator=g) for _ in range(2)]
+    scales = torch.ones(M, K // 128, device="cuda")
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    ws = W4Workspace(rows)
+    want = []
+    for w in [W4Linear.from_codes(c, scales) for c in codes] + [W4Linear.from_weight(d, scale_dtype=torch.float32) for d in dense]:
+        out = torch.zeros(rows, M, device="cuda")
+        w.product(x, out, ws)
+        torch.cuda.synchronize()
+        want.append(out)
+    w = W4Linear(M, K, scale_dtype=torch.float32)
+    got = [torch.zeros_like(o) for o in want]
+
+    def calls():
+        for i in (0, 2, 1, 3):
+            s = torch.cuda.current_stream()
+            if i < 2:
+                capi.dflash_w4_pack(w._c, codes[i], scales, None, s)
+            else:
+                capi.dflash_w4_quantize(w._c, capi.F32, dense[i - 2], K, s)
+            w.product(x, got[i], ws)
+
+    for _ in range(5):
+        calls()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    for o in got:
+        o.zero_()
+    for _ in range(5):
+        graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
