@@ -148,9 +148,10 @@ __device__ __forceinline__ void w4_results(const W4View& w, const W4Epi& epi, in
       const long long n = n0 + c + u;
       if (epi.swiglu) {  // (row m + 1 is the next lane's)
         const float up = __shfl_down_sync(0xffffffffu, v[u], 1);
+        // (both sides of the quotient by 1/4: the fast division is 0 where the divisor is past 2^126, v below -87.3)
         if (live && !(m & 1) && c + u < count)
           reinterpret_cast<bf16*>(epi.out)[n * (w.M / 2) + m / 2] =
-              from_f<bf16>(__fdividef(v[u], 1.f + __expf(-v[u])) * up);
+              from_f<bf16>(__fdividef(0.25f * v[u], fmaf(0.25f, __expf(-v[u]), 0.25f)) * up);
       } else if (live && c + u < count) {
         reinterpret_cast<float*>(epi.out)[n * w.M + m] = v[u];
       }

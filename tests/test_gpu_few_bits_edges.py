@@ -289,3 +289,24 @@ def test_products_directly_behind_packing(rows):
     for _ in range(5):
         graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 8, 16, 40])
+def test_gates_far_below_zero(rows, dtype):
+    """Gates down to -88.5, where e^-g is still a float32, times values of 1e30.  Gate and value are exact here; the
+    exponential's argument is rounded (2^-24 of 128, twice that of the result), the rest is a few roundings, and the
+    result is rounded once more."""
+    code = torch.full((2, 32), 8, dtype=torch.uint8, device="cuda")
+    code[0, 0] = code[1, 1] = 9
+    w = W4Linear.from_codes(code[:, 0::2] | code[:, 1::2] << 4, torch.ones(2, 1, device="cuda"))
+    gates = [-88.5, -88.0, -87.5, -87.0, -60.0, -1.0, 0.0, 50.0]
+    x = torch.zeros(rows, 32, dtype=TDT[dtype], device="cuda")
+    x[:, 0] = torch.tensor([gates[i % len(gates)] for i in range(rows)])
+    x[:, 1] = torch.tensor([(-1) ** i * 1e30 for i in range(rows)])
+    out = torch.zeros(rows, 1, dtype=TDT[dtype], device="cuda")
+    w.product(x, out, W4Workspace(rows), swiglu=True)
+    g, u = x[:, 0].double(), x[:, 1].double()
+    want = g / (1 + torch.exp(-g)) * u
+    tol = (2.0 ** -15 + (2.0 ** -8 if dtype == "bf16" else 0)) * want.abs()
+    assert ((out[:, 0].double() - want).abs() <= tol).all()
