@@ -310,3 +310,35 @@ def test_gates_far_below_zero(rows, dtype):
     want = g / (1 + torch.exp(-g)) * u
     tol = (2.0 ** -15 + (2.0 ** -8 if dtype == "bf16" else 0)) * want.abs()
     assert ((out[:, 0].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("M, K, group", [(1, 32, 32), (130, 32, 32), (257, 64, 64), (40, 96, 32), (2, 128, 128), (300, 224, 32)])
+@pytest.mark.parametrize("rows", [1, 16, 17, 33, 65, 128])
+def test_matrices_narrower_than_a_block(M, K, group, rows):
+    """Fewer columns than a block of 128, or than half of one."""
+    g = torch.Generator(device="cuda").manual_seed(34)
+    w = W4Linear.from_weight(torch.empty(M, K, device="cuda").normal_(generator=g), group, zeros=True)
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    out = torch.full((rows + 2, M), 77.0, device="cuda")
+    ws = W4Workspace(rows)
+    w.product(x, out[1:-1], ws)
+    dense = w.weight().double()
+    want, mag = x.double() @ dense.T, x.double().abs() @ dense.abs().T
+    assert ws.status() == 0 and (out[0] == 77.0).all() and (out[-1] == 77.0).all()
+    assert ((out[1:-1].double() - want).abs() <= (K + 4) * 2.0 ** -23 * mag).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 4, 40])
+@pytest.mark.parametrize("shared", [None, 64])
+def test_a_batch_without_rows(n, shared, dtype):
+    """No sequence has a row: nothing is written, the status stays clear, and the next call is right."""
+    x = Batch8(dtype, 8, 2, 128, 32, [200, 70], n, shared=shared or 0)
+    q = x.query()
+    want = attend(x, q, shared=shared)
+    x.n_rows = torch.zeros(2, dtype=torch.int32, device="cuda")
+    assert (attend(x, q, shared=shared) == 77.0).all()
+    x.n_rows.fill_(-3)
+    assert (attend(x, q, shared=shared) == 77.0).all()
+    x.n_rows = None
+    assert torch.equal(attend(x, q, shared=shared), want) and x.cache.status() == 0
