@@ -615,7 +615,9 @@ __global__ void __launch_bounds__(kQ8Threads, (Q8Layout<HD, ROWS>::kCtas))
   }
 }
 
-// Stacked rows that one sequence's queries, or the batch's behind a shared prefix, make.
+// Stacked rows that one sequence's queries, or the batch's behind a shared prefix, make.  (The batch's choose for the
+// sequences' own keys too: 32 tokens behind 64 common keys and 2K..8K of their own take 216 us, without the shared
+// length 68.)
 static int q8_stack(const PagedGeom& g) { return (g.shared ? g.batch : 1) * g.n * g.G; }
 // Up to 32 rows a key's codes are expanded for one or two row tiles; beyond, once for 128 rows.  At 32 rows (8 sequences,
 // 2K..6K keys) 54 us here and 58 there, at 30 over 0.5K..36K keys 147 and 179, at 16 38 and 56; at 64 83 (in groups of

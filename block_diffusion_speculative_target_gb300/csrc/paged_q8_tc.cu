@@ -212,50 +212,50 @@ __global__ void __launch_bounds__(kThreads, 2)
   // The piece's queries: half, each row by a power of two.
   auto load_queries = [&] {
     const int x0 = pc.rt * (pc.prefix ? g.rp : g.ri);
-      constexpr int kLanes = HD / 16;  // a lane takes 16 entries of a row
-      const int c = tid % kLanes;
+    constexpr int kLanes = HD / 16;  // a lane takes 16 entries of a row
+    const int c = tid % kLanes;
 #pragma unroll 2
-      for (int r = tid / kLanes; r < kRows; r += kThreads / kLanes) {
-        const ItemRow row = item_row(g, pc.prefix, pc.b, pc.hk, x0, r);
-        uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-        int4 span = make_int4(0, 0, INT32_MAX, 0);
-        if (row.live) {
-          const uint4* src =
-              reinterpret_cast<const uint4*>(q + (((long long)row.b * g.n + row.i) * g.nq + row.head) * HD + 16 * c);
-          raw[0] = src[0];
-          raw[1] = src[1];
-          if (c == 0) row_span(g, paged_len(g, row.b), paged_rows(g, row.b), row.i, span.x, span.y, span.z);
-        }
-        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
-        float most = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 f = __bfloat1622float2(h[e]);
-          most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        // 2^up brings the largest entry to 2^7..2^8 (a row of zeros, or one that holds Inf: as it is)
-        const int ex = (int)(__float_as_uint(most) >> 23);
-        const int up = ex > 0 && ex < 255 ? 134 - ex : ex == 0 && most > 0.f ? 133 : 0;
-        const float u1 = exp2f((float)(up / 2)), u2 = exp2f((float)(up - up / 2));
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 f = __bfloat1622float2(h[e]);
-          w[e] = half2_of(f.x * u1 * u2, f.y * u1 * u2);
-        }
-        uint8_t* dst = sm + L::kQ + (c >> 2) * (kRows * 128) + r * 128;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<uint4*>(dst + (((2 * (c & 3) + e) ^ (r & 7)) << 4)) =
-              make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        if (c == 0) {
-          span.w = __float_as_int(exp2f((float)-up));
-          spans[r] = span;
-        }
+    for (int r = tid / kLanes; r < kRows; r += kThreads / kLanes) {
+      const ItemRow row = item_row(g, pc.prefix, pc.b, pc.hk, x0, r);
+      uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      int4 span = make_int4(0, 0, INT32_MAX, 0);
+      if (row.live) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(q + (((long long)row.b * g.n + row.i) * g.nq + row.head) * HD + 16 * c);
+        raw[0] = src[0];
+        raw[1] = src[1];
+        if (c == 0) row_span(g, paged_len(g, row.b), paged_rows(g, row.b), row.i, span.x, span.y, span.z);
       }
-      fence_proxy_async_smem();
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
+      float most = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 f = __bfloat1622float2(h[e]);
+        most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      // 2^up brings the largest entry to 2^7..2^8 (a row of zeros, or one that holds Inf: as it is)
+      const int ex = (int)(__float_as_uint(most) >> 23);
+      const int up = ex > 0 && ex < 255 ? 134 - ex : ex == 0 && most > 0.f ? 133 : 0;
+      const float u1 = exp2f((float)(up / 2)), u2 = exp2f((float)(up - up / 2));
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 f = __bfloat1622float2(h[e]);
+        w[e] = half2_of(f.x * u1 * u2, f.y * u1 * u2);
+      }
+      uint8_t* dst = sm + L::kQ + (c >> 2) * (kRows * 128) + r * 128;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<uint4*>(dst + (((2 * (c & 3) + e) ^ (r & 7)) << 4)) =
+            make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+      if (c == 0) {
+        span.w = __float_as_int(exp2f((float)-up));
+        spans[r] = span;
+      }
+    }
+    fence_proxy_async_smem();
   };
   int done = 0;  // tiles of the pieces before
   if (warp >= 4) {
@@ -397,41 +397,41 @@ __global__ void __launch_bounds__(kThreads, 2)
     walk.start();
     bool first = true;
     while (true) {
-    if (warp == 0) {
-      Segment sg;
-      const bool more = walk.next(sg);
-      if (first && !g.shared) {
-        // the item that this CTA's run begins inside of, when it is the second to hold a piece of it
-        int c0 = 0, nc = 0;
-        if (more && sg.t0 > 0) nc = walk.pieces(sg, c0);
-        if (c0 + 1 != (int)blockIdx.x) nc = 0;
-        int4* rec = reinterpret_cast<int4*>(g.records) + 2 * blockIdx.x;
+      if (warp == 0) {
+        Segment sg;
+        const bool more = walk.next(sg);
+        if (first && !g.shared) {
+          // the item that this CTA's run begins inside of, when it is the second to hold a piece of it
+          int c0 = 0, nc = 0;
+          if (more && sg.t0 > 0) nc = walk.pieces(sg, c0);
+          if (c0 + 1 != (int)blockIdx.x) nc = 0;
+          int4* rec = reinterpret_cast<int4*>(g.records) + 2 * blockIdx.x;
+          if (lane == 0) {
+            rec[0] = make_int4(nc, sg.b, sg.rt, sg.hk);
+            rec[1].x = c0;
+          }
+        }
         if (lane == 0) {
-          rec[0] = make_int4(nc, sg.b, sg.rt, sg.hk);
-          rec[1].x = c0;
+          pc.nt = more ? sg.nt : 0;
+          if (more) {
+            pc.prefix = sg.prefix;
+            pc.b = sg.b;
+            pc.rt = sg.rt;
+            pc.hk = sg.hk;
+            pc.whole = walk.whole(sg);
+            pc.s0 = sg.span.s0;
+            pc.sn = sg.span.s1 - sg.span.s0;
+            pc.w0 = sg.span.w0;
+            pc.t0 = sg.t0;
+            pc.key_lo = sg.prefix ? 0 : pv.sh_tiles * kKeys;
+            pc.key_end = sg.prefix ? pv.sh_tiles * kKeys : key_limit(g, sg.b);
+            int hi;
+            row_span(g, sg.prefix ? pv.min_len : paged_len(g, sg.b), paged_rows(g, sg.b),
+                     sg.prefix ? 0 : div_g(g, sg.rt * g.ri), pc.seen_sink, pc.seen_lo, hi);
+            pc.slot_row = sg.slot_row;
+          }
         }
       }
-      if (lane == 0) {
-        pc.nt = more ? sg.nt : 0;
-        if (more) {
-          pc.prefix = sg.prefix;
-          pc.b = sg.b;
-          pc.rt = sg.rt;
-          pc.hk = sg.hk;
-          pc.whole = walk.whole(sg);
-          pc.s0 = sg.span.s0;
-          pc.sn = sg.span.s1 - sg.span.s0;
-          pc.w0 = sg.span.w0;
-          pc.t0 = sg.t0;
-          pc.key_lo = sg.prefix ? 0 : pv.sh_tiles * kKeys;
-          pc.key_end = sg.prefix ? pv.sh_tiles * kKeys : key_limit(g, sg.b);
-          int hi;
-          row_span(g, sg.prefix ? pv.min_len : paged_len(g, sg.b), paged_rows(g, sg.b),
-                   sg.prefix ? 0 : div_g(g, sg.rt * g.ri), pc.seen_sink, pc.seen_lo, hi);
-          pc.slot_row = sg.slot_row;
-        }
-      }
-    }
       first = false;
       cta_sync();
       const int nt = pc.nt;

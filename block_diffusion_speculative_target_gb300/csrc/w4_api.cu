@@ -182,7 +182,8 @@ int dflash_linear_w4(int32_t dtype, const void* x, int64_t ldx, const dflash_w4*
   REQ(cudaGetDevice(&device) == cudaSuccess && device == ws->device);
   const W4Epi epi = {add, swiglu != 0, y};
   // 16 rows of 6144 x 4096: 11 us fed from registers, 15 through TMEM; 15 rows of 151936 x 5120: 100 and 198.  32 rows of
-  // 4096 x 12288: 30 and 21.
+  // 4096 x 12288: 30 (in a form of four column tiles, since dropped) and 21.  On large matrices the 17th row costs a step:
+  // 24576 x 4096 with the gate 23 -> 36 us, 151936 x 5120 100 -> 199 (217 with 64 rows).
   if (dtype == DFLASH_BF16 && rows <= kW4MmaRows)
     CK(w4_linear_mma(v, x, ldx, rows, epi, ws->sc, (cudaStream_t)stream));
   else if (dtype == DFLASH_BF16)

@@ -28,12 +28,12 @@
 // alone and in a block.
 //
 // Measured: 15 rows of 151936 x 5120 100 us (4.1 TB/s, the floor 60), 16 rows of
-// 24576 x 4096 with the activation 22.3 us (2.4 TB/s), one row of 4096 x 4096 7.7 us.
-// Large matrices are bound by issue (59% of the slots) and by the latency that 16 warps a
-// multiprocessor leave open; small ones by a chain of trips to memory: first block, x,
-// partial sums, ticket, join.
+// 24576 x 4096 with the activation 22.7 us (2.4 TB/s), one row of 4096 x 4096 7.8 us.
+// On large matrices neither issue (59% of the slots) nor memory (50%) is at its limit:
+// four warps in step at a barrier a block, 16 warps a multiprocessor.  Small ones are a
+// chain of trips to memory: first block, x, partial sums, ticket, join.
 // 17 rows and more go to the kernel that expands codes once for 128 columns: with 32 rows
-// of 4096 x 12288 that takes 21 us, this one's form of four column tiles 30.
+// of 4096 x 12288 that took 21 us, a form of four column tiles of this one 30.
 //
 // The waits for copies are bounded (dflash_debug_set_wait_limit); a CTA whose wait
 // runs out sets DFLASH_STATUS_TIMEOUT, waits for what it has in flight and leaves

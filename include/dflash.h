@@ -585,7 +585,9 @@ int dflash_paged_attention(dflash_pages *p, int32_t layer, const void *q, int32_
  * the same keys and values in every sequence with rows in this call: those are
  * read once for the whole batch, from the pages that the first such sequence's
  * table names, with all sequences' rows stacked against them.  Values of
- * *shared_len outside [0, min len] are clamped to it. */
+ * *shared_len outside [0, min len] are clamped to it.  Over 8-bit pages the call
+ * pays where most keys are common: the whole batch's rows choose the kernel for the
+ * sequences' own keys too, which can make those of single tokens three times slower. */
 int dflash_paged_attention_shared(dflash_pages *p, int32_t layer, const void *q, int32_t batch, int32_t n,
                                   const int32_t *n_rows, int32_t causal, int32_t window, int32_t sinks,
                                   const int32_t *table, int32_t table_stride, const int32_t *len,
